@@ -346,6 +346,182 @@ ck_status ck_lif_run(ck_graph_t g, const ck_lif_params* params, const int32_t* v
 ck_status ck_profile_collect_lif(double* gather_ms, int64_t* gather_launches, double* update_ms,
                                  int64_t* update_launches);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Sequence operators: what a text model runs before and behind the graph
+ * recurrence, on tensors laid out time first like its drives and states.  A
+ * short causal convolution and a selective state space scan mix a window's
+ * steps (with the backward for training, lengths and carried states for
+ * prompts, and a form for single tokens), and a counter-based dropout
+ * regularises the training.
+ *
+ * Conventions of these entry points, beside those above
+ *   - A sequence tensor [T, B, channels] is a ck_seq: its channels are
+ *     adjacent, its steps and batch rows lie stride_t and stride_b elements
+ *     apart (0 <= stride_t < 2^26 and 0 <= stride_b, else CK_ERR_BAD_VALUE: a
+ *     slice of a wider tensor, batch-major storage, or 0 for an input that
+ *     is the same at every step or row).  Elements are of the call's
+ *     ck_dtype; parameters, scan states and their gradients are fp32 and
+ *     contiguous.
+ *   - Outputs must not overlap inputs or each other unless stated.
+ *   - T may be 0 (the state passes through); B and D are positive.
+ *   - lengths: int32[B] device or NULL (every row T steps).  Row b holds
+ *     text at steps t < lengths[b] only (values outside [0, T] count as the
+ *     nearer bound): later steps change no state, what the inputs hold there
+ *     is not used, outputs and gradients are 0 there.
+ *   - Sums, states and statistics are kept in fp32; outputs are rounded once.
+ *     Two calls on the same inputs give the same bits.
+ *   - These calls take no graph handle, allocate nothing, do not synchronise
+ *     and may be captured into a HIP graph.
+ */
+typedef enum {
+  CK_F32 = 0,
+  CK_BF16 = 1,
+  CK_F16 = 2
+} ck_dtype;
+
+typedef struct {
+  void* data;       /* element [0][0][0]; not written through for inputs */
+  int64_t stride_t; /* elements between steps */
+  int64_t stride_b; /* elements between batch rows */
+} ck_seq;
+
+/*
+ * Selective state space scan.  Per row b, channel d and state n < N:
+ *
+ *   dt_t   = softplus(delta_t + delta_bias)   (delta_softplus; else delta_t + delta_bias)
+ *   h_t    = exp(dt_t A[d][n]) h_{t-1} + dt_t B_t[n] u_t
+ *   y_t    = sum_n C_t[n] h_t + D[d] u_t
+ *   out_t  = y_t z_t sigmoid(z_t)             (y_t without z)
+ *
+ * with h_{-1} = state0.  B and C are [T, B, G, N]: channels
+ * [g D/G, (g+1) D/G) share group g (G divides D; the G*N values of a step
+ * and row are adjacent).
+ */
+typedef struct {
+  int64_t T, B, D; /* steps, batch rows, channels */
+  int64_t N;       /* states per channel, 1..64 */
+  int64_t G;       /* groups of B and C */
+  int32_t dtype;   /* ck_dtype of the sequence tensors */
+  int32_t delta_softplus;
+} ck_scan_shape;
+
+typedef struct {
+  ck_seq u, delta;         /* [T, B, D] */
+  ck_seq b, c;             /* [T, B, G, N] */
+  ck_seq z;                /* [T, B, D]; data NULL: no gate */
+  const float* a;          /* [D][N] */
+  const float* d;          /* [D] or NULL (0) */
+  const float* delta_bias; /* [D] or NULL (0) */
+  const float* state0;     /* [B][D][N] or NULL (0) */
+  const int32_t* lengths;  /* [B] or NULL */
+} ck_scan_inputs;
+
+/* Gradients, all overwritten; layouts as the inputs'.  z is required when the
+ * call has a gate; d, delta_bias and state0 may be NULL (not wanted). */
+typedef struct {
+  ck_seq u, delta, b, c, z;
+  float *a, *d, *delta_bias, *state0;
+} ck_scan_grads;
+
+/* saved_bytes: states the forward leaves for the backward (one per tile of
+ * steps; its layout is internal).  forward_bytes, backward_bytes: scratch of
+ * each call (a workspace of 0 bytes may be NULL).  Any pointer may be NULL. */
+ck_status ck_scan_sizes(const ck_scan_shape* shape, size_t* saved_bytes, size_t* forward_bytes,
+                        size_t* backward_bytes);
+
+/*
+ *   out        [T, B, D]     written
+ *   state      fp32[B][D][N] written: the state after each row's last step (NULL: not wanted)
+ *   saved      saved_bytes   written for ck_scan_backward, or NULL when no backward follows
+ *   workspace  forward_bytes
+ */
+ck_status ck_scan_forward(const ck_scan_shape* shape, const ck_scan_inputs* in, ck_seq out,
+                          float* state, void* saved, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream);
+
+/* Gradients of L given grad_out = dL/dout and grad_state = dL/dstate
+ * (fp32[B][D][N], NULL for 0).  `saved` must come from the forward with the
+ * same shape and inputs. */
+ck_status ck_scan_backward(const ck_scan_shape* shape, const ck_scan_inputs* in, const void* saved,
+                           ck_seq grad_out, const float* grad_state, const ck_scan_grads* grads,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* One token per row (shape->T must be 1, lengths NULL): out[0] and the new
+ * state from state0.  `state` may be state0 itself (updated in place). */
+ck_status ck_scan_step(const ck_scan_shape* shape, const ck_scan_inputs* in, ck_seq out,
+                       float* state, hipStream_t stream);
+
+/*
+ * Short causal convolution, each channel on its own, width W:
+ *
+ *   p_t = bias[d] + sum_{k<W} weight[d][k] x_{t-(W-1)+k},   y_t = p_t or p_t sigmoid(p_t) (silu)
+ *
+ * x before step 0 comes from state0 [W-1, B, D] (contiguous, oldest first;
+ * NULL: 0).  The new state holds the last W-1 inputs of each row.
+ */
+typedef struct {
+  int64_t T, B, D;
+  int64_t W;     /* taps, 1..8 */
+  int32_t dtype; /* ck_dtype of x, y and the states */
+  int32_t silu;
+} ck_conv_shape;
+
+/* Scratch of ck_conv_backward. */
+ck_status ck_conv_sizes(const ck_conv_shape* shape, size_t* workspace_bytes);
+
+/*
+ *   weight  fp32[D][W]      bias  fp32[D] or NULL (0)
+ *   y       [T, B, D]       written
+ *   state   [W-1][B][D]     written (NULL: not wanted)
+ */
+ck_status ck_conv_forward(const ck_conv_shape* shape, ck_seq x, const float* weight,
+                          const float* bias, const void* state0, const int32_t* lengths, ck_seq y,
+                          void* state, hipStream_t stream);
+
+/* Gradients given grad_y and grad_state (= dL/dstate, NULL for 0); grad_bias
+ * and grad_state0 may be NULL (not wanted). */
+ck_status ck_conv_backward(const ck_conv_shape* shape, ck_seq x, const float* weight,
+                           const float* bias, const void* state0, const int32_t* lengths,
+                           ck_seq grad_y, const void* grad_state, ck_seq grad_x,
+                           float* grad_weight, float* grad_bias, void* grad_state0,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* One token per row (shape->T must be 1).  `state` may be state0 itself. */
+ck_status ck_conv_step(const ck_conv_shape* shape, ck_seq x, const float* weight,
+                       const float* bias, const void* state0, ck_seq y, void* state,
+                       hipStream_t stream);
+
+/*
+ * Dropout whose mask is recomputed from counters and never stored:
+ *
+ *   out = residual + (r >= q ? x * 65536 / (65536 - q) : 0),   q = floor(65536 p + 1/2)
+ *
+ * r is 16 bits of the Philox4x32-10 generator (J. Salmon et al., "Parallel
+ * random numbers: as easy as 1, 2, 3", SC 2011) keyed by `seed` at counter
+ * words (d / 8, row, offset low, offset high), channel d taking half d mod 8
+ * of the 128 bits (low halves first).  row = t B + b, or b when the mask is
+ * held for the whole window.  With `counter` (device int64[1], may be NULL)
+ * its value is added to `offset`, so that a captured graph can draw another
+ * mask at every replay.  A dropped element of x counts as 0 whatever it holds.
+ */
+typedef struct {
+  int64_t T, B, D;
+  int32_t dtype;
+  int32_t held; /* one mask for all steps */
+  double p;     /* probability of dropping, 0..1 */
+  uint64_t seed, offset;
+  const int64_t* counter;
+} ck_dropout_shape;
+
+/* residual.data NULL: none.  out may be x or the residual itself. */
+ck_status ck_dropout_forward(const ck_dropout_shape* shape, ck_seq x, ck_seq residual, ck_seq out,
+                             hipStream_t stream);
+/* grad_x = mask and scale of the forward with the same shape on grad_out (the
+ * residual's gradient is grad_out itself).  grad_x may be grad_out. */
+ck_status ck_dropout_backward(const ck_dropout_shape* shape, ck_seq grad_out, ck_seq grad_x,
+                              hipStream_t stream);
+
 /* Static name of a status value. */
 const char* ck_status_string(ck_status s);
 

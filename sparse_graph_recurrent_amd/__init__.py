@@ -16,6 +16,10 @@ edge_values fp32 [E] in the caller's edge order, leak/bias fp32 [N],
 drives fp32 [T, n_in, B], state0 fp32 [B, N] and out fp32 [T, B, N].
 ``sparse_recurrence`` is differentiable in all five tensor arguments.
 
+The sequence operators that a text model runs before and behind the
+recurrence (short convolution, selective scan, dropout) are in ``sequence``
+and reached by the same names here.
+
 The library is required: importing works without it, but every call raises
 ``CkLibraryMissing`` if ``libck_hip.so`` has not been built
 (``python -m sparse_graph_recurrent_amd.build``).  There is no fallback.
@@ -41,7 +45,9 @@ EXPORTED = ("ck_graph_create", "ck_graph_destroy", "ck_graph_sizes", "ck_graph_e
             "ck_recurrence_sizes", "ck_recurrence_path", "ck_recurrence_forward",
             "ck_recurrence_backward", "ck_recurrence_status", "ck_recurrence_forward_noalloc",
             "ck_lif_workspace_size", "ck_lif_forward", "ck_lif_prepare", "ck_lif_run",
-            "ck_profile_collect_lif",
+            "ck_profile_collect_lif", "ck_scan_sizes", "ck_scan_forward", "ck_scan_backward",
+            "ck_scan_step", "ck_conv_sizes", "ck_conv_forward", "ck_conv_backward",
+            "ck_conv_step", "ck_dropout_forward", "ck_dropout_backward",
             "ck_profile_enable", "ck_profile_collect", "ck_status_string", "ck_last_error")
 
 
@@ -96,6 +102,7 @@ def lib() -> ctypes.CDLL:
         ip = ctypes.POINTER(i64)
         L.ck_profile_collect.argtypes = [dp, ip, dp, ip]
         L.ck_profile_collect_lif.argtypes = [dp, ip, dp, ip]
+        sequence._declare(L)
         for name in EXPORTED[:-2]:
             getattr(L, name).restype = ctypes.c_int
         L.ck_status_string.argtypes = [ctypes.c_int]
@@ -450,7 +457,13 @@ def sparse_recurrence(edge_values, leak, bias, drives, state0, graph: SparseGrap
                                    int(microsteps), bool(check))
 
 
+from . import sequence  # noqa: E402  (uses the helpers above)
+from .sequence import (  # noqa: E402
+    dropout, dropout_backward, dropout_forward, selective_scan, selective_scan_backward,
+    selective_scan_forward, selective_scan_sizes, selective_scan_step, short_conv,
+    short_conv_backward, short_conv_forward, short_conv_step)
+
 __all__ = ["SparseGraph", "sparse_recurrence", "recurrence_forward", "recurrence_backward",
            "recurrence_forward_noalloc", "lif_forward", "profile_collect_lif", "LifParams",
            "recurrence_sizes", "recurrence_status", "recurrence_path", "profile_enable", "profile_collect", "CkError", "CkLibraryMissing",
-           "lib", "LIB_PATH", "EXPORTED"]
+           "lib", "LIB_PATH", "EXPORTED"] + sequence.__all__

@@ -1,0 +1,175 @@
+// sequence.h -- element types, argument checks and lane exchanges shared by
+// the sequence operators (convolution, selective scan, dropout).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "ck.h"
+#include "ck_internal.h"
+
+namespace ckhip {
+namespace {
+
+typedef __bf16 bf16_t;
+typedef _Float16 f16_t;
+
+inline size_t seq_elem_bytes(int dtype) { return dtype == CK_F32 ? 4 : 2; }
+
+// Calls fn with a null pointer of the element type of `dtype` (checked before).
+template <typename F>
+ck_status seq_dispatch(int dtype, F&& fn) {
+  switch (dtype) {
+    case CK_F32: return fn((float*)nullptr);
+    case CK_BF16: return fn((bf16_t*)nullptr);
+    default: return fn((f16_t*)nullptr);
+  }
+}
+
+// T >= 0 steps (an empty window is allowed), B and D positive, and every
+// count the kernels hold in 32 bits below 2^31.
+inline ck_status seq_check_shape(int64_t T, int64_t B, int64_t D, int dtype) {
+  if (T < 0 || B <= 0 || D <= 0) {
+    set_error("bad sizes: T=%lld B=%lld D=%lld", (long long)T, (long long)B, (long long)D);
+    return CK_ERR_BAD_SIZE;
+  }
+  if (T >= INT_MAX || B >= INT_MAX || D >= INT_MAX || B * D >= (int64_t(1) << 36) ||
+      (T > 0 && B * D > (int64_t(1) << 46) / T)) {
+    set_error("T=%lld, B=%lld or D=%lld is too large", (long long)T, (long long)B, (long long)D);
+    return CK_ERR_TOO_LARGE;
+  }
+  if (dtype != CK_F32 && dtype != CK_BF16 && dtype != CK_F16) {
+    set_error("unknown element type %d", dtype);
+    return CK_ERR_BAD_VALUE;
+  }
+  return CK_OK;
+}
+
+// Step strides stay below this many elements, so that the byte offset of any
+// step of a 16-step tile from the tile's first fits 32 unsigned bits.
+constexpr int64_t kSeqMaxStrideT = int64_t(1) << 26;
+
+// A [T, B, ...] tensor: present unless optional, aligned to its elements, with
+// strides in range (a zero stride broadcasts an input).
+inline ck_status seq_check(const ck_seq& s, int dtype, bool optional, const char* what) {
+  if (!s.data) {
+    if (optional) return CK_OK;
+    set_error("%s is NULL", what);
+    return CK_ERR_NULL_ARG;
+  }
+  if (reinterpret_cast<uintptr_t>(s.data) % seq_elem_bytes(dtype) != 0) {
+    set_error("%s is not aligned to its element type", what);
+    return CK_ERR_BAD_VALUE;
+  }
+  if (s.stride_t < 0 || s.stride_t >= kSeqMaxStrideT || s.stride_b < 0) {
+    set_error("%s has strides (%lld, %lld); they must be in [0, 2^26) and not negative", what,
+              (long long)s.stride_t, (long long)s.stride_b);
+    return CK_ERR_BAD_VALUE;
+  }
+  return CK_OK;
+}
+
+inline ck_status seq_check_ws(const void* workspace, size_t bytes, size_t need) {
+  if (need == 0) return CK_OK;
+  if (!workspace) {
+    set_error("workspace is NULL");
+    return CK_ERR_NULL_ARG;
+  }
+  const ck_status rc = check_aligned(workspace, "workspace");
+  if (rc != CK_OK) return rc;
+  if (bytes < need) {
+    set_error("workspace of %zu bytes is below the %zu required", bytes, need);
+    return CK_ERR_WORKSPACE;
+  }
+  return CK_OK;
+}
+
+// Typed view of a ck_seq inside a kernel.
+template <typename E>
+struct Seq {
+  E* p;
+  int64_t st, sb;
+  __device__ __forceinline__ E* row(int64_t t, int64_t b) const { return p + t * st + b * sb; }
+};
+// True when rows of V elements can be read whole: every row of every listed
+// tensor starts on a V-element boundary.
+template <typename E, int V>
+bool seq_vec_ok(const ck_seq& s) {
+  return reinterpret_cast<uintptr_t>(s.data) % (V * sizeof(E)) == 0 && s.stride_t % V == 0 &&
+         s.stride_b % V == 0;
+}
+template <typename E>
+Seq<E> seq_of(const ck_seq& s) {
+  return Seq<E>{static_cast<E*>(s.data), s.stride_t, s.stride_b};
+}
+
+// V adjacent elements, moved with one access of V * sizeof(E) bytes.
+template <typename E, int V>
+struct alignas(V * sizeof(E)) Pack {
+  E v[V];
+};
+template <typename E, int V>
+__device__ __forceinline__ void pack_load(float (&x)[V], const E* p) {
+  const Pack<E, V> w = *reinterpret_cast<const Pack<E, V>*>(p);
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] = (float)w.v[i];
+}
+template <typename E, int V>
+__device__ __forceinline__ void pack_store(E* p, const float (&x)[V]) {
+  Pack<E, V> w;
+#pragma unroll
+  for (int i = 0; i < V; ++i) w.v[i] = (E)x[i];
+  *reinterpret_cast<Pack<E, V>*>(p) = w;
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float rcp_hw(float x) { return __builtin_amdgcn_rcpf(x); }
+
+// 1 / (1 + exp(-x)): the exponential's overflow for x below -88 makes the
+// reciprocal an exact 0; hardware exponential and reciprocal, about 3 ulp.
+__device__ __forceinline__ float sigmoid_hw(float x) {
+  return rcp_hw(1.0f + exp2_hw(-kLog2e * x));
+}
+
+// log(1 + exp(x)) = max(x, 0) + log1p(exp(-|x|)).  The part of e that the sum
+// w = 1 + e rounds away is added back to first order, so the result keeps its
+// relative accuracy down to exp(x) itself for very negative x.
+__device__ __forceinline__ float softplus_hw(float x) {
+  const float e = exp2_hw(-kLog2e * fabsf(x));
+  const float w = 1.0f + e;
+  const float l = fmaf(kLn2, __builtin_amdgcn_logf(w), (e - (w - 1.0f)) * rcp_hw(w));
+  return fmaxf(x, 0.0f) + l;
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+// value of lane J of the caller's quad (lanes 4k .. 4k + 3)
+template <int J>
+__device__ __forceinline__ float quad_get(float x) {
+  return dpp<J * 0x55>(x);
+}
+__device__ __forceinline__ float quad_xor1(float x) { return dpp<0xB1>(x); }
+__device__ __forceinline__ float quad_xor2(float x) { return dpp<0x4E>(x); }
+__device__ __forceinline__ float quad_sum(float x) {
+  x += quad_xor1(x);
+  return x + quad_xor2(x);
+}
+// Lane q of each quad gets the quad's sum of v_q: a reduce-scatter, 3 adds
+// where four butterflies would take 8.
+__device__ __forceinline__ float quad_reduce4(float v0, float v1, float v2, float v3, int q) {
+  const bool hi = q & 2, odd = q & 1;
+  const float r0 = (hi ? v2 : v0) + quad_xor2(hi ? v0 : v2);
+  const float r1 = (hi ? v3 : v1) + quad_xor2(hi ? v1 : v3);
+  return (odd ? r1 : r0) + quad_xor1(odd ? r0 : r1);
+}
+
+}  // namespace
+}  // namespace ckhip

@@ -1,0 +1,547 @@
+"""The sequence operators (short convolution, selective scan, dropout) against
+their fp64 definitions, at the sizes, lengths, strides and types where such
+kernels go wrong.
+
+Tolerances.  Every output is held to
+
+    |got - want| <= (eps / 2) (|want| + err) + err,   err = k 2^-24 m
+
+where eps / 2 is the one rounding to the output's type, m the sum of the
+magnitudes of the output's terms (``sequence_ref``, magnitude=True) and k the
+count of fp32 roundings on a term's way: about 8 a step through the
+recurrence's products and hardware functions (the decay's error, relative
+8 |dt A|, is largest where dt A exp(dt A) is, at 3 / 8 of that), once more in
+the gradients, whose terms hold a state and an adjoint, and the additions
+across channels, rows and steps.
+"""
+import numpy as np
+import pytest
+import torch
+
+import sequence_ref as ref
+import sparse_graph_recurrent_amd as sgr
+from gpu_helpers import log
+
+pytestmark = pytest.mark.gpu
+
+DT = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    sgr.lib()
+
+
+def close(got, want, mag, k, name):
+    got_t = got.detach()
+    fi = torch.finfo(got_t.dtype)
+    g = got_t.double().cpu().numpy()
+    assert g.shape == want.shape, name
+    err = k * ref.U32 * mag
+    tol = fi.eps / 2 * (np.abs(want) + err) + err + fi.smallest_normal * fi.eps
+    bad = ~(np.abs(g - want) <= tol)
+    assert not bad.any(), (f"{name}: {bad.sum()} of {bad.size} beyond the bound, worst "
+                           f"{np.nanmax(np.abs(g - want) / tol):.3g} times it, "
+                           f"{np.isnan(g).sum()} NaN, first at {np.argwhere(bad)[0]}")
+
+
+def place(a, dtype, layout, pad_nan=None):
+    """The fp64 array [T, B, ...] on the device: "time" contiguous, "batch"
+    batch outermost, "slice" a slice of a wider tensor (odd offset, odd row
+    stride).  Returns (tensor, its exact values in fp64)."""
+    t = torch.from_numpy(np.ascontiguousarray(a)).to(dtype)
+    val = t.double().numpy()
+    if pad_nan is not None:
+        t[torch.from_numpy(~pad_nan)] = float("nan")
+    T, B = t.shape[:2]
+    inner = t.shape[2:]
+    n = int(np.prod(inner))
+    if layout == "batch":
+        s = torch.empty((B, T) + tuple(inner), dtype=dtype, device="cuda").transpose(0, 1)
+    elif layout == "slice":
+        s = torch.full((T, B, n + 5), 7.0, dtype=dtype, device="cuda")[:, :, 3:3 + n]
+        s = s.unflatten(2, tuple(inner)) if n else s.reshape((T, B) + tuple(inner))
+    else:
+        s = torch.empty(t.shape, dtype=dtype, device="cuda")
+    s.copy_(t)
+    return s, val
+
+
+def _f32(a):
+    t = torch.from_numpy(np.ascontiguousarray(a)).float()
+    return t.cuda(), t.double().numpy()
+
+
+def scan_problem(seed, T, B, D, N, G, dtype, gate, softplus, lengths, layout, state0=True,
+                 extras=True, nan=True):
+    """(GPU arguments, fp64 problem) with the same values."""
+    r = np.random.default_rng(seed)
+    ok = ref.valid(T, B, None if lengths is None else np.array(lengths))
+    pad = ok if nan and lengths is not None else None
+    raw = {"u": r.standard_normal((T, B, D)),
+           "delta": (r.standard_normal((T, B, D)) - 2 if softplus else
+                     r.uniform(0.0, 0.5, (T, B, D))),
+           "B": r.standard_normal((T, B, G, N)), "C": r.standard_normal((T, B, G, N)),
+           "go": r.standard_normal((T, B, D))}
+    if gate:
+        raw["z"] = 2 * r.standard_normal((T, B, D))
+    gpu, p = {}, {"softplus": softplus, "lengths": None if lengths is None else np.array(lengths)}
+    for k, a in raw.items():
+        gpu[k], p[k] = place(a, DT[dtype], layout, pad)
+    par = {"A": -np.exp(r.uniform(np.log(0.05), np.log(16), (D, N))),
+           "gstate": r.standard_normal((B, D, N))}
+    if extras:
+        par.update(D=r.standard_normal(D),
+                   delta_bias=0.2 * (r.standard_normal(D) if softplus else r.random(D)))
+    if state0:
+        par["state0"] = r.standard_normal((B, D, N))
+    for k, a in par.items():
+        gpu[k], p[k] = _f32(a)
+    gpu["lengths"] = None if lengths is None else torch.tensor(lengths, dtype=torch.int32,
+                                                               device="cuda")
+    return gpu, p
+
+
+def scan_run(g, softplus, stream=None, **kw):
+    args = (g["u"], g["delta"], g["A"], g["B"], g["C"])
+    opt = dict(D=g.get("D"), z=g.get("z"), delta_bias=g.get("delta_bias"), lengths=g["lengths"],
+               delta_softplus=softplus, stream=stream)
+    out, state, saved, _ = sgr.selective_scan_forward(*args, state0=g.get("state0"), **opt, **kw)
+    grads = sgr.selective_scan_backward(*args, saved, g["go"], grad_state=g["gstate"], **opt)
+    return out, state, grads
+
+
+def scan_check(g, p, softplus, got=None):
+    T, B, D = g["u"].shape
+    want, mag = ref.scan(p), ref.scan(p, magnitude=True)
+    out, state, grads = got or scan_run(g, softplus)
+    torch.cuda.synchronize()
+    k = 32 + 8 * T
+    close(out, want["out"], mag["out"], k, "out")
+    close(state, want["state"], mag["state"], k, "state")
+    k = 64 + 16 * T + B + 64
+    for name, t in grads.items():
+        if name in ("g_D", "g_delta_bias") and name not in want:
+            continue
+        close(t, want[name], mag[name], k, name)
+
+
+SCAN = [  # T, B, D, N, G, dtype, gate, softplus, lengths, layout
+    (1, 1, 1, 1, 1, "fp32", False, False, None, "time"),
+    (16, 2, 64, 16, 1, "fp32", True, True, None, "time"),
+    (15, 2, 63, 16, 1, "bf16", True, True, None, "slice"),
+    (17, 3, 65, 13, 5, "fp16", True, True, None, "batch"),
+    (33, 2, 130, 4, 2, "fp32", False, True, None, "batch"),
+    (40, 1, 96, 8, 3, "bf16", True, False, None, "time"),
+    (100, 2, 70, 16, 7, "fp32", True, True, None, "slice"),
+    (19, 2, 64, 17, 1, "fp32", True, True, None, "time"),
+    (21, 2, 48, 32, 2, "fp16", False, True, None, "time"),
+    (11, 2, 33, 33, 1, "fp32", True, True, None, "batch"),
+    (13, 2, 32, 64, 1, "bf16", True, True, None, "time"),
+    (50, 6, 66, 16, 2, "fp32", True, True, [0, 50, 1, 16, 17, 33], "time"),
+    (50, 5, 40, 3, 1, "bf16", True, True, [49, 0, 32, 2, 48], "batch"),
+    (9, 4, 20, 40, 4, "fp32", False, True, [0, 9, 4, 5], "slice"),
+    (20, 4, 24, 16, 1, "fp16", True, True, [-3, 25, 20, 7], "time"),
+    (200, 1, 128, 16, 1, "fp32", True, True, None, "time"),
+    (1500, 1, 16, 16, 1, "fp32", True, True, None, "time"),
+    (700, 3, 40, 16, 2, "fp32", True, True, [700, 333, 0], "batch"),
+]
+
+
+@pytest.mark.parametrize("case", SCAN, ids=lambda c: "-".join(map(str, c[:6])))
+def test_scan(case):
+    log(f"scan {case}")
+    g, p = scan_problem(1, *case)
+    scan_check(g, p, case[7])
+
+
+def test_scan_without_optional_inputs():
+    g, p = scan_problem(2, 20, 2, 64, 16, 1, "fp32", False, True, None, "time", state0=False,
+                        extras=False)
+    out, state, grads = scan_run(g, True)
+    scan_check(g, p, True, (out, state, grads))
+
+
+def test_scan_empty_window_passes_the_state():
+    g, p = scan_problem(3, 0, 2, 33, 5, 1, "fp32", True, True, None, "time")
+    out, state, saved, _ = sgr.selective_scan_forward(
+        g["u"], g["delta"], g["A"], g["B"], g["C"], g["D"], g["z"], g["delta_bias"], g["state0"],
+        delta_softplus=True)
+    gr = sgr.selective_scan_backward(g["u"], g["delta"], g["A"], g["B"], g["C"], saved, g["go"],
+                                     g["D"], g["z"], g["delta_bias"], delta_softplus=True,
+                                     grad_state=g["gstate"])
+    torch.cuda.synchronize()
+    assert out.shape == (0, 2, 33)
+    assert torch.equal(state, g["state0"]) and torch.equal(gr["g_state0"], g["gstate"])
+    for k in ("g_A", "g_D", "g_delta_bias"):
+        assert not gr[k].any(), k
+
+
+def test_scan_broadcast_inputs_and_windows():
+    """u the same at every row and step (strides 0); a window cut in two gives
+    the whole window's outputs through the carried state."""
+    g, p = scan_problem(4, 37, 3, 64, 16, 1, "fp32", True, True, None, "time")
+    g["u"] = g["u"][:1, :1].expand(37, 3, 64)
+    p["u"] = np.broadcast_to(p["u"][:1, :1], p["u"].shape)
+    out, state, grads = scan_run(g, True)
+    scan_check(g, p, True, (out, state, grads))
+    part = lambda a, b, s: sgr.selective_scan_forward(
+        *(g[k][a:b] if k != "A" else g[k] for k in ("u", "delta", "A", "B", "C")), D=g["D"],
+        z=g["z"][a:b], delta_bias=g["delta_bias"], state0=s, delta_softplus=True, save=False)
+    o1, s1, saved, _ = part(0, 20, g["state0"])
+    o2, s2, _, _ = part(20, 37, s1)
+    assert saved is None
+    want, mag = ref.scan(p), ref.scan(p, magnitude=True)
+    close(torch.cat([o1, o2]), want["out"], mag["out"], 32 + 8 * 37, "out")
+    close(s2, want["state"], mag["state"], 32 + 8 * 37, "state")
+
+
+def test_scan_extremes():
+    """Large and infinite inputs: softplus and the gate saturate as the
+    definition does, and an infinite step forgets the state."""
+    T, D, N = 4, 8, 16
+    g, p = scan_problem(5, T, 1, D, N, 1, "fp32", True, True, None, "time")
+    for i, v in enumerate((-200.0, -30.0, 30.0, 300.0)):
+        g["delta"][:, :, i] = v
+        p["delta"][:, :, i] = v
+        g["z"][:, :, 4 + i] = v
+        p["z"][:, :, 4 + i] = v
+    scan_check(g, p, True)
+    g["delta"][2, 0, 0] = float("inf")
+    out, state, _, _ = sgr.selective_scan_forward(
+        g["u"], g["delta"], g["A"], g["B"], g["C"], state0=g["state0"], delta_softplus=True)
+    assert not torch.isfinite(out[2, 0, 0])          # inf * u * B
+    assert torch.isfinite(out[:, 0, 1:]).all()       # other channels do not see it
+    assert torch.isfinite(out[:2, 0, 0]).all()       # nor do earlier steps
+
+
+def test_scan_same_bits_every_time_and_on_another_stream():
+    g, p = scan_problem(6, 70, 2, 130, 16, 1, "bf16", True, True, [70, 41], "time")
+    a = scan_run(g, True)
+    b = scan_run(g, True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    c = scan_run(g, True, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    for o in (b, c):
+        assert torch.equal(a[0], o[0]) and torch.equal(a[1], o[1])
+        for k in a[2]:
+            assert torch.equal(a[2][k], o[2][k]), k
+
+
+@pytest.mark.parametrize("dtype,B,D,N,G", [("fp32", 1, 1, 1, 1), ("bf16", 3, 70, 16, 7),
+                                           ("fp16", 5, 64, 13, 1), ("bf16", 2, 130, 33, 2),
+                                           ("fp32", 4, 66, 64, 2), ("fp32", 2, 36, 6, 3)])
+def test_scan_step_walks_the_window(dtype, B, D, N, G):
+    """Single tokens, state in place, against the definition of the window."""
+    T = 6
+    g, p = scan_problem(7, T, B, D, N, G, dtype, True, True, None, "slice")
+    want, mag = ref.scan(p), ref.scan(p, magnitude=True)
+    state = g["state0"].clone()
+    outs = []
+    for t in range(T):
+        o, s = sgr.selective_scan_step(state, g["u"][t], g["delta"][t], g["A"], g["B"][t],
+                                       g["C"][t], g["D"], g["z"][t], g["delta_bias"], True)
+        assert s is state
+        outs.append(o)
+    close(torch.stack(outs), want["out"], mag["out"], 32 + 8 * T, "out")
+    close(state, want["state"], mag["state"], 32 + 8 * T, "state")
+    keep = g["state0"].clone()
+    o, s = sgr.selective_scan_step(g["state0"], g["u"][0], g["delta"][0], g["A"], g["B"][0],
+                                   g["C"][0], g["D"], g["z"][0], g["delta_bias"], True,
+                                   new_state=torch.empty_like(keep))
+    assert torch.equal(o, outs[0]) and torch.equal(g["state0"], keep)
+
+
+def test_scan_autograd_with_shared_inputs():
+    """Gradients through the autograd node where one tensor feeds several
+    inputs and B, C come from a broadcast, against fp64 autograd of the
+    definition written step by step."""
+    T, B, D, N = 12, 2, 24, 4
+    r = np.random.default_rng(8)
+    x0 = torch.from_numpy(r.standard_normal((T, B, D))).float()
+    bc0 = torch.from_numpy(r.standard_normal((T, 1, 1, N))).float()
+    a0 = torch.from_numpy(-r.uniform(0.1, 2, (D, N))).float()
+
+    def loss_of(x, bc, a, fn):
+        out, state = fn(x, 0.3 * x - 1, a, bc.expand(T, B, 1, N), bc.expand(T, B, 1, N), x)
+        return (out * out).sum() + state.sum()
+
+    def define(u, d, a, Bm, Cm, z):
+        h, outs = torch.zeros(B, D, N, dtype=u.dtype), []
+        for t in range(T):
+            dt = torch.nn.functional.softplus(d[t]).unsqueeze(-1)
+            h = torch.exp(dt * a) * h + dt * u[t].unsqueeze(-1) * Bm[t]
+            outs.append((h * Cm[t]).sum(-1) * z[t] * torch.sigmoid(z[t]))
+        return torch.stack(outs), h
+
+    lw = [t.double().requires_grad_() for t in (x0, bc0, a0)]
+    loss_of(*lw, define).backward()
+    lg = [t.cuda().requires_grad_() for t in (x0, bc0, a0)]
+    loss_of(*lg, lambda u, d, a, Bm, Cm, z: sgr.selective_scan(
+        u, d, a, Bm, Cm, z=z, delta_softplus=True)).backward()
+    for w, g, name in zip(lw, lg, ("x", "bc", "a")):
+        # rounding of sums of some hundred terms: 1e-5 of the largest gradient
+        scale = w.grad.abs().max().item()
+        assert (g.grad.double().cpu() - w.grad).abs().max().item() <= 1e-5 * scale, name
+
+
+# --------------------------------------------------------------- convolution
+
+def conv_problem(seed, T, B, D, W, dtype, silu, lengths, layout, state0=True, bias=True):
+    r = np.random.default_rng(seed)
+    ok = ref.valid(T, B, None if lengths is None else np.array(lengths))
+    pad = None if lengths is None else ok
+    gpu, p = {}, {"silu": silu, "lengths": None if lengths is None else np.array(lengths)}
+    gpu["x"], p["x"] = place(r.standard_normal((T, B, D)), DT[dtype], layout, pad)
+    gpu["gy"], p["gy"] = place(r.standard_normal((T, B, D)), DT[dtype], layout, pad)
+    gpu["weight"], p["weight"] = _f32(r.standard_normal((D, W)))
+    gpu["bias"] = gpu["state0"] = None
+    if bias:
+        gpu["bias"], p["bias"] = _f32(r.standard_normal(D))
+    for k in ("state0", "gstate") if state0 else ("gstate",):
+        t = torch.from_numpy(r.standard_normal((W - 1, B, D))).to(DT[dtype])
+        gpu[k], p[k] = t.cuda(), t.double().numpy()
+    gpu["lengths"] = None if lengths is None else torch.tensor(lengths, dtype=torch.int32,
+                                                               device="cuda")
+    return gpu, p
+
+
+def conv_run(g, silu, stream=None):
+    kw = dict(bias=g["bias"], state0=g["state0"], lengths=g["lengths"],
+              activation="silu" if silu else None, stream=stream)
+    y, state = sgr.short_conv_forward(g["x"], g["weight"], **kw)
+    return y, state, sgr.short_conv_backward(g["x"], g["weight"], g["gy"],
+                                             grad_state=g["gstate"], **kw)
+
+
+CONV = [  # T, B, D, W, dtype, silu, lengths, layout
+    (1, 1, 1, 4, "fp32", True, None, "time"),
+    (0, 2, 16, 4, "fp32", True, None, "time"),
+    (2, 3, 64, 4, "bf16", True, None, "time"),
+    (16, 2, 256, 4, "bf16", True, None, "time"),
+    (17, 2, 72, 3, "fp16", False, None, "batch"),
+    (33, 3, 1025, 4, "bf16", True, None, "time"),
+    (65, 2, 520, 2, "fp32", True, None, "batch"),
+    (40, 2, 64, 1, "fp32", True, None, "time"),
+    (40, 2, 64, 8, "bf16", True, None, "time"),
+    (70, 1, 24, 7, "fp32", True, None, "slice"),
+    (35, 2, 40, 5, "fp16", True, None, "time"),
+    (35, 2, 41, 6, "fp32", False, None, "batch"),
+    (50, 7, 64, 4, "bf16", True, [0, 1, 2, 3, 50, 32, 33], "time"),
+    (50, 6, 37, 4, "fp32", True, [0, 1, 2, 49, 16, 17], "batch"),
+    (4, 3, 16, 8, "fp32", False, [0, 3, 4], "time"),
+    (20, 4, 16, 4, "fp16", True, [-1, 21, 20, 5], "slice"),
+]
+
+
+@pytest.mark.parametrize("case", CONV, ids=lambda c: "-".join(map(str, c[:5])))
+@pytest.mark.parametrize("full", [True, False])
+def test_conv(case, full):
+    T, B, D, W, dtype, silu, lengths, layout = case
+    log(f"conv {case} full={full}")
+    g, p = conv_problem(1, *case, state0=full, bias=full)
+    want, mag = ref.conv(p), ref.conv(p, magnitude=True)
+    y, state, grads = conv_run(g, silu)
+    torch.cuda.synchronize()
+    close(y, want["y"], mag["y"], 16 + 2 * W, "y")
+    # the state is a copy of inputs
+    assert np.array_equal(state.double().cpu().numpy(), want["state"])
+    # sums over all steps and rows in runs and pieces of them
+    for k, n in (("g_x", W), ("g_state0", W), ("g_weight", T * B), ("g_bias", T * B)):
+        close(grads[k], want[k], mag[k], 24 + 2 * W + n, k)
+
+
+@pytest.mark.parametrize("dtype,B,D,W", [("fp32", 1, 1, 4), ("bf16", 3, 64, 4),
+                                         ("fp16", 2, 37, 3), ("fp32", 2, 20, 1),
+                                         ("bf16", 2, 2048, 8)])
+def test_conv_step_walks_the_window(dtype, B, D, W):
+    T = 2 * W + 1
+    g, p = conv_problem(2, T, B, D, W, dtype, True, None, "slice")
+    want, mag = ref.conv(p), ref.conv(p, magnitude=True)
+    state, ys = g["state0"].clone(), []
+    for t in range(T):
+        y, s = sgr.short_conv_step(state, g["x"][t], g["weight"], g["bias"], "silu")
+        assert s is state
+        ys.append(y)
+    close(torch.stack(ys), want["y"], mag["y"], 16 + 2 * W, "y")
+    assert np.array_equal(state.double().cpu().numpy(), want["state"])
+    keep = g["state0"].clone()
+    y, s = sgr.short_conv_step(g["state0"], g["x"][0], g["weight"], g["bias"], "silu",
+                               new_state=torch.empty_like(keep))
+    assert torch.equal(y, ys[0]) and torch.equal(g["state0"], keep)
+
+
+def test_conv_autograd():
+    """Through the autograd node, against fp64 differences along random
+    directions of the definition."""
+    g, p = conv_problem(3, 30, 2, 24, 4, "fp32", True, [30, 17], "time")
+    x = torch.nan_to_num(g["x"]).requires_grad_()
+    leaves = [x] + [g[k].clone().requires_grad_() for k in ("weight", "bias", "state0")]
+    y, state = sgr.short_conv(leaves[0], leaves[1], leaves[2], leaves[3], g["lengths"], "silu")
+    gy = torch.nan_to_num(g["gy"])
+    ((y * gy).sum() + (state * g["gstate"]).sum()).backward()
+    r = np.random.default_rng(9)
+    names = ("x", "weight", "bias", "state0")
+    q = {k: v for k, v in p.items() if k not in ("gy", "gstate")}
+    loss = lambda o: (o["y"] * ref.cut(p["gy"], ref.valid(30, 2, p["lengths"]))).sum() + \
+        (o["state"] * p["gstate"]).sum()
+    for leaf, k in zip(leaves, names):
+        d = r.standard_normal(p[k].shape)
+        e = 1e-6
+        hi, lo = (loss(ref.conv({**q, k: p[k] + s * e * d})) for s in (1, -1))
+        slope = (leaf.grad.double().cpu().numpy() * d).sum()
+        size = np.abs(leaf.grad.double().cpu().numpy() * d).sum()
+        # the difference is good to about 1e-8, the fp32 gradient to 100 roundings
+        assert abs(slope - (hi - lo) / (2 * e)) <= (100 * ref.U32 + 1e-7) * size, k
+
+
+def test_conv_same_bits_every_time():
+    g, _ = conv_problem(4, 100, 3, 200, 4, "bf16", True, [100, 50, 7], "time")
+    a, b = conv_run(g, True), conv_run(g, True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert all(torch.equal(a[2][k], b[2][k]) for k in a[2])
+
+
+# ------------------------------------------------------------------- dropout
+
+@pytest.mark.parametrize("T,B,D,dtype,layout", [
+    (1, 1, 1, "fp32", "time"), (5, 3, 64, "bf16", "time"), (9, 2, 37, "fp16", "batch"),
+    (17, 2, 1000, "fp32", "time"), (8, 3, 40, "bf16", "slice"), (0, 2, 8, "fp32", "time")])
+@pytest.mark.parametrize("held", [False, True])
+@pytest.mark.parametrize("p", [0.0, 0.1, 0.5, 1.0])
+def test_dropout(T, B, D, dtype, layout, held, p):
+    r = np.random.default_rng(10)
+    x, xv = place(r.standard_normal((T, B, D)), DT[dtype], layout)
+    res, rv = place(r.standard_normal((T, B, D)), DT[dtype], layout)
+    seed, offset = 0x123456789ABCDEF0, 0xFEDCBA9876543210
+    m, scale = ref.keep(T, B, D, p, seed, offset, held)
+    kw = dict(p=p, seed=seed, offset=offset, held=held)
+    for got, want in ((sgr.dropout_forward(x, **kw), m * xv * scale),
+                      (sgr.dropout_backward(x, **kw), m * xv * scale),
+                      (sgr.dropout_forward(x, residual=res, **kw), rv + m * xv * scale)):
+        # one product, one sum, the scale's own rounding
+        close(got, want, np.abs(rv) + np.abs(xv) * scale, 3, "out")
+    out = sgr.dropout_forward(x, **kw)
+    assert np.array_equal((out != 0).cpu().numpy(), m & (xv != 0))
+
+
+def test_dropout_nan_counter_in_place_and_autograd():
+    x = torch.randn(6, 4, 100, device="cuda")
+    m, scale = ref.keep(6, 4, 100, 0.4, 7, 3, True)
+    keep = torch.from_numpy(m.copy()).cuda()
+    bad = torch.where(keep, x, torch.full_like(x, float("nan")))
+    ok = sgr.dropout_forward(bad, 0.4, 7, 3, held=True)
+    assert torch.isfinite(ok).all() and not ok[~keep].any()
+    # the counter adds to the offset
+    c = torch.tensor([3], dtype=torch.int64, device="cuda")
+    assert torch.equal(sgr.dropout_forward(x, 0.4, 7, 0, held=True, counter=c),
+                       sgr.dropout_forward(x, 0.4, 7, 3, held=True))
+    y = x.clone()
+    assert sgr.dropout_forward(y, 0.4, 7, 3, held=True, out=y) is y
+    assert torch.equal(y, sgr.dropout_forward(x, 0.4, 7, 3, held=True))
+    leaf, res = x.clone().requires_grad_(), torch.randn_like(x).requires_grad_()
+    out = sgr.dropout(leaf, 0.4, 7, 0, residual=res, held=True, counter=c)
+    c += 5  # a later step's value does not change this step's mask
+    go = torch.randn_like(x)
+    out.backward(go)
+    assert torch.equal(leaf.grad, sgr.dropout_backward(go, 0.4, 7, 3, held=True))
+    assert torch.equal(res.grad, go)
+    # one step's rows, as in a token's path
+    assert torch.equal(sgr.dropout_forward(x[0], 0.4, 7, 3), sgr.dropout_forward(x[:1], 0.4, 7, 3)[0])
+
+
+# --------------------------------------------------- large offsets and graphs
+
+def test_offsets_past_32_bits():
+    """Rows of one storage more than 2^31 elements apart."""
+    far = 2 ** 31 + 64
+    T, D, N = 18, 64, 16
+    g, p = scan_problem(11, T, 2, D, N, 1, "bf16", True, True, None, "time")
+    store = torch.zeros(far + 4 * T * D, dtype=torch.bfloat16, device="cuda")
+    def spread(t, at):
+        v = store.as_strided((T, 2, D), (D, far, 1), at * T * D)
+        v.copy_(t)
+        return v
+    for i, k in enumerate(("u", "delta", "z", "go")):
+        g[k] = spread(g[k], i)
+    scan_check(g, p, True)
+    conv, q = conv_problem(12, T, 2, D, 4, "bf16", True, None, "time")
+    conv["x"], conv["gy"] = spread(conv["x"], 0), spread(conv["gy"], 1)
+    y, state, grads = conv_run(conv, True)
+    want, mag = ref.conv(q), ref.conv(q, magnitude=True)
+    close(y, want["y"], mag["y"], 24, "y")
+    close(grads["g_x"], want["g_x"], mag["g_x"], 36, "g_x")
+    x = spread(conv["x"], 2)
+    out = spread(torch.zeros(T, 2, D, dtype=torch.bfloat16, device="cuda"), 3)
+    sgr.dropout_forward(x, 0.5, 1, out=out)
+    assert torch.equal(out, sgr.dropout_forward(x.contiguous(), 0.5, 1))
+
+
+def test_captured_graph_replays():
+    """Forward, backward and tokens in one HIP graph: every replay equals the
+    eager result on the inputs of that moment, with eager work between."""
+    g, p = scan_problem(13, 40, 2, 64, 16, 1, "fp32", True, True, [40, 23], "time", nan=False)
+    w = torch.randn(64, 4, device="cuda")
+    counter = torch.zeros(1, dtype=torch.int64, device="cuda")
+    step_state = torch.zeros(2, 64, 16, device="cuda")
+
+    def work():
+        x, _ = sgr.short_conv_forward(g["u"], w, activation="silu")
+        h = dict(g, u=x)
+        out, state, grads = scan_run(h, True)
+        cg = sgr.short_conv_backward(g["u"], w, grads["g_u"], activation="silu")
+        tok, _ = sgr.selective_scan_step(step_state, x[0], g["delta"][0], g["A"], g["B"][0],
+                                         g["C"][0], new_state=torch.empty_like(step_state))
+        dr = sgr.dropout_forward(out, 0.3, 5, residual=x, counter=counter)
+        return [out, state, cg["g_x"], cg["g_weight"], tok, dr] + list(grads.values())
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        res = work()
+    for i in range(4):
+        g["u"].copy_(torch.randn_like(g["u"]))
+        counter.fill_(i)
+        graph.replay()
+        torch.cuda.synchronize()
+        for k, (a, b) in enumerate(zip(res, work())):
+            assert torch.equal(a, b), (i, k)
+
+
+def test_binding_refusals():
+    g, _ = scan_problem(14, 4, 2, 8, 4, 1, "fp32", True, True, None, "time")
+    args = lambda **kw: [{**g, **kw}[k] for k in ("u", "delta", "A", "B", "C")]
+    for kw, err in ((dict(u=g["u"].double()), TypeError), (dict(u=g["u"].cpu()), TypeError),
+                    (dict(delta=g["delta"].bfloat16()), TypeError),
+                    (dict(delta=g["delta"][:2]), ValueError),
+                    (dict(B=g["B"][:, :, :, :2]), ValueError),
+                    (dict(A=g["A"].bfloat16()), TypeError),
+                    (dict(u=g["u"].transpose(0, 2).contiguous().transpose(0, 2)), ValueError)):
+        with pytest.raises(err):
+            sgr.selective_scan_forward(*args(**kw))
+    with pytest.raises(ValueError):
+        sgr.selective_scan_forward(*args(), lengths=torch.zeros(3, dtype=torch.int32,
+                                                                device="cuda"))
+    with pytest.raises(TypeError):
+        sgr.selective_scan_forward(*args(), lengths=torch.zeros(2, dtype=torch.int64,
+                                                                device="cuda"))
+    with pytest.raises(ValueError):
+        sgr.selective_scan_backward(*args(), None, g["go"][:2])
+    with pytest.raises(ValueError):
+        sgr.short_conv_forward(g["u"], torch.ones(8, 4, device="cuda"), activation="tanh")
+    with pytest.raises(sgr.CkError):
+        sgr.short_conv_forward(g["u"], torch.ones(8, 9, device="cuda"))
+    with pytest.raises(sgr.CkError):
+        sgr.dropout_forward(g["u"], 1.5, 1)
+    # the autograd node takes what the calls refuse for its layout alone
+    u = g["u"].transpose(0, 2).contiguous().transpose(0, 2)
+    a, _ = sgr.selective_scan(*args(u=u))
+    assert torch.equal(a, sgr.selective_scan(*args())[0])
