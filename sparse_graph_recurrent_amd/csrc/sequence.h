@@ -11,7 +11,6 @@
 #include "ck_internal.h"
 
 namespace ckhip {
-namespace {
 
 typedef __bf16 bf16_t;
 typedef _Float16 f16_t;
@@ -171,5 +170,4 @@ __device__ __forceinline__ float quad_reduce4(float v0, float v1, float v2, floa
   return (odd ? r1 : r0) + quad_xor1(odd ? r0 : r1);
 }
 
-}  // namespace
 }  // namespace ckhip
