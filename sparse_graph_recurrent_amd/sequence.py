@@ -19,6 +19,7 @@ and ``*_step`` take one token per row, from and to the carried states.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -67,41 +68,64 @@ class DropoutShape(ctypes.Structure):
                 ("counter", ctypes.c_void_p)]
 
 
+# The calls fill these structures as packed bytes, several times quicker than
+# ctypes fills nested ones (a token's call takes about as long as its kernel).
+_SCAN_SHAPE = struct.Struct("=5q2i")
+_SCAN_INPUTS = struct.Struct("=20Q")
+_SCAN_GRADS = struct.Struct("=19Q")
+_CONV_SHAPE = struct.Struct("=4q2i")
+_DROP_SHAPE = struct.Struct("=3q2id3Q")
+assert _SCAN_SHAPE.size == ctypes.sizeof(ScanShape)
+assert _SCAN_INPUTS.size == ctypes.sizeof(ScanInputs)
+assert _SCAN_GRADS.size == ctypes.sizeof(ScanGrads)
+assert _CONV_SHAPE.size == ctypes.sizeof(ConvShape)
+assert _DROP_SHAPE.size == ctypes.sizeof(DropoutShape)
+
+_NONE = (0, 0, 0)  # a ck_seq that is absent
+
+
 def _declare(L: ctypes.CDLL) -> None:
-    """Argument types of the sequence entry points (called once, by ``lib``)."""
+    """Argument types of the sequence entry points (called once, by ``lib``).
+    Structures are passed by address: a ctypes instance or its bytes."""
     p, sz, q = ctypes.c_void_p, ctypes.c_size_t, CkSeq
     szp = ctypes.POINTER(sz)
-    scan, conv, drop = (ctypes.POINTER(s) for s in (ScanShape, ConvShape, DropoutShape))
-    inp, grads = ctypes.POINTER(ScanInputs), ctypes.POINTER(ScanGrads)
-    L.ck_scan_sizes.argtypes = [scan, szp, szp, szp]
-    L.ck_scan_forward.argtypes = [scan, inp, q, p, p, p, sz, p]
-    L.ck_scan_backward.argtypes = [scan, inp, p, q, p, grads, p, sz, p]
-    L.ck_scan_step.argtypes = [scan, inp, q, p, p]
-    L.ck_conv_sizes.argtypes = [conv, szp]
-    L.ck_conv_forward.argtypes = [conv, q, p, p, p, p, q, p, p]
-    L.ck_conv_backward.argtypes = [conv, q, p, p, p, p, q, p, q, p, p, p, p, sz, p]
-    L.ck_conv_step.argtypes = [conv, q, p, p, p, q, p, p]
-    L.ck_dropout_forward.argtypes = [drop, q, q, q, p]
-    L.ck_dropout_backward.argtypes = [drop, q, q, p]
+    L.ck_scan_sizes.argtypes = [_Struct, szp, szp, szp]
+    L.ck_scan_forward.argtypes = [_Struct, _Struct, q, p, p, p, sz, p]
+    L.ck_scan_backward.argtypes = [_Struct, _Struct, p, q, p, _Struct, p, sz, p]
+    L.ck_scan_step.argtypes = [_Struct, _Struct, q, p, p]
+    L.ck_conv_sizes.argtypes = [_Struct, szp]
+    L.ck_conv_forward.argtypes = [_Struct, q, p, p, p, p, q, p, p]
+    L.ck_conv_backward.argtypes = [_Struct, q, p, p, p, p, q, p, q, p, p, p, p, sz, p]
+    L.ck_conv_step.argtypes = [_Struct, q, p, p, p, q, p, p]
+    L.ck_dropout_forward.argtypes = [_Struct, q, q, q, p]
+    L.ck_dropout_backward.argtypes = [_Struct, q, q, p]
 
 
-class _On:
-    """The device and stream of a call: makes the tensors' device current while
-    the library runs, and keeps the memory of tensors made here from being
-    reused while a stream other than the current one still works on them."""
+class _Struct:
+    """Argument converter of ``const struct*`` parameters."""
 
-    def __init__(self, device: torch.device, stream):
-        self.device = device
-        self.stream = stream
+    @classmethod
+    def from_param(cls, v):
+        if v is None or isinstance(v, bytes):
+            return ctypes.c_char_p(v)
+        return ctypes.byref(v)
 
-    def __call__(self, fn, *args, made=()):
-        with torch.cuda.device(self.device):
-            s = torch.cuda.current_stream() if self.stream is None else self.stream
-            _check(fn(*args, ctypes.c_void_p(s.cuda_stream)))
-            if self.stream is not None:
-                for t in made:
-                    if t is not None:
-                        t.record_stream(s)
+
+def _call(fn, like: torch.Tensor, stream, args, made=()):
+    """Runs one entry point with like's device current on `stream` (None: the
+    current one); memory of the tensors in `made`, allocated here for another
+    stream than the current, is kept from reuse until that stream is done."""
+    dev = like.device.index
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(fn, like, stream, args, made)
+    if stream is None:
+        _check(fn(*args, torch._C._cuda_getCurrentRawStream(dev)))
+        return
+    _check(fn(*args, stream.cuda_stream))
+    for t in made:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _adjacent(t: torch.Tensor, last: int) -> bool:
@@ -114,49 +138,52 @@ def _adjacent(t: torch.Tensor, last: int) -> bool:
     return True
 
 
-def _seq(t: torch.Tensor, name: str, like: torch.Tensor, shape, last: int = 1) -> CkSeq:
-    """The ck_seq of a [T, B, ...] tensor (a step's [B, ...] tensor counts as T = 1)."""
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+def _seq(t: torch.Tensor, name: str, like: torch.Tensor, shape, last: int = 1):
+    """(address, stride_t, stride_b) of a [T, B, ...] tensor (a step's [B, ...]
+    tensor counts as T = 1), checked."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.dtype != like.dtype:
         raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.numel() == 0:
-        return CkSeq(None, 0, 0)
-    if not _adjacent(t, last):
-        raise ValueError(f"{name} must have its last {last} dimension(s) contiguous")
-    st = t.stride()
-    lead = t.dim() - last  # [T, B] or [B]
-    return CkSeq(t.data_ptr(), st[0] if lead == 2 and t.shape[0] > 1 else 0,
-                 st[lead - 1] if t.shape[lead - 1] > 1 else 0)
-
-
-def _par(t, name: str, like: torch.Tensor, shape, dtype=torch.float32):
-    """Pointer of an optional contiguous parameter, state or length vector."""
-    if t is None:
-        return None
-    _dev(t, name, dtype, shape)
     if t.device != like.device:
         raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-    return t.data_ptr() if t.numel() else None
+    if t.numel() == 0:
+        return _NONE
+    st = t.stride()
+    if last == 1 and st[-1] != 1 or last == 2 and (st[-1] != 1 or st[-2] != shape[-1]):
+        if not _adjacent(t, last):  # sizes of 1 may have any stride
+            raise ValueError(f"{name} must have its last {last} dimension(s) contiguous")
+    if len(shape) - last == 1:
+        return t.data_ptr(), 0, st[0] if shape[0] > 1 else 0
+    return t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0
 
 
-def _first(t, name: str, dims) -> torch.Tensor:
-    """The tensor that gives a call its type, device and sizes."""
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+def _par(t, name: str, like: torch.Tensor, shape, dtype=torch.float32) -> int:
+    """Address of an optional contiguous parameter, state or length vector."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _dev(t, name, dtype, shape)
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    return t.data_ptr() if t.numel() else 0
+
+
+def _first(t, name: str, dims) -> int:
+    """Checks the tensor that gives a call its type, device and sizes; its ck_dtype."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.dtype not in _DTYPES:
         raise TypeError(f"{name} must be fp32, bf16 or fp16, got {t.dtype}")
     if t.dim() not in dims:
         raise ValueError(f"{name} must have {' or '.join(map(str, dims))} dimensions, "
                          f"got {t.dim()}")
-    return t
+    return _DTYPES[t.dtype]
 
 
-def _into(t, name: str, like: torch.Tensor, shape, dtype=None):
+def _into(t, like: torch.Tensor, shape, dtype=None):
     """(tensor, was made here) of an output: the caller's, or a new one."""
     if t is not None:
         return t, False
@@ -179,41 +206,34 @@ def _bytes(buf) -> int:
 # ------------------------------------------------------------ selective scan
 
 def _scan_call(u, delta, A, B, C, D, z, delta_bias, state0, lengths, delta_softplus, step=False):
-    """(shape, inputs) structures of a scan call, checked."""
-    _first(u, "u", (2,) if step else (3,))
-    lead = tuple(u.shape[:-1])
-    ch = u.shape[-1]
+    """(shape, inputs, sizes (T, B, D, N, G)) of a scan call, checked."""
+    dtype = _first(u, "u", (2,) if step else (3,))
+    us = u.shape
     if not isinstance(A, torch.Tensor) or A.dim() != 2:
         raise ValueError("A must be a [channels, states] tensor")
-    if not isinstance(B, torch.Tensor) or B.dim() != u.dim() + 1:
-        raise ValueError(f"B must have {u.dim() + 1} dimensions (.., groups, states)")
+    if not isinstance(B, torch.Tensor) or B.dim() != len(us) + 1:
+        raise ValueError(f"B must have {len(us) + 1} dimensions (.., groups, states)")
+    T, rows, ch = (1,) + us if step else us
     N, G = A.shape[1], B.shape[-2]
-    T, rows = (1,) + lead if step else lead
-    shape = ScanShape(T, rows, ch, N, G, _DTYPES[u.dtype], 1 if delta_softplus else 0)
-    none = CkSeq(None, 0, 0)
-    return shape, ScanInputs(
-        _seq(u, "u", u, lead + (ch,)), _seq(delta, "delta", u, lead + (ch,)),
-        _seq(B, "B", u, lead + (G, N), 2), _seq(C, "C", u, lead + (G, N), 2),
-        none if z is None else _seq(z, "z", u, lead + (ch,)),
+    bs = us[:-1] + (G, N)
+    sizes = (T, rows, ch, N, G)
+    return _SCAN_SHAPE.pack(*sizes, dtype, 1 if delta_softplus else 0), _SCAN_INPUTS.pack(
+        *_seq(u, "u", u, us), *_seq(delta, "delta", u, us), *_seq(B, "B", u, bs, 2),
+        *_seq(C, "C", u, bs, 2), *(_NONE if z is None else _seq(z, "z", u, us)),
         _par(A, "A", u, (ch, N)), _par(D, "D", u, (ch,)),
         _par(delta_bias, "delta_bias", u, (ch,)), _par(state0, "state0", u, (rows, ch, N)),
-        _par(lengths, "lengths", u, (rows,), torch.int32))
-
-
-def selective_scan_sizes(T: int, B: int, D: int, N: int, G: int = 1, dtype=torch.float32):
-    """(saved_bytes, forward_bytes, backward_bytes) of ``ck_scan_sizes``."""
-    s, f, b = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t()
-    shape = ScanShape(int(T), int(B), int(D), int(N), int(G), _DTYPES[dtype], 0)
-    _check(lib().ck_scan_sizes(ctypes.byref(shape), ctypes.byref(s), ctypes.byref(f),
-                               ctypes.byref(b)))
-    return s.value, f.value, b.value
+        _par(lengths, "lengths", u, (rows,), torch.int32)), sizes
 
 
 def _scan_sizes(shape):
     s, f, b = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t()
-    _check(lib().ck_scan_sizes(ctypes.byref(shape), ctypes.byref(s), ctypes.byref(f),
-                               ctypes.byref(b)))
+    _check(lib().ck_scan_sizes(shape, ctypes.byref(s), ctypes.byref(f), ctypes.byref(b)))
     return s.value, f.value, b.value
+
+
+def selective_scan_sizes(T: int, B: int, D: int, N: int, G: int = 1, dtype=torch.float32):
+    """(saved_bytes, forward_bytes, backward_bytes) of ``ck_scan_sizes``."""
+    return _scan_sizes(ScanShape(int(T), int(B), int(D), int(N), int(G), _DTYPES[dtype], 0))
 
 
 def selective_scan_forward(u, delta, A, B, C, D=None, z=None, delta_bias=None, state0=None,
@@ -224,20 +244,20 @@ def selective_scan_forward(u, delta, A, B, C, D=None, z=None, delta_bias=None, s
     u, delta, z: [T, B, D]; B, C: [T, B, G, N]; A: [D, N]; D, delta_bias: [D];
     state0 and the returned state: [B, D, N].  ``saved`` is what
     ``selective_scan_backward`` needs (None with save=False)."""
-    shape, inp = _scan_call(u, delta, A, B, C, D, z, delta_bias, state0, lengths, delta_softplus)
+    shape, inputs, (T, rows, ch, N, _) = _scan_call(u, delta, A, B, C, D, z, delta_bias, state0,
+                                                    lengths, delta_softplus)
     sb, fb, _ = _scan_sizes(shape)
-    out, m0 = _into(out, "out", u, u.shape)
-    state, m1 = _into(state, "state", u, (shape.B, shape.D, shape.N), torch.float32)
+    out, m0 = _into(out, u, u.shape)
+    state, m1 = _into(state, u, (rows, ch, N), torch.float32)
     m2, m3 = saved is None, workspace is None
     saved = _buffer(saved, sb, u, "saved") if save or not m2 else None
     workspace = _buffer(workspace, fb, u, "workspace")
-    o = _seq(out, "out", u, u.shape)
-    st = _par(state, "state", u, (shape.B, shape.D, shape.N))
-    _On(u.device, stream)(
-        lib().ck_scan_forward, ctypes.byref(shape), ctypes.byref(inp), o, st, _ptr(saved),
-        _ptr(workspace), _bytes(workspace),
-        made=(out if m0 else None, state if m1 else None, saved if m2 else None,
-              workspace if m3 else None))
+    _call(lib().ck_scan_forward, u, stream,
+          (shape, inputs, CkSeq(*_seq(out, "out", u, u.shape)),
+           _par(state, "state", u, (rows, ch, N)), _ptr(saved), _ptr(workspace),
+           _bytes(workspace)),
+          (out if m0 else None, state if m1 else None, saved if m2 else None,
+           workspace if m3 else None))
     return out, state, saved, workspace
 
 
@@ -247,39 +267,37 @@ def selective_scan_backward(u, delta, A, B, C, saved, grad_out, D=None, z=None, 
     """Run ``ck_scan_backward``; returns the gradients (overwritten) by the
     names g_u, g_delta, g_A, g_B, g_C, g_D, g_delta_bias, g_state0 and, with a
     gate, g_z."""
-    shape, inp = _scan_call(u, delta, A, B, C, D, z, delta_bias, None, lengths, delta_softplus)
+    shape, inputs, (T, rows, ch, N, _) = _scan_call(u, delta, A, B, C, D, z, delta_bias, None,
+                                                    lengths, delta_softplus)
     sb, _, wb = _scan_sizes(shape)
-    saved = _buffer(saved, sb, u, "saved") if sb else None
     if sb and saved is None:
         raise ValueError("saved is missing")
-    go = _seq(grad_out, "grad_out", u, u.shape)
-    state = (shape.B, shape.D, shape.N)
-    gs = _par(grad_state, "grad_state", u, state)
+    saved = _buffer(saved, sb, u, "saved")
+    us, bs, state = u.shape, B.shape, (rows, ch, N)
+    go = CkSeq(*_seq(grad_out, "grad_out", u, us))
     m0, m1 = grads is None, workspace is None
     if m0:
+        e = dict(dtype=u.dtype, device=u.device)
         f = dict(dtype=torch.float32, device=u.device)
-        grads = {"g_u": torch.empty(u.shape, dtype=u.dtype, device=u.device),
-                 "g_delta": torch.empty(u.shape, dtype=u.dtype, device=u.device),
-                 "g_A": torch.empty(A.shape, **f),
-                 "g_B": torch.empty(B.shape, dtype=u.dtype, device=u.device),
-                 "g_C": torch.empty(B.shape, dtype=u.dtype, device=u.device),
-                 "g_D": torch.empty(shape.D, **f), "g_delta_bias": torch.empty(shape.D, **f),
-                 "g_state0": torch.empty(state, **f)}
+        grads = {"g_u": torch.empty(us, **e), "g_delta": torch.empty(us, **e),
+                 "g_A": torch.empty(A.shape, **f), "g_B": torch.empty(bs, **e),
+                 "g_C": torch.empty(bs, **e), "g_D": torch.empty(ch, **f),
+                 "g_delta_bias": torch.empty(ch, **f), "g_state0": torch.empty(state, **f)}
         if z is not None:
-            grads["g_z"] = torch.empty(u.shape, dtype=u.dtype, device=u.device)
+            grads["g_z"] = torch.empty(us, **e)
     g = grads
-    out = ScanGrads(
-        _seq(g["g_u"], "g_u", u, u.shape), _seq(g["g_delta"], "g_delta", u, u.shape),
-        _seq(g["g_B"], "g_B", u, B.shape, 2), _seq(g["g_C"], "g_C", u, B.shape, 2),
-        CkSeq(None, 0, 0) if z is None else _seq(g["g_z"], "g_z", u, u.shape),
-        _par(g["g_A"], "g_A", u, A.shape), _par(g.get("g_D"), "g_D", u, (shape.D,)),
-        _par(g.get("g_delta_bias"), "g_delta_bias", u, (shape.D,)),
+    out = _SCAN_GRADS.pack(
+        *_seq(g["g_u"], "g_u", u, us), *_seq(g["g_delta"], "g_delta", u, us),
+        *_seq(g["g_B"], "g_B", u, bs, 2), *_seq(g["g_C"], "g_C", u, bs, 2),
+        *(_NONE if z is None else _seq(g["g_z"], "g_z", u, us)),
+        _par(g["g_A"], "g_A", u, A.shape), _par(g.get("g_D"), "g_D", u, (ch,)),
+        _par(g.get("g_delta_bias"), "g_delta_bias", u, (ch,)),
         _par(g.get("g_state0"), "g_state0", u, state))
     workspace = _buffer(workspace, wb, u, "workspace")
-    _On(u.device, stream)(
-        lib().ck_scan_backward, ctypes.byref(shape), ctypes.byref(inp), _ptr(saved), go, gs,
-        ctypes.byref(out), _ptr(workspace), _bytes(workspace),
-        made=(tuple(grads.values()) if m0 else ()) + ((workspace,) if m1 else ()))
+    _call(lib().ck_scan_backward, u, stream,
+          (shape, inputs, _ptr(saved), go, _par(grad_state, "grad_state", u, state), out,
+           _ptr(workspace), _bytes(workspace)),
+          (tuple(grads.values()) if m0 else ()) + ((workspace,) if m1 else ()))
     return grads
 
 
@@ -288,16 +306,15 @@ def selective_scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=Non
     """Run ``ck_scan_step``: one token per row.  u, delta, z: [B, D]; B, C:
     [B, G, N]; state: [B, D, N], updated in place unless ``new_state`` is
     given.  Returns (out [B, D], the new state)."""
-    shape, inp = _scan_call(u, delta, A, B, C, D, z, delta_bias, state, None, delta_softplus,
-                            step=True)
     if state is None:
         raise ValueError("state is missing")
+    shape, inputs, (_, rows, ch, N, _) = _scan_call(u, delta, A, B, C, D, z, delta_bias, state,
+                                                    None, delta_softplus, step=True)
     new_state = state if new_state is None else new_state
-    out, made = _into(out, "out", u, u.shape)
-    o = _seq(out, "out", u, u.shape)
-    st = _par(new_state, "new_state", u, (shape.B, shape.D, shape.N))
-    _On(u.device, stream)(lib().ck_scan_step, ctypes.byref(shape), ctypes.byref(inp), o, st,
-                          made=(out,) if made else ())
+    out, made = _into(out, u, u.shape)
+    _call(lib().ck_scan_step, u, stream,
+          (shape, inputs, CkSeq(*_seq(out, "out", u, u.shape)),
+           _par(new_state, "new_state", u, (rows, ch, N))), (out,) if made else ())
     return out, new_state
 
 
@@ -352,16 +369,17 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, state0=No
 # --------------------------------------------------------- short convolution
 
 def _conv_call(x, weight, bias, activation, step=False):
-    _first(x, "x", (2,) if step else (3,))
-    if activation not in (None, "silu"):
+    """(shape, state shape, x's ck_seq, weight, bias) of a convolution call, checked."""
+    dtype = _first(x, "x", (2,) if step else (3,))
+    if activation is not None and activation != "silu":
         raise ValueError(f"activation must be None or 'silu', got {activation!r}")
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be a [channels, taps] tensor")
-    T, rows, ch = (1,) + tuple(x.shape) if step else tuple(x.shape)
+    T, rows, ch = (1,) + x.shape if step else x.shape
     W = weight.shape[1]
-    shape = ConvShape(T, rows, ch, W, _DTYPES[x.dtype], 1 if activation else 0)
-    return (shape, (W - 1, rows, ch), _seq(x, "x", x, x.shape),
-            _par(weight, "weight", x, (ch, W)), _par(bias, "bias", x, (ch,)))
+    return (_CONV_SHAPE.pack(T, rows, ch, W, dtype, 1 if activation else 0), (W - 1, rows, ch),
+            CkSeq(*_seq(x, "x", x, x.shape)), _par(weight, "weight", x, (ch, W)),
+            _par(bias, "bias", x, (ch,)))
 
 
 def short_conv_forward(x, weight, bias=None, state0=None, lengths=None, activation=None, y=None,
@@ -369,14 +387,13 @@ def short_conv_forward(x, weight, bias=None, state0=None, lengths=None, activati
     """Run ``ck_conv_forward``; returns (y, state).  x: [T, B, D]; weight:
     [D, W]; bias: [D]; state0 and the returned state: [W - 1, B, D], the last
     inputs of each row; activation: None or "silu"."""
-    shape, sshape, xs, w, b = _conv_call(x, weight, bias, activation)
-    s0 = _par(state0, "state0", x, sshape, x.dtype)
-    ln = _par(lengths, "lengths", x, (shape.B,), torch.int32)
-    y, m0 = _into(y, "y", x, x.shape)
-    state, m1 = _into(state, "state", x, sshape)
-    ys, st = _seq(y, "y", x, x.shape), _par(state, "state", x, sshape, x.dtype)
-    _On(x.device, stream)(lib().ck_conv_forward, ctypes.byref(shape), xs, w, b, s0, ln, ys, st,
-                          made=(y if m0 else None, state if m1 else None))
+    shape, ss, xs, w, b = _conv_call(x, weight, bias, activation)
+    y, m0 = _into(y, x, x.shape)
+    state, m1 = _into(state, x, ss)
+    _call(lib().ck_conv_forward, x, stream,
+          (shape, xs, w, b, _par(state0, "state0", x, ss, x.dtype),
+           _par(lengths, "lengths", x, (ss[1],), torch.int32), CkSeq(*_seq(y, "y", x, x.shape)),
+           _par(state, "state", x, ss, x.dtype)), (y if m0 else None, state if m1 else None))
     return y, state
 
 
@@ -384,28 +401,27 @@ def short_conv_backward(x, weight, grad_y, bias=None, state0=None, lengths=None,
                         grad_state=None, grads=None, workspace=None, stream=None) -> dict:
     """Run ``ck_conv_backward``; returns the gradients (overwritten) g_x,
     g_weight, g_bias and g_state0."""
-    shape, sshape, xs, w, b = _conv_call(x, weight, bias, activation)
-    s0 = _par(state0, "state0", x, sshape, x.dtype)
-    ln = _par(lengths, "lengths", x, (shape.B,), torch.int32)
-    gy = _seq(grad_y, "grad_y", x, x.shape)
-    gs = _par(grad_state, "grad_state", x, sshape, x.dtype)
+    shape, ss, xs, w, b = _conv_call(x, weight, bias, activation)
     need = ctypes.c_size_t()
-    _check(lib().ck_conv_sizes(ctypes.byref(shape), ctypes.byref(need)))
+    _check(lib().ck_conv_sizes(shape, ctypes.byref(need)))
     m0, m1 = grads is None, workspace is None
     if m0:
         f = dict(dtype=torch.float32, device=x.device)
         grads = {"g_x": torch.empty(x.shape, dtype=x.dtype, device=x.device),
-                 "g_weight": torch.empty(weight.shape, **f), "g_bias": torch.empty(shape.D, **f),
-                 "g_state0": torch.empty(sshape, dtype=x.dtype, device=x.device)}
+                 "g_weight": torch.empty(weight.shape, **f), "g_bias": torch.empty(ss[2], **f),
+                 "g_state0": torch.empty(ss, dtype=x.dtype, device=x.device)}
     workspace = _buffer(workspace, need.value, x, "workspace")
-    gx = _seq(grads["g_x"], "g_x", x, x.shape)
-    gw = _par(grads["g_weight"], "g_weight", x, weight.shape)
-    gb = _par(grads.get("g_bias"), "g_bias", x, (shape.D,))
-    gs0 = _par(grads.get("g_state0"), "g_state0", x, sshape, x.dtype)
-    _On(x.device, stream)(
-        lib().ck_conv_backward, ctypes.byref(shape), xs, w, b, s0, ln, gy, gs, gx, gw, gb, gs0,
-        _ptr(workspace), _bytes(workspace),
-        made=(tuple(grads.values()) if m0 else ()) + ((workspace,) if m1 else ()))
+    _call(lib().ck_conv_backward, x, stream,
+          (shape, xs, w, b, _par(state0, "state0", x, ss, x.dtype),
+           _par(lengths, "lengths", x, (ss[1],), torch.int32),
+           CkSeq(*_seq(grad_y, "grad_y", x, x.shape)),
+           _par(grad_state, "grad_state", x, ss, x.dtype),
+           CkSeq(*_seq(grads["g_x"], "g_x", x, x.shape)),
+           _par(grads["g_weight"], "g_weight", x, weight.shape),
+           _par(grads.get("g_bias"), "g_bias", x, (ss[2],)),
+           _par(grads.get("g_state0"), "g_state0", x, ss, x.dtype), _ptr(workspace),
+           _bytes(workspace)),
+          (tuple(grads.values()) if m0 else ()) + ((workspace,) if m1 else ()))
     return grads
 
 
@@ -414,13 +430,13 @@ def short_conv_step(state, x, weight, bias=None, activation=None, y=None, new_st
     """Run ``ck_conv_step``: one token per row.  x: [B, D]; state: [W - 1, B,
     D], updated in place unless ``new_state`` is given.  Returns (y [B, D],
     the new state)."""
-    shape, sshape, xs, w, b = _conv_call(x, weight, bias, activation, step=True)
-    s0 = _par(state, "state", x, sshape, x.dtype)
+    shape, ss, xs, w, b = _conv_call(x, weight, bias, activation, step=True)
     new_state = state if new_state is None else new_state
-    y, made = _into(y, "y", x, x.shape)
-    ys, st = _seq(y, "y", x, x.shape), _par(new_state, "new_state", x, sshape, x.dtype)
-    _On(x.device, stream)(lib().ck_conv_step, ctypes.byref(shape), xs, w, b, s0, ys, st,
-                          made=(y,) if made else ())
+    y, made = _into(y, x, x.shape)
+    _call(lib().ck_conv_step, x, stream,
+          (shape, xs, w, b, _par(state, "state", x, ss, x.dtype),
+           CkSeq(*_seq(y, "y", x, x.shape)), _par(new_state, "new_state", x, ss, x.dtype)),
+          (y,) if made else ())
     return y, new_state
 
 
@@ -454,12 +470,13 @@ def short_conv(x, weight, bias=None, state0=None, lengths=None, activation=None)
 # ------------------------------------------------------------------- dropout
 
 def _drop_call(x, name, p, seed, offset, held, counter):
-    _first(x, name, (2, 3))
-    T, rows, ch = (1,) + tuple(x.shape) if x.dim() == 2 else tuple(x.shape)
+    """(shape, x's ck_seq) of a dropout call, checked."""
+    dtype = _first(x, name, (2, 3))
+    T, rows, ch = (1,) + x.shape if x.dim() == 2 else x.shape
     m = 0xFFFFFFFFFFFFFFFF
-    shape = DropoutShape(T, rows, ch, _DTYPES[x.dtype], 1 if held else 0, float(p), int(seed) & m,
-                         int(offset) & m, _par(counter, "counter", x, (1,), torch.int64))
-    return shape, _seq(x, name, x, x.shape)
+    return _DROP_SHAPE.pack(T, rows, ch, dtype, 1 if held else 0, p, seed & m, offset & m,
+                            _par(counter, "counter", x, (1,), torch.int64)), \
+        CkSeq(*_seq(x, name, x, x.shape))
 
 
 def dropout_forward(x, p: float, seed: int, offset: int = 0, residual=None, held: bool = False,
@@ -471,11 +488,11 @@ def dropout_forward(x, p: float, seed: int, offset: int = 0, residual=None, held
     offset, so that a replayed graph can draw new masks.  ``out`` may be x or
     the residual."""
     shape, xs = _drop_call(x, "x", p, seed, offset, held, counter)
-    rs = CkSeq(None, 0, 0) if residual is None else _seq(residual, "residual", x, x.shape)
-    out, made = _into(out, "out", x, x.shape)
-    o = _seq(out, "out", x, x.shape)
-    _On(x.device, stream)(lib().ck_dropout_forward, ctypes.byref(shape), xs, rs, o,
-                          made=(out,) if made else ())
+    out, made = _into(out, x, x.shape)
+    _call(lib().ck_dropout_forward, x, stream,
+          (shape, xs, CkSeq(*(_NONE if residual is None else
+                              _seq(residual, "residual", x, x.shape))),
+           CkSeq(*_seq(out, "out", x, x.shape))), (out,) if made else ())
     return out
 
 
@@ -483,10 +500,10 @@ def dropout_backward(grad_out, p: float, seed: int, offset: int = 0, held: bool 
                      counter=None, grad_x=None, stream=None) -> torch.Tensor:
     """Run ``ck_dropout_backward``: the forward's mask and scale on grad_out."""
     shape, gs = _drop_call(grad_out, "grad_out", p, seed, offset, held, counter)
-    grad_x, made = _into(grad_x, "grad_x", grad_out, grad_out.shape)
-    o = _seq(grad_x, "grad_x", grad_out, grad_out.shape)
-    _On(grad_out.device, stream)(lib().ck_dropout_backward, ctypes.byref(shape), gs, o,
-                                 made=(grad_x,) if made else ())
+    grad_x, made = _into(grad_x, grad_out, grad_out.shape)
+    _call(lib().ck_dropout_backward, grad_out, stream,
+          (shape, gs, CkSeq(*_seq(grad_x, "grad_x", grad_out, grad_out.shape))),
+          (grad_x,) if made else ())
     return grad_x
 
 
