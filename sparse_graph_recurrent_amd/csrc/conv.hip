@@ -4,7 +4,7 @@
 //   p_t = bias + sum_k w_k x_{t - (W-1) + k},   y_t = p_t or p_t sigmoid(p_t)
 //
 // HBM bounds all three (2 W + 4 operations an element against 4 to 8 bytes):
-// a thread owns V adjacent channels (16 bytes) and walks a run of steps with
+// a thread owns four adjacent channels and walks a run of steps with
 // the last W - 1 inputs in registers, so that within a run every input is
 // read once; a run reads W - 1 steps before it again (and after it, in the
 // backward).
@@ -23,6 +23,8 @@ constexpr int64_t kConvMaxW = 8;
 constexpr int kConvThreads = 256;
 constexpr int kConvRun = 16;     // steps per thread, forward
 constexpr int kConvRunBwd = 32;  // and backward, whose run reads 2 (W - 1) steps more
+constexpr int kConvAhead = 4;    // rows in flight: loaded while the ones before are worked on
+constexpr int kConvV = 4;        // channels per thread
 
 template <typename E>
 struct ConvArgs {
@@ -32,9 +34,9 @@ struct ConvArgs {
   const E *state0, *gstate;
   E *state, *gstate0;
   const int32_t* lengths;
-  float* part;   // backward: [parts][D][W + 1]
+  float* part;   // backward: [parts][W + 1][D]
   int T, B, D;
-  int nv;        // channel groups of V
+  int nv;        // channel groups of kConvV
   int vx;        // of them per workgroup (a power of two at most 64)
   int runs;      // runs of the window
   int silu;
@@ -42,11 +44,12 @@ struct ConvArgs {
 
 struct ConvPlace {
   int b, run, c, len;
+  int n;        // channels of this group (fewer than kConvV at the end of a row)
   bool active;
 };
 
 // Workgroup: vx channel groups times 256 / vx (row, run) pairs.
-template <int V, typename E>
+template <typename E>
 __device__ __forceinline__ ConvPlace conv_place(const ConvArgs<E>& s) {
   ConvPlace p;
   const int vblocks = (s.nv + s.vx - 1) / s.vx;
@@ -54,7 +57,8 @@ __device__ __forceinline__ ConvPlace conv_place(const ConvArgs<E>& s) {
   const int64_t br = (int64_t)(blockIdx.x / vblocks) * (kConvThreads / s.vx) +
                      (int)threadIdx.x / s.vx;
   p.active = vi < s.nv && br < (int64_t)s.B * s.runs;
-  p.c = vi * V;
+  p.c = vi * kConvV;
+  p.n = s.D - p.c;
   p.run = (int)(br % s.runs);
   p.b = (int)min(br / s.runs, (int64_t)s.B - 1);
   p.len = s.T;
@@ -62,156 +66,219 @@ __device__ __forceinline__ ConvPlace conv_place(const ConvArgs<E>& s) {
   return p;
 }
 
-template <int V, int W>
+constexpr int V = kConvV;
+
+template <bool FULL, int W>
 __device__ __forceinline__ void conv_weights(float (&w)[W][V], float (&bias)[V],
-                                             const float* weight, const float* b, int c) {
+                                             const float* weight, const float* b, int c, int n) {
+  const Pack<float, V * W> wp =
+      pack_load<FULL, float, V * W>(weight + (int64_t)c * W, n * W);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
+  for (int i = 0; i < V; ++i)
 #pragma unroll
-    for (int k = 0; k < W; ++k) w[k][i] = weight[(int64_t)(c + i) * W + k];
-    bias[i] = b ? b[c + i] : 0.0f;
-  }
+    for (int k = 0; k < W; ++k) w[k][i] = wp.v[i * W + k];
+  Pack<float, V> bp = {};
+  if (b) bp = pack_load<FULL, float, V>(b + c, n);
+#pragma unroll
+  for (int i = 0; i < V; ++i) bias[i] = bp.v[i];
 }
 
 // Input at step t, which may lie before the window (state0) but not at or
 // past the row's length.
-template <int V, int W, typename E>
-__device__ __forceinline__ void conv_input(float (&x)[V], const ConvArgs<E>& s, int b, int c,
-                                           int t) {
-  if (t >= 0) {
-    pack_load<E, V>(x, s.x.row(t, b) + c);
-  } else if (s.state0) {
-    pack_load<E, V>(x, s.state0 + ((int64_t)(t + W - 1) * s.B + b) * s.D + c);
-  } else {
+template <bool FULL, int W, typename E>
+__device__ __forceinline__ void conv_input(float (&x)[V], const ConvArgs<E>& s,
+                                           const ConvPlace& p, int t) {
+  Pack<E, V> v = {};
+  if (t >= 0)
+    v = pack_load<FULL, E, V>(s.x.row(t, p.b) + p.c, p.n);
+  else if (s.state0)
+    v = pack_load<FULL, E, V>(s.state0 + ((int64_t)(t + W - 1) * s.B + p.b) * s.D + p.c, p.n);
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = 0.0f;
-  }
+  for (int i = 0; i < V; ++i) x[i] = (float)v.v[i];
 }
 
-template <typename E, int V, int W>
-__global__ __launch_bounds__(kConvThreads) void conv_fwd(const ConvArgs<E> s) {
-  const ConvPlace p = conv_place<V>(s);
-  if (!p.active) return;
+// Rows rel .. rel + kConvAhead - 1 of a run, those past `last` replaced by it.
+template <bool FULL, typename E>
+__device__ __forceinline__ void conv_rows(Pack<E, V> (&r)[kConvAhead], const Rows<const E>& rows,
+                                          int rel, int last, int n) {
+#pragma unroll
+  for (int i = 0; i < kConvAhead; ++i)
+    r[i] = pack_load<FULL, E, V>(rows.at(min(rel + i, last)), n);
+}
+
+template <bool FULL, int W, typename E>
+__device__ __forceinline__ void conv_fwd_run(const ConvArgs<E>& s, const ConvPlace& p) {
   const int t0 = p.run * kConvRun, t1 = min(t0 + kConvRun, s.T);
-  const int te = min(t1, p.len);
-  float w[W][V], bias[V];
-  conv_weights<V, W>(w, bias, s.weight, s.bias, p.c);
-  if (t0 < te) {
+  const int te = min(t1, p.len), n = te - t0;
+  Rows<E> ry(s.y, t0, p.b, p.c);
+  if (n > 0) {
+    float w[W][V], bias[V];
+    Pack<E, V> now[kConvAhead], next[kConvAhead];
+    const Rows<const E> rx(s.x, t0, p.b, p.c);
+    conv_rows<FULL>(now, rx, 0, n - 1, p.n);
+    conv_weights<FULL, W>(w, bias, s.weight, s.bias, p.c, p.n);
     float x[W][V];  // steps t - W + 1 .. t
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) conv_input<V, W>(x[k], s, p.b, p.c, t0 - (W - 1) + k);
-#pragma unroll 4
-    for (int t = t0; t < te; ++t) {
-      pack_load<E, V>(x[W - 1], s.x.row(t, p.b) + p.c);
-      float y[V];
+    for (int k = 0; k < W - 1; ++k) conv_input<FULL, W>(x[k], s, p, t0 - (W - 1) + k);
+    for (int t = 0; t < n; t += kConvAhead) {
+      if (t + kConvAhead < n) conv_rows<FULL>(next, rx, t + kConvAhead, n - 1, p.n);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float a = bias[i];
+      for (int j = 0; j < kConvAhead; ++j) {
+        float y[V];
 #pragma unroll
-        for (int k = 0; k < W; ++k) a = fmaf(w[k][i], x[k][i], a);
-        y[i] = s.silu ? a * sigmoid_hw(a) : a;
+        for (int i = 0; i < V; ++i) {
+          x[W - 1][i] = (float)now[j].v[i];
+          float a = bias[i];
 #pragma unroll
-        for (int k = 0; k + 1 < W; ++k) x[k][i] = x[k + 1][i];
+          for (int k = 0; k < W; ++k) a = fmaf(w[k][i], x[k][i], a);
+          y[i] = s.silu ? a * sigmoid_hw(a) : a;
+#pragma unroll
+          for (int k = 0; k + 1 < W; ++k) x[k][i] = x[k + 1][i];
+        }
+        if (t + j < n) pack_store<FULL, E, V>(ry.at(t + j), y, p.n);
       }
-      pack_store<E, V>(s.y.row(t, p.b) + p.c, y);
+#pragma unroll
+      for (int j = 0; j < kConvAhead; ++j) now[j] = next[j];
     }
   }
   const float zero[V] = {};
-  for (int t = max(t0, te); t < t1; ++t) pack_store<E, V>(s.y.row(t, p.b) + p.c, zero);
+  for (int t = max(n, 0); t < t1 - t0; ++t) pack_store<FULL, E, V>(ry.at(t), zero, p.n);
   if (s.state && p.run == max(p.len - 1, 0) / kConvRun) {
     for (int k = 0; k < W - 1; ++k) {
       float x[V];
-      conv_input<V, W>(x, s, p.b, p.c, p.len - (W - 1) + k);
-      pack_store<E, V>(s.state + ((int64_t)k * s.B + p.b) * s.D + p.c, x);
+      conv_input<FULL, W>(x, s, p, p.len - (W - 1) + k);
+      pack_store<FULL, E, V>(s.state + ((int64_t)k * s.B + p.b) * s.D + p.c, x, p.n);
     }
   }
 }
 
-template <typename E, int V, int W>
+template <typename E, int W>
+__global__ __launch_bounds__(kConvThreads) void conv_fwd(const ConvArgs<E> s) {
+  const ConvPlace p = conv_place(s);
+  if (!p.active) return;
+  if (p.n >= V)
+    conv_fwd_run<true, W>(s, p);
+  else
+    conv_fwd_run<false, W>(s, p);
+}
+
+template <bool FULL, int W, typename E>
+__device__ __forceinline__ void conv_bwd_run(float (&gw)[W + 1][V], const ConvArgs<E>& s,
+                                             const ConvPlace& p) {
+  // steps are counted from the run's first; step t completes the gradient of
+  // the input W - 1 steps earlier, so the run goes on for W - 1 steps behind
+  // its own, and run 0 starts with the gradients of state0
+  const int t0 = p.run * kConvRunBwd, t1 = min(kConvRunBwd, s.T - t0);
+  const int len = p.len - t0, last = min(len, t1 + W - 1) - 1;
+  const Rows<const E> rx(s.x, t0, p.b, p.c), rg(s.gy, t0, p.b, p.c);
+  Rows<E> ro(s.gx, t0, p.b, p.c);
+  float w[W][V], bias[V], x[W][V], ga[W][V];  // ga: dL/dp of steps t - W + 1 .. t
+  Pack<E, V> xn[kConvAhead] = {}, gn[kConvAhead] = {};
+  if (last >= 0) {
+    conv_rows<FULL>(xn, rx, 0, last, p.n);
+    conv_rows<FULL>(gn, rg, 0, last, p.n);
+  }
+  conv_weights<FULL, W>(w, bias, s.weight, s.bias, p.c, p.n);
+#pragma unroll
+  for (int k = 0; k < W; ++k)
+#pragma unroll
+    for (int i = 0; i < V; ++i) ga[k][i] = x[k][i] = 0.0f;
+  if (last >= 0) {
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) conv_input<FULL, W>(x[k], s, p, t0 - (W - 1) + k);
+  }
+  // OWN: the weights' gradients of these steps are this run's
+  auto steps = [&](auto own, int tb) {
+    constexpr bool OWN = decltype(own)::value;
+    Pack<E, V> xp[kConvAhead] = {}, gp[kConvAhead] = {};
+    if (tb + kConvAhead <= last) {
+      conv_rows<FULL>(xp, rx, tb + kConvAhead, last, p.n);
+      conv_rows<FULL>(gp, rg, tb + kConvAhead, last, p.n);
+    }
+#pragma unroll
+    for (int j = 0; j < kConvAhead; ++j) {
+      const int t = tb + j;
+      const bool in = t <= last;  // (a run's own steps past its end are past the text's)
+      float gx[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        x[W - 1][i] = in ? (float)xn[j].v[i] : 0.0f;
+        float g = in ? (float)gn[j].v[i] : 0.0f;
+        if (s.silu) {
+          float a = bias[i];
+#pragma unroll
+          for (int k = 0; k < W; ++k) a = fmaf(w[k][i], x[k][i], a);
+          const float sg = sigmoid_hw(a);
+          g *= sg * fmaf(a, 1.0f - sg, 1.0f);
+        }
+        ga[W - 1][i] = in ? g : 0.0f;
+        if constexpr (OWN) {
+#pragma unroll
+          for (int k = 0; k < W; ++k) gw[k][i] = fmaf(ga[W - 1][i], x[k][i], gw[k][i]);
+          gw[W][i] += ga[W - 1][i];
+        }
+        gx[i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) gx[i] = fmaf(w[k][i], ga[W - 1 - k][i], gx[i]);
+#pragma unroll
+        for (int k = 0; k + 1 < W; ++k) {
+          x[k][i] = x[k + 1][i];
+          ga[k][i] = ga[k + 1][i];
+        }
+      }
+      const int ti = t - (W - 1);       // the input whose gradient is complete
+      const int slot = ti - len + W - 1;  // its row in the final state
+      if (s.gstate && slot >= 0 && slot < W - 1 && t < t1 + W - 1) {
+        const Pack<E, V> gs =
+            pack_load<FULL, E, V>(s.gstate + ((int64_t)slot * s.B + p.b) * s.D + p.c, p.n);
+#pragma unroll
+        for (int i = 0; i < V; ++i) gx[i] += (float)gs.v[i];
+      }
+      if (ti >= 0 && ti < t1) {
+        if (ti >= len) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) gx[i] = 0.0f;
+        }
+        pack_store<FULL, E, V>(ro.at(ti), gx, p.n);
+      } else if (ti + t0 < 0 && t < t1 + W - 1 && s.gstate0) {
+        pack_store<FULL, E, V>(s.gstate0 + ((int64_t)t * s.B + p.b) * s.D + p.c, gx, p.n);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kConvAhead; ++j) {
+      xn[j] = xp[j];
+      gn[j] = gp[j];
+    }
+  };
+  static_assert(kConvRunBwd % kConvAhead == 0, "a run is whole groups of rows");
+  for (int t = 0; t < t1; t += kConvAhead) steps(std::true_type(), t);
+  // (after a shorter run than kConvRunBwd, the window's last, no text follows)
+  const int tail = (t1 + kConvAhead - 1) / kConvAhead * kConvAhead;
+#pragma unroll
+  for (int t = 0; t < W - 1; t += kConvAhead) steps(std::false_type(), tail + t);
+}
+
+template <typename E, int W>
 __global__ __launch_bounds__(kConvThreads) void conv_bwd(const ConvArgs<E> s) {
   __shared__ float red[kConvThreads * V];  // [pairs of the workgroup][vx * V]
-  const ConvPlace p = conv_place<V>(s);
+  const ConvPlace p = conv_place(s);
   float gw[W + 1][V];
 #pragma unroll
   for (int k = 0; k <= W; ++k)
 #pragma unroll
     for (int i = 0; i < V; ++i) gw[k][i] = 0.0f;
   if (p.active) {
-    const int t0 = p.run * kConvRunBwd, t1 = min(t0 + kConvRunBwd, s.T);
-    float w[W][V], bias[V], x[W][V], ga[W][V];  // ga: dL/dp of steps t - W + 1 .. t
-    conv_weights<V, W>(w, bias, s.weight, s.bias, p.c);
-#pragma unroll
-    for (int k = 0; k < W; ++k)
-#pragma unroll
-      for (int i = 0; i < V; ++i) ga[k][i] = 0.0f;
-    if (t0 < p.len) {
-#pragma unroll
-      for (int k = 0; k < W - 1; ++k) conv_input<V, W>(x[k], s, p.b, p.c, t0 - (W - 1) + k);
-    }
-    // step t completes the gradient of the input W - 1 steps earlier; run 0
-    // starts with those of state0
-#pragma unroll 2
-    for (int t = t0; t < t1 + W - 1; ++t) {
-      if (t < p.len) {
-        float g[V];
-        pack_load<E, V>(x[W - 1], s.x.row(t, p.b) + p.c);
-        pack_load<E, V>(g, s.gy.row(t, p.b) + p.c);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if (s.silu) {
-            float a = bias[i];
-#pragma unroll
-            for (int k = 0; k < W; ++k) a = fmaf(w[k][i], x[k][i], a);
-            const float sg = sigmoid_hw(a);
-            g[i] *= sg * fmaf(a, 1.0f - sg, 1.0f);
-          }
-          ga[W - 1][i] = g[i];
-          if (t < t1) {
-#pragma unroll
-            for (int k = 0; k < W; ++k) gw[k][i] = fmaf(g[i], x[k][i], gw[k][i]);
-            gw[W][i] += g[i];
-          }
-#pragma unroll
-          for (int k = 0; k + 1 < W; ++k) x[k][i] = x[k + 1][i];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) ga[W - 1][i] = 0.0f;
-      }
-      const int ti = t - (W - 1);  // the input whose gradient is complete
-      float gx[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        gx[i] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < W; ++k) gx[i] = fmaf(w[k][i], ga[W - 1 - k][i], gx[i]);
-#pragma unroll
-        for (int k = 0; k + 1 < W; ++k) ga[k][i] = ga[k + 1][i];
-      }
-      const int slot = ti - p.len + W - 1;  // its row in the final state
-      if (s.gstate && slot >= 0 && slot < W - 1) {
-        float gs[V];
-        pack_load<E, V>(gs, s.gstate + ((int64_t)slot * s.B + p.b) * s.D + p.c);
-#pragma unroll
-        for (int i = 0; i < V; ++i) gx[i] += gs[i];
-      }
-      if (ti >= t0) {
-        if (ti >= p.len) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) gx[i] = 0.0f;
-        }
-        pack_store<E, V>(s.gx.row(ti, p.b) + p.c, gx);
-      } else if (ti < 0 && s.gstate0) {
-        pack_store<E, V>(s.gstate0 + ((int64_t)t * s.B + p.b) * s.D + p.c, gx);
-      }
-    }
+    if (p.n >= V)
+      conv_bwd_run<true, W>(gw, s, p);
+    else
+      conv_bwd_run<false, W>(gw, s, p);
   }
   // the workgroup's (row, run) pairs, summed in order, one tap at a time
   const int n = s.vx * V, pairs = kConvThreads / s.vx;
   const int vi = (int)threadIdx.x & (s.vx - 1), ty = (int)threadIdx.x / s.vx;
   const int vblocks = (s.nv + s.vx - 1) / s.vx;
   const int c0 = (int)(blockIdx.x % vblocks) * n;
-  float* part = s.part + ((int64_t)(blockIdx.x / vblocks) * s.D + c0) * (W + 1);
+  float* part = s.part + (int64_t)(blockIdx.x / vblocks) * (W + 1) * s.D + c0;
 #pragma unroll
   for (int k = 0; k <= W; ++k) {
     __syncthreads();
@@ -221,35 +288,44 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd(const ConvArgs<E> s) {
     for (int e = threadIdx.x; e < n && c0 + e < s.D; e += kConvThreads) {
       float sum = 0.0f;
       for (int r = 0; r < pairs; ++r) sum += red[r * n + e];
-      part[(int64_t)e * (W + 1) + k] = sum;
+      part[(int64_t)k * s.D + e] = sum;
     }
   }
 }
 
-// Gradients of the weights and the bias: the workgroups' sums, in order.
+// Gradients of the weights and the bias: the workgroups' sums in a fixed
+// order.  A workgroup takes 32 sums, eight threads each one a stretch of the
+// parts.
 template <int W>
-__global__ __launch_bounds__(256) void conv_sum(const float* part, int64_t D, int64_t parts,
+__global__ __launch_bounds__(256) void conv_sum(const float* part, int D, int64_t parts,
                                                 float* gw, float* gbias) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= D * (W + 1)) return;
-  const int k = (int)(i % (W + 1));
+  __shared__ float red[8][32];
+  const int64_t n = (int64_t)D * (W + 1), i = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
+  const int y = threadIdx.x >> 5;
+  const int64_t each = (parts + 7) / 8, r0 = each * y, r1 = min(r0 + each, parts);
   float sum = 0.0f;
-  for (int64_t r = 0; r < parts; ++r) sum += part[r * D * (W + 1) + i];
+  if (i < n) {
+#pragma unroll 4
+    for (int64_t r = r0; r < r1; ++r) sum += part[r * n + i];
+  }
+  red[y][threadIdx.x & 31] = sum;
+  __syncthreads();
+  if (y != 0 || i >= n) return;
+  sum = 0.0f;
+  for (int j = 0; j < 8; ++j) sum += red[j][threadIdx.x];
+  const int k = (int)(i / D), d = (int)(i % D);
   if (k < W)
-    gw[i / (W + 1) * W + k] = sum;
+    gw[(int64_t)d * W + k] = sum;
   else if (gbias)
-    gbias[i / (W + 1)] = sum;
+    gbias[d] = sum;
 }
 
-template <typename E, int V, int W>
-__global__ __launch_bounds__(kConvThreads) void conv_one(const ConvArgs<E> s) {
-  const int64_t i0 = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
-  if (i0 >= (int64_t)s.B * s.nv) return;
-  const int b = (int)(i0 / s.nv), c = (int)(i0 % s.nv) * V;
+template <bool FULL, int W, typename E>
+__device__ __forceinline__ void conv_one_row(const ConvArgs<E>& s, const ConvPlace& p) {
   float w[W][V], bias[V], x[W][V], y[V];
-  conv_weights<V, W>(w, bias, s.weight, s.bias, c);
 #pragma unroll
-  for (int k = 0; k < W; ++k) conv_input<V, W>(x[k], s, b, c, k - (W - 1));
+  for (int k = 0; k < W; ++k) conv_input<FULL, W>(x[k], s, p, k - (W - 1));
+  conv_weights<FULL, W>(w, bias, s.weight, s.bias, p.c, p.n);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     float a = bias[i];
@@ -257,10 +333,24 @@ __global__ __launch_bounds__(kConvThreads) void conv_one(const ConvArgs<E> s) {
     for (int k = 0; k < W; ++k) a = fmaf(w[k][i], x[k][i], a);
     y[i] = s.silu ? a * sigmoid_hw(a) : a;
   }
-  pack_store<E, V>(s.y.row(0, b) + c, y);
+  pack_store<FULL, E, V>(s.y.row(0, p.b) + p.c, y, p.n);
 #pragma unroll
   for (int k = 0; k + 1 < W; ++k)
-    pack_store<E, V>(s.state + ((int64_t)k * s.B + b) * s.D + c, x[k + 1]);
+    pack_store<FULL, E, V>(s.state + ((int64_t)k * s.B + p.b) * s.D + p.c, x[k + 1], p.n);
+}
+
+template <typename E, int W>
+__global__ __launch_bounds__(kConvThreads) void conv_one(const ConvArgs<E> s) {
+  const int64_t i0 = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
+  if (i0 >= (int64_t)s.B * s.nv) return;
+  ConvPlace p = {};
+  p.b = (int)(i0 / s.nv);
+  p.c = (int)(i0 % s.nv) * V;
+  p.n = s.D - p.c;
+  if (p.n >= V)
+    conv_one_row<true, W>(s, p);
+  else
+    conv_one_row<false, W>(s, p);
 }
 
 ck_status conv_check_shape(const ck_conv_shape* s) {
@@ -274,8 +364,8 @@ ck_status conv_check_shape(const ck_conv_shape* s) {
     set_error("W must be in [1, 8] (got %lld)", (long long)s->W);
     return CK_ERR_BAD_SIZE;
   }
-  // workgroups of one launch (a thread of the scalar path takes one channel)
-  const int64_t pairs = s->B * (s->T / kConvRun + 1), nv = s->D;
+  // workgroups of one launch
+  const int64_t pairs = s->B * (s->T / kConvRun + 1), nv = (s->D + kConvV - 1) / kConvV;
   if ((pairs / 4 + 1) > INT_MAX / (nv / 32 + 1)) {
     set_error("T=%lld, B=%lld or D=%lld is too large", (long long)s->T, (long long)s->B,
               (long long)s->D);
@@ -293,9 +383,9 @@ struct ConvDims {
   int nv, vx, runs;
   int64_t vblocks, pblocks;  // workgroups over the channels, over the (row, run) pairs
 };
-ConvDims conv_dims(const ck_conv_shape& s, int V, int run) {
+ConvDims conv_dims(const ck_conv_shape& s, int run) {
   ConvDims d;
-  d.nv = (int)(s.D / V);
+  d.nv = (int)((s.D + kConvV - 1) / kConvV);
   d.vx = 1;
   while (d.vx < 64 && d.vx < d.nv) d.vx *= 2;
   d.runs = (int)std::max<int64_t>((s.T + run - 1) / run, 1);
@@ -333,23 +423,6 @@ void conv_by_width(int W, F&& fn) {
   }
 }
 
-// fn(V, W) as constants: V the elements of 16 bytes when all rows of the
-// call's tensors can be read so, else 1.
-template <typename E, typename F>
-void conv_by_kind(const ck_conv_shape& s, std::initializer_list<ck_seq> seqs,
-                  std::initializer_list<const void*> states, F&& fn) {
-  constexpr int V = 16 / sizeof(E);
-  bool vec = s.D % V == 0;
-  for (const ck_seq& q : seqs) vec = vec && seq_vec_ok<E, V>(q);
-  for (const void* p : states) vec = vec && reinterpret_cast<uintptr_t>(p) % 16 == 0;
-  conv_by_width((int)s.W, [&](auto w) {
-    if (vec)
-      fn(std::integral_constant<int, V>(), w);
-    else
-      fn(std::integral_constant<int, 1>(), w);
-  });
-}
-
 }  // namespace
 }  // namespace ckhip
 
@@ -359,12 +432,8 @@ extern "C" ck_status ck_conv_sizes(const ck_conv_shape* shape, size_t* workspace
   clear_error();
   const ck_status rc = conv_check_shape(shape);
   if (rc != CK_OK) return rc;
-  // enough for either path (the scalar path's workgroups take at most as many pairs)
-  size_t need = 0;
-  for (int V : {1, (int)(16 / seq_elem_bytes(shape->dtype))})
-    if (shape->D % V == 0)
-      need = std::max(need, (size_t)conv_dims(*shape, V, kConvRunBwd).pblocks * shape->D *
-                                (shape->W + 1) * 4);
+  const size_t need =
+      (size_t)conv_dims(*shape, kConvRunBwd).pblocks * shape->D * (shape->W + 1) * 4;
   if (workspace_bytes) *workspace_bytes = need;
   return CK_OK;
 }
@@ -388,14 +457,14 @@ extern "C" ck_status ck_conv_forward(const ck_conv_shape* shape, ck_seq x, const
   if (rc != CK_OK) return rc;
   return seq_dispatch(shape->dtype, [&](auto* e) -> ck_status {
     using E = std::remove_pointer_t<decltype(e)>;
-    conv_by_kind<E>(*shape, {x, y}, {state0, state}, [&](auto v, auto w) {
-      constexpr int V = decltype(v)::value, W = decltype(w)::value;
-      const ConvDims d = conv_dims(*shape, V, kConvRun);
+    conv_by_width((int)shape->W, [&](auto w) {
+      constexpr int W = decltype(w)::value;
+      const ConvDims d = conv_dims(*shape, kConvRun);
       ConvArgs<E> a = conv_args<E>(*shape, x, weight, bias, state0, lengths);
       a.y = seq_of<E>(y);
       a.state = W > 1 ? static_cast<E*>(state) : nullptr;
       a.nv = d.nv; a.vx = d.vx; a.runs = d.runs;
-      conv_fwd<E, V, W><<<(unsigned)(d.vblocks * d.pblocks), kConvThreads, 0, stream>>>(a);
+      conv_fwd<E, W><<<(unsigned)(d.vblocks * d.pblocks), kConvThreads, 0, stream>>>(a);
     });
     CK_HIP_TRY(hipGetLastError());
     return CK_OK;
@@ -429,10 +498,9 @@ extern "C" ck_status ck_conv_backward(const ck_conv_shape* shape, ck_seq x, cons
   if (rc != CK_OK) return rc;
   return seq_dispatch(shape->dtype, [&](auto* e) -> ck_status {
     using E = std::remove_pointer_t<decltype(e)>;
-    conv_by_kind<E>(*shape, {x, grad_y, grad_x}, {state0, grad_state, grad_state0},
-                    [&](auto v, auto w) {
-      constexpr int V = decltype(v)::value, W = decltype(w)::value;
-      const ConvDims d = conv_dims(*shape, V, kConvRunBwd);
+    conv_by_width((int)shape->W, [&](auto w) {
+      constexpr int W = decltype(w)::value;
+      const ConvDims d = conv_dims(*shape, kConvRunBwd);
       ConvArgs<E> a = conv_args<E>(*shape, x, weight, bias, state0, lengths);
       a.gy = seq_of<const E>(grad_y);
       a.gx = seq_of<E>(grad_x);
@@ -440,9 +508,9 @@ extern "C" ck_status ck_conv_backward(const ck_conv_shape* shape, ck_seq x, cons
       a.gstate0 = W > 1 ? static_cast<E*>(grad_state0) : nullptr;
       a.part = static_cast<float*>(workspace);
       a.nv = d.nv; a.vx = d.vx; a.runs = d.runs;
-      conv_bwd<E, V, W><<<(unsigned)(d.vblocks * d.pblocks), kConvThreads, 0, stream>>>(a);
-      conv_sum<W><<<(unsigned)((shape->D * (W + 1) + 255) / 256), 256, 0, stream>>>(
-          a.part, shape->D, d.pblocks, grad_weight, grad_bias);
+      conv_bwd<E, W><<<(unsigned)(d.vblocks * d.pblocks), kConvThreads, 0, stream>>>(a);
+      conv_sum<W><<<(unsigned)((shape->D * (W + 1) + 31) / 32), 256, 0, stream>>>(
+          a.part, a.D, d.pblocks, grad_weight, grad_bias);
     });
     CK_HIP_TRY(hipGetLastError());
     return CK_OK;
@@ -470,14 +538,14 @@ extern "C" ck_status ck_conv_step(const ck_conv_shape* shape, ck_seq x, const fl
   if (rc != CK_OK) return rc;
   return seq_dispatch(shape->dtype, [&](auto* e) -> ck_status {
     using E = std::remove_pointer_t<decltype(e)>;
-    conv_by_kind<E>(*shape, {x, y}, {state0, state}, [&](auto v, auto w) {
-      constexpr int V = decltype(v)::value, W = decltype(w)::value;
+    conv_by_width((int)shape->W, [&](auto w) {
+      constexpr int W = decltype(w)::value;
       ConvArgs<E> a = conv_args<E>(*shape, x, weight, bias, state0, nullptr);
       a.y = seq_of<E>(y);
       a.state = W > 1 ? static_cast<E*>(state) : nullptr;
-      a.nv = (int)(shape->D / V);
+      a.nv = (int)((shape->D + kConvV - 1) / kConvV);
       const int64_t n = shape->B * a.nv;
-      conv_one<E, V, W><<<(unsigned)((n + kConvThreads - 1) / kConvThreads), kConvThreads, 0,
+      conv_one<E, W><<<(unsigned)((n + kConvThreads - 1) / kConvThreads), kConvThreads, 0,
                           stream>>>(a);
     });
     CK_HIP_TRY(hipGetLastError());

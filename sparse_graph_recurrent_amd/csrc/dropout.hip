@@ -50,32 +50,24 @@ __device__ __forceinline__ uint4 philox(uint32_t c0, uint32_t c1, uint32_t c2, u
   return make_uint4(c0, c1, c2, c3);
 }
 
-template <typename E, bool VEC>
-__device__ __forceinline__ void drop_load(float (&v)[8], const E* p, int n) {
-  if constexpr (VEC) {
-    constexpr int V = 16 / sizeof(E);
+template <typename E, bool HELD, bool FULL>
+__device__ __forceinline__ void drop_rows(const DropArgs<E>& s, const uint32_t (&h)[8], int b,
+                                          int run, int c, int n) {
+  const int t0 = HELD ? run * kDropHeld : run, t1 = HELD ? min(t0 + kDropHeld, s.T) : run + 1;
+#pragma unroll 2
+  for (int t = t0; t < t1; ++t) {
+    const Pack<E, 8> x = pack_load<FULL, E, 8>(s.x.row(t, b) + c, n);
+    Pack<E, 8> z = {};
+    if (s.res.p) z = pack_load<FULL, E, 8>(s.res.row(t, b) + c, n);
+    float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; i += V) pack_load<E, V>(*reinterpret_cast<float(*)[V]>(&v[i]), p + i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? (float)p[i] : 0.0f;
-  }
-}
-template <typename E, bool VEC>
-__device__ __forceinline__ void drop_store(E* p, const float (&v)[8], int n) {
-  if constexpr (VEC) {
-    constexpr int V = 16 / sizeof(E);
-#pragma unroll
-    for (int i = 0; i < 8; i += V)
-      pack_store<E, V>(p + i, *reinterpret_cast<const float(*)[V]>(&v[i]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = (E)v[i];
+    for (int k = 0; k < 8; ++k)
+      y[k] = (float)z.v[k] + (h[k] >= s.q ? (float)x.v[k] * s.scale : 0.0f);
+    pack_store<FULL, E, 8>(s.out.row(t, b) + c, y, n);
   }
 }
 
-template <typename E, bool VEC, bool HELD>
+template <typename E, bool HELD>
 __global__ __launch_bounds__(kDropThreads) void drop(const DropArgs<E> s) {
   const int64_t i = (int64_t)blockIdx.x * kDropThreads + threadIdx.x;
   const int col = (int)(i % s.cols);
@@ -89,20 +81,10 @@ __global__ __launch_bounds__(kDropThreads) void drop(const DropArgs<E> s) {
   const uint32_t h[8] = {w.x & 0xFFFF, w.x >> 16, w.y & 0xFFFF, w.y >> 16,
                          w.z & 0xFFFF, w.z >> 16, w.w & 0xFFFF, w.w >> 16};
   const int n = s.D - col * 8;
-  const int t0 = HELD ? run * kDropHeld : run, t1 = HELD ? min(t0 + kDropHeld, s.T) : run + 1;
-#pragma unroll 2
-  for (int t = t0; t < t1; ++t) {
-    float x[8], y[8];
-    drop_load<E, VEC>(x, s.x.row(t, b) + col * 8, n);
-    if (s.res.p)
-      drop_load<E, VEC>(y, s.res.row(t, b) + col * 8, n);
-    else
-#pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] += h[k] >= s.q ? x[k] * s.scale : 0.0f;
-    drop_store<E, VEC>(s.out.row(t, b) + col * 8, y, n);
-  }
+  if (n >= 8)
+    drop_rows<E, HELD, true>(s, h, b, run, col * 8, n);
+  else
+    drop_rows<E, HELD, false>(s, h, b, run, col * 8, n);
 }
 
 ck_status drop_run(const ck_dropout_shape* s, const ck_seq& x, const ck_seq& res, const ck_seq& out,
@@ -131,7 +113,6 @@ ck_status drop_run(const ck_dropout_shape* s, const ck_seq& x, const ck_seq& res
   const uint32_t q = (uint32_t)std::floor(65536.0 * s->p + 0.5);
   return seq_dispatch(s->dtype, [&](auto* e) -> ck_status {
     using E = std::remove_pointer_t<decltype(e)>;
-    constexpr int V = 16 / sizeof(E);
     DropArgs<E> a = {};
     a.x = seq_of<const E>(x);
     a.res = seq_of<const E>(res);
@@ -145,18 +126,12 @@ ck_status drop_run(const ck_dropout_shape* s, const ck_seq& x, const ck_seq& res
     a.runs = (int)((s->T + kDropHeld - 1) / kDropHeld);
     a.q = q;
     a.scale = q < 65536 ? (float)(65536.0 / (65536.0 - q)) : 0.0f;
-    const bool vec = s->D % 8 == 0 && seq_vec_ok<E, V>(x) && seq_vec_ok<E, V>(out) &&
-                     (!res.data || seq_vec_ok<E, V>(res));
     const int64_t n = (s->held ? (int64_t)a.runs * s->B : rows) * cols;
     const unsigned grid = (unsigned)((n + kDropThreads - 1) / kDropThreads);
-    if (s->held && vec)
-      drop<E, true, true><<<grid, kDropThreads, 0, stream>>>(a);
-    else if (s->held)
-      drop<E, false, true><<<grid, kDropThreads, 0, stream>>>(a);
-    else if (vec)
-      drop<E, true, false><<<grid, kDropThreads, 0, stream>>>(a);
+    if (s->held)
+      drop<E, true><<<grid, kDropThreads, 0, stream>>>(a);
     else
-      drop<E, false, false><<<grid, kDropThreads, 0, stream>>>(a);
+      drop<E, false><<<grid, kDropThreads, 0, stream>>>(a);
     CK_HIP_TRY(hipGetLastError());
     return CK_OK;
   });

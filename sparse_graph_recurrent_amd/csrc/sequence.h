@@ -6,6 +6,7 @@
 
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "ck.h"
 #include "ck_internal.h"
@@ -92,36 +93,55 @@ struct Seq {
   int64_t st, sb;
   __device__ __forceinline__ E* row(int64_t t, int64_t b) const { return p + t * st + b * sb; }
 };
-// True when rows of V elements can be read whole: every row of every listed
-// tensor starts on a V-element boundary.
-template <typename E, int V>
-bool seq_vec_ok(const ck_seq& s) {
-  return reinterpret_cast<uintptr_t>(s.data) % (V * sizeof(E)) == 0 && s.stride_t % V == 0 &&
-         s.stride_b % V == 0;
-}
 template <typename E>
 Seq<E> seq_of(const ck_seq& s) {
   return Seq<E>{static_cast<E*>(s.data), s.stride_t, s.stride_b};
 }
 
-// V adjacent elements, moved with one access of V * sizeof(E) bytes.
+// V adjacent elements as one load or store of up to 16 bytes an access.  The
+// type asks for no more than the element's own alignment: global memory takes
+// wide accesses at any address (rows of odd length start anywhere), at full
+// rate where they are aligned.
 template <typename E, int V>
-struct alignas(V * sizeof(E)) Pack {
+struct __attribute__((packed, aligned(alignof(E)))) Pack {
   E v[V];
 };
-template <typename E, int V>
-__device__ __forceinline__ void pack_load(float (&x)[V], const E* p) {
-  const Pack<E, V> w = *reinterpret_cast<const Pack<E, V>*>(p);
+// FULL: all V elements are there; else the first n, 0 beyond.
+template <bool FULL, typename E, int V>
+__device__ __forceinline__ Pack<E, V> pack_load(const E* p, int n) {
+  if constexpr (FULL) return *reinterpret_cast<const Pack<E, V>*>(p);
+  Pack<E, V> w;
 #pragma unroll
-  for (int i = 0; i < V; ++i) x[i] = (float)w.v[i];
+  for (int i = 0; i < V; ++i) w.v[i] = i < n ? p[i] : (E)0.0f;
+  return w;
 }
-template <typename E, int V>
-__device__ __forceinline__ void pack_store(E* p, const float (&x)[V]) {
+template <bool FULL, typename E, int V>
+__device__ __forceinline__ void pack_store(E* p, const float (&x)[V], int n) {
   Pack<E, V> w;
 #pragma unroll
   for (int i = 0; i < V; ++i) w.v[i] = (E)x[i];
-  *reinterpret_cast<Pack<E, V>*>(p) = w;
+  if constexpr (FULL) {
+    *reinterpret_cast<Pack<E, V>*>(p) = w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) p[i] = w.v[i];
+  }
 }
+// The rows of one tensor from step t on at a thread's channels: one 32 x 32 +
+// 64 bit multiply-add an address.
+template <typename E>
+struct Rows {
+  const char* base;
+  uint32_t step;
+  __device__ __forceinline__ Rows(const Seq<E>& s, int64_t t, int64_t b, int64_t c)
+      : base(reinterpret_cast<const char*>(s.row(t, b) + c)),
+        step((uint32_t)s.st * (uint32_t)sizeof(E)) {}
+  __device__ __forceinline__ E* at(int rel) const {
+    using M = std::remove_const_t<E>;
+    return reinterpret_cast<M*>(const_cast<char*>(base) + (uint64_t)(uint32_t)rel * step);
+  }
+};
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
