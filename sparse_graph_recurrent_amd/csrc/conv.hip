@@ -22,7 +22,10 @@ namespace {
 constexpr int64_t kConvMaxW = 8;
 constexpr int kConvThreads = 256;
 constexpr int kConvRun = 16;     // steps per thread, forward
-constexpr int kConvRunBwd = 32;  // and backward, whose run reads 2 (W - 1) steps more
+// and backward, whose run reads 2 (W - 1) steps more: long ones where they
+// still give every CU two workgroups, else short ones
+constexpr int kConvRunBwdMax = 48, kConvRunBwdMin = 16;
+constexpr int64_t kConvFullWgs = 512;
 constexpr int kConvAhead = 4;    // rows in flight: loaded while the ones before are worked on
 constexpr int kConvV = 4;        // channels per thread
 
@@ -39,6 +42,7 @@ struct ConvArgs {
   int nv;        // channel groups of kConvV
   int vx;        // of them per workgroup (a power of two at most 64)
   int runs;      // runs of the window
+  int run;       // steps of a run (a multiple of kConvAhead)
   int silu;
 };
 
@@ -168,7 +172,7 @@ __device__ __forceinline__ void conv_bwd_run(float (&gw)[W + 1][V], const ConvAr
   // steps are counted from the run's first; step t completes the gradient of
   // the input W - 1 steps earlier, so the run goes on for W - 1 steps behind
   // its own, and run 0 starts with the gradients of state0
-  const int t0 = p.run * kConvRunBwd, t1 = min(kConvRunBwd, s.T - t0);
+  const int t0 = p.run * s.run, t1 = min(s.run, s.T - t0);
   const int len = p.len - t0, last = min(len, t1 + W - 1) - 1;
   const Rows<const E> rx(s.x, t0, p.b, p.c), rg(s.gy, t0, p.b, p.c);
   Rows<E> ro(s.gx, t0, p.b, p.c);
@@ -250,9 +254,8 @@ __device__ __forceinline__ void conv_bwd_run(float (&gw)[W + 1][V], const ConvAr
       gn[j] = gp[j];
     }
   };
-  static_assert(kConvRunBwd % kConvAhead == 0, "a run is whole groups of rows");
   for (int t = 0; t < t1; t += kConvAhead) steps(std::true_type(), t);
-  // (after a shorter run than kConvRunBwd, the window's last, no text follows)
+  // (behind a shorter run, the window's last, no text follows)
   const int tail = (t1 + kConvAhead - 1) / kConvAhead * kConvAhead;
 #pragma unroll
   for (int t = 0; t < W - 1; t += kConvAhead) steps(std::false_type(), tail + t);
@@ -380,7 +383,7 @@ ck_status conv_check_state(const void* p, const ck_conv_shape& s, bool optional,
 }
 
 struct ConvDims {
-  int nv, vx, runs;
+  int nv, vx, run, runs;
   int64_t vblocks, pblocks;  // workgroups over the channels, over the (row, run) pairs
 };
 ConvDims conv_dims(const ck_conv_shape& s, int run) {
@@ -388,11 +391,17 @@ ConvDims conv_dims(const ck_conv_shape& s, int run) {
   d.nv = (int)((s.D + kConvV - 1) / kConvV);
   d.vx = 1;
   while (d.vx < 64 && d.vx < d.nv) d.vx *= 2;
+  d.run = run;
   d.runs = (int)std::max<int64_t>((s.T + run - 1) / run, 1);
   d.vblocks = (d.nv + d.vx - 1) / d.vx;
   const int pairs = kConvThreads / d.vx;
   d.pblocks = (s.B * d.runs + pairs - 1) / pairs;
   return d;
+}
+
+ConvDims conv_dims_backward(const ck_conv_shape& s) {
+  const ConvDims d = conv_dims(s, kConvRunBwdMax);
+  return d.vblocks * d.pblocks >= kConvFullWgs ? d : conv_dims(s, kConvRunBwdMin);
 }
 
 template <typename E>
@@ -433,7 +442,7 @@ extern "C" ck_status ck_conv_sizes(const ck_conv_shape* shape, size_t* workspace
   const ck_status rc = conv_check_shape(shape);
   if (rc != CK_OK) return rc;
   const size_t need =
-      (size_t)conv_dims(*shape, kConvRunBwd).pblocks * shape->D * (shape->W + 1) * 4;
+      (size_t)conv_dims_backward(*shape).pblocks * shape->D * (shape->W + 1) * 4;
   if (workspace_bytes) *workspace_bytes = need;
   return CK_OK;
 }
@@ -463,7 +472,7 @@ extern "C" ck_status ck_conv_forward(const ck_conv_shape* shape, ck_seq x, const
       ConvArgs<E> a = conv_args<E>(*shape, x, weight, bias, state0, lengths);
       a.y = seq_of<E>(y);
       a.state = W > 1 ? static_cast<E*>(state) : nullptr;
-      a.nv = d.nv; a.vx = d.vx; a.runs = d.runs;
+      a.nv = d.nv; a.vx = d.vx; a.run = d.run; a.runs = d.runs;
       conv_fwd<E, W><<<(unsigned)(d.vblocks * d.pblocks), kConvThreads, 0, stream>>>(a);
     });
     CK_HIP_TRY(hipGetLastError());
@@ -500,14 +509,14 @@ extern "C" ck_status ck_conv_backward(const ck_conv_shape* shape, ck_seq x, cons
     using E = std::remove_pointer_t<decltype(e)>;
     conv_by_width((int)shape->W, [&](auto w) {
       constexpr int W = decltype(w)::value;
-      const ConvDims d = conv_dims(*shape, kConvRunBwd);
+      const ConvDims d = conv_dims_backward(*shape);
       ConvArgs<E> a = conv_args<E>(*shape, x, weight, bias, state0, lengths);
       a.gy = seq_of<const E>(grad_y);
       a.gx = seq_of<E>(grad_x);
       a.gstate = W > 1 ? static_cast<const E*>(grad_state) : nullptr;
       a.gstate0 = W > 1 ? static_cast<E*>(grad_state0) : nullptr;
       a.part = static_cast<float*>(workspace);
-      a.nv = d.nv; a.vx = d.vx; a.runs = d.runs;
+      a.nv = d.nv; a.vx = d.vx; a.run = d.run; a.runs = d.runs;
       conv_bwd<E, W><<<(unsigned)(d.vblocks * d.pblocks), kConvThreads, 0, stream>>>(a);
       conv_sum<W><<<(unsigned)((shape->D * (W + 1) + 31) / 32), 256, 0, stream>>>(
           a.part, a.D, d.pblocks, grad_weight, grad_bias);

@@ -5,18 +5,22 @@
 //   dt_t = softplus(delta_t + bias)      a_t = exp(dt_t A)
 //   h_t  = a_t h_{t-1} + dt_t B_t u_t    y_t = C_t . h_t + D u_t    out = y silu(z)
 //
-// Work split.  Four adjacent lanes (a quad) own one channel, each of them NL
-// of its N states, and walk the steps in tiles of K.  The per-channel work of
-// a step (loads, softplus, gate, store) is done by one lane of the quad: lane
-// q takes step 4i + q of a tile and the quad reads dt and dt u of the others
-// through DPP, so that work is not repeated four times.
+// Layout.  A wave owns 16 channels and walks the steps in tiles of K: lane
+// (c, q) = (lane % 16, lane / 16) holds states 16 m + 4 q + r (r < 4, m < M) of
+// channel c.  The per-channel work of a step (loads, softplus, gate, store) is
+// done once, by the lane (c, q) with t % 4 = q, and the channel's other lanes
+// read its dt and dt u from LDS, four steps an access.  What bounds the kernels
+// is the vector ALU: exponentials take 8.5 cycles a wave, plain fp32
+// operations 2.7 to 4, exchanges and selects 4.4.  (The outer product dt u x B
+// as fp32 matrix instructions was slower: they keep the vector ALU waiting,
+// 36 cycles for 4 products a lane.)
 //
-// Few rows leave most of the chip idle, so the window is then cut into chunks
+// Few rows leave most of the chip idle, and the window is then cut into chunks
 // that run side by side: a first launch finds what each chunk makes of a zero
 // state (and the sum of its dt, from which its decay exp(A sum dt) follows), a
 // small one joins these to every chunk's entering state, and the main launch
-// starts each chunk from it.  The backward does the same with its adjoint
-// from the other end.
+// starts each chunk from it.  The backward does the same with its adjoint from
+// the other end.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -27,18 +31,18 @@
 
 namespace ckhip {
 
-constexpr int kScanThreads = 256;             // 4 waves
-constexpr int kScanChan = kScanThreads / 4;   // channels per workgroup
+constexpr int kScanChan = 64;                 // channels per workgroup
+constexpr int kScanThreads = 4 * kScanChan;   // 4 waves
 constexpr int64_t kScanMaxN = 64;
 
-// Steps per tile: a lane of the backward holds a_t and h_{t-1} of a whole
-// tile in registers (2 K NL values).
-constexpr int scan_tile(int NL) { return NL <= 4 ? 16 : 64 / NL; }
+// Steps per tile for M blocks of 16 states: a lane of the backward holds a_t
+// and h_{t-1} of a whole tile in registers (8 K M values).
+constexpr int scan_tile(int M) { return M == 1 ? 8 : 4; }
 
 // Sizes that both directions share.
 struct ScanDims {
   int64_t T, B, D, N, G;
-  int NL, NP, K;    // states per lane, padded states (4 NL), steps per tile
+  int M, NP, K;     // blocks of 16 states, padded states (16 M), steps per tile
   int64_t Dg, P;    // channels per group, workgroups per group
   int64_t tiles;    // tiles of the window
   int64_t chunks, chunk_steps;  // chunks of the window (steps: a multiple of K)
@@ -74,12 +78,12 @@ void scan_launch_forward(const ScanDims& d, const ScanArgs<E>& a, hipStream_t st
 template <typename E>
 void scan_launch_backward(const ScanDims& d, const ScanArgs<E>& a, hipStream_t stream);
 
-// What a workgroup computes: channels [g Dg + blk 64, ...) of row b over the
+// What a wave computes: 16 of channels [g Dg + blk 64, ...) of row b over the
 // steps [t0, t1) of its chunk, of which the row's text covers those up to te.
 struct Place {
   int b, g, blk, chunk;
   int t0, t1, te, len;
-  int q;        // lane of the quad
+  int c, q;     // lane: channel of the wave, and its row of lanes
   int d;        // channel (clamped to the group's last)
   bool active;  // the channel exists
 };
@@ -94,8 +98,10 @@ __device__ __forceinline__ Place scan_place(const ScanArgs<E>& s) {
   i /= s.G;
   p.b = i % s.B;
   p.chunk = i / s.B;
-  p.q = threadIdx.x & 3;
-  const int dg = p.blk * kScanChan + (int)(threadIdx.x >> 2);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  p.c = threadIdx.x & 15;
+  p.q = (threadIdx.x & 63) >> 4;
+  const int dg = p.blk * kScanChan + wave * 16 + p.c;
   p.active = dg < s.Dg;
   p.d = p.g * s.Dg + min(dg, s.Dg - 1);
   p.len = s.T;
@@ -119,103 +125,155 @@ struct Walk {
         off((uint32_t)(lane_step * (uint32_t)s.st + (uint32_t)channel) * (uint32_t)sizeof(E)),
         step((uint32_t)s.st * (uint32_t)sizeof(E)) {}
   __device__ __forceinline__ void advance(int steps) { tile += (int64_t)steps * (int64_t)step; }
-  // element `ahead` steps after the lane's, or of step `last` of the tile if
-  // that comes first
+  // element `ahead` steps after the lane's, at most at the offset `limit`
   __device__ __forceinline__ E load(int ahead, uint32_t limit) const {
     return *reinterpret_cast<const E*>(tile + min(off + (uint32_t)ahead * step, limit));
   }
+  // offset of step `last` of the tile for the lane whose first step is q
+  __device__ __forceinline__ uint32_t limit(int q, int last) const {
+    return last >= scan_tile(1) ? 0xFFFFFFFFu : off + (uint32_t)(last - q) * step;
+  }
   __device__ __forceinline__ E* at(int ahead) const {
-    using M = std::remove_const_t<E>;
-    return reinterpret_cast<M*>(const_cast<char*>(tile) + (off + (uint32_t)ahead * step));
+    using X = std::remove_const_t<E>;
+    return reinterpret_cast<X*>(const_cast<char*>(tile) + (off + (uint32_t)ahead * step));
   }
 };
 
-template <int NL>
-using StatesV = float __attribute__((ext_vector_type(NL)));
+using f32x4 = float __attribute__((ext_vector_type(4)));
 
-template <int NL>
-__device__ __forceinline__ void load_vec(float (&v)[NL], const float* p) {
-  const StatesV<NL> w = *reinterpret_cast<const StatesV<NL>*>(p);
+// The lane's states: f32x4[M], block m holding states 16 m + 4 q + r.
+template <int M>
+__device__ __forceinline__ void load_rows(f32x4 (&v)[M], const float* p, int q) {
 #pragma unroll
-  for (int k = 0; k < NL; ++k) v[k] = w[k];
+  for (int m = 0; m < M; ++m) v[m] = *reinterpret_cast<const f32x4*>(p + 16 * m + 4 * q);
 }
-template <int NL>
-__device__ __forceinline__ void store_vec(float* p, const float (&v)[NL]) {
-  StatesV<NL> w;
+template <int M>
+__device__ __forceinline__ void store_rows(float* p, const f32x4 (&v)[M], int q) {
 #pragma unroll
-  for (int k = 0; k < NL; ++k) w[k] = v[k];
-  *reinterpret_cast<StatesV<NL>*>(p) = w;
+  for (int m = 0; m < M; ++m) *reinterpret_cast<f32x4*>(p + 16 * m + 4 * q) = v[m];
 }
-
-template <int NL>
-__device__ __forceinline__ void load_a(float (&a)[NL], const float* A, int d, int q, int N) {
-#pragma unroll
-  for (int k = 0; k < NL; ++k) {
-    const int n = q * NL + k;
-    a[k] = n < N ? A[(int64_t)d * N + n] : 0.0f;
-  }
-}
-template <int NL>
-__device__ __forceinline__ void load_state(float (&h)[NL], const float* s, int64_t row, int q,
-                                           int N) {
-#pragma unroll
-  for (int k = 0; k < NL; ++k) {
-    const int n = q * NL + k;
-    h[k] = s && n < N ? s[row * N + n] : 0.0f;
-  }
-}
-template <int NL>
-__device__ __forceinline__ void store_state(const float (&h)[NL], float* s, int64_t row, int q,
+// From and to [rows][N] arrays of the caller (N need not be padded); 0 if absent.
+template <int M>
+__device__ __forceinline__ void load_states(f32x4 (&v)[M], const float* s, int64_t row, int q,
                                             int N) {
 #pragma unroll
-  for (int k = 0; k < NL; ++k) {
-    const int n = q * NL + k;
-    if (n < N) s[row * N + n] = h[k];
-  }
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int n = 16 * m + 4 * q + r;
+      v[m][r] = s && n < N ? s[row * N + n] : 0.0f;
+    }
+}
+template <int M>
+__device__ __forceinline__ void store_states(const f32x4 (&v)[M], float* s, int64_t row, int q,
+                                             int N) {
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int n = 16 * m + 4 * q + r;
+      if (n < N) s[row * N + n] = v[m][r];
+    }
 }
 
-// One thread's share of a tile's B and C (fp32 [K][NP] in LDS, 0 past the
-// text's end or N): step threadIdx.x / NP, state threadIdx.x % NP.
-template <typename E, int K, int NP>
+__device__ __forceinline__ f32x4 exp2_4(f32x4 x) {
+  return f32x4{exp2_hw(x[0]), exp2_hw(x[1]), exp2_hw(x[2]), exp2_hw(x[3])};
+}
+__device__ __forceinline__ f32x4 fma_4(f32x4 a, f32x4 b, f32x4 c) {
+  return f32x4{fmaf(a[0], b[0], c[0]), fmaf(a[1], b[1], c[1]), fmaf(a[2], b[2], c[2]),
+               fmaf(a[3], b[3], c[3])};
+}
+
+// x + y after the swap of their halves (rows): lanes of the lower half (even
+// rows) get x summed over a pair of lanes 32 (16) apart, the others y.
+__device__ __forceinline__ float swap32_add(float x, float y) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, x),
+                                                  __builtin_bit_cast(unsigned, y), false, false);
+  const unsigned lo = r[0], hi = r[1];
+  return __builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi);
+}
+__device__ __forceinline__ float swap16_add(float x, float y) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, x),
+                                                  __builtin_bit_cast(unsigned, y), false, false);
+  const unsigned lo = r[0], hi = r[1];
+  return __builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi);
+}
+// Row q of the lanes gets v[q] summed over the four rows (a channel's states).
+__device__ __forceinline__ float rows_reduce4(const float (&v)[4]) {
+  return swap16_add(swap32_add(v[0], v[2]), swap32_add(v[1], v[3]));
+}
+__device__ __forceinline__ float rows_sum(float x) {
+  return swap16_add(swap32_add(x, x), swap32_add(x, x));
+}
+
+// Orders a wave's LDS accesses through which its lanes exchange values.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// A wave's exchange of one value a step and channel: lane (c, q) puts its steps
+// 4 i + q, all rows read four steps at once.  12 floats a channel keep the 16
+// channels' reads on different banks.
+struct StepsLds {
+  static constexpr int kStride = 12, kFloats = 16 * kStride;
+  static __device__ __forceinline__ void put(float* p, int c, int q, int i, float v) {
+    p[c * kStride + 4 * i + q] = v;
+  }
+  static __device__ __forceinline__ f32x4 get(const float* p, int c, int i) {
+    return *reinterpret_cast<const f32x4*>(p + c * kStride + 4 * i);
+  }
+};
+
+// The workgroup's B and C over a tile as fp32 rows [K][NP] in LDS, 0 past
+// the text's end or N.  A thread moves one value of B or of C (M < 4), or one
+// of each: loaded a tile ahead, stored behind the tile before.
+template <typename E, int M>
 struct TileBC {
-  Walk<const E> b, c;
-  bool mine;
-  int ts;
+  static constexpr int NP = 16 * M, K = scan_tile(M), kRows = K * NP;
+  static constexpr bool kBoth = kRows == kScanThreads;
+  static_assert(kBoth || 2 * kRows == kScanThreads, "each thread has its share");
+
+  const char *b, *c;        // the thread's rows of the tile
+  uint32_t bstep, cstep;
+  int ts, e;                // its step of the tile, its place in LDS
+  bool mine, is_c;
   E vb, vc;
   bool in;
 
-  __device__ __forceinline__ TileBC(const ScanArgs<E>& s, const Place& p, int t)
-      : b(s.b, t, p.b, (int)threadIdx.x / NP,
-          p.g * s.N + min((int)threadIdx.x % NP, s.N - 1)),
-        c(s.c, t, p.b, (int)threadIdx.x / NP,
-          p.g * s.N + min((int)threadIdx.x % NP, s.N - 1)),
-        mine((int)threadIdx.x < K * NP && (int)threadIdx.x % NP < s.N),
-        ts((int)threadIdx.x / NP) {}
-  // last: the last step of the text, relative to the tile
-  __device__ __forceinline__ void load(const ScanArgs<E>&, int last) {
-    in = mine && ts <= last;
-    if (in) {
-      vb = *b.at(0);
-      vc = *c.at(0);
-    }
+  __device__ __forceinline__ TileBC(const ScanArgs<E>& s, const Place& p, int t) {
+    const int tid = threadIdx.x;
+    is_c = !kBoth && tid >= kRows;
+    e = kBoth ? tid : tid % kRows;
+    ts = e / NP;
+    const int n = e % NP;
+    mine = n < s.N;
+    const int64_t at = (int64_t)p.g * s.N + min(n, s.N - 1);
+    const Seq<const E>& first = is_c ? s.c : s.b;
+    bstep = (uint32_t)first.st * (uint32_t)sizeof(E);
+    cstep = (uint32_t)s.c.st * (uint32_t)sizeof(E);
+    b = reinterpret_cast<const char*>(first.row(t, p.b) + at) + (uint64_t)ts * bstep;
+    c = reinterpret_cast<const char*>(s.c.row(t, p.b) + at) + (uint64_t)ts * cstep;
   }
   __device__ __forceinline__ void advance(int steps) {
-    b.advance(steps);
-    c.advance(steps);
+    b += (int64_t)steps * (int64_t)bstep;
+    c += (int64_t)steps * (int64_t)cstep;
   }
-  __device__ __forceinline__ void store(float* sb, float* sc) const {
-    if ((int)threadIdx.x >= K * NP) return;
-    sb[threadIdx.x] = in ? (float)vb : 0.0f;
-    sc[threadIdx.x] = in ? (float)vc : 0.0f;
+  // last: the last step of the text, relative to the tile's first
+  __device__ __forceinline__ void load(int last) {
+    in = mine && ts <= last;
+    if (in) {
+      vb = *reinterpret_cast<const E*>(b);
+      if constexpr (kBoth) vc = *reinterpret_cast<const E*>(c);
+    }
+  }
+  // rows: [2][K][NP], B then C
+  __device__ __forceinline__ void store(float* rows) const {
+    rows[(is_c ? kRows : 0) + e] = in ? (float)vb : 0.0f;
+    if constexpr (kBoth) rows[kRows + e] = in ? (float)vc : 0.0f;
   }
 };
-
-// Offset of step `last` of a tile, for Walk::load.
-template <typename W>
-__device__ __forceinline__ uint32_t walk_limit(const W& w, int q, int last) {
-  // the lane's own offset is q steps into the tile
-  return last >= scan_tile(1) ? 0xFFFFFFFFu : w.off + (uint32_t)(last - q) * w.step;
-}
 
 template <typename E>
 __device__ __forceinline__ void zero_steps(const Seq<E>& s, const Place& p) {
@@ -235,6 +293,7 @@ __global__ __launch_bounds__(256) void scan_join(float* edge, const float* dtsum
   const int64_t row = i / NP;
   const float a2 = n < N ? kLog2e * A[row % D * N + n] : 0.0f;
   float cur = first && n < N ? first[row * N + n] : 0.0f;
+#pragma unroll 8
   for (int k = 0; k < chunks; ++k) {
     const int c = FORWARD ? k : chunks - 1 - k;
     const int64_t at = (int64_t)c * rows;

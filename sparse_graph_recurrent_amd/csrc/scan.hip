@@ -8,12 +8,12 @@
 namespace ckhip {
 namespace {
 
-ScanDims scan_dims(const ck_scan_shape& s) {
+ScanDims scan_sizes(const ck_scan_shape& s) {
   ScanDims d;
   d.T = s.T; d.B = s.B; d.D = s.D; d.N = s.N; d.G = s.G;
-  d.NL = s.N <= 4 ? 1 : s.N <= 8 ? 2 : s.N <= 16 ? 4 : s.N <= 32 ? 8 : 16;
-  d.NP = 4 * d.NL;
-  d.K = scan_tile(d.NL);
+  d.M = s.N <= 16 ? 1 : s.N <= 32 ? 2 : 4;
+  d.NP = 16 * d.M;
+  d.K = scan_tile(d.M);
   d.Dg = s.D / s.G;
   d.P = (d.Dg + kScanChan - 1) / kScanChan;
   d.tiles = (s.T + d.K - 1) / d.K;
@@ -29,46 +29,64 @@ void scan_cut(ScanDims* d, int64_t want) {
   d->chunks = std::max<int64_t>((d->tiles + per - 1) / per, 1);
 }
 
-// Workgroups below which the window is cut, and the shortest chunk.
-constexpr int64_t kScanFwdGroups = 512, kScanBwdGroups = 512, kScanMinChunk = 64;
+// Cutting pays below this many workgroups: the second pass over a chunk's steps
+// costs 0.7 of a forward's and 0.25 of a backward's main pass, the idle SIMDs
+// and single waves more.  Training pass at 2048 channels x 1024 steps in bf16,
+// uncut and cut to about 2048 workgroups: 128 workgroups 439 and 226 us, 256 473
+// and 402, 384 630 and 622, 512 642 and 768.
+constexpr int64_t kScanFewGroups = 384, kScanGoalGroups = 2048, kScanMinChunk = 64;
 
-ScanDims scan_dims(const ck_scan_shape& s, bool backward) {
-  ScanDims d = scan_dims(s);
-  const int64_t wgs = d.P * d.G * d.B, goal = backward ? kScanBwdGroups : kScanFwdGroups;
-  if (wgs * 2 <= goal)
-    scan_cut(&d, std::min(goal / wgs, std::max<int64_t>(s.T / kScanMinChunk, 1)));
+ScanDims scan_dims(const ck_scan_shape& s) {
+  ScanDims d = scan_sizes(s);
+  const int64_t wgs = d.P * d.G * d.B;
+  if (wgs < kScanFewGroups)
+    scan_cut(&d, std::min(kScanGoalGroups / wgs, std::max<int64_t>(s.T / kScanMinChunk, 1)));
   return d;
 }
 
-template <typename E, int NL>
-__global__ __launch_bounds__(kScanThreads) void scan_one(const ScanArgs<E> s) {
-  const Place p = scan_place(s);
-  if (!p.active) return;  // whole quads
-  const int64_t row = (int64_t)p.b * s.D + p.d;
-  float a[NL], h[NL];
-  load_a<NL>(a, s.a, p.d, p.q, s.N);
-  load_state<NL>(h, s.state0, row, p.q, s.N);
-  const float raw = (float)s.delta.row(0, p.b)[p.d] + (s.delta_bias ? s.delta_bias[p.d] : 0.0f);
-  const float dt = s.softplus ? softplus_hw(raw) : raw;
-  const float u = (float)s.u.row(0, p.b)[p.d], x = dt * u;
-  const E *pb = s.b.row(0, p.b) + (int64_t)p.g * s.N, *pc = s.c.row(0, p.b) + (int64_t)p.g * s.N;
-  float y = 0.0f;
+// One token.  A quad of lanes takes a channel, each lane NL adjacent states, so
+// that the states (which are all but a few bytes of what the step reads and
+// writes) move in 16-byte accesses wherever N and the addresses allow it.
+constexpr int kOneThreads = 256;
+
+template <bool FULL, int NL, typename E>
+__device__ __forceinline__ void scan_one_row(const ScanArgs<E>& s, int b, int d, int q) {
+  const int64_t row = (int64_t)b * s.D + d;
+  const int n0 = q * NL, left = s.N - n0;
+  const Pack<float, NL> a = pack_load<FULL, float, NL>(s.a + (int64_t)d * s.N + n0, left);
+  Pack<float, NL> h = {};
+  if (s.state0) h = pack_load<FULL, float, NL>(s.state0 + row * s.N + n0, left);
+  const int64_t at = (int64_t)(d / s.Dg) * s.N + n0;
+  const Pack<E, NL> bb = pack_load<FULL, E, NL>(s.b.row(0, b) + at, left);
+  const Pack<E, NL> cc = pack_load<FULL, E, NL>(s.c.row(0, b) + at, left);
+  const float raw = (float)s.delta.row(0, b)[d] + (s.delta_bias ? s.delta_bias[d] : 0.0f);
+  const float dt = s.softplus ? softplus_hw(raw).value : raw;
+  const float u = (float)s.u.row(0, b)[d], x = dt * u;
+  float y = 0.0f, hn[NL];
 #pragma unroll
   for (int k = 0; k < NL; ++k) {
-    const int n = p.q * NL + k;
-    if (n < s.N) {
-      h[k] = fmaf(exp2_hw(dt * (kLog2e * a[k])), h[k], x * (float)pb[n]);
-      y = fmaf((float)pc[n], h[k], y);
-    }
+    hn[k] = fmaf(exp2_hw(dt * (kLog2e * a.v[k])), h.v[k], x * (float)bb.v[k]);
+    y += FULL || k < left ? (float)cc.v[k] * hn[k] : 0.0f;
   }
   y = quad_sum(y);
-  if (s.d) y = fmaf(s.d[p.d], u, y);
+  if (s.d) y = fmaf(s.d[d], u, y);
   if (s.z.p) {
-    const float zf = (float)s.z.row(0, p.b)[p.d];
+    const float zf = (float)s.z.row(0, b)[d];
     y *= zf * sigmoid_hw(zf);
   }
-  if (p.q == 0) s.out.row(0, p.b)[p.d] = (E)y;
-  store_state<NL>(h, s.state, row, p.q, s.N);
+  if (q == 0) s.out.row(0, b)[d] = (E)y;
+  pack_store<FULL, float, NL>(s.state + row * s.N + n0, hn, left);
+}
+
+template <typename E, int NL>
+__global__ __launch_bounds__(kOneThreads) void scan_one(const ScanArgs<E> s) {
+  const int64_t i = (int64_t)blockIdx.x * (kOneThreads / 4) + (threadIdx.x >> 2);
+  if (i >= (int64_t)s.B * s.D) return;  // whole quads
+  const int b = (int)(i / s.D), d = (int)(i % s.D), q = threadIdx.x & 3;
+  if (s.N == 4 * NL)
+    scan_one_row<true, NL>(s, b, d, q);
+  else
+    scan_one_row<false, NL>(s, b, d, q);
 }
 
 // Workspace byte offsets of a call.
@@ -106,7 +124,7 @@ ck_status scan_check_shape(const ck_scan_shape* s) {
     return CK_ERR_BAD_SIZE;
   }
   const ScanDims d = scan_dims(*s);
-  if (d.P * d.G * d.B >= INT_MAX || d.D * d.NP >= INT_MAX ||
+  if (d.P * d.G * d.B >= INT_MAX / 2 || d.B * d.D / 64 >= INT_MAX || d.D * d.NP >= INT_MAX ||
       (d.T > 0 && d.B * d.G * d.NP >= (int64_t(1) << 36) / d.T)) {
     set_error("B=%lld, D=%lld or T=%lld is too large", (long long)d.B, (long long)d.D,
               (long long)d.T);
@@ -157,15 +175,10 @@ ScanArgs<E> scan_args(const ck_scan_shape& s, const ScanDims& d, const ck_scan_i
   return a;
 }
 
-template <typename F>
-void scan_by_states(int NL, F&& fn) {
-  switch (NL) {
-    case 1: fn(std::integral_constant<int, 1>()); break;
-    case 2: fn(std::integral_constant<int, 2>()); break;
-    case 4: fn(std::integral_constant<int, 4>()); break;
-    case 8: fn(std::integral_constant<int, 8>()); break;
-    default: fn(std::integral_constant<int, 16>()); break;
-  }
+template <typename E, int NL>
+void scan_launch_one(const ScanArgs<E>& a, hipStream_t stream) {
+  const int64_t n = (int64_t)a.B * a.D, per = kOneThreads / 4;
+  scan_one<E, NL><<<(unsigned)((n + per - 1) / per), kOneThreads, 0, stream>>>(a);
 }
 
 }  // namespace
@@ -180,8 +193,8 @@ extern "C" ck_status ck_scan_sizes(const ck_scan_shape* shape, size_t* saved_byt
   if (rc != CK_OK) return rc;
   const ScanDims d = scan_dims(*shape);
   if (saved_bytes) *saved_bytes = scan_saved(d);
-  if (forward_bytes) *forward_bytes = scan_ws(scan_dims(*shape, false), false).total;
-  if (backward_bytes) *backward_bytes = scan_ws(scan_dims(*shape, true), true).total;
+  if (forward_bytes) *forward_bytes = scan_ws(scan_dims(*shape), false).total;
+  if (backward_bytes) *backward_bytes = scan_ws(scan_dims(*shape), true).total;
   return CK_OK;
 }
 
@@ -193,7 +206,7 @@ extern "C" ck_status ck_scan_forward(const ck_scan_shape* shape, const ck_scan_i
   if (rc == CK_OK) rc = scan_check_inputs(*shape, in);
   if (rc == CK_OK) rc = seq_check(out, shape->dtype, shape->T == 0, "out");
   if (rc != CK_OK) return rc;
-  const ScanDims d = scan_dims(*shape, false);
+  const ScanDims d = scan_dims(*shape);
   const ScanWs ws = scan_ws(d, false);
   rc = seq_check_ws(workspace, workspace_bytes, ws.total);
   if (rc == CK_OK && saved) rc = check_aligned(saved, "saved");
@@ -231,7 +244,7 @@ extern "C" ck_status ck_scan_backward(const ck_scan_shape* shape, const ck_scan_
   if (rc == CK_OK)
     rc = seq_check(grads->z, shape->dtype, none || !in->z.data, "the gradient of z");
   if (rc != CK_OK) return rc;
-  const ScanDims d = scan_dims(*shape, true);
+  const ScanDims d = scan_dims(*shape);
   const ScanWs ws = scan_ws(d, true);
   rc = seq_check_ws(workspace, workspace_bytes, ws.total);
   if (rc == CK_OK && saved) rc = check_aligned(saved, "saved");
@@ -279,10 +292,16 @@ extern "C" ck_status ck_scan_step(const ck_scan_shape* shape, const ck_scan_inpu
     ScanArgs<E> a = scan_args<E>(*shape, d, *in, nullptr, ScanWs{});
     a.out = seq_of<E>(out);
     a.state = state;
-    scan_by_states(d.NL, [&](auto nl) {
-      scan_one<E, decltype(nl)::value>
-          <<<(unsigned)(d.P * d.G * d.B), kScanThreads, 0, stream>>>(a);
-    });
+    if (a.N <= 4)
+      scan_launch_one<E, 1>(a, stream);
+    else if (a.N <= 8)
+      scan_launch_one<E, 2>(a, stream);
+    else if (a.N <= 16)
+      scan_launch_one<E, 4>(a, stream);
+    else if (a.N <= 32)
+      scan_launch_one<E, 8>(a, stream);
+    else
+      scan_launch_one<E, 16>(a, stream);
     CK_HIP_TRY(hipGetLastError());
     return CK_OK;
   });

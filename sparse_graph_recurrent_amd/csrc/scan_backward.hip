@@ -9,8 +9,8 @@
 // start, from which the tile's states are computed again into registers (a
 // step back through h_{t-1} = (h_t - x) / a_t would lose everything where a_t
 // is small), then the adjoint runs down through them.  As the forward, it is
-// bound by the vector ALU.  The sums over channels of gB and gC cost most of
-// the rest: 16 values are summed over a wave's 16 channels by halving
+// bound by the vector ALU.  The sums over channels of gB and gC are a quarter
+// of its work: 16 values are summed over a wave's 16 channels by halving
 // exchanges, the four waves' sums are added in LDS and the workgroups' by a
 // last launch, all in a fixed order.
 #include "scan.h"
@@ -20,57 +20,72 @@
 namespace ckhip {
 namespace {
 
-// x + y after the swap of their halves (rows): lanes of the lower half (even
-// rows) get x summed over a pair of lanes 32 (16) apart, the others y.
-__device__ __forceinline__ float swap32_add(float x, float y) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, x),
-                                                  __builtin_bit_cast(unsigned, y), false, false);
-  const unsigned lo = r[0], hi = r[1];
-  return __builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi);
+// v[i] of the channels' lanes 0-7 of each row, v[i + 8] of lanes 8-15, summed
+// over lanes 8 apart.  (DPP operands need two wait states behind a write.)
+__device__ __forceinline__ void halve8(float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 4)
+    asm("s_nop 1\n\t"
+        "v_add_f32_dpp %0, %0, %0 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %1, %1, %1 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %2, %2, %2 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %3, %3, %3 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %0, %4, %4 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+        "v_add_f32_dpp %1, %5, %5 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+        "v_add_f32_dpp %2, %6, %6 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+        "v_add_f32_dpp %3, %7, %7 row_ror:8 row_mask:0xf bank_mask:0xc"
+        : "+v"(v[i]), "+v"(v[i + 1]), "+v"(v[i + 2]), "+v"(v[i + 3])
+        : "v"(v[i + 8]), "v"(v[i + 9]), "v"(v[i + 10]), "v"(v[i + 11]));
 }
-__device__ __forceinline__ float swap16_add(float x, float y) {
-  const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, x),
-                                                  __builtin_bit_cast(unsigned, y), false, false);
-  const unsigned lo = r[0], hi = r[1];
-  return __builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi);
+// The same for v[i] and v[i + 4] and lanes n and n ^ 7.
+__device__ __forceinline__ void halve4(float (&v)[16]) {
+  asm("s_nop 1\n\t"
+      "v_add_f32_dpp %0, %0, %0 row_half_mirror row_mask:0xf bank_mask:0x5\n\t"
+      "v_add_f32_dpp %1, %1, %1 row_half_mirror row_mask:0xf bank_mask:0x5\n\t"
+      "v_add_f32_dpp %2, %2, %2 row_half_mirror row_mask:0xf bank_mask:0x5\n\t"
+      "v_add_f32_dpp %3, %3, %3 row_half_mirror row_mask:0xf bank_mask:0x5\n\t"
+      "v_add_f32_dpp %0, %4, %4 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
+      "v_add_f32_dpp %1, %5, %5 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
+      "v_add_f32_dpp %2, %6, %6 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
+      "v_add_f32_dpp %3, %7, %7 row_half_mirror row_mask:0xf bank_mask:0xa"
+      : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3])
+      : "v"(v[4]), "v"(v[5]), "v"(v[6]), "v"(v[7]));
 }
 
-// Sums v[0..15] over the 16 channels of a wave: the lanes of channel slot s
-// (lane >> 2) receive the total of v[s].  Halving exchanges: 15 adds and about
-// as many moves, where 16 butterflies over 16 lanes would take 64 of each.
-__device__ __forceinline__ float channel_reduce16(float (&v)[16], int lane) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = swap32_add(v[i], v[i + 8]);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = swap16_add(v[i], v[i + 4]);
-  const bool b3 = lane & 8, b2 = lane & 4;
-  const float r0 = (b3 ? v[2] : v[0]) + dpp<0x128>(b3 ? v[0] : v[2]);  // row_ror:8
-  const float r1 = (b3 ? v[3] : v[1]) + dpp<0x128>(b3 ? v[1] : v[3]);
-  // exchange with lane ^ 4: reverse the quad, then mirror each half row
-  const float x = dpp<0x141>(dpp<0x1B>(b2 ? r0 : r1));
-  return (b2 ? r1 : r0) + x;
+// Sums v[0..15] over a wave's 16 channels (the lanes of a row): lane c of each
+// row gets the total of v[c].  Halving exchanges with lanes c ^ 8, c ^ 7,
+// c ^ 2 and c ^ 1 (each one DPP): 33 operations, where 16 butterflies take 64.
+__device__ __forceinline__ float channel_reduce16(float (&v)[16], int c) {
+  halve8(v);
+  halve4(v);
+  const bool b1 = c & 2, b0 = c & 1;
+  const float r0 = (b1 ? v[2] : v[0]) + quad_xor2(b1 ? v[0] : v[2]);
+  const float r1 = (b1 ? v[3] : v[1]) + quad_xor2(b1 ? v[1] : v[3]);
+  return (b0 ? r1 : r0) + quad_xor1(b0 ? r0 : r1);
 }
 
 // The adjoint's share of a chunk: what it hands to the chunk before, given
 // nothing from the one behind, and the sum of the chunk's dt.
-template <typename E, int NL, bool GATE>
-__global__ __launch_bounds__(kScanThreads, 2) void scan_bwd_part(const ScanArgs<E> s) {
-  constexpr int K = scan_tile(NL), KQ = K / 4, NP = 4 * NL;
-  __shared__ float sb[2][K * NP], sc[2][K * NP];
+template <typename E, int M, bool GATE>
+__global__ __launch_bounds__(kScanThreads) void scan_bwd_part(const ScanArgs<E> s) {
+  constexpr int K = scan_tile(M), KQ = K / 4, NP = 16 * M;
+  __shared__ __align__(16) float lds_dt[4][StepsLds::kFloats], lds_dy[4][StepsLds::kFloats];
+  __shared__ __align__(16) float lds_bc[2][2 * K * NP];
   Place p = scan_place(s);
   // chunk 0 hands nothing on: the grid covers chunks 1 ..
   p.chunk += 1;
   p.t0 += s.chunk_steps;
   p.t1 = min(p.t0 + s.chunk_steps, s.T);
   p.te = min(p.t1, p.len);
-  const int q = p.q;
+  const int q = p.q, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float *ldt = lds_dt[wave], *ldy = lds_dy[wave];
   const int64_t row = (int64_t)p.b * s.D + p.d;
-  float a2[NL], g[NL];
-  load_a<NL>(a2, s.a, p.d, q, s.N);
+  f32x4 a2[M], g[M];
+  load_states<M>(a2, s.a, p.d, q, s.N);
 #pragma unroll
-  for (int k = 0; k < NL; ++k) {
-    a2[k] *= kLog2e;
-    g[k] = 0.0f;
+  for (int m = 0; m < M; ++m) {
+    a2[m] *= kLog2e;
+    g[m] = 0.0f;
   }
   const float bias = s.delta_bias ? s.delta_bias[p.d] : 0.0f;
   float dtsum = 0.0f;
@@ -78,95 +93,102 @@ __global__ __launch_bounds__(kScanThreads, 2) void scan_bwd_part(const ScanArgs<
     const int tl = p.t0 + (p.te - 1 - p.t0) / K * K;
     Walk<const E> wd(s.delta, tl, p.b, q, p.d), wg(s.go, tl, p.b, q, p.d);
     Walk<const E> wz(GATE ? s.z : s.go, tl, p.b, q, p.d);
-    TileBC<E, K, NP> bc(s, p, tl);
+    TileBC<E, M> bc(s, p, tl);
     E de[KQ], go[KQ], z[KQ];
     auto fetch = [&](int last) {
-      const uint32_t ld = walk_limit(wd, q, last), lg = walk_limit(wg, q, last);
+      const uint32_t ld = wd.limit(q, last), lg = wg.limit(q, last);
 #pragma unroll
       for (int i = 0; i < KQ; ++i) {
         de[i] = wd.load(4 * i, ld);
         go[i] = wg.load(4 * i, lg);
       }
       if constexpr (GATE) {
-        const uint32_t lz = walk_limit(wz, q, last);
+        const uint32_t lz = wz.limit(q, last);
 #pragma unroll
         for (int i = 0; i < KQ; ++i) z[i] = wz.load(4 * i, lz);
       }
-      bc.load(s, last);
     };
     fetch(p.te - 1 - tl);
+    bc.load(p.te - 1 - tl);
+    bc.store(lds_bc[0]);
+    __syncthreads();
     int buf = 0;
     for (int t0 = tl; t0 >= p.t0; t0 -= K, buf ^= 1) {
       const int last = p.te - 1 - t0;
-      bc.store(sb[buf], sc[buf]);
-      __syncthreads();
-      float dt[KQ], dy[KQ];
+      const bool more = t0 > p.t0;
+      wave_sync();
 #pragma unroll
       for (int i = 0; i < KQ; ++i) {
         const bool in = 4 * i + q <= last;
-        const float raw = (float)de[i] + bias, sp = softplus_hw(raw);
-        dt[i] = in ? (s.softplus ? sp : raw) : 0.0f;
-        dtsum += dt[i];
+        const float raw = (float)de[i] + bias, sp = softplus_hw(raw).value;
+        StepsLds::put(ldt, p.c, q, i, in ? (s.softplus ? sp : raw) : 0.0f);
         float y = (float)go[i];
         if constexpr (GATE) {
           const float zf = (float)z[i];
           y *= zf * sigmoid_hw(zf);
         }
-        dy[i] = in ? y : 0.0f;
+        StepsLds::put(ldy, p.c, q, i, in ? y : 0.0f);
       }
-      if (t0 > p.t0) {
+      wave_sync();
+      if (more) {
         wd.advance(-K);
         wg.advance(-K);
         if constexpr (GATE) wz.advance(-K);
         bc.advance(-K);
         fetch(last + K);
+        bc.load(last + K);
       }
-      const float* lc = &sc[buf][q * NL];
+      const float* lc = lds_bc[buf] + K * NP;
 #pragma unroll
       for (int i = KQ - 1; i >= 0; --i) {
-        auto step = [&](auto jc) {
-          constexpr int j = decltype(jc)::value;
-          const float dj = quad_get<j>(dt[i]), yj = quad_get<j>(dy[i]);
-          float cc[NL];
-          load_vec<NL>(cc, lc + (4 * i + j) * NP);
+        const f32x4 d4 = StepsLds::get(ldt, p.c, i), y4 = StepsLds::get(ldy, p.c, i);
+        dtsum += (d4[0] + d4[1]) + (d4[2] + d4[3]);
 #pragma unroll
-          for (int k = 0; k < NL; ++k) g[k] = exp2_hw(dj * a2[k]) * fmaf(cc[k], yj, g[k]);
-        };
-        step(std::integral_constant<int, 3>());
-        step(std::integral_constant<int, 2>());
-        step(std::integral_constant<int, 1>());
-        step(std::integral_constant<int, 0>());
+        for (int j = 3; j >= 0; --j) {
+          f32x4 c4[M];
+          load_rows<M>(c4, lc + (4 * i + j) * NP, q);
+#pragma unroll
+          for (int m = 0; m < M; ++m)
+            g[m] = exp2_4(d4[j] * a2[m]) * fma_4(c4[m], f32x4(y4[j]), g[m]);
+        }
       }
+      if (more) bc.store(lds_bc[buf ^ 1]);
+      __syncthreads();
     }
   }
-  dtsum = quad_sum(dtsum);
   if (!p.active) return;
   const int64_t at = (int64_t)p.chunk * s.B * s.D + row;
-  store_vec<NL>(s.edge + at * NP + q * NL, g);
+  store_rows<M>(s.edge + at * NP, g, q);
   if (q == 0) s.dtsum[at] = dtsum;
 }
 
-template <typename E, int NL, bool GATE>
-__global__ __launch_bounds__(kScanThreads, 1) void scan_bwd(const ScanArgs<E> s) {
-  constexpr int K = scan_tile(NL), KQ = K / 4, NP = 4 * NL;
-  __shared__ float sb[K * NP], sc[K * NP];
-  __shared__ float red[4][K * 2 * NP];
+template <typename E, int M, bool GATE>
+__global__ __launch_bounds__(kScanThreads, M < 4 ? 2 : 1) void scan_bwd(const ScanArgs<E> s) {
+  constexpr int K = scan_tile(M), KQ = K / 4, NP = 16 * M;
+  __shared__ __align__(16) float lds_dt[4][StepsLds::kFloats];
+  __shared__ __align__(16) float lds_x[4][StepsLds::kFloats];
+  __shared__ __align__(16) float lds_dy[4][StepsLds::kFloats];
+  __shared__ __align__(16) float lds_bc[2][2 * K * NP];
+  __shared__ __align__(16) float red[4][K * 2 * NP];
   const Place p = scan_place(s);
-  const int q = p.q, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int q = p.q, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float *ldt = lds_dt[wave], *lx = lds_x[wave], *ldy = lds_dy[wave];
   const int64_t row = (int64_t)p.b * s.D + p.d;
-  float a1[NL], ga[NL], g[NL];
-  load_a<NL>(a1, s.a, p.d, q, s.N);
+  f32x4 a1[M], ga[M], g[M];
+  load_states<M>(a1, p.active ? s.a : nullptr, p.d, q, s.N);
 #pragma unroll
-  for (int k = 0; k < NL; ++k) ga[k] = 0.0f;
-  if (s.chunks > 1)
-    load_vec<NL>(g, s.edge + ((int64_t)p.chunk * s.B * s.D + row) * NP + q * NL);
-  else
-    load_state<NL>(g, s.gstate, row, q, s.N);
+  for (int m = 0; m < M; ++m) ga[m] = g[m] = 0.0f;
+  // Lanes without a channel hold zeros throughout, so they add nothing to gB, gC.
+  if (p.active) {
+    if (s.chunks > 1)
+      load_rows<M>(g, s.edge + ((int64_t)p.chunk * s.B * s.D + row) * NP, q);
+    else
+      load_states<M>(g, s.gstate, row, q, s.N);
+  }
   const float bias = s.delta_bias ? s.delta_bias[p.d] : 0.0f;
   const float skip = s.d ? s.d[p.d] : 0.0f;
   float gskip = 0.0f, gbias = 0.0f;
-  // what this lane ends channel_reduce16 with: a step of the flush, B or C, a state
-  const int slot = lane >> 2;
+  const bool part_wg = (p.blk + 1) * kScanChan > s.Dg;  // some lanes have no channel
 
   if (p.t0 < p.te) {
     const int tl = p.t0 + (p.te - 1 - p.t0) / K * K;
@@ -174,14 +196,15 @@ __global__ __launch_bounds__(kScanThreads, 1) void scan_bwd(const ScanArgs<E> s)
     Walk<const E> wg(s.go, tl, p.b, q, p.d), wz(GATE ? s.z : s.u, tl, p.b, q, p.d);
     Walk<E> ou(s.gu, tl, p.b, q, p.d), od(s.gdelta, tl, p.b, q, p.d);
     Walk<E> oz(GATE ? s.gz : s.gu, tl, p.b, q, p.d);
-    TileBC<E, K, NP> bc(s, p, tl);
+    TileBC<E, M> bc(s, p, tl);
     const int64_t ck_step = (int64_t)s.B * s.D * NP;
-    const float* ck = s.saved + (int64_t)(tl / K) * ck_step + row * NP + q * NL;
+    const float* ck = s.saved + (int64_t)(tl / K) * ck_step + row * NP;
     E eu[KQ], ede[KQ], ez[KQ], ego[KQ];
-    float h[NL];
+    f32x4 h[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m) h[m] = 0.0f;
     auto fetch = [&](int last) {
-      const uint32_t lu = walk_limit(wu, q, last), ld = walk_limit(wd, q, last);
-      const uint32_t lg = walk_limit(wg, q, last);
+      const uint32_t lu = wu.limit(q, last), ld = wd.limit(q, last), lg = wg.limit(q, last);
 #pragma unroll
       for (int i = 0; i < KQ; ++i) {
         eu[i] = wu.load(4 * i, lu);
@@ -189,132 +212,149 @@ __global__ __launch_bounds__(kScanThreads, 1) void scan_bwd(const ScanArgs<E> s)
         ego[i] = wg.load(4 * i, lg);
       }
       if constexpr (GATE) {
-        const uint32_t lz = walk_limit(wz, q, last);
+        const uint32_t lz = wz.limit(q, last);
 #pragma unroll
         for (int i = 0; i < KQ; ++i) ez[i] = wz.load(4 * i, lz);
       }
-      bc.load(s, last);
-      load_vec<NL>(h, ck);
+      if (p.active) load_rows<M>(h, ck, q);
     };
     fetch(p.te - 1 - tl);
+    bc.load(p.te - 1 - tl);
+    bc.store(lds_bc[0]);
+    __syncthreads();
 
-    for (int t0 = tl; t0 >= p.t0; t0 -= K) {
-      const int last = p.te - 1 - t0;
-      bc.store(sb, sc);
-      float dt[KQ], x[KQ], u[KQ], dy[KQ], raw[KQ], gzf[KQ];
+    int buf = 0;
+    for (int t0 = tl; t0 >= p.t0; t0 -= K, buf ^= 1) {
+      const int last = p.te - 1 - t0;  // of the tile's steps, the last with text
+      const bool more = t0 > p.t0;
+      float dt[KQ], u[KQ], dy[KQ], sg[KQ], gzf[KQ];
 #pragma unroll
       for (int i = 0; i < KQ; ++i) {
-        const bool in = 4 * i + q <= last;
-        raw[i] = (float)ede[i] + bias;
-        const float sp = softplus_hw(raw[i]);
-        dt[i] = in ? (s.softplus ? sp : raw[i]) : 0.0f;
-        u[i] = in ? (float)eu[i] : 0.0f;
-        x[i] = dt[i] * u[i];
-        dy[i] = in ? (float)ego[i] : 0.0f;
+        const float raw = (float)ede[i] + bias;
+        const Softplus sp = softplus_hw(raw);
+        sg[i] = s.softplus ? sp.slope : 1.0f;
+        dt[i] = s.softplus ? sp.value : raw;
+        u[i] = (float)eu[i];
+        dy[i] = (float)ego[i];
         if constexpr (GATE) {
-          const float zf = in ? (float)ez[i] : 0.0f, sg = sigmoid_hw(zf);
-          gzf[i] = dy[i] * (sg * fmaf(zf, 1.0f - sg, 1.0f));
-          dy[i] *= zf * sg;
+          const float zf = (float)ez[i], sz = sigmoid_hw(zf);
+          gzf[i] = dy[i] * (sz * fmaf(zf, 1.0f - sz, 1.0f));
+          dy[i] *= zf * sz;
         }
       }
-      __syncthreads();
-
-      // the tile's states again, from its first
-      float a[K][NL], hp[K][NL];
+      if (last < K - 1 || part_wg) {
+#pragma unroll
+        for (int i = 0; i < KQ; ++i) {
+          const bool in = 4 * i + q <= last && p.active;
+          sg[i] = in ? sg[i] : 0.0f;
+          dt[i] = in ? dt[i] : 0.0f;
+          u[i] = in ? u[i] : 0.0f;
+          dy[i] = in ? dy[i] : 0.0f;
+        }
+      }
+      wave_sync();
 #pragma unroll
       for (int i = 0; i < KQ; ++i) {
-        float acc[4];
-        auto step = [&](auto jc) {
-          constexpr int j = decltype(jc)::value;
-          const int t = 4 * i + j;
-          const float dj = quad_get<j>(dt[i]), xj = quad_get<j>(x[i]);
-          float bb[NL], cc[NL];
-          load_vec<NL>(bb, &sb[t * NP + q * NL]);
-          if constexpr (GATE) load_vec<NL>(cc, &sc[t * NP + q * NL]);
-          float y = 0.0f;
-#pragma unroll
-          for (int k = 0; k < NL; ++k) {
-            a[t][k] = exp2_hw(dj * (kLog2e * a1[k]));
-            hp[t][k] = h[k];
-            h[k] = fmaf(a[t][k], h[k], xj * bb[k]);
-            if constexpr (GATE) y = k ? fmaf(cc[k], h[k], y) : cc[k] * h[k];
-          }
-          acc[j] = y;
-        };
-        step(std::integral_constant<int, 0>());
-        step(std::integral_constant<int, 1>());
-        step(std::integral_constant<int, 2>());
-        step(std::integral_constant<int, 3>());
-        if constexpr (GATE)
-          gzf[i] *= fmaf(skip, u[i], quad_reduce4(acc[0], acc[1], acc[2], acc[3], q));
+        StepsLds::put(ldt, p.c, q, i, dt[i]);
+        StepsLds::put(lx, p.c, q, i, dt[i] * u[i]);
+        StepsLds::put(ldy, p.c, q, i, dy[i]);
       }
+      wave_sync();
+      if (more) {
+        bc.advance(-K);
+        bc.load(last + K);
+      }
+      const float *lb = lds_bc[buf], *lc = lb + K * NP;
+
+      // the tile's states again, from its first
+      f32x4 a[K][M], before[K][M];  // decays, and the states before each step
+#pragma unroll
+      for (int i = 0; i < KQ; ++i) {
+        const f32x4 d4 = StepsLds::get(ldt, p.c, i), x4 = StepsLds::get(lx, p.c, i);
+        float acc[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f32x4 y4 = 0.0f, b4[M], c4[M];
+          load_rows<M>(b4, lb + (4 * i + j) * NP, q);
+          if constexpr (GATE) load_rows<M>(c4, lc + (4 * i + j) * NP, q);
+#pragma unroll
+          for (int m = 0; m < M; ++m) {
+            a[4 * i + j][m] = exp2_4(d4[j] * (kLog2e * a1[m]));
+            before[4 * i + j][m] = h[m];
+            h[m] = fma_4(a[4 * i + j][m], h[m], x4[j] * b4[m]);
+            if constexpr (GATE) y4 = m ? fma_4(c4[m], h[m], y4) : c4[m] * h[m];
+          }
+          acc[j] = (y4[0] + y4[1]) + (y4[2] + y4[3]);
+        }
+        if constexpr (GATE) gzf[i] *= fmaf(skip, u[i], rows_reduce4(acc));
+      }
+
+      if (more) bc.store(lds_bc[buf ^ 1]);
+      __syncthreads();  // (and the waves' sums of the tiles before are read)
 
       // and backwards: g enters a step as a_{t+1} dL/dh_{t+1}
       float v[16], gu[KQ], gd[KQ];
 #pragma unroll
       for (int i = KQ - 1; i >= 0; --i) {
+        const f32x4 d4 = StepsLds::get(ldt, p.c, i), x4 = StepsLds::get(lx, p.c, i);
+        const f32x4 y4 = StepsLds::get(ldy, p.c, i);
         float sx[4], sa[4];
-        auto step = [&](auto jc) {
-          constexpr int j = decltype(jc)::value;
-          const int t = 4 * i + j;
-          const float dj = quad_get<j>(dt[i]), xj = quad_get<j>(x[i]), yj = quad_get<j>(dy[i]);
-          float bb[NL], cc[NL];
-          load_vec<NL>(bb, &sb[t * NP + q * NL]);
-          load_vec<NL>(cc, &sc[t * NP + q * NL]);
-          float s1 = 0.0f, s2 = 0.0f;
-          [[maybe_unused]] float v2[16];
 #pragma unroll
-          for (int k = 0; k < NL; ++k) {
-            const float gh = fmaf(cc[k], yj, g[k]);
-            const float ht = t + 1 < K ? hp[t + 1 < K ? t + 1 : t][k] : h[k];
-            // inactive lanes repeat the group's last channel: they add nothing
-            const float vgb = p.active ? gh * xj : 0.0f, vgc = p.active ? ht * yj : 0.0f;
-            if constexpr (NL <= 8) {
-              const int tt = t % (8 / NL);
-              v[tt * 2 * NL + k] = vgb;
-              v[tt * 2 * NL + NL + k] = vgc;
-            } else {
-              v[k] = vgb;
-              v2[k] = vgc;
+        for (int j = 3; j >= 0; --j) {
+          const int t = 4 * i + j;
+          f32x4 b4[M], c4[M], s1 = 0.0f, s2 = 0.0f;
+          load_rows<M>(b4, lb + t * NP, q);
+          load_rows<M>(c4, lc + t * NP, q);
+#pragma unroll
+          for (int m = 0; m < M; ++m) {
+            const f32x4 gh = fma_4(c4[m], f32x4(y4[j]), g[m]);
+            const f32x4 vb = gh * x4[j], vc = h[m] * y4[j];
+            h[m] = before[t][m];
+            s1 = m ? fma_4(gh, b4[m], s1) : gh * b4[m];
+            g[m] = a[t][m] * gh;
+            const f32x4 w = g[m] * h[m];
+            ga[m] = fma_4(w, f32x4(d4[j]), ga[m]);
+            s2 = m ? fma_4(w, a1[m], s2) : w * a1[m];
+            // values of two (step, block) pairs make 16 sums over the channels
+            const int half = (t * M + m) % 2;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              v[half * 8 + r] = vb[r];
+              v[half * 8 + 4 + r] = vc[r];
             }
-            s1 = fmaf(gh, bb[k], s1);
-            g[k] = a[t][k] * gh;
-            const float w = g[k] * hp[t][k];
-            ga[k] = fmaf(w, dj, ga[k]);
-            s2 = fmaf(w, a1[k], s2);
-          }
-          sx[j] = s1;
-          sa[j] = s2;
-          if constexpr (NL <= 8) {
-            if (t % (8 / NL) == 0) {
-              const float r = channel_reduce16(v, lane);
-              const int tt = slot / (2 * NL), kind = slot / NL % 2, k = slot % NL;
-              red[wave][((t + tt) * 2 + kind) * NP + q * NL + k] = r;
+            if constexpr (M > 1) {
+              // pairs are the blocks 2 k, 2 k + 1 of a step
+              if (half == 1) {
+                const int kind = p.c / 4 % 2, blk = m - 1 + p.c / 8;
+                red[wave][(t * 2 + kind) * NP + 16 * blk + 4 * q + p.c % 4] =
+                    channel_reduce16(v, p.c);
+              }
             }
-          } else {
-            red[wave][(t * 2) * NP + q * NL + slot] = channel_reduce16(v, lane);
-            red[wave][(t * 2 + 1) * NP + q * NL + slot] = channel_reduce16(v2, lane);
           }
-        };
-        step(std::integral_constant<int, 3>());
-        step(std::integral_constant<int, 2>());
-        step(std::integral_constant<int, 1>());
-        step(std::integral_constant<int, 0>());
-        const float gx = quad_reduce4(sx[0], sx[1], sx[2], sx[3], q);  // dL/d(dt u)
-        const float gl = quad_reduce4(sa[0], sa[1], sa[2], sa[3], q);  // sum_n dL/d(dt A) A
-        const float sg = sigmoid_hw(raw[i]), gr = fmaf(u[i], gx, gl);
-        gd[i] = 4 * i + q <= last ? (s.softplus ? gr * sg : gr) : 0.0f;
+          if constexpr (M == 1) {
+            // pairs are the steps t + 1 and t (t even)
+            if (t % 2 == 0) {
+              const int kind = p.c / 4 % 2;
+              red[wave][((t + p.c / 8) * 2 + kind) * NP + 4 * q + p.c % 4] =
+                  channel_reduce16(v, p.c);
+            }
+          }
+          sx[j] = (s1[0] + s1[1]) + (s1[2] + s1[3]);
+          sa[j] = (s2[0] + s2[1]) + (s2[2] + s2[3]);
+        }
+        const float gx = rows_reduce4(sx);  // dL/d(dt u)
+        const float gl = rows_reduce4(sa);  // sum_n dL/d(dt A) A
+        gd[i] = fmaf(u[i], gx, gl) * sg[i];
         gu[i] = fmaf(dt[i], gx, skip * dy[i]);
         gbias += gd[i];
         gskip = fmaf(dy[i], u[i], gskip);
       }
-      // the tile before, while the waves' sums are joined
-      if (t0 > p.t0) {
+      // the tiles before, while the waves' sums are joined
+      if (more) {
         wu.advance(-K);
         wd.advance(-K);
         wg.advance(-K);
         if constexpr (GATE) wz.advance(-K);
-        bc.advance(-K);
         ck -= ck_step;
         fetch(last + K);
       }
@@ -343,12 +383,14 @@ __global__ __launch_bounds__(kScanThreads, 1) void scan_bwd(const ScanArgs<E> s)
   zero_steps(s.gdelta, p);
   if constexpr (GATE) zero_steps(s.gz, p);
   if (!p.active) return;
-  if (s.gstate0 && p.chunk == 0) store_state<NL>(g, s.gstate0, row, q, s.N);
+  if (s.gstate0 && p.chunk == 0) store_states<M>(g, s.gstate0, row, q, s.N);
   float* pa = s.part_a + ((int64_t)p.chunk * s.B * s.D + row) * (NP + 2);
 #pragma unroll
-  for (int k = 0; k < NL; ++k) pa[q * NL + k] = ga[k];
-  gskip = quad_sum(gskip);
-  gbias = quad_sum(gbias);
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) pa[16 * m + 4 * q + r] = ga[m][r];
+  gskip = rows_sum(gskip);
+  gbias = rows_sum(gbias);
   if (q == 0) {
     pa[NP] = gskip;
     pa[NP + 1] = gbias;
@@ -370,50 +412,63 @@ __global__ __launch_bounds__(256) void scan_sum_bc(const float* part, int T, int
   const int b = (int)(r % B), t = (int)(r / B);
   if (n >= N) return;
   float sum = 0.0f;
-  if (!lengths || t < lengths[b])
+  if (!lengths || t < lengths[b]) {
+#pragma unroll 8
     for (int k = 0; k < P; ++k) sum += part[k * stride + i];
+  }
   (kind ? gc : gb).row(t, b)[(int64_t)g * N + n] = (E)sum;
 }
 
-// Gradients of A, D and the bias: the sums of all rows and chunks, in order.
+// Gradients of A, D and the bias: the sums of all rows and chunks in a fixed
+// order.  A workgroup takes 32 sums, eight threads each one a stretch of them.
 __global__ __launch_bounds__(256) void scan_sum_a(const float* part, int64_t D, int N, int NP,
                                                   int64_t rows, float* ga, float* gd,
                                                   float* gbias) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= D * (NP + 2)) return;
+  __shared__ float red[8][32];
+  const int64_t all = D * (NP + 2), i = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
+  const int y = threadIdx.x >> 5;
+  const int64_t each = (rows + 7) / 8, r0 = each * y, r1 = min(r0 + each, rows);
+  float sum = 0.0f;
+  if (i < all) {
+#pragma unroll 4
+    for (int64_t r = r0; r < r1; ++r) sum += part[r * all + i];
+  }
+  red[y][threadIdx.x & 31] = sum;
+  __syncthreads();
+  if (y != 0 || i >= all) return;
+  sum = 0.0f;
+  for (int j = 0; j < 8; ++j) sum += red[j][threadIdx.x];
   const int n = (int)(i % (NP + 2));
   const int64_t d = i / (NP + 2);
-  float* out = n < N ? ga + d * N + n : n < NP ? nullptr : n == NP ? gd : gbias;
-  if (!out) return;
-  if (n >= NP) out += d;
-  float sum = 0.0f;
-  for (int64_t r = 0; r < rows; ++r) sum += part[r * D * (NP + 2) + i];
-  *out = sum;
+  if (n < N)
+    ga[d * N + n] = sum;
+  else if (n == NP && gd)
+    gd[d] = sum;
+  else if (n == NP + 1 && gbias)
+    gbias[d] = sum;
 }
 
-template <typename E, int NL>
+template <typename E, int M>
 void launch(const ScanDims& d, const ScanArgs<E>& a, hipStream_t stream) {
-  const unsigned wgs = (unsigned)(d.P * d.G * d.B);
+  const unsigned wgs = (unsigned)(d.P * d.G * d.B), grid = wgs * (unsigned)d.chunks;
   if (d.chunks > 1) {
-    const unsigned grid = wgs * (unsigned)(d.chunks - 1);
     if (a.z.p)
-      scan_bwd_part<E, NL, true><<<grid, kScanThreads, 0, stream>>>(a);
+      scan_bwd_part<E, M, true><<<grid - wgs, kScanThreads, 0, stream>>>(a);
     else
-      scan_bwd_part<E, NL, false><<<grid, kScanThreads, 0, stream>>>(a);
+      scan_bwd_part<E, M, false><<<grid - wgs, kScanThreads, 0, stream>>>(a);
     const int64_t n = d.B * d.D * d.NP;
     scan_join<false><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
         a.edge, a.dtsum, a.a, a.gstate, d.B * d.D, a.D, a.N, d.NP, a.chunks);
   }
-  const unsigned grid = wgs * (unsigned)d.chunks;
   if (a.z.p)
-    scan_bwd<E, NL, true><<<grid, kScanThreads, 0, stream>>>(a);
+    scan_bwd<E, M, true><<<grid, kScanThreads, 0, stream>>>(a);
   else
-    scan_bwd<E, NL, false><<<grid, kScanThreads, 0, stream>>>(a);
+    scan_bwd<E, M, false><<<grid, kScanThreads, 0, stream>>>(a);
   const int64_t bc = d.T * d.B * d.G * 2 * d.NP, ae = d.D * (d.NP + 2);
   if (bc > 0)
     scan_sum_bc<E><<<(unsigned)((bc + 255) / 256), 256, 0, stream>>>(
         a.part_bc, a.T, a.B, a.G, a.N, d.NP, a.P, a.lengths, a.gb, a.gc);
-  scan_sum_a<<<(unsigned)((ae + 255) / 256), 256, 0, stream>>>(
+  scan_sum_a<<<(unsigned)((ae + 31) / 32), 256, 0, stream>>>(
       a.part_a, d.D, a.N, d.NP, d.chunks * d.B, a.ga, a.gd, a.gbias);
 }
 
@@ -421,12 +476,10 @@ void launch(const ScanDims& d, const ScanArgs<E>& a, hipStream_t stream) {
 
 template <typename E>
 void scan_launch_backward(const ScanDims& d, const ScanArgs<E>& a, hipStream_t stream) {
-  switch (d.NL) {
+  switch (d.M) {
     case 1: return launch<E, 1>(d, a, stream);
     case 2: return launch<E, 2>(d, a, stream);
-    case 4: return launch<E, 4>(d, a, stream);
-    case 8: return launch<E, 8>(d, a, stream);
-    default: return launch<E, 16>(d, a, stream);
+    default: return launch<E, 4>(d, a, stream);
   }
 }
 template void scan_launch_backward<float>(const ScanDims&, const ScanArgs<float>&, hipStream_t);

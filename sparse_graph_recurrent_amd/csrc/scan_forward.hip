@@ -1,11 +1,4 @@
 // scan_forward.hip -- the selective scan over a window (see scan.h).
-//
-// What bounds it is the vector ALU: per step and state an exponential, two
-// products and two multiply-adds, against 6 to 8 bytes per step and channel of
-// 16-bit tensors.  A wave's steps depend on each other only through h, one
-// multiply-add a step, so a single wave per SIMD keeps its ALU busy as long as
-// nothing else is waited for: the next tile's global loads are issued a tile
-// ahead and B, C come from LDS four steps ahead of their use.
 #include "scan.h"
 
 #include <type_traits>
@@ -14,26 +7,29 @@ namespace ckhip {
 namespace {
 
 // PART: only the chunk's summary (what it makes of a zero state, sum of dt).
-template <typename E, int NL, bool GATE, bool PART>
-__global__ __launch_bounds__(kScanThreads, 2) void scan_fwd(const ScanArgs<E> s) {
-  constexpr int K = scan_tile(NL), KQ = K / 4, NP = 4 * NL;
-  __shared__ float sb[2][K * NP], sc[2][K * NP];
+template <typename E, int M, bool GATE, bool PART>
+__global__ __launch_bounds__(kScanThreads) void scan_fwd(const ScanArgs<E> s) {
+  constexpr int K = scan_tile(M), KQ = K / 4, NP = 16 * M;
+  __shared__ __align__(16) float lds_dt[4][StepsLds::kFloats];
+  __shared__ __align__(16) float lds_x[4][StepsLds::kFloats];
+  __shared__ __align__(16) float lds_bc[2][2 * K * NP];
   const Place p = scan_place(s);
-  const int q = p.q;
+  const int q = p.q, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float *ldt = lds_dt[wave], *lx = lds_x[wave];
   const int64_t row = (int64_t)p.b * s.D + p.d;
-  const int64_t edge = ((int64_t)p.chunk * s.B * s.D + row) * NP + q * NL;
-  float a2[NL], h[NL];
-  load_a<NL>(a2, s.a, p.d, q, s.N);
+  float* edge = s.edge + ((int64_t)p.chunk * s.B * s.D + row) * NP;
+  f32x4 a2[M], h[M];
+  load_states<M>(a2, s.a, p.d, q, s.N);
 #pragma unroll
-  for (int k = 0; k < NL; ++k) {
-    a2[k] *= kLog2e;
-    h[k] = 0.0f;
+  for (int m = 0; m < M; ++m) {
+    a2[m] *= kLog2e;
+    h[m] = 0.0f;
   }
   if constexpr (!PART) {
     if (s.chunks > 1)
-      load_vec<NL>(h, s.edge + edge);
+      load_rows<M>(h, edge, q);
     else
-      load_state<NL>(h, s.state0, row, q, s.N);
+      load_states<M>(h, s.state0, row, q, s.N);
   }
   const float bias = s.delta_bias ? s.delta_bias[p.d] : 0.0f;
   const float skip = s.d ? s.d[p.d] : 0.0f;
@@ -43,109 +39,93 @@ __global__ __launch_bounds__(kScanThreads, 2) void scan_fwd(const ScanArgs<E> s)
     Walk<const E> wu(s.u, p.t0, p.b, q, p.d), wd(s.delta, p.t0, p.b, q, p.d);
     Walk<const E> wz(GATE ? s.z : s.u, p.t0, p.b, q, p.d);
     Walk<E> wo(s.out, p.t0, p.b, q, p.d);
-    TileBC<E, K, NP> bc(s, p, p.t0);
+    TileBC<E, M> bc(s, p, p.t0);
     E u[KQ], de[KQ], z[KQ];
     auto fetch = [&](int last) {
-      const uint32_t lu = walk_limit(wu, q, last), ld = walk_limit(wd, q, last);
+      const uint32_t lu = wu.limit(q, last), ld = wd.limit(q, last);
 #pragma unroll
       for (int i = 0; i < KQ; ++i) {
         u[i] = wu.load(4 * i, lu);
         de[i] = wd.load(4 * i, ld);
       }
       if constexpr (GATE && !PART) {
-        const uint32_t lz = walk_limit(wz, q, last);
+        const uint32_t lz = wz.limit(q, last);
 #pragma unroll
         for (int i = 0; i < KQ; ++i) z[i] = wz.load(4 * i, lz);
       }
-      bc.load(s, last);
     };
     fetch(p.te - 1 - p.t0);
-    float* ck = s.saved;
+    bc.load(p.te - 1 - p.t0);
+    bc.store(lds_bc[0]);
     const int64_t ck_step = (int64_t)s.B * s.D * NP;
-    if (ck) ck += (int64_t)(p.t0 / K) * ck_step + row * NP + q * NL;
+    float* ck = nullptr;
+    if (s.saved) ck = s.saved + (int64_t)(p.t0 / K) * ck_step + row * NP;
+    __syncthreads();
 
     int buf = 0;
     for (int t0 = p.t0; t0 < p.te; t0 += K, buf ^= 1) {
       const int last = p.te - 1 - t0;  // of the tile's steps, the last with text
-      bc.store(sb[buf], sc[buf]);
-      __syncthreads();
-      float bb[4][NL], cc[4][NL];
-      const float *lb = &sb[buf][q * NL], *lc = &sc[buf][q * NL];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        load_vec<NL>(bb[j], lb + j * NP);
-        if constexpr (!PART) load_vec<NL>(cc[j], lc + j * NP);
-      }
+      const bool more = t0 + K < p.te;
       float dt[KQ], x[KQ], y0[KQ], gt[KQ];
 #pragma unroll
       for (int i = 0; i < KQ; ++i) {
-        const bool in = 4 * i + q <= last;
-        const float raw = (float)de[i] + bias, sp = softplus_hw(raw);
-        dt[i] = in ? (s.softplus ? sp : raw) : 0.0f;
-        const float uf = in ? (float)u[i] : 0.0f;
-        x[i] = dt[i] * uf;
-        if constexpr (PART) {
-          dtsum += dt[i];
-        } else {
-          y0[i] = skip * uf;
-          gt[i] = 1.0f;
-          if constexpr (GATE) {
-            const float zf = (float)z[i];
-            gt[i] = zf * sigmoid_hw(zf);
-          }
+        const float raw = (float)de[i] + bias, sp = softplus_hw(raw).value;
+        dt[i] = s.softplus ? sp : raw;
+        y0[i] = (float)u[i];
+      }
+      if (last < K - 1) {
+#pragma unroll
+        for (int i = 0; i < KQ; ++i) {
+          const bool in = 4 * i + q <= last;
+          dt[i] = in ? dt[i] : 0.0f;
+          y0[i] = in ? y0[i] : 0.0f;
         }
       }
-      if (t0 + K < p.te) {
+      wave_sync();  // the tile before has read its rows
+#pragma unroll
+      for (int i = 0; i < KQ; ++i) {
+        x[i] = dt[i] * y0[i];
+        StepsLds::put(ldt, p.c, q, i, dt[i]);
+        StepsLds::put(lx, p.c, q, i, x[i]);
+        y0[i] *= skip;
+        gt[i] = 1.0f;
+        if constexpr (GATE && !PART) {
+          const float zf = (float)z[i];
+          gt[i] = zf * sigmoid_hw(zf);
+        }
+      }
+      wave_sync();
+      if (more) {
         wu.advance(K);
         wd.advance(K);
         if constexpr (GATE) wz.advance(K);
         bc.advance(K);
         fetch(last - K);
+        bc.load(last - K);
       }
-      if constexpr (!PART) {
-        if (ck) {
-          if (p.active) store_vec<NL>(ck, h);
-          ck += ck_step;
-        }
-      }
+      const float *lb = lds_bc[buf], *lc = lb + K * NP;
+
+      if constexpr (!PART)
+        if (ck && p.active) store_rows<M>(ck, h, q);
       float yo[KQ];
 #pragma unroll
       for (int i = 0; i < KQ; ++i) {
-        float nb[4][NL], nc[4][NL];
-        if (i + 1 < KQ) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            load_vec<NL>(nb[j], lb + (4 * i + 4 + j) * NP);
-            if constexpr (!PART) load_vec<NL>(nc[j], lc + (4 * i + 4 + j) * NP);
-          }
-        }
         float acc[4];
-        auto step = [&](auto jc) {
-          constexpr int j = decltype(jc)::value;
-          const float dj = quad_get<j>(dt[i]), xj = quad_get<j>(x[i]);
-          float y = 0.0f;
+        const f32x4 d4 = StepsLds::get(ldt, p.c, i), x4 = StepsLds::get(lx, p.c, i);
+        if constexpr (PART) dtsum += (d4[0] + d4[1]) + (d4[2] + d4[3]);
 #pragma unroll
-          for (int k = 0; k < NL; ++k) {
-            h[k] = fmaf(exp2_hw(dj * a2[k]), h[k], xj * bb[j][k]);
-            if constexpr (!PART) y = k ? fmaf(cc[j][k], h[k], y) : cc[j][k] * h[k];
+        for (int j = 0; j < 4; ++j) {
+          f32x4 y4 = 0.0f, b4[M], c4[M];
+          load_rows<M>(b4, lb + (4 * i + j) * NP, q);
+          if constexpr (!PART) load_rows<M>(c4, lc + (4 * i + j) * NP, q);
+#pragma unroll
+          for (int m = 0; m < M; ++m) {
+            h[m] = fma_4(exp2_4(d4[j] * a2[m]), h[m], x4[j] * b4[m]);
+            if constexpr (!PART) y4 = m ? fma_4(c4[m], h[m], y4) : c4[m] * h[m];
           }
-          acc[j] = y;
-        };
-        step(std::integral_constant<int, 0>());
-        step(std::integral_constant<int, 1>());
-        step(std::integral_constant<int, 2>());
-        step(std::integral_constant<int, 3>());
-        if constexpr (!PART)
-          yo[i] = (y0[i] + quad_reduce4(acc[0], acc[1], acc[2], acc[3], q)) * gt[i];
-        if (i + 1 < KQ) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int k = 0; k < NL; ++k) {
-              bb[j][k] = nb[j][k];
-              if constexpr (!PART) cc[j][k] = nc[j][k];
-            }
+          acc[j] = (y4[0] + y4[1]) + (y4[2] + y4[3]);
         }
+        if constexpr (!PART) yo[i] = (y0[i] + rows_reduce4(acc)) * gt[i];
       }
       if constexpr (!PART) {
         if (p.active) {
@@ -154,50 +134,49 @@ __global__ __launch_bounds__(kScanThreads, 2) void scan_fwd(const ScanArgs<E> s)
             if (4 * i + q <= last) *wo.at(4 * i) = (E)yo[i];
         }
         wo.advance(K);
+        if (ck) ck += ck_step;
       }
+      if (more) bc.store(lds_bc[buf ^ 1]);
+      __syncthreads();
     }
   }
   if constexpr (PART) {
-    dtsum = quad_sum(dtsum);
     if (p.active) {
-      store_vec<NL>(s.edge + edge, h);
+      store_rows<M>(edge, h, q);
       if (q == 0) s.dtsum[(int64_t)p.chunk * s.B * s.D + row] = dtsum;
     }
   } else {
     zero_steps(s.out, p);
     // the chunk in which the text ends has the final state
     if (s.state && p.active && p.chunk == min(p.len / s.chunk_steps, s.chunks - 1))
-      store_state<NL>(h, s.state, row, q, s.N);
+      store_states<M>(h, s.state, row, q, s.N);
   }
 }
 
-template <typename E, int NL>
+template <typename E, int M>
 void launch(const ScanDims& d, const ScanArgs<E>& a, hipStream_t stream) {
-  const unsigned wgs = (unsigned)(d.P * d.G * d.B);
+  const unsigned wgs = (unsigned)(d.P * d.G * d.B), grid = wgs * (unsigned)d.chunks;
   if (d.chunks > 1) {
-    scan_fwd<E, NL, false, true>
-        <<<wgs * (unsigned)(d.chunks - 1), kScanThreads, 0, stream>>>(a);
+    // (nothing follows the last chunk)
+    scan_fwd<E, M, false, true><<<grid - wgs, kScanThreads, 0, stream>>>(a);
     const int64_t n = d.B * d.D * d.NP;
     scan_join<true><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
         a.edge, a.dtsum, a.a, a.state0, d.B * d.D, a.D, a.N, d.NP, a.chunks);
   }
-  const unsigned grid = wgs * (unsigned)d.chunks;
   if (a.z.p)
-    scan_fwd<E, NL, true, false><<<grid, kScanThreads, 0, stream>>>(a);
+    scan_fwd<E, M, true, false><<<grid, kScanThreads, 0, stream>>>(a);
   else
-    scan_fwd<E, NL, false, false><<<grid, kScanThreads, 0, stream>>>(a);
+    scan_fwd<E, M, false, false><<<grid, kScanThreads, 0, stream>>>(a);
 }
 
 }  // namespace
 
 template <typename E>
 void scan_launch_forward(const ScanDims& d, const ScanArgs<E>& a, hipStream_t stream) {
-  switch (d.NL) {
+  switch (d.M) {
     case 1: return launch<E, 1>(d, a, stream);
     case 2: return launch<E, 2>(d, a, stream);
-    case 4: return launch<E, 4>(d, a, stream);
-    case 8: return launch<E, 8>(d, a, stream);
-    default: return launch<E, 16>(d, a, stream);
+    default: return launch<E, 4>(d, a, stream);
   }
 }
 template void scan_launch_forward<float>(const ScanDims&, const ScanArgs<float>&, hipStream_t);

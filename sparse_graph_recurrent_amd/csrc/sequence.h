@@ -155,14 +155,18 @@ __device__ __forceinline__ float sigmoid_hw(float x) {
   return rcp_hw(1.0f + exp2_hw(-kLog2e * x));
 }
 
-// log(1 + exp(x)) = max(x, 0) + log1p(exp(-|x|)).  The part of e that the sum
-// w = 1 + e rounds away is added back to first order, so the result keeps its
-// relative accuracy down to exp(x) itself for very negative x.
-__device__ __forceinline__ float softplus_hw(float x) {
+// log(1 + exp(x)) = max(x, 0) + log1p(e), e = exp(-|x|), and its derivative
+// 1 / (1 + exp(-x)).  The part of e that the sum w = 1 + e rounds away is added
+// back to first order, so both keep their relative accuracy down to exp(x)
+// itself for very negative x.
+struct Softplus {
+  float value, slope;
+};
+__device__ __forceinline__ Softplus softplus_hw(float x) {
   const float e = exp2_hw(-kLog2e * fabsf(x));
-  const float w = 1.0f + e;
-  const float l = fmaf(kLn2, __builtin_amdgcn_logf(w), (e - (w - 1.0f)) * rcp_hw(w));
-  return fmaxf(x, 0.0f) + l;
+  const float w = 1.0f + e, r = rcp_hw(w);
+  const float l = fmaf(kLn2, __builtin_amdgcn_logf(w), (e - (w - 1.0f)) * r);
+  return Softplus{fmaxf(x, 0.0f) + l, x < 0.0f ? e * r : r};
 }
 
 template <int CTRL>
@@ -170,24 +174,10 @@ __device__ __forceinline__ float dpp(float x) {
   return __builtin_bit_cast(
       float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
 }
-// value of lane J of the caller's quad (lanes 4k .. 4k + 3)
-template <int J>
-__device__ __forceinline__ float quad_get(float x) {
-  return dpp<J * 0x55>(x);
-}
 __device__ __forceinline__ float quad_xor1(float x) { return dpp<0xB1>(x); }
 __device__ __forceinline__ float quad_xor2(float x) { return dpp<0x4E>(x); }
 __device__ __forceinline__ float quad_sum(float x) {
   x += quad_xor1(x);
   return x + quad_xor2(x);
 }
-// Lane q of each quad gets the quad's sum of v_q: a reduce-scatter, 3 adds
-// where four butterflies would take 8.
-__device__ __forceinline__ float quad_reduce4(float v0, float v1, float v2, float v3, int q) {
-  const bool hi = q & 2, odd = q & 1;
-  const float r0 = (hi ? v2 : v0) + quad_xor2(hi ? v0 : v2);
-  const float r1 = (hi ? v3 : v1) + quad_xor2(hi ? v1 : v3);
-  return (odd ? r1 : r0) + quad_xor1(odd ? r0 : r1);
-}
-
 }  // namespace ckhip
