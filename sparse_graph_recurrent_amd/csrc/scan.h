@@ -293,15 +293,22 @@ __global__ __launch_bounds__(256) void scan_join(float* edge, const float* dtsum
   const int64_t row = i / NP;
   const float a2 = n < N ? kLog2e * A[row % D * N + n] : 0.0f;
   float cur = first && n < N ? first[row * N + n] : 0.0f;
-#pragma unroll 8
-  for (int k = 0; k < chunks; ++k) {
-    const int c = FORWARD ? k : chunks - 1 - k;
-    const int64_t at = (int64_t)c * rows;
-    // the chunk that no other follows has no summary
-    const bool more = k + 1 < chunks;
-    const float made = more ? edge[at * NP + i] : 0.0f, dt = more ? dtsum[at + row] : 0.0f;
-    edge[at * NP + i] = cur;
-    cur = fmaf(exp2_hw(a2 * dt), cur, made);
+  // in the order of the walk; the chunk that no other follows has no summary
+  auto at = [&](int k) { return (int64_t)(FORWARD ? k : chunks - 1 - k) * rows; };
+  for (int k0 = 0; k0 < chunks; k0 += 8) {
+    float made[8], dt[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t from = at(min(k0 + j, max(chunks - 2, 0)));
+      made[j] = edge[from * NP + i];
+      dt[j] = dtsum[from + row];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (k0 + j < chunks) {
+        edge[at(k0 + j) * NP + i] = cur;
+        cur = fmaf(exp2_hw(a2 * dt[j]), cur, made[j]);
+      }
   }
 }
 

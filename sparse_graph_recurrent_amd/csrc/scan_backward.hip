@@ -399,39 +399,36 @@ __global__ __launch_bounds__(kScanThreads, M < 4 ? 2 : 1) void scan_bwd(const Sc
 
 // Gradients of B and C: the workgroups' partial sums of a group, in order.
 template <typename E>
-__global__ __launch_bounds__(256) void scan_sum_bc(const float* part, int T, int B, int G, int N,
-                                                   int NP, int P, const int32_t* lengths,
-                                                   Seq<E> gb, Seq<E> gc) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t rows = (int64_t)T * B * G, stride = rows * 2 * NP;
+__device__ __forceinline__ void sum_bc(const ScanArgs<E>& s, int NP, int64_t i) {
+  const int64_t stride = (int64_t)s.T * s.B * s.G * 2 * NP;
   if (i >= stride) return;
   const int e = (int)(i % (2 * NP)), kind = e / NP, n = e % NP;
   int64_t r = i / (2 * NP);
-  const int g = (int)(r % G);
-  r /= G;
-  const int b = (int)(r % B), t = (int)(r / B);
-  if (n >= N) return;
+  const int g = (int)(r % s.G);
+  r /= s.G;
+  const int b = (int)(r % s.B), t = (int)(r / s.B);
+  if (n >= s.N) return;
   float sum = 0.0f;
-  if (!lengths || t < lengths[b]) {
+  if (!s.lengths || t < s.lengths[b]) {
 #pragma unroll 8
-    for (int k = 0; k < P; ++k) sum += part[k * stride + i];
+    for (int k = 0; k < s.P; ++k) sum += s.part_bc[k * stride + i];
   }
-  (kind ? gc : gb).row(t, b)[(int64_t)g * N + n] = (E)sum;
+  (kind ? s.gc : s.gb).row(t, b)[(int64_t)g * s.N + n] = (E)sum;
 }
 
 // Gradients of A, D and the bias: the sums of all rows and chunks in a fixed
 // order.  A workgroup takes 32 sums, eight threads each one a stretch of them.
-__global__ __launch_bounds__(256) void scan_sum_a(const float* part, int64_t D, int N, int NP,
-                                                  int64_t rows, float* ga, float* gd,
-                                                  float* gbias) {
+template <typename E>
+__device__ __forceinline__ void sum_a(const ScanArgs<E>& s, int NP, int64_t first) {
   __shared__ float red[8][32];
-  const int64_t all = D * (NP + 2), i = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
+  const int64_t all = (int64_t)s.D * (NP + 2), i = first + (threadIdx.x & 31);
   const int y = threadIdx.x >> 5;
+  const int64_t rows = (int64_t)s.chunks * s.B;
   const int64_t each = (rows + 7) / 8, r0 = each * y, r1 = min(r0 + each, rows);
   float sum = 0.0f;
   if (i < all) {
 #pragma unroll 4
-    for (int64_t r = r0; r < r1; ++r) sum += part[r * all + i];
+    for (int64_t r = r0; r < r1; ++r) sum += s.part_a[r * all + i];
   }
   red[y][threadIdx.x & 31] = sum;
   __syncthreads();
@@ -440,12 +437,21 @@ __global__ __launch_bounds__(256) void scan_sum_a(const float* part, int64_t D, 
   for (int j = 0; j < 8; ++j) sum += red[j][threadIdx.x];
   const int n = (int)(i % (NP + 2));
   const int64_t d = i / (NP + 2);
-  if (n < N)
-    ga[d * N + n] = sum;
-  else if (n == NP && gd)
-    gd[d] = sum;
-  else if (n == NP + 1 && gbias)
-    gbias[d] = sum;
+  if (n < s.N)
+    s.ga[d * s.N + n] = sum;
+  else if (n == NP && s.gd)
+    s.gd[d] = sum;
+  else if (n == NP + 1 && s.gbias)
+    s.gbias[d] = sum;
+}
+
+// The last launch: both kinds of sums, the first a_wgs workgroups those of A.
+template <typename E>
+__global__ __launch_bounds__(256) void scan_sums(const ScanArgs<E> s, int NP, unsigned a_wgs) {
+  if (blockIdx.x < a_wgs)
+    sum_a(s, NP, (int64_t)blockIdx.x * 32);
+  else
+    sum_bc(s, NP, (int64_t)(blockIdx.x - a_wgs) * 256 + threadIdx.x);
 }
 
 template <typename E, int M>
@@ -465,11 +471,8 @@ void launch(const ScanDims& d, const ScanArgs<E>& a, hipStream_t stream) {
   else
     scan_bwd<E, M, false><<<grid, kScanThreads, 0, stream>>>(a);
   const int64_t bc = d.T * d.B * d.G * 2 * d.NP, ae = d.D * (d.NP + 2);
-  if (bc > 0)
-    scan_sum_bc<E><<<(unsigned)((bc + 255) / 256), 256, 0, stream>>>(
-        a.part_bc, a.T, a.B, a.G, a.N, d.NP, a.P, a.lengths, a.gb, a.gc);
-  scan_sum_a<<<(unsigned)((ae + 31) / 32), 256, 0, stream>>>(
-      a.part_a, d.D, a.N, d.NP, d.chunks * d.B, a.ga, a.gd, a.gbias);
+  const unsigned a_wgs = (unsigned)((ae + 31) / 32);
+  scan_sums<E><<<a_wgs + (unsigned)((bc + 255) / 256), 256, 0, stream>>>(a, d.NP, a_wgs);
 }
 
 }  // namespace

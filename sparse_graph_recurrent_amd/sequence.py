@@ -19,12 +19,13 @@ and ``*_step`` take one token per row, from and to the carried states.
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _byte_buffer, _check, _dev, _ptr, lib
+from . import _check, lib
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
@@ -111,14 +112,13 @@ class _Struct:
         return ctypes.byref(v)
 
 
-def _call(fn, like: torch.Tensor, stream, args, made=()):
-    """Runs one entry point with like's device current on `stream` (None: the
+def _call(fn, dev: int, stream, args, made=()):
+    """Runs one entry point with device `dev` current on `stream` (None: the
     current one); memory of the tensors in `made`, allocated here for another
     stream than the current, is kept from reuse until that stream is done."""
-    dev = like.device.index
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _call(fn, like, stream, args, made)
+            return _call(fn, dev, stream, args, made)
     if stream is None:
         _check(fn(*args, torch._C._cuda_getCurrentRawStream(dev)))
         return
@@ -138,41 +138,51 @@ def _adjacent(t: torch.Tensor, last: int) -> bool:
     return True
 
 
-def _seq(t: torch.Tensor, name: str, like: torch.Tensor, shape, last: int = 1):
-    """(address, stride_t, stride_b) of a [T, B, ...] tensor (a step's [B, ...]
-    tensor counts as T = 1), checked."""
+def _refuse(t, name: str, dtype, dev: int, shape):
+    """Raises the error that `t` not being a tensor of this type, device and shape calls for."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-    if t.numel() == 0:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _fits(t, dtype, dev: int, shape) -> bool:
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev \
+        and t.shape == shape
+
+
+def _seq(t, name: str, dtype, dev: int, shape, last: int = 1):
+    """(address, stride_t, stride_b) of a [T, B, ...] tensor (a step's [B, ...]
+    tensor counts as T = 1), checked."""
+    if not _fits(t, dtype, dev, shape):
+        _refuse(t, name, dtype, dev, shape)
+    if 0 in shape:
         return _NONE
     st = t.stride()
-    if last == 1 and st[-1] != 1 or last == 2 and (st[-1] != 1 or st[-2] != shape[-1]):
-        if not _adjacent(t, last):  # sizes of 1 may have any stride
+    if st[-1] != 1 or last == 2 and st[-2] != shape[-1]:
+        if not _adjacent(t, last):  # (sizes of 1 may have any stride)
             raise ValueError(f"{name} must have its last {last} dimension(s) contiguous")
     if len(shape) - last == 1:
         return t.data_ptr(), 0, st[0] if shape[0] > 1 else 0
     return t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0
 
 
-def _par(t, name: str, like: torch.Tensor, shape, dtype=torch.float32) -> int:
+def _par(t, name: str, dev: int, shape, dtype=torch.float32) -> int:
     """Address of an optional contiguous parameter, state or length vector."""
     if t is None:
         return 0
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        _dev(t, name, dtype, shape)
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-    return t.data_ptr() if t.numel() else 0
+    if not _fits(t, dtype, dev, shape) or not t.is_contiguous():
+        _refuse(t, name, dtype, dev, shape)
+    return 0 if 0 in shape else t.data_ptr()
 
 
 def _first(t, name: str, dims) -> int:
-    """Checks the tensor that gives a call its type, device and sizes; its ck_dtype."""
+    """Checks the tensor that gives a call its type, device and sizes; its device."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.dtype not in _DTYPES:
@@ -180,35 +190,51 @@ def _first(t, name: str, dims) -> int:
     if t.dim() not in dims:
         raise ValueError(f"{name} must have {' or '.join(map(str, dims))} dimensions, "
                          f"got {t.dim()}")
-    return _DTYPES[t.dtype]
+    return t.get_device()
 
 
-def _into(t, like: torch.Tensor, shape, dtype=None):
-    """(tensor, was made here) of an output: the caller's, or a new one."""
+def _out_seq(t, name: str, like: torch.Tensor, shape, last: int = 1):
+    """(tensor, its ck_seq fields, made here) of an output: the caller's, checked,
+    or a new contiguous one."""
     if t is not None:
-        return t, False
-    return torch.empty(shape, dtype=dtype or like.dtype, device=like.device), True
+        return t, _seq(t, name, like.dtype, like.get_device(), shape, last), False
+    t = like.new_empty(shape)
+    if 0 in shape:
+        return t, _NONE, True
+    st = t.stride()
+    if len(shape) - last == 1:
+        return t, (t.data_ptr(), 0, st[0]), True
+    return t, (t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0), True
+
+
+def _out_par(t, name: str, like: torch.Tensor, shape, dtype=torch.float32):
+    """(tensor, its address, made here) of a contiguous output."""
+    if t is not None:
+        return t, _par(t, name, like.get_device(), shape, dtype), False
+    t = like.new_empty(shape, dtype=dtype)
+    return t, 0 if 0 in shape else t.data_ptr(), True
 
 
 def _buffer(buf, nbytes: int, like: torch.Tensor, name: str):
-    """A byte buffer of the caller's (checked) or a new one; None for 0 bytes."""
+    """(byte buffer, its address, its size, made here): the caller's, checked, or a
+    new one; none for 0 bytes."""
     if buf is None:
-        return _byte_buffer(nbytes, like.device) if nbytes else None
-    if buf.device != like.device or buf.numel() * buf.element_size() < nbytes:
-        raise ValueError(f"{name} buffer too small or on another device")
-    return buf
-
-
-def _bytes(buf) -> int:
-    return 0 if buf is None else buf.numel() * buf.element_size()
+        if not nbytes:
+            return None, None, 0, False
+        buf = like.new_empty((nbytes,), dtype=torch.uint8)
+        return buf, buf.data_ptr(), nbytes, True
+    size = buf.numel() * buf.element_size()
+    if buf.get_device() != like.get_device() or size < nbytes or not buf.is_contiguous():
+        raise ValueError(f"{name} buffer too small, not contiguous or on another device")
+    return buf, buf.data_ptr() if size else None, size, False
 
 
 # ------------------------------------------------------------ selective scan
 
 def _scan_call(u, delta, A, B, C, D, z, delta_bias, state0, lengths, delta_softplus, step=False):
-    """(shape, inputs, sizes (T, B, D, N, G)) of a scan call, checked."""
-    dtype = _first(u, "u", (2,) if step else (3,))
-    us = u.shape
+    """(shape, inputs, device, sizes (T, B, D, N, G)) of a scan call, checked."""
+    dev = _first(u, "u", (2,) if step else (3,))
+    us, dt = u.shape, u.dtype
     if not isinstance(A, torch.Tensor) or A.dim() != 2:
         raise ValueError("A must be a [channels, states] tensor")
     if not isinstance(B, torch.Tensor) or B.dim() != len(us) + 1:
@@ -217,15 +243,17 @@ def _scan_call(u, delta, A, B, C, D, z, delta_bias, state0, lengths, delta_softp
     N, G = A.shape[1], B.shape[-2]
     bs = us[:-1] + (G, N)
     sizes = (T, rows, ch, N, G)
-    return _SCAN_SHAPE.pack(*sizes, dtype, 1 if delta_softplus else 0), _SCAN_INPUTS.pack(
-        *_seq(u, "u", u, us), *_seq(delta, "delta", u, us), *_seq(B, "B", u, bs, 2),
-        *_seq(C, "C", u, bs, 2), *(_NONE if z is None else _seq(z, "z", u, us)),
-        _par(A, "A", u, (ch, N)), _par(D, "D", u, (ch,)),
-        _par(delta_bias, "delta_bias", u, (ch,)), _par(state0, "state0", u, (rows, ch, N)),
-        _par(lengths, "lengths", u, (rows,), torch.int32)), sizes
+    return _SCAN_SHAPE.pack(*sizes, _DTYPES[dt], 1 if delta_softplus else 0), _SCAN_INPUTS.pack(
+        *_seq(u, "u", dt, dev, us), *_seq(delta, "delta", dt, dev, us),
+        *_seq(B, "B", dt, dev, bs, 2), *_seq(C, "C", dt, dev, bs, 2),
+        *(_NONE if z is None else _seq(z, "z", dt, dev, us)),
+        _par(A, "A", dev, (ch, N)), _par(D, "D", dev, (ch,)),
+        _par(delta_bias, "delta_bias", dev, (ch,)), _par(state0, "state0", dev, (rows, ch, N)),
+        _par(lengths, "lengths", dev, (rows,), torch.int32)), dev, sizes
 
 
-def _scan_sizes(shape):
+@functools.lru_cache(maxsize=256)
+def _scan_sizes(shape: bytes):
     s, f, b = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t()
     _check(lib().ck_scan_sizes(shape, ctypes.byref(s), ctypes.byref(f), ctypes.byref(b)))
     return s.value, f.value, b.value
@@ -233,7 +261,7 @@ def _scan_sizes(shape):
 
 def selective_scan_sizes(T: int, B: int, D: int, N: int, G: int = 1, dtype=torch.float32):
     """(saved_bytes, forward_bytes, backward_bytes) of ``ck_scan_sizes``."""
-    return _scan_sizes(ScanShape(int(T), int(B), int(D), int(N), int(G), _DTYPES[dtype], 0))
+    return _scan_sizes(_SCAN_SHAPE.pack(T, B, D, N, G, _DTYPES[dtype], 0))
 
 
 def selective_scan_forward(u, delta, A, B, C, D=None, z=None, delta_bias=None, state0=None,
@@ -244,18 +272,15 @@ def selective_scan_forward(u, delta, A, B, C, D=None, z=None, delta_bias=None, s
     u, delta, z: [T, B, D]; B, C: [T, B, G, N]; A: [D, N]; D, delta_bias: [D];
     state0 and the returned state: [B, D, N].  ``saved`` is what
     ``selective_scan_backward`` needs (None with save=False)."""
-    shape, inputs, (T, rows, ch, N, _) = _scan_call(u, delta, A, B, C, D, z, delta_bias, state0,
-                                                    lengths, delta_softplus)
+    shape, inputs, dev, (T, rows, ch, N, _) = _scan_call(
+        u, delta, A, B, C, D, z, delta_bias, state0, lengths, delta_softplus)
     sb, fb, _ = _scan_sizes(shape)
-    out, m0 = _into(out, u, u.shape)
-    state, m1 = _into(state, u, (rows, ch, N), torch.float32)
-    m2, m3 = saved is None, workspace is None
-    saved = _buffer(saved, sb, u, "saved") if save or not m2 else None
-    workspace = _buffer(workspace, fb, u, "workspace")
-    _call(lib().ck_scan_forward, u, stream,
-          (shape, inputs, CkSeq(*_seq(out, "out", u, u.shape)),
-           _par(state, "state", u, (rows, ch, N)), _ptr(saved), _ptr(workspace),
-           _bytes(workspace)),
+    out, os, m0 = _out_seq(out, "out", u, u.shape)
+    state, st, m1 = _out_par(state, "state", u, (rows, ch, N))
+    saved, sp, _, m2 = _buffer(saved, sb, u, "saved") if save or saved is not None else \
+        (None, None, 0, False)
+    workspace, wp, wn, m3 = _buffer(workspace, fb, u, "workspace")
+    _call(lib().ck_scan_forward, dev, stream, (shape, inputs, CkSeq(*os), st, sp, wp, wn),
           (out if m0 else None, state if m1 else None, saved if m2 else None,
            workspace if m3 else None))
     return out, state, saved, workspace
@@ -267,38 +292,32 @@ def selective_scan_backward(u, delta, A, B, C, saved, grad_out, D=None, z=None, 
     """Run ``ck_scan_backward``; returns the gradients (overwritten) by the
     names g_u, g_delta, g_A, g_B, g_C, g_D, g_delta_bias, g_state0 and, with a
     gate, g_z."""
-    shape, inputs, (T, rows, ch, N, _) = _scan_call(u, delta, A, B, C, D, z, delta_bias, None,
-                                                    lengths, delta_softplus)
+    shape, inputs, dev, (T, rows, ch, N, _) = _scan_call(
+        u, delta, A, B, C, D, z, delta_bias, None, lengths, delta_softplus)
     sb, _, wb = _scan_sizes(shape)
     if sb and saved is None:
         raise ValueError("saved is missing")
-    saved = _buffer(saved, sb, u, "saved")
-    us, bs, state = u.shape, B.shape, (rows, ch, N)
-    go = CkSeq(*_seq(grad_out, "grad_out", u, us))
-    m0, m1 = grads is None, workspace is None
-    if m0:
-        e = dict(dtype=u.dtype, device=u.device)
-        f = dict(dtype=torch.float32, device=u.device)
-        grads = {"g_u": torch.empty(us, **e), "g_delta": torch.empty(us, **e),
-                 "g_A": torch.empty(A.shape, **f), "g_B": torch.empty(bs, **e),
-                 "g_C": torch.empty(bs, **e), "g_D": torch.empty(ch, **f),
-                 "g_delta_bias": torch.empty(ch, **f), "g_state0": torch.empty(state, **f)}
-        if z is not None:
-            grads["g_z"] = torch.empty(us, **e)
-    g = grads
-    out = _SCAN_GRADS.pack(
-        *_seq(g["g_u"], "g_u", u, us), *_seq(g["g_delta"], "g_delta", u, us),
-        *_seq(g["g_B"], "g_B", u, bs, 2), *_seq(g["g_C"], "g_C", u, bs, 2),
-        *(_NONE if z is None else _seq(g["g_z"], "g_z", u, us)),
-        _par(g["g_A"], "g_A", u, A.shape), _par(g.get("g_D"), "g_D", u, (ch,)),
-        _par(g.get("g_delta_bias"), "g_delta_bias", u, (ch,)),
-        _par(g.get("g_state0"), "g_state0", u, state))
-    workspace = _buffer(workspace, wb, u, "workspace")
-    _call(lib().ck_scan_backward, u, stream,
-          (shape, inputs, _ptr(saved), go, _par(grad_state, "grad_state", u, state), out,
-           _ptr(workspace), _bytes(workspace)),
-          (tuple(grads.values()) if m0 else ()) + ((workspace,) if m1 else ()))
-    return grads
+    _, sp, _, _ = _buffer(saved, sb, u, "saved")
+    us, bs, ss = u.shape, B.shape, (rows, ch, N)
+    go = CkSeq(*_seq(grad_out, "grad_out", u.dtype, dev, us))
+    gs = _par(grad_state, "grad_state", dev, ss)
+    made = grads is None
+    g = {} if made else grads
+    q = {}
+    for name, sh, last in (("g_u", us, 1), ("g_delta", us, 1), ("g_B", bs, 2), ("g_C", bs, 2)):
+        g[name], q[name], _ = _out_seq(None if made else grads[name], name, u, sh, last)
+    if z is not None:
+        g["g_z"], q["g_z"], _ = _out_seq(None if made else grads["g_z"], "g_z", u, us)
+    for name, sh in (("g_A", A.shape), ("g_D", (ch,)), ("g_delta_bias", (ch,)), ("g_state0", ss)):
+        if made or grads.get(name) is not None:
+            g[name], q[name], _ = _out_par(None if made else grads[name], name, u, sh)
+    out = _SCAN_GRADS.pack(*q["g_u"], *q["g_delta"], *q["g_B"], *q["g_C"], *q.get("g_z", _NONE),
+                           q.get("g_A", 0), q.get("g_D", 0), q.get("g_delta_bias", 0),
+                           q.get("g_state0", 0))
+    workspace, wp, wn, m1 = _buffer(workspace, wb, u, "workspace")
+    _call(lib().ck_scan_backward, dev, stream, (shape, inputs, sp, go, gs, out, wp, wn),
+          (tuple(g.values()) if made else ()) + ((workspace,) if m1 else ()))
+    return g
 
 
 def selective_scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=None,
@@ -308,13 +327,13 @@ def selective_scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=Non
     given.  Returns (out [B, D], the new state)."""
     if state is None:
         raise ValueError("state is missing")
-    shape, inputs, (_, rows, ch, N, _) = _scan_call(u, delta, A, B, C, D, z, delta_bias, state,
-                                                    None, delta_softplus, step=True)
+    shape, inputs, dev, (_, rows, ch, N, _) = _scan_call(
+        u, delta, A, B, C, D, z, delta_bias, state, None, delta_softplus, step=True)
     new_state = state if new_state is None else new_state
-    out, made = _into(out, u, u.shape)
-    _call(lib().ck_scan_step, u, stream,
-          (shape, inputs, CkSeq(*_seq(out, "out", u, u.shape)),
-           _par(new_state, "new_state", u, (rows, ch, N))), (out,) if made else ())
+    out, os, made = _out_seq(out, "out", u, u.shape)
+    _call(lib().ck_scan_step, dev, stream,
+          (shape, inputs, CkSeq(*os), _par(new_state, "new_state", dev, (rows, ch, N))),
+          (out,) if made else ())
     return out, new_state
 
 
@@ -369,17 +388,24 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, state0=No
 # --------------------------------------------------------- short convolution
 
 def _conv_call(x, weight, bias, activation, step=False):
-    """(shape, state shape, x's ck_seq, weight, bias) of a convolution call, checked."""
-    dtype = _first(x, "x", (2,) if step else (3,))
+    """(shape, device, state shape, x's ck_seq, weight, bias) of a convolution call, checked."""
+    dev = _first(x, "x", (2,) if step else (3,))
     if activation is not None and activation != "silu":
         raise ValueError(f"activation must be None or 'silu', got {activation!r}")
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be a [channels, taps] tensor")
     T, rows, ch = (1,) + x.shape if step else x.shape
     W = weight.shape[1]
-    return (_CONV_SHAPE.pack(T, rows, ch, W, dtype, 1 if activation else 0), (W - 1, rows, ch),
-            CkSeq(*_seq(x, "x", x, x.shape)), _par(weight, "weight", x, (ch, W)),
-            _par(bias, "bias", x, (ch,)))
+    return (_CONV_SHAPE.pack(T, rows, ch, W, _DTYPES[x.dtype], 1 if activation else 0), dev,
+            (W - 1, rows, ch), CkSeq(*_seq(x, "x", x.dtype, dev, x.shape)),
+            _par(weight, "weight", dev, (ch, W)), _par(bias, "bias", dev, (ch,)))
+
+
+@functools.lru_cache(maxsize=256)
+def _conv_sizes(shape: bytes) -> int:
+    need = ctypes.c_size_t()
+    _check(lib().ck_conv_sizes(shape, ctypes.byref(need)))
+    return need.value
 
 
 def short_conv_forward(x, weight, bias=None, state0=None, lengths=None, activation=None, y=None,
@@ -387,13 +413,13 @@ def short_conv_forward(x, weight, bias=None, state0=None, lengths=None, activati
     """Run ``ck_conv_forward``; returns (y, state).  x: [T, B, D]; weight:
     [D, W]; bias: [D]; state0 and the returned state: [W - 1, B, D], the last
     inputs of each row; activation: None or "silu"."""
-    shape, ss, xs, w, b = _conv_call(x, weight, bias, activation)
-    y, m0 = _into(y, x, x.shape)
-    state, m1 = _into(state, x, ss)
-    _call(lib().ck_conv_forward, x, stream,
-          (shape, xs, w, b, _par(state0, "state0", x, ss, x.dtype),
-           _par(lengths, "lengths", x, (ss[1],), torch.int32), CkSeq(*_seq(y, "y", x, x.shape)),
-           _par(state, "state", x, ss, x.dtype)), (y if m0 else None, state if m1 else None))
+    shape, dev, ss, xs, w, b = _conv_call(x, weight, bias, activation)
+    y, ys, m0 = _out_seq(y, "y", x, x.shape)
+    state, st, m1 = _out_par(state, "state", x, ss, x.dtype)
+    _call(lib().ck_conv_forward, dev, stream,
+          (shape, xs, w, b, _par(state0, "state0", dev, ss, x.dtype),
+           _par(lengths, "lengths", dev, (ss[1],), torch.int32), CkSeq(*ys), st),
+          (y if m0 else None, state if m1 else None))
     return y, state
 
 
@@ -401,28 +427,25 @@ def short_conv_backward(x, weight, grad_y, bias=None, state0=None, lengths=None,
                         grad_state=None, grads=None, workspace=None, stream=None) -> dict:
     """Run ``ck_conv_backward``; returns the gradients (overwritten) g_x,
     g_weight, g_bias and g_state0."""
-    shape, ss, xs, w, b = _conv_call(x, weight, bias, activation)
-    need = ctypes.c_size_t()
-    _check(lib().ck_conv_sizes(shape, ctypes.byref(need)))
-    m0, m1 = grads is None, workspace is None
-    if m0:
-        f = dict(dtype=torch.float32, device=x.device)
-        grads = {"g_x": torch.empty(x.shape, dtype=x.dtype, device=x.device),
-                 "g_weight": torch.empty(weight.shape, **f), "g_bias": torch.empty(ss[2], **f),
-                 "g_state0": torch.empty(ss, dtype=x.dtype, device=x.device)}
-    workspace = _buffer(workspace, need.value, x, "workspace")
-    _call(lib().ck_conv_backward, x, stream,
-          (shape, xs, w, b, _par(state0, "state0", x, ss, x.dtype),
-           _par(lengths, "lengths", x, (ss[1],), torch.int32),
-           CkSeq(*_seq(grad_y, "grad_y", x, x.shape)),
-           _par(grad_state, "grad_state", x, ss, x.dtype),
-           CkSeq(*_seq(grads["g_x"], "g_x", x, x.shape)),
-           _par(grads["g_weight"], "g_weight", x, weight.shape),
-           _par(grads.get("g_bias"), "g_bias", x, (ss[2],)),
-           _par(grads.get("g_state0"), "g_state0", x, ss, x.dtype), _ptr(workspace),
-           _bytes(workspace)),
-          (tuple(grads.values()) if m0 else ()) + ((workspace,) if m1 else ()))
-    return grads
+    shape, dev, ss, xs, w, b = _conv_call(x, weight, bias, activation)
+    made = grads is None
+    g = {} if made else grads
+    have = (lambda name: None) if made else grads.get
+    g["g_x"], gx, _ = _out_seq(have("g_x"), "g_x", x, x.shape)
+    g["g_weight"], gw, _ = _out_par(have("g_weight"), "g_weight", x, weight.shape)
+    gb = gs0 = 0
+    if made or grads.get("g_bias") is not None:
+        g["g_bias"], gb, _ = _out_par(have("g_bias"), "g_bias", x, (ss[2],))
+    if made or grads.get("g_state0") is not None:
+        g["g_state0"], gs0, _ = _out_par(have("g_state0"), "g_state0", x, ss, x.dtype)
+    workspace, wp, wn, m1 = _buffer(workspace, _conv_sizes(shape), x, "workspace")
+    _call(lib().ck_conv_backward, dev, stream,
+          (shape, xs, w, b, _par(state0, "state0", dev, ss, x.dtype),
+           _par(lengths, "lengths", dev, (ss[1],), torch.int32),
+           CkSeq(*_seq(grad_y, "grad_y", x.dtype, dev, x.shape)),
+           _par(grad_state, "grad_state", dev, ss, x.dtype), CkSeq(*gx), gw, gb, gs0, wp, wn),
+          (tuple(g.values()) if made else ()) + ((workspace,) if m1 else ()))
+    return g
 
 
 def short_conv_step(state, x, weight, bias=None, activation=None, y=None, new_state=None,
@@ -430,13 +453,12 @@ def short_conv_step(state, x, weight, bias=None, activation=None, y=None, new_st
     """Run ``ck_conv_step``: one token per row.  x: [B, D]; state: [W - 1, B,
     D], updated in place unless ``new_state`` is given.  Returns (y [B, D],
     the new state)."""
-    shape, ss, xs, w, b = _conv_call(x, weight, bias, activation, step=True)
+    shape, dev, ss, xs, w, b = _conv_call(x, weight, bias, activation, step=True)
     new_state = state if new_state is None else new_state
-    y, made = _into(y, x, x.shape)
-    _call(lib().ck_conv_step, x, stream,
-          (shape, xs, w, b, _par(state, "state", x, ss, x.dtype),
-           CkSeq(*_seq(y, "y", x, x.shape)), _par(new_state, "new_state", x, ss, x.dtype)),
-          (y,) if made else ())
+    y, ys, made = _out_seq(y, "y", x, x.shape)
+    _call(lib().ck_conv_step, dev, stream,
+          (shape, xs, w, b, _par(state, "state", dev, ss, x.dtype), CkSeq(*ys),
+           _par(new_state, "new_state", dev, ss, x.dtype)), (y,) if made else ())
     return y, new_state
 
 
@@ -470,13 +492,13 @@ def short_conv(x, weight, bias=None, state0=None, lengths=None, activation=None)
 # ------------------------------------------------------------------- dropout
 
 def _drop_call(x, name, p, seed, offset, held, counter):
-    """(shape, x's ck_seq) of a dropout call, checked."""
-    dtype = _first(x, name, (2, 3))
+    """(shape, device, x's ck_seq) of a dropout call, checked."""
+    dev = _first(x, name, (2, 3))
     T, rows, ch = (1,) + x.shape if x.dim() == 2 else x.shape
     m = 0xFFFFFFFFFFFFFFFF
-    return _DROP_SHAPE.pack(T, rows, ch, dtype, 1 if held else 0, p, seed & m, offset & m,
-                            _par(counter, "counter", x, (1,), torch.int64)), \
-        CkSeq(*_seq(x, name, x, x.shape))
+    return _DROP_SHAPE.pack(T, rows, ch, _DTYPES[x.dtype], 1 if held else 0, p, seed & m,
+                            offset & m, _par(counter, "counter", dev, (1,), torch.int64)), dev, \
+        CkSeq(*_seq(x, name, x.dtype, dev, x.shape))
 
 
 def dropout_forward(x, p: float, seed: int, offset: int = 0, residual=None, held: bool = False,
@@ -487,22 +509,20 @@ def dropout_forward(x, p: float, seed: int, offset: int = 0, residual=None, held
     window the same mask.  A device ``counter`` (int64 [1]) is added to the
     offset, so that a replayed graph can draw new masks.  ``out`` may be x or
     the residual."""
-    shape, xs = _drop_call(x, "x", p, seed, offset, held, counter)
-    out, made = _into(out, x, x.shape)
-    _call(lib().ck_dropout_forward, x, stream,
-          (shape, xs, CkSeq(*(_NONE if residual is None else
-                              _seq(residual, "residual", x, x.shape))),
-           CkSeq(*_seq(out, "out", x, x.shape))), (out,) if made else ())
+    shape, dev, xs = _drop_call(x, "x", p, seed, offset, held, counter)
+    rs = _NONE if residual is None else _seq(residual, "residual", x.dtype, dev, x.shape)
+    out, os, made = _out_seq(out, "out", x, x.shape)
+    _call(lib().ck_dropout_forward, dev, stream, (shape, xs, CkSeq(*rs), CkSeq(*os)),
+          (out,) if made else ())
     return out
 
 
 def dropout_backward(grad_out, p: float, seed: int, offset: int = 0, held: bool = False,
                      counter=None, grad_x=None, stream=None) -> torch.Tensor:
     """Run ``ck_dropout_backward``: the forward's mask and scale on grad_out."""
-    shape, gs = _drop_call(grad_out, "grad_out", p, seed, offset, held, counter)
-    grad_x, made = _into(grad_x, grad_out, grad_out.shape)
-    _call(lib().ck_dropout_backward, grad_out, stream,
-          (shape, gs, CkSeq(*_seq(grad_x, "grad_x", grad_out, grad_out.shape))),
+    shape, dev, gs = _drop_call(grad_out, "grad_out", p, seed, offset, held, counter)
+    grad_x, os, made = _out_seq(grad_x, "grad_x", grad_out, grad_out.shape)
+    _call(lib().ck_dropout_backward, dev, stream, (shape, gs, CkSeq(*os)),
           (grad_x,) if made else ())
     return grad_x
 
