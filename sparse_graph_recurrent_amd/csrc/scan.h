@@ -184,6 +184,11 @@ __device__ __forceinline__ f32x4 fma_4(f32x4 a, f32x4 b, f32x4 c) {
                fmaf(a[3], b[3], c[3])};
 }
 
+// sum of a[r] b[r] added to c, one operation a state
+__device__ __forceinline__ float dot_add(f32x4 a, f32x4 b, float c) {
+  return fmaf(a[3], b[3], fmaf(a[2], b[2], fmaf(a[1], b[1], fmaf(a[0], b[0], c))));
+}
+
 // x + y after the swap of their halves (rows): lanes of the lower half (even
 // rows) get x summed over a pair of lanes 32 (16) apart, the others y.
 __device__ __forceinline__ float swap32_add(float x, float y) {

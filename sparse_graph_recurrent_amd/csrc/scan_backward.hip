@@ -200,9 +200,9 @@ __global__ __launch_bounds__(kScanThreads, M < 4 ? 2 : 1) void scan_bwd(const Sc
     const int64_t ck_step = (int64_t)s.B * s.D * NP;
     const float* ck = s.saved + (int64_t)(tl / K) * ck_step + row * NP;
     E eu[KQ], ede[KQ], ez[KQ], ego[KQ];
-    f32x4 h[M];
+    f32x4 h[M], hn[M];  // states; those the next tile starts from
 #pragma unroll
-    for (int m = 0; m < M; ++m) h[m] = 0.0f;
+    for (int m = 0; m < M; ++m) hn[m] = 0.0f;
     auto fetch = [&](int last) {
       const uint32_t lu = wu.limit(q, last), ld = wd.limit(q, last), lg = wg.limit(q, last);
 #pragma unroll
@@ -216,7 +216,7 @@ __global__ __launch_bounds__(kScanThreads, M < 4 ? 2 : 1) void scan_bwd(const Sc
 #pragma unroll
         for (int i = 0; i < KQ; ++i) ez[i] = wz.load(4 * i, lz);
       }
-      if (p.active) load_rows<M>(h, ck, q);
+      if (p.active) load_rows<M>(hn, ck, q);
     };
     fetch(p.te - 1 - tl);
     bc.load(p.te - 1 - tl);
@@ -260,8 +260,17 @@ __global__ __launch_bounds__(kScanThreads, M < 4 ? 2 : 1) void scan_bwd(const Sc
         StepsLds::put(ldy, p.c, q, i, dy[i]);
       }
       wave_sync();
+#pragma unroll
+      for (int m = 0; m < M; ++m) h[m] = hn[m];
+      // the tile before, a whole tile's work ahead of its use
       if (more) {
+        wu.advance(-K);
+        wd.advance(-K);
+        wg.advance(-K);
+        if constexpr (GATE) wz.advance(-K);
         bc.advance(-K);
+        ck -= ck_step;
+        fetch(last + K);
         bc.load(last + K);
       }
       const float *lb = lds_bc[buf], *lc = lb + K * NP;
@@ -274,7 +283,8 @@ __global__ __launch_bounds__(kScanThreads, M < 4 ? 2 : 1) void scan_bwd(const Sc
         float acc[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          f32x4 y4 = 0.0f, b4[M], c4[M];
+          f32x4 b4[M], c4[M];
+          float y = 0.0f;
           load_rows<M>(b4, lb + (4 * i + j) * NP, q);
           if constexpr (GATE) load_rows<M>(c4, lc + (4 * i + j) * NP, q);
 #pragma unroll
@@ -282,9 +292,9 @@ __global__ __launch_bounds__(kScanThreads, M < 4 ? 2 : 1) void scan_bwd(const Sc
             a[4 * i + j][m] = exp2_4(d4[j] * (kLog2e * a1[m]));
             before[4 * i + j][m] = h[m];
             h[m] = fma_4(a[4 * i + j][m], h[m], x4[j] * b4[m]);
-            if constexpr (GATE) y4 = m ? fma_4(c4[m], h[m], y4) : c4[m] * h[m];
+            if constexpr (GATE) y = dot_add(c4[m], h[m], y);
           }
-          acc[j] = (y4[0] + y4[1]) + (y4[2] + y4[3]);
+          acc[j] = y;
         }
         if constexpr (GATE) gzf[i] *= fmaf(skip, u[i], rows_reduce4(acc));
       }
@@ -302,7 +312,8 @@ __global__ __launch_bounds__(kScanThreads, M < 4 ? 2 : 1) void scan_bwd(const Sc
 #pragma unroll
         for (int j = 3; j >= 0; --j) {
           const int t = 4 * i + j;
-          f32x4 b4[M], c4[M], s1 = 0.0f, s2 = 0.0f;
+          f32x4 b4[M], c4[M];
+          float s1 = 0.0f, s2 = 0.0f;
           load_rows<M>(b4, lb + t * NP, q);
           load_rows<M>(c4, lc + t * NP, q);
 #pragma unroll
@@ -310,11 +321,11 @@ __global__ __launch_bounds__(kScanThreads, M < 4 ? 2 : 1) void scan_bwd(const Sc
             const f32x4 gh = fma_4(c4[m], f32x4(y4[j]), g[m]);
             const f32x4 vb = gh * x4[j], vc = h[m] * y4[j];
             h[m] = before[t][m];
-            s1 = m ? fma_4(gh, b4[m], s1) : gh * b4[m];
+            s1 = dot_add(gh, b4[m], s1);
             g[m] = a[t][m] * gh;
             const f32x4 w = g[m] * h[m];
             ga[m] = fma_4(w, f32x4(d4[j]), ga[m]);
-            s2 = m ? fma_4(w, a1[m], s2) : w * a1[m];
+            s2 = dot_add(w, a1[m], s2);
             // values of two (step, block) pairs make 16 sums over the channels
             const int half = (t * M + m) % 2;
 #pragma unroll
@@ -339,8 +350,8 @@ __global__ __launch_bounds__(kScanThreads, M < 4 ? 2 : 1) void scan_bwd(const Sc
                   channel_reduce16(v, p.c);
             }
           }
-          sx[j] = (s1[0] + s1[1]) + (s1[2] + s1[3]);
-          sa[j] = (s2[0] + s2[1]) + (s2[2] + s2[3]);
+          sx[j] = s1;
+          sa[j] = s2;
         }
         const float gx = rows_reduce4(sx);  // dL/d(dt u)
         const float gl = rows_reduce4(sa);  // sum_n dL/d(dt A) A
@@ -348,15 +359,6 @@ __global__ __launch_bounds__(kScanThreads, M < 4 ? 2 : 1) void scan_bwd(const Sc
         gu[i] = fmaf(dt[i], gx, skip * dy[i]);
         gbias += gd[i];
         gskip = fmaf(dy[i], u[i], gskip);
-      }
-      // the tiles before, while the waves' sums are joined
-      if (more) {
-        wu.advance(-K);
-        wd.advance(-K);
-        wg.advance(-K);
-        if constexpr (GATE) wz.advance(-K);
-        ck -= ck_step;
-        fetch(last + K);
       }
       if (p.active) {
 #pragma unroll

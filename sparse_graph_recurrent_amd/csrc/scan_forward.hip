@@ -115,15 +115,16 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd(const ScanArgs<E> s) {
         if constexpr (PART) dtsum += (d4[0] + d4[1]) + (d4[2] + d4[3]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          f32x4 y4 = 0.0f, b4[M], c4[M];
+          f32x4 b4[M], c4[M];
+          float y = 0.0f;
           load_rows<M>(b4, lb + (4 * i + j) * NP, q);
           if constexpr (!PART) load_rows<M>(c4, lc + (4 * i + j) * NP, q);
 #pragma unroll
           for (int m = 0; m < M; ++m) {
             h[m] = fma_4(exp2_4(d4[j] * a2[m]), h[m], x4[j] * b4[m]);
-            if constexpr (!PART) y4 = m ? fma_4(c4[m], h[m], y4) : c4[m] * h[m];
+            if constexpr (!PART) y = dot_add(c4[m], h[m], y);
           }
-          acc[j] = (y4[0] + y4[1]) + (y4[2] + y4[3]);
+          acc[j] = y;
         }
         if constexpr (!PART) yo[i] = (y0[i] + rows_reduce4(acc)) * gt[i];
       }
