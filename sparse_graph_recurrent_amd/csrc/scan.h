@@ -15,8 +15,14 @@
 // as fp32 matrix instructions was slower: they keep the vector ALU waiting,
 // 36 cycles for 4 products a lane.)
 //
-// Few rows leave most of the chip idle, and the window is then cut into chunks
-// that run side by side: a first launch finds what each chunk makes of a zero
+// Waves.  A SIMD issues to several waves better than to one, so where rows give
+// it only one, a workgroup works on TW tiles at once, 4 waves each: every wave
+// finds what its tile makes of a zero state, the waves fold these through LDS
+// into the state each tile starts from, and every wave goes over its tile from
+// there with the decays it holds in registers.
+//
+// Still fewer rows leave most of the chip idle, and the window is then cut into
+// chunks that run side by side: a first launch finds what each chunk makes of a zero
 // state (and the sum of its dt, from which its decay exp(A sum dt) follows), a
 // small one joins these to every chunk's entering state, and the main launch
 // starts each chunk from it.  The backward does the same with its adjoint from
@@ -32,7 +38,10 @@
 namespace ckhip {
 
 constexpr int kScanChan = 64;                 // channels per workgroup
-constexpr int kScanThreads = 4 * kScanChan;   // 4 waves
+constexpr int kScanThreads = 4 * kScanChan;   // threads per time tile (4 waves)
+// Time tiles a workgroup works on at once where it works on several: what the
+// registers allow (forward 126 of 128 at 16 waves, backward 223 of 256 at 8).
+constexpr int kScanFwdTW = 4, kScanBwdTW = 2;
 constexpr int64_t kScanMaxN = 64;
 
 // Steps per tile for M blocks of 16 states: a lane of the backward holds a_t
@@ -46,6 +55,7 @@ struct ScanDims {
   int64_t Dg, P;    // channels per group, workgroups per group
   int64_t tiles;    // tiles of the window
   int64_t chunks, chunk_steps;  // chunks of the window (steps: a multiple of K)
+  bool waves;       // several time tiles a workgroup (one chunk only)
 };
 
 template <typename E>
@@ -83,7 +93,9 @@ void scan_launch_backward(const ScanDims& d, const ScanArgs<E>& a, hipStream_t s
 struct Place {
   int b, g, blk, chunk;
   int t0, t1, te, len;
+  int tw;       // the wave's tile among the workgroup's
   int c, q;     // lane: channel of the wave, and its row of lanes
+  int wc;       // channel of the workgroup
   int d;        // channel (clamped to the group's last)
   bool active;  // the channel exists
 };
@@ -99,9 +111,11 @@ __device__ __forceinline__ Place scan_place(const ScanArgs<E>& s) {
   p.b = i % s.B;
   p.chunk = i / s.B;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  p.tw = wave >> 2;
   p.c = threadIdx.x & 15;
   p.q = (threadIdx.x & 63) >> 4;
-  const int dg = p.blk * kScanChan + wave * 16 + p.c;
+  p.wc = (wave & 3) * 16 + p.c;
+  const int dg = p.blk * kScanChan + p.wc;
   p.active = dg < s.Dg;
   p.d = p.g * s.Dg + min(dg, s.Dg - 1);
   p.len = s.T;
@@ -231,18 +245,19 @@ struct StepsLds {
   }
 };
 
-// The workgroup's B and C over a tile as fp32 rows [K][NP] in LDS, 0 past
+// The workgroup's B and C over its KT steps as fp32 rows [KT][NP] in LDS, 0 past
 // the text's end or N.  A thread moves one value of B or of C (M < 4), or one
 // of each: loaded a tile ahead, stored behind the tile before.
-template <typename E, int M>
+template <typename E, int M, int TW>
 struct TileBC {
-  static constexpr int NP = 16 * M, K = scan_tile(M), kRows = K * NP;
-  static constexpr bool kBoth = kRows == kScanThreads;
-  static_assert(kBoth || 2 * kRows == kScanThreads, "each thread has its share");
+  static constexpr int NP = 16 * M, KT = scan_tile(M) * TW, kRows = KT * NP;
+  static constexpr int kThreads = kScanThreads * TW;
+  static constexpr bool kBoth = kRows == kThreads;
+  static_assert(kBoth || 2 * kRows == kThreads, "each thread has its share");
 
-  const char *b, *c;        // the thread's rows of the tile
+  const char *b, *c;        // the thread's rows of the tiles
   uint32_t bstep, cstep;
-  int ts, e;                // its step of the tile, its place in LDS
+  int ts, e;                // its step of the tiles, its place in LDS
   bool mine, is_c;
   E vb, vc;
   bool in;
@@ -265,7 +280,7 @@ struct TileBC {
     b += (int64_t)steps * (int64_t)bstep;
     c += (int64_t)steps * (int64_t)cstep;
   }
-  // last: the last step of the text, relative to the tile's first
+  // last: the last step of the text, relative to the tiles' first
   __device__ __forceinline__ void load(int last) {
     in = mine && ts <= last;
     if (in) {
@@ -273,7 +288,7 @@ struct TileBC {
       if constexpr (kBoth) vc = *reinterpret_cast<const E*>(c);
     }
   }
-  // rows: [2][K][NP], B then C
+  // rows: [2][KT][NP], B then C
   __device__ __forceinline__ void store(float* rows) const {
     rows[(is_c ? kRows : 0) + e] = in ? (float)vb : 0.0f;
     if constexpr (kBoth) rows[kRows + e] = in ? (float)vc : 0.0f;
@@ -284,6 +299,32 @@ template <typename E>
 __device__ __forceinline__ void zero_steps(const Seq<E>& s, const Place& p) {
   if (!p.active) return;
   for (int t = max(p.t0, p.len) + p.q; t < p.t1; t += 4) s.row(t, p.b)[p.d] = (E)0.0f;
+}
+
+// Folds what TW tiles make of a zero state (made) and their decays into the
+// state the wave's tile starts from; next: the state behind the last of them.
+// FORWARD runs up from `start`, else down.
+template <int M, int TW, bool FORWARD>
+__device__ __forceinline__ void fold_tiles(f32x4 (&start)[M], f32x4 (&next)[M], const float* made,
+                                           const float* decay, const Place& p) {
+  constexpr int NP = 16 * M;
+  f32x4 cur[M];
+#pragma unroll
+  for (int m = 0; m < M; ++m) cur[m] = start[m];
+#pragma unroll
+  for (int i = 0; i < TW; ++i) {
+    const int w = FORWARD ? i : TW - 1 - i;
+    f32x4 mw[M], ew[M];
+    load_rows<M>(mw, made + (w * kScanChan + p.wc) * NP, p.q);
+    load_rows<M>(ew, decay + (w * kScanChan + p.wc) * NP, p.q);
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      if (w == p.tw) start[m] = cur[m];
+      cur[m] = fma_4(ew[m], cur[m], mw[m]);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m) next[m] = cur[m];
 }
 
 // Joins the chunks: edge[c] from "made of a zero state" to "starts from".

@@ -17,6 +17,7 @@ ScanDims scan_sizes(const ck_scan_shape& s) {
   d.Dg = s.D / s.G;
   d.P = (d.Dg + kScanChan - 1) / kScanChan;
   d.tiles = (s.T + d.K - 1) / d.K;
+  d.waves = false;
   d.chunks = 1;
   d.chunk_steps = std::max<int64_t>(d.tiles, 1) * d.K;
   return d;
@@ -29,18 +30,28 @@ void scan_cut(ScanDims* d, int64_t want) {
   d->chunks = std::max<int64_t>((d->tiles + per - 1) / per, 1);
 }
 
-// Cutting pays below this many workgroups: the second pass over a chunk's steps
-// costs 0.7 of a forward's and 0.25 of a backward's main pass, the idle SIMDs
-// and single waves more.  Training pass at 2048 channels x 1024 steps in bf16,
-// uncut and cut to about 2048 workgroups: 128 workgroups 439 and 226 us, 256 473
-// and 402, 384 630 and 622, 512 642 and 768.
-constexpr int64_t kScanFewGroups = 384, kScanGoalGroups = 2048, kScanMinChunk = 64;
+// How a window is spread over the chip, by the workgroups that its rows and
+// channels give (forward + backward of 2048 channels in bf16, 1024 steps, us):
+//   - from kScanFewGroups on, each walks the window alone (384: 618 against 711
+//     with several tiles each; 512: 635 against 768 cut);
+//   - a workgroup a CU, nearly (256): several tiles each (366 against 409 cut;
+//     but 192 workgroups: 355 against 331, and from 257 on some CU would have two);
+//   - fewer: cut to about kScanGoalGroups (128: 243 against 353 with several tiles
+//     each; uncut 439).  The second pass over the steps costs 0.7 of a forward's
+//     and 0.25 of a backward's main launch.
+// Rows of unequal lengths leave CUs idle unless cut.  Windows too short to cut
+// take several tiles each (64 steps x 32 x 256 channels: 37 against 41).
+constexpr int64_t kScanFewGroups = 384, kScanCus = 256, kScanGoalGroups = 2048;
+constexpr int64_t kScanMinChunk = 64;  // steps
 
-ScanDims scan_dims(const ck_scan_shape& s) {
+ScanDims scan_dims(const ck_scan_shape& s, bool ragged) {
   ScanDims d = scan_sizes(s);
   const int64_t wgs = d.P * d.G * d.B;
-  if (wgs < kScanFewGroups)
-    scan_cut(&d, std::min(kScanGoalGroups / wgs, std::max<int64_t>(s.T / kScanMinChunk, 1)));
+  const bool is_short = s.T < 2 * kScanMinChunk;
+  if (d.M == 1 && wgs <= kScanCus && (is_short || (!ragged && wgs > kScanCus * 13 / 16)))
+    d.waves = true;
+  else if (wgs < kScanFewGroups && !is_short)
+    scan_cut(&d, std::min(kScanGoalGroups / wgs, s.T / kScanMinChunk));
   return d;
 }
 
@@ -105,7 +116,7 @@ ScanWs scan_ws(const ScanDims& d, bool backward) {
   w.edge = take(edges * d.NP);
   w.dtsum = take(edges);
   w.part_bc = take(backward ? d.P * d.T * d.B * d.G * 2 * d.NP : 0);
-  w.part_a = take(backward ? d.chunks * d.B * d.D * (d.NP + 2) : 0);
+  w.part_a = take(backward ? (d.waves ? kScanBwdTW : d.chunks) * d.B * d.D * (d.NP + 2) : 0);
   w.total = at;
   return w;
 }
@@ -123,7 +134,7 @@ ck_status scan_check_shape(const ck_scan_shape* s) {
               (long long)s->G, (long long)s->D);
     return CK_ERR_BAD_SIZE;
   }
-  const ScanDims d = scan_dims(*s);
+  const ScanDims d = scan_sizes(*s);
   if (d.P * d.G * d.B >= INT_MAX / 2 || d.B * d.D / 64 >= INT_MAX || d.D * d.NP >= INT_MAX ||
       (d.T > 0 && d.B * d.G * d.NP >= (int64_t(1) << 36) / d.T)) {
     set_error("B=%lld, D=%lld or T=%lld is too large", (long long)d.B, (long long)d.D,
@@ -191,10 +202,14 @@ extern "C" ck_status ck_scan_sizes(const ck_scan_shape* shape, size_t* saved_byt
   clear_error();
   const ck_status rc = scan_check_shape(shape);
   if (rc != CK_OK) return rc;
-  const ScanDims d = scan_dims(*shape);
+  const ScanDims d = scan_sizes(*shape);
   if (saved_bytes) *saved_bytes = scan_saved(d);
-  if (forward_bytes) *forward_bytes = scan_ws(scan_dims(*shape), false).total;
-  if (backward_bytes) *backward_bytes = scan_ws(scan_dims(*shape), true).total;
+  auto most = [&](bool backward) {  // whether lengths will be given or not
+    return std::max(scan_ws(scan_dims(*shape, false), backward).total,
+                    scan_ws(scan_dims(*shape, true), backward).total);
+  };
+  if (forward_bytes) *forward_bytes = most(false);
+  if (backward_bytes) *backward_bytes = most(true);
   return CK_OK;
 }
 
@@ -206,7 +221,7 @@ extern "C" ck_status ck_scan_forward(const ck_scan_shape* shape, const ck_scan_i
   if (rc == CK_OK) rc = scan_check_inputs(*shape, in);
   if (rc == CK_OK) rc = seq_check(out, shape->dtype, shape->T == 0, "out");
   if (rc != CK_OK) return rc;
-  const ScanDims d = scan_dims(*shape);
+  const ScanDims d = scan_dims(*shape, in->lengths != nullptr);
   const ScanWs ws = scan_ws(d, false);
   rc = seq_check_ws(workspace, workspace_bytes, ws.total);
   if (rc == CK_OK && saved) rc = check_aligned(saved, "saved");
@@ -244,7 +259,7 @@ extern "C" ck_status ck_scan_backward(const ck_scan_shape* shape, const ck_scan_
   if (rc == CK_OK)
     rc = seq_check(grads->z, shape->dtype, none || !in->z.data, "the gradient of z");
   if (rc != CK_OK) return rc;
-  const ScanDims d = scan_dims(*shape);
+  const ScanDims d = scan_dims(*shape, in->lengths != nullptr);
   const ScanWs ws = scan_ws(d, true);
   rc = seq_check_ws(workspace, workspace_bytes, ws.total);
   if (rc == CK_OK && saved) rc = check_aligned(saved, "saved");
@@ -286,7 +301,7 @@ extern "C" ck_status ck_scan_step(const ck_scan_shape* shape, const ck_scan_inpu
     set_error(state ? "a step takes no lengths" : "state is NULL");
     return state ? CK_ERR_BAD_VALUE : CK_ERR_NULL_ARG;
   }
-  const ScanDims d = scan_dims(*shape);
+  const ScanDims d = scan_dims(*shape, in->lengths != nullptr);
   return seq_dispatch(shape->dtype, [&](auto* e) -> ck_status {
     using E = std::remove_pointer_t<decltype(e)>;
     ScanArgs<E> a = scan_args<E>(*shape, d, *in, nullptr, ScanWs{});

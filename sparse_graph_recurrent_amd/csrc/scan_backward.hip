@@ -93,7 +93,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_bwd_part(const ScanArgs<E> 
     const int tl = p.t0 + (p.te - 1 - p.t0) / K * K;
     Walk<const E> wd(s.delta, tl, p.b, q, p.d), wg(s.go, tl, p.b, q, p.d);
     Walk<const E> wz(GATE ? s.z : s.go, tl, p.b, q, p.d);
-    TileBC<E, M> bc(s, p, tl);
+    TileBC<E, M, 1> bc(s, p, tl);
     E de[KQ], go[KQ], z[KQ];
     auto fetch = [&](int last) {
       const uint32_t ld = wd.limit(q, last), lg = wg.limit(q, last);
@@ -162,19 +162,22 @@ __global__ __launch_bounds__(kScanThreads) void scan_bwd_part(const ScanArgs<E> 
   if (q == 0) s.dtsum[at] = dtsum;
 }
 
-template <typename E, int M, bool GATE>
-__global__ __launch_bounds__(kScanThreads, M < 4 ? 2 : 1) void scan_bwd(const ScanArgs<E> s) {
-  constexpr int K = scan_tile(M), KQ = K / 4, NP = 16 * M;
-  __shared__ __align__(16) float lds_dt[4][StepsLds::kFloats];
-  __shared__ __align__(16) float lds_x[4][StepsLds::kFloats];
-  __shared__ __align__(16) float lds_dy[4][StepsLds::kFloats];
-  __shared__ __align__(16) float lds_bc[2][2 * K * NP];
-  __shared__ __align__(16) float red[4][K * 2 * NP];
+template <typename E, int M, int TW, bool GATE>
+__global__ __launch_bounds__(kScanThreads * TW, M < 4 && TW == 1 ? 2 : 1) void scan_bwd(const ScanArgs<E> s) {
+  constexpr int K = scan_tile(M), KQ = K / 4, NP = 16 * M, KT = K * TW;
+  __shared__ __align__(16) float lds_dt[4 * TW][StepsLds::kFloats];
+  __shared__ __align__(16) float lds_x[4 * TW][StepsLds::kFloats];
+  __shared__ __align__(16) float lds_dy[4 * TW][StepsLds::kFloats];
+  __shared__ __align__(16) float lds_bc[2][2 * KT * NP];
+  __shared__ __align__(16) float red[4 * TW][K * 2 * NP];
+  // what each tile hands on of a zero adjoint, and its decay
+  __shared__ __align__(16) float made[TW > 1 ? TW * kScanChan * NP : 4];
+  __shared__ __align__(16) float decay[TW > 1 ? TW * kScanChan * NP : 4];
   const Place p = scan_place(s);
   const int q = p.q, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float *ldt = lds_dt[wave], *lx = lds_x[wave], *ldy = lds_dy[wave];
   const int64_t row = (int64_t)p.b * s.D + p.d;
-  f32x4 a1[M], ga[M], g[M];
+  f32x4 a1[M], ga[M], g[M];  // g: the adjoint the workgroup's tiles start from
   load_states<M>(a1, p.active ? s.a : nullptr, p.d, q, s.N);
 #pragma unroll
   for (int m = 0; m < M; ++m) ga[m] = g[m] = 0.0f;
@@ -191,19 +194,21 @@ __global__ __launch_bounds__(kScanThreads, M < 4 ? 2 : 1) void scan_bwd(const Sc
   const bool part_wg = (p.blk + 1) * kScanChan > s.Dg;  // some lanes have no channel
 
   if (p.t0 < p.te) {
-    const int tl = p.t0 + (p.te - 1 - p.t0) / K * K;
-    Walk<const E> wu(s.u, tl, p.b, q, p.d), wd(s.delta, tl, p.b, q, p.d);
-    Walk<const E> wg(s.go, tl, p.b, q, p.d), wz(GATE ? s.z : s.u, tl, p.b, q, p.d);
-    Walk<E> ou(s.gu, tl, p.b, q, p.d), od(s.gdelta, tl, p.b, q, p.d);
-    Walk<E> oz(GATE ? s.gz : s.gu, tl, p.b, q, p.d);
-    TileBC<E, M> bc(s, p, tl);
+    const int tl = p.t0 + (p.te - 1 - p.t0) / KT * KT, tw0 = tl + p.tw * K;
+    Walk<const E> wu(s.u, tw0, p.b, q, p.d), wd(s.delta, tw0, p.b, q, p.d);
+    Walk<const E> wg(s.go, tw0, p.b, q, p.d), wz(GATE ? s.z : s.u, tw0, p.b, q, p.d);
+    Walk<E> ou(s.gu, tw0, p.b, q, p.d), od(s.gdelta, tw0, p.b, q, p.d);
+    Walk<E> oz(GATE ? s.gz : s.gu, tw0, p.b, q, p.d);
+    TileBC<E, M, TW> bc(s, p, tl);
     const int64_t ck_step = (int64_t)s.B * s.D * NP;
-    const float* ck = s.saved + (int64_t)(tl / K) * ck_step + row * NP;
+    const float* ck = s.saved + (int64_t)(tw0 / K) * ck_step + row * NP;
     E eu[KQ], ede[KQ], ez[KQ], ego[KQ];
     f32x4 h[M], hn[M];  // states; those the next tile starts from
 #pragma unroll
     for (int m = 0; m < M; ++m) hn[m] = 0.0f;
+    // the wave's tile, whose last step with text is `last` (negative: none)
     auto fetch = [&](int last) {
+      if (TW > 1 && last < 0) return;
       const uint32_t lu = wu.limit(q, last), ld = wd.limit(q, last), lg = wg.limit(q, last);
 #pragma unroll
       for (int i = 0; i < KQ; ++i) {
@@ -218,14 +223,14 @@ __global__ __launch_bounds__(kScanThreads, M < 4 ? 2 : 1) void scan_bwd(const Sc
       }
       if (p.active) load_rows<M>(hn, ck, q);
     };
-    fetch(p.te - 1 - tl);
+    fetch(p.te - 1 - tw0);
     bc.load(p.te - 1 - tl);
     bc.store(lds_bc[0]);
     __syncthreads();
 
     int buf = 0;
-    for (int t0 = tl; t0 >= p.t0; t0 -= K, buf ^= 1) {
-      const int last = p.te - 1 - t0;  // of the tile's steps, the last with text
+    for (int t0 = tl; t0 >= p.t0; t0 -= KT, buf ^= 1) {
+      const int last = p.te - 1 - t0 - p.tw * K;  // of the tile's steps, the last with text
       const bool more = t0 > p.t0;
       float dt[KQ], u[KQ], dy[KQ], sg[KQ], gzf[KQ];
 #pragma unroll
@@ -264,22 +269,24 @@ __global__ __launch_bounds__(kScanThreads, M < 4 ? 2 : 1) void scan_bwd(const Sc
       for (int m = 0; m < M; ++m) h[m] = hn[m];
       // the tile before, a whole tile's work ahead of its use
       if (more) {
-        wu.advance(-K);
-        wd.advance(-K);
-        wg.advance(-K);
-        if constexpr (GATE) wz.advance(-K);
-        bc.advance(-K);
-        ck -= ck_step;
-        fetch(last + K);
-        bc.load(last + K);
+        wu.advance(-KT);
+        wd.advance(-KT);
+        wg.advance(-KT);
+        if constexpr (GATE) wz.advance(-KT);
+        bc.advance(-KT);
+        ck -= TW * ck_step;
+        fetch(last + KT);
+        bc.load(p.te - 1 - t0 + KT);
       }
-      const float *lb = lds_bc[buf], *lc = lb + K * NP;
+      const float *lb = lds_bc[buf] + p.tw * K * NP, *lc = lb + KT * NP;
 
       // the tile's states again, from its first
       f32x4 a[K][M], before[K][M];  // decays, and the states before each step
+      float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < KQ; ++i) {
         const f32x4 d4 = StepsLds::get(ldt, p.c, i), x4 = StepsLds::get(lx, p.c, i);
+        if constexpr (TW > 1) sum += (d4[0] + d4[1]) + (d4[2] + d4[3]);
         float acc[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -299,8 +306,34 @@ __global__ __launch_bounds__(kScanThreads, M < 4 ? 2 : 1) void scan_bwd(const Sc
         if constexpr (GATE) gzf[i] *= fmaf(skip, u[i], rows_reduce4(acc));
       }
 
+      f32x4 next[M];
+      if constexpr (TW > 1) {
+        // what the tile hands on of a zero adjoint
+        f32x4 mk[M], e[M];
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          mk[m] = 0.0f;
+          e[m] = exp2_4(sum * (kLog2e * a1[m]));
+        }
+#pragma unroll
+        for (int i = KQ - 1; i >= 0; --i) {
+          const f32x4 y4 = StepsLds::get(ldy, p.c, i);
+#pragma unroll
+          for (int j = 3; j >= 0; --j) {
+            f32x4 c4[M];
+            load_rows<M>(c4, lc + (4 * i + j) * NP, q);
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+              mk[m] = a[4 * i + j][m] * fma_4(c4[m], f32x4(y4[j]), mk[m]);
+          }
+        }
+        const int at = (p.tw * kScanChan + p.wc) * NP;
+        store_rows<M>(&made[at], mk, q);
+        store_rows<M>(&decay[at], e, q);
+      }
       if (more) bc.store(lds_bc[buf ^ 1]);
       __syncthreads();  // (and the waves' sums of the tiles before are read)
+      if constexpr (TW > 1) fold_tiles<M, TW, false>(g, next, made, decay, p);
 
       // and backwards: g enters a step as a_{t+1} dL/dh_{t+1}
       float v[16], gu[KQ], gd[KQ];
@@ -369,24 +402,32 @@ __global__ __launch_bounds__(kScanThreads, M < 4 ? 2 : 1) void scan_bwd(const Sc
             if constexpr (GATE) *oz.at(4 * i) = (E)gzf[i];
           }
       }
-      ou.advance(-K);
-      od.advance(-K);
-      if constexpr (GATE) oz.advance(-K);
+      ou.advance(-KT);
+      od.advance(-KT);
+      if constexpr (GATE) oz.advance(-KT);
+      if constexpr (TW > 1) {
+#pragma unroll
+        for (int m = 0; m < M; ++m) g[m] = next[m];
+      }
       __syncthreads();
-      for (int e = threadIdx.x; e < K * 2 * NP; e += kScanThreads) {
-        const int t = e / (2 * NP);
-        if (t <= last)
-          s.part_bc[((((int64_t)p.blk * s.T + t0 + t) * s.B + p.b) * s.G + p.g) * (2 * NP) +
-                    e % (2 * NP)] = (red[0][e] + red[1][e]) + (red[2][e] + red[3][e]);
+      for (int e = threadIdx.x; e < KT * 2 * NP; e += kScanThreads * TW) {
+        const int t = t0 + e / (2 * NP), w = e / (K * 2 * NP) * 4, i = e % (K * 2 * NP);
+        if (t < p.te)
+          s.part_bc[((((int64_t)p.blk * s.T + t) * s.B + p.b) * s.G + p.g) * (2 * NP) +
+                    e % (2 * NP)] =
+              (red[w][i] + red[w + 1][i]) + (red[w + 2][i] + red[w + 3][i]);
       }
     }
   }
-  zero_steps(s.gu, p);
-  zero_steps(s.gdelta, p);
-  if constexpr (GATE) zero_steps(s.gz, p);
+  if (p.tw == 0) {
+    zero_steps(s.gu, p);
+    zero_steps(s.gdelta, p);
+    if constexpr (GATE) zero_steps(s.gz, p);
+    if (s.gstate0 && p.chunk == 0 && p.active) store_states<M>(g, s.gstate0, row, q, s.N);
+  }
   if (!p.active) return;
-  if (s.gstate0 && p.chunk == 0) store_states<M>(g, s.gstate0, row, q, s.N);
-  float* pa = s.part_a + ((int64_t)p.chunk * s.B * s.D + row) * (NP + 2);
+  // (with several tiles a workgroup there is one chunk, and tw in its place)
+  float* pa = s.part_a + ((int64_t)(p.chunk + p.tw) * s.B * s.D + row) * (NP + 2);
 #pragma unroll
   for (int m = 0; m < M; ++m)
 #pragma unroll
@@ -421,11 +462,11 @@ __device__ __forceinline__ void sum_bc(const ScanArgs<E>& s, int NP, int64_t i) 
 // Gradients of A, D and the bias: the sums of all rows and chunks in a fixed
 // order.  A workgroup takes 32 sums, eight threads each one a stretch of them.
 template <typename E>
-__device__ __forceinline__ void sum_a(const ScanArgs<E>& s, int NP, int64_t first) {
+__device__ __forceinline__ void sum_a(const ScanArgs<E>& s, int NP, int parts, int64_t first) {
   __shared__ float red[8][32];
   const int64_t all = (int64_t)s.D * (NP + 2), i = first + (threadIdx.x & 31);
   const int y = threadIdx.x >> 5;
-  const int64_t rows = (int64_t)s.chunks * s.B;
+  const int64_t rows = (int64_t)parts * s.B;
   const int64_t each = (rows + 7) / 8, r0 = each * y, r1 = min(r0 + each, rows);
   float sum = 0.0f;
   if (i < all) {
@@ -449,11 +490,20 @@ __device__ __forceinline__ void sum_a(const ScanArgs<E>& s, int NP, int64_t firs
 
 // The last launch: both kinds of sums, the first a_wgs workgroups those of A.
 template <typename E>
-__global__ __launch_bounds__(256) void scan_sums(const ScanArgs<E> s, int NP, unsigned a_wgs) {
+__global__ __launch_bounds__(256) void scan_sums(const ScanArgs<E> s, int NP, int parts,
+                                                  unsigned a_wgs) {
   if (blockIdx.x < a_wgs)
-    sum_a(s, NP, (int64_t)blockIdx.x * 32);
+    sum_a(s, NP, parts, (int64_t)blockIdx.x * 32);
   else
     sum_bc(s, NP, (int64_t)(blockIdx.x - a_wgs) * 256 + threadIdx.x);
+}
+
+template <typename E, int M, int TW>
+void launch_main(unsigned grid, const ScanArgs<E>& a, hipStream_t stream) {
+  if (a.z.p)
+    scan_bwd<E, M, TW, true><<<grid, kScanThreads * TW, 0, stream>>>(a);
+  else
+    scan_bwd<E, M, TW, false><<<grid, kScanThreads * TW, 0, stream>>>(a);
 }
 
 template <typename E, int M>
@@ -468,13 +518,15 @@ void launch(const ScanDims& d, const ScanArgs<E>& a, hipStream_t stream) {
     scan_join<false><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
         a.edge, a.dtsum, a.a, a.gstate, d.B * d.D, a.D, a.N, d.NP, a.chunks);
   }
-  if (a.z.p)
-    scan_bwd<E, M, true><<<grid, kScanThreads, 0, stream>>>(a);
-  else
-    scan_bwd<E, M, false><<<grid, kScanThreads, 0, stream>>>(a);
+  int parts = a.chunks;  // partial sums of A's gradient a row
+  if constexpr (M == 1) {
+    if (d.waves) parts = kScanBwdTW;
+    if (d.waves) launch_main<E, M, kScanBwdTW>(grid, a, stream);
+  }
+  if (!d.waves) launch_main<E, M, 1>(grid, a, stream);
   const int64_t bc = d.T * d.B * d.G * 2 * d.NP, ae = d.D * (d.NP + 2);
   const unsigned a_wgs = (unsigned)((ae + 31) / 32);
-  scan_sums<E><<<a_wgs + (unsigned)((bc + 255) / 256), 256, 0, stream>>>(a, d.NP, a_wgs);
+  scan_sums<E><<<a_wgs + (unsigned)((bc + 255) / 256), 256, 0, stream>>>(a, d.NP, parts, a_wgs);
 }
 
 }  // namespace

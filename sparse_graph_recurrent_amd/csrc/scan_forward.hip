@@ -7,18 +7,22 @@ namespace ckhip {
 namespace {
 
 // PART: only the chunk's summary (what it makes of a zero state, sum of dt).
-template <typename E, int M, bool GATE, bool PART>
-__global__ __launch_bounds__(kScanThreads) void scan_fwd(const ScanArgs<E> s) {
-  constexpr int K = scan_tile(M), KQ = K / 4, NP = 16 * M;
-  __shared__ __align__(16) float lds_dt[4][StepsLds::kFloats];
-  __shared__ __align__(16) float lds_x[4][StepsLds::kFloats];
-  __shared__ __align__(16) float lds_bc[2][2 * K * NP];
+template <typename E, int M, int TW, bool GATE, bool PART>
+__global__ __launch_bounds__(kScanThreads * TW) void scan_fwd(const ScanArgs<E> s) {
+  constexpr int K = scan_tile(M), KQ = K / 4, NP = 16 * M, KT = K * TW;
+  constexpr int kBufs = TW > 1 ? 3 : 2;  // (with one barrier amid the tile's work)
+  __shared__ __align__(16) float lds_dt[4 * TW][StepsLds::kFloats];
+  __shared__ __align__(16) float lds_x[4 * TW][StepsLds::kFloats];
+  __shared__ __align__(16) float lds_bc[kBufs][2 * KT * NP];
+  // what each tile makes of a zero state, and its decay
+  __shared__ __align__(16) float made[2][TW > 1 ? TW * kScanChan * NP : 4];
+  __shared__ __align__(16) float decay[2][TW > 1 ? TW * kScanChan * NP : 4];
   const Place p = scan_place(s);
   const int q = p.q, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float *ldt = lds_dt[wave], *lx = lds_x[wave];
   const int64_t row = (int64_t)p.b * s.D + p.d;
   float* edge = s.edge + ((int64_t)p.chunk * s.B * s.D + row) * NP;
-  f32x4 a2[M], h[M];
+  f32x4 a2[M], h[M];  // h: the state the workgroup's tiles start from
   load_states<M>(a2, s.a, p.d, q, s.N);
 #pragma unroll
   for (int m = 0; m < M; ++m) {
@@ -36,12 +40,15 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd(const ScanArgs<E> s) {
   float dtsum = 0.0f;
 
   if (p.t0 < p.te) {
-    Walk<const E> wu(s.u, p.t0, p.b, q, p.d), wd(s.delta, p.t0, p.b, q, p.d);
-    Walk<const E> wz(GATE ? s.z : s.u, p.t0, p.b, q, p.d);
-    Walk<E> wo(s.out, p.t0, p.b, q, p.d);
-    TileBC<E, M> bc(s, p, p.t0);
+    const int tw0 = p.t0 + p.tw * K;
+    Walk<const E> wu(s.u, tw0, p.b, q, p.d), wd(s.delta, tw0, p.b, q, p.d);
+    Walk<const E> wz(GATE ? s.z : s.u, tw0, p.b, q, p.d);
+    Walk<E> wo(s.out, tw0, p.b, q, p.d);
+    TileBC<E, M, TW> bc(s, p, p.t0);
     E u[KQ], de[KQ], z[KQ];
+    // the wave's tile, whose last step with text is `last` (negative: none)
     auto fetch = [&](int last) {
+      if (TW > 1 && last < 0) return;
       const uint32_t lu = wu.limit(q, last), ld = wd.limit(q, last);
 #pragma unroll
       for (int i = 0; i < KQ; ++i) {
@@ -54,18 +61,19 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd(const ScanArgs<E> s) {
         for (int i = 0; i < KQ; ++i) z[i] = wz.load(4 * i, lz);
       }
     };
-    fetch(p.te - 1 - p.t0);
+    fetch(p.te - 1 - tw0);
     bc.load(p.te - 1 - p.t0);
     bc.store(lds_bc[0]);
     const int64_t ck_step = (int64_t)s.B * s.D * NP;
     float* ck = nullptr;
-    if (s.saved) ck = s.saved + (int64_t)(p.t0 / K) * ck_step + row * NP;
+    if (s.saved) ck = s.saved + (int64_t)(tw0 / K) * ck_step + row * NP;
     __syncthreads();
 
-    int buf = 0;
-    for (int t0 = p.t0; t0 < p.te; t0 += K, buf ^= 1) {
-      const int last = p.te - 1 - t0;  // of the tile's steps, the last with text
-      const bool more = t0 + K < p.te;
+    int buf = 0, par = 0;
+    for (int t0 = p.t0; t0 < p.te; t0 += KT, par ^= 1) {
+      const int last = p.te - 1 - t0 - p.tw * K;  // of the tile's steps, the last with text
+      const int nbuf = buf + 1 < kBufs ? buf + 1 : 0;
+      const bool more = t0 + KT < p.te;
       float dt[KQ], x[KQ], y0[KQ], gt[KQ];
 #pragma unroll
       for (int i = 0; i < KQ; ++i) {
@@ -96,17 +104,49 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd(const ScanArgs<E> s) {
       }
       wave_sync();
       if (more) {
-        wu.advance(K);
-        wd.advance(K);
-        if constexpr (GATE) wz.advance(K);
-        bc.advance(K);
-        fetch(last - K);
-        bc.load(last - K);
+        wu.advance(KT);
+        wd.advance(KT);
+        if constexpr (GATE) wz.advance(KT);
+        bc.advance(KT);
+        fetch(last - KT);
+        bc.load(p.te - 1 - t0 - KT);
       }
-      const float *lb = lds_bc[buf], *lc = lb + K * NP;
+      const float *lb = lds_bc[buf] + p.tw * K * NP, *lc = lb + KT * NP;
+
+      f32x4 a[TW > 1 ? K : 1][M], next[M];
+      if constexpr (TW > 1) {
+        // decays, and what the tile makes of a zero state
+        f32x4 mk[M], e[M];
+        float sum = 0.0f;
+#pragma unroll
+        for (int m = 0; m < M; ++m) mk[m] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < KQ; ++i) {
+          const f32x4 d4 = StepsLds::get(ldt, p.c, i), x4 = StepsLds::get(lx, p.c, i);
+          sum += (d4[0] + d4[1]) + (d4[2] + d4[3]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            f32x4 b4[M];
+            load_rows<M>(b4, lb + (4 * i + j) * NP, q);
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+              a[4 * i + j][m] = exp2_4(d4[j] * a2[m]);
+              mk[m] = fma_4(a[4 * i + j][m], mk[m], x4[j] * b4[m]);
+            }
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < M; ++m) e[m] = exp2_4(sum * a2[m]);
+        const int at = (p.tw * kScanChan + p.wc) * NP;
+        store_rows<M>(&made[par][at], mk, q);
+        store_rows<M>(&decay[par][at], e, q);
+        if (more) bc.store(lds_bc[nbuf]);
+        __syncthreads();
+        fold_tiles<M, TW, true>(h, next, made[par], decay[par], p);
+      }
 
       if constexpr (!PART)
-        if (ck && p.active) store_rows<M>(ck, h, q);
+        if (ck && p.active && (TW == 1 || last >= 0)) store_rows<M>(ck, h, q);
       float yo[KQ];
 #pragma unroll
       for (int i = 0; i < KQ; ++i) {
@@ -121,7 +161,12 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd(const ScanArgs<E> s) {
           if constexpr (!PART) load_rows<M>(c4, lc + (4 * i + j) * NP, q);
 #pragma unroll
           for (int m = 0; m < M; ++m) {
-            h[m] = fma_4(exp2_4(d4[j] * a2[m]), h[m], x4[j] * b4[m]);
+            f32x4 am;
+            if constexpr (TW > 1)
+              am = a[4 * i + j][m];
+            else
+              am = exp2_4(d4[j] * a2[m]);
+            h[m] = fma_4(am, h[m], x4[j] * b4[m]);
             if constexpr (!PART) y = dot_add(c4[m], h[m], y);
           }
           acc[j] = y;
@@ -134,11 +179,17 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd(const ScanArgs<E> s) {
           for (int i = 0; i < KQ; ++i)
             if (4 * i + q <= last) *wo.at(4 * i) = (E)yo[i];
         }
-        wo.advance(K);
-        if (ck) ck += ck_step;
+        wo.advance(KT);
+        if (ck) ck += TW * ck_step;
       }
-      if (more) bc.store(lds_bc[buf ^ 1]);
-      __syncthreads();
+      if constexpr (TW > 1) {
+#pragma unroll
+        for (int m = 0; m < M; ++m) h[m] = next[m];
+      } else {
+        if (more) bc.store(lds_bc[nbuf]);
+        __syncthreads();
+      }
+      buf = nbuf;
     }
   }
   if constexpr (PART) {
@@ -146,7 +197,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd(const ScanArgs<E> s) {
       store_rows<M>(edge, h, q);
       if (q == 0) s.dtsum[(int64_t)p.chunk * s.B * s.D + row] = dtsum;
     }
-  } else {
+  } else if (p.tw == 0) {
     zero_steps(s.out, p);
     // the chunk in which the text ends has the final state
     if (s.state && p.active && p.chunk == min(p.len / s.chunk_steps, s.chunks - 1))
@@ -154,20 +205,28 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd(const ScanArgs<E> s) {
   }
 }
 
+template <typename E, int M, int TW>
+void launch_main(unsigned grid, const ScanArgs<E>& a, hipStream_t stream) {
+  if (a.z.p)
+    scan_fwd<E, M, TW, true, false><<<grid, kScanThreads * TW, 0, stream>>>(a);
+  else
+    scan_fwd<E, M, TW, false, false><<<grid, kScanThreads * TW, 0, stream>>>(a);
+}
+
 template <typename E, int M>
 void launch(const ScanDims& d, const ScanArgs<E>& a, hipStream_t stream) {
   const unsigned wgs = (unsigned)(d.P * d.G * d.B), grid = wgs * (unsigned)d.chunks;
   if (d.chunks > 1) {
     // (nothing follows the last chunk)
-    scan_fwd<E, M, false, true><<<grid - wgs, kScanThreads, 0, stream>>>(a);
+    scan_fwd<E, M, 1, false, true><<<grid - wgs, kScanThreads, 0, stream>>>(a);
     const int64_t n = d.B * d.D * d.NP;
     scan_join<true><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
         a.edge, a.dtsum, a.a, a.state0, d.B * d.D, a.D, a.N, d.NP, a.chunks);
   }
-  if (a.z.p)
-    scan_fwd<E, M, true, false><<<grid, kScanThreads, 0, stream>>>(a);
-  else
-    scan_fwd<E, M, false, false><<<grid, kScanThreads, 0, stream>>>(a);
+  if constexpr (M == 1) {
+    if (d.waves) return launch_main<E, M, kScanFwdTW>(grid, a, stream);
+  }
+  launch_main<E, M, 1>(grid, a, stream);
 }
 
 }  // namespace

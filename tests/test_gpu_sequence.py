@@ -147,6 +147,12 @@ SCAN = [  # T, B, D, N, G, dtype, gate, softplus, lengths, layout
     (200, 1, 128, 16, 1, "fp32", True, True, None, "time"),
     (1500, 1, 16, 16, 1, "fp32", True, True, None, "time"),
     (700, 3, 40, 16, 2, "fp32", True, True, [700, 333, 0], "batch"),
+    # enough rows for a workgroup each without cutting the window, and for
+    # several tiles a workgroup over a long one
+    (20, 400, 64, 16, 1, "bf16", True, True, None, "time"),
+    (25, 390, 40, 16, 1, "fp32", False, True, [(7 * b) % 26 for b in range(390)], "time"),
+    (131, 210, 64, 12, 1, "fp32", True, True, None, "time"),
+    (10, 390, 48, 24, 1, "fp32", True, True, None, "time"),
 ]
 
 
