@@ -139,13 +139,21 @@ struct Walk {
         off((uint32_t)(lane_step * (uint32_t)s.st + (uint32_t)channel) * (uint32_t)sizeof(E)),
         step((uint32_t)s.st * (uint32_t)sizeof(E)) {}
   __device__ __forceinline__ void advance(int steps) { tile += (int64_t)steps * (int64_t)step; }
-  // element `ahead` steps after the lane's, at most at the offset `limit`
-  __device__ __forceinline__ E load(int ahead, uint32_t limit) const {
-    return *reinterpret_cast<const E*>(tile + min(off + (uint32_t)ahead * step, limit));
-  }
-  // offset of step `last` of the tile for the lane whose first step is q
-  __device__ __forceinline__ uint32_t limit(int q, int last) const {
-    return last >= scan_tile(1) ? 0xFFFFFFFFu : off + (uint32_t)(last - q) * step;
+  // The lane's elements of a tile of 4 KQ steps whose last with text is `last`;
+  // past it, that step's.  (A uniform branch: selects of the offsets instead
+  // cost a tenth of the forward's vector ALU time.)
+  template <int KQ>
+  __device__ __forceinline__ void load(std::remove_const_t<E> (&v)[KQ], int q, int last) const {
+    if (last >= 4 * KQ - 1) {
+#pragma unroll
+      for (int i = 0; i < KQ; ++i)
+        v[i] = *reinterpret_cast<const E*>(tile + (off + (uint32_t)(4 * i) * step));
+    } else {
+      const uint32_t most = off + (uint32_t)(last - q) * step;
+#pragma unroll
+      for (int i = 0; i < KQ; ++i)
+        v[i] = *reinterpret_cast<const E*>(tile + min(off + (uint32_t)(4 * i) * step, most));
+    }
   }
   __device__ __forceinline__ E* at(int ahead) const {
     using X = std::remove_const_t<E>;

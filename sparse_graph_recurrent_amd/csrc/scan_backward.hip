@@ -96,17 +96,9 @@ __global__ __launch_bounds__(kScanThreads) void scan_bwd_part(const ScanArgs<E> 
     TileBC<E, M, 1> bc(s, p, tl);
     E de[KQ], go[KQ], z[KQ];
     auto fetch = [&](int last) {
-      const uint32_t ld = wd.limit(q, last), lg = wg.limit(q, last);
-#pragma unroll
-      for (int i = 0; i < KQ; ++i) {
-        de[i] = wd.load(4 * i, ld);
-        go[i] = wg.load(4 * i, lg);
-      }
-      if constexpr (GATE) {
-        const uint32_t lz = wz.limit(q, last);
-#pragma unroll
-        for (int i = 0; i < KQ; ++i) z[i] = wz.load(4 * i, lz);
-      }
+      wd.load(de, q, last);
+      wg.load(go, q, last);
+      if constexpr (GATE) wz.load(z, q, last);
     };
     fetch(p.te - 1 - tl);
     bc.load(p.te - 1 - tl);
@@ -209,18 +201,10 @@ __global__ __launch_bounds__(kScanThreads * TW, M < 4 && TW == 1 ? 2 : 1) void s
     // the wave's tile, whose last step with text is `last` (negative: none)
     auto fetch = [&](int last) {
       if (TW > 1 && last < 0) return;
-      const uint32_t lu = wu.limit(q, last), ld = wd.limit(q, last), lg = wg.limit(q, last);
-#pragma unroll
-      for (int i = 0; i < KQ; ++i) {
-        eu[i] = wu.load(4 * i, lu);
-        ede[i] = wd.load(4 * i, ld);
-        ego[i] = wg.load(4 * i, lg);
-      }
-      if constexpr (GATE) {
-        const uint32_t lz = wz.limit(q, last);
-#pragma unroll
-        for (int i = 0; i < KQ; ++i) ez[i] = wz.load(4 * i, lz);
-      }
+      wu.load(eu, q, last);
+      wd.load(ede, q, last);
+      wg.load(ego, q, last);
+      if constexpr (GATE) wz.load(ez, q, last);
       if (p.active) load_rows<M>(hn, ck, q);
     };
     fetch(p.te - 1 - tw0);

@@ -49,17 +49,9 @@ __global__ __launch_bounds__(kScanThreads * TW) void scan_fwd(const ScanArgs<E> 
     // the wave's tile, whose last step with text is `last` (negative: none)
     auto fetch = [&](int last) {
       if (TW > 1 && last < 0) return;
-      const uint32_t lu = wu.limit(q, last), ld = wd.limit(q, last);
-#pragma unroll
-      for (int i = 0; i < KQ; ++i) {
-        u[i] = wu.load(4 * i, lu);
-        de[i] = wd.load(4 * i, ld);
-      }
-      if constexpr (GATE && !PART) {
-        const uint32_t lz = wz.limit(q, last);
-#pragma unroll
-        for (int i = 0; i < KQ; ++i) z[i] = wz.load(4 * i, lz);
-      }
+      wu.load(u, q, last);
+      wd.load(de, q, last);
+      if constexpr (GATE && !PART) wz.load(z, q, last);
     };
     fetch(p.te - 1 - tw0);
     bc.load(p.te - 1 - p.t0);
