@@ -153,6 +153,9 @@ SCAN = [  # T, B, D, N, G, dtype, gate, softplus, lengths, layout
     (25, 390, 40, 16, 1, "fp32", False, True, [(7 * b) % 26 for b in range(390)], "time"),
     (131, 210, 64, 12, 1, "fp32", True, True, None, "time"),
     (10, 390, 48, 24, 1, "fp32", True, True, None, "time"),
+    # cut windows with more than 16 states, and with groups that end in a workgroup
+    (200, 1, 40, 33, 1, "fp32", True, True, None, "time"),
+    (150, 2, 66, 20, 3, "bf16", False, True, [150, 77], "batch"),
 ]
 
 
@@ -221,6 +224,23 @@ def test_scan_extremes():
     assert not torch.isfinite(out[2, 0, 0])          # inf * u * B
     assert torch.isfinite(out[:, 0, 1:]).all()       # other channels do not see it
     assert torch.isfinite(out[:2, 0, 0]).all()       # nor do earlier steps
+
+
+def test_scan_values_of_one_step_stay_in_it():
+    """An infinite or undefined B, C or u reaches no earlier step and no other row."""
+    for k in ("B", "C", "u"):
+        g, _ = scan_problem(15, 12, 2, 20, 16, 1, "fp32", True, True, None, "time")
+        clean, _, _, _ = sgr.selective_scan_forward(
+            g["u"], g["delta"], g["A"], g["B"], g["C"], g["D"], g["z"], g["delta_bias"],
+            g["state0"], delta_softplus=True)
+        g[k][6, 0] = float("nan")
+        out, state, _, _ = sgr.selective_scan_forward(
+            g["u"], g["delta"], g["A"], g["B"], g["C"], g["D"], g["z"], g["delta_bias"],
+            g["state0"], delta_softplus=True)
+        assert torch.equal(out[:6], clean[:6]) and torch.equal(out[:, 1], clean[:, 1]), k
+        assert torch.isnan(out[6, 0]).all(), k
+        # C enters no state: the steps behind are clean again
+        assert torch.equal(out[7:, 0], clean[7:, 0]) == (k == "C"), k
 
 
 def test_scan_same_bits_every_time_and_on_another_stream():
