@@ -20,7 +20,7 @@ namespace ckhip {
 namespace {
 
 constexpr int kDropThreads = 256;
-constexpr int kDropHeld = 8;  // steps a thread gives one held mask to
+constexpr int kDropHeld = 4;  // steps a thread gives one held mask to
 
 template <typename E>
 struct DropArgs {

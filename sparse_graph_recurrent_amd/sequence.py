@@ -87,40 +87,32 @@ _NONE = (0, 0, 0)  # a ck_seq that is absent
 
 def _declare(L: ctypes.CDLL) -> None:
     """Argument types of the sequence entry points (called once, by ``lib``).
-    Structures are passed by address: a ctypes instance or its bytes."""
+    Structures are passed by address: their packed bytes, or ``ctypes.byref``."""
     p, sz, q = ctypes.c_void_p, ctypes.c_size_t, CkSeq
     szp = ctypes.POINTER(sz)
-    L.ck_scan_sizes.argtypes = [_Struct, szp, szp, szp]
-    L.ck_scan_forward.argtypes = [_Struct, _Struct, q, p, p, p, sz, p]
-    L.ck_scan_backward.argtypes = [_Struct, _Struct, p, q, p, _Struct, p, sz, p]
-    L.ck_scan_step.argtypes = [_Struct, _Struct, q, p, p]
-    L.ck_conv_sizes.argtypes = [_Struct, szp]
-    L.ck_conv_forward.argtypes = [_Struct, q, p, p, p, p, q, p, p]
-    L.ck_conv_backward.argtypes = [_Struct, q, p, p, p, p, q, p, q, p, p, p, p, sz, p]
-    L.ck_conv_step.argtypes = [_Struct, q, p, p, p, q, p, p]
-    L.ck_dropout_forward.argtypes = [_Struct, q, q, q, p]
-    L.ck_dropout_backward.argtypes = [_Struct, q, q, p]
-
-
-class _Struct:
-    """Argument converter of ``const struct*`` parameters."""
-
-    @classmethod
-    def from_param(cls, v):
-        if v is None or isinstance(v, bytes):
-            return ctypes.c_char_p(v)
-        return ctypes.byref(v)
+    L.ck_scan_sizes.argtypes = [p, szp, szp, szp]
+    L.ck_scan_forward.argtypes = [p, p, q, p, p, p, sz, p]
+    L.ck_scan_backward.argtypes = [p, p, p, q, p, p, p, sz, p]
+    L.ck_scan_step.argtypes = [p, p, q, p, p]
+    L.ck_conv_sizes.argtypes = [p, szp]
+    L.ck_conv_forward.argtypes = [p, q, p, p, p, p, q, p, p]
+    L.ck_conv_backward.argtypes = [p, q, p, p, p, p, q, p, q, p, p, p, p, sz, p]
+    L.ck_conv_step.argtypes = [p, q, p, p, p, q, p, p]
+    L.ck_dropout_forward.argtypes = [p, q, q, q, p]
+    L.ck_dropout_backward.argtypes = [p, q, q, p]
 
 
 def _call(fn, dev: int, stream, args, made=()):
     """Runs one entry point with device `dev` current on `stream` (None: the
     current one); memory of the tensors in `made`, allocated here for another
     stream than the current, is kept from reuse until that stream is done."""
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return _call(fn, dev, stream, args, made)
     if stream is None:
-        _check(fn(*args, torch._C._cuda_getCurrentRawStream(dev)))
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+        if status:
+            _check(status)
         return
     _check(fn(*args, stream.cuda_stream))
     for t in made:
@@ -151,15 +143,11 @@ def _refuse(t, name: str, dtype, dev: int, shape):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _fits(t, dtype, dev: int, shape) -> bool:
-    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev \
-        and t.shape == shape
-
-
 def _seq(t, name: str, dtype, dev: int, shape, last: int = 1):
     """(address, stride_t, stride_b) of a [T, B, ...] tensor (a step's [B, ...]
     tensor counts as T = 1), checked."""
-    if not _fits(t, dtype, dev, shape):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
+            and t.shape == shape):
         _refuse(t, name, dtype, dev, shape)
     if 0 in shape:
         return _NONE
@@ -176,7 +164,8 @@ def _par(t, name: str, dev: int, shape, dtype=torch.float32) -> int:
     """Address of an optional contiguous parameter, state or length vector."""
     if t is None:
         return 0
-    if not _fits(t, dtype, dev, shape) or not t.is_contiguous():
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
+            and t.shape == shape and t.is_contiguous()):
         _refuse(t, name, dtype, dev, shape)
     return 0 if 0 in shape else t.data_ptr()
 

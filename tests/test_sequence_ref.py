@@ -96,15 +96,15 @@ def L():
 
 
 def _scan(**kw):
-    return ScanShape(*[kw.get(k, v) for k, v in dict(T=8, B=2, D=64, N=16, G=1, dtype=1,
-                                                     delta_softplus=1).items()])
+    return ctypes.byref(ScanShape(*[kw.get(k, v) for k, v in dict(
+        T=8, B=2, D=64, N=16, G=1, dtype=1, delta_softplus=1).items()]))
 
 
 def _inputs(**kw):
     v = dict(u=SEQ, delta=SEQ, b=SEQ, c=SEQ, z=NONE, a=FAKE, d=None, delta_bias=None, state0=None,
              lengths=None)
     v.update(kw)
-    return ScanInputs(*v.values())
+    return ctypes.byref(ScanInputs(*v.values()))
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -131,7 +131,7 @@ def test_scan_input_refusals(L, kw, status):
 
 
 def test_scan_call_refusals(L):
-    g = ScanGrads(SEQ, SEQ, SEQ, SEQ, NONE, FAKE, None, None, None)
+    g = ctypes.byref(ScanGrads(SEQ, SEQ, SEQ, SEQ, NONE, FAKE, None, None, None))
     s, i = _scan(), _inputs()
     assert L.ck_scan_sizes(None, None, None, None) == NULL_ARG
     assert L.ck_scan_forward(s, None, SEQ, None, None, None, 0, None) == NULL_ARG
@@ -151,8 +151,8 @@ def test_scan_call_refusals(L):
 
 
 def _conv(**kw):
-    return ConvShape(*[kw.get(k, v) for k, v in dict(T=8, B=2, D=64, W=4, dtype=1,
-                                                     silu=1).items()])
+    return ctypes.byref(ConvShape(*[kw.get(k, v) for k, v in dict(
+        T=8, B=2, D=64, W=4, dtype=1, silu=1).items()]))
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -192,14 +192,14 @@ def test_conv_call_refusals(L):
     (dict(p=1.5), BAD_VALUE), (dict(p=float("nan")), BAD_VALUE), (dict(dtype=5), BAD_VALUE),
     (dict(T=2**20, B=2**12), TOO_LARGE)])
 def test_dropout_refusals(L, kw, status):
-    s = DropoutShape(*[kw.get(k, v) for k, v in dict(T=8, B=2, D=64, dtype=1, held=0, p=0.5,
-                                                     seed=1, offset=0, counter=None).items()])
+    s = ctypes.byref(DropoutShape(*[kw.get(k, v) for k, v in dict(
+        T=8, B=2, D=64, dtype=1, held=0, p=0.5, seed=1, offset=0, counter=None).items()]))
     assert L.ck_dropout_forward(s, SEQ, NONE, SEQ, None) == status
     assert L.ck_dropout_backward(s, SEQ, SEQ, None) == status
 
 
 def test_dropout_call_refusals(L):
-    s = DropoutShape(8, 2, 64, 1, 0, 0.5, 1, 0, None)
+    s = ctypes.byref(DropoutShape(8, 2, 64, 1, 0, 0.5, 1, 0, None))
     assert L.ck_dropout_forward(None, SEQ, NONE, SEQ, None) == NULL_ARG
     assert L.ck_dropout_forward(s, NONE, NONE, SEQ, None) == NULL_ARG
     assert L.ck_dropout_forward(s, SEQ, NONE, NONE, None) == NULL_ARG
