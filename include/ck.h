@@ -358,7 +358,7 @@ ck_status ck_profile_collect_lif(double* gather_ms, int64_t* gather_launches, do
  * Conventions of these entry points, beside those above
  *   - A sequence tensor [T, B, channels] is a ck_seq: its channels are
  *     adjacent, its steps and batch rows lie stride_t and stride_b elements
- *     apart (0 <= stride_t < 2^26 and 0 <= stride_b, else CK_ERR_BAD_VALUE: a
+ *     apart (0 <= stride_t < 2^24 and 0 <= stride_b, else CK_ERR_BAD_VALUE: a
  *     slice of a wider tensor, batch-major storage, or 0 for an input that
  *     is the same at every step or row).  Elements are of the call's
  *     ck_dtype; parameters, scan states and their gradients are fp32 and

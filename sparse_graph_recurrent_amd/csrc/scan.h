@@ -263,43 +263,52 @@ struct TileBC {
   static constexpr bool kBoth = kRows == kThreads;
   static_assert(kBoth || 2 * kRows == kThreads, "each thread has its share");
 
-  const char *b, *c;        // the thread's rows of the tiles
+  const char *b, *c;   // the tiles' first step (uniform)
+  uint32_t bo, co;     // the thread's byte offsets from it
   uint32_t bstep, cstep;
-  int ts, e;                // its step of the tiles, its place in LDS
+  int ts, e;           // its step of the tiles, its place in LDS
   bool mine, is_c;
   E vb, vc;
-  bool in;
 
   __device__ __forceinline__ TileBC(const ScanArgs<E>& s, const Place& p, int t) {
     const int tid = threadIdx.x;
-    is_c = !kBoth && tid >= kRows;
+    // (uniform: a wave moves values of B or of C)
+    is_c = !kBoth && __builtin_amdgcn_readfirstlane(tid) >= kRows;
     e = kBoth ? tid : tid % kRows;
     ts = e / NP;
     const int n = e % NP;
     mine = n < s.N;
-    const int64_t at = (int64_t)p.g * s.N + min(n, s.N - 1);
+    const uint32_t at = (uint32_t)(p.g * s.N + min(n, s.N - 1)) * (uint32_t)sizeof(E);
     const Seq<const E>& first = is_c ? s.c : s.b;
     bstep = (uint32_t)first.st * (uint32_t)sizeof(E);
     cstep = (uint32_t)s.c.st * (uint32_t)sizeof(E);
-    b = reinterpret_cast<const char*>(first.row(t, p.b) + at) + (uint64_t)ts * bstep;
-    c = reinterpret_cast<const char*>(s.c.row(t, p.b) + at) + (uint64_t)ts * cstep;
+    b = reinterpret_cast<const char*>(first.row(t, p.b));
+    c = reinterpret_cast<const char*>(s.c.row(t, p.b));
+    bo = (uint32_t)ts * bstep + at;
+    co = (uint32_t)ts * cstep + at;
+    vb = vc = (E)0.0f;
   }
   __device__ __forceinline__ void advance(int steps) {
     b += (int64_t)steps * (int64_t)bstep;
-    c += (int64_t)steps * (int64_t)cstep;
+    if constexpr (kBoth) c += (int64_t)steps * (int64_t)cstep;
   }
   // last: the last step of the text, relative to the tiles' first
   __device__ __forceinline__ void load(int last) {
-    in = mine && ts <= last;
-    if (in) {
-      vb = *reinterpret_cast<const E*>(b);
-      if constexpr (kBoth) vc = *reinterpret_cast<const E*>(c);
+    if (last >= KT - 1) {
+      vb = *reinterpret_cast<const E*>(b + bo);
+      if constexpr (kBoth) vc = *reinterpret_cast<const E*>(c + co);
+    } else {
+      vb = vc = (E)0.0f;
+      if (ts <= last) {
+        vb = *reinterpret_cast<const E*>(b + bo);
+        if constexpr (kBoth) vc = *reinterpret_cast<const E*>(c + co);
+      }
     }
   }
   // rows: [2][KT][NP], B then C
   __device__ __forceinline__ void store(float* rows) const {
-    rows[(is_c ? kRows : 0) + e] = in ? (float)vb : 0.0f;
-    if constexpr (kBoth) rows[kRows + e] = in ? (float)vc : 0.0f;
+    rows[(is_c ? kRows : 0) + e] = mine ? (float)vb : 0.0f;
+    if constexpr (kBoth) rows[kRows + e] = mine ? (float)vc : 0.0f;
   }
 };
 

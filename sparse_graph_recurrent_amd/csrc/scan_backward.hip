@@ -113,7 +113,9 @@ __global__ __launch_bounds__(kScanThreads) void scan_bwd_part(const ScanArgs<E> 
       for (int i = 0; i < KQ; ++i) {
         const bool in = 4 * i + q <= last;
         const float raw = (float)de[i] + bias, sp = softplus_hw(raw).value;
-        StepsLds::put(ldt, p.c, q, i, in ? (s.softplus ? sp : raw) : 0.0f);
+        const float dt = in ? (s.softplus ? sp : raw) : 0.0f;
+        dtsum += dt;
+        StepsLds::put(ldt, p.c, q, i, dt);
         float y = (float)go[i];
         if constexpr (GATE) {
           const float zf = (float)z[i];
@@ -134,7 +136,6 @@ __global__ __launch_bounds__(kScanThreads) void scan_bwd_part(const ScanArgs<E> 
 #pragma unroll
       for (int i = KQ - 1; i >= 0; --i) {
         const f32x4 d4 = StepsLds::get(ldt, p.c, i), y4 = StepsLds::get(ldy, p.c, i);
-        dtsum += (d4[0] + d4[1]) + (d4[2] + d4[3]);
 #pragma unroll
         for (int j = 3; j >= 0; --j) {
           f32x4 c4[M];
@@ -148,6 +149,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_bwd_part(const ScanArgs<E> 
       __syncthreads();
     }
   }
+  dtsum = rows_sum(dtsum);
   if (!p.active) return;
   const int64_t at = (int64_t)p.chunk * s.B * s.D + row;
   store_rows<M>(s.edge + at * NP, g, q);

@@ -85,6 +85,7 @@ __global__ __launch_bounds__(kScanThreads * TW) void scan_fwd(const ScanArgs<E> 
 #pragma unroll
       for (int i = 0; i < KQ; ++i) {
         x[i] = dt[i] * y0[i];
+        if constexpr (PART) dtsum += dt[i];
         StepsLds::put(ldt, p.c, q, i, dt[i]);
         StepsLds::put(lx, p.c, q, i, x[i]);
         y0[i] *= skip;
@@ -144,7 +145,6 @@ __global__ __launch_bounds__(kScanThreads * TW) void scan_fwd(const ScanArgs<E> 
       for (int i = 0; i < KQ; ++i) {
         float acc[4];
         const f32x4 d4 = StepsLds::get(ldt, p.c, i), x4 = StepsLds::get(lx, p.c, i);
-        if constexpr (PART) dtsum += (d4[0] + d4[1]) + (d4[2] + d4[3]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           f32x4 b4[M], c4[M];
@@ -185,6 +185,7 @@ __global__ __launch_bounds__(kScanThreads * TW) void scan_fwd(const ScanArgs<E> 
     }
   }
   if constexpr (PART) {
+    dtsum = rows_sum(dtsum);
     if (p.active) {
       store_rows<M>(edge, h, q);
       if (q == 0) s.dtsum[(int64_t)p.chunk * s.B * s.D + row] = dtsum;

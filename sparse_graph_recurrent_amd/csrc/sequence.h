@@ -47,9 +47,9 @@ inline ck_status seq_check_shape(int64_t T, int64_t B, int64_t D, int dtype) {
   return CK_OK;
 }
 
-// Step strides stay below this many elements, so that the byte offset of any
-// step of a 16-step tile from the tile's first fits 32 unsigned bits.
-constexpr int64_t kSeqMaxStrideT = int64_t(1) << 26;
+// Step strides stay below this many elements, so that the byte offset of 32
+// steps and a row fits 32 unsigned bits.
+constexpr int64_t kSeqMaxStrideT = int64_t(1) << 24;
 
 // A [T, B, ...] tensor: present unless optional, aligned to its elements, with
 // strides in range (a zero stride broadcasts an input).
@@ -64,7 +64,7 @@ inline ck_status seq_check(const ck_seq& s, int dtype, bool optional, const char
     return CK_ERR_BAD_VALUE;
   }
   if (s.stride_t < 0 || s.stride_t >= kSeqMaxStrideT || s.stride_b < 0) {
-    set_error("%s has strides (%lld, %lld); they must be in [0, 2^26) and not negative", what,
+    set_error("%s has strides (%lld, %lld); they must be in [0, 2^24) and not negative", what,
               (long long)s.stride_t, (long long)s.stride_b);
     return CK_ERR_BAD_VALUE;
   }
@@ -157,7 +157,8 @@ __device__ __forceinline__ float sigmoid_hw(float x) {
 
 // log(1 + exp(x)) = max(x, 0) + log1p(e), e = exp(-|x|), and its derivative
 // 1 / (1 + exp(-x)).  The part of e that the sum w = 1 + e rounds away is added
-// back to first order, so both keep their relative accuracy down to exp(x)
+// back, to first order and without its factor 1 / w (which changes it by less
+// than 2^-24 of the result): both keep their relative accuracy down to exp(x)
 // itself for very negative x.
 struct Softplus {
   float value, slope;
@@ -165,7 +166,7 @@ struct Softplus {
 __device__ __forceinline__ Softplus softplus_hw(float x) {
   const float e = exp2_hw(-kLog2e * fabsf(x));
   const float w = 1.0f + e, r = rcp_hw(w);
-  const float l = fmaf(kLn2, __builtin_amdgcn_logf(w), (e - (w - 1.0f)) * r);
+  const float l = fmaf(kLn2, __builtin_amdgcn_logf(w), e - (w - 1.0f));
   return Softplus{fmaxf(x, 0.0f) + l, x < 0.0f ? e * r : r};
 }
 
