@@ -355,7 +355,7 @@ ck_status ck_profile_collect_lif(double* gather_ms, int64_t* gather_launches, do
  * prompts, and a form for single tokens), and a counter-based dropout
  * regularises the training.
  *
- * Conventions of these entry points, beside those above
+ * Conventions of these entry points, where they differ from those above
  *   - A sequence tensor [T, B, channels] is a ck_seq: its channels are
  *     adjacent, its steps and batch rows lie stride_t and stride_b elements
  *     apart (0 <= stride_t < 2^24 and 0 <= stride_b, else CK_ERR_BAD_VALUE: a

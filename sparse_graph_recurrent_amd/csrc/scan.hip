@@ -48,10 +48,15 @@ ScanDims scan_dims(const ck_scan_shape& s, bool ragged) {
   ScanDims d = scan_sizes(s);
   const int64_t wgs = d.P * d.G * d.B;
   const bool is_short = s.T < 2 * kScanMinChunk;
-  if (d.M == 1 && wgs <= kScanCus && (is_short || (!ragged && wgs > kScanCus * 13 / 16)))
+  if (d.M == 1 && wgs <= kScanCus && (is_short || (!ragged && wgs > kScanCus * 13 / 16))) {
     d.waves = true;
-  else if (wgs < kScanFewGroups && !is_short)
-    scan_cut(&d, std::min(kScanGoalGroups / wgs, s.T / kScanMinChunk));
+  } else if (wgs < kScanFewGroups && !is_short) {
+    // chunks are joined one after the other, eight in about a step's time of a
+    // lone wave: no more of them than about a chunk has steps
+    int64_t most = 64;
+    while (most * most < s.T) most *= 2;
+    scan_cut(&d, std::min(kScanGoalGroups / wgs, std::min(s.T / kScanMinChunk, most)));
+  }
   return d;
 }
 
@@ -136,6 +141,7 @@ ck_status scan_check_shape(const ck_scan_shape* s) {
   }
   const ScanDims d = scan_sizes(*s);
   if (d.P * d.G * d.B >= INT_MAX / 2 || d.B * d.D / 64 >= INT_MAX || d.D * d.NP >= INT_MAX ||
+      d.G * d.N > (int64_t(1) << 28) ||  // (byte offsets in a step of B or C: 32 bits)
       (d.T > 0 && d.B * d.G * d.NP >= (int64_t(1) << 36) / d.T)) {
     set_error("B=%lld, D=%lld or T=%lld is too large", (long long)d.B, (long long)d.D,
               (long long)d.T);

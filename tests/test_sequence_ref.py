@@ -111,7 +111,8 @@ def _inputs(**kw):
     (dict(T=-1), BAD_SIZE), (dict(B=0), BAD_SIZE), (dict(D=0), BAD_SIZE), (dict(N=0), BAD_SIZE),
     (dict(N=65), BAD_SIZE), (dict(G=0), BAD_SIZE), (dict(G=3), BAD_SIZE), (dict(G=128), BAD_SIZE),
     (dict(T=2**31), TOO_LARGE), (dict(B=2**31), TOO_LARGE), (dict(D=2**31), TOO_LARGE),
-    (dict(B=2**30, D=2**10), TOO_LARGE), (dict(T=2**30, B=2**20, D=64), TOO_LARGE),
+    (dict(B=2**30, D=2**10), TOO_LARGE), (dict(D=2**28, N=1), TOO_LARGE),
+    (dict(D=2**26, G=2**26, N=16), TOO_LARGE), (dict(T=2**30, B=2**20, D=64), TOO_LARGE),
     (dict(dtype=3), BAD_VALUE), (dict(dtype=-1), BAD_VALUE)])
 def test_scan_shape_refusals(L, kw, status):
     s = ctypes.c_size_t()
@@ -124,7 +125,7 @@ def test_scan_shape_refusals(L, kw, status):
     (dict(u=NONE), NULL_ARG), (dict(delta=NONE), NULL_ARG), (dict(b=NONE), NULL_ARG),
     (dict(c=NONE), NULL_ARG), (dict(a=None), NULL_ARG),
     (dict(u=CkSeq(FAKE + 1, 64, 64)), BAD_VALUE), (dict(z=CkSeq(FAKE, -64, 64)), BAD_VALUE),
-    (dict(delta=CkSeq(FAKE, 64, -1)), BAD_VALUE), (dict(c=CkSeq(FAKE, 2**26, 64)), BAD_VALUE)])
+    (dict(delta=CkSeq(FAKE, 64, -1)), BAD_VALUE), (dict(c=CkSeq(FAKE, 2**24, 64)), BAD_VALUE)])
 def test_scan_input_refusals(L, kw, status):
     assert L.ck_scan_forward(_scan(), _inputs(**kw), SEQ, None, None, FAKE, 2**40, None) == status
     assert L.ck_scan_step(_scan(T=1), _inputs(**kw), SEQ, FAKE, None) == status
