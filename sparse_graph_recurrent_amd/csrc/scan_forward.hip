@@ -1,4 +1,12 @@
 // scan_forward.hip -- the selective scan over a window (see scan.h).
+//
+// Bound by the vector ALU: per step and state an exponential (8.5 cycles a
+// wave), two products and two multiply-adds (4 each where they mix with
+// others), and a fifth of that again for the per-channel work.  Measured, 16
+// states, bf16, gated: a training window of 2048 steps x 8 rows x 2048 channels
+// in 230 to 250 us (vector ALU 83 % busy; 550 MB, half of it the states left
+// for the backward, at 2.2 TB/s); a prompt of 16384 steps, one row, in 105
+// (summaries, ALU 86 % busy) + 9 (join) + 140 us (96 %; 2.0 TB/s).
 #include "scan.h"
 
 #include <type_traits>
