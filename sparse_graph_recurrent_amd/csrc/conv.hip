@@ -206,12 +206,15 @@ __device__ __forceinline__ void conv_bwd_run(float (&gw)[W + 1][V], const ConvAr
 #pragma unroll
     for (int j = 0; j < kConvAhead; ++j) {
       const int t = tb + j;
-      const bool in = t <= last;  // (a run's own steps past its end are past the text's)
+      // Past the text (as a run's own steps past its end are) x and g are 0, and
+      // so is dL/dp unless the text's last inputs make it NaN: then it is NaN at
+      // its last step already, wherever these reach.
+      const Pack<E, V> xj = pack_keep(xn[j], t <= last), gj = pack_keep(gn[j], t <= last);
       float gx[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        x[W - 1][i] = in ? (float)xn[j].v[i] : 0.0f;
-        float g = in ? (float)gn[j].v[i] : 0.0f;
+        x[W - 1][i] = (float)xj.v[i];
+        float g = (float)gj.v[i];
         if (s.silu) {
           float a = bias[i];
 #pragma unroll
@@ -219,7 +222,7 @@ __device__ __forceinline__ void conv_bwd_run(float (&gw)[W + 1][V], const ConvAr
           const float sg = sigmoid_hw(a);
           g *= sg * fmaf(a, 1.0f - sg, 1.0f);
         }
-        ga[W - 1][i] = in ? g : 0.0f;
+        ga[W - 1][i] = g;
         if constexpr (OWN) {
 #pragma unroll
           for (int k = 0; k < W; ++k) gw[k][i] = fmaf(ga[W - 1][i], x[k][i], gw[k][i]);
