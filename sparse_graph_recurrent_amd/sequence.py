@@ -145,12 +145,10 @@ def _refuse(t, name: str, dtype, dev: int, shape):
 
 def _seq(t, name: str, dtype, dev: int, shape, last: int = 1):
     """(address, stride_t, stride_b) of a [T, B, ...] tensor (a step's [B, ...]
-    tensor counts as T = 1), checked."""
+    tensor counts as T = 1), checked.  (An empty tensor's address is 0.)"""
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
             and t.shape == shape):
         _refuse(t, name, dtype, dev, shape)
-    if 0 in shape:
-        return _NONE
     st = t.stride()
     if st[-1] != 1 or last == 2 and st[-2] != shape[-1]:
         if not _adjacent(t, last):  # (sizes of 1 may have any stride)
@@ -167,7 +165,7 @@ def _par(t, name: str, dev: int, shape, dtype=torch.float32) -> int:
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
             and t.shape == shape and t.is_contiguous()):
         _refuse(t, name, dtype, dev, shape)
-    return 0 if 0 in shape else t.data_ptr()
+    return t.data_ptr()
 
 
 def _first(t, name: str, dims) -> int:
@@ -182,26 +180,22 @@ def _first(t, name: str, dims) -> int:
     return t.get_device()
 
 
-def _out_seq(t, name: str, like: torch.Tensor, shape, last: int = 1):
-    """(tensor, its ck_seq fields, made here) of an output: the caller's, checked,
-    or a new contiguous one."""
-    if t is not None:
-        return t, _seq(t, name, like.dtype, like.get_device(), shape, last), False
-    t = like.new_empty(shape)
-    if 0 in shape:
-        return t, _NONE, True
-    st = t.stride()
-    if len(shape) - last == 1:
-        return t, (t.data_ptr(), 0, st[0]), True
-    return t, (t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0), True
+def _out_seq(t, name: str, like: torch.Tensor, last: int = 1):
+    """(tensor, its ck_seq fields, made here) of an output of like's shape: the
+    caller's, checked, or a new contiguous one."""
+    made = t is None
+    if made:  # (a copy of a tensor's layout is the quicker of the two calls)
+        t = torch.empty_like(like) if like.is_contiguous() else like.new_empty(like.shape)
+    return t, _seq(t, name, like.dtype, like.get_device(), like.shape, last), made
 
 
-def _out_par(t, name: str, like: torch.Tensor, shape, dtype=torch.float32):
-    """(tensor, its address, made here) of a contiguous output."""
+def _out_par(t, name: str, like: torch.Tensor, shape, dtype=torch.float32, model=None):
+    """(tensor, its address, made here) of a contiguous output; `model`: a
+    contiguous tensor of its shape and type, if there is one (quicker to copy)."""
     if t is not None:
         return t, _par(t, name, like.get_device(), shape, dtype), False
-    t = like.new_empty(shape, dtype=dtype)
-    return t, 0 if 0 in shape else t.data_ptr(), True
+    t = like.new_empty(shape, dtype=dtype) if model is None else torch.empty_like(model)
+    return t, t.data_ptr(), True
 
 
 def _buffer(buf, nbytes: int, like: torch.Tensor, name: str):
@@ -210,7 +204,7 @@ def _buffer(buf, nbytes: int, like: torch.Tensor, name: str):
     if buf is None:
         if not nbytes:
             return None, None, 0, False
-        buf = like.new_empty((nbytes,), dtype=torch.uint8)
+        buf = torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=like.device)
         return buf, buf.data_ptr(), nbytes, True
     size = buf.numel() * buf.element_size()
     if buf.get_device() != like.get_device() or size < nbytes or not buf.is_contiguous():
@@ -264,8 +258,8 @@ def selective_scan_forward(u, delta, A, B, C, D=None, z=None, delta_bias=None, s
     shape, inputs, dev, (T, rows, ch, N, _) = _scan_call(
         u, delta, A, B, C, D, z, delta_bias, state0, lengths, delta_softplus)
     sb, fb, _ = _scan_sizes(shape)
-    out, os, m0 = _out_seq(out, "out", u, u.shape)
-    state, st, m1 = _out_par(state, "state", u, (rows, ch, N))
+    out, os, m0 = _out_seq(out, "out", u)
+    state, st, m1 = _out_par(state, "state", u, (rows, ch, N), model=state0)
     saved, sp, _, m2 = _buffer(saved, sb, u, "saved") if save or saved is not None else \
         (None, None, 0, False)
     workspace, wp, wn, m3 = _buffer(workspace, fb, u, "workspace")
@@ -287,19 +281,21 @@ def selective_scan_backward(u, delta, A, B, C, saved, grad_out, D=None, z=None, 
     if sb and saved is None:
         raise ValueError("saved is missing")
     _, sp, _, _ = _buffer(saved, sb, u, "saved")
-    us, bs, ss = u.shape, B.shape, (rows, ch, N)
-    go = CkSeq(*_seq(grad_out, "grad_out", u.dtype, dev, us))
+    ss = (rows, ch, N)
+    go = CkSeq(*_seq(grad_out, "grad_out", u.dtype, dev, u.shape))
     gs = _par(grad_state, "grad_state", dev, ss)
     made = grads is None
     g = {} if made else grads
     q = {}
-    for name, sh, last in (("g_u", us, 1), ("g_delta", us, 1), ("g_B", bs, 2), ("g_C", bs, 2)):
-        g[name], q[name], _ = _out_seq(None if made else grads[name], name, u, sh, last)
-    if z is not None:
-        g["g_z"], q["g_z"], _ = _out_seq(None if made else grads["g_z"], "g_z", u, us)
-    for name, sh in (("g_A", A.shape), ("g_D", (ch,)), ("g_delta_bias", (ch,)), ("g_state0", ss)):
+    for name, like, last in (("g_u", u, 1), ("g_delta", delta, 1), ("g_B", B, 2), ("g_C", C, 2)) \
+            + ((("g_z", z, 1),) if z is not None else ()):
+        g[name], q[name], _ = _out_seq(None if made else grads[name], name, like, last)
+    for name, shape_, model in (("g_A", A.shape, A), ("g_D", (ch,), D),
+                                ("g_delta_bias", (ch,), delta_bias),
+                                ("g_state0", ss, grad_state)):
         if made or grads.get(name) is not None:
-            g[name], q[name], _ = _out_par(None if made else grads[name], name, u, sh)
+            g[name], q[name], _ = _out_par(None if made else grads[name], name, u, shape_,
+                                           model=model)
     out = _SCAN_GRADS.pack(*q["g_u"], *q["g_delta"], *q["g_B"], *q["g_C"], *q.get("g_z", _NONE),
                            q.get("g_A", 0), q.get("g_D", 0), q.get("g_delta_bias", 0),
                            q.get("g_state0", 0))
@@ -319,7 +315,7 @@ def selective_scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=Non
     shape, inputs, dev, (_, rows, ch, N, _) = _scan_call(
         u, delta, A, B, C, D, z, delta_bias, state, None, delta_softplus, step=True)
     new_state = state if new_state is None else new_state
-    out, os, made = _out_seq(out, "out", u, u.shape)
+    out, os, made = _out_seq(out, "out", u)
     _call(lib().ck_scan_step, dev, stream,
           (shape, inputs, CkSeq(*os), _par(new_state, "new_state", dev, (rows, ch, N))),
           (out,) if made else ())
@@ -403,8 +399,8 @@ def short_conv_forward(x, weight, bias=None, state0=None, lengths=None, activati
     [D, W]; bias: [D]; state0 and the returned state: [W - 1, B, D], the last
     inputs of each row; activation: None or "silu"."""
     shape, dev, ss, xs, w, b = _conv_call(x, weight, bias, activation)
-    y, ys, m0 = _out_seq(y, "y", x, x.shape)
-    state, st, m1 = _out_par(state, "state", x, ss, x.dtype)
+    y, ys, m0 = _out_seq(y, "y", x)
+    state, st, m1 = _out_par(state, "state", x, ss, x.dtype, state0)
     _call(lib().ck_conv_forward, dev, stream,
           (shape, xs, w, b, _par(state0, "state0", dev, ss, x.dtype),
            _par(lengths, "lengths", dev, (ss[1],), torch.int32), CkSeq(*ys), st),
@@ -420,13 +416,14 @@ def short_conv_backward(x, weight, grad_y, bias=None, state0=None, lengths=None,
     made = grads is None
     g = {} if made else grads
     have = (lambda name: None) if made else grads.get
-    g["g_x"], gx, _ = _out_seq(have("g_x"), "g_x", x, x.shape)
-    g["g_weight"], gw, _ = _out_par(have("g_weight"), "g_weight", x, weight.shape)
+    g["g_x"], gx, _ = _out_seq(have("g_x"), "g_x", x)
+    g["g_weight"], gw, _ = _out_par(have("g_weight"), "g_weight", x, weight.shape, model=weight)
     gb = gs0 = 0
     if made or grads.get("g_bias") is not None:
-        g["g_bias"], gb, _ = _out_par(have("g_bias"), "g_bias", x, (ss[2],))
+        g["g_bias"], gb, _ = _out_par(have("g_bias"), "g_bias", x, (ss[2],), model=bias)
     if made or grads.get("g_state0") is not None:
-        g["g_state0"], gs0, _ = _out_par(have("g_state0"), "g_state0", x, ss, x.dtype)
+        g["g_state0"], gs0, _ = _out_par(have("g_state0"), "g_state0", x, ss, x.dtype,
+                                         state0)
     workspace, wp, wn, m1 = _buffer(workspace, _conv_sizes(shape), x, "workspace")
     _call(lib().ck_conv_backward, dev, stream,
           (shape, xs, w, b, _par(state0, "state0", dev, ss, x.dtype),
@@ -444,7 +441,7 @@ def short_conv_step(state, x, weight, bias=None, activation=None, y=None, new_st
     the new state)."""
     shape, dev, ss, xs, w, b = _conv_call(x, weight, bias, activation, step=True)
     new_state = state if new_state is None else new_state
-    y, ys, made = _out_seq(y, "y", x, x.shape)
+    y, ys, made = _out_seq(y, "y", x)
     _call(lib().ck_conv_step, dev, stream,
           (shape, xs, w, b, _par(state, "state", dev, ss, x.dtype), CkSeq(*ys),
            _par(new_state, "new_state", dev, ss, x.dtype)), (y,) if made else ())
@@ -500,7 +497,7 @@ def dropout_forward(x, p: float, seed: int, offset: int = 0, residual=None, held
     the residual."""
     shape, dev, xs = _drop_call(x, "x", p, seed, offset, held, counter)
     rs = _NONE if residual is None else _seq(residual, "residual", x.dtype, dev, x.shape)
-    out, os, made = _out_seq(out, "out", x, x.shape)
+    out, os, made = _out_seq(out, "out", x)
     _call(lib().ck_dropout_forward, dev, stream, (shape, xs, CkSeq(*rs), CkSeq(*os)),
           (out,) if made else ())
     return out
@@ -510,7 +507,7 @@ def dropout_backward(grad_out, p: float, seed: int, offset: int = 0, held: bool 
                      counter=None, grad_x=None, stream=None) -> torch.Tensor:
     """Run ``ck_dropout_backward``: the forward's mask and scale on grad_out."""
     shape, dev, gs = _drop_call(grad_out, "grad_out", p, seed, offset, held, counter)
-    grad_x, os, made = _out_seq(grad_x, "grad_x", grad_out, grad_out.shape)
+    grad_x, os, made = _out_seq(grad_x, "grad_x", grad_out)
     _call(lib().ck_dropout_backward, dev, stream, (shape, gs, CkSeq(*os)),
           (grad_x,) if made else ())
     return grad_x
