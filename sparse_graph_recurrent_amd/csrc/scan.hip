@@ -39,15 +39,23 @@ void scan_cut(ScanDims* d, int64_t want) {
 //   - fewer: cut to about kScanGoalGroups (128: 243 against 353 with several tiles
 //     each; uncut 439).  The second pass over the steps costs 0.7 of a forward's
 //     and 0.25 of a backward's main launch.
-// Rows of unequal lengths leave CUs idle unless cut.  Windows too short to cut
-// take several tiles each (64 steps x 32 x 256 channels: 37 against 41).
-constexpr int64_t kScanFewGroups = 384, kScanCus = 256, kScanGoalGroups = 2048;
-constexpr int64_t kScanMinChunk = 64;  // steps
+// Chunks of fewer than kScanLongChunk steps pay more for their ends than they
+// spread (512 steps x 16 x 512: 126 against 138 in chunks of 32), unless the chip
+// is far from full: then what counts is that the workgroups that fit at once
+// (kScanRound of them backward) take the window in one round of shorter chunks
+// (332 steps x 3 x 64 channels: 37 against 62; 657 x 17 x 128: 70 against 87;
+// 14803 x 2 x 131: 187 against 197 in a round and a half).
+// Rows of unequal lengths leave CUs idle unless cut, and are cut finer.  Windows
+// too short to cut take several tiles each (64 steps x 32 x 256 channels: 37
+// against 41; 64 steps x 8 x 256: 36 against 32, less than what the two more
+// launches of each direction cost the host).
+constexpr int64_t kScanFewGroups = 384, kScanCus = 256, kScanGoalGroups = 2048, kScanRound = 512;
+constexpr int64_t kScanMinChunk = 16, kScanLongChunk = 64, kScanShort = 128;  // steps
 
 ScanDims scan_dims(const ck_scan_shape& s, bool ragged) {
   ScanDims d = scan_sizes(s);
   const int64_t wgs = d.P * d.G * d.B;
-  const bool is_short = s.T < 2 * kScanMinChunk;
+  const bool is_short = s.T < kScanShort;
   if (d.M == 1 && wgs <= kScanCus && (is_short || (!ragged && wgs > kScanCus * 13 / 16))) {
     d.waves = true;
   } else if (wgs < kScanFewGroups && !is_short) {
@@ -55,7 +63,11 @@ ScanDims scan_dims(const ck_scan_shape& s, bool ragged) {
     // lone wave: no more of them than about a chunk has steps
     int64_t most = 64;
     while (most * most < s.T) most *= 2;
-    scan_cut(&d, std::min(kScanGoalGroups / wgs, std::min(s.T / kScanMinChunk, most)));
+    int64_t want = std::min({kScanGoalGroups / wgs, s.T / kScanLongChunk, most});
+    const int64_t fine =
+        std::min({kScanRound * (ragged ? 2 : 1) / wgs, s.T / kScanMinChunk, most});
+    if (want * wgs < 2 * kScanRound && 2 * fine >= want) want = fine;
+    scan_cut(&d, want);
   }
   return d;
 }
