@@ -56,6 +56,7 @@ struct ScanDims {
   int64_t tiles;    // tiles of the window
   int64_t chunks, chunk_steps;  // chunks of the window (steps: a multiple of K)
   bool waves;       // several time tiles a workgroup (one chunk only)
+  bool fold;        // each chunk folds those before it; no launch joins them
 };
 
 template <typename E>
@@ -66,9 +67,10 @@ struct ScanArgs {
   int T, B, D, N, G, Dg, P;
   int chunks, chunk_steps;
   int softplus;
-  // [chunks][B][D][NP]: what a chunk makes of a zero state (adjoint), then
+  // [chunks][B][D][NP]: what a chunk makes of a zero state (adjoint), then, joined,
   // the state (adjoint) it starts from; and the sum of its dt, [chunks][B][D]
   float *edge, *dtsum;
+  int fold;  // whether each chunk sees to that itself
   // forward
   Seq<E> out;
   float* state;
@@ -342,6 +344,34 @@ __device__ __forceinline__ void fold_tiles(f32x4 (&start)[M], f32x4 (&next)[M], 
   }
 #pragma unroll
   for (int m = 0; m < M; ++m) next[m] = cur[m];
+}
+
+// The state a chunk starts from, or (not FORWARD) the adjoint: the window's first,
+// in h, folded with what the chunks walked before this one make of zero.  The
+// same sums as scan_join's, in the same order.
+template <int M, bool FORWARD, typename E>
+__device__ __forceinline__ void fold_chunks(f32x4 (&h)[M], const f32x4 (&a2)[M],
+                                            const ScanArgs<E>& s, const Place& p, int64_t row) {
+  constexpr int NP = 16 * M, kAhead = 8 / M;
+  const int64_t rows = (int64_t)s.B * s.D;
+  const int count = FORWARD ? p.chunk : s.chunks - 1 - p.chunk;
+  for (int k0 = 0; k0 < count; k0 += kAhead) {
+    f32x4 made[kAhead][M];
+    float dt[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = min(k0 + j, count - 1);
+      const int64_t at = (FORWARD ? k : s.chunks - 1 - k) * rows + row;
+      load_rows<M>(made[j], s.edge + at * NP, p.q);
+      dt[j] = s.dtsum[at];
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (k0 + j < count) {
+#pragma unroll
+        for (int m = 0; m < M; ++m) h[m] = fma_4(exp2_4(dt[j] * a2[m]), h[m], made[j][m]);
+      }
+  }
 }
 
 // Joins the chunks: edge[c] from "made of a zero state" to "starts from".

@@ -17,7 +17,7 @@ ScanDims scan_sizes(const ck_scan_shape& s) {
   d.Dg = s.D / s.G;
   d.P = (d.Dg + kScanChan - 1) / kScanChan;
   d.tiles = (s.T + d.K - 1) / d.K;
-  d.waves = false;
+  d.waves = d.fold = false;
   d.chunks = 1;
   d.chunk_steps = std::max<int64_t>(d.tiles, 1) * d.K;
   return d;
@@ -47,15 +47,21 @@ void scan_cut(ScanDims* d, int64_t want) {
 // 14803 x 2 x 131: 187 against 197 in a round and a half).
 // Rows of unequal lengths leave CUs idle unless cut, and are cut finer.  Windows
 // too short to cut take several tiles each (64 steps x 32 x 256 channels: 37
-// against 41; 64 steps x 8 x 256: 36 against 32, less than what the two more
-// launches of each direction cost the host).
+// against 41; 64 steps x 8 x 256: 36 against 28, but a launch less in each
+// direction; 100 steps x 16 x 256: 54 against 36, but x 50 x 256: 57 against 61).
+// Workgroups that run at once, or read few chunks (half of `chunks` each, 4 KB of
+// what another XCD wrote), fold the chunks before their own (256 steps x 8 x 256:
+// 39 against 44 joined by a launch; 200 x 30 x 640: 120 against 124; but 2048 x 4 x
+// 1024 in 32 chunks: 233 against 224, and 1023 x 16 x 1024 ragged, forward alone,
+// in 8: 91 against 86).
 constexpr int64_t kScanFewGroups = 384, kScanCus = 256, kScanGoalGroups = 2048, kScanRound = 512;
-constexpr int64_t kScanMinChunk = 16, kScanLongChunk = 64, kScanShort = 128;  // steps
+constexpr int64_t kScanMinChunk = 16, kScanLongChunk = 64, kScanShort = 96;  // steps
+constexpr int64_t kScanFold = 8192;  // chunks times workgroups
 
 ScanDims scan_dims(const ck_scan_shape& s, bool ragged) {
   ScanDims d = scan_sizes(s);
   const int64_t wgs = d.P * d.G * d.B;
-  const bool is_short = s.T < kScanShort;
+  const bool is_short = s.T < (2 * wgs <= kScanCus ? kScanShort : 2 * kScanLongChunk);
   if (d.M == 1 && wgs <= kScanCus && (is_short || (!ragged && wgs > kScanCus * 13 / 16))) {
     d.waves = true;
   } else if (wgs < kScanFewGroups && !is_short) {
@@ -68,6 +74,8 @@ ScanDims scan_dims(const ck_scan_shape& s, bool ragged) {
         std::min({kScanRound * (ragged ? 2 : 1) / wgs, s.T / kScanMinChunk, most});
     if (want * wgs < 2 * kScanRound && 2 * fine >= want) want = fine;
     scan_cut(&d, want);
+    const int64_t all = wgs * d.chunks;
+    d.fold = d.chunks > 1 && (all <= kScanRound || all * d.chunks <= kScanFold);
   }
   return d;
 }
@@ -186,6 +194,7 @@ ScanArgs<E> scan_args(const ck_scan_shape& s, const ScanDims& d, const ck_scan_i
   };
   a.edge = part(ws.edge);
   a.dtsum = part(ws.dtsum);
+  a.fold = d.fold;
   a.part_bc = part(ws.part_bc);
   a.part_a = part(ws.part_a);
   a.u = seq_of<const E>(in.u);

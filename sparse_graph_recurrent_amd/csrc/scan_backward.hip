@@ -181,10 +181,17 @@ __global__ __launch_bounds__(kScanThreads * TW, M < 4 && TW == 1 ? 2 : 1) void s
   for (int m = 0; m < M; ++m) ga[m] = g[m] = 0.0f;
   // Lanes without a channel hold zeros throughout, so they add nothing to gB, gC.
   if (p.active) {
-    if (s.chunks > 1)
+    if (s.chunks > 1 && !s.fold) {
       load_rows<M>(g, s.edge + ((int64_t)p.chunk * s.B * s.D + row) * NP, q);
-    else
+    } else {
       load_states<M>(g, s.gstate, row, q, s.N);
+      if (TW == 1 && s.chunks > 1) {
+        f32x4 a2[M];
+#pragma unroll
+        for (int m = 0; m < M; ++m) a2[m] = kLog2e * a1[m];
+        fold_chunks<M, false>(g, a2, s, p, row);
+      }
+    }
   }
   const float bias = s.delta_bias ? s.delta_bias[p.d] : 0.0f;
   const float skip = s.d ? s.d[p.d] : 0.0f;
@@ -504,9 +511,11 @@ void launch(const ScanDims& d, const ScanArgs<E>& a, hipStream_t stream) {
       scan_bwd_part<E, M, true><<<grid - wgs, kScanThreads, 0, stream>>>(a);
     else
       scan_bwd_part<E, M, false><<<grid - wgs, kScanThreads, 0, stream>>>(a);
-    const int64_t n = d.B * d.D * d.NP;
-    scan_join<false><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
-        a.edge, a.dtsum, a.a, a.gstate, d.B * d.D, a.D, a.N, d.NP, a.chunks);
+    if (!d.fold) {
+      const int64_t n = d.B * d.D * d.NP;
+      scan_join<false><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
+          a.edge, a.dtsum, a.a, a.gstate, d.B * d.D, a.D, a.N, d.NP, a.chunks);
+    }
   }
   int parts = a.chunks;  // partial sums of A's gradient a row
   if constexpr (M == 1) {

@@ -38,10 +38,12 @@ __global__ __launch_bounds__(kScanThreads * TW) void scan_fwd(const ScanArgs<E> 
     h[m] = 0.0f;
   }
   if constexpr (!PART) {
-    if (s.chunks > 1)
+    if (s.chunks > 1 && !s.fold) {
       load_rows<M>(h, edge, q);
-    else
+    } else {
       load_states<M>(h, s.state0, row, q, s.N);
+      if (TW == 1 && s.chunks > 1) fold_chunks<M, true>(h, a2, s, p, row);
+    }
   }
   const float bias = s.delta_bias ? s.delta_bias[p.d] : 0.0f;
   const float skip = s.d ? s.d[p.d] : 0.0f;
@@ -220,9 +222,11 @@ void launch(const ScanDims& d, const ScanArgs<E>& a, hipStream_t stream) {
   if (d.chunks > 1) {
     // (nothing follows the last chunk)
     scan_fwd<E, M, 1, false, true><<<grid - wgs, kScanThreads, 0, stream>>>(a);
-    const int64_t n = d.B * d.D * d.NP;
-    scan_join<true><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
-        a.edge, a.dtsum, a.a, a.state0, d.B * d.D, a.D, a.N, d.NP, a.chunks);
+    if (!d.fold) {
+      const int64_t n = d.B * d.D * d.NP;
+      scan_join<true><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
+          a.edge, a.dtsum, a.a, a.state0, d.B * d.D, a.D, a.N, d.NP, a.chunks);
+    }
   }
   if constexpr (M == 1) {
     if (d.waves) return launch_main<E, M, kScanFwdTW>(grid, a, stream);

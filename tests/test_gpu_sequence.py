@@ -166,6 +166,25 @@ def test_scan(case):
     scan_check(g, p, case[7])
 
 
+# Windows cut where neither all workgroups run at once nor few chunks are read, so
+# that a launch joins the chunks; and short windows of few rows, cut finely.
+JOINED = [
+    (520, 130, 16, 16, 1, "fp32", True, True, None, "time"),
+    (521, 131, 20, 5, 1, "bf16", True, True, [(37 * b) % 522 for b in range(131)], "batch"),
+    (515, 130, 6, 20, 2, "fp32", False, True, None, "time"),
+    (514, 130, 3, 33, 1, "fp16", False, True, [514 - 3 * b for b in range(130)], "time"),
+    (97, 2, 40, 16, 1, "fp32", True, True, [97, 40], "time"),
+    (129, 3, 64, 16, 1, "bf16", False, True, None, "slice"),
+]
+
+
+@pytest.mark.parametrize("case", JOINED, ids=lambda c: "-".join(map(str, c[:6])))
+def test_scan_chunks(case):
+    log(f"scan chunks {case[:8]}")
+    g, p = scan_problem(12, *case)
+    scan_check(g, p, case[7])
+
+
 def test_scan_without_optional_inputs():
     g, p = scan_problem(2, 20, 2, 64, 16, 1, "fp32", False, True, None, "time", state0=False,
                         extras=False)
