@@ -180,13 +180,28 @@ def _first(t, name: str, dims) -> int:
     return t.get_device()
 
 
-def _out_seq(t, name: str, like: torch.Tensor, last: int = 1):
-    """(tensor, its ck_seq fields, made here) of an output of like's shape: the
+def _fresh(like: torch.Tensor) -> torch.Tensor:
+    """A new contiguous tensor of like's shape and type."""
+    # (a copy of a tensor's layout is the quicker of the two calls)
+    return torch.empty_like(like) if like.is_contiguous() else like.new_empty(like.shape)
+
+
+def _dense(shape, inner: int):
+    """(stride_t, stride_b) of a contiguous [T, B, ...] tensor, `inner` elements a
+    row, or of a step's [B, ...]; 0 where there is but one."""
+    if len(shape) == 2:
+        return 0, inner if shape[0] > 1 else 0
+    return inner * shape[1] if shape[0] > 1 else 0, inner if shape[1] > 1 else 0
+
+
+def _out_seq(t, name: str, like: torch.Tensor):
+    """(tensor, its ck_seq, made here) of an output of like's [.., D] shape: the
     caller's, checked, or a new contiguous one."""
-    made = t is None
-    if made:  # (a copy of a tensor's layout is the quicker of the two calls)
-        t = torch.empty_like(like) if like.is_contiguous() else like.new_empty(like.shape)
-    return t, _seq(t, name, like.dtype, like.get_device(), like.shape, last), made
+    shape = like.shape
+    if t is None:
+        t = _fresh(like)
+        return t, CkSeq(t.data_ptr(), *_dense(shape, shape[-1])), True
+    return t, CkSeq(*_seq(t, name, like.dtype, like.get_device(), shape)), False
 
 
 def _out_par(t, name: str, like: torch.Tensor, shape, dtype=torch.float32, model=None):
@@ -263,7 +278,7 @@ def selective_scan_forward(u, delta, A, B, C, D=None, z=None, delta_bias=None, s
     saved, sp, _, m2 = _buffer(saved, sb, u, "saved") if save or saved is not None else \
         (None, None, 0, False)
     workspace, wp, wn, m3 = _buffer(workspace, fb, u, "workspace")
-    _call(lib().ck_scan_forward, dev, stream, (shape, inputs, CkSeq(*os), st, sp, wp, wn),
+    _call(lib().ck_scan_forward, dev, stream, (shape, inputs, os, st, sp, wp, wn),
           (out if m0 else None, state if m1 else None, saved if m2 else None,
            workspace if m3 else None))
     return out, state, saved, workspace
@@ -275,7 +290,7 @@ def selective_scan_backward(u, delta, A, B, C, saved, grad_out, D=None, z=None, 
     """Run ``ck_scan_backward``; returns the gradients (overwritten) by the
     names g_u, g_delta, g_A, g_B, g_C, g_D, g_delta_bias, g_state0 and, with a
     gate, g_z."""
-    shape, inputs, dev, (T, rows, ch, N, _) = _scan_call(
+    shape, inputs, dev, (T, rows, ch, N, G) = _scan_call(
         u, delta, A, B, C, D, z, delta_bias, None, lengths, delta_softplus)
     sb, _, wb = _scan_sizes(shape)
     if sb and saved is None:
@@ -285,20 +300,34 @@ def selective_scan_backward(u, delta, A, B, C, saved, grad_out, D=None, z=None, 
     go = CkSeq(*_seq(grad_out, "grad_out", u.dtype, dev, u.shape))
     gs = _par(grad_state, "grad_state", dev, ss)
     made = grads is None
-    g = {} if made else grads
-    q = {}
-    for name, like, last in (("g_u", u, 1), ("g_delta", delta, 1), ("g_B", B, 2), ("g_C", C, 2)) \
-            + ((("g_z", z, 1),) if z is not None else ()):
-        g[name], q[name], _ = _out_seq(None if made else grads[name], name, like, last)
-    for name, shape_, model in (("g_A", A.shape, A), ("g_D", (ch,), D),
-                                ("g_delta_bias", (ch,), delta_bias),
-                                ("g_state0", ss, grad_state)):
-        if made or grads.get(name) is not None:
-            g[name], q[name], _ = _out_par(None if made else grads[name], name, u, shape_,
-                                           model=model)
-    out = _SCAN_GRADS.pack(*q["g_u"], *q["g_delta"], *q["g_B"], *q["g_C"], *q.get("g_z", _NONE),
-                           q.get("g_A", 0), q.get("g_D", 0), q.get("g_delta_bias", 0),
-                           q.get("g_state0", 0))
+    if made:
+        g = {"g_u": _fresh(u), "g_delta": _fresh(delta), "g_B": _fresh(B), "g_C": _fresh(C),
+             "g_A": torch.empty_like(A), "g_D": D, "g_delta_bias": delta_bias,
+             "g_state0": grad_state}
+        for name, shape_ in (("g_D", (ch,)), ("g_delta_bias", (ch,)), ("g_state0", ss)):
+            like = g[name]
+            g[name] = A.new_empty(shape_) if like is None else torch.empty_like(like)
+        rows_, bcs = _dense(u.shape, ch), _dense(u.shape, G * N)
+        gz = _NONE
+        if z is not None:
+            g["g_z"] = _fresh(z)
+            gz = (g["g_z"].data_ptr(), *rows_)
+        out = _SCAN_GRADS.pack(
+            g["g_u"].data_ptr(), *rows_, g["g_delta"].data_ptr(), *rows_,
+            g["g_B"].data_ptr(), *bcs, g["g_C"].data_ptr(), *bcs, *gz,
+            g["g_A"].data_ptr(), g["g_D"].data_ptr(), g["g_delta_bias"].data_ptr(),
+            g["g_state0"].data_ptr())
+    else:
+        g = grads
+        out = _SCAN_GRADS.pack(
+            *_seq(g["g_u"], "g_u", u.dtype, dev, u.shape),
+            *_seq(g["g_delta"], "g_delta", u.dtype, dev, u.shape),
+            *_seq(g["g_B"], "g_B", u.dtype, dev, B.shape, 2),
+            *_seq(g["g_C"], "g_C", u.dtype, dev, B.shape, 2),
+            *(_NONE if z is None else _seq(g["g_z"], "g_z", u.dtype, dev, u.shape)),
+            _par(g.get("g_A"), "g_A", dev, A.shape), _par(g.get("g_D"), "g_D", dev, (ch,)),
+            _par(g.get("g_delta_bias"), "g_delta_bias", dev, (ch,)),
+            _par(g.get("g_state0"), "g_state0", dev, ss))
     workspace, wp, wn, m1 = _buffer(workspace, wb, u, "workspace")
     _call(lib().ck_scan_backward, dev, stream, (shape, inputs, sp, go, gs, out, wp, wn),
           (tuple(g.values()) if made else ()) + ((workspace,) if m1 else ()))
@@ -317,7 +346,7 @@ def selective_scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=Non
     new_state = state if new_state is None else new_state
     out, os, made = _out_seq(out, "out", u)
     _call(lib().ck_scan_step, dev, stream,
-          (shape, inputs, CkSeq(*os), _par(new_state, "new_state", dev, (rows, ch, N))),
+          (shape, inputs, os, _par(new_state, "new_state", dev, (rows, ch, N))),
           (out,) if made else ())
     return out, new_state
 
@@ -403,7 +432,7 @@ def short_conv_forward(x, weight, bias=None, state0=None, lengths=None, activati
     state, st, m1 = _out_par(state, "state", x, ss, x.dtype, state0)
     _call(lib().ck_conv_forward, dev, stream,
           (shape, xs, w, b, _par(state0, "state0", dev, ss, x.dtype),
-           _par(lengths, "lengths", dev, (ss[1],), torch.int32), CkSeq(*ys), st),
+           _par(lengths, "lengths", dev, (ss[1],), torch.int32), ys, st),
           (y if m0 else None, state if m1 else None))
     return y, state
 
@@ -429,7 +458,7 @@ def short_conv_backward(x, weight, grad_y, bias=None, state0=None, lengths=None,
           (shape, xs, w, b, _par(state0, "state0", dev, ss, x.dtype),
            _par(lengths, "lengths", dev, (ss[1],), torch.int32),
            CkSeq(*_seq(grad_y, "grad_y", x.dtype, dev, x.shape)),
-           _par(grad_state, "grad_state", dev, ss, x.dtype), CkSeq(*gx), gw, gb, gs0, wp, wn),
+           _par(grad_state, "grad_state", dev, ss, x.dtype), gx, gw, gb, gs0, wp, wn),
           (tuple(g.values()) if made else ()) + ((workspace,) if m1 else ()))
     return g
 
@@ -443,7 +472,7 @@ def short_conv_step(state, x, weight, bias=None, activation=None, y=None, new_st
     new_state = state if new_state is None else new_state
     y, ys, made = _out_seq(y, "y", x)
     _call(lib().ck_conv_step, dev, stream,
-          (shape, xs, w, b, _par(state, "state", dev, ss, x.dtype), CkSeq(*ys),
+          (shape, xs, w, b, _par(state, "state", dev, ss, x.dtype), ys,
            _par(new_state, "new_state", dev, ss, x.dtype)), (y,) if made else ())
     return y, new_state
 
@@ -498,7 +527,7 @@ def dropout_forward(x, p: float, seed: int, offset: int = 0, residual=None, held
     shape, dev, xs = _drop_call(x, "x", p, seed, offset, held, counter)
     rs = _NONE if residual is None else _seq(residual, "residual", x.dtype, dev, x.shape)
     out, os, made = _out_seq(out, "out", x)
-    _call(lib().ck_dropout_forward, dev, stream, (shape, xs, CkSeq(*rs), CkSeq(*os)),
+    _call(lib().ck_dropout_forward, dev, stream, (shape, xs, CkSeq(*rs), os),
           (out,) if made else ())
     return out
 
@@ -508,7 +537,7 @@ def dropout_backward(grad_out, p: float, seed: int, offset: int = 0, held: bool 
     """Run ``ck_dropout_backward``: the forward's mask and scale on grad_out."""
     shape, dev, gs = _drop_call(grad_out, "grad_out", p, seed, offset, held, counter)
     grad_x, os, made = _out_seq(grad_x, "grad_x", grad_out)
-    _call(lib().ck_dropout_backward, dev, stream, (shape, gs, CkSeq(*os)),
+    _call(lib().ck_dropout_backward, dev, stream, (shape, gs, os),
           (grad_x,) if made else ())
     return grad_x
 
