@@ -6,8 +6,9 @@
 //   h_t  = a_t h_{t-1} + dt_t B_t u_t    y_t = C_t . h_t + D u_t    out = y silu(z)
 //
 // Layout.  A wave owns 16 channels and walks the steps in tiles of K: lane
-// (c, q) = (lane % 16, lane / 16) holds states 16 m + 4 q + r (r < 4, m < M) of
-// channel c.  The per-channel work of a step (loads, softplus, gate, store) is
+// (c, q) = (lane % 16, lane / 16) holds states 16 m + R q + r (r < R, m < M) of
+// channel c; R = 4, but 2 for up to 8 states (2048 steps x 8 x 2048 channels x 8
+// states: 193 + 343 us against 212 + 495 with half of each lane's states empty).  The per-channel work of a step (loads, softplus, gate, store) is
 // done once, by the lane (c, q) with t % 4 = q, and the channel's other lanes
 // read its dt and dt u from LDS, four steps an access.  What bounds the kernels
 // is the vector ALU: exponentials take 8.5 cycles a wave, plain fp32
@@ -31,6 +32,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "ck.h"
 #include "ck_internal.h"
 #include "sequence.h"
@@ -44,14 +47,18 @@ constexpr int kScanThreads = 4 * kScanChan;   // threads per time tile (4 waves)
 constexpr int kScanFwdTW = 4, kScanBwdTW = 2;
 constexpr int64_t kScanMaxN = 64;
 
-// Steps per tile for M blocks of 16 states: a lane of the backward holds a_t
-// and h_{t-1} of a whole tile in registers (8 K M values).
-constexpr int scan_tile(int M) { return M == 1 ? 8 : 4; }
+// Steps per tile for NP padded states: a lane of the backward holds a_t and
+// h_{t-1} of a whole tile in registers (K NP / 2 values).
+constexpr int scan_tile(int NP) { return NP <= 16 ? 8 : 4; }
+// States are padded to NP = 8, 16, 32 or 64, in blocks of scan_lane states on
+// each of a wave's 4 rows of lanes.
+constexpr int scan_lane(int NP) { return NP < 16 ? NP / 4 : 4; }
+constexpr int scan_blocks(int NP) { return NP < 16 ? 1 : NP / 16; }
 
 // Sizes that both directions share.
 struct ScanDims {
   int64_t T, B, D, N, G;
-  int M, NP, K;     // blocks of 16 states, padded states (16 M), steps per tile
+  int NP, K;        // padded states, steps per tile
   int64_t Dg, P;    // channels per group, workgroups per group
   int64_t tiles;    // tiles of the window
   int64_t chunks, chunk_steps;  // chunks of the window (steps: a multiple of K)
@@ -164,53 +171,70 @@ struct Walk {
 };
 
 using f32x4 = float __attribute__((ext_vector_type(4)));
+using f32x2 = float __attribute__((ext_vector_type(2)));
 
-// The lane's states: f32x4[M], block m holding states 16 m + 4 q + r.
-template <int M>
-__device__ __forceinline__ void load_rows(f32x4 (&v)[M], const float* p, int q) {
+// The lane's states: States<NP>[M], block m holding states 16 m + R q + r.
+template <int NP>
+using States = std::conditional_t<scan_lane(NP) == 4, f32x4, f32x2>;
+
+template <int NP>
+__device__ __forceinline__ void load_rows(States<NP> (&v)[scan_blocks(NP)], const float* p, int q) {
 #pragma unroll
-  for (int m = 0; m < M; ++m) v[m] = *reinterpret_cast<const f32x4*>(p + 16 * m + 4 * q);
+  for (int m = 0; m < scan_blocks(NP); ++m)
+    v[m] = *reinterpret_cast<const States<NP>*>(p + 16 * m + scan_lane(NP) * q);
 }
-template <int M>
-__device__ __forceinline__ void store_rows(float* p, const f32x4 (&v)[M], int q) {
+template <int NP>
+__device__ __forceinline__ void store_rows(float* p, const States<NP> (&v)[scan_blocks(NP)],
+                                           int q) {
 #pragma unroll
-  for (int m = 0; m < M; ++m) *reinterpret_cast<f32x4*>(p + 16 * m + 4 * q) = v[m];
+  for (int m = 0; m < scan_blocks(NP); ++m)
+    *reinterpret_cast<States<NP>*>(p + 16 * m + scan_lane(NP) * q) = v[m];
 }
 // From and to [rows][N] arrays of the caller (N need not be padded); 0 if absent.
-template <int M>
-__device__ __forceinline__ void load_states(f32x4 (&v)[M], const float* s, int64_t row, int q,
-                                            int N) {
+template <int NP>
+__device__ __forceinline__ void load_states(States<NP> (&v)[scan_blocks(NP)], const float* s,
+                                            int64_t row, int q, int N) {
 #pragma unroll
-  for (int m = 0; m < M; ++m)
+  for (int m = 0; m < scan_blocks(NP); ++m)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int n = 16 * m + 4 * q + r;
+    for (int r = 0; r < scan_lane(NP); ++r) {
+      const int n = 16 * m + scan_lane(NP) * q + r;
       v[m][r] = s && n < N ? s[row * N + n] : 0.0f;
     }
 }
-template <int M>
-__device__ __forceinline__ void store_states(const f32x4 (&v)[M], float* s, int64_t row, int q,
-                                             int N) {
+template <int NP>
+__device__ __forceinline__ void store_states(const States<NP> (&v)[scan_blocks(NP)], float* s,
+                                             int64_t row, int q, int N) {
 #pragma unroll
-  for (int m = 0; m < M; ++m)
+  for (int m = 0; m < scan_blocks(NP); ++m)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int n = 16 * m + 4 * q + r;
+    for (int r = 0; r < scan_lane(NP); ++r) {
+      const int n = 16 * m + scan_lane(NP) * q + r;
       if (n < N) s[row * N + n] = v[m][r];
     }
 }
 
-__device__ __forceinline__ f32x4 exp2_4(f32x4 x) {
-  return f32x4{exp2_hw(x[0]), exp2_hw(x[1]), exp2_hw(x[2]), exp2_hw(x[3])};
+template <typename V>
+__device__ __forceinline__ V exp2_v(V x) {
+  V y;
+#pragma unroll
+  for (int r = 0; r < (int)(sizeof(V) / 4); ++r) y[r] = exp2_hw(x[r]);
+  return y;
 }
-__device__ __forceinline__ f32x4 fma_4(f32x4 a, f32x4 b, f32x4 c) {
-  return f32x4{fmaf(a[0], b[0], c[0]), fmaf(a[1], b[1], c[1]), fmaf(a[2], b[2], c[2]),
-               fmaf(a[3], b[3], c[3])};
+template <typename V>
+__device__ __forceinline__ V fma_v(V a, V b, V c) {
+  V y;
+#pragma unroll
+  for (int r = 0; r < (int)(sizeof(V) / 4); ++r) y[r] = fmaf(a[r], b[r], c[r]);
+  return y;
 }
 
 // sum of a[r] b[r] added to c, one operation a state
-__device__ __forceinline__ float dot_add(f32x4 a, f32x4 b, float c) {
-  return fmaf(a[3], b[3], fmaf(a[2], b[2], fmaf(a[1], b[1], fmaf(a[0], b[0], c))));
+template <typename V>
+__device__ __forceinline__ float dot_add(V a, V b, float c) {
+#pragma unroll
+  for (int r = 0; r < (int)(sizeof(V) / 4); ++r) c = fmaf(a[r], b[r], c);
+  return c;
 }
 
 // x + y after the swap of their halves (rows): lanes of the lower half (even
@@ -256,26 +280,27 @@ struct StepsLds {
 };
 
 // The workgroup's B and C over its KT steps as fp32 rows [KT][NP] in LDS, 0 past
-// the text's end or N.  A thread moves one value of B or of C (M < 4), or one
-// of each: loaded a tile ahead, stored behind the tile before.
-template <typename E, int M, int TW>
+// the text's end or N.  A thread moves one value of B or of C (NP < 64; with 8 half
+// of them move none), or one of each: loaded a tile ahead, stored behind the tile before.
+template <typename E, int NP, int TW>
 struct TileBC {
-  static constexpr int NP = 16 * M, KT = scan_tile(M) * TW, kRows = KT * NP;
+  static constexpr int KT = scan_tile(NP) * TW, kRows = KT * NP;
   static constexpr int kThreads = kScanThreads * TW;
   static constexpr bool kBoth = kRows == kThreads;
-  static_assert(kBoth || 2 * kRows == kThreads, "each thread has its share");
+  static_assert(kBoth || 2 * kRows <= kThreads, "each thread has its share");
 
   const char *b, *c;   // the tiles' first step (uniform)
   uint32_t bo, co;     // the thread's byte offsets from it
   uint32_t bstep, cstep;
   int ts, e;           // its step of the tiles, its place in LDS
-  bool mine, is_c;
+  bool mine, is_c, spare;
   E vb, vc;
 
   __device__ __forceinline__ TileBC(const ScanArgs<E>& s, const Place& p, int t) {
     const int tid = threadIdx.x;
     // (uniform: a wave moves values of B or of C)
     is_c = !kBoth && __builtin_amdgcn_readfirstlane(tid) >= kRows;
+    spare = !kBoth && __builtin_amdgcn_readfirstlane(tid) >= 2 * kRows;
     e = kBoth ? tid : tid % kRows;
     ts = e / NP;
     const int n = e % NP;
@@ -296,6 +321,7 @@ struct TileBC {
   }
   // last: the last step of the text, relative to the tiles' first
   __device__ __forceinline__ void load(int last) {
+    if (NP < 16 && spare) return;
     if (last >= KT - 1) {
       vb = *reinterpret_cast<const E*>(b + bo);
       if constexpr (kBoth) vc = *reinterpret_cast<const E*>(c + co);
@@ -309,6 +335,7 @@ struct TileBC {
   }
   // rows: [2][KT][NP], B then C
   __device__ __forceinline__ void store(float* rows) const {
+    if (NP < 16 && spare) return;
     rows[(is_c ? kRows : 0) + e] = mine ? (float)vb : 0.0f;
     if constexpr (kBoth) rows[kRows + e] = mine ? (float)vc : 0.0f;
   }
@@ -323,23 +350,24 @@ __device__ __forceinline__ void zero_steps(const Seq<E>& s, const Place& p) {
 // Folds what TW tiles make of a zero state (made) and their decays into the
 // state the wave's tile starts from; next: the state behind the last of them.
 // FORWARD runs up from `start`, else down.
-template <int M, int TW, bool FORWARD>
-__device__ __forceinline__ void fold_tiles(f32x4 (&start)[M], f32x4 (&next)[M], const float* made,
+template <int NP, int TW, bool FORWARD>
+__device__ __forceinline__ void fold_tiles(States<NP> (&start)[scan_blocks(NP)],
+                                           States<NP> (&next)[scan_blocks(NP)], const float* made,
                                            const float* decay, const Place& p) {
-  constexpr int NP = 16 * M;
-  f32x4 cur[M];
+  constexpr int M = scan_blocks(NP);
+  States<NP> cur[M];
 #pragma unroll
   for (int m = 0; m < M; ++m) cur[m] = start[m];
 #pragma unroll
   for (int i = 0; i < TW; ++i) {
     const int w = FORWARD ? i : TW - 1 - i;
-    f32x4 mw[M], ew[M];
-    load_rows<M>(mw, made + (w * kScanChan + p.wc) * NP, p.q);
-    load_rows<M>(ew, decay + (w * kScanChan + p.wc) * NP, p.q);
+    States<NP> mw[M], ew[M];
+    load_rows<NP>(mw, made + (w * kScanChan + p.wc) * NP, p.q);
+    load_rows<NP>(ew, decay + (w * kScanChan + p.wc) * NP, p.q);
 #pragma unroll
     for (int m = 0; m < M; ++m) {
       if (w == p.tw) start[m] = cur[m];
-      cur[m] = fma_4(ew[m], cur[m], mw[m]);
+      cur[m] = fma_v(ew[m], cur[m], mw[m]);
     }
   }
 #pragma unroll
@@ -349,27 +377,28 @@ __device__ __forceinline__ void fold_tiles(f32x4 (&start)[M], f32x4 (&next)[M], 
 // The state a chunk starts from, or (not FORWARD) the adjoint: the window's first,
 // in h, folded with what the chunks walked before this one make of zero.  The
 // same sums as scan_join's, in the same order.
-template <int M, bool FORWARD, typename E>
-__device__ __forceinline__ void fold_chunks(f32x4 (&h)[M], const f32x4 (&a2)[M],
+template <int NP, bool FORWARD, typename E>
+__device__ __forceinline__ void fold_chunks(States<NP> (&h)[scan_blocks(NP)],
+                                            const States<NP> (&a2)[scan_blocks(NP)],
                                             const ScanArgs<E>& s, const Place& p, int64_t row) {
-  constexpr int NP = 16 * M, kAhead = 8 / M;
+  constexpr int M = scan_blocks(NP), kAhead = 8 / M;
   const int64_t rows = (int64_t)s.B * s.D;
   const int count = FORWARD ? p.chunk : s.chunks - 1 - p.chunk;
   for (int k0 = 0; k0 < count; k0 += kAhead) {
-    f32x4 made[kAhead][M];
+    States<NP> made[kAhead][M];
     float dt[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int k = min(k0 + j, count - 1);
       const int64_t at = (FORWARD ? k : s.chunks - 1 - k) * rows + row;
-      load_rows<M>(made[j], s.edge + at * NP, p.q);
+      load_rows<NP>(made[j], s.edge + at * NP, p.q);
       dt[j] = s.dtsum[at];
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
       if (k0 + j < count) {
 #pragma unroll
-        for (int m = 0; m < M; ++m) h[m] = fma_4(exp2_4(dt[j] * a2[m]), h[m], made[j][m]);
+        for (int m = 0; m < M; ++m) h[m] = fma_v(exp2_v(dt[j] * a2[m]), h[m], made[j][m]);
       }
   }
 }

@@ -11,9 +11,8 @@ namespace {
 ScanDims scan_sizes(const ck_scan_shape& s) {
   ScanDims d;
   d.T = s.T; d.B = s.B; d.D = s.D; d.N = s.N; d.G = s.G;
-  d.M = s.N <= 16 ? 1 : s.N <= 32 ? 2 : 4;
-  d.NP = 16 * d.M;
-  d.K = scan_tile(d.M);
+  d.NP = s.N <= 8 ? 8 : s.N <= 16 ? 16 : s.N <= 32 ? 32 : 64;
+  d.K = scan_tile(d.NP);
   d.Dg = s.D / s.G;
   d.P = (d.Dg + kScanChan - 1) / kScanChan;
   d.tiles = (s.T + d.K - 1) / d.K;
@@ -62,7 +61,7 @@ ScanDims scan_dims(const ck_scan_shape& s, bool ragged) {
   ScanDims d = scan_sizes(s);
   const int64_t wgs = d.P * d.G * d.B;
   const bool is_short = s.T < (2 * wgs <= kScanCus ? kScanShort : 2 * kScanLongChunk);
-  if (d.M == 1 && wgs <= kScanCus && (is_short || (!ragged && wgs > kScanCus * 13 / 16))) {
+  if (d.NP <= 16 && wgs <= kScanCus && (is_short || (!ragged && wgs > kScanCus * 13 / 16))) {
     d.waves = true;
   } else if (wgs < kScanFewGroups && !is_short) {
     // chunks are joined one after the other, eight in about a step's time of a

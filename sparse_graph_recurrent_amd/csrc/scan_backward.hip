@@ -70,9 +70,9 @@ __device__ __forceinline__ float channel_reduce16(float (&v)[16], int c) {
 
 // The adjoint's share of a chunk: what it hands to the chunk before, given
 // nothing from the one behind, and the sum of the chunk's dt.
-template <typename E, int M, bool GATE>
+template <typename E, int NP, bool GATE>
 __global__ __launch_bounds__(kScanThreads) void scan_bwd_part(const ScanArgs<E> s) {
-  constexpr int K = scan_tile(M), KQ = K / 4, NP = 16 * M;
+  constexpr int M = scan_blocks(NP), K = scan_tile(NP), KQ = K / 4;
   __shared__ __align__(16) float lds_dt[4][StepsLds::kFloats], lds_dy[4][StepsLds::kFloats];
   __shared__ __align__(16) float lds_bc[2][2 * K * NP];
   Place p = scan_place(s);
@@ -84,8 +84,8 @@ __global__ __launch_bounds__(kScanThreads) void scan_bwd_part(const ScanArgs<E> 
   const int q = p.q, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float *ldt = lds_dt[wave], *ldy = lds_dy[wave];
   const int64_t row = (int64_t)p.b * s.D + p.d;
-  f32x4 a2[M], g[M];
-  load_states<M>(a2, s.a, p.d, q, s.N);
+  States<NP> a2[M], g[M];
+  load_states<NP>(a2, s.a, p.d, q, s.N);
 #pragma unroll
   for (int m = 0; m < M; ++m) {
     a2[m] *= kLog2e;
@@ -97,7 +97,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_bwd_part(const ScanArgs<E> 
     const int tl = p.t0 + (p.te - 1 - p.t0) / K * K;
     Walk<const E> wd(s.delta, tl, p.b, q, p.d), wg(s.go, tl, p.b, q, p.d);
     Walk<const E> wz(GATE ? s.z : s.go, tl, p.b, q, p.d);
-    TileBC<E, M, 1> bc(s, p, tl);
+    TileBC<E, NP, 1> bc(s, p, tl);
     E de[KQ], go[KQ], z[KQ];
     auto fetch = [&](int last) {
       wd.load(de, q, last);
@@ -142,11 +142,11 @@ __global__ __launch_bounds__(kScanThreads) void scan_bwd_part(const ScanArgs<E> 
         const f32x4 d4 = StepsLds::get(ldt, p.c, i), y4 = StepsLds::get(ldy, p.c, i);
 #pragma unroll
         for (int j = 3; j >= 0; --j) {
-          f32x4 c4[M];
-          load_rows<M>(c4, lc + (4 * i + j) * NP, q);
+          States<NP> c4[M];
+          load_rows<NP>(c4, lc + (4 * i + j) * NP, q);
 #pragma unroll
           for (int m = 0; m < M; ++m)
-            g[m] = exp2_4(d4[j] * a2[m]) * fma_4(c4[m], f32x4(y4[j]), g[m]);
+            g[m] = exp2_v(d4[j] * a2[m]) * fma_v(c4[m], States<NP>(y4[j]), g[m]);
         }
       }
       if (more) bc.store(lds_bc[buf ^ 1]);
@@ -156,13 +156,14 @@ __global__ __launch_bounds__(kScanThreads) void scan_bwd_part(const ScanArgs<E> 
   dtsum = rows_sum(dtsum);
   if (!p.active) return;
   const int64_t at = (int64_t)p.chunk * s.B * s.D + row;
-  store_rows<M>(s.edge + at * NP, g, q);
+  store_rows<NP>(s.edge + at * NP, g, q);
   if (q == 0) s.dtsum[at] = dtsum;
 }
 
-template <typename E, int M, int TW, bool GATE>
-__global__ __launch_bounds__(kScanThreads * TW, M < 4 && TW == 1 ? 2 : 1) void scan_bwd(const ScanArgs<E> s) {
-  constexpr int K = scan_tile(M), KQ = K / 4, NP = 16 * M, KT = K * TW;
+template <typename E, int NP, int TW, bool GATE>
+__global__ __launch_bounds__(kScanThreads * TW, NP < 64 && TW == 1 ? 2 : 1) void scan_bwd(const ScanArgs<E> s) {
+  constexpr int M = scan_blocks(NP), K = scan_tile(NP), KQ = K / 4, KT = K * TW;
+  constexpr int R = scan_lane(NP), S = 8 / R;
   __shared__ __align__(16) float lds_dt[4 * TW][StepsLds::kFloats];
   __shared__ __align__(16) float lds_x[4 * TW][StepsLds::kFloats];
   __shared__ __align__(16) float lds_dy[4 * TW][StepsLds::kFloats];
@@ -175,21 +176,21 @@ __global__ __launch_bounds__(kScanThreads * TW, M < 4 && TW == 1 ? 2 : 1) void s
   const int q = p.q, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float *ldt = lds_dt[wave], *lx = lds_x[wave], *ldy = lds_dy[wave];
   const int64_t row = (int64_t)p.b * s.D + p.d;
-  f32x4 a1[M], ga[M], g[M];  // g: the adjoint the workgroup's tiles start from
-  load_states<M>(a1, p.active ? s.a : nullptr, p.d, q, s.N);
+  States<NP> a1[M], ga[M], g[M];  // g: the adjoint the workgroup's tiles start from
+  load_states<NP>(a1, p.active ? s.a : nullptr, p.d, q, s.N);
 #pragma unroll
   for (int m = 0; m < M; ++m) ga[m] = g[m] = 0.0f;
   // Lanes without a channel hold zeros throughout, so they add nothing to gB, gC.
   if (p.active) {
     if (s.chunks > 1 && !s.fold) {
-      load_rows<M>(g, s.edge + ((int64_t)p.chunk * s.B * s.D + row) * NP, q);
+      load_rows<NP>(g, s.edge + ((int64_t)p.chunk * s.B * s.D + row) * NP, q);
     } else {
-      load_states<M>(g, s.gstate, row, q, s.N);
+      load_states<NP>(g, s.gstate, row, q, s.N);
       if (TW == 1 && s.chunks > 1) {
-        f32x4 a2[M];
+        States<NP> a2[M];
 #pragma unroll
         for (int m = 0; m < M; ++m) a2[m] = kLog2e * a1[m];
-        fold_chunks<M, false>(g, a2, s, p, row);
+        fold_chunks<NP, false>(g, a2, s, p, row);
       }
     }
   }
@@ -204,11 +205,11 @@ __global__ __launch_bounds__(kScanThreads * TW, M < 4 && TW == 1 ? 2 : 1) void s
     Walk<const E> wg(s.go, tw0, p.b, q, p.d), wz(GATE ? s.z : s.u, tw0, p.b, q, p.d);
     Walk<E> ou(s.gu, tw0, p.b, q, p.d), od(s.gdelta, tw0, p.b, q, p.d);
     Walk<E> oz(GATE ? s.gz : s.gu, tw0, p.b, q, p.d);
-    TileBC<E, M, TW> bc(s, p, tl);
+    TileBC<E, NP, TW> bc(s, p, tl);
     const int64_t ck_step = (int64_t)s.B * s.D * NP;
     const float* ck = s.saved + (int64_t)(tw0 / K) * ck_step + row * NP;
     E eu[KQ], ede[KQ], ez[KQ], ego[KQ];
-    f32x4 h[M], hn[M];  // states; those the next tile starts from
+    States<NP> h[M], hn[M];  // states; those the next tile starts from
 #pragma unroll
     for (int m = 0; m < M; ++m) hn[m] = 0.0f;
     // the wave's tile, whose last step with text is `last` (negative: none)
@@ -218,7 +219,7 @@ __global__ __launch_bounds__(kScanThreads * TW, M < 4 && TW == 1 ? 2 : 1) void s
       wd.load(ede, q, last);
       wg.load(ego, q, last);
       if constexpr (GATE) wz.load(ez, q, last);
-      if (p.active) load_rows<M>(hn, ck, q);
+      if (p.active) load_rows<NP>(hn, ck, q);
     };
     fetch(p.te - 1 - tw0);
     bc.load(p.te - 1 - tl);
@@ -278,7 +279,7 @@ __global__ __launch_bounds__(kScanThreads * TW, M < 4 && TW == 1 ? 2 : 1) void s
       const float *lb = lds_bc[buf] + p.tw * K * NP, *lc = lb + KT * NP;
 
       // the tile's states again, from its first
-      f32x4 a[K][M], before[K][M];  // decays, and the states before each step
+      States<NP> a[K][M], before[K][M];  // decays, and the states before each step
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < KQ; ++i) {
@@ -287,15 +288,15 @@ __global__ __launch_bounds__(kScanThreads * TW, M < 4 && TW == 1 ? 2 : 1) void s
         float acc[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          f32x4 b4[M], c4[M];
+          States<NP> b4[M], c4[M];
           float y = 0.0f;
-          load_rows<M>(b4, lb + (4 * i + j) * NP, q);
-          if constexpr (GATE) load_rows<M>(c4, lc + (4 * i + j) * NP, q);
+          load_rows<NP>(b4, lb + (4 * i + j) * NP, q);
+          if constexpr (GATE) load_rows<NP>(c4, lc + (4 * i + j) * NP, q);
 #pragma unroll
           for (int m = 0; m < M; ++m) {
-            a[4 * i + j][m] = exp2_4(d4[j] * (kLog2e * a1[m]));
+            a[4 * i + j][m] = exp2_v(d4[j] * (kLog2e * a1[m]));
             before[4 * i + j][m] = h[m];
-            h[m] = fma_4(a[4 * i + j][m], h[m], x4[j] * b4[m]);
+            h[m] = fma_v(a[4 * i + j][m], h[m], x4[j] * b4[m]);
             if constexpr (GATE) y = dot_add(c4[m], h[m], y);
           }
           acc[j] = y;
@@ -303,34 +304,34 @@ __global__ __launch_bounds__(kScanThreads * TW, M < 4 && TW == 1 ? 2 : 1) void s
         if constexpr (GATE) gzf[i] *= fmaf(skip, u[i], rows_reduce4(acc));
       }
 
-      f32x4 next[M];
+      States<NP> next[M];
       if constexpr (TW > 1) {
         // what the tile hands on of a zero adjoint
-        f32x4 mk[M], e[M];
+        States<NP> mk[M], e[M];
 #pragma unroll
         for (int m = 0; m < M; ++m) {
           mk[m] = 0.0f;
-          e[m] = exp2_4(sum * (kLog2e * a1[m]));
+          e[m] = exp2_v(sum * (kLog2e * a1[m]));
         }
 #pragma unroll
         for (int i = KQ - 1; i >= 0; --i) {
           const f32x4 y4 = StepsLds::get(ldy, p.c, i);
 #pragma unroll
           for (int j = 3; j >= 0; --j) {
-            f32x4 c4[M];
-            load_rows<M>(c4, lc + (4 * i + j) * NP, q);
+            States<NP> c4[M];
+            load_rows<NP>(c4, lc + (4 * i + j) * NP, q);
 #pragma unroll
             for (int m = 0; m < M; ++m)
-              mk[m] = a[4 * i + j][m] * fma_4(c4[m], f32x4(y4[j]), mk[m]);
+              mk[m] = a[4 * i + j][m] * fma_v(c4[m], States<NP>(y4[j]), mk[m]);
           }
         }
         const int at = (p.tw * kScanChan + p.wc) * NP;
-        store_rows<M>(&made[at], mk, q);
-        store_rows<M>(&decay[at], e, q);
+        store_rows<NP>(&made[at], mk, q);
+        store_rows<NP>(&decay[at], e, q);
       }
       if (more) bc.store(lds_bc[buf ^ 1]);
       __syncthreads();  // (and the waves' sums of the tiles before are read)
-      if constexpr (TW > 1) fold_tiles<M, TW, false>(g, next, made, decay, p);
+      if constexpr (TW > 1) fold_tiles<NP, TW, false>(g, next, made, decay, p);
 
       // and backwards: g enters a step as a_{t+1} dL/dh_{t+1}
       float v[16], gu[KQ], gd[KQ];
@@ -342,30 +343,30 @@ __global__ __launch_bounds__(kScanThreads * TW, M < 4 && TW == 1 ? 2 : 1) void s
 #pragma unroll
         for (int j = 3; j >= 0; --j) {
           const int t = 4 * i + j;
-          f32x4 b4[M], c4[M];
+          States<NP> b4[M], c4[M];
           float s1 = 0.0f, s2 = 0.0f;
-          load_rows<M>(b4, lb + t * NP, q);
-          load_rows<M>(c4, lc + t * NP, q);
+          load_rows<NP>(b4, lb + t * NP, q);
+          load_rows<NP>(c4, lc + t * NP, q);
 #pragma unroll
           for (int m = 0; m < M; ++m) {
-            const f32x4 gh = fma_4(c4[m], f32x4(y4[j]), g[m]);
-            const f32x4 vb = gh * x4[j], vc = h[m] * y4[j];
+            const States<NP> gh = fma_v(c4[m], States<NP>(y4[j]), g[m]);
+            const States<NP> vb = gh * x4[j], vc = h[m] * y4[j];
             h[m] = before[t][m];
             s1 = dot_add(gh, b4[m], s1);
             g[m] = a[t][m] * gh;
-            const f32x4 w = g[m] * h[m];
-            ga[m] = fma_4(w, f32x4(d4[j]), ga[m]);
+            const States<NP> w = g[m] * h[m];
+            ga[m] = fma_v(w, States<NP>(d4[j]), ga[m]);
             s2 = dot_add(w, a1[m], s2);
-            // values of two (step, block) pairs make 16 sums over the channels
-            const int half = (t * M + m) % 2;
+            // values of S (step, block) pairs make 16 sums over the channels
+            const int part = (t * M + m) % S;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              v[half * 8 + r] = vb[r];
-              v[half * 8 + 4 + r] = vc[r];
+            for (int r = 0; r < R; ++r) {
+              v[part * 2 * R + r] = vb[r];
+              v[part * 2 * R + R + r] = vc[r];
             }
             if constexpr (M > 1) {
               // pairs are the blocks 2 k, 2 k + 1 of a step
-              if (half == 1) {
+              if (part == 1) {
                 const int kind = p.c / 4 % 2, blk = m - 1 + p.c / 8;
                 red[wave][(t * 2 + kind) * NP + 16 * blk + 4 * q + p.c % 4] =
                     channel_reduce16(v, p.c);
@@ -373,10 +374,10 @@ __global__ __launch_bounds__(kScanThreads * TW, M < 4 && TW == 1 ? 2 : 1) void s
             }
           }
           if constexpr (M == 1) {
-            // pairs are the steps t + 1 and t (t even)
-            if (t % 2 == 0) {
-              const int kind = p.c / 4 % 2;
-              red[wave][((t + p.c / 8) * 2 + kind) * NP + 4 * q + p.c % 4] =
+            // the steps t .. t + S - 1
+            if (t % S == 0) {
+              const int kind = p.c / R % 2;
+              red[wave][((t + p.c / (2 * R)) * 2 + kind) * NP + R * q + p.c % R] =
                   channel_reduce16(v, p.c);
             }
           }
@@ -420,7 +421,7 @@ __global__ __launch_bounds__(kScanThreads * TW, M < 4 && TW == 1 ? 2 : 1) void s
     zero_steps(s.gu, p);
     zero_steps(s.gdelta, p);
     if constexpr (GATE) zero_steps(s.gz, p);
-    if (s.gstate0 && p.chunk == 0 && p.active) store_states<M>(g, s.gstate0, row, q, s.N);
+    if (s.gstate0 && p.chunk == 0 && p.active) store_states<NP>(g, s.gstate0, row, q, s.N);
   }
   if (!p.active) return;
   // (with several tiles a workgroup there is one chunk, and tw in its place)
@@ -428,7 +429,7 @@ __global__ __launch_bounds__(kScanThreads * TW, M < 4 && TW == 1 ? 2 : 1) void s
 #pragma unroll
   for (int m = 0; m < M; ++m)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) pa[16 * m + 4 * q + r] = ga[m][r];
+    for (int r = 0; r < R; ++r) pa[16 * m + R * q + r] = ga[m][r];
   gskip = rows_sum(gskip);
   gbias = rows_sum(gbias);
   if (q == 0) {
@@ -495,22 +496,22 @@ __global__ __launch_bounds__(256) void scan_sums(const ScanArgs<E> s, int NP, in
     sum_bc(s, NP, (int64_t)(blockIdx.x - a_wgs) * 256 + threadIdx.x);
 }
 
-template <typename E, int M, int TW>
+template <typename E, int NP, int TW>
 void launch_main(unsigned grid, const ScanArgs<E>& a, hipStream_t stream) {
   if (a.z.p)
-    scan_bwd<E, M, TW, true><<<grid, kScanThreads * TW, 0, stream>>>(a);
+    scan_bwd<E, NP, TW, true><<<grid, kScanThreads * TW, 0, stream>>>(a);
   else
-    scan_bwd<E, M, TW, false><<<grid, kScanThreads * TW, 0, stream>>>(a);
+    scan_bwd<E, NP, TW, false><<<grid, kScanThreads * TW, 0, stream>>>(a);
 }
 
-template <typename E, int M>
+template <typename E, int NP>
 void launch(const ScanDims& d, const ScanArgs<E>& a, hipStream_t stream) {
   const unsigned wgs = (unsigned)(d.P * d.G * d.B), grid = wgs * (unsigned)d.chunks;
   if (d.chunks > 1) {
     if (a.z.p)
-      scan_bwd_part<E, M, true><<<grid - wgs, kScanThreads, 0, stream>>>(a);
+      scan_bwd_part<E, NP, true><<<grid - wgs, kScanThreads, 0, stream>>>(a);
     else
-      scan_bwd_part<E, M, false><<<grid - wgs, kScanThreads, 0, stream>>>(a);
+      scan_bwd_part<E, NP, false><<<grid - wgs, kScanThreads, 0, stream>>>(a);
     if (!d.fold) {
       const int64_t n = d.B * d.D * d.NP;
       scan_join<false><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
@@ -518,11 +519,11 @@ void launch(const ScanDims& d, const ScanArgs<E>& a, hipStream_t stream) {
     }
   }
   int parts = a.chunks;  // partial sums of A's gradient a row
-  if constexpr (M == 1) {
+  if constexpr (NP <= 16) {
     if (d.waves) parts = kScanBwdTW;
-    if (d.waves) launch_main<E, M, kScanBwdTW>(grid, a, stream);
+    if (d.waves) launch_main<E, NP, kScanBwdTW>(grid, a, stream);
   }
-  if (!d.waves) launch_main<E, M, 1>(grid, a, stream);
+  if (!d.waves) launch_main<E, NP, 1>(grid, a, stream);
   const int64_t bc = d.T * d.B * d.G * 2 * d.NP, ae = d.D * (d.NP + 2);
   const unsigned a_wgs = (unsigned)((ae + 31) / 32);
   scan_sums<E><<<a_wgs + (unsigned)((bc + 255) / 256), 256, 0, stream>>>(a, d.NP, parts, a_wgs);
@@ -532,10 +533,11 @@ void launch(const ScanDims& d, const ScanArgs<E>& a, hipStream_t stream) {
 
 template <typename E>
 void scan_launch_backward(const ScanDims& d, const ScanArgs<E>& a, hipStream_t stream) {
-  switch (d.M) {
-    case 1: return launch<E, 1>(d, a, stream);
-    case 2: return launch<E, 2>(d, a, stream);
-    default: return launch<E, 4>(d, a, stream);
+  switch (d.NP) {
+    case 8: return launch<E, 8>(d, a, stream);
+    case 16: return launch<E, 16>(d, a, stream);
+    case 32: return launch<E, 32>(d, a, stream);
+    default: return launch<E, 64>(d, a, stream);
   }
 }
 template void scan_launch_backward<float>(const ScanDims&, const ScanArgs<float>&, hipStream_t);

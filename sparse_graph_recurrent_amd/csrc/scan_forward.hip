@@ -15,9 +15,9 @@ namespace ckhip {
 namespace {
 
 // PART: only the chunk's summary (what it makes of a zero state, sum of dt).
-template <typename E, int M, int TW, bool GATE, bool PART>
+template <typename E, int NP, int TW, bool GATE, bool PART>
 __global__ __launch_bounds__(kScanThreads * TW) void scan_fwd(const ScanArgs<E> s) {
-  constexpr int K = scan_tile(M), KQ = K / 4, NP = 16 * M, KT = K * TW;
+  constexpr int M = scan_blocks(NP), K = scan_tile(NP), KQ = K / 4, KT = K * TW;
   constexpr int kBufs = TW > 1 ? 3 : 2;  // (with one barrier amid the tile's work)
   __shared__ __align__(16) float lds_dt[4 * TW][StepsLds::kFloats];
   __shared__ __align__(16) float lds_x[4 * TW][StepsLds::kFloats];
@@ -30,8 +30,8 @@ __global__ __launch_bounds__(kScanThreads * TW) void scan_fwd(const ScanArgs<E> 
   float *ldt = lds_dt[wave], *lx = lds_x[wave];
   const int64_t row = (int64_t)p.b * s.D + p.d;
   float* edge = s.edge + ((int64_t)p.chunk * s.B * s.D + row) * NP;
-  f32x4 a2[M], h[M];  // h: the state the workgroup's tiles start from
-  load_states<M>(a2, s.a, p.d, q, s.N);
+  States<NP> a2[M], h[M];  // h: the state the workgroup's tiles start from
+  load_states<NP>(a2, s.a, p.d, q, s.N);
 #pragma unroll
   for (int m = 0; m < M; ++m) {
     a2[m] *= kLog2e;
@@ -39,10 +39,10 @@ __global__ __launch_bounds__(kScanThreads * TW) void scan_fwd(const ScanArgs<E> 
   }
   if constexpr (!PART) {
     if (s.chunks > 1 && !s.fold) {
-      load_rows<M>(h, edge, q);
+      load_rows<NP>(h, edge, q);
     } else {
-      load_states<M>(h, s.state0, row, q, s.N);
-      if (TW == 1 && s.chunks > 1) fold_chunks<M, true>(h, a2, s, p, row);
+      load_states<NP>(h, s.state0, row, q, s.N);
+      if (TW == 1 && s.chunks > 1) fold_chunks<NP, true>(h, a2, s, p, row);
     }
   }
   const float bias = s.delta_bias ? s.delta_bias[p.d] : 0.0f;
@@ -54,7 +54,7 @@ __global__ __launch_bounds__(kScanThreads * TW) void scan_fwd(const ScanArgs<E> 
     Walk<const E> wu(s.u, tw0, p.b, q, p.d), wd(s.delta, tw0, p.b, q, p.d);
     Walk<const E> wz(GATE ? s.z : s.u, tw0, p.b, q, p.d);
     Walk<E> wo(s.out, tw0, p.b, q, p.d);
-    TileBC<E, M, TW> bc(s, p, p.t0);
+    TileBC<E, NP, TW> bc(s, p, p.t0);
     E u[KQ], de[KQ], z[KQ];
     // the wave's tile, whose last step with text is `last` (negative: none)
     auto fetch = [&](int last) {
@@ -116,10 +116,10 @@ __global__ __launch_bounds__(kScanThreads * TW) void scan_fwd(const ScanArgs<E> 
       }
       const float *lb = lds_bc[buf] + p.tw * K * NP, *lc = lb + KT * NP;
 
-      f32x4 a[TW > 1 ? K : 1][M], next[M];
+      States<NP> a[TW > 1 ? K : 1][M], next[M];
       if constexpr (TW > 1) {
         // decays, and what the tile makes of a zero state
-        f32x4 mk[M], e[M];
+        States<NP> mk[M], e[M];
         float sum = 0.0f;
 #pragma unroll
         for (int m = 0; m < M; ++m) mk[m] = 0.0f;
@@ -129,27 +129,27 @@ __global__ __launch_bounds__(kScanThreads * TW) void scan_fwd(const ScanArgs<E> 
           sum += (d4[0] + d4[1]) + (d4[2] + d4[3]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            f32x4 b4[M];
-            load_rows<M>(b4, lb + (4 * i + j) * NP, q);
+            States<NP> b4[M];
+            load_rows<NP>(b4, lb + (4 * i + j) * NP, q);
 #pragma unroll
             for (int m = 0; m < M; ++m) {
-              a[4 * i + j][m] = exp2_4(d4[j] * a2[m]);
-              mk[m] = fma_4(a[4 * i + j][m], mk[m], x4[j] * b4[m]);
+              a[4 * i + j][m] = exp2_v(d4[j] * a2[m]);
+              mk[m] = fma_v(a[4 * i + j][m], mk[m], x4[j] * b4[m]);
             }
           }
         }
 #pragma unroll
-        for (int m = 0; m < M; ++m) e[m] = exp2_4(sum * a2[m]);
+        for (int m = 0; m < M; ++m) e[m] = exp2_v(sum * a2[m]);
         const int at = (p.tw * kScanChan + p.wc) * NP;
-        store_rows<M>(&made[par][at], mk, q);
-        store_rows<M>(&decay[par][at], e, q);
+        store_rows<NP>(&made[par][at], mk, q);
+        store_rows<NP>(&decay[par][at], e, q);
         if (more) bc.store(lds_bc[nbuf]);
         __syncthreads();
-        fold_tiles<M, TW, true>(h, next, made[par], decay[par], p);
+        fold_tiles<NP, TW, true>(h, next, made[par], decay[par], p);
       }
 
       if constexpr (!PART)
-        if (ck && p.active && (TW == 1 || last >= 0)) store_rows<M>(ck, h, q);
+        if (ck && p.active && (TW == 1 || last >= 0)) store_rows<NP>(ck, h, q);
       float yo[KQ];
 #pragma unroll
       for (int i = 0; i < KQ; ++i) {
@@ -157,18 +157,18 @@ __global__ __launch_bounds__(kScanThreads * TW) void scan_fwd(const ScanArgs<E> 
         const f32x4 d4 = StepsLds::get(ldt, p.c, i), x4 = StepsLds::get(lx, p.c, i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          f32x4 b4[M], c4[M];
+          States<NP> b4[M], c4[M];
           float y = 0.0f;
-          load_rows<M>(b4, lb + (4 * i + j) * NP, q);
-          if constexpr (!PART) load_rows<M>(c4, lc + (4 * i + j) * NP, q);
+          load_rows<NP>(b4, lb + (4 * i + j) * NP, q);
+          if constexpr (!PART) load_rows<NP>(c4, lc + (4 * i + j) * NP, q);
 #pragma unroll
           for (int m = 0; m < M; ++m) {
-            f32x4 am;
+            States<NP> am;
             if constexpr (TW > 1)
               am = a[4 * i + j][m];
             else
-              am = exp2_4(d4[j] * a2[m]);
-            h[m] = fma_4(am, h[m], x4[j] * b4[m]);
+              am = exp2_v(d4[j] * a2[m]);
+            h[m] = fma_v(am, h[m], x4[j] * b4[m]);
             if constexpr (!PART) y = dot_add(c4[m], h[m], y);
           }
           acc[j] = y;
@@ -197,51 +197,52 @@ __global__ __launch_bounds__(kScanThreads * TW) void scan_fwd(const ScanArgs<E> 
   if constexpr (PART) {
     dtsum = rows_sum(dtsum);
     if (p.active) {
-      store_rows<M>(edge, h, q);
+      store_rows<NP>(edge, h, q);
       if (q == 0) s.dtsum[(int64_t)p.chunk * s.B * s.D + row] = dtsum;
     }
   } else if (p.tw == 0) {
     zero_steps(s.out, p);
     // the chunk in which the text ends has the final state
     if (s.state && p.active && p.chunk == min(p.len / s.chunk_steps, s.chunks - 1))
-      store_states<M>(h, s.state, row, q, s.N);
+      store_states<NP>(h, s.state, row, q, s.N);
   }
 }
 
-template <typename E, int M, int TW>
+template <typename E, int NP, int TW>
 void launch_main(unsigned grid, const ScanArgs<E>& a, hipStream_t stream) {
   if (a.z.p)
-    scan_fwd<E, M, TW, true, false><<<grid, kScanThreads * TW, 0, stream>>>(a);
+    scan_fwd<E, NP, TW, true, false><<<grid, kScanThreads * TW, 0, stream>>>(a);
   else
-    scan_fwd<E, M, TW, false, false><<<grid, kScanThreads * TW, 0, stream>>>(a);
+    scan_fwd<E, NP, TW, false, false><<<grid, kScanThreads * TW, 0, stream>>>(a);
 }
 
-template <typename E, int M>
+template <typename E, int NP>
 void launch(const ScanDims& d, const ScanArgs<E>& a, hipStream_t stream) {
   const unsigned wgs = (unsigned)(d.P * d.G * d.B), grid = wgs * (unsigned)d.chunks;
   if (d.chunks > 1) {
     // (nothing follows the last chunk)
-    scan_fwd<E, M, 1, false, true><<<grid - wgs, kScanThreads, 0, stream>>>(a);
+    scan_fwd<E, NP, 1, false, true><<<grid - wgs, kScanThreads, 0, stream>>>(a);
     if (!d.fold) {
       const int64_t n = d.B * d.D * d.NP;
       scan_join<true><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
           a.edge, a.dtsum, a.a, a.state0, d.B * d.D, a.D, a.N, d.NP, a.chunks);
     }
   }
-  if constexpr (M == 1) {
-    if (d.waves) return launch_main<E, M, kScanFwdTW>(grid, a, stream);
+  if constexpr (NP <= 16) {
+    if (d.waves) return launch_main<E, NP, kScanFwdTW>(grid, a, stream);
   }
-  launch_main<E, M, 1>(grid, a, stream);
+  launch_main<E, NP, 1>(grid, a, stream);
 }
 
 }  // namespace
 
 template <typename E>
 void scan_launch_forward(const ScanDims& d, const ScanArgs<E>& a, hipStream_t stream) {
-  switch (d.M) {
-    case 1: return launch<E, 1>(d, a, stream);
-    case 2: return launch<E, 2>(d, a, stream);
-    default: return launch<E, 4>(d, a, stream);
+  switch (d.NP) {
+    case 8: return launch<E, 8>(d, a, stream);
+    case 16: return launch<E, 16>(d, a, stream);
+    case 32: return launch<E, 32>(d, a, stream);
+    default: return launch<E, 64>(d, a, stream);
   }
 }
 template void scan_launch_forward<float>(const ScanDims&, const ScanArgs<float>&, hipStream_t);

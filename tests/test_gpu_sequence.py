@@ -178,6 +178,24 @@ JOINED = [
 ]
 
 
+# Up to 8 states, which have a layout of their own: uncut, several tiles a
+# workgroup over long and short windows, and cut.
+NARROW = [
+    (20, 400, 64, 7, 1, "bf16", True, True, None, "time"),
+    (131, 210, 64, 6, 1, "fp32", True, True, None, "time"),
+    (70, 3, 96, 8, 2, "fp16", True, True, [70, 0, 33], "batch"),
+    (333, 2, 70, 8, 1, "fp32", True, False, None, "slice"),
+    (333, 3, 40, 2, 2, "bf16", False, True, [333, 100, 1], "time"),
+]
+
+
+@pytest.mark.parametrize("case", NARROW, ids=lambda c: "-".join(map(str, c[:6])))
+def test_scan_few_states(case):
+    log(f"scan few states {case[:8]}")
+    g, p = scan_problem(13, *case)
+    scan_check(g, p, case[7])
+
+
 @pytest.mark.parametrize("case", JOINED, ids=lambda c: "-".join(map(str, c[:6])))
 def test_scan_chunks(case):
     log(f"scan chunks {case[:8]}")
