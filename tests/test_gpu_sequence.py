@@ -418,6 +418,13 @@ def test_conv(case, full):
         close(grads[k], want[k], mag[k], 24 + 2 * W + n, k)
 
 
+# rows that end within a group of channels, at the end of a workgroup's or short of one
+@pytest.mark.parametrize("D", [2, 3, 5, 6, 7, 254, 257, 259])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_conv_row_ends(D, dtype):
+    test_conv((35, 3, D, 4, dtype, True, [35, 0, 20], "slice"), True)
+
+
 @pytest.mark.parametrize("dtype,B,D,W", [("fp32", 1, 1, 4), ("bf16", 3, 64, 4),
                                          ("fp16", 2, 37, 3), ("fp32", 2, 20, 1),
                                          ("bf16", 2, 2048, 8)])
@@ -490,6 +497,18 @@ def test_dropout(T, B, D, dtype, layout, held, p):
         close(got, want, np.abs(rv) + np.abs(xv) * scale, 3, "out")
     out = sgr.dropout_forward(x, **kw)
     assert np.array_equal((out != 0).cpu().numpy(), m & (xv != 0))
+
+
+@pytest.mark.parametrize("D", [2, 3, 4, 5, 6, 7, 9, 10, 11, 12, 14, 15, 518])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_dropout_row_ends(D, dtype):
+    test_dropout(6, 3, D, dtype, "slice", True, 0.3)
+    test_dropout(6, 3, D, dtype, "time", False, 0.3)
+    # nothing past a row's end is written
+    wide = torch.full((6, 3, D + 3), 5.0, dtype=DT[dtype], device="cuda")
+    sgr.dropout_forward(torch.randn(6, 3, D, device="cuda").to(DT[dtype]), 0.3, seed=1,
+                        out=wide[:, :, 1:1 + D])
+    assert bool((wide[:, :, 0] == 5).all()) and bool((wide[:, :, 1 + D:] == 5).all())
 
 
 def test_dropout_nan_counter_in_place_and_autograd():
