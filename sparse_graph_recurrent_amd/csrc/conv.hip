@@ -44,7 +44,8 @@ struct ConvArgs {
   float* part;   // backward: [parts][W + 1][D]
   int T, B, D;
   int nv;        // channel groups of kConvV
-  int vx;        // of them per workgroup (a power of two at most 64)
+  int vx;        // of them per workgroup (at most 64)
+  int pairs;     // (row, run) pairs per workgroup: 256 / vx
   int runs;      // runs of the window
   int run;       // steps of a run (a multiple of kConvAhead)
   int silu;
@@ -57,7 +58,7 @@ struct ConvPlace {
   bool active;
 };
 
-// Workgroup: vx channel groups times 256 / vx (row, run) pairs.  A last group that
+// Workgroup: vx channel groups times `pairs` (row, run) pairs.  A last group that
 // would be short begins earlier and writes what its neighbour writes: with code of
 // its own, element by element, it made its whole wave wait (256 steps x 24 x 498
 // channels, bf16: forward 14 us against 8, backward 36 against 15).
@@ -65,10 +66,10 @@ template <typename E>
 __device__ __forceinline__ ConvPlace conv_place(const ConvArgs<E>& s) {
   ConvPlace p;
   const int vblocks = (s.nv + s.vx - 1) / s.vx;
-  const int vi = (int)(blockIdx.x % vblocks) * s.vx + ((int)threadIdx.x & (s.vx - 1));
-  const int64_t br = (int64_t)(blockIdx.x / vblocks) * (kConvThreads / s.vx) +
-                     (int)threadIdx.x / s.vx;
-  p.active = vi < s.nv && br < (int64_t)s.B * s.runs;
+  const int vi = (int)(blockIdx.x % vblocks) * s.vx + (int)threadIdx.x % s.vx;
+  const int ty = (int)threadIdx.x / s.vx;
+  const int64_t br = (int64_t)(blockIdx.x / vblocks) * s.pairs + ty;
+  p.active = vi < s.nv && ty < s.pairs && br < (int64_t)s.B * s.runs;
   p.c = max(min(vi * kConvV, s.D - kConvV), 0);
   p.n = s.D - p.c;
   p.again = vi * kConvV - p.c;
@@ -289,8 +290,8 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd(const ConvArgs<E> s) {
       conv_bwd_run<false, W>(gw, s, p);
   }
   // the workgroup's (row, run) pairs, summed in order, one tap at a time
-  const int n = s.vx * V, pairs = kConvThreads / s.vx;
-  const int vi = (int)threadIdx.x & (s.vx - 1), ty = (int)threadIdx.x / s.vx;
+  const int n = s.vx * V;
+  const int vi = (int)threadIdx.x % s.vx, ty = (int)threadIdx.x / s.vx;
   const int vblocks = (s.nv + s.vx - 1) / s.vx;
   const int c0 = (int)(blockIdx.x % vblocks) * n;
   float* part = s.part + (int64_t)(blockIdx.x / vblocks) * (W + 1) * s.D + c0;
@@ -303,7 +304,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd(const ConvArgs<E> s) {
     __syncthreads();
     for (int e = threadIdx.x; e < n && c0 + e < s.D; e += kConvThreads) {
       float sum = 0.0f;
-      for (int r = 0; r < pairs; ++r) sum += red[r * n + e];
+      for (int r = 0; r < s.pairs; ++r) sum += red[r * n + e];
       part[(int64_t)k * s.D + e] = sum;
     }
   }
@@ -396,19 +397,20 @@ ck_status conv_check_state(const void* p, const ck_conv_shape& s, bool optional,
 }
 
 struct ConvDims {
-  int nv, vx, run, runs;
+  int nv, vx, pairs, run, runs;
   int64_t vblocks, pblocks;  // workgroups over the channels, over the (row, run) pairs
 };
 ConvDims conv_dims(const ck_conv_shape& s, int run) {
   ConvDims d;
   d.nv = (int)((s.D + kConvV - 1) / kConvV);
-  d.vx = 1;
-  while (d.vx < 64 && d.vx < d.nv) d.vx *= 2;
+  // (as many groups in each workgroup as in the others: of 256 threads 228 have
+  // work at 152 channels, 152 if a row took 64)
+  d.vblocks = (d.nv + 63) / 64;
+  d.vx = (int)((d.nv + d.vblocks - 1) / d.vblocks);
+  d.pairs = kConvThreads / d.vx;
   d.run = run;
   d.runs = (int)std::max<int64_t>((s.T + run - 1) / run, 1);
-  d.vblocks = (d.nv + d.vx - 1) / d.vx;
-  const int pairs = kConvThreads / d.vx;
-  d.pblocks = (s.B * d.runs + pairs - 1) / pairs;
+  d.pblocks = (s.B * d.runs + d.pairs - 1) / d.pairs;
   return d;
 }
 
@@ -485,7 +487,7 @@ extern "C" ck_status ck_conv_forward(const ck_conv_shape* shape, ck_seq x, const
       ConvArgs<E> a = conv_args<E>(*shape, x, weight, bias, state0, lengths);
       a.y = seq_of<E>(y);
       a.state = W > 1 ? static_cast<E*>(state) : nullptr;
-      a.nv = d.nv; a.vx = d.vx; a.run = d.run; a.runs = d.runs;
+      a.nv = d.nv; a.vx = d.vx; a.pairs = d.pairs; a.run = d.run; a.runs = d.runs;
       conv_fwd<E, W><<<(unsigned)(d.vblocks * d.pblocks), kConvThreads, 0, stream>>>(a);
     });
     CK_HIP_TRY(hipGetLastError());
@@ -529,7 +531,7 @@ extern "C" ck_status ck_conv_backward(const ck_conv_shape* shape, ck_seq x, cons
       a.gstate = W > 1 ? static_cast<const E*>(grad_state) : nullptr;
       a.gstate0 = W > 1 ? static_cast<E*>(grad_state0) : nullptr;
       a.part = static_cast<float*>(workspace);
-      a.nv = d.nv; a.vx = d.vx; a.run = d.run; a.runs = d.runs;
+      a.nv = d.nv; a.vx = d.vx; a.pairs = d.pairs; a.run = d.run; a.runs = d.runs;
       conv_bwd<E, W><<<(unsigned)(d.vblocks * d.pblocks), kConvThreads, 0, stream>>>(a);
       conv_sum<W><<<(unsigned)((shape->D * (W + 1) + 31) / 32), 256, 0, stream>>>(
           a.part, a.D, d.pblocks, grad_weight, grad_bias);
