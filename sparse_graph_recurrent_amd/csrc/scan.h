@@ -24,9 +24,10 @@
 //
 // Still fewer rows leave most of the chip idle, and the window is then cut into
 // chunks that run side by side: a first launch finds what each chunk makes of a zero
-// state (and the sum of its dt, from which its decay exp(A sum dt) follows), a
-// small one joins these to every chunk's entering state, and the main launch
-// starts each chunk from it.  The backward does the same with its adjoint from
+// state (and the sum of its dt, from which its decay exp(A sum dt) follows), and the
+// main launch starts each chunk from what those before it make of the window's first
+// state.  It folds them itself where they are few, or finds them joined by a small
+// launch between the two.  The backward does the same with its adjoint from
 // the other end.
 #pragma once
 
