@@ -442,20 +442,23 @@ def short_conv_backward(x, weight, grad_y, bias=None, state0=None, lengths=None,
     """Run ``ck_conv_backward``; returns the gradients (overwritten) g_x,
     g_weight, g_bias and g_state0."""
     shape, dev, ss, xs, w, b = _conv_call(x, weight, bias, activation)
+    s0 = _par(state0, "state0", dev, ss, x.dtype)
     made = grads is None
-    g = {} if made else grads
-    have = (lambda name: None) if made else grads.get
-    g["g_x"], gx, _ = _out_seq(have("g_x"), "g_x", x)
-    g["g_weight"], gw, _ = _out_par(have("g_weight"), "g_weight", x, weight.shape, model=weight)
-    gb = gs0 = 0
-    if made or grads.get("g_bias") is not None:
-        g["g_bias"], gb, _ = _out_par(have("g_bias"), "g_bias", x, (ss[2],), model=bias)
-    if made or grads.get("g_state0") is not None:
-        g["g_state0"], gs0, _ = _out_par(have("g_state0"), "g_state0", x, ss, x.dtype,
-                                         state0)
+    if made:
+        g = {"g_x": _fresh(x), "g_weight": torch.empty_like(weight),
+             "g_bias": weight.new_empty(ss[2]) if bias is None else torch.empty_like(bias),
+             "g_state0": x.new_empty(ss) if state0 is None else torch.empty_like(state0)}
+        gx = CkSeq(g["g_x"].data_ptr(), *_dense(x.shape, ss[2]))
+        gw, gb, gs0 = (g[k].data_ptr() for k in ("g_weight", "g_bias", "g_state0"))
+    else:
+        g = grads
+        gx = CkSeq(*_seq(g["g_x"], "g_x", x.dtype, dev, x.shape))
+        gw = _par(g["g_weight"], "g_weight", dev, weight.shape)
+        gb = _par(g.get("g_bias"), "g_bias", dev, (ss[2],))
+        gs0 = _par(g.get("g_state0"), "g_state0", dev, ss, x.dtype)
     workspace, wp, wn, m1 = _buffer(workspace, _conv_sizes(shape), x, "workspace")
     _call(lib().ck_conv_backward, dev, stream,
-          (shape, xs, w, b, _par(state0, "state0", dev, ss, x.dtype),
+          (shape, xs, w, b, s0,
            _par(lengths, "lengths", dev, (ss[1],), torch.int32),
            CkSeq(*_seq(grad_y, "grad_y", x.dtype, dev, x.shape)),
            _par(grad_state, "grad_state", dev, ss, x.dtype), gx, gw, gb, gs0, wp, wn),
