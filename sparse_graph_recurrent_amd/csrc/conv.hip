@@ -26,11 +26,13 @@ namespace {
 constexpr int64_t kConvMaxW = 8;
 constexpr int kConvThreads = 256;
 constexpr int kConvRun = 16;     // steps per thread, forward
-// and backward, whose run reads 2 (W - 1) steps more: long ones where they
-// still give every CU two workgroups, else short ones
-constexpr int kConvRunBwdMax = 48, kConvRunBwdMin = 16;
-constexpr int64_t kConvFullWgs = 512;
 constexpr int kConvAhead = 4;    // rows in flight: loaded while the ones before are worked on
+// and backward, whose run reads 2 (W - 1) steps more: the shortest with which all
+// workgroups run at once, as many a CU as registers allow (1000 x 32 x 500 bf16, all
+// of a training pass: 53 us in 672 workgroups of runs of 24; 58 in 1008 of 16).  Runs
+// of 8 where even those would fit: 1816 x 14 x 152 bf16 32 us against 30.
+constexpr int kConvRunBwdMax = 48, kConvRunBwdMin = 16;
+constexpr int64_t kConvCus = 256;
 constexpr int kConvV = 4;        // channels per thread
 
 template <typename E>
@@ -415,8 +417,14 @@ ConvDims conv_dims(const ck_conv_shape& s, int run) {
 }
 
 ConvDims conv_dims_backward(const ck_conv_shape& s) {
-  const ConvDims d = conv_dims(s, kConvRunBwdMax);
-  return d.vblocks * d.pblocks >= kConvFullWgs ? d : conv_dims(s, kConvRunBwdMin);
+  const int64_t round = kConvCus * (s.W <= 4 ? 3 : 2);
+  ConvDims d = conv_dims(s, kConvRunBwdMax);
+  for (int run = kConvRunBwdMax; run >= kConvRunBwdMin; run -= kConvAhead) {
+    const ConvDims shorter = conv_dims(s, run);
+    if (shorter.vblocks * shorter.pblocks > round) break;
+    d = shorter;
+  }
+  return d;
 }
 
 template <typename E>
