@@ -129,6 +129,24 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on_stream(stream, fn, *args):
+    """fn(*args) with `stream` current, so that what the call allocates is that
+    stream's own memory: a block that the caller has just freed on another
+    stream may still be read by work queued there, and is not handed out.  What
+    the call returns is kept from reuse until the stream that is current now
+    has done what it was given to do with it."""
+    for t in args:
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.device != stream.device:
+            raise ValueError(f"a tensor is on {t.device}, the stream on {stream.device}")
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        res = fn(*args)
+    for t in res.values() if isinstance(res, dict) else res if isinstance(res, tuple) else (res,):
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(caller)
+    return res
+
+
 def _dev(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> torch.Tensor:
     if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")

@@ -15,6 +15,8 @@ give 0.
 
 are differentiable; ``*_forward`` / ``*_backward`` are the calls behind them
 and ``*_step`` take one token per row, from and to the carried states.
+These calls take a ``stream`` to run on instead of the current one; their
+inputs have to be ready there, and what they allocate is that stream's memory.
 """
 from __future__ import annotations
 
@@ -25,7 +27,7 @@ import struct
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _check, lib
+from . import _check, _on_stream, lib
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
@@ -102,22 +104,14 @@ def _declare(L: ctypes.CDLL) -> None:
     L.ck_dropout_backward.argtypes = [p, q, q, p]
 
 
-def _call(fn, dev: int, stream, args, made=()):
-    """Runs one entry point with device `dev` current on `stream` (None: the
-    current one); memory of the tensors in `made`, allocated here for another
-    stream than the current, is kept from reuse until that stream is done."""
+def _call(fn, dev: int, args):
+    """Runs one entry point with device `dev` current, on its current stream."""
     if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
-            return _call(fn, dev, stream, args, made)
-    if stream is None:
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
-        if status:
-            _check(status)
-        return
-    _check(fn(*args, stream.cuda_stream))
-    for t in made:
-        if t is not None:
-            t.record_stream(stream)
+            return _call(fn, dev, args)
+    status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        _check(status)
 
 
 def _adjacent(t: torch.Tensor, last: int) -> bool:
@@ -195,36 +189,36 @@ def _dense(shape, inner: int):
 
 
 def _out_seq(t, name: str, like: torch.Tensor):
-    """(tensor, its ck_seq, made here) of an output of like's [.., D] shape: the
-    caller's, checked, or a new contiguous one."""
+    """(tensor, its ck_seq) of an output of like's [.., D] shape: the caller's,
+    checked, or a new contiguous one."""
     shape = like.shape
     if t is None:
         t = _fresh(like)
-        return t, CkSeq(t.data_ptr(), *_dense(shape, shape[-1])), True
-    return t, CkSeq(*_seq(t, name, like.dtype, like.get_device(), shape)), False
+        return t, CkSeq(t.data_ptr(), *_dense(shape, shape[-1]))
+    return t, CkSeq(*_seq(t, name, like.dtype, like.get_device(), shape))
 
 
 def _out_par(t, name: str, like: torch.Tensor, shape, dtype=torch.float32, model=None):
-    """(tensor, its address, made here) of a contiguous output; `model`: a
-    contiguous tensor of its shape and type, if there is one (quicker to copy)."""
+    """(tensor, its address) of a contiguous output; `model`: a contiguous tensor
+    of its shape and type, if there is one (quicker to copy)."""
     if t is not None:
-        return t, _par(t, name, like.get_device(), shape, dtype), False
+        return t, _par(t, name, like.get_device(), shape, dtype)
     t = like.new_empty(shape, dtype=dtype) if model is None else torch.empty_like(model)
-    return t, t.data_ptr(), True
+    return t, t.data_ptr()
 
 
 def _buffer(buf, nbytes: int, like: torch.Tensor, name: str):
-    """(byte buffer, its address, its size, made here): the caller's, checked, or a
-    new one; none for 0 bytes."""
+    """(byte buffer, its address, its size): the caller's, checked, or a new one;
+    none for 0 bytes."""
     if buf is None:
         if not nbytes:
-            return None, None, 0, False
+            return None, None, 0
         buf = torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=like.device)
-        return buf, buf.data_ptr(), nbytes, True
+        return buf, buf.data_ptr(), nbytes
     size = buf.numel() * buf.element_size()
     if buf.get_device() != like.get_device() or size < nbytes or not buf.is_contiguous():
         raise ValueError(f"{name} buffer too small, not contiguous or on another device")
-    return buf, buf.data_ptr() if size else None, size, False
+    return buf, buf.data_ptr() if size else None, size
 
 
 # ------------------------------------------------------------ selective scan
@@ -270,17 +264,18 @@ def selective_scan_forward(u, delta, A, B, C, D=None, z=None, delta_bias=None, s
     u, delta, z: [T, B, D]; B, C: [T, B, G, N]; A: [D, N]; D, delta_bias: [D];
     state0 and the returned state: [B, D, N].  ``saved`` is what
     ``selective_scan_backward`` needs (None with save=False)."""
+    if stream is not None:
+        return _on_stream(stream, selective_scan_forward, u, delta, A, B, C, D, z, delta_bias,
+                          state0, lengths, delta_softplus, save, out, state, saved, workspace)
     shape, inputs, dev, (T, rows, ch, N, _) = _scan_call(
         u, delta, A, B, C, D, z, delta_bias, state0, lengths, delta_softplus)
     sb, fb, _ = _scan_sizes(shape)
-    out, os, m0 = _out_seq(out, "out", u)
-    state, st, m1 = _out_par(state, "state", u, (rows, ch, N), model=state0)
-    saved, sp, _, m2 = _buffer(saved, sb, u, "saved") if save or saved is not None else \
-        (None, None, 0, False)
-    workspace, wp, wn, m3 = _buffer(workspace, fb, u, "workspace")
-    _call(lib().ck_scan_forward, dev, stream, (shape, inputs, os, st, sp, wp, wn),
-          (out if m0 else None, state if m1 else None, saved if m2 else None,
-           workspace if m3 else None))
+    out, os = _out_seq(out, "out", u)
+    state, st = _out_par(state, "state", u, (rows, ch, N), model=state0)
+    saved, sp, _ = _buffer(saved, sb, u, "saved") if save or saved is not None else \
+        (None, None, 0)
+    workspace, wp, wn = _buffer(workspace, fb, u, "workspace")
+    _call(lib().ck_scan_forward, dev, (shape, inputs, os, st, sp, wp, wn))
     return out, state, saved, workspace
 
 
@@ -290,17 +285,19 @@ def selective_scan_backward(u, delta, A, B, C, saved, grad_out, D=None, z=None, 
     """Run ``ck_scan_backward``; returns the gradients (overwritten) by the
     names g_u, g_delta, g_A, g_B, g_C, g_D, g_delta_bias, g_state0 and, with a
     gate, g_z."""
+    if stream is not None:
+        return _on_stream(stream, selective_scan_backward, u, delta, A, B, C, saved, grad_out, D, z,
+                          delta_bias, lengths, delta_softplus, grad_state, grads, workspace)
     shape, inputs, dev, (T, rows, ch, N, G) = _scan_call(
         u, delta, A, B, C, D, z, delta_bias, None, lengths, delta_softplus)
     sb, _, wb = _scan_sizes(shape)
     if sb and saved is None:
         raise ValueError("saved is missing")
-    _, sp, _, _ = _buffer(saved, sb, u, "saved")
+    _, sp, _ = _buffer(saved, sb, u, "saved")
     ss = (rows, ch, N)
     go = CkSeq(*_seq(grad_out, "grad_out", u.dtype, dev, u.shape))
     gs = _par(grad_state, "grad_state", dev, ss)
-    made = grads is None
-    if made:
+    if grads is None:
         g = {"g_u": _fresh(u), "g_delta": _fresh(delta), "g_B": _fresh(B), "g_C": _fresh(C),
              "g_A": torch.empty_like(A), "g_D": D, "g_delta_bias": delta_bias,
              "g_state0": grad_state}
@@ -328,9 +325,8 @@ def selective_scan_backward(u, delta, A, B, C, saved, grad_out, D=None, z=None, 
             _par(g.get("g_A"), "g_A", dev, A.shape), _par(g.get("g_D"), "g_D", dev, (ch,)),
             _par(g.get("g_delta_bias"), "g_delta_bias", dev, (ch,)),
             _par(g.get("g_state0"), "g_state0", dev, ss))
-    workspace, wp, wn, m1 = _buffer(workspace, wb, u, "workspace")
-    _call(lib().ck_scan_backward, dev, stream, (shape, inputs, sp, go, gs, out, wp, wn),
-          (tuple(g.values()) if made else ()) + ((workspace,) if m1 else ()))
+    workspace, wp, wn = _buffer(workspace, wb, u, "workspace")
+    _call(lib().ck_scan_backward, dev, (shape, inputs, sp, go, gs, out, wp, wn))
     return g
 
 
@@ -339,15 +335,17 @@ def selective_scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=Non
     """Run ``ck_scan_step``: one token per row.  u, delta, z: [B, D]; B, C:
     [B, G, N]; state: [B, D, N], updated in place unless ``new_state`` is
     given.  Returns (out [B, D], the new state)."""
+    if stream is not None:
+        return _on_stream(stream, selective_scan_step, state, u, delta, A, B, C, D, z, delta_bias,
+                          delta_softplus, out, new_state)
     if state is None:
         raise ValueError("state is missing")
     shape, inputs, dev, (_, rows, ch, N, _) = _scan_call(
         u, delta, A, B, C, D, z, delta_bias, state, None, delta_softplus, step=True)
     new_state = state if new_state is None else new_state
-    out, os, made = _out_seq(out, "out", u)
-    _call(lib().ck_scan_step, dev, stream,
-          (shape, inputs, os, _par(new_state, "new_state", dev, (rows, ch, N))),
-          (out,) if made else ())
+    out, os = _out_seq(out, "out", u)
+    _call(lib().ck_scan_step, dev,
+          (shape, inputs, os, _par(new_state, "new_state", dev, (rows, ch, N))))
     return out, new_state
 
 
@@ -427,13 +425,15 @@ def short_conv_forward(x, weight, bias=None, state0=None, lengths=None, activati
     """Run ``ck_conv_forward``; returns (y, state).  x: [T, B, D]; weight:
     [D, W]; bias: [D]; state0 and the returned state: [W - 1, B, D], the last
     inputs of each row; activation: None or "silu"."""
+    if stream is not None:
+        return _on_stream(stream, short_conv_forward, x, weight, bias, state0, lengths, activation,
+                          y, state)
     shape, dev, ss, xs, w, b = _conv_call(x, weight, bias, activation)
-    y, ys, m0 = _out_seq(y, "y", x)
-    state, st, m1 = _out_par(state, "state", x, ss, x.dtype, state0)
-    _call(lib().ck_conv_forward, dev, stream,
+    y, ys = _out_seq(y, "y", x)
+    state, st = _out_par(state, "state", x, ss, x.dtype, state0)
+    _call(lib().ck_conv_forward, dev,
           (shape, xs, w, b, _par(state0, "state0", dev, ss, x.dtype),
-           _par(lengths, "lengths", dev, (ss[1],), torch.int32), ys, st),
-          (y if m0 else None, state if m1 else None))
+           _par(lengths, "lengths", dev, (ss[1],), torch.int32), ys, st))
     return y, state
 
 
@@ -441,10 +441,12 @@ def short_conv_backward(x, weight, grad_y, bias=None, state0=None, lengths=None,
                         grad_state=None, grads=None, workspace=None, stream=None) -> dict:
     """Run ``ck_conv_backward``; returns the gradients (overwritten) g_x,
     g_weight, g_bias and g_state0."""
+    if stream is not None:
+        return _on_stream(stream, short_conv_backward, x, weight, grad_y, bias, state0, lengths,
+                          activation, grad_state, grads, workspace)
     shape, dev, ss, xs, w, b = _conv_call(x, weight, bias, activation)
     s0 = _par(state0, "state0", dev, ss, x.dtype)
-    made = grads is None
-    if made:
+    if grads is None:
         g = {"g_x": _fresh(x), "g_weight": torch.empty_like(weight),
              "g_bias": weight.new_empty(ss[2]) if bias is None else torch.empty_like(bias),
              "g_state0": x.new_empty(ss) if state0 is None else torch.empty_like(state0)}
@@ -456,13 +458,12 @@ def short_conv_backward(x, weight, grad_y, bias=None, state0=None, lengths=None,
         gw = _par(g["g_weight"], "g_weight", dev, weight.shape)
         gb = _par(g.get("g_bias"), "g_bias", dev, (ss[2],))
         gs0 = _par(g.get("g_state0"), "g_state0", dev, ss, x.dtype)
-    workspace, wp, wn, m1 = _buffer(workspace, _conv_sizes(shape), x, "workspace")
-    _call(lib().ck_conv_backward, dev, stream,
+    workspace, wp, wn = _buffer(workspace, _conv_sizes(shape), x, "workspace")
+    _call(lib().ck_conv_backward, dev,
           (shape, xs, w, b, s0,
            _par(lengths, "lengths", dev, (ss[1],), torch.int32),
            CkSeq(*_seq(grad_y, "grad_y", x.dtype, dev, x.shape)),
-           _par(grad_state, "grad_state", dev, ss, x.dtype), gx, gw, gb, gs0, wp, wn),
-          (tuple(g.values()) if made else ()) + ((workspace,) if m1 else ()))
+           _par(grad_state, "grad_state", dev, ss, x.dtype), gx, gw, gb, gs0, wp, wn))
     return g
 
 
@@ -471,12 +472,14 @@ def short_conv_step(state, x, weight, bias=None, activation=None, y=None, new_st
     """Run ``ck_conv_step``: one token per row.  x: [B, D]; state: [W - 1, B,
     D], updated in place unless ``new_state`` is given.  Returns (y [B, D],
     the new state)."""
+    if stream is not None:
+        return _on_stream(stream, short_conv_step, state, x, weight, bias, activation, y, new_state)
     shape, dev, ss, xs, w, b = _conv_call(x, weight, bias, activation, step=True)
     new_state = state if new_state is None else new_state
-    y, ys, made = _out_seq(y, "y", x)
-    _call(lib().ck_conv_step, dev, stream,
+    y, ys = _out_seq(y, "y", x)
+    _call(lib().ck_conv_step, dev,
           (shape, xs, w, b, _par(state, "state", dev, ss, x.dtype), ys,
-           _par(new_state, "new_state", dev, ss, x.dtype)), (y,) if made else ())
+           _par(new_state, "new_state", dev, ss, x.dtype)))
     return y, new_state
 
 
@@ -527,21 +530,24 @@ def dropout_forward(x, p: float, seed: int, offset: int = 0, residual=None, held
     window the same mask.  A device ``counter`` (int64 [1]) is added to the
     offset, so that a replayed graph can draw new masks.  ``out`` may be x or
     the residual."""
+    if stream is not None:
+        return _on_stream(stream, dropout_forward, x, p, seed, offset, residual, held, counter, out)
     shape, dev, xs = _drop_call(x, "x", p, seed, offset, held, counter)
     rs = _NONE if residual is None else _seq(residual, "residual", x.dtype, dev, x.shape)
-    out, os, made = _out_seq(out, "out", x)
-    _call(lib().ck_dropout_forward, dev, stream, (shape, xs, CkSeq(*rs), os),
-          (out,) if made else ())
+    out, os = _out_seq(out, "out", x)
+    _call(lib().ck_dropout_forward, dev, (shape, xs, CkSeq(*rs), os))
     return out
 
 
 def dropout_backward(grad_out, p: float, seed: int, offset: int = 0, held: bool = False,
                      counter=None, grad_x=None, stream=None) -> torch.Tensor:
     """Run ``ck_dropout_backward``: the forward's mask and scale on grad_out."""
+    if stream is not None:
+        return _on_stream(stream, dropout_backward, grad_out, p, seed, offset, held, counter,
+                          grad_x)
     shape, dev, gs = _drop_call(grad_out, "grad_out", p, seed, offset, held, counter)
-    grad_x, os, made = _out_seq(grad_x, "grad_x", grad_out)
-    _call(lib().ck_dropout_backward, dev, stream, (shape, gs, os),
-          (grad_x,) if made else ())
+    grad_x, os = _out_seq(grad_x, "grad_x", grad_out)
+    _call(lib().ck_dropout_backward, dev, (shape, gs, os))
     return grad_x
 
 

@@ -627,3 +627,73 @@ def test_binding_refusals():
     u = g["u"].transpose(0, 2).contiguous().transpose(0, 2)
     a, _ = sgr.selective_scan(*args(u=u))
     assert torch.equal(a, sgr.selective_scan(*args())[0])
+
+
+# ------------------------------------------------------------------- streams
+
+def _flat(res):
+    return [t for r in res for t in (r.values() if isinstance(r, dict) else
+                                     r if isinstance(r, tuple) else (r,)) if t is not None]
+
+
+def _ranges(res):
+    return [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in _flat(res)]
+
+
+@pytest.mark.parametrize("op", ["scan", "conv", "dropout", "steps"])
+def test_a_call_on_another_stream_takes_no_memory_of_the_current_one(op):
+    """What a call with stream= allocates is that stream's memory: blocks freed on
+    the current stream, which work queued there may still read, are not among it."""
+    side = torch.cuda.Stream()
+    g, _ = scan_problem(21, 40, 8, 256, 16, 1, "fp32", True, True, None, "time")
+    w, x, state = torch.randn(256, 4, device="cuda"), g["u"], torch.zeros(3, 8, 256, device="cuda")
+
+    def work(stream):
+        if op == "scan":
+            a = (g["u"], g["delta"], g["A"], g["B"], g["C"])
+            o = dict(D=g["D"], z=g["z"], delta_bias=g["delta_bias"], stream=stream)
+            f = sgr.selective_scan_forward(*a, **o)
+            return f, sgr.selective_scan_backward(*a, f[2], g["go"], **o)
+        if op == "conv":
+            return (sgr.short_conv_forward(x, w, stream=stream),
+                    sgr.short_conv_backward(x, w, g["go"], stream=stream))
+        if op == "dropout":
+            return (sgr.dropout_forward(x, 0.5, 1, stream=stream),
+                    sgr.dropout_backward(x, 0.5, 1, stream=stream))
+        return (sgr.selective_scan_step(g["state0"], g["u"][0], g["delta"][0], g["A"], g["B"][0],
+                                        g["C"][0], stream=stream)[0],
+                sgr.short_conv_step(state, x[0], w, stream=stream)[0])
+
+    # the current stream's free blocks: one of every size that the call makes, twice
+    old = [work(None), work(None)]
+    torch.cuda.synchronize()
+    freed = _ranges(old[0]) + _ranges(old[1])
+    del old
+    res = work(side)
+    torch.cuda.current_stream().wait_stream(side)
+    made = _ranges(res)
+    assert made
+    for lo, hi in made:
+        assert not any(lo < b and a < hi for a, b in freed), (lo, hi)
+    want = work(None)
+    torch.cuda.synchronize()
+    if op == "steps":  # (the states have moved on)
+        return
+    for i, (a, b) in enumerate(zip(_flat(res), _flat(want))):
+        # bit for bit: the steps' negative dt makes states outgrow fp32 here
+        if a.dtype == torch.float32:
+            assert torch.equal(a.view(torch.int32), b.view(torch.int32)), i
+
+
+def test_a_call_on_another_stream_leaves_the_current_one_current():
+    """The current stream is the caller's again behind a call, also one that raises."""
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    x = torch.randn(4, 2, 8, device="cuda")
+    before = torch.cuda.current_stream()
+    sgr.dropout_forward(x, 0.5, 1, stream=side)
+    assert torch.cuda.current_stream() == before
+    with pytest.raises(sgr.CkError):
+        sgr.dropout_forward(x, 1.5, 1, stream=side)
+    assert torch.cuda.current_stream() == before
+    torch.cuda.synchronize()
