@@ -246,6 +246,9 @@ def _byte_buffer(nbytes: int, device) -> torch.Tensor:
 def recurrence_forward(graph: SparseGraph, edge_values, leak, bias, drives, state0,
                        microsteps: int, out=None, saved=None, workspace=None, stream=None):
     """Run ``ck_recurrence_forward``; returns (out, saved, workspace)."""
+    if stream is not None:
+        return _on_stream(stream, recurrence_forward, graph, edge_values, leak, bias, drives,
+                          state0, microsteps, out, saved, workspace)
     N, E, n_in = graph.num_nodes, graph.num_edges, graph.num_inputs
     B = state0.shape[0]
     T = drives.shape[0]
@@ -265,7 +268,7 @@ def recurrence_forward(graph: SparseGraph, edge_values, leak, bias, drives, stat
     _check(lib().ck_recurrence_forward(
         graph.handle, _ptr(edge_values), _ptr(leak), _ptr(bias), _ptr(drives), _ptr(state0),
         T, B, int(microsteps), _ptr(out), _ptr(saved), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        workspace.numel() * workspace.element_size(), _stream()))
     return out, saved, workspace
 
 
@@ -294,6 +297,9 @@ def recurrence_forward_noalloc(graph: SparseGraph, edge_values, leak, bias, driv
 def recurrence_backward(graph: SparseGraph, edge_values, leak, state0, microsteps: int, saved,
                         grad_out, workspace=None, grads=None, stream=None) -> dict:
     """Run ``ck_recurrence_backward``; returns the five gradients (overwritten)."""
+    if stream is not None:
+        return _on_stream(stream, recurrence_backward, graph, edge_values, leak, state0, microsteps,
+                          saved, grad_out, workspace, grads)
     N, E, n_in = graph.num_nodes, graph.num_edges, graph.num_inputs
     T, B = grad_out.shape[0], grad_out.shape[1]
     _dev(edge_values, "edge_values", torch.float32, (E,))
@@ -314,7 +320,7 @@ def recurrence_backward(graph: SparseGraph, edge_values, leak, state0, microstep
         graph.handle, _ptr(edge_values), _ptr(leak), _ptr(state0), T, B, int(microsteps),
         _ptr(saved), _ptr(grad_out), _ptr(grads["g_edge_values"]), _ptr(grads["g_leak"]),
         _ptr(grads["g_bias"]), _ptr(grads["g_drives"]), _ptr(grads["g_state0"]),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream()))
     return grads
 
 
@@ -378,6 +384,9 @@ def lif_forward(graph: SparseGraph, impulses, delays, v0, T: int, threshold: int
     [T, N]).  Synchronises the stream; raises CkError with status
     CK_ERR_OVERFLOW (and .step, the first overflowing timestep) if a
     potential left the int32 range."""
+    if stream is not None:
+        return _on_stream(stream, lif_forward, graph, impulses, delays, v0, T, threshold, reset,
+                          refractory_steps, decay_shifts, workspace)
     N, E = graph.num_nodes, graph.num_edges
     _dev(impulses, "impulses", torch.int16, (E,))
     _dev(delays, "delays", torch.int32, (E,))
@@ -389,7 +398,7 @@ def lif_forward(graph: SparseGraph, impulses, delays, v0, T: int, threshold: int
     st = lib().ck_lif_forward(graph.handle, _ptr(impulses), _ptr(delays), ctypes.byref(prm),
                               _ptr(v0), int(T), _ptr(spikes), _ptr(pot), ctypes.byref(step),
                               _ptr(workspace), workspace.numel() * workspace.element_size(),
-                              _stream(stream))
+                              _stream())
     if st != 0:
         _lif_raise(st, step)
     return spikes, pot
@@ -398,12 +407,14 @@ def lif_forward(graph: SparseGraph, impulses, delays, v0, T: int, threshold: int
 def lif_prepare(graph: SparseGraph, impulses, delays, workspace=None, stream=None) -> torch.Tensor:
     """``ck_lif_prepare``: validate the delays and pack the synapses into a
     workspace (allocated when None), returned for ``lif_run``."""
+    if stream is not None:
+        return _on_stream(stream, lif_prepare, graph, impulses, delays, workspace)
     E = graph.num_edges
     _dev(impulses, "impulses", torch.int16, (E,))
     _dev(delays, "delays", torch.int32, (E,))
     workspace = lif_workspace(graph, impulses.device) if workspace is None else workspace
     _check(lib().ck_lif_prepare(graph.handle, _ptr(impulses), _ptr(delays), _ptr(workspace),
-                                workspace.numel() * workspace.element_size(), _stream(stream)))
+                                workspace.numel() * workspace.element_size(), _stream()))
     return workspace
 
 
@@ -411,6 +422,9 @@ def lif_run(graph: SparseGraph, workspace, v0, T: int, threshold: int, reset: in
             refractory_steps: int, decay_shifts=(), stream=None):
     """``ck_lif_run``: T steps from v0 on the synapses ``lif_prepare`` left in
     ``workspace``; returns and raises as ``lif_forward``."""
+    if stream is not None:
+        return _on_stream(stream, lif_run, graph, workspace, v0, T, threshold, reset,
+                          refractory_steps, decay_shifts)
     N = graph.num_nodes
     _dev(v0, "v0", torch.int32, (N,))
     prm = _lif_params(threshold, reset, refractory_steps, decay_shifts)
@@ -418,7 +432,7 @@ def lif_run(graph: SparseGraph, workspace, v0, T: int, threshold: int, reset: in
     step = ctypes.c_int64(-1)
     st = lib().ck_lif_run(graph.handle, ctypes.byref(prm), _ptr(v0), int(T), _ptr(spikes),
                           _ptr(pot), ctypes.byref(step), _ptr(workspace),
-                          workspace.numel() * workspace.element_size(), _stream(stream))
+                          workspace.numel() * workspace.element_size(), _stream())
     if st != 0:
         _lif_raise(st, step)
     return spikes, pot
