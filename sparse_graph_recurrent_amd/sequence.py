@@ -364,12 +364,13 @@ def _cont(t):
 
 class _SelectiveScan(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, u, delta, A, B, C, D, z, delta_bias, state0, lengths, delta_softplus):
+    def forward(ctx, u, delta, A, B, C, D, z, delta_bias, state0, lengths, delta_softplus,
+                recording):
         u, delta, z, B, C = _rows(u), _rows(delta), _rows(z), _groups(B), _groups(C)
         A, D, delta_bias, state0 = (_cont(t) for t in (A, D, delta_bias, state0))
         out, state, saved, _ = selective_scan_forward(
             u, delta, A, B, C, D, z, delta_bias, state0, lengths, delta_softplus,
-            save=any(ctx.needs_input_grad))
+            save=recording and any(ctx.needs_input_grad))
         ctx.softplus = delta_softplus
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(u, delta, A, B, C, D, z, delta_bias, lengths, saved)
@@ -385,7 +386,7 @@ class _SelectiveScan(torch.autograd.Function):
         return (g["g_u"], g["g_delta"], g["g_A"], g["g_B"], g["g_C"],
                 None if D is None else g["g_D"], g.get("g_z"),
                 None if delta_bias is None else g["g_delta_bias"],
-                g["g_state0"] if ctx.needs_input_grad[8] else None, None, None)
+                g["g_state0"] if ctx.needs_input_grad[8] else None, None, None, None)
 
 
 def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, state0=None, lengths=None,
@@ -393,8 +394,10 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, state0=No
     """The selective scan as one autograd node: returns (out [T, B, D], the
     state after each row's last step [B, D, N]); gradients reach every tensor
     argument but ``lengths``.  Shapes as for ``selective_scan_forward``."""
+    # needs_input_grad says nothing of the grad mode, which is off inside the node:
+    # without it a prompt would leave the backward's states for nobody
     return _SelectiveScan.apply(u, delta, A, B, C, D, z, delta_bias, state0, lengths,
-                                bool(delta_softplus))
+                                bool(delta_softplus), torch.is_grad_enabled())
 
 
 # --------------------------------------------------------- short convolution

@@ -206,3 +206,26 @@ def test_dropout_call_refusals(L):
     assert L.ck_dropout_forward(s, SEQ, NONE, NONE, None) == NULL_ARG
     assert L.ck_dropout_forward(s, SEQ, CkSeq(FAKE + 1, 0, 0), SEQ, None) == BAD_VALUE
     assert L.ck_dropout_backward(s, SEQ, CkSeq(FAKE, 0, -8), None) == BAD_VALUE
+
+
+@pytest.mark.parametrize("mode", ["grad", "no_grad", "inference", "no leaf"])
+def test_scan_saves_states_for_a_backward_alone(monkeypatch, mode):
+    """Without a backward to come (grad mode off, or nothing that requires a
+    gradient) the node does not have the forward leave its states."""
+    import torch
+
+    from sparse_graph_recurrent_amd import sequence
+    asked = []
+
+    def forward(u, delta, A, B, C, *args, save=True, **kw):
+        asked.append(save)
+        return torch.zeros_like(u), u.new_zeros(u.shape[1:] + A.shape[1:]), None, None
+
+    monkeypatch.setattr(sequence, "selective_scan_forward", forward)
+    A = torch.ones(4, 2, requires_grad=mode != "no leaf")
+    x, b = torch.ones(3, 1, 4), torch.ones(3, 1, 1, 2)
+    with {"no_grad": torch.no_grad, "inference": torch.inference_mode}.get(
+            mode, torch.enable_grad)():
+        out, _ = sgr.selective_scan(x, x, A, b, b)
+    assert asked == [mode == "grad"]
+    assert out.requires_grad == (mode == "grad")
