@@ -203,6 +203,23 @@ __device__ __forceinline__ void load_states(States<NP> (&v)[scan_blocks(NP)], co
       v[m][r] = s && n < N ? s[row * N + n] : 0.0f;
     }
 }
+// A rate of the decays as the kernels hold it: an infinite one (a state that
+// forgets everything) counts as the largest here, whose product with log2 e is
+// finite, so that steps past the text, with dt = 0, have the decay 1 and not
+// exp(0 inf).  (From dt = 1e-36 on the decay of such a state is 0 all the same.)
+__device__ __forceinline__ float scan_rate(float a) {
+  constexpr float kMax = 2e38f;
+  return fabsf(a) > kMax ? copysignf(kMax, a) : a;
+}
+template <int NP>
+__device__ __forceinline__ void load_rates(States<NP> (&v)[scan_blocks(NP)], const float* A, int d,
+                                           int q, int N) {
+  load_states<NP>(v, A, d, q, N);
+#pragma unroll
+  for (int m = 0; m < scan_blocks(NP); ++m)
+#pragma unroll
+    for (int r = 0; r < scan_lane(NP); ++r) v[m][r] = scan_rate(v[m][r]);
+}
 template <int NP>
 __device__ __forceinline__ void store_states(const States<NP> (&v)[scan_blocks(NP)], float* s,
                                              int64_t row, int q, int N) {
@@ -414,7 +431,7 @@ __global__ __launch_bounds__(256) void scan_join(float* edge, const float* dtsum
   if (i >= rows * NP) return;
   const int n = (int)(i % NP);
   const int64_t row = i / NP;
-  const float a2 = n < N ? kLog2e * A[row % D * N + n] : 0.0f;
+  const float a2 = n < N ? kLog2e * scan_rate(A[row % D * N + n]) : 0.0f;
   float cur = first && n < N ? first[row * N + n] : 0.0f;
   // in the order of the walk; the chunk that no other follows has no summary
   auto at = [&](int k) { return (int64_t)(FORWARD ? k : chunks - 1 - k) * rows; };

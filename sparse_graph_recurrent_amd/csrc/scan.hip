@@ -101,7 +101,7 @@ __device__ __forceinline__ void scan_one_row(const ScanArgs<E>& s, int b, int d,
   float y = 0.0f, hn[NL];
 #pragma unroll
   for (int k = 0; k < NL; ++k) {
-    hn[k] = fmaf(exp2_hw(dt * (kLog2e * a.v[k])), h.v[k], x * (float)bb.v[k]);
+    hn[k] = fmaf(exp2_hw(dt * (kLog2e * scan_rate(a.v[k]))), h.v[k], x * (float)bb.v[k]);
     y += FULL || k < left ? (float)cc.v[k] * hn[k] : 0.0f;
   }
   y = quad_sum(y);

@@ -85,7 +85,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_bwd_part(const ScanArgs<E> 
   float *ldt = lds_dt[wave], *ldy = lds_dy[wave];
   const int64_t row = (int64_t)p.b * s.D + p.d;
   States<NP> a2[M], g[M];
-  load_states<NP>(a2, s.a, p.d, q, s.N);
+  load_rates<NP>(a2, s.a, p.d, q, s.N);
 #pragma unroll
   for (int m = 0; m < M; ++m) {
     a2[m] *= kLog2e;
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(kScanThreads * TW, NP < 64 && TW == 1 ? 2 : 1) void
   float *ldt = lds_dt[wave], *lx = lds_x[wave], *ldy = lds_dy[wave];
   const int64_t row = (int64_t)p.b * s.D + p.d;
   States<NP> a1[M], ga[M], g[M];  // g: the adjoint the workgroup's tiles start from
-  load_states<NP>(a1, p.active ? s.a : nullptr, p.d, q, s.N);
+  load_rates<NP>(a1, p.active ? s.a : nullptr, p.d, q, s.N);
 #pragma unroll
   for (int m = 0; m < M; ++m) ga[m] = g[m] = 0.0f;
   // Lanes without a channel hold zeros throughout, so they add nothing to gB, gC.
@@ -386,7 +386,8 @@ __global__ __launch_bounds__(kScanThreads * TW, NP < 64 && TW == 1 ? 2 : 1) void
         }
         const float gx = rows_reduce4(sx);  // dL/d(dt u)
         const float gl = rows_reduce4(sa);  // sum_n dL/d(dt A) A
-        gd[i] = fmaf(u[i], gx, gl) * sg[i];
+        // (past the text gl, with a decay of 1, may be anything)
+        gd[i] = 4 * i + q <= last ? fmaf(u[i], gx, gl) * sg[i] : 0.0f;
         gu[i] = fmaf(dt[i], gx, skip * dy[i]);
         gbias += gd[i];
         gskip = fmaf(dy[i], u[i], gskip);

@@ -31,7 +31,7 @@ __global__ __launch_bounds__(kScanThreads * TW) void scan_fwd(const ScanArgs<E> 
   const int64_t row = (int64_t)p.b * s.D + p.d;
   float* edge = s.edge + ((int64_t)p.chunk * s.B * s.D + row) * NP;
   States<NP> a2[M], h[M];  // h: the state the workgroup's tiles start from
-  load_states<NP>(a2, s.a, p.d, q, s.N);
+  load_rates<NP>(a2, s.a, p.d, q, s.N);
 #pragma unroll
   for (int m = 0; m < M; ++m) {
     a2[m] *= kLog2e;

@@ -263,6 +263,41 @@ def test_scan_extremes():
     assert torch.isfinite(out[:2, 0, 0]).all()       # nor do earlier steps
 
 
+# windows that end inside a tile, on each of the ways over the chip: several tiles a
+# workgroup, uncut, cut and folded, cut and joined; every number of padded states
+FORGETS = [
+    (13, 2, 40, 16, 1, "fp32", True, True, [13, 6], "time"),
+    (77, 210, 16, 5, 1, "fp32", False, True, None, "time"),
+    (21, 390, 20, 16, 1, "bf16", True, True, [(5 * b) % 22 for b in range(390)], "time"),
+    (203, 2, 70, 16, 2, "fp32", True, True, [203, 58], "batch"),
+    (203, 1, 40, 33, 1, "fp32", False, True, None, "time"),
+    (517, 130, 6, 7, 2, "fp32", True, True, [(29 * b) % 518 for b in range(130)], "time"),
+    (515, 130, 6, 20, 2, "fp16", True, True, None, "time"),
+]
+
+
+@pytest.mark.parametrize("case", FORGETS, ids=lambda c: "-".join(map(str, c[:6])))
+def test_scan_state_that_forgets_everything(case):
+    """A = -inf, as -exp(log_a) overflows to: each step's decay is 0, and the steps
+    past a row's end still change nothing.  The definition's own limit is taken at
+    -1e30, where exp(dt A) is 0 as well."""
+    log(f"scan forgets {case[:6]}")
+    g, p = scan_problem(22, *case)
+    g["A"][::3, ::2] = g["A"][1, -1] = float("-inf")
+    p["A"][::3, ::2] = p["A"][1, -1] = -1e30
+    scan_check(g, p, case[7])
+
+
+def test_scan_step_of_a_state_that_forgets_everything():
+    g, p = scan_problem(23, 1, 3, 20, 5, 1, "fp32", True, True, None, "time")
+    g["A"][::3], p["A"][::3] = float("-inf"), -1e30
+    want, mag = ref.scan(p), ref.scan(p, magnitude=True)
+    o, s = sgr.selective_scan_step(g["state0"], g["u"][0], g["delta"][0], g["A"], g["B"][0],
+                                   g["C"][0], g["D"], g["z"][0], g["delta_bias"], True)
+    close(o[None], want["out"], mag["out"], 40, "out")
+    close(s, want["state"], mag["state"], 40, "state")
+
+
 def test_scan_values_of_one_step_stay_in_it():
     """An infinite or undefined B, C or u reaches no earlier step and no other row."""
     for k in ("B", "C", "u"):
