@@ -194,6 +194,7 @@ __global__ __launch_bounds__(kScanThreads * TW, NP < 64 && TW == 1 ? 2 : 1) void
       }
     }
   }
+  const bool grows = TW > 1 && scan_grows<NP>(a1, s.softplus);
   const float bias = s.delta_bias ? s.delta_bias[p.d] : 0.0f;
   const float skip = s.d ? s.d[p.d] : 0.0f;
   float gskip = 0.0f, gbias = 0.0f;
@@ -311,7 +312,7 @@ __global__ __launch_bounds__(kScanThreads * TW, NP < 64 && TW == 1 ? 2 : 1) void
 #pragma unroll
         for (int m = 0; m < M; ++m) {
           mk[m] = 0.0f;
-          e[m] = exp2_v(sum * (kLog2e * a1[m]));
+          e[m] = tile_decay(sum, kLog2e * a1[m], grows);
         }
 #pragma unroll
         for (int i = KQ - 1; i >= 0; --i) {
@@ -331,7 +332,7 @@ __global__ __launch_bounds__(kScanThreads * TW, NP < 64 && TW == 1 ? 2 : 1) void
       }
       if (more) bc.store(lds_bc[buf ^ 1]);
       __syncthreads();  // (and the waves' sums of the tiles before are read)
-      if constexpr (TW > 1) fold_tiles<NP, TW, false>(g, next, made, decay, p);
+      if constexpr (TW > 1) fold_tiles<NP, TW, false>(g, next, made, decay, p, grows);
 
       // and backwards: g enters a step as a_{t+1} dL/dh_{t+1}
       float v[16], gu[KQ], gd[KQ];

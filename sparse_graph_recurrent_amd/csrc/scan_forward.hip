@@ -45,6 +45,7 @@ __global__ __launch_bounds__(kScanThreads * TW) void scan_fwd(const ScanArgs<E> 
       if (TW == 1 && s.chunks > 1) fold_chunks<NP, true>(h, a2, s, p, row);
     }
   }
+  const bool grows = TW > 1 && scan_grows<NP>(a2, s.softplus);
   const float bias = s.delta_bias ? s.delta_bias[p.d] : 0.0f;
   const float skip = s.d ? s.d[p.d] : 0.0f;
   float dtsum = 0.0f;
@@ -139,13 +140,13 @@ __global__ __launch_bounds__(kScanThreads * TW) void scan_fwd(const ScanArgs<E> 
           }
         }
 #pragma unroll
-        for (int m = 0; m < M; ++m) e[m] = exp2_v(sum * a2[m]);
+        for (int m = 0; m < M; ++m) e[m] = tile_decay(sum, a2[m], grows);
         const int at = (p.tw * kScanChan + p.wc) * NP;
         store_rows<NP>(&made[par][at], mk, q);
         store_rows<NP>(&decay[par][at], e, q);
         if (more) bc.store(lds_bc[nbuf]);
         __syncthreads();
-        fold_tiles<NP, TW, true>(h, next, made[par], decay[par], p);
+        fold_tiles<NP, TW, true>(h, next, made[par], decay[par], p, grows);
       }
 
       if constexpr (!PART)

@@ -298,6 +298,75 @@ def test_scan_step_of_a_state_that_forgets_everything():
     close(s, want["state"], mag["state"], 40, "state")
 
 
+def growing(seed, case, rate, zero):
+    """A problem whose states grow by exp(|dt A|) a step, |dt A| up to `rate`, A
+    positive or dt negative.  zero: u is 0 before the last two steps and the outputs'
+    gradient behind the first two, so that states and adjoints are 0 in between;
+    else everything starts at 1e-15 and stays in range over the rows' lengths."""
+    T, B, D, N, G, _, gate, positive, lengths, layout = case
+    g, p = scan_problem(seed, T, B, D, N, G, "fp32", gate, False, lengths, layout,
+                        extras=False, nan=False)
+    r = np.random.default_rng(seed + 1)
+    sign = 1.0 if positive else -1.0
+    g["A"], p["A"] = _f32(sign * rate * r.uniform(0.9, 1.0, (D, N)))
+    g["delta"], p["delta"] = place(sign * r.uniform(0.95, 1.0, (T, B, D)), torch.float32, layout)
+    for k in ("u", "go", "state0", "gstate"):
+        a = p[k].copy() if zero else 1e-15 * p[k]
+        if zero:
+            a[{"u": slice(0, T - 2), "go": slice(2, T)}.get(k, slice(None))] = 0.0
+        g[k], p[k] = place(a, torch.float32, layout) if a.ndim == 3 and k in ("u", "go") else _f32(a)
+    return g, p
+
+
+GROWS = [  # T, B, D, N, G, dtype, gate, A positive (else dt negative), lengths, layout
+    (40, 2, 40, 16, 1, "fp32", False, True, None, "time"),
+    (40, 2, 40, 16, 1, "fp32", True, False, None, "time"),
+    (77, 210, 16, 5, 1, "fp32", False, True, None, "time"),
+    (131, 210, 16, 12, 1, "fp32", False, False, None, "time"),
+    (203, 2, 70, 16, 2, "fp32", True, True, None, "batch"),
+    (203, 1, 40, 33, 1, "fp32", False, False, None, "time"),
+    (517, 130, 6, 7, 2, "fp32", False, True, None, "time"),
+    (515, 130, 6, 20, 2, "fp32", False, False, None, "time"),
+]
+
+
+def growing_check(g, p, rate):
+    # A step's decay is off by 4 |dt A| roundings for its exponent and 4 more; the
+    # other 8 (16 in the gradients) a step are scan_check's.
+    T, B, _ = g["u"].shape
+    want, mag = ref.scan(p), ref.scan(p, magnitude=True)
+    out, state, grads = scan_run(g, False)
+    torch.cuda.synchronize()
+    k = 32 + (12 + 4 * rate) * T
+    close(out, want["out"], mag["out"], k, "out")
+    close(state, want["state"], mag["state"], k, "state")
+    for name, t in grads.items():
+        if name in want:
+            close(t, want[name], mag[name], 2 * k + B + 64, name)
+
+
+@pytest.mark.parametrize("case", GROWS, ids=lambda c: "-".join(map(str, c[:5])))
+def test_scan_keeps_zero_states_where_decays_overflow(case):
+    """Over a tile or chunk the decay is far beyond fp32, each step's is not: a
+    zero state (adjoint) stays zero."""
+    log(f"scan grows {case[:5]}")
+    g, p = growing(24, case, 16.0, True)
+    growing_check(g, p, 16.0)
+
+
+@pytest.mark.parametrize("case,rate", [
+    ((9, 2, 40, 16, 1, "fp32", False, True, None, "time"), 12.0),
+    ((9, 3, 70, 6, 1, "fp32", True, False, None, "time"), 12.0),
+    ((203, 2, 70, 16, 2, "fp32", False, True, [26, 25], "time"), 4.2),
+    ((517, 130, 6, 20, 2, "fp32", False, False, [64 + b % 24 for b in range(130)], "time"), 1.3),
+], ids=lambda c: "-".join(map(str, c[:5])) if isinstance(c, tuple) else str(c))
+def test_scan_small_states_grow_past_a_decay_beyond_range(case, rate):
+    """A tile's or chunk's decay overflows fp32, the states it is applied to do not."""
+    log(f"scan grows {case[:5]}")
+    g, p = growing(26, case, rate, False)
+    growing_check(g, p, rate)
+
+
 def test_scan_values_of_one_step_stay_in_it():
     """An infinite or undefined B, C or u reaches no earlier step and no other row."""
     for k in ("B", "C", "u"):
