@@ -214,15 +214,15 @@ __device__ __forceinline__ void conv_bwd_run(float (&gw)[W + 1][V], const ConvAr
 #pragma unroll
     for (int j = 0; j < kConvAhead; ++j) {
       const int t = tb + j;
-      // Past the text (as a run's own steps past its end are) x and g are 0, and
-      // so is dL/dp unless the text's last inputs make it NaN: then it is NaN at
-      // its last step already, wherever these reach.
-      const Pack<E, V> xj = pack_keep(xn[j], t <= last), gj = pack_keep(gn[j], t <= last);
+      // Past the text (as a run's own steps past its end are) dL/dp is 0 whatever the
+      // loads, of its last row, make of it; and nothing is added to the weights'
+      // gradients, since 0 times an infinite input of the window would be.
+      const bool in = t <= last;
       float gx[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        x[W - 1][i] = (float)xj.v[i];
-        float g = (float)gj.v[i];
+        x[W - 1][i] = (float)xn[j].v[i];
+        float g = (float)gn[j].v[i];
         if (s.silu) {
           float a = bias[i];
 #pragma unroll
@@ -230,8 +230,8 @@ __device__ __forceinline__ void conv_bwd_run(float (&gw)[W + 1][V], const ConvAr
           const float sg = sigmoid_hw(a);
           g *= sg * fmaf(a, 1.0f - sg, 1.0f);
         }
-        ga[W - 1][i] = g;
-        if constexpr (OWN) {
+        ga[W - 1][i] = in ? g : 0.0f;
+        if (OWN && in) {
 #pragma unroll
           for (int k = 0; k < W; ++k) gw[k][i] = fmaf(ga[W - 1][i], x[k][i], gw[k][i]);
           gw[W][i] += ga[W - 1][i];
@@ -276,8 +276,9 @@ __device__ __forceinline__ void conv_bwd_run(float (&gw)[W + 1][V], const ConvAr
   for (int t = 0; t < W - 1; t += kConvAhead) steps(std::false_type(), tail + t);
 }
 
+// (as many waves a SIMD as conv_dims_backward counts on)
 template <typename E, int W>
-__global__ __launch_bounds__(kConvThreads) void conv_bwd(const ConvArgs<E> s) {
+__global__ __launch_bounds__(kConvThreads, W <= 4 ? 3 : 2) void conv_bwd(const ConvArgs<E> s) {
   __shared__ float red[kConvThreads * V];  // [pairs of the workgroup][vx * V]
   const ConvPlace p = conv_place(s);
   float gw[W + 1][V];

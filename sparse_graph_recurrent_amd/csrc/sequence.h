@@ -115,19 +115,6 @@ __device__ __forceinline__ Pack<E, V> pack_load(const E* p, int n) {
   for (int i = 0; i < V; ++i) w.v[i] = i < n ? p[i] : (E)0.0f;
   return w;
 }
-// The pack, or zeros: a select for every 4 bytes.
-template <typename E, int V>
-__device__ __forceinline__ Pack<E, V> pack_keep(const Pack<E, V>& p, bool keep) {
-  constexpr int kWords = V * sizeof(E) / 4;
-  static_assert(kWords * 4 == V * sizeof(E), "whole words");
-  uint32_t w[kWords];
-  Pack<E, V> r;
-  __builtin_memcpy(w, &p, sizeof(p));
-#pragma unroll
-  for (int i = 0; i < kWords; ++i) w[i] = keep ? w[i] : 0u;
-  __builtin_memcpy(&r, w, sizeof(r));
-  return r;
-}
 template <bool FULL, typename E, int V>
 __device__ __forceinline__ void pack_store(E* p, const float (&x)[V], int n) {
   Pack<E, V> w;

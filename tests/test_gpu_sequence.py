@@ -573,6 +573,73 @@ def test_conv_autograd():
         assert abs(slope - (hi - lo) / (2 * e)) <= (100 * ref.U32 + 1e-7) * size, k
 
 
+def rows_alone(p, lengths):
+    """The definition with each row a window of its own length: nothing behind a
+    row's text enters any sum."""
+    T, B, D = p["x"].shape
+    W = p["weight"].shape[1]
+    r = {"y": np.zeros((T, B, D)), "g_x": np.zeros((T, B, D)), "state": np.zeros((W - 1, B, D)),
+         "g_state0": np.zeros((W - 1, B, D)), "g_weight": np.zeros((D, W)), "g_bias": np.zeros(D)}
+    for b, n in enumerate(lengths):
+        q = {k: v[:n, b:b + 1] if k in ("x", "gy") else v[:, b:b + 1] if k in ("state0", "gstate")
+             else v for k, v in p.items() if k != "lengths"}
+        with np.errstate(all="ignore"):
+            one = ref.conv(q)
+            for k in ("g_weight", "g_bias"):
+                r[k] += one[k]
+        for k in ("y", "g_x"):
+            r[k][:n, b] = one[k][:, 0]
+        for k in ("state", "g_state0"):
+            r[k][:, b] = one[k][:, 0]
+    return r
+
+
+@pytest.mark.parametrize("D", [3, 12, 66])
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+def test_conv_infinite_last_input_reaches_its_own_taps_alone(D, dtype):
+    """Behind a row's end there are no steps: an infinite last input reaches the
+    gradient of the tap that saw it, not those that would see it later."""
+    lengths = [5, 16, 17, 0, 40, 36, 31, 33]
+    g, p = conv_problem(5, 40, 8, D, 4, dtype, False, lengths, "time")
+    for b, n in enumerate(lengths[:7]):
+        if n:
+            g["x"][n - 1, b, b % D] = float("inf")
+            p["x"][n - 1, b, b % D] = np.inf
+    want = rows_alone(p, lengths)
+    _, _, grads = conv_run(g, False)
+    torch.cuda.synchronize()
+    p["x"] = np.where(np.isinf(p["x"]), 0.0, p["x"])
+    mag = ref.conv(p, magnitude=True)
+    for k in ("g_x", "g_weight", "g_bias", "g_state0"):
+        fine = np.isfinite(want[k])
+        got = grads[k].double().cpu().numpy()
+        assert np.array_equal(np.isfinite(got), fine), k
+        close(torch.where(torch.from_numpy(fine).cuda(), grads[k], 0), np.where(fine, want[k], 0.0),
+              mag[k], 24 + 8 + 320, k)
+    assert np.isfinite(want["g_weight"][:, :3]).all() and not np.isfinite(want["g_weight"]).all()
+
+
+def test_conv_overflow_behind_the_text_reaches_nothing():
+    """With silu: the pre-activation overflows only at steps behind the text."""
+    lengths = [5, 16, 17, 40, 20]
+    g, p = conv_problem(6, 40, 5, 10, 4, "fp32", True, lengths, "batch")
+    for k, w in (("weight", torch.tensor([2.0, 2.0, 2.0, 1e-30], device="cuda")),):
+        g[k][:] = w
+        p[k][:] = w.double().cpu().numpy()
+    for b, n in enumerate(lengths):
+        if n < 40:
+            g["x"][n - 1, b], p["x"][n - 1, b] = 3e38, float(np.float32(3e38))
+            g["gy"][n - 1, b], p["gy"][n - 1, b] = 0.0625, 0.0625
+    want = rows_alone(p, lengths)
+    y, state, grads = conv_run(g, True)
+    torch.cuda.synchronize()
+    for k, t in grads.items():
+        assert np.isfinite(want[k]).all() and torch.isfinite(t).all(), k
+        # every term's roundings, against the largest terms: the huge input's own
+        size = np.abs(want[k]).max() if k == "g_weight" else np.maximum(np.abs(want[k]), 20.0)
+        assert (np.abs(t.double().cpu().numpy() - want[k]) <= 400 * ref.U32 * size).all(), k
+
+
 def test_conv_same_bits_every_time():
     g, _ = conv_problem(4, 100, 3, 200, 4, "bf16", True, [100, 50, 7], "time")
     a, b = conv_run(g, True), conv_run(g, True)
