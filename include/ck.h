@@ -358,9 +358,12 @@ ck_status ck_profile_collect_lif(double* gather_ms, int64_t* gather_launches, do
  * Conventions of these entry points, where they differ from those above
  *   - A sequence tensor [T, B, channels] is a ck_seq: its channels are
  *     adjacent, its steps and batch rows lie stride_t and stride_b elements
- *     apart (0 <= stride_t < 2^24 and 0 <= stride_b, else CK_ERR_BAD_VALUE: a
- *     slice of a wider tensor, batch-major storage, or 0 for an input that
- *     is the same at every step or row).  Elements are of the call's
+ *     apart (not negative, else CK_ERR_BAD_VALUE: a slice of a wider tensor,
+ *     batch-major storage, or 0 for an input that is the same at every step or
+ *     row).  The convolution takes stride_t < 2^30; the scan takes what a tile's
+ *     offsets reach: 8 steps (4 from N = 17 on) within 4 GiB, and stride_t < 2^24
+ *     where few rows and channels (at most 256 times 64 channels of a group and
+ *     row) have a workgroup work on several tiles.  Elements are of the call's
  *     ck_dtype; parameters, scan states and their gradients are fp32 and
  *     contiguous.
  *   - Outputs must not overlap inputs or each other unless stated.

@@ -34,6 +34,8 @@ constexpr int kConvAhead = 4;    // rows in flight: loaded while the ones before
 constexpr int kConvRunBwdMax = 48, kConvRunBwdMin = 16;
 constexpr int64_t kConvCus = 256;
 constexpr int kConvV = 4;        // channels per thread
+// (a step's bytes, 4 an element and fewer, in 32 bits: see Rows)
+constexpr int64_t kConvMaxStrideT = (int64_t(1) << 30) - 1;
 
 template <typename E>
 struct ConvArgs {
@@ -483,8 +485,8 @@ extern "C" ck_status ck_conv_forward(const ck_conv_shape* shape, ck_seq x, const
     set_error("weight is NULL");
     return CK_ERR_NULL_ARG;
   }
-  rc = seq_check(x, shape->dtype, none, "x");
-  if (rc == CK_OK) rc = seq_check(y, shape->dtype, none, "y");
+  rc = seq_check(x, shape->dtype, none, "x", kConvMaxStrideT);
+  if (rc == CK_OK) rc = seq_check(y, shape->dtype, none, "y", kConvMaxStrideT);
   if (rc == CK_OK) rc = conv_check_state(state0, *shape, true, "state0");
   if (rc == CK_OK) rc = conv_check_state(state, *shape, true, "state");
   if (rc != CK_OK) return rc;
@@ -518,9 +520,9 @@ extern "C" ck_status ck_conv_backward(const ck_conv_shape* shape, ck_seq x, cons
     set_error("weight or its gradient is NULL");
     return CK_ERR_NULL_ARG;
   }
-  rc = seq_check(x, shape->dtype, none, "x");
-  if (rc == CK_OK) rc = seq_check(grad_y, shape->dtype, none, "grad_y");
-  if (rc == CK_OK) rc = seq_check(grad_x, shape->dtype, none, "grad_x");
+  rc = seq_check(x, shape->dtype, none, "x", kConvMaxStrideT);
+  if (rc == CK_OK) rc = seq_check(grad_y, shape->dtype, none, "grad_y", kConvMaxStrideT);
+  if (rc == CK_OK) rc = seq_check(grad_x, shape->dtype, none, "grad_x", kConvMaxStrideT);
   if (rc == CK_OK) rc = conv_check_state(state0, *shape, true, "state0");
   if (rc == CK_OK) rc = conv_check_state(grad_state, *shape, true, "grad_state");
   if (rc == CK_OK) rc = conv_check_state(grad_state0, *shape, true, "grad_state0");
@@ -564,8 +566,8 @@ extern "C" ck_status ck_conv_step(const ck_conv_shape* shape, ck_seq x, const fl
     set_error("weight is NULL");
     return CK_ERR_NULL_ARG;
   }
-  rc = seq_check(x, shape->dtype, false, "x");
-  if (rc == CK_OK) rc = seq_check(y, shape->dtype, false, "y");
+  rc = seq_check(x, shape->dtype, false, "x", kConvMaxStrideT);
+  if (rc == CK_OK) rc = seq_check(y, shape->dtype, false, "y", kConvMaxStrideT);
   if (rc == CK_OK) rc = conv_check_state(state0, *shape, true, "state0");
   if (rc == CK_OK) rc = conv_check_state(state, *shape, false, "state");
   if (rc != CK_OK) return rc;

@@ -170,17 +170,31 @@ ck_status scan_check_shape(const ck_scan_shape* s) {
   return CK_OK;
 }
 
-ck_status scan_check_inputs(const ck_scan_shape& s, const ck_scan_inputs* in) {
+// The largest step stride of a tensor of `row` elements a step: offsets from a
+// tile's first step are 32-bit bytes.  Where a workgroup works on several tiles they
+// reach over 32 steps, else over one tile.
+int64_t scan_max_stride(const ck_scan_shape& s, const ScanDims& d, int64_t row) {
+  if (d.waves) return (int64_t(1) << 24) - 1;
+  return (UINT32_MAX / (int64_t)seq_elem_bytes(s.dtype) - row) / (d.K - 1);
+}
+
+// Sizes and inputs of a call; d: how it is spread over the chip.
+ck_status scan_check_inputs(const ck_scan_shape* shape, const ck_scan_inputs* in, ScanDims* d) {
+  ck_status rc = scan_check_shape(shape);
+  if (rc != CK_OK) return rc;
   if (!in || !in->a) {
     set_error("inputs or A is NULL");
     return CK_ERR_NULL_ARG;
   }
+  const ck_scan_shape& s = *shape;
+  *d = scan_dims(s, in->lengths != nullptr);
   const bool none = s.T == 0;
-  ck_status rc = seq_check(in->u, s.dtype, none, "u");
-  if (rc == CK_OK) rc = seq_check(in->delta, s.dtype, none, "delta");
-  if (rc == CK_OK) rc = seq_check(in->b, s.dtype, none, "B");
-  if (rc == CK_OK) rc = seq_check(in->c, s.dtype, none, "C");
-  if (rc == CK_OK) rc = seq_check(in->z, s.dtype, true, "z");
+  const int64_t most = scan_max_stride(s, *d, s.D), most_bc = scan_max_stride(s, *d, s.G * s.N);
+  rc = seq_check(in->u, s.dtype, none, "u", most);
+  if (rc == CK_OK) rc = seq_check(in->delta, s.dtype, none, "delta", most);
+  if (rc == CK_OK) rc = seq_check(in->b, s.dtype, none, "B", most_bc);
+  if (rc == CK_OK) rc = seq_check(in->c, s.dtype, none, "C", most_bc);
+  if (rc == CK_OK) rc = seq_check(in->z, s.dtype, true, "z", most);
   return rc;
 }
 
@@ -244,11 +258,11 @@ extern "C" ck_status ck_scan_forward(const ck_scan_shape* shape, const ck_scan_i
                                      ck_seq out, float* state, void* saved, void* workspace,
                                      size_t workspace_bytes, hipStream_t stream) {
   clear_error();
-  ck_status rc = scan_check_shape(shape);
-  if (rc == CK_OK) rc = scan_check_inputs(*shape, in);
-  if (rc == CK_OK) rc = seq_check(out, shape->dtype, shape->T == 0, "out");
+  ScanDims d;
+  ck_status rc = scan_check_inputs(shape, in, &d);
+  if (rc == CK_OK)
+    rc = seq_check(out, shape->dtype, shape->T == 0, "out", scan_max_stride(*shape, d, d.D));
   if (rc != CK_OK) return rc;
-  const ScanDims d = scan_dims(*shape, in->lengths != nullptr);
   const ScanWs ws = scan_ws(d, false);
   rc = seq_check_ws(workspace, workspace_bytes, ws.total);
   if (rc == CK_OK && saved) rc = check_aligned(saved, "saved");
@@ -270,23 +284,23 @@ extern "C" ck_status ck_scan_backward(const ck_scan_shape* shape, const ck_scan_
                                       const ck_scan_grads* grads, void* workspace,
                                       size_t workspace_bytes, hipStream_t stream) {
   clear_error();
-  ck_status rc = scan_check_shape(shape);
-  if (rc == CK_OK) rc = scan_check_inputs(*shape, in);
+  ScanDims d;
+  ck_status rc = scan_check_inputs(shape, in, &d);
   if (rc != CK_OK) return rc;
   const bool none = shape->T == 0;
   if (!grads || !grads->a || (!saved && !none)) {
     set_error("grads, the gradient of A or saved is NULL");
     return CK_ERR_NULL_ARG;
   }
-  rc = seq_check(grad_out, shape->dtype, none, "grad_out");
-  if (rc == CK_OK) rc = seq_check(grads->u, shape->dtype, none, "the gradient of u");
-  if (rc == CK_OK) rc = seq_check(grads->delta, shape->dtype, none, "the gradient of delta");
+  const int64_t most = scan_max_stride(*shape, d, d.D);
+  rc = seq_check(grad_out, shape->dtype, none, "grad_out", most);
+  if (rc == CK_OK) rc = seq_check(grads->u, shape->dtype, none, "the gradient of u", most);
+  if (rc == CK_OK) rc = seq_check(grads->delta, shape->dtype, none, "the gradient of delta", most);
   if (rc == CK_OK) rc = seq_check(grads->b, shape->dtype, none, "the gradient of B");
   if (rc == CK_OK) rc = seq_check(grads->c, shape->dtype, none, "the gradient of C");
   if (rc == CK_OK)
-    rc = seq_check(grads->z, shape->dtype, none || !in->z.data, "the gradient of z");
+    rc = seq_check(grads->z, shape->dtype, none || !in->z.data, "the gradient of z", most);
   if (rc != CK_OK) return rc;
-  const ScanDims d = scan_dims(*shape, in->lengths != nullptr);
   const ScanWs ws = scan_ws(d, true);
   rc = seq_check_ws(workspace, workspace_bytes, ws.total);
   if (rc == CK_OK && saved) rc = check_aligned(saved, "saved");
@@ -321,14 +335,14 @@ extern "C" ck_status ck_scan_step(const ck_scan_shape* shape, const ck_scan_inpu
     set_error("a step takes T = 1 (got %lld)", (long long)shape->T);
     return CK_ERR_BAD_SIZE;
   }
-  rc = scan_check_inputs(*shape, in);
+  ScanDims d;
+  rc = scan_check_inputs(shape, in, &d);
   if (rc == CK_OK) rc = seq_check(out, shape->dtype, false, "out");
   if (rc != CK_OK) return rc;
   if (!state || in->lengths) {
     set_error(state ? "a step takes no lengths" : "state is NULL");
     return state ? CK_ERR_BAD_VALUE : CK_ERR_NULL_ARG;
   }
-  const ScanDims d = scan_dims(*shape, in->lengths != nullptr);
   return seq_dispatch(shape->dtype, [&](auto* e) -> ck_status {
     using E = std::remove_pointer_t<decltype(e)>;
     ScanArgs<E> a = scan_args<E>(*shape, d, *in, nullptr, ScanWs{});

@@ -47,13 +47,11 @@ inline ck_status seq_check_shape(int64_t T, int64_t B, int64_t D, int dtype) {
   return CK_OK;
 }
 
-// Step strides stay below this many elements, so that the byte offset of 32
-// steps and a row fits 32 unsigned bits.
-constexpr int64_t kSeqMaxStrideT = int64_t(1) << 24;
-
 // A [T, B, ...] tensor: present unless optional, aligned to its elements, with
-// strides in range (a zero stride broadcasts an input).
-inline ck_status seq_check(const ck_seq& s, int dtype, bool optional, const char* what) {
+// strides in range (a zero stride broadcasts an input; max_stride_t: what a
+// kernel's 32-bit offsets from a 64-bit row address reach).
+inline ck_status seq_check(const ck_seq& s, int dtype, bool optional, const char* what,
+                           int64_t max_stride_t = INT64_MAX) {
   if (!s.data) {
     if (optional) return CK_OK;
     set_error("%s is NULL", what);
@@ -63,9 +61,9 @@ inline ck_status seq_check(const ck_seq& s, int dtype, bool optional, const char
     set_error("%s is not aligned to its element type", what);
     return CK_ERR_BAD_VALUE;
   }
-  if (s.stride_t < 0 || s.stride_t >= kSeqMaxStrideT || s.stride_b < 0) {
-    set_error("%s has strides (%lld, %lld); they must be in [0, 2^24) and not negative", what,
-              (long long)s.stride_t, (long long)s.stride_b);
+  if (s.stride_t < 0 || s.stride_t > max_stride_t || s.stride_b < 0) {
+    set_error("%s has strides (%lld, %lld); they must be in [0, %lld] and not negative", what,
+              (long long)s.stride_t, (long long)s.stride_b, (long long)max_stride_t);
     return CK_ERR_BAD_VALUE;
   }
   return CK_OK;

@@ -734,6 +734,41 @@ def test_offsets_past_32_bits():
     assert torch.equal(out, sgr.dropout_forward(x.contiguous(), 0.5, 1))
 
 
+def test_long_step_strides():
+    """Steps 2^24 elements and more apart, as in a window of many wide rows."""
+    def far(t, stride, fill=None):
+        T = t.shape[0]
+        v = torch.empty((T - 1) * stride + t[0].numel(), dtype=t.dtype, device="cuda")
+        v = v.as_strided(t.shape, (stride,) + tuple(t[0].stride()), 0)
+        return v.copy_(t) if fill is None else v.fill_(fill)
+
+    x = torch.randn(5, 3, 70, device="cuda").bfloat16()
+    r = torch.randn_like(x)
+    for stride in (2**24, 2**31 + 2):
+        out = sgr.dropout_forward(far(x, stride), 0.3, 5, residual=far(r, stride),
+                                  out=far(x, stride, 0))
+        assert torch.equal(out, sgr.dropout_forward(x, 0.3, 5, residual=r)), stride
+    g, p = conv_problem(14, 22, 2, 70, 4, "bf16", True, [22, 9], "time")
+    want = conv_run(g, True)
+    f = dict(g, x=far(g["x"], 2**27 + 6), gy=far(g["gy"], 2**27 + 6))
+    y = far(g["x"], 2**27 + 6, 0)
+    sgr.short_conv_forward(f["x"], f["weight"], f["bias"], f["state0"], f["lengths"], "silu", y=y)
+    got = conv_run(f, True)
+    assert torch.equal(y, want[0]) and torch.equal(got[0], want[0])
+    assert all(torch.equal(got[2][k], want[2][k]) for k in want[2])
+    # the scan: a workgroup each; cut
+    for T, B, D, far_by in ((9, 400, 20, 2**26 + 2), (100, 2, 40, 2**25)):
+        g, p = scan_problem(24, T, B, D, 16, 1, "bf16", True, True, None, "time")
+        want = scan_run(g, True)
+        f = dict(g, **{k: far(g[k], far_by) for k in ("u", "delta", "z", "go")})
+        f.update({k: far(g[k], 2**24 + 2) for k in ("B", "C")})
+        got = scan_run(f, True)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert all(torch.equal(got[2][k], want[2][k]) for k in want[2])
+    del f, y, out
+    torch.cuda.empty_cache()  # (some 30 GB of it)
+
+
 def test_captured_graph_replays():
     """Forward, backward and tokens in one HIP graph: every replay equals the
     eager result on the inputs of that moment, with eager work between."""

@@ -131,6 +131,36 @@ def test_scan_input_refusals(L, kw, status):
     assert L.ck_scan_step(_scan(T=1), _inputs(**kw), SEQ, FAKE, None) == status
 
 
+def test_step_strides_a_call_takes(L):
+    """Long strides are refused only where a kernel's offsets end.  (What is taken is
+    seen by the next refusal, the workspace's: nothing runs.)"""
+    far = lambda stride: CkSeq(FAKE, stride, 64)
+    grads = lambda q: ctypes.byref(ScanGrads(q, q, SEQ, SEQ, q, FAKE, None, None, None))
+
+    def scan(q, bc, **kw):
+        return L.ck_scan_backward(_scan(**kw), _inputs(u=q, delta=q, b=bc, c=bc, z=q), FAKE, q,
+                                  None, grads(q), FAKE, 0, None)
+
+    many, cut = dict(T=40, B=400), dict(T=200, B=2)   # a workgroup each; chunks
+    for kw in (many, cut):
+        for dtype, last in ((0, 2**26), (1, 2**27), (2, 2**27)):
+            assert scan(far(last), far(last), dtype=dtype, **kw) == WORKSPACE
+            assert scan(far(8 * last), SEQ, dtype=dtype, **kw) == BAD_VALUE
+            assert scan(SEQ, far(8 * last), dtype=dtype, **kw) == BAD_VALUE
+    assert scan(far(2**24 - 1), far(2**24 - 1)) == WORKSPACE      # several tiles a workgroup
+    assert scan(far(2**24), SEQ) == BAD_VALUE and scan(SEQ, far(2**24)) == BAD_VALUE
+    # the gradients of B and C are written row by row
+    g = ctypes.byref(ScanGrads(SEQ, SEQ, far(2**40), far(2**40), NONE, FAKE, None, None, None))
+    assert L.ck_scan_backward(_scan(), _inputs(), FAKE, SEQ, None, g, FAKE, 0, None) == WORKSPACE
+
+    def conv(q):
+        return L.ck_conv_backward(_conv(), q, FAKE, None, None, None, q, None, q, FAKE, None, None,
+                                  FAKE, 0, None)
+
+    assert conv(far(2**24)) == WORKSPACE and conv(far(2**30 - 1)) == WORKSPACE
+    assert conv(far(2**30)) == BAD_VALUE
+
+
 def test_scan_call_refusals(L):
     g = ctypes.byref(ScanGrads(SEQ, SEQ, SEQ, SEQ, NONE, FAKE, None, None, None))
     s, i = _scan(), _inputs()
