@@ -366,7 +366,9 @@ ck_status ck_profile_collect_lif(double* gather_ms, int64_t* gather_launches, do
  *     row) have a workgroup work on several tiles.  Elements are of the call's
  *     ck_dtype; parameters, scan states and their gradients are fp32 and
  *     contiguous.
- *   - Outputs must not overlap inputs or each other unless stated.
+ *   - Outputs must not overlap inputs or each other unless stated; one whose
+ *     rows lie over one another (strides below its rows' length) gives
+ *     CK_ERR_BAD_VALUE.
  *   - T may be 0 (the state passes through); B and D are positive.
  *   - lengths: int32[B] device or NULL (every row T steps).  Row b holds
  *     text at steps t < lengths[b] only (values outside [0, T] count as the

@@ -401,6 +401,11 @@ ck_status conv_check_state(const void* p, const ck_conv_shape& s, bool optional,
   return seq_check(ck_seq{const_cast<void*>(p), 0, 0}, s.dtype, optional, what);
 }
 
+ck_status conv_check_out(const ck_conv_shape& s, const ck_seq& q, bool optional,
+                         const char* what) {
+  return seq_check_out(q, s.T, s.B, s.D, s.dtype, optional, what, kConvMaxStrideT);
+}
+
 struct ConvDims {
   int nv, vx, pairs, run, runs;
   int64_t vblocks, pblocks;  // workgroups over the channels, over the (row, run) pairs
@@ -486,7 +491,7 @@ extern "C" ck_status ck_conv_forward(const ck_conv_shape* shape, ck_seq x, const
     return CK_ERR_NULL_ARG;
   }
   rc = seq_check(x, shape->dtype, none, "x", kConvMaxStrideT);
-  if (rc == CK_OK) rc = seq_check(y, shape->dtype, none, "y", kConvMaxStrideT);
+  if (rc == CK_OK) rc = conv_check_out(*shape, y, none, "y");
   if (rc == CK_OK) rc = conv_check_state(state0, *shape, true, "state0");
   if (rc == CK_OK) rc = conv_check_state(state, *shape, true, "state");
   if (rc != CK_OK) return rc;
@@ -522,7 +527,7 @@ extern "C" ck_status ck_conv_backward(const ck_conv_shape* shape, ck_seq x, cons
   }
   rc = seq_check(x, shape->dtype, none, "x", kConvMaxStrideT);
   if (rc == CK_OK) rc = seq_check(grad_y, shape->dtype, none, "grad_y", kConvMaxStrideT);
-  if (rc == CK_OK) rc = seq_check(grad_x, shape->dtype, none, "grad_x", kConvMaxStrideT);
+  if (rc == CK_OK) rc = conv_check_out(*shape, grad_x, none, "grad_x");
   if (rc == CK_OK) rc = conv_check_state(state0, *shape, true, "state0");
   if (rc == CK_OK) rc = conv_check_state(grad_state, *shape, true, "grad_state");
   if (rc == CK_OK) rc = conv_check_state(grad_state0, *shape, true, "grad_state0");
@@ -567,7 +572,7 @@ extern "C" ck_status ck_conv_step(const ck_conv_shape* shape, ck_seq x, const fl
     return CK_ERR_NULL_ARG;
   }
   rc = seq_check(x, shape->dtype, false, "x", kConvMaxStrideT);
-  if (rc == CK_OK) rc = seq_check(y, shape->dtype, false, "y", kConvMaxStrideT);
+  if (rc == CK_OK) rc = conv_check_out(*shape, y, false, "y");
   if (rc == CK_OK) rc = conv_check_state(state0, *shape, true, "state0");
   if (rc == CK_OK) rc = conv_check_state(state, *shape, false, "state");
   if (rc != CK_OK) return rc;

@@ -120,7 +120,7 @@ ck_status drop_run(const ck_dropout_shape* s, const ck_seq& x, const ck_seq& res
   const bool none = s->T == 0;
   rc = seq_check(x, s->dtype, none, "the input");
   if (rc == CK_OK) rc = seq_check(res, s->dtype, true, "residual");
-  if (rc == CK_OK) rc = seq_check(out, s->dtype, none, "the output");
+  if (rc == CK_OK) rc = seq_check_out(out, s->T, s->B, s->D, s->dtype, none, "the output");
   if (rc != CK_OK || none) return rc;
   const uint32_t q = (uint32_t)std::floor(65536.0 * s->p + 0.5);
   return seq_dispatch(s->dtype, [&](auto* e) -> ck_status {

@@ -178,6 +178,11 @@ int64_t scan_max_stride(const ck_scan_shape& s, const ScanDims& d, int64_t row) 
   return (UINT32_MAX / (int64_t)seq_elem_bytes(s.dtype) - row) / (d.K - 1);
 }
 
+ck_status scan_check_out(const ck_scan_shape& s, const ScanDims& d, const ck_seq& q, bool optional,
+                         const char* what) {
+  return seq_check_out(q, s.T, s.B, s.D, s.dtype, optional, what, scan_max_stride(s, d, s.D));
+}
+
 // Sizes and inputs of a call; d: how it is spread over the chip.
 ck_status scan_check_inputs(const ck_scan_shape* shape, const ck_scan_inputs* in, ScanDims* d) {
   ck_status rc = scan_check_shape(shape);
@@ -260,8 +265,7 @@ extern "C" ck_status ck_scan_forward(const ck_scan_shape* shape, const ck_scan_i
   clear_error();
   ScanDims d;
   ck_status rc = scan_check_inputs(shape, in, &d);
-  if (rc == CK_OK)
-    rc = seq_check(out, shape->dtype, shape->T == 0, "out", scan_max_stride(*shape, d, d.D));
+  if (rc == CK_OK) rc = scan_check_out(*shape, d, out, shape->T == 0, "out");
   if (rc != CK_OK) return rc;
   const ScanWs ws = scan_ws(d, false);
   rc = seq_check_ws(workspace, workspace_bytes, ws.total);
@@ -292,14 +296,16 @@ extern "C" ck_status ck_scan_backward(const ck_scan_shape* shape, const ck_scan_
     set_error("grads, the gradient of A or saved is NULL");
     return CK_ERR_NULL_ARG;
   }
-  const int64_t most = scan_max_stride(*shape, d, d.D);
-  rc = seq_check(grad_out, shape->dtype, none, "grad_out", most);
-  if (rc == CK_OK) rc = seq_check(grads->u, shape->dtype, none, "the gradient of u", most);
-  if (rc == CK_OK) rc = seq_check(grads->delta, shape->dtype, none, "the gradient of delta", most);
-  if (rc == CK_OK) rc = seq_check(grads->b, shape->dtype, none, "the gradient of B");
-  if (rc == CK_OK) rc = seq_check(grads->c, shape->dtype, none, "the gradient of C");
+  rc = seq_check(grad_out, shape->dtype, none, "grad_out", scan_max_stride(*shape, d, d.D));
+  if (rc == CK_OK) rc = scan_check_out(*shape, d, grads->u, none, "the gradient of u");
+  if (rc == CK_OK) rc = scan_check_out(*shape, d, grads->delta, none, "the gradient of delta");
+  auto check_bc = [&](const ck_seq& q, const char* what) {
+    return seq_check_out(q, d.T, d.B, d.G * d.N, shape->dtype, none, what);
+  };
+  if (rc == CK_OK) rc = check_bc(grads->b, "the gradient of B");
+  if (rc == CK_OK) rc = check_bc(grads->c, "the gradient of C");
   if (rc == CK_OK)
-    rc = seq_check(grads->z, shape->dtype, none || !in->z.data, "the gradient of z", most);
+    rc = scan_check_out(*shape, d, grads->z, none || !in->z.data, "the gradient of z");
   if (rc != CK_OK) return rc;
   const ScanWs ws = scan_ws(d, true);
   rc = seq_check_ws(workspace, workspace_bytes, ws.total);
@@ -337,7 +343,7 @@ extern "C" ck_status ck_scan_step(const ck_scan_shape* shape, const ck_scan_inpu
   }
   ScanDims d;
   rc = scan_check_inputs(shape, in, &d);
-  if (rc == CK_OK) rc = seq_check(out, shape->dtype, false, "out");
+  if (rc == CK_OK) rc = scan_check_out(*shape, d, out, false, "out");
   if (rc != CK_OK) return rc;
   if (!state || in->lengths) {
     set_error(state ? "a step takes no lengths" : "state is NULL");

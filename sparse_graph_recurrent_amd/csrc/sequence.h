@@ -69,6 +69,21 @@ inline ck_status seq_check(const ck_seq& s, int dtype, bool optional, const char
   return CK_OK;
 }
 
+// An output: rows of `row` elements that would be written over one another (a zero
+// stride, as a broadcast tensor has) are refused.
+inline ck_status seq_check_out(const ck_seq& s, int64_t T, int64_t B, int64_t row, int dtype,
+                               bool optional, const char* what,
+                               int64_t max_stride_t = INT64_MAX) {
+  const ck_status rc = seq_check(s, dtype, optional, what, max_stride_t);
+  if (rc != CK_OK || !s.data) return rc;
+  if (T > 0 && ((T > 1 && s.stride_t < row) || (B > 1 && s.stride_b < row))) {
+    set_error("%s has strides (%lld, %lld): its rows of %lld elements overlap", what,
+              (long long)s.stride_t, (long long)s.stride_b, (long long)row);
+    return CK_ERR_BAD_VALUE;
+  }
+  return CK_OK;
+}
+
 inline ck_status seq_check_ws(const void* workspace, size_t bytes, size_t need) {
   if (need == 0) return CK_OK;
   if (!workspace) {

@@ -161,6 +161,33 @@ def test_step_strides_a_call_takes(L):
     assert conv(far(2**30)) == BAD_VALUE
 
 
+@pytest.mark.parametrize("st,sb", [(0, 64), (64, 0), (63, 64), (128, 63)])
+def test_outputs_over_one_another_are_refused(L, st, sb):
+    """An output that is the same memory at several steps or rows (a broadcast
+    tensor) has no one value; inputs may be broadcast."""
+    q = CkSeq(FAKE, st, sb)
+    s, one, i = _scan(), _scan(T=1), _inputs()
+    assert L.ck_scan_forward(s, i, q, None, None, FAKE, 2**40, None) == BAD_VALUE
+    for k in range(5):
+        v = [SEQ] * 5
+        v[k] = q if k not in (2, 3) else CkSeq(FAKE, st // 4, sb // 4)  # 16 values a row
+        g = ctypes.byref(ScanGrads(*v, FAKE, None, None, None))
+        assert L.ck_scan_backward(s, _inputs(z=q), FAKE, q, None, g, FAKE, 0, None) == BAD_VALUE
+    g = ctypes.byref(ScanGrads(*[SEQ] * 5, FAKE, None, None, None))
+    assert L.ck_scan_backward(s, _inputs(u=q, b=q, z=q), FAKE, q, None, g, FAKE, 0,
+                              None) == WORKSPACE
+    assert L.ck_conv_forward(_conv(), SEQ, FAKE, None, None, None, q, None, None) == BAD_VALUE
+    back = lambda gy, gx: L.ck_conv_backward(_conv(), q, FAKE, None, None, None, gy, None, gx,
+                                             FAKE, None, None, FAKE, 0, None)
+    assert back(q, q) == BAD_VALUE and back(q, SEQ) == WORKSPACE
+    d = ctypes.byref(DropoutShape(8, 2, 64, 1, 0, 0.5, 1, 0, None))
+    assert L.ck_dropout_forward(d, SEQ, NONE, q, None) == BAD_VALUE
+    assert L.ck_dropout_backward(d, SEQ, q, None) == BAD_VALUE
+    if sb < 64:  # a step has no stride between steps
+        assert L.ck_scan_step(one, i, q, FAKE, None) == BAD_VALUE
+        assert L.ck_conv_step(_conv(T=1), SEQ, FAKE, None, None, q, FAKE, None) == BAD_VALUE
+
+
 def test_scan_call_refusals(L):
     g = ctypes.byref(ScanGrads(SEQ, SEQ, SEQ, SEQ, NONE, FAKE, None, None, None))
     s, i = _scan(), _inputs()
