@@ -322,7 +322,7 @@ template <int W>
 __global__ __launch_bounds__(256) void conv_sum(const float* part, int D, int64_t parts,
                                                 float* gw, float* gbias) {
   __shared__ float red[8][32];
-  const int64_t n = (int64_t)D * (W + 1), i = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
+  const int64_t n = (int64_t)D * (W + 1), i = seq_block() * 32 + (threadIdx.x & 31);
   const int y = threadIdx.x >> 5;
   const int64_t each = (parts + 7) / 8, r0 = each * y, r1 = min(r0 + each, parts);
   float sum = 0.0f;
@@ -363,7 +363,7 @@ __device__ __forceinline__ void conv_one_row(const ConvArgs<E>& s, const ConvPla
 
 template <typename E, int W>
 __global__ __launch_bounds__(kConvThreads) void conv_one(const ConvArgs<E> s) {
-  const int64_t i0 = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
+  const int64_t i0 = seq_block() * kConvThreads + threadIdx.x;
   if (i0 >= (int64_t)s.B * s.nv) return;
   ConvPlace p = {};
   p.b = (int)(i0 / s.nv);
@@ -373,37 +373,6 @@ __global__ __launch_bounds__(kConvThreads) void conv_one(const ConvArgs<E> s) {
     conv_one_row<true, W>(s, p);
   else
     conv_one_row<false, W>(s, p);
-}
-
-ck_status conv_check_shape(const ck_conv_shape* s) {
-  if (!s) {
-    set_error("shape is NULL");
-    return CK_ERR_NULL_ARG;
-  }
-  const ck_status rc = seq_check_shape(s->T, s->B, s->D, s->dtype);
-  if (rc != CK_OK) return rc;
-  if (s->W < 1 || s->W > kConvMaxW) {
-    set_error("W must be in [1, 8] (got %lld)", (long long)s->W);
-    return CK_ERR_BAD_SIZE;
-  }
-  // workgroups of one launch
-  const int64_t pairs = s->B * (s->T / kConvRun + 1), nv = (s->D + kConvV - 1) / kConvV;
-  if ((pairs / 4 + 1) > INT_MAX / (nv / 32 + 1)) {
-    set_error("T=%lld, B=%lld or D=%lld is too large", (long long)s->T, (long long)s->B,
-              (long long)s->D);
-    return CK_ERR_TOO_LARGE;
-  }
-  return CK_OK;
-}
-
-ck_status conv_check_state(const void* p, const ck_conv_shape& s, bool optional, const char* what) {
-  if (s.W == 1) return CK_OK;  // a state of no elements
-  return seq_check(ck_seq{const_cast<void*>(p), 0, 0}, s.dtype, optional, what);
-}
-
-ck_status conv_check_out(const ck_conv_shape& s, const ck_seq& q, bool optional,
-                         const char* what) {
-  return seq_check_out(q, s.T, s.B, s.D, s.dtype, optional, what, kConvMaxStrideT);
 }
 
 struct ConvDims {
@@ -422,6 +391,37 @@ ConvDims conv_dims(const ck_conv_shape& s, int run) {
   d.runs = (int)std::max<int64_t>((s.T + run - 1) / run, 1);
   d.pblocks = (s.B * d.runs + d.pairs - 1) / d.pairs;
   return d;
+}
+
+ck_status conv_check_shape(const ck_conv_shape* s) {
+  if (!s) {
+    set_error("shape is NULL");
+    return CK_ERR_NULL_ARG;
+  }
+  const ck_status rc = seq_check_shape(s->T, s->B, s->D, s->dtype);
+  if (rc != CK_OK) return rc;
+  if (s->W < 1 || s->W > kConvMaxW) {
+    set_error("W must be in [1, 8] (got %lld)", (long long)s->W);
+    return CK_ERR_BAD_SIZE;
+  }
+  // (the backward's runs are no shorter)
+  const ConvDims d = conv_dims(*s, kConvRun);
+  if (d.pblocks >= kSeqMaxThreads / kConvThreads / d.vblocks) {
+    set_error("T=%lld, B=%lld or D=%lld is too large", (long long)s->T, (long long)s->B,
+              (long long)s->D);
+    return CK_ERR_TOO_LARGE;
+  }
+  return CK_OK;
+}
+
+ck_status conv_check_state(const void* p, const ck_conv_shape& s, bool optional, const char* what) {
+  if (s.W == 1) return CK_OK;  // a state of no elements
+  return seq_check(ck_seq{const_cast<void*>(p), 0, 0}, s.dtype, optional, what);
+}
+
+ck_status conv_check_out(const ck_conv_shape& s, const ck_seq& q, bool optional,
+                         const char* what) {
+  return seq_check_out(q, s.T, s.B, s.D, s.dtype, optional, what, kConvMaxStrideT);
 }
 
 ConvDims conv_dims_backward(const ck_conv_shape& s) {
@@ -549,7 +549,7 @@ extern "C" ck_status ck_conv_backward(const ck_conv_shape* shape, ck_seq x, cons
       a.part = static_cast<float*>(workspace);
       a.nv = d.nv; a.vx = d.vx; a.pairs = d.pairs; a.run = d.run; a.runs = d.runs;
       conv_bwd<E, W><<<(unsigned)(d.vblocks * d.pblocks), kConvThreads, 0, stream>>>(a);
-      conv_sum<W><<<(unsigned)((shape->D * (W + 1) + 31) / 32), 256, 0, stream>>>(
+      conv_sum<W><<<seq_grid((shape->D * (W + 1) + 31) / 32), 256, 0, stream>>>(
           a.part, a.D, d.pblocks, grad_weight, grad_bias);
     });
     CK_HIP_TRY(hipGetLastError());
@@ -585,8 +585,8 @@ extern "C" ck_status ck_conv_step(const ck_conv_shape* shape, ck_seq x, const fl
       a.state = W > 1 ? static_cast<E*>(state) : nullptr;
       a.nv = (int)((shape->D + kConvV - 1) / kConvV);
       const int64_t n = shape->B * a.nv;
-      conv_one<E, W><<<(unsigned)((n + kConvThreads - 1) / kConvThreads), kConvThreads, 0,
-                          stream>>>(a);
+      conv_one<E, W><<<seq_grid((n + kConvThreads - 1) / kConvThreads), kConvThreads, 0,
+                       stream>>>(a);
     });
     CK_HIP_TRY(hipGetLastError());
     return CK_OK;

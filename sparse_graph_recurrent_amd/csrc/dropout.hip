@@ -73,7 +73,7 @@ __device__ __forceinline__ void drop_rows(const DropArgs<E>& s, const uint32_t (
 
 template <typename E, bool HELD>
 __global__ __launch_bounds__(kDropThreads) void drop(const DropArgs<E> s) {
-  const int64_t i = (int64_t)blockIdx.x * kDropThreads + threadIdx.x;
+  const int64_t i = seq_block() * kDropThreads + threadIdx.x;
   const int col = (int)(i % s.cols);
   const int64_t r = i / s.cols;
   const int b = (int)(r % s.B), run = (int)(r / s.B);
@@ -139,7 +139,7 @@ ck_status drop_run(const ck_dropout_shape* s, const ck_seq& x, const ck_seq& res
     a.q = q;
     a.scale = q < 65536 ? (float)(65536.0 / (65536.0 - q)) : 0.0f;
     const int64_t n = (s->held ? (int64_t)a.runs * s->B : rows) * cols;
-    const unsigned grid = (unsigned)((n + kDropThreads - 1) / kDropThreads);
+    const dim3 grid = seq_grid((n + kDropThreads - 1) / kDropThreads);
     if (s->held)
       drop<E, true><<<grid, kDropThreads, 0, stream>>>(a);
     else

@@ -116,7 +116,7 @@ __device__ __forceinline__ void scan_one_row(const ScanArgs<E>& s, int b, int d,
 
 template <typename E, int NL>
 __global__ __launch_bounds__(kOneThreads) void scan_one(const ScanArgs<E> s) {
-  const int64_t i = (int64_t)blockIdx.x * (kOneThreads / 4) + (threadIdx.x >> 2);
+  const int64_t i = seq_block() * (kOneThreads / 4) + (threadIdx.x >> 2);
   if (i >= (int64_t)s.B * s.D) return;  // whole quads
   const int b = (int)(i / s.D), d = (int)(i % s.D), q = threadIdx.x & 3;
   if (s.N == 4 * NL)
@@ -160,7 +160,7 @@ ck_status scan_check_shape(const ck_scan_shape* s) {
     return CK_ERR_BAD_SIZE;
   }
   const ScanDims d = scan_sizes(*s);
-  if (d.P * d.G * d.B >= INT_MAX / 2 || d.B * d.D / 64 >= INT_MAX || d.D * d.NP >= INT_MAX ||
+  if (d.P * d.G * d.B >= kSeqMaxThreads / kScanThreads || d.D * d.NP >= INT_MAX ||
       d.G * d.N > (int64_t(1) << 28) ||  // (byte offsets in a step of B or C: 32 bits)
       (d.T > 0 && d.B * d.G * d.NP >= (int64_t(1) << 36) / d.T)) {
     set_error("B=%lld, D=%lld or T=%lld is too large", (long long)d.B, (long long)d.D,
@@ -235,7 +235,7 @@ ScanArgs<E> scan_args(const ck_scan_shape& s, const ScanDims& d, const ck_scan_i
 template <typename E, int NL>
 void scan_launch_one(const ScanArgs<E>& a, hipStream_t stream) {
   const int64_t n = (int64_t)a.B * a.D, per = kOneThreads / 4;
-  scan_one<E, NL><<<(unsigned)((n + per - 1) / per), kOneThreads, 0, stream>>>(a);
+  scan_one<E, NL><<<seq_grid((n + per - 1) / per), kOneThreads, 0, stream>>>(a);
 }
 
 }  // namespace

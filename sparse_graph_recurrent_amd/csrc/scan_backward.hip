@@ -492,10 +492,11 @@ __device__ __forceinline__ void sum_a(const ScanArgs<E>& s, int NP, int parts, i
 template <typename E>
 __global__ __launch_bounds__(256) void scan_sums(const ScanArgs<E> s, int NP, int parts,
                                                   unsigned a_wgs) {
-  if (blockIdx.x < a_wgs)
-    sum_a(s, NP, parts, (int64_t)blockIdx.x * 32);
+  const int64_t wg = seq_block();
+  if (wg < a_wgs)
+    sum_a(s, NP, parts, wg * 32);
   else
-    sum_bc(s, NP, (int64_t)(blockIdx.x - a_wgs) * 256 + threadIdx.x);
+    sum_bc(s, NP, (wg - a_wgs) * 256 + threadIdx.x);
 }
 
 template <typename E, int NP, int TW>
@@ -528,7 +529,7 @@ void launch(const ScanDims& d, const ScanArgs<E>& a, hipStream_t stream) {
   if (!d.waves) launch_main<E, NP, 1>(grid, a, stream);
   const int64_t bc = d.T * d.B * d.G * 2 * d.NP, ae = d.D * (d.NP + 2);
   const unsigned a_wgs = (unsigned)((ae + 31) / 32);
-  scan_sums<E><<<a_wgs + (unsigned)((bc + 255) / 256), 256, 0, stream>>>(a, d.NP, parts, a_wgs);
+  scan_sums<E><<<seq_grid(a_wgs + (bc + 255) / 256), 256, 0, stream>>>(a, d.NP, parts, a_wgs);
 }
 
 }  // namespace

@@ -29,13 +29,15 @@ ck_status seq_dispatch(int dtype, F&& fn) {
 }
 
 // T >= 0 steps (an empty window is allowed), B and D positive, and every
-// count the kernels hold in 32 bits below 2^31.
+// count the kernels hold in 32 bits below 2^31, with room for the ends of tiles,
+// runs and workgroups that lie past T or D.
 inline ck_status seq_check_shape(int64_t T, int64_t B, int64_t D, int dtype) {
   if (T < 0 || B <= 0 || D <= 0) {
     set_error("bad sizes: T=%lld B=%lld D=%lld", (long long)T, (long long)B, (long long)D);
     return CK_ERR_BAD_SIZE;
   }
-  if (T >= INT_MAX || B >= INT_MAX || D >= INT_MAX || B * D >= (int64_t(1) << 36) ||
+  constexpr int64_t most = INT_MAX - 1024;
+  if (T > most || B > most || D > most || B * D >= (int64_t(1) << 36) ||
       (T > 0 && B * D > (int64_t(1) << 46) / T)) {
     set_error("T=%lld, B=%lld or D=%lld is too large", (long long)T, (long long)B, (long long)D);
     return CK_ERR_TOO_LARGE;
@@ -82,6 +84,19 @@ inline ck_status seq_check_out(const ck_seq& s, int64_t T, int64_t B, int64_t ro
     return CK_ERR_BAD_VALUE;
   }
   return CK_OK;
+}
+
+// A launch holds fewer than 2^32 threads along a dimension of its grid.
+constexpr int64_t kSeqMaxThreads = int64_t(1) << 32;
+// Workgroups whose kernel takes its number from seq_block(), and leaves when there is
+// nothing for it, go on in the grid's second dimension.
+constexpr int64_t kSeqGridX = int64_t(1) << 22;
+inline dim3 seq_grid(int64_t workgroups) {
+  if (workgroups <= kSeqGridX) return dim3((unsigned)workgroups);
+  return dim3((unsigned)kSeqGridX, (unsigned)((workgroups + kSeqGridX - 1) / kSeqGridX));
+}
+__device__ __forceinline__ int64_t seq_block() {
+  return (int64_t)blockIdx.y * kSeqGridX + blockIdx.x;
 }
 
 inline ck_status seq_check_ws(const void* workspace, size_t bytes, size_t need) {

@@ -769,6 +769,60 @@ def test_long_step_strides():
     torch.cuda.empty_cache()  # (some 30 GB of it)
 
 
+def test_more_workgroups_than_a_grid_dimension_holds():
+    """Launches that go on in the grid's second dimension (from 2^22 workgroups on)."""
+    # dropout, 2^20 + 1024 rows of 8192 channels, in place
+    T, B, D = 1025, 1024, 8192
+    x = torch.ones(T, B, D, dtype=torch.bfloat16, device="cuda")
+    sgr.dropout_forward(x, 0.25, 7, 3, out=x)
+    for t, b in ((0, 0), (1023, 1023), (1024, 0), (1024, 1023)):
+        ctr = np.zeros((D // 8, 4), np.uint64)
+        ctr[:, 0], ctr[:, 1], ctr[:, 2] = np.arange(D // 8), t * B + b, 3
+        w = ref.philox(ctr, (7, 0))
+        r = np.stack([w & np.uint64(0xFFFF), w >> np.uint64(16)], -1).reshape(D)
+        want = torch.from_numpy(np.where(r >= 16384, 65536 / 49152, 0.0)).bfloat16()
+        assert torch.equal(x[t, b].cpu(), want), (t, b)
+    del x
+    # sums of the gradients of B and C, 4097 x 256 x 64 groups; rows are independent
+    T, B, D = 4097, 256, 64
+    mk = lambda *shape: torch.randn(*shape, device="cuda").bfloat16()
+    u, go = mk(T, B, D), mk(T, B, D)
+    bm, cm = mk(T, B, D, 1), mk(T, B, D, 1)
+    delta, A = 0.1 * u.abs() + 0.1, -torch.ones(D, 1, device="cuda")
+
+    def grads(rows):
+        a = (u[:, rows], delta[:, rows], A, bm[:, rows], cm[:, rows])
+        saved = sgr.selective_scan_forward(*a)[2]
+        return sgr.selective_scan_backward(*a, saved, go[:, rows])
+
+    whole = grads(slice(0, B))
+    for rows in (slice(0, 8), slice(B - 8, B)):
+        few = grads(rows)
+        for k in ("g_B", "g_C", "g_u"):
+            assert torch.equal(whole[k][:, rows], few[k]), (k, rows)
+    assert torch.isfinite(whole["g_A"]).all()
+    del u, go, bm, cm, delta, whole, few
+    # single tokens: 2^28 + 1024 channels, 2^32 + 4096 channels
+    B, D = 2**18 + 1, 1024
+    a = [mk(B, D), mk(B, D), -torch.ones(D, 1, device="cuda"), mk(B, 1, 1), mk(B, 1, 1)]
+    state = torch.randn(B, D, 1, device="cuda")
+    out, new = sgr.selective_scan_step(state, *a, new_state=torch.empty_like(state))
+    for rows in (slice(0, 2), slice(B - 2, B)):
+        one, s1 = sgr.selective_scan_step(state[rows].clone(), a[0][rows], a[1][rows], a[2],
+                                          a[3][rows], a[4][rows])
+        assert torch.equal(out[rows], one) and torch.equal(new[rows], s1), rows
+    del a, state, out, new
+    B, D = 2**20 + 1, 4096
+    x = torch.empty(B, D, dtype=torch.bfloat16, device="cuda").uniform_(-1, 1)
+    w, state = torch.randn(D, 2, device="cuda"), x.unsqueeze(0) * 0.5
+    y, new = sgr.short_conv_step(state, x, w, new_state=torch.empty_like(state))
+    for rows in (slice(0, 2), slice(B - 2, B)):
+        one, s1 = sgr.short_conv_step(state[:, rows].contiguous(), x[rows], w)
+        assert torch.equal(y[rows], one) and torch.equal(new[:, rows], s1), rows
+    del x, state, y, new
+    torch.cuda.empty_cache()
+
+
 def test_captured_graph_replays():
     """Forward, backward and tokens in one HIP graph: every replay equals the
     eager result on the inputs of that moment, with eager work between."""

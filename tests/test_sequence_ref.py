@@ -131,6 +131,23 @@ def test_scan_input_refusals(L, kw, status):
     assert L.ck_scan_step(_scan(T=1), _inputs(**kw), SEQ, FAKE, None) == status
 
 
+def test_sizes_beyond_the_kernels_counts_are_refused(L):
+    """32-bit steps and channels need room for a tile's or workgroup's end, and a
+    launch has fewer than 2^32 threads: sizes that were taken until they did not
+    launch, or wrapped."""
+    s = ctypes.c_size_t()
+    end = 2**31 - 8
+    for kw in (dict(T=end, B=1, D=1), dict(T=1, B=2**24, D=64), dict(T=1, B=2**18, D=64 * 64, G=64)):
+        assert L.ck_scan_sizes(_scan(N=1, **kw), ctypes.byref(s), None, None) == TOO_LARGE, kw
+    assert L.ck_scan_sizes(_scan(N=1, T=1, B=2**24 - 1), ctypes.byref(s), None, None) == 0
+    for kw in (dict(T=end, B=1, D=1), dict(T=1, B=1, D=end), dict(T=1, B=2**24, D=2**11)):
+        assert L.ck_conv_sizes(_conv(**kw), ctypes.byref(s)) == TOO_LARGE, kw
+    assert L.ck_conv_sizes(_conv(T=1, B=2**22, D=2**11), ctypes.byref(s)) == 0
+    for T, D in ((end, 1), (1, end)):
+        d = ctypes.byref(DropoutShape(T, 1, D, 1, 0, 0.5, 1, 0, None))
+        assert L.ck_dropout_forward(d, NONE, NONE, NONE, None) == TOO_LARGE
+
+
 def test_step_strides_a_call_takes(L):
     """Long strides are refused only where a kernel's offsets end.  (What is taken is
     seen by the next refusal, the workspace's: nothing runs.)"""
