@@ -188,6 +188,11 @@ def _dense(shape, inner: int):
     return inner * shape[1] if shape[0] > 1 else 0, inner if shape[1] > 1 else 0
 
 
+# Tells autograd that tensors (a tuple of them) were written: a backward that saved
+# what one held before raises, as it does behind torch's own in-place operations.
+_written = torch._C._increment_version
+
+
 def _out_seq(t, name: str, like: torch.Tensor):
     """(tensor, its ck_seq) of an output of like's [.., D] shape: the caller's,
     checked, or a new contiguous one."""
@@ -195,14 +200,18 @@ def _out_seq(t, name: str, like: torch.Tensor):
     if t is None:
         t = _fresh(like)
         return t, CkSeq(t.data_ptr(), *_dense(shape, shape[-1]))
-    return t, CkSeq(*_seq(t, name, like.dtype, like.get_device(), shape))
+    q = CkSeq(*_seq(t, name, like.dtype, like.get_device(), shape))
+    _written((t,))
+    return t, q
 
 
 def _out_par(t, name: str, like: torch.Tensor, shape, dtype=torch.float32, model=None):
     """(tensor, its address) of a contiguous output; `model`: a contiguous tensor
     of its shape and type, if there is one (quicker to copy)."""
     if t is not None:
-        return t, _par(t, name, like.get_device(), shape, dtype)
+        at = _par(t, name, like.get_device(), shape, dtype)
+        _written((t,))
+        return t, at
     t = like.new_empty(shape, dtype=dtype) if model is None else torch.empty_like(model)
     return t, t.data_ptr()
 
@@ -325,6 +334,7 @@ def selective_scan_backward(u, delta, A, B, C, saved, grad_out, D=None, z=None, 
             _par(g.get("g_A"), "g_A", dev, A.shape), _par(g.get("g_D"), "g_D", dev, (ch,)),
             _par(g.get("g_delta_bias"), "g_delta_bias", dev, (ch,)),
             _par(g.get("g_state0"), "g_state0", dev, ss))
+        _written(tuple(t for t in g.values() if t is not None))
     workspace, wp, wn = _buffer(workspace, wb, u, "workspace")
     _call(lib().ck_scan_backward, dev, (shape, inputs, sp, go, gs, out, wp, wn))
     return g
@@ -346,6 +356,7 @@ def selective_scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=Non
     out, os = _out_seq(out, "out", u)
     _call(lib().ck_scan_step, dev,
           (shape, inputs, os, _par(new_state, "new_state", dev, (rows, ch, N))))
+    _written((new_state,))
     return out, new_state
 
 
@@ -461,6 +472,7 @@ def short_conv_backward(x, weight, grad_y, bias=None, state0=None, lengths=None,
         gw = _par(g["g_weight"], "g_weight", dev, weight.shape)
         gb = _par(g.get("g_bias"), "g_bias", dev, (ss[2],))
         gs0 = _par(g.get("g_state0"), "g_state0", dev, ss, x.dtype)
+        _written(tuple(t for t in g.values() if t is not None))
     workspace, wp, wn = _buffer(workspace, _conv_sizes(shape), x, "workspace")
     _call(lib().ck_conv_backward, dev,
           (shape, xs, w, b, s0,
@@ -483,6 +495,8 @@ def short_conv_step(state, x, weight, bias=None, activation=None, y=None, new_st
     _call(lib().ck_conv_step, dev,
           (shape, xs, w, b, _par(state, "state", dev, ss, x.dtype), ys,
            _par(new_state, "new_state", dev, ss, x.dtype)))
+    if new_state is not None:
+        _written((new_state,))
     return y, new_state
 
 

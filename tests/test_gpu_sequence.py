@@ -707,6 +707,53 @@ def test_dropout_nan_counter_in_place_and_autograd():
     assert torch.equal(sgr.dropout_forward(x[0], 0.4, 7, 3), sgr.dropout_forward(x[:1], 0.4, 7, 3)[0])
 
 
+def test_a_write_into_a_saved_tensor_is_seen():
+    """What a call writes into, a pending backward may have saved: it raises, as
+    behind torch's in-place operations, and does not use the new values."""
+    x = torch.randn(5, 2, 8, device="cuda")
+    w = torch.randn(8, 4, device="cuda", requires_grad=True)
+    A, b = -torch.ones(8, 2, device="cuda"), torch.randn(5, 2, 1, 2, device="cuda")
+    h = torch.zeros(2, 8, 2, device="cuda")
+
+    def fresh():
+        s0 = torch.randn(3, 2, 8, device="cuda")
+        y, _ = sgr.short_conv(x, w, state0=s0)
+        return y.sum(), s0
+
+    def pending(shape):
+        t = torch.randn(shape, device="cuda")
+        return (t * torch.ones_like(t).requires_grad_()).sum(), t
+
+    def cases():
+        loss, s0 = fresh()
+        yield loss, lambda: sgr.short_conv_step(s0, x[0], w.detach())
+        loss, t = pending((2, 8, 2))
+        yield loss, lambda: sgr.selective_scan_step(t, x[0], x[0], A, b[0], b[0])
+        for call in (lambda t: sgr.dropout_forward(t, 0.5, 1, out=t),
+                     lambda t: sgr.dropout_backward(t, 0.5, 1, grad_x=t),
+                     lambda t: sgr.short_conv_forward(x, w.detach(), y=t),
+                     lambda t: sgr.selective_scan_forward(x, x, A, b, b, out=t),
+                     lambda t: sgr.short_conv_step(fresh()[1], x[0], w.detach(), y=t[0])):
+            loss, t = pending((5, 2, 8))
+            yield loss, lambda: call(t)
+        loss, t = pending((2, 8, 2))
+        yield loss, lambda: sgr.selective_scan_forward(x, x, A, b, b, state=t)
+        loss, t = pending((5, 2, 8))
+        g = sgr.short_conv_backward(x, w.detach(), x)
+        yield loss, lambda: sgr.short_conv_backward(x, w.detach(), x, grads=dict(g, g_x=t))
+        loss, t = pending((8, 2))
+        f = sgr.selective_scan_forward(x, x, A, b, b)
+        g = sgr.selective_scan_backward(x, x, A, b, b, f[2], x)
+        yield loss, lambda: sgr.selective_scan_backward(x, x, A, b, b, f[2], x,
+                                                        grads=dict(g, g_A=t))
+
+    for i, (loss, write) in enumerate(cases()):
+        write()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+            pytest.fail(f"case {i}")
+
+
 # --------------------------------------------------- large offsets and graphs
 
 def test_offsets_past_32_bits():
