@@ -14,6 +14,8 @@ recurrence's products and hardware functions (the decay's error, relative
 the gradients, whose terms hold a state and an adjoint, and the additions
 across channels, rows and steps.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -21,6 +23,7 @@ import torch
 import sequence_ref as ref
 import sparse_graph_recurrent_amd as sgr
 from gpu_helpers import log
+from sparse_graph_recurrent_amd import sequence
 
 pytestmark = pytest.mark.gpu
 
@@ -456,6 +459,110 @@ def test_scan_autograd_with_shared_inputs():
         assert (g.grad.double().cpu() - w.grad).abs().max().item() <= 1e-5 * scale, name
 
 
+# several tiles a workgroup, a workgroup each, cut; rows and states that fill nothing
+GIVEN = [
+    (21, 3, 70, 13, 7, "bf16", True, True, [21, 0, 10], "time"),
+    (13, 390, 9, 5, 1, "fp32", False, True, None, "batch"),
+    (140, 2, 66, 20, 3, "fp16", True, True, [140, 77], "time"),
+]
+
+
+def given(like, fill=7.0):
+    """(a tensor of like's shape inside a wider storage of another order, batch
+    outermost and one element past an aligned address; that storage)"""
+    T, B = like.shape[:2]
+    n = like[0, 0].numel()
+    store = torch.full((B, T + 1, n + 3), fill, dtype=like.dtype, device="cuda")
+    return store[:, :T, 1:1 + n].transpose(0, 1).unflatten(2, like.shape[2:]), store
+
+
+def untouched(store, n, fill=7.0):
+    return bool((store[:, -1] == fill).all() and (store[..., 0] == fill).all() and
+                (store[..., 1 + n:] == fill).all())
+
+
+@pytest.mark.parametrize("case", GIVEN, ids=lambda c: "-".join(map(str, c[:6])))
+def test_scan_into_given_tensors(case):
+    """The caller's outputs, gradients (strided), saved states and workspaces get the
+    bits that tensors made by the calls get, and nothing beside them is written."""
+    g, p = scan_problem(31, *case)
+    softplus = case[7]
+    args = (g["u"], g["delta"], g["A"], g["B"], g["C"])
+    opt = dict(D=g["D"], z=g.get("z"), delta_bias=g["delta_bias"], lengths=g["lengths"],
+               delta_softplus=softplus)
+    scan_check(g, p, softplus)
+    want = sgr.selective_scan_forward(*args, state0=g["state0"], **opt)
+    wg = sgr.selective_scan_backward(*args, want[2], g["go"], grad_state=g["gstate"], **opt)
+    sb, fb, bb = sgr.selective_scan_sizes(*g["u"].shape, case[3], case[4], g["u"].dtype)
+    out, so = given(g["u"])
+    state = torch.full_like(g["state0"], 7.0)
+    buf = lambda n: torch.full((max(n, 1) + 256,), 0x5A, dtype=torch.uint8, device="cuda")
+    saved, fw, bw = buf(sb), buf(fb), buf(bb)
+    r = sgr.selective_scan_forward(*args, state0=g["state0"], out=out, state=state, saved=saved,
+                                   workspace=fw, **opt)
+    assert r[0] is out and r[1] is state and r[2] is saved and r[3] is fw
+    assert torch.equal(out, want[0]) and torch.equal(state, want[1])
+    assert untouched(so, case[2])
+    for b, n in ((saved, sb), (fw, fb)):
+        assert bool((b[n:] == 0x5A).all())
+    grads, stores = {}, {}
+    for k, t in wg.items():
+        if k in ("g_u", "g_delta", "g_B", "g_C", "g_z"):
+            grads[k], stores[k] = given(t)
+        else:
+            grads[k] = torch.full_like(t, 7.0)
+    assert sgr.selective_scan_backward(*args, saved, g["go"], grad_state=g["gstate"], grads=grads,
+                                       workspace=bw, **opt) is grads
+    for k, t in wg.items():
+        assert torch.equal(grads[k], t), k
+    for k, s in stores.items():
+        assert untouched(s, wg[k][0, 0].numel()), k
+    assert bool((bw[bb:] == 0x5A).all())
+    # gradients that are not wanted
+    some = {k: v for k, v in grads.items() if k not in ("g_D", "g_delta_bias", "g_state0")}
+    sgr.selective_scan_backward(*args, saved, g["go"], grad_state=g["gstate"], grads=some, **opt)
+    assert all(torch.equal(some[k], wg[k]) for k in some)
+    for kw in (dict(saved=saved[:sb - 1]), dict(workspace=fw[:fb - 1] if fb else fw[::2]),
+               dict(out=out[:-1]), dict(state=state[:, :, :-1]),
+               dict(out=g["u"].new_empty(1, *g["u"].shape[1:]).expand_as(g["u"]))):
+        with pytest.raises((ValueError, sgr.CkError)):
+            sgr.selective_scan_forward(*args, state0=g["state0"], **kw, **opt)
+    for kw in (dict(workspace=bw[:bb - 1]), dict(grads=dict(grads, g_A=g["A"][:, :-1])),
+               dict(grads=dict(grads, g_B=grads["g_B"][:-1])), dict(saved=saved[:sb - 1])):
+        s = kw.pop("saved", saved)
+        with pytest.raises(ValueError):
+            sgr.selective_scan_backward(*args, s, g["go"], **kw, **opt)
+
+
+@pytest.mark.parametrize("case", GIVEN, ids=lambda c: "-".join(map(str, c[:6])))
+def test_scan_autograd_reaches_every_input(case):
+    """The node's gradients of all inputs, with lengths, against the definition's;
+    parameters in another order of storage."""
+    T, B, D, N, G, dtype, gate, softplus, lengths, _ = case
+    g, p = scan_problem(32, *case, nan=False)
+    leaf = lambda t: t.detach().clone().requires_grad_()
+    turned = lambda t: t.transpose(-1, -2).contiguous().transpose(-1, -2).detach().requires_grad_()
+    names = ["u", "delta", "A", "B", "C", "D", "delta_bias", "state0"] + (["z"] if gate else [])
+    t = {k: (turned if k in ("A", "state0", "B") else leaf)(g[k]) for k in names}
+    out, state = sgr.selective_scan(t["u"], t["delta"], t["A"], t["B"], t["C"], t["D"], t.get("z"),
+                                    t["delta_bias"], t["state0"], g["lengths"], softplus)
+    got = torch.autograd.grad((out, state), [t[k] for k in names], (g["go"], g["gstate"]))
+    want, mag = ref.scan(p), ref.scan(p, magnitude=True)
+    close(out, want["out"], mag["out"], 32 + 8 * T, "out")
+    for k, gr in zip(names, got):
+        close(gr, want["g_" + k], mag["g_" + k], 64 + 16 * T + B + 64, k)
+    # the state alone, and out alone
+    def run(no):
+        o, s = sgr.selective_scan(t["u"], t["delta"], t["A"], t["B"], t["C"], t["D"], t.get("z"),
+                                  t["delta_bias"], t["state0"], g["lengths"], softplus)
+        return torch.autograd.grad(*((s, t["state0"], g["gstate"]) if no == "out" else
+                                     (o, t["state0"], g["go"])))[0]
+    for no, zero in (("out", "go"), ("state", "gstate")):
+        q = dict(p, **{zero: np.zeros_like(p[zero])})
+        close(run(no), ref.scan(q)["g_state0"], ref.scan(q, magnitude=True)["g_state0"],
+              128 + 16 * T + B, no)
+
+
 # --------------------------------------------------------------- convolution
 
 def conv_problem(seed, T, B, D, W, dtype, silu, lengths, layout, state0=True, bias=True):
@@ -520,6 +627,47 @@ def test_conv(case, full):
     # sums over all steps and rows in runs and pieces of them
     for k, n in (("g_x", W), ("g_state0", W), ("g_weight", T * B), ("g_bias", T * B)):
         close(grads[k], want[k], mag[k], 24 + 2 * W + n, k)
+
+
+# Backward runs longer than the 16 steps that few rows get: T, B, D, W, dtype, silu,
+# and the run that these sizes select (no shorter one gives as few workgroups); T
+# ends inside a run.
+LONG_RUNS = [
+    (81, 19558, 5, 4, "fp32", True, 20),
+    (101, 39116, 3, 4, "bf16", True, 24),
+    (121, 13004, 7, 7, "bf16", True, 28),
+    (201, 13004, 6, 8, "fp32", True, 44),
+    (221, 39116, 1, 3, "fp16", False, 48),
+]
+
+
+@pytest.mark.parametrize("case", LONG_RUNS, ids=lambda c: "-".join(map(str, c)))
+def test_conv_long_runs(case):
+    T, B, D, W, dtype, silu, run = case
+    log(f"conv long runs {case}")
+    # the workspace has a row of partial sums for each of the backward's workgroups along
+    # time and rows: 256 threads, one run of 4 channels each
+    def workgroups(run):
+        return -(-B * -(-T // run) // (256 // -(-D // 4)))
+    need = ctypes.c_size_t()
+    sgr.lib().ck_conv_sizes(ctypes.byref(sequence.ConvShape(
+        T, B, D, W, sequence._DTYPES[DT[dtype]], int(silu))), ctypes.byref(need))
+    assert need.value == workgroups(run) * D * (W + 1) * 4
+    assert workgroups(run) not in {workgroups(shorter) for shorter in range(16, run, 4)}
+    # texts that end at a run's end, within W - 1 steps of it, anywhere and nowhere
+    r = np.random.default_rng(7)
+    ends = np.array([run * k + e for k in range(1, T // run + 1) for e in range(-W, W + 1)])
+    lengths = np.where(r.random(B) < 0.5, r.choice(ends, B), r.integers(0, T + 1, B))
+    lengths[::3] = T
+    g, p = conv_problem(7, T, B, D, W, dtype, silu, np.minimum(lengths, T).tolist(), "time")
+    want, mag = ref.conv(p), ref.conv(p, magnitude=True)
+    _, state, grads = conv_run(g, silu)
+    torch.cuda.synchronize()
+    assert np.array_equal(state.double().cpu().numpy(), want["state"])
+    # sums: a run's steps, a workgroup's 256 runs, an eighth of the workgroups, eight eighths
+    n = 48 + 256 + workgroups(run) // 8 + 8
+    for k, m in (("g_x", W), ("g_state0", W), ("g_weight", n), ("g_bias", n)):
+        close(grads[k], want[k], mag[k], 24 + 2 * W + m, k)
 
 
 # rows that end within a group of channels, at the end of a workgroup's or short of one
@@ -638,6 +786,38 @@ def test_conv_overflow_behind_the_text_reaches_nothing():
         # every term's roundings, against the largest terms: the huge input's own
         size = np.abs(want[k]).max() if k == "g_weight" else np.maximum(np.abs(want[k]), 20.0)
         assert (np.abs(t.double().cpu().numpy() - want[k]) <= 400 * ref.U32 * size).all(), k
+
+
+@pytest.mark.parametrize("T,B,D,W,dtype", [(37, 3, 41, 4, "bf16"), (20, 2, 3, 8, "fp32"),
+                                           (5, 4, 260, 2, "fp16")])
+def test_conv_into_given_tensors(T, B, D, W, dtype):
+    g, p = conv_problem(33, T, B, D, W, dtype, True, [T] + [T // 2] * (B - 1), "slice")
+    kw = dict(bias=g["bias"], state0=g["state0"], lengths=g["lengths"], activation="silu")
+    y, state, wg = conv_run(g, True)
+    oy, sy = given(y)
+    os = torch.full_like(state, 7.0)
+    r = sgr.short_conv_forward(g["x"], g["weight"], y=oy, state=os, **kw)
+    assert r[0] is oy and r[1] is os and torch.equal(oy, y) and torch.equal(os, state)
+    gx, sx = given(y)
+    grads = dict({k: torch.full_like(v, 7.0) for k, v in wg.items()}, g_x=gx)
+    need = sequence._conv_sizes(sequence._CONV_SHAPE.pack(T, B, D, W, sequence._DTYPES[DT[dtype]],
+                                                          1))
+    ws = torch.full((need + 256,), 0x5A, dtype=torch.uint8, device="cuda")
+    assert sgr.short_conv_backward(g["x"], g["weight"], g["gy"], grad_state=g["gstate"],
+                                   grads=grads, workspace=ws, **kw) is grads
+    assert all(torch.equal(grads[k], wg[k]) for k in wg)
+    assert untouched(sy, D) and untouched(sx, D) and bool((ws[need:] == 0x5A).all())
+    some = {k: grads[k] for k in ("g_x", "g_weight")}
+    sgr.short_conv_backward(g["x"], g["weight"], g["gy"], grad_state=g["gstate"], grads=some, **kw)
+    assert all(torch.equal(some[k], wg[k]) for k in some)
+    for bad in (dict(y=oy[:-1]), dict(state=os[:-1]), dict(y=oy.float() if dtype != "fp32" else
+                                                          oy.bfloat16())):
+        with pytest.raises((ValueError, TypeError)):
+            sgr.short_conv_forward(g["x"], g["weight"], **bad, **kw)
+    for bad in (dict(workspace=ws[:need - 1]), dict(grads=dict(grads, g_x=gx[:-1])),
+                dict(grads=dict(grads, g_weight=g["weight"].t().contiguous().t()))):
+        with pytest.raises(ValueError):
+            sgr.short_conv_backward(g["x"], g["weight"], g["gy"], **bad, **kw)
 
 
 def test_conv_same_bits_every_time():
