@@ -25,7 +25,8 @@ namespace ckhip {
 namespace {
 
 // v[i] of the channels' lanes 0-7 of each row, v[i + 8] of lanes 8-15, summed
-// over lanes 8 apart.  (DPP operands need two wait states behind a write.)
+// over lanes 8 apart.  (DPP operands need two wait states behind a write; outputs
+// written before the last operand is read are early-clobbered.)
 __device__ __forceinline__ void halve8(float (&v)[16]) {
 #pragma unroll
   for (int i = 0; i < 8; i += 4)
@@ -38,7 +39,7 @@ __device__ __forceinline__ void halve8(float (&v)[16]) {
         "v_add_f32_dpp %1, %5, %5 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
         "v_add_f32_dpp %2, %6, %6 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
         "v_add_f32_dpp %3, %7, %7 row_ror:8 row_mask:0xf bank_mask:0xc"
-        : "+v"(v[i]), "+v"(v[i + 1]), "+v"(v[i + 2]), "+v"(v[i + 3])
+        : "+&v"(v[i]), "+&v"(v[i + 1]), "+&v"(v[i + 2]), "+&v"(v[i + 3])
         : "v"(v[i + 8]), "v"(v[i + 9]), "v"(v[i + 10]), "v"(v[i + 11]));
 }
 // The same for v[i] and v[i + 4] and lanes n and n ^ 7.
@@ -52,7 +53,7 @@ __device__ __forceinline__ void halve4(float (&v)[16]) {
       "v_add_f32_dpp %1, %5, %5 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
       "v_add_f32_dpp %2, %6, %6 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
       "v_add_f32_dpp %3, %7, %7 row_half_mirror row_mask:0xf bank_mask:0xa"
-      : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3])
+      : "+&v"(v[0]), "+&v"(v[1]), "+&v"(v[2]), "+&v"(v[3])
       : "v"(v[4]), "v"(v[5]), "v"(v[6]), "v"(v[7]));
 }
 
