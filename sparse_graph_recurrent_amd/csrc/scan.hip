@@ -45,16 +45,21 @@ void scan_cut(ScanDims* d, int64_t want) {
 // (332 steps x 3 x 64 channels: 37 against 62; 657 x 17 x 128: 70 against 87;
 // 14803 x 2 x 131: 187 against 197 in a round and a half).
 // Rows of unequal lengths leave CUs idle unless cut, and are cut finer.  Windows
-// too short to cut take several tiles each (64 steps x 32 x 256 channels: 37
-// against 41; 64 steps x 8 x 256: 36 against 28, but a launch less in each
-// direction; 100 steps x 16 x 256: 54 against 36, but x 50 x 256: 57 against 61).
+// too short to cut take several tiles each: up to 127 steps (100 steps x 50 x 256:
+// 57 against 61), but where at most half of the CUs have a workgroup up to 64.
+// There a launch less in each direction counts, and it depends on the caller: 64
+// steps x 8 x 256 take 39 against 45 called one by one, which the host bounds, but
+// 38 against 29 in a graph (x 32 x 256: 40 against 44, and 40 against 38).  Beyond,
+// with a third round of tiles, the host sees no difference and a graph does (72
+// steps x 8 x 256: 44 against 45, and 44 against 33; 88 steps x 32 x 256: 51
+// against 45, and 52 against 45).
 // Workgroups that run at once, or read few chunks (half of `chunks` each, 4 KB of
 // what another XCD wrote), fold the chunks before their own (256 steps x 8 x 256:
 // 39 against 44 joined by a launch; 200 x 30 x 640: 120 against 124; but 2048 x 4 x
 // 1024 in 32 chunks: 233 against 224, and 1023 x 16 x 1024 ragged, forward alone,
 // in 8: 91 against 86).
 constexpr int64_t kScanFewGroups = 384, kScanCus = 256, kScanGoalGroups = 2048, kScanRound = 512;
-constexpr int64_t kScanMinChunk = 16, kScanLongChunk = 64, kScanShort = 96;  // steps
+constexpr int64_t kScanMinChunk = 16, kScanLongChunk = 64, kScanShort = 65;  // steps
 constexpr int64_t kScanFold = 8192;  // chunks times workgroups
 
 ScanDims scan_dims(const ck_scan_shape& s, bool ragged) {

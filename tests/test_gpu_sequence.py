@@ -206,6 +206,19 @@ def test_scan_chunks(case):
     scan_check(g, p, case[7])
 
 
+# around the length from which few rows are cut
+@pytest.mark.parametrize("T", [63, 64, 65, 66, 95])
+@pytest.mark.parametrize("rest", [(2, 70, 16, 1, "bf16", True, True, [64, 40], "slice"),
+                                  (3, 40, 6, 2, "fp32", False, True, None, "time"),
+                                  (2, 24, 20, 1, "fp16", True, True, None, "batch")],
+                         ids=lambda c: "-".join(map(str, c[:5])))
+def test_scan_short_windows(T, rest):
+    case = (T,) + rest
+    log(f"scan short {case[:6]}")
+    g, p = scan_problem(16, *case)
+    scan_check(g, p, case[7])
+
+
 def test_scan_without_optional_inputs():
     g, p = scan_problem(2, 20, 2, 64, 16, 1, "fp32", False, True, None, "time", state0=False,
                         extras=False)
