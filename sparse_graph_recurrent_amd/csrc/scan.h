@@ -370,8 +370,9 @@ __device__ __forceinline__ void zero_steps(const Seq<E>& s, const Place& p) {
 // does not: a zero state stays zero however many steps it is kept for.  So it is
 // applied as its square root, twice, each at most 2^127: within range for every
 // normal state that stays in range itself.
+constexpr float kMaxRoot = 0x1p127f;
 __device__ __forceinline__ float half_decay(float log2_decay) {
-  return fminf(exp2_hw(0.5f * log2_decay), 0x1p127f);
+  return fminf(exp2_hw(0.5f * log2_decay), kMaxRoot);
 }
 template <typename V>
 __device__ __forceinline__ V half_decay_v(V x) {
@@ -390,16 +391,16 @@ __device__ __forceinline__ bool scan_grows(const States<NP> (&a)[scan_blocks(NP)
     for (int r = 0; r < scan_lane(NP); ++r) up = up || a[m][r] > 0.0f;
   return __builtin_amdgcn_ballot_w64(up) != 0;
 }
-// A tile's decay as fold_tiles takes it: its root where a state can grow, else
-// the decay itself (a root everywhere costs the backward 3 %, the branch 1 %).
+// A tile's decay as fold_tiles takes it: its root (not bounded yet) where a state can
+// grow, else the decay itself.  (A root everywhere costs the backward 3 %.)
 template <typename V>
 __device__ __forceinline__ V tile_decay(float dt, V a2, bool grows) {
-  return half_decay_v((grows ? dt : 2.0f * dt) * a2);
+  return exp2_v((grows ? 0.5f * dt : dt) * a2);
 }
 
 // Folds what TW tiles make of a zero state (made) and their decays into the
 // state the wave's tile starts from; next: the state behind the last of them.
-// FORWARD runs up from `start`, else down.  ROOTS: the decays are half_decays.
+// FORWARD runs up from `start`, else down.  ROOTS: the decays are roots.
 template <int NP, int TW, bool FORWARD, bool ROOTS>
 __device__ __forceinline__ void fold_tiles_by(States<NP> (&start)[scan_blocks(NP)],
                                               States<NP> (&next)[scan_blocks(NP)],
@@ -418,7 +419,13 @@ __device__ __forceinline__ void fold_tiles_by(States<NP> (&start)[scan_blocks(NP
 #pragma unroll
     for (int m = 0; m < M; ++m) {
       if (w == p.tw) start[m] = cur[m];
-      cur[m] = fma_v(ew[m], ROOTS ? ew[m] * cur[m] : cur[m], mw[m]);
+      if constexpr (ROOTS) {
+#pragma unroll
+        for (int r = 0; r < scan_lane(NP); ++r) ew[m][r] = fminf(ew[m][r], kMaxRoot);
+        cur[m] = fma_v(ew[m], ew[m] * cur[m], mw[m]);
+      } else {
+        cur[m] = fma_v(ew[m], cur[m], mw[m]);
+      }
     }
   }
 #pragma unroll

@@ -195,7 +195,6 @@ __global__ __launch_bounds__(kScanThreads * TW, NP < 64 && TW == 1 ? 2 : 1) void
       }
     }
   }
-  const bool grows = TW > 1 && scan_grows<NP>(a1, s.softplus);
   const float bias = s.delta_bias ? s.delta_bias[p.d] : 0.0f;
   const float skip = s.d ? s.d[p.d] : 0.0f;
   float gskip = 0.0f, gbias = 0.0f;
@@ -225,6 +224,7 @@ __global__ __launch_bounds__(kScanThreads * TW, NP < 64 && TW == 1 ? 2 : 1) void
     };
     fetch(p.te - 1 - tw0);
     bc.load(p.te - 1 - tl);
+    const bool grows = TW > 1 && scan_grows<NP>(a1, s.softplus);  // (waits for A)
     bc.store(lds_bc[0]);
     __syncthreads();
 

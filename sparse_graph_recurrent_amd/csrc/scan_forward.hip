@@ -45,7 +45,6 @@ __global__ __launch_bounds__(kScanThreads * TW) void scan_fwd(const ScanArgs<E> 
       if (TW == 1 && s.chunks > 1) fold_chunks<NP, true>(h, a2, s, p, row);
     }
   }
-  const bool grows = TW > 1 && scan_grows<NP>(a2, s.softplus);
   const float bias = s.delta_bias ? s.delta_bias[p.d] : 0.0f;
   const float skip = s.d ? s.d[p.d] : 0.0f;
   float dtsum = 0.0f;
@@ -66,6 +65,8 @@ __global__ __launch_bounds__(kScanThreads * TW) void scan_fwd(const ScanArgs<E> 
     };
     fetch(p.te - 1 - tw0);
     bc.load(p.te - 1 - p.t0);
+    // (asked only here: it waits for A, and the first tiles' loads are on their way)
+    const bool grows = TW > 1 && scan_grows<NP>(a2, s.softplus);
     bc.store(lds_bc[0]);
     const int64_t ck_step = (int64_t)s.B * s.D * NP;
     float* ck = nullptr;
