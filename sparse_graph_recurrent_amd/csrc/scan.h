@@ -44,7 +44,7 @@ namespace ckhip {
 constexpr int kScanChan = 64;                 // channels per workgroup
 constexpr int kScanThreads = 4 * kScanChan;   // threads per time tile (4 waves)
 // Time tiles a workgroup works on at once where it works on several: what the
-// registers allow (forward 126 of 128 at 16 waves, backward 223 of 256 at 8).
+// registers allow (forward 126 of 128 at 16 waves, backward 216 of 256 at 8).
 constexpr int kScanFwdTW = 4, kScanBwdTW = 2;
 constexpr int64_t kScanMaxN = 64;
 

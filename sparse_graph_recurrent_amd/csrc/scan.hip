@@ -48,11 +48,11 @@ void scan_cut(ScanDims* d, int64_t want) {
 // too short to cut take several tiles each: up to 127 steps (100 steps x 50 x 256:
 // 57 against 61), but where at most half of the CUs have a workgroup up to 64.
 // There a launch less in each direction counts, and it depends on the caller: 64
-// steps x 8 x 256 take 39 against 45 called one by one, which the host bounds, but
-// 38 against 29 in a graph (x 32 x 256: 40 against 44, and 40 against 38).  Beyond,
-// with a third round of tiles, the host sees no difference and a graph does (72
-// steps x 8 x 256: 44 against 45, and 44 against 33; 88 steps x 32 x 256: 51
-// against 45, and 52 against 45).
+// steps x 8 x 256 take 40 against 44 called one by one, which the host bounds, but
+// 36 against 29 in a graph (x 32 x 256: 39 against 43, and 39 against 38).  Beyond,
+// with a third round of tiles, cutting costs the host little or nothing and saves
+// the graph more (72 steps x 8 x 256: 42 against 44, and 42 against 33; 88 steps x
+// 32 x 256: 48 against 44, and 49 against 44).
 // Workgroups that run at once, or read few chunks (half of `chunks` each, 4 KB of
 // what another XCD wrote), fold the chunks before their own (256 steps x 8 x 256:
 // 39 against 44 joined by a launch; 200 x 30 x 640: 120 against 124; but 2048 x 4 x
@@ -87,7 +87,7 @@ ScanDims scan_dims(const ck_scan_shape& s, bool ragged) {
 // One token.  A quad of lanes takes a channel, each lane NL adjacent states, so
 // that the states (which are all but a few bytes of what the step reads and
 // writes, and bound it) move in 16-byte accesses.  256 tokens of 2048 channels x
-// 16 states: 16.5 us, 4.3 TB/s; one token of 256 channels: 2.8 us, the launch.
+// 16 states: 15.7 us, 4.6 TB/s; one token of 256 channels: 2.8 us, the launch.
 constexpr int kOneThreads = 256;
 
 template <bool FULL, int NL, typename E>

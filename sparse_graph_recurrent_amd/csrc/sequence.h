@@ -178,7 +178,9 @@ __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2
 __device__ __forceinline__ float rcp_hw(float x) { return __builtin_amdgcn_rcpf(x); }
 
 // 1 / (1 + exp(-x)): the exponential's overflow for x below -88 makes the
-// reciprocal an exact 0; hardware exponential and reciprocal, about 3 ulp.
+// reciprocal an exact 0.  Hardware exponential and reciprocal, and the rounding of
+// the exponent: relative error up to about (4 + 1.3 |x|) 2^-24 for x < 0, which is
+// 2^-17 where the value is about to vanish, and 4 2^-24 for x > 0.
 __device__ __forceinline__ float sigmoid_hw(float x) {
   return rcp_hw(1.0f + exp2_hw(-kLog2e * x));
 }
@@ -186,8 +188,8 @@ __device__ __forceinline__ float sigmoid_hw(float x) {
 // log(1 + exp(x)) = max(x, 0) + log1p(e), e = exp(-|x|), and its derivative
 // 1 / (1 + exp(-x)).  The part of e that the sum w = 1 + e rounds away is added
 // back, to first order and without its factor 1 / w (which changes it by less
-// than 2^-24 of the result): both keep their relative accuracy down to exp(x)
-// itself for very negative x.
+// than 2^-24 of the result): for very negative x both go over into exp(x), with
+// sigmoid_hw's relative error.
 struct Softplus {
   float value, slope;
 };
