@@ -192,6 +192,8 @@ class SparseGraph:
         return n.value, e.value, k.value
 
     def export(self, stream=None) -> dict:
+        if stream is not None:
+            return _on_stream(stream, self.export)
         N, E = self.num_nodes, self.num_edges
         kw = dict(dtype=torch.int32, device=self.device)
         res = {"row_ptr": torch.empty(N + 1, **kw), "col_idx": torch.empty(E, **kw),
@@ -201,7 +203,7 @@ class SparseGraph:
         _check(self._lib.ck_graph_export(
             self.handle, *[_ptr(res[k]) for k in ("row_ptr", "col_idx", "perm", "t_row_ptr",
                                                   "t_col_idx", "t_perm", "input_slot")],
-            _stream(stream)))
+            _stream()))
         return res
 
     def destroy(self):

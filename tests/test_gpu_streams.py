@@ -55,6 +55,11 @@ def test_recurrence_on_another_stream(path):
     _check(work)
 
 
+def test_export_on_another_stream():
+    g = make_graph(synthetic.make("tiny"))
+    _check(lambda stream: [g.export(stream=stream)])
+
+
 def test_lif_on_another_stream():
     w = synthetic.make("tiny")
     g = make_graph(w)
