@@ -370,17 +370,9 @@ __device__ __forceinline__ void zero_steps(const Seq<E>& s, const Place& p) {
 // does not: a zero state stays zero however many steps it is kept for.  So it is
 // applied as its square root, twice, each at most 2^127: within range for every
 // normal state that stays in range itself.
+// (Only there: applied to all, roots cost a window's backward 3 % and prompts of many
+// chunks and few rows a tenth, 1150 steps x 2 x 109 channels 18.5 -> 20.3 us.)
 constexpr float kMaxRoot = 0x1p127f;
-__device__ __forceinline__ float half_decay(float log2_decay) {
-  return fminf(exp2_hw(0.5f * log2_decay), kMaxRoot);
-}
-template <typename V>
-__device__ __forceinline__ V half_decay_v(V x) {
-  V y;
-#pragma unroll
-  for (int r = 0; r < (int)(sizeof(V) / 4); ++r) y[r] = half_decay(x[r]);
-  return y;
-}
 // Whether states of the wave can grow: the same for all waves of its channels.
 template <int NP>
 __device__ __forceinline__ bool scan_grows(const States<NP> (&a)[scan_blocks(NP)], int softplus) {
@@ -392,7 +384,7 @@ __device__ __forceinline__ bool scan_grows(const States<NP> (&a)[scan_blocks(NP)
   return __builtin_amdgcn_ballot_w64(up) != 0;
 }
 // A tile's decay as fold_tiles takes it: its root (not bounded yet) where a state can
-// grow, else the decay itself.  (A root everywhere costs the backward 3 %.)
+// grow, else the decay itself.
 template <typename V>
 __device__ __forceinline__ V tile_decay(float dt, V a2, bool grows) {
   return exp2_v((grows ? 0.5f * dt : dt) * a2);
@@ -441,13 +433,24 @@ __device__ __forceinline__ void fold_tiles(States<NP> (&start)[scan_blocks(NP)],
     fold_tiles_by<NP, TW, FORWARD, false>(start, next, made, decay, p);
 }
 
+// The root of a decay, or the decay itself where no state of the wave can grow, and
+// a state kept by it.
+template <bool ROOTS>
+__device__ __forceinline__ float chunk_decay(float log2_decay) {
+  return ROOTS ? fminf(exp2_hw(0.5f * log2_decay), kMaxRoot) : exp2_hw(log2_decay);
+}
+template <bool ROOTS>
+__device__ __forceinline__ float decay_add(float decay, float h, float made) {
+  return fmaf(decay, ROOTS ? decay * h : h, made);
+}
+
 // The state a chunk starts from, or (not FORWARD) the adjoint: the window's first,
 // in h, folded with what the chunks walked before this one make of zero.  The
 // same sums as scan_join's, in the same order.
-template <int NP, bool FORWARD, typename E>
-__device__ __forceinline__ void fold_chunks(States<NP> (&h)[scan_blocks(NP)],
-                                            const States<NP> (&a2)[scan_blocks(NP)],
-                                            const ScanArgs<E>& s, const Place& p, int64_t row) {
+template <int NP, bool FORWARD, bool ROOTS, typename E>
+__device__ __forceinline__ void fold_chunks_by(States<NP> (&h)[scan_blocks(NP)],
+                                               const States<NP> (&a2)[scan_blocks(NP)],
+                                               const ScanArgs<E>& s, const Place& p, int64_t row) {
   constexpr int M = scan_blocks(NP), kAhead = 8 / M;
   const int64_t rows = (int64_t)s.B * s.D;
   const int count = FORWARD ? p.chunk : s.chunks - 1 - p.chunk;
@@ -465,26 +468,31 @@ __device__ __forceinline__ void fold_chunks(States<NP> (&h)[scan_blocks(NP)],
     for (int j = 0; j < kAhead; ++j)
       if (k0 + j < count) {
 #pragma unroll
-        for (int m = 0; m < M; ++m) {
-          const States<NP> e = half_decay_v(dt[j] * a2[m]);
-          h[m] = fma_v(e, e * h[m], made[j][m]);
-        }
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+          for (int r = 0; r < scan_lane(NP); ++r)
+            h[m][r] = decay_add<ROOTS>(chunk_decay<ROOTS>(dt[j] * a2[m][r]), h[m][r],
+                                       made[j][m][r]);
       }
   }
 }
 
+template <int NP, bool FORWARD, typename E>
+__device__ __forceinline__ void fold_chunks(States<NP> (&h)[scan_blocks(NP)],
+                                            const States<NP> (&a2)[scan_blocks(NP)],
+                                            const ScanArgs<E>& s, const Place& p, int64_t row) {
+  if (scan_grows<NP>(a2, s.softplus))
+    fold_chunks_by<NP, FORWARD, true>(h, a2, s, p, row);
+  else
+    fold_chunks_by<NP, FORWARD, false>(h, a2, s, p, row);
+}
+
 // Joins the chunks: edge[c] from "made of a zero state" to "starts from".
 // FORWARD walks up from state0, else down from the state's gradient.
-template <bool FORWARD>
-__global__ __launch_bounds__(256) void scan_join(float* edge, const float* dtsum, const float* A,
-                                                 const float* first, int64_t rows, int D, int N,
-                                                 int NP, int chunks) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= rows * NP) return;
-  const int n = (int)(i % NP);
-  const int64_t row = i / NP;
-  const float a2 = n < N ? kLog2e * scan_rate(A[row % D * N + n]) : 0.0f;
-  float cur = first && n < N ? first[row * N + n] : 0.0f;
+template <bool FORWARD, bool ROOTS>
+__device__ __forceinline__ void scan_join_by(float* edge, const float* dtsum, float a2, float cur,
+                                             int64_t row, int64_t i, int64_t rows, int NP,
+                                             int chunks) {
   // in the order of the walk; the chunk that no other follows has no summary
   auto at = [&](int k) { return (int64_t)(FORWARD ? k : chunks - 1 - k) * rows; };
   for (int k0 = 0; k0 < chunks; k0 += 8) {
@@ -499,10 +507,24 @@ __global__ __launch_bounds__(256) void scan_join(float* edge, const float* dtsum
     for (int j = 0; j < 8; ++j)
       if (k0 + j < chunks) {
         edge[at(k0 + j) * NP + i] = cur;
-        const float e = half_decay(a2 * dt[j]);
-        cur = fmaf(e, e * cur, made[j]);
+        cur = decay_add<ROOTS>(chunk_decay<ROOTS>(a2 * dt[j]), cur, made[j]);
       }
   }
+}
+template <bool FORWARD>
+__global__ __launch_bounds__(256) void scan_join(float* edge, const float* dtsum, const float* A,
+                                                 const float* first, int64_t rows, int D, int N,
+                                                 int NP, int chunks, int softplus) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= rows * NP) return;
+  const int n = (int)(i % NP);
+  const int64_t row = i / NP;
+  const float a2 = n < N ? kLog2e * scan_rate(A[row % D * N + n]) : 0.0f;
+  const float cur = first && n < N ? first[row * N + n] : 0.0f;
+  if (__builtin_amdgcn_ballot_w64(!softplus || a2 > 0.0f) != 0)
+    scan_join_by<FORWARD, true>(edge, dtsum, a2, cur, row, i, rows, NP, chunks);
+  else
+    scan_join_by<FORWARD, false>(edge, dtsum, a2, cur, row, i, rows, NP, chunks);
 }
 
 }  // namespace ckhip

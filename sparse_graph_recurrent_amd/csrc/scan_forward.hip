@@ -229,7 +229,7 @@ void launch(const ScanDims& d, const ScanArgs<E>& a, hipStream_t stream) {
     if (!d.fold) {
       const int64_t n = d.B * d.D * d.NP;
       scan_join<true><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
-          a.edge, a.dtsum, a.a, a.state0, d.B * d.D, a.D, a.N, d.NP, a.chunks);
+          a.edge, a.dtsum, a.a, a.state0, d.B * d.D, a.D, a.N, d.NP, a.chunks, a.softplus);
     }
   }
   if constexpr (NP <= 16) {
