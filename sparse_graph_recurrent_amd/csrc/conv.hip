@@ -8,10 +8,10 @@
 // W - 1 inputs in registers, so that within a run every input is read once; a
 // run reads W - 1 steps before it again (and after it, in the backward).  The
 // next four rows are in flight while four are worked on.  Measured, W = 4, bf16,
-// silu: 2048 steps x 8 rows x 2048 channels forward 29 us (4.9 TB/s, what a copy
+// silu: 2048 steps x 8 rows x 2048 channels forward 28 us (5.1 TB/s, what a copy
 // reaches), backward 48 to 55 us (4.0 to 4.5 TB/s, three waves a SIMD) and 5 us for
 // its sums, 82 for the pass; ragged prompts of 1023 x 16 x 1025 fp16 channels (rows
-// at odd addresses) 16.5 us, 3.7 TB/s; 256 tokens of 2048 channels 4.6 us, mostly
+// at odd addresses) 16.8 us, 3.6 TB/s; 256 tokens of 2048 channels 4.6 us, mostly
 // the launch.
 #include <hip/hip_runtime.h>
 

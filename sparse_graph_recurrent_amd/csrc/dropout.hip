@@ -7,8 +7,8 @@
 // their values, so that at 16-bit tensors (4 bytes an element and more) HBM
 // and not the generator bounds the kernel.  16 bits a value make p a multiple
 // of 2^-16; the scale uses that multiple, so the mean is kept exactly.
-// Measured: 2048 x 8 x 2048 bf16 with a residual 38 us (5.2 TB/s), without
-// (backward) 25 to 30 us (4.4 to 5.3 TB/s; ALU 54 and 71 % busy); one mask held over
+// Measured: 2048 x 8 x 2048 bf16 with a residual 38 us (5.3 TB/s), without
+// (backward) 25 to 30 us (4.5 to 5.3 TB/s; ALU 54 and 71 % busy); one mask held over
 // 64 steps of 32 x 5000 fp32 states 18 us from memory (4.5 TB/s), 14 us from the
 // last-level cache.
 #include <hip/hip_runtime.h>

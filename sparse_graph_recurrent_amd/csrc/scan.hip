@@ -88,7 +88,7 @@ ScanDims scan_dims(const ck_scan_shape& s, bool ragged) {
 // One token.  A quad of lanes takes a channel, each lane NL adjacent states, so
 // that the states (which are all but a few bytes of what the step reads and
 // writes, and bound it) move in 16-byte accesses.  256 tokens of 2048 channels x
-// 16 states: 15.7 us, 4.6 TB/s; one token of 256 channels: 2.8 us, the launch.
+// 16 states: 15.6 us, 4.6 TB/s; one token of 256 channels: 2.7 us, the launch.
 constexpr int kOneThreads = 256;
 
 template <bool FULL, int NL, typename E>

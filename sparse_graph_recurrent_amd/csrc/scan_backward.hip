@@ -16,7 +16,7 @@
 // workgroups' by a last launch, all in a fixed order.  Registers allow two
 // waves a SIMD; a third cost 16 spilled registers and a fifth of the speed.
 // Measured at 2048 steps x 8 rows x 2048 channels x 16 states, bf16, gated:
-// 457 us (ALU 81 % busy, 820 MB at 1.8 TB/s; 25.8 vector instructions for 64 states
+// 459 us (ALU 81 % busy, 820 MB at 1.8 TB/s; 25.8 vector instructions for 64 states
 // of a step, of which the formulas are 13 and an exponential) and 18 us for the sums.
 #include "scan.h"
 

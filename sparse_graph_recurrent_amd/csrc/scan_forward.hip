@@ -4,9 +4,9 @@
 // wave), two products and two multiply-adds (4 each where they mix with
 // others), and a fifth of that again for the per-channel work.  Measured, 16
 // states, bf16, gated: a training window of 2048 steps x 8 rows x 2048 channels
-// in 209 us (vector ALU 84 % busy; 550 MB, half of it the states left for the
+// in 210 us (vector ALU 83 % busy; 550 MB, half of it the states left for the
 // backward, at 2.6 TB/s); a prompt of 16384 steps, one row, in 95 (summaries, ALU
-// 87 % busy) + 9 (join) + 126 us (95 %; 2.3 TB/s).  For 64 states of a step a wave
+// 87 % busy) + 9 (join) + 125 us (95 %; 2.3 TB/s).  For 64 states of a step a wave
 // executes 7.8 vector instructions on one tile, 11.5 on several, whose decays it
 // keeps but whose products it forms twice.
 #include "scan.h"
