@@ -527,6 +527,169 @@ ck_status ck_dropout_forward(const ck_dropout_shape* shape, ck_seq x, ck_seq res
 ck_status ck_dropout_backward(const ck_dropout_shape* shape, ck_seq grad_out, ck_seq grad_x,
                               hipStream_t stream);
 
+/*
+ * Gated scan: a linear recurrence of each channel on its own, whose decay and input
+ * weight are gates (s is the logistic function):
+ *
+ *   a_t   = s(f_t + f_bias[d])
+ *   g_t   = s(i_t + i_bias[d])        (without i: 1 - a_t)
+ *   h_t   = a_t h_{t-1} + g_t x_t
+ *   out_t = h_t z_t s(z_t)            (h_t without z)
+ *
+ * with h_{-1} = state0.  Steps lie less than 2^30 elements apart.  A gate that is
+ * almost 1 is held as what it lacks, so that a state is kept over as many steps as
+ * the gate says.  A state that is not finite may go on as a NaN.
+ */
+typedef struct {
+  int64_t T, B, D; /* steps, batch rows, channels */
+  int32_t dtype;   /* ck_dtype of the sequence tensors */
+} ck_gated_shape;
+
+typedef struct {
+  ck_seq x, f;          /* [T, B, D] */
+  ck_seq i;             /* [T, B, D]; data NULL: no input gate of its own */
+  ck_seq z;             /* [T, B, D]; data NULL: no output gate */
+  const float* f_bias;  /* [D] or NULL (0) */
+  const float* i_bias;  /* [D] or NULL (0); not used without i */
+  const float* state0;  /* [B][D] or NULL (0) */
+  const int32_t* lengths; /* [B] or NULL */
+} ck_gated_inputs;
+
+/* Gradients, all overwritten; layouts as the inputs'.  i and z are required when the
+ * call has that gate; the others may be NULL (not wanted). */
+typedef struct {
+  ck_seq x, f, i, z;
+  float *f_bias, *i_bias, *state0;
+} ck_gated_grads;
+
+/* saved_bytes: states the forward leaves for the backward (one every 8 steps);
+ * forward_bytes, backward_bytes: scratch of each call (a workspace of 0 bytes may be
+ * NULL).  Any pointer may be NULL. */
+ck_status ck_gated_sizes(const ck_gated_shape* shape, size_t* saved_bytes, size_t* forward_bytes,
+                         size_t* backward_bytes);
+
+/*
+ *   out        [T, B, D]     written
+ *   state      fp32[B][D]    written: the state after each row's last step (NULL: not wanted)
+ *   saved      saved_bytes   written for ck_gated_backward, or NULL when no backward follows
+ *   workspace  forward_bytes
+ */
+ck_status ck_gated_forward(const ck_gated_shape* shape, const ck_gated_inputs* in, ck_seq out,
+                           float* state, void* saved, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+
+/* Gradients of L given grad_out = dL/dout and grad_state = dL/dstate (fp32[B][D],
+ * NULL for 0).  `saved` must come from the forward with the same shape and inputs;
+ * state0 is not read. */
+ck_status ck_gated_backward(const ck_gated_shape* shape, const ck_gated_inputs* in,
+                            const void* saved, ck_seq grad_out, const float* grad_state,
+                            const ck_gated_grads* grads, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream);
+
+/* One token per row (shape->T must be 1, lengths NULL): out[0] and the new state from
+ * state0.  `state` may be state0 itself (updated in place). */
+ck_status ck_gated_step(const ck_gated_shape* shape, const ck_gated_inputs* in, ck_seq out,
+                        float* state, hipStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The norm of a model's gradients, and their scaling to a limit:
+ *
+ *   n = sqrt(sum over all tensors of g^2)
+ *   c = max_norm / n if n > max_norm, else 1;   out = c g
+ *
+ * Squares are summed in 64 bits, in one order (two calls give the same bits).  A norm
+ * that is not finite as fp32 scales nothing (c = 1): the caller sees it in `norm`.
+ * Each tensor is `n` adjacent elements, at any address that suits its type.  What is
+ * written must not lie over another tensor of the call, nor over its own gradient
+ * unless it is that gradient itself (CK_ERR_BAD_VALUE).  Allocates nothing on the
+ * device, does not synchronise, and may be captured into a HIP graph.
+ */
+typedef struct {
+  const void* grad;
+  void* out;     /* grad itself: scaled in place; NULL: counts to the norm, is not scaled */
+  int64_t n;     /* elements, may be 0 */
+  int32_t dtype; /* ck_dtype of both */
+} ck_clip_tensor;
+
+/* Scratch of ck_clip_grad_norm for up to `count` tensors. */
+ck_status ck_clip_sizes(int64_t count, size_t* workspace_bytes);
+
+/*
+ *   tensors   host array of `count` (at most 2^20), read before the call returns
+ *   max_norm  0 .. infinity (else CK_ERR_BAD_VALUE)
+ *   norm      fp32[1] device, written: n
+ */
+ck_status ck_clip_grad_norm(const ck_clip_tensor* tensors, int64_t count, double max_norm,
+                            float* norm, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Beam search's step: of B texts with K beams each, the K best continuations,
+ *
+ *   score(k, v) = scores[k] + x[k][v] - log sum_w exp x[k][w]
+ *
+ * over all beams k and tokens v of a text, best first; of equal scores the lower
+ * k V + v is first.  A finished beam has one continuation, the end token, at its own
+ * score.  A logit of -inf, and a NaN, is never taken before any other (its score is
+ * -inf, as are all of a beam whose own score is -inf or NaN, and of a finished beam
+ * but the end token's); +inf counts as the largest finite fp32 value.  Logits of a
+ * beam without any above -inf, or whose score is -inf, or that is finished, are not
+ * looked at for a sum.  Scores are compared in 64 bits (sums of exponentials are held
+ * in 32) and rounded once.  Two calls on the same inputs give the same bits.
+ */
+typedef struct {
+  int64_t B, K;  /* texts, beams a text: K 1..32 */
+  int64_t V;     /* tokens */
+  int64_t eos;   /* the end token, or -1: none */
+  int32_t dtype; /* ck_dtype of the logits */
+} ck_beam_shape;
+
+/* Scratch of ck_beam_select. */
+ck_status ck_beam_sizes(const ck_beam_shape* shape, size_t* workspace_bytes);
+
+/*
+ *   logits        [B, K, V]     a ck_seq: stride_t between texts, stride_b between beams
+ *   scores        fp32[B][K]
+ *   finished      uint8[B][K] (0 or not) or NULL (none is); with it eos is required
+ *   out_scores    fp32[B][K]    written (may be scores)
+ *   parents       int64[B][K]   written: the beam k that each new beam goes on from
+ *   tokens        int64[B][K]   written
+ *   out_finished  uint8[B][K]   written (may be finished): the parent was, or the token is
+ *                               eos; NULL: not wanted
+ */
+ck_status ck_beam_select(const ck_beam_shape* shape, ck_seq logits, const float* scores,
+                         const uint8_t* finished, float* out_scores, int64_t* parents,
+                         int64_t* tokens, uint8_t* out_finished, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Reorders what beams carry: for every state, text b and beam j,
+ *
+ *   out[b K + j] = in[b K + parents[b][j]]
+ *
+ * A state's row is `segments` pieces of `bytes` adjacent bytes.  `out` is the state
+ * itself (the same strides: reordered in place) or does not overlap it; rows of `out`
+ * must not lie over one another, nor one state over what is written of another
+ * (CK_ERR_BAD_VALUE where the addresses show it).  A parent outside [0, K) counts as
+ * the nearer bound.
+ */
+typedef struct {
+  const void* in;
+  void* out;
+  int64_t segments, bytes;
+  int64_t in_row, in_segment;   /* bytes between rows, and between pieces */
+  int64_t out_row, out_segment;
+} ck_beam_state;
+
+/*
+ *   states   host array of `count`, read before the call returns
+ *   parents  int64[B][K] device
+ */
+ck_status ck_beam_reorder(const ck_beam_state* states, int64_t count, const int64_t* parents,
+                          int64_t B, int64_t K, hipStream_t stream);
+
 /* Static name of a status value. */
 const char* ck_status_string(ck_status s);
 

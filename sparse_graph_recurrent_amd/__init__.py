@@ -17,8 +17,10 @@ drives fp32 [T, n_in, B], state0 fp32 [B, N] and out fp32 [T, B, N].
 ``sparse_recurrence`` is differentiable in all five tensor arguments.
 
 The sequence operators that a text model runs before and behind the
-recurrence (short convolution, selective scan, dropout) are in ``sequence``
-and reached by the same names here.
+recurrence (short convolution, selective scan, gated scan, dropout) are in
+``sequence``, the clipping of a training step's gradients in ``clip`` and
+beam search's selection and reordering in ``beam``; all are reached by the
+same names here.
 
 The library is required: importing works without it, but every call raises
 ``CkLibraryMissing`` if ``libck_hip.so`` has not been built
@@ -48,6 +50,9 @@ EXPORTED = ("ck_graph_create", "ck_graph_destroy", "ck_graph_sizes", "ck_graph_e
             "ck_profile_collect_lif", "ck_scan_sizes", "ck_scan_forward", "ck_scan_backward",
             "ck_scan_step", "ck_conv_sizes", "ck_conv_forward", "ck_conv_backward",
             "ck_conv_step", "ck_dropout_forward", "ck_dropout_backward",
+            "ck_gated_sizes", "ck_gated_forward", "ck_gated_backward", "ck_gated_step",
+            "ck_clip_sizes", "ck_clip_grad_norm", "ck_beam_sizes", "ck_beam_select",
+            "ck_beam_reorder",
             "ck_profile_enable", "ck_profile_collect", "ck_status_string", "ck_last_error")
 
 
@@ -103,6 +108,8 @@ def lib() -> ctypes.CDLL:
         L.ck_profile_collect.argtypes = [dp, ip, dp, ip]
         L.ck_profile_collect_lif.argtypes = [dp, ip, dp, ip]
         sequence._declare(L)
+        clip._declare(L)
+        beam._declare(L)
         for name in EXPORTED[:-2]:
             getattr(L, name).restype = ctypes.c_int
         L.ck_status_string.argtypes = [ctypes.c_int]
@@ -492,12 +499,16 @@ def sparse_recurrence(edge_values, leak, bias, drives, state0, graph: SparseGrap
 
 
 from . import sequence  # noqa: E402  (uses the helpers above)
+from . import beam, clip  # noqa: E402
+from .beam import beam_reorder, beam_select  # noqa: E402
+from .clip import clip_grad_norm, grad_norm  # noqa: E402
 from .sequence import (  # noqa: E402
-    dropout, dropout_backward, dropout_forward, selective_scan, selective_scan_backward,
+    dropout, dropout_backward, dropout_forward, gated_scan, gated_scan_backward,
+    gated_scan_forward, gated_scan_sizes, gated_scan_step, selective_scan, selective_scan_backward,
     selective_scan_forward, selective_scan_sizes, selective_scan_step, short_conv,
     short_conv_backward, short_conv_forward, short_conv_step)
 
 __all__ = ["SparseGraph", "sparse_recurrence", "recurrence_forward", "recurrence_backward",
            "recurrence_forward_noalloc", "lif_forward", "profile_collect_lif", "LifParams",
            "recurrence_sizes", "recurrence_status", "recurrence_path", "profile_enable", "profile_collect", "CkError", "CkLibraryMissing",
-           "lib", "LIB_PATH", "EXPORTED"] + sequence.__all__
+           "lib", "LIB_PATH", "EXPORTED"] + sequence.__all__ + clip.__all__ + beam.__all__

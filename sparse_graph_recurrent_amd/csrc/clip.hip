@@ -1,0 +1,324 @@
+// clip.hip -- the norm of all gradients of a model, and their scaling to a limit.
+//
+//   n = sqrt(sum over all tensors of g^2),   c = max_norm / n if n > max_norm else 1,   out = c g
+//
+// HBM bounds both launches: the norm has to be known before anything is scaled, so
+// every gradient is read twice and written once.  Squares are summed in 64 bits (a
+// conversion and a multiply-add an element, a tenth of what the vector ALU has at
+// HBM's rate): no gradient that its type can hold overflows them.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <new>
+#include <vector>
+
+#include "ck.h"
+#include "ck_internal.h"
+#include "sequence.h"
+
+namespace ckhip {
+namespace {
+
+constexpr int kClipThreads = 256;
+constexpr int kClipTable = 96;      // tensors a launch (the table is its argument: at most 4 KB)
+constexpr int kClipV = 8;           // elements a thread and access
+constexpr int kClipDeep = 4;        // accesses in flight
+constexpr int kClipUnit = kClipThreads * kClipV;  // elements of a chunk, times 1 .. kClipDeep
+constexpr int kClipBlocks = 1024;   // of a launch that sums: as many partial sums
+
+struct ClipTable {
+  const void* in[kClipTable];
+  void* out[kClipTable];
+  int64_t n[kClipTable];
+  int64_t first[kClipTable + 1];  // first chunk of each tensor
+  int8_t dtype[kClipTable];
+  int count;
+  int units;  // of a chunk
+};
+
+// The tensor that a chunk lies in.
+__device__ __forceinline__ int clip_find(const ClipTable& t, int64_t chunk) {
+  int lo = 0, hi = t.count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (t.first[mid] <= chunk) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// fn(pack, first element, elements there are) for the thread's share of a chunk,
+// all loads before the first call.
+template <typename E, typename F>
+__device__ __forceinline__ void clip_chunk(const void* data, int64_t n, int64_t chunk, int units,
+                                           F&& fn) {
+  const E* p = static_cast<const E*>(data);
+  const int64_t base = chunk * units * kClipUnit;
+  Pack<E, kClipV> v[kClipDeep];
+#pragma unroll
+  for (int u = 0; u < kClipDeep; ++u) {
+    if (u >= units) continue;
+    const int64_t at = base + u * kClipUnit + (int64_t)threadIdx.x * kClipV;
+    if (at + kClipV <= n) v[u] = pack_load<true, E, kClipV>(p + at, kClipV);
+    else if (at < n) v[u] = pack_load<false, E, kClipV>(p + at, (int)(n - at));
+  }
+#pragma unroll
+  for (int u = 0; u < kClipDeep; ++u) {
+    if (u >= units) continue;
+    const int64_t at = base + u * kClipUnit + (int64_t)threadIdx.x * kClipV;
+    if (at < n) fn(v[u], at, (int)min(n - at, (int64_t)kClipV));
+  }
+}
+
+__device__ __forceinline__ double clip_block_sum(double x) {
+  __shared__ double lds[kClipThreads / 64];
+#pragma unroll
+  for (int m = 32; m; m >>= 1) x += __shfl_xor(x, m);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
+  __syncthreads();
+  x = 0.0;
+#pragma unroll
+  for (int w = 0; w < kClipThreads / 64; ++w) x += lds[w];
+  return x;
+}
+
+template <typename E>
+__device__ __forceinline__ void clip_square(const ClipTable& t, int i, int64_t chunk, double& sum) {
+  clip_chunk<E>(t.in[i], t.n[i], chunk, t.units, [&](const Pack<E, kClipV>& v, int64_t, int) {
+#pragma unroll
+    for (int j = 0; j < kClipV; ++j) {  // (elements there are not are 0)
+      const double g = (double)(float)v.v[j];
+      sum = fma(g, g, sum);
+    }
+  });
+}
+
+__global__ __launch_bounds__(kClipThreads) void clip_norm(const ClipTable t, double* part) {
+  double sum = 0.0;
+  const int64_t chunks = t.first[t.count];
+  for (int64_t k = blockIdx.x; k < chunks; k += gridDim.x) {
+    const int i = clip_find(t, k);
+    const int64_t chunk = k - t.first[i];
+    if (t.dtype[i] == CK_F32) clip_square<float>(t, i, chunk, sum);
+    else if (t.dtype[i] == CK_BF16) clip_square<bf16_t>(t, i, chunk, sum);
+    else clip_square<f16_t>(t, i, chunk, sum);
+  }
+  sum = clip_block_sum(sum);
+  if (threadIdx.x == 0) part[blockIdx.x] = sum;
+}
+
+template <typename E>
+__device__ __forceinline__ void clip_write(const ClipTable& t, int i, int64_t chunk, double c) {
+  E* out = static_cast<E*>(t.out[i]);
+  clip_chunk<E>(t.in[i], t.n[i], chunk, t.units,
+                [&](const Pack<E, kClipV>& v, int64_t at, int n) {
+    float y[kClipV];
+#pragma unroll
+    for (int j = 0; j < kClipV; ++j) {
+      if constexpr (sizeof(E) == 4) y[j] = (float)((double)(float)v.v[j] * c);
+      else y[j] = (float)v.v[j] * (float)c;
+    }
+    if (n == kClipV) pack_store<true, E, kClipV>(out + at, y, n);
+    else pack_store<false, E, kClipV>(out + at, y, n);
+  });
+}
+
+// Every workgroup adds the partial sums, in one order, for itself.  `same`: every
+// output of the table is its gradient, so that nothing is to do where nothing is
+// scaled.  Chunks are taken last first: the last are what the sums' launch left in
+// the last-level cache.
+__global__ __launch_bounds__(kClipThreads) void clip_scale(const ClipTable t, const double* part,
+                                                           int parts, double max_norm, int same,
+                                                           float* norm) {
+  double sum = 0.0;
+  for (int k = threadIdx.x; k < parts; k += kClipThreads) sum += part[k];
+  const double n = sqrt(clip_block_sum(sum));
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
+  // a norm that is not finite scales nothing: there is no direction to keep
+  const bool scales = n > max_norm && (float)n < __builtin_inff();
+  if (!scales && same) return;
+  const double c = scales ? max_norm / n : 1.0;
+  const int64_t chunks = t.first[t.count];
+  for (int64_t k = blockIdx.x; k < chunks; k += gridDim.x) {
+    const int i = clip_find(t, chunks - 1 - k);
+    const int64_t chunk = chunks - 1 - k - t.first[i];
+    if (!t.out[i]) continue;
+    if (t.dtype[i] == CK_F32) clip_write<float>(t, i, chunk, c);
+    else if (t.dtype[i] == CK_BF16) clip_write<bf16_t>(t, i, chunk, c);
+    else clip_write<f16_t>(t, i, chunk, c);
+  }
+}
+
+ck_status clip_check(const ck_clip_tensor* tensors, int64_t count, int64_t* most) {
+  *most = 0;
+  if (count < 0) {
+    set_error("bad count %lld", (long long)count);
+    return CK_ERR_BAD_SIZE;
+  }
+  if (count > (int64_t(1) << 20)) {
+    set_error("count=%lld is too large", (long long)count);
+    return CK_ERR_TOO_LARGE;
+  }
+  if (count > 0 && !tensors) {
+    set_error("tensors are NULL");
+    return CK_ERR_NULL_ARG;
+  }
+  for (int64_t i = 0; i < count; ++i) {
+    const ck_clip_tensor& t = tensors[i];
+    if (t.n < 0) {
+      set_error("tensor %lld has %lld elements", (long long)i, (long long)t.n);
+      return CK_ERR_BAD_SIZE;
+    }
+    if (t.n > (int64_t(1) << 44)) {
+      set_error("tensor %lld is too large", (long long)i);
+      return CK_ERR_TOO_LARGE;
+    }
+    if (t.dtype != CK_F32 && t.dtype != CK_BF16 && t.dtype != CK_F16) {
+      set_error("unknown element type %d", t.dtype);
+      return CK_ERR_BAD_VALUE;
+    }
+    if (t.n > 0 && !t.grad) {
+      set_error("tensor %lld is NULL", (long long)i);
+      return CK_ERR_NULL_ARG;
+    }
+    const size_t e = seq_elem_bytes(t.dtype);
+    if (reinterpret_cast<uintptr_t>(t.grad) % e || reinterpret_cast<uintptr_t>(t.out) % e) {
+      set_error("tensor %lld is not aligned to its element type", (long long)i);
+      return CK_ERR_BAD_VALUE;
+    }
+    *most += t.n;
+  }
+  return CK_OK;
+}
+
+// Whether what is written lies over something else that is written, or that is read
+// as another tensor.
+bool clip_overlaps(const ck_clip_tensor* tensors, int64_t count) {
+  struct Range {
+    uintptr_t from, to;
+    bool written;
+  };
+  std::vector<Range> ranges;
+  ranges.reserve(2 * count);
+  for (int64_t i = 0; i < count; ++i) {
+    const ck_clip_tensor& t = tensors[i];
+    const size_t bytes = (size_t)t.n * seq_elem_bytes(t.dtype);
+    const uintptr_t g = reinterpret_cast<uintptr_t>(t.grad), o = reinterpret_cast<uintptr_t>(t.out);
+    if (!bytes) continue;
+    if (o) ranges.push_back({o, o + bytes, true});
+    if (o != g) ranges.push_back({g, g + bytes, false});
+  }
+  std::sort(ranges.begin(), ranges.end(),
+            [](const Range& a, const Range& b) { return a.from < b.from; });
+  uintptr_t any = 0, written = 0;  // the furthest ends so far
+  for (const Range& r : ranges) {
+    if (r.from < (r.written ? any : written)) return true;
+    any = std::max(any, r.to);
+    if (r.written) written = std::max(written, r.to);
+  }
+  return false;
+}
+
+size_t clip_workspace(int64_t count) {
+  const int64_t launches = std::max<int64_t>(1, (count + kClipTable - 1) / kClipTable);
+  return (size_t)launches * kClipBlocks * sizeof(double);
+}
+
+// The table of the tensors [i, ..) that a launch takes; the first that it does not.
+int64_t clip_fill(const ck_clip_tensor* tensors, int64_t count, int64_t i, int units,
+                  ClipTable* t, bool* same) {
+  t->count = 0;
+  t->units = units;
+  t->first[0] = 0;
+  *same = true;
+  for (; i < count && t->count < kClipTable; ++i) {
+    const ck_clip_tensor& x = tensors[i];
+    if (x.n == 0) continue;
+    const int k = t->count++;
+    t->in[k] = x.grad;
+    t->out[k] = x.out;
+    t->n[k] = x.n;
+    t->dtype[k] = (int8_t)x.dtype;
+    const int64_t unit = (int64_t)units * kClipUnit;
+    t->first[k + 1] = t->first[k] + (x.n + unit - 1) / unit;
+    if (x.out && x.out != x.grad) *same = false;
+  }
+  return i;
+}
+
+}  // namespace
+}  // namespace ckhip
+
+using namespace ckhip;
+
+extern "C" ck_status ck_clip_sizes(int64_t count, size_t* workspace_bytes) {
+  clear_error();
+  if (count < 0) {
+    set_error("bad count %lld", (long long)count);
+    return CK_ERR_BAD_SIZE;
+  }
+  if (workspace_bytes) *workspace_bytes = clip_workspace(count);
+  return CK_OK;
+}
+
+extern "C" ck_status ck_clip_grad_norm(const ck_clip_tensor* tensors, int64_t count,
+                                       double max_norm, float* norm, void* workspace,
+                                       size_t workspace_bytes, hipStream_t stream) {
+  clear_error();
+  int64_t total = 0;
+  ck_status rc = clip_check(tensors, count, &total);
+  if (rc != CK_OK) return rc;
+  if (!(max_norm >= 0.0)) {
+    set_error("max_norm must not be negative (got %g)", max_norm);
+    return CK_ERR_BAD_VALUE;
+  }
+  if (!norm) {
+    set_error("norm is NULL");
+    return CK_ERR_NULL_ARG;
+  }
+  if (reinterpret_cast<uintptr_t>(norm) % sizeof(float)) {
+    set_error("norm is not aligned to its element type");
+    return CK_ERR_BAD_VALUE;
+  }
+  rc = seq_check_ws(workspace, workspace_bytes, clip_workspace(count));
+  if (rc != CK_OK) return rc;
+  try {
+    if (clip_overlaps(tensors, count)) {
+      set_error("a tensor that is written lies over another one");
+      return CK_ERR_BAD_VALUE;
+    }
+  } catch (const std::bad_alloc&) {
+    set_error("out of host memory");
+    return CK_ERR_NOMEM;
+  }
+  // chunks long enough to keep loads in flight, short enough to reach all CUs
+  int units = kClipDeep;
+  while (units > 1 && total / ((int64_t)units * kClipUnit) < kClipBlocks) units >>= 1;
+  double* part = static_cast<double*>(workspace);
+  ClipTable t;
+  bool same;
+  int parts = 0;
+  int64_t i = 0;
+  do {
+    i = clip_fill(tensors, count, i, units, &t, &same);
+    const int blocks =
+        (int)std::min<int64_t>(kClipBlocks, std::max<int64_t>(1, t.first[t.count]));
+    clip_norm<<<blocks, kClipThreads, 0, stream>>>(t, part + parts);
+    parts += blocks;
+  } while (i < count);
+  i = 0;
+  float* to = norm;
+  do {
+    i = clip_fill(tensors, count, i, units, &t, &same);
+    bool writes = false;
+    for (int k = 0; k < t.count; ++k) writes = writes || t.out[k];
+    if (!writes && !to) continue;
+    const int64_t chunks = writes ? t.first[t.count] : 1;
+    const int blocks = (int)std::min<int64_t>(2 * kClipBlocks, std::max<int64_t>(1, chunks));
+    clip_scale<<<blocks, kClipThreads, 0, stream>>>(t, part, parts, writes ? max_norm : INFINITY,
+                                                    same ? 1 : 0, to);
+    to = nullptr;
+  } while (i < count);
+  CK_HIP_TRY(hipGetLastError());
+  return CK_OK;
+}

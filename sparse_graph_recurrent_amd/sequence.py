@@ -1,5 +1,6 @@
 """Sequence operators of a text model around the graph recurrence: a short
-causal convolution, a selective state space scan and a counter-based dropout.
+causal convolution, a selective state space scan, a gated scan and a
+counter-based dropout.
 
 The layouts are the recurrence's: windows are time first, [T, B, channels].
 Sequence tensors may be fp32, bf16 or fp16 (one type per call) and need only
@@ -11,6 +12,7 @@ give 0.
 
     y, conv_state = short_conv(x, weight, bias, activation="silu")
     out, state = selective_scan(u, delta, A, B, C, D, z=z, delta_bias=bias, delta_softplus=True)
+    out, state = gated_scan(x, f, i, z, f_bias=f_bias, i_bias=i_bias)
     h = dropout(out, p, seed, residual=x)
 
 are differentiable; ``*_forward`` / ``*_backward`` are the calls behind them
@@ -57,6 +59,24 @@ class ScanGrads(ctypes.Structure):
                [(n, ctypes.c_void_p) for n in ("a", "d", "delta_bias", "state0")]
 
 
+class GatedShape(ctypes.Structure):
+    """ck_gated_shape of include/ck.h."""
+    _fields_ = [("T", ctypes.c_int64), ("B", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
+
+
+class GatedInputs(ctypes.Structure):
+    """ck_gated_inputs of include/ck.h."""
+    _fields_ = [(n, CkSeq) for n in ("x", "f", "i", "z")] + \
+               [(n, ctypes.c_void_p) for n in ("f_bias", "i_bias", "state0", "lengths")]
+
+
+class GatedGrads(ctypes.Structure):
+    """ck_gated_grads of include/ck.h."""
+    _fields_ = [(n, CkSeq) for n in ("x", "f", "i", "z")] + \
+               [(n, ctypes.c_void_p) for n in ("f_bias", "i_bias", "state0")]
+
+
 class ConvShape(ctypes.Structure):
     """ck_conv_shape of include/ck.h."""
     _fields_ = [("T", ctypes.c_int64), ("B", ctypes.c_int64), ("D", ctypes.c_int64),
@@ -76,11 +96,17 @@ class DropoutShape(ctypes.Structure):
 _SCAN_SHAPE = struct.Struct("=5q2i")
 _SCAN_INPUTS = struct.Struct("=20Q")
 _SCAN_GRADS = struct.Struct("=19Q")
+_GATED_SHAPE = struct.Struct("=3qi4x")
+_GATED_INPUTS = struct.Struct("=16Q")
+_GATED_GRADS = struct.Struct("=15Q")
 _CONV_SHAPE = struct.Struct("=4q2i")
 _DROP_SHAPE = struct.Struct("=3q2id3Q")
 assert _SCAN_SHAPE.size == ctypes.sizeof(ScanShape)
 assert _SCAN_INPUTS.size == ctypes.sizeof(ScanInputs)
 assert _SCAN_GRADS.size == ctypes.sizeof(ScanGrads)
+assert _GATED_SHAPE.size == ctypes.sizeof(GatedShape)
+assert _GATED_INPUTS.size == ctypes.sizeof(GatedInputs)
+assert _GATED_GRADS.size == ctypes.sizeof(GatedGrads)
 assert _CONV_SHAPE.size == ctypes.sizeof(ConvShape)
 assert _DROP_SHAPE.size == ctypes.sizeof(DropoutShape)
 
@@ -96,6 +122,10 @@ def _declare(L: ctypes.CDLL) -> None:
     L.ck_scan_forward.argtypes = [p, p, q, p, p, p, sz, p]
     L.ck_scan_backward.argtypes = [p, p, p, q, p, p, p, sz, p]
     L.ck_scan_step.argtypes = [p, p, q, p, p]
+    L.ck_gated_sizes.argtypes = [p, szp, szp, szp]
+    L.ck_gated_forward.argtypes = [p, p, q, p, p, p, sz, p]
+    L.ck_gated_backward.argtypes = [p, p, p, q, p, p, p, sz, p]
+    L.ck_gated_step.argtypes = [p, p, q, p, p]
     L.ck_conv_sizes.argtypes = [p, szp]
     L.ck_conv_forward.argtypes = [p, q, p, p, p, p, q, p, p]
     L.ck_conv_backward.argtypes = [p, q, p, p, p, p, q, p, q, p, p, p, p, sz, p]
@@ -411,6 +441,154 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, state0=No
                                 bool(delta_softplus), torch.is_grad_enabled())
 
 
+# ---------------------------------------------------------------- gated scan
+
+def _gated_call(x, f, i, z, f_bias, i_bias, state0, lengths, step=False):
+    """(shape, inputs, device, shape of a state) of a gated scan's call, checked."""
+    dev = _first(x, "x", (2,) if step else (3,))
+    xs, dt = x.shape, x.dtype
+    T, rows, ch = (1,) + xs if step else xs
+    if i is None and i_bias is not None:
+        raise ValueError("i_bias is the input gate's: i is missing")
+    return _GATED_SHAPE.pack(T, rows, ch, _DTYPES[dt]), _GATED_INPUTS.pack(
+        *_seq(x, "x", dt, dev, xs), *_seq(f, "f", dt, dev, xs),
+        *(_NONE if i is None else _seq(i, "i", dt, dev, xs)),
+        *(_NONE if z is None else _seq(z, "z", dt, dev, xs)),
+        _par(f_bias, "f_bias", dev, (ch,)), _par(i_bias, "i_bias", dev, (ch,)),
+        _par(state0, "state0", dev, (rows, ch)),
+        _par(lengths, "lengths", dev, (rows,), torch.int32)), dev, (rows, ch)
+
+
+@functools.lru_cache(maxsize=256)
+def _gated_sizes(shape: bytes):
+    s, f, b = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().ck_gated_sizes(shape, ctypes.byref(s), ctypes.byref(f), ctypes.byref(b)))
+    return s.value, f.value, b.value
+
+
+def gated_scan_sizes(T: int, B: int, D: int, dtype=torch.float32):
+    """(saved_bytes, forward_bytes, backward_bytes) of ``ck_gated_sizes``."""
+    return _gated_sizes(_GATED_SHAPE.pack(T, B, D, _DTYPES[dtype]))
+
+
+def gated_scan_forward(x, f, i=None, z=None, f_bias=None, i_bias=None, state0=None, lengths=None,
+                       save: bool = True, out=None, state=None, saved=None, workspace=None,
+                       stream=None):
+    """Run ``ck_gated_forward``; returns (out, state, saved, workspace).
+
+    x, the gates f (forget), i (input; None: what the forget gate lets go) and
+    z (output; None: open): [T, B, D]; f_bias, i_bias: [D]; state0 and the
+    returned state: fp32 [B, D].  ``saved`` is what ``gated_scan_backward``
+    needs (None with save=False)."""
+    if stream is not None:
+        return _on_stream(stream, gated_scan_forward, x, f, i, z, f_bias, i_bias, state0, lengths,
+                          save, out, state, saved, workspace)
+    shape, inputs, dev, ss = _gated_call(x, f, i, z, f_bias, i_bias, state0, lengths)
+    sb, fb, _ = _gated_sizes(shape)
+    out, os = _out_seq(out, "out", x)
+    state, st = _out_par(state, "state", x, ss, model=state0)
+    saved, sp, _ = _buffer(saved, sb, x, "saved") if save or saved is not None else \
+        (None, None, 0)
+    workspace, wp, wn = _buffer(workspace, fb, x, "workspace")
+    _call(lib().ck_gated_forward, dev, (shape, inputs, os, st, sp, wp, wn))
+    return out, state, saved, workspace
+
+
+def gated_scan_backward(x, f, saved, grad_out, i=None, z=None, f_bias=None, i_bias=None,
+                        lengths=None, grad_state=None, grads=None, workspace=None,
+                        stream=None) -> dict:
+    """Run ``ck_gated_backward``; returns the gradients (overwritten) by the
+    names g_x, g_f, g_f_bias, g_state0 and, with that gate, g_i and g_i_bias,
+    g_z."""
+    if stream is not None:
+        return _on_stream(stream, gated_scan_backward, x, f, saved, grad_out, i, z, f_bias, i_bias,
+                          lengths, grad_state, grads, workspace)
+    shape, inputs, dev, ss = _gated_call(x, f, i, z, f_bias, i_bias, None, lengths)
+    sb, _, wb = _gated_sizes(shape)
+    if sb and saved is None:
+        raise ValueError("saved is missing")
+    _, sp, _ = _buffer(saved, sb, x, "saved")
+    go = CkSeq(*_seq(grad_out, "grad_out", x.dtype, dev, x.shape))
+    gs = _par(grad_state, "grad_state", dev, ss)
+    ch = ss[1:]
+    if grads is None:
+        new = functools.partial(torch.empty, dtype=torch.float32, device=x.device)
+        g = {"g_x": _fresh(x), "g_f": _fresh(f),
+             "g_f_bias": new(ch) if f_bias is None else torch.empty_like(f_bias),
+             "g_state0": new(ss) if grad_state is None else torch.empty_like(grad_state)}
+        if i is not None:
+            g["g_i"] = _fresh(i)
+            g["g_i_bias"] = new(ch) if i_bias is None else torch.empty_like(i_bias)
+        if z is not None:
+            g["g_z"] = _fresh(z)
+        rows_ = _dense(x.shape, ch[0])
+        seqs = [(g[k].data_ptr(), *rows_) if k in g else _NONE
+                for k in ("g_x", "g_f", "g_i", "g_z")]
+        pars = [g[k].data_ptr() if k in g else 0 for k in ("g_f_bias", "g_i_bias", "g_state0")]
+    else:
+        g = grads
+        seqs = [_NONE if t is None else _seq(g[k], k, x.dtype, dev, x.shape)
+                for k, t in (("g_x", x), ("g_f", f), ("g_i", i), ("g_z", z))]
+        pars = [_par(g.get("g_f_bias"), "g_f_bias", dev, ch),
+                0 if i is None else _par(g.get("g_i_bias"), "g_i_bias", dev, ch),
+                _par(g.get("g_state0"), "g_state0", dev, ss)]
+        _written(tuple(t for t in g.values() if t is not None))
+    out = _GATED_GRADS.pack(*seqs[0], *seqs[1], *seqs[2], *seqs[3], *pars)
+    workspace, wp, wn = _buffer(workspace, wb, x, "workspace")
+    _call(lib().ck_gated_backward, dev, (shape, inputs, sp, go, gs, out, wp, wn))
+    return g
+
+
+def gated_scan_step(state, x, f, i=None, z=None, f_bias=None, i_bias=None, out=None,
+                    new_state=None, stream=None):
+    """Run ``ck_gated_step``: one token per row.  x, f, i, z: [B, D]; state:
+    fp32 [B, D], updated in place unless ``new_state`` is given.  Returns (out
+    [B, D], the new state)."""
+    if stream is not None:
+        return _on_stream(stream, gated_scan_step, state, x, f, i, z, f_bias, i_bias, out,
+                          new_state)
+    if state is None:
+        raise ValueError("state is missing")
+    shape, inputs, dev, ss = _gated_call(x, f, i, z, f_bias, i_bias, state, None, step=True)
+    new_state = state if new_state is None else new_state
+    out, os = _out_seq(out, "out", x)
+    _call(lib().ck_gated_step, dev, (shape, inputs, os, _par(new_state, "new_state", dev, ss)))
+    _written((new_state,))
+    return out, new_state
+
+
+class _GatedScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, f, i, z, f_bias, i_bias, state0, lengths, recording):
+        x, f, i, z = (_rows(t) for t in (x, f, i, z))
+        f_bias, i_bias, state0 = _cont(f_bias), _cont(i_bias), _cont(state0)
+        out, state, saved, _ = gated_scan_forward(
+            x, f, i, z, f_bias, i_bias, state0, lengths,
+            save=recording and any(ctx.needs_input_grad))
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(x, f, i, z, f_bias, i_bias, lengths, saved)
+        return out, state
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_out, grad_state):
+        x, f, i, z, f_bias, i_bias, lengths, saved = ctx.saved_tensors
+        go = torch.zeros_like(x) if grad_out is None else _rows(grad_out)
+        g = gated_scan_backward(x, f, saved, go, i, z, f_bias, i_bias, lengths,
+                                grad_state=_cont(grad_state))
+        return (g["g_x"], g["g_f"], g.get("g_i"), g.get("g_z"),
+                None if f_bias is None else g["g_f_bias"],
+                None if i_bias is None else g["g_i_bias"],
+                g["g_state0"] if ctx.needs_input_grad[6] else None, None, None)
+
+
+def gated_scan(x, f, i=None, z=None, f_bias=None, i_bias=None, state0=None, lengths=None):
+    """The gated scan as one autograd node: returns (out [T, B, D], the state
+    after each row's last step [B, D]); gradients reach every tensor argument
+    but ``lengths``.  Shapes as for ``gated_scan_forward``."""
+    return _GatedScan.apply(x, f, i, z, f_bias, i_bias, state0, lengths, torch.is_grad_enabled())
+
+
 # --------------------------------------------------------- short convolution
 
 def _conv_call(x, weight, bias, activation, step=False):
@@ -594,6 +772,7 @@ def dropout(x, p: float, seed: int, offset: int = 0, residual=None, held: bool =
 
 
 __all__ = ["selective_scan", "selective_scan_sizes", "selective_scan_forward",
-           "selective_scan_backward", "selective_scan_step", "short_conv", "short_conv_forward",
+           "selective_scan_backward", "selective_scan_step", "gated_scan", "gated_scan_sizes",
+           "gated_scan_forward", "gated_scan_backward", "gated_scan_step", "short_conv", "short_conv_forward",
            "short_conv_backward", "short_conv_step", "dropout", "dropout_forward",
            "dropout_backward"]

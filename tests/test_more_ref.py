@@ -1,0 +1,266 @@
+"""The fp64 definition of the gated scan against differences and against a scan
+that knows it as a special case, and the host-side refusals of the gated scan, the
+gradients' norm and beam search (checked before any device work)."""
+import ctypes
+import os
+
+import numpy as np
+import pytest
+
+import gated_ref
+import sequence_ref
+import sparse_graph_recurrent_amd as sgr
+from sparse_graph_recurrent_amd.beam import BeamShape, BeamState
+from sparse_graph_recurrent_amd.clip import ClipTensor
+from sparse_graph_recurrent_amd.sequence import CkSeq, GatedGrads, GatedInputs, GatedShape
+
+NULL_ARG, BAD_SIZE, TOO_LARGE, WORKSPACE, BAD_VALUE = 1, 2, 5, 6, 12
+
+
+def problem(seed, T, B, D, own, z, lengths, grads=True):
+    r = np.random.default_rng(seed)
+    p = {"x": r.standard_normal((T, B, D)), "f": 2 * r.standard_normal((T, B, D)),
+         "i": r.standard_normal((T, B, D)) if own else None,
+         "z": r.standard_normal((T, B, D)) if z else None, "f_bias": r.standard_normal(D),
+         "i_bias": r.standard_normal(D) if own else None, "state0": r.standard_normal((B, D)),
+         "lengths": None if lengths is None else np.array(lengths)}
+    if grads:
+        p.update(go=r.standard_normal((T, B, D)), gstate=r.standard_normal((B, D)))
+    return p
+
+
+@pytest.mark.parametrize("own,z,lengths", [(True, True, None), (False, False, None),
+                                           (False, True, [0, 3, 6]), (True, False, [6, 1, 9])])
+def test_gradient_formulas_against_differences(own, z, lengths):
+    p = problem(3, 6, 3, 2, own, z, lengths)
+    got = gated_ref.gated(p)
+    q = {k: v for k, v in p.items() if k not in ("go", "gstate")}
+    eps = 1e-6
+
+    def loss():
+        o = gated_ref.gated(q)
+        return (o["out"][0] * p["go"]).sum() + (o["state"][0] * p["gstate"]).sum()
+
+    for k in ("x", "f", "f_bias", "state0") + (("i", "i_bias") if own else ()) + \
+            (("z",) if z else ()):
+        want = np.zeros_like(q[k])
+        for at in np.ndindex(*q[k].shape):
+            old = q[k][at]
+            q[k][at] = old + eps
+            hi = loss()
+            q[k][at] = old - eps
+            want[at] = (hi - loss()) / (2 * eps)
+            q[k][at] = old
+        # central differences of a smooth function: about 1e-9 of the values
+        np.testing.assert_allclose(got["g_" + k][0], want, rtol=1e-6, atol=1e-7, err_msg=k)
+
+
+def test_definition_is_a_selective_scan_of_one_state():
+    """With A = -1, dt = -log a and the input g x / dt for every channel alone."""
+    T, B, D = 9, 2, 3
+    p = problem(4, T, B, D, True, True, [9, 5], grads=False)
+    got = gated_ref.gated(p)
+    for d in range(D):
+        a = sequence_ref.sigmoid(p["f"][..., d] + p["f_bias"][d])
+        g = sequence_ref.sigmoid(p["i"][..., d] + p["i_bias"][d])
+        dt = -np.log(a)[..., None]
+        s = sequence_ref.scan({
+            "u": (g * p["x"][..., d])[..., None] / dt, "delta": dt, "A": -np.ones((1, 1)),
+            "B": np.ones((T, B, 1, 1)), "C": np.ones((T, B, 1, 1)), "D": np.zeros(1),
+            "z": p["z"][..., d:d + 1], "delta_bias": np.zeros(1),
+            "state0": p["state0"][:, d:d + 1, None], "lengths": p["lengths"], "softplus": False})
+        np.testing.assert_allclose(got["out"][0][..., d], s["out"][..., 0], rtol=1e-12, atol=1e-14)
+        np.testing.assert_allclose(got["state"][0][:, d], s["state"][:, 0, 0], rtol=1e-12)
+
+
+# ------------------------------------------------------------------ refusals
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(sgr.LIB_PATH):
+        from sparse_graph_recurrent_amd import build
+        build.build()
+    return sgr.lib()
+
+
+FAKE = 0x10000  # never dereferenced: every call here fails before any device work
+NONE = CkSeq(None, 0, 0)
+SEQ = CkSeq(FAKE, 128, 64)
+
+
+def _shape(**kw):
+    return ctypes.byref(GatedShape(*[kw.get(k, v) for k, v in
+                                     dict(T=40, B=2, D=64, dtype=1).items()]))
+
+
+def _inputs(x=SEQ, f=SEQ, i=NONE, z=NONE, f_bias=None, i_bias=None, state0=None, lengths=None):
+    return ctypes.byref(GatedInputs(x, f, i, z, f_bias, i_bias, state0, lengths))
+
+
+def _grads(x=SEQ, f=SEQ, i=NONE, z=NONE, f_bias=None, i_bias=None, state0=None):
+    return ctypes.byref(GatedGrads(x, f, i, z, f_bias, i_bias, state0))
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), BAD_SIZE), (dict(B=0), BAD_SIZE), (dict(D=-2), BAD_SIZE),
+    (dict(T=2**31), TOO_LARGE), (dict(B=2**31), TOO_LARGE), (dict(T=2**20, B=2**30), TOO_LARGE),
+    (dict(dtype=3), BAD_VALUE)])
+def test_gated_shape_refusals(L, kw, status):
+    n = ctypes.c_size_t()
+    assert L.ck_gated_sizes(_shape(**kw), ctypes.byref(n), None, None) == status
+    assert L.ck_gated_forward(_shape(**kw), _inputs(), SEQ, None, None, FAKE, 2**40,
+                              None) == status
+    assert L.ck_gated_backward(_shape(**kw), _inputs(), FAKE, SEQ, None, _grads(), FAKE, 2**40,
+                               None) == status
+    if "T" not in kw:
+        assert L.ck_gated_step(_shape(**{"T": 1, **kw}), _inputs(), SEQ, FAKE, None) == status
+
+
+def test_gated_call_refusals(L):
+    s = _shape()
+    assert L.ck_gated_sizes(None, None, None, None) == NULL_ARG
+    fwd = lambda i=_inputs(), out=SEQ, state=None, saved=None, ws=FAKE: L.ck_gated_forward(
+        s, i, out, state, saved, ws, 2**40, None)
+    assert fwd(i=None) == NULL_ARG
+    assert fwd(out=NONE) == NULL_ARG
+    assert fwd(i=_inputs(x=NONE)) == NULL_ARG
+    assert fwd(i=_inputs(f=NONE)) == NULL_ARG
+    assert fwd(i=_inputs(i=CkSeq(FAKE + 1, 128, 64))) == BAD_VALUE
+    assert fwd(i=_inputs(z=CkSeq(FAKE, -128, 64))) == BAD_VALUE
+    assert fwd(i=_inputs(x=CkSeq(FAKE, 2**30, 64))) == BAD_VALUE
+    assert fwd(i=_inputs(f_bias=FAKE + 2)) == BAD_VALUE
+    assert fwd(i=_inputs(i_bias=FAKE + 2)) == BAD_VALUE
+    assert fwd(i=_inputs(state0=FAKE + 1)) == BAD_VALUE
+    assert fwd(state=FAKE + 2) == BAD_VALUE
+    assert fwd(saved=FAKE + 16) == BAD_VALUE
+    for q in (CkSeq(FAKE, 0, 64), CkSeq(FAKE, 128, 0), CkSeq(FAKE, 63, 64), CkSeq(FAKE, 128, 63)):
+        assert fwd(out=q) == BAD_VALUE
+    back = lambda i=_inputs(), saved=FAKE, go=SEQ, gs=None, g=_grads(), ws=FAKE, n=2**40: \
+        L.ck_gated_backward(s, i, saved, go, gs, g, ws, n, None)
+    assert back(saved=None) == NULL_ARG and back(saved=FAKE + 16) == BAD_VALUE
+    assert back(go=NONE) == NULL_ARG and back(g=None) == NULL_ARG and back(i=None) == NULL_ARG
+    assert back(g=_grads(x=NONE)) == NULL_ARG and back(g=_grads(f=NONE)) == NULL_ARG
+    # a gate's gradient is required when there is that gate
+    assert back(i=_inputs(i=SEQ)) == NULL_ARG and back(i=_inputs(z=SEQ)) == NULL_ARG
+    assert back(gs=FAKE + 2) == BAD_VALUE and back(g=_grads(f_bias=FAKE + 2)) == BAD_VALUE
+    assert back(g=_grads(i_bias=FAKE + 2)) == BAD_VALUE
+    assert back(g=_grads(state0=FAKE + 2)) == BAD_VALUE
+    for q in (CkSeq(FAKE, 0, 64), CkSeq(FAKE, 128, 63)):
+        assert back(g=_grads(x=q)) == BAD_VALUE and back(g=_grads(f=q)) == BAD_VALUE
+        assert back(i=_inputs(i=SEQ), g=_grads(i=q)) == BAD_VALUE
+        assert back(i=_inputs(z=SEQ), g=_grads(z=q)) == BAD_VALUE
+    assert back(ws=None) == NULL_ARG and back(n=16) == WORKSPACE
+    assert back(ws=FAKE + 16) == BAD_VALUE
+    # inputs may be broadcast (the next refusal is the workspace's)
+    assert back(i=_inputs(x=CkSeq(FAKE, 0, 0)), go=CkSeq(FAKE, 0, 64), n=16) == WORKSPACE
+    one = _shape(T=1)
+    assert L.ck_gated_step(s, _inputs(), SEQ, FAKE, None) == BAD_SIZE
+    assert L.ck_gated_step(one, None, SEQ, FAKE, None) == NULL_ARG
+    assert L.ck_gated_step(one, _inputs(), NONE, FAKE, None) == NULL_ARG
+    assert L.ck_gated_step(one, _inputs(), SEQ, None, None) == NULL_ARG
+    assert L.ck_gated_step(one, _inputs(), SEQ, FAKE + 2, None) == BAD_VALUE
+    assert L.ck_gated_step(one, _inputs(lengths=FAKE), SEQ, FAKE, None) == BAD_VALUE
+
+
+def _tensors(*rows):
+    return (ClipTensor * len(rows))(*[ClipTensor(*r) for r in rows])
+
+
+def test_clip_refusals(L):
+    ok = _tensors((FAKE, FAKE, 64, 0))
+    call = lambda t=ok, n=1, m=1.0, norm=FAKE, ws=FAKE, wn=2**20: L.ck_clip_grad_norm(
+        t, n, m, norm, ws, wn, None)
+    assert L.ck_clip_sizes(-1, None) == BAD_SIZE
+    assert call(n=-1) == BAD_SIZE and call(n=2**20 + 1) == TOO_LARGE and call(t=None) == NULL_ARG
+    assert call(t=_tensors((FAKE, FAKE, -1, 0))) == BAD_SIZE
+    assert call(t=_tensors((FAKE, FAKE, 2**45, 0))) == TOO_LARGE
+    assert call(t=_tensors((FAKE, FAKE, 8, 3))) == BAD_VALUE
+    assert call(t=_tensors((None, FAKE, 8, 0))) == NULL_ARG
+    assert call(t=_tensors((FAKE + 2, FAKE + 2, 8, 0))) == BAD_VALUE
+    assert call(t=_tensors((FAKE, FAKE + 1, 8, 1))) == BAD_VALUE
+    for m in (-1.0, float("nan")):
+        assert call(m=m) == BAD_VALUE
+    assert call(norm=None) == NULL_ARG and call(norm=FAKE + 2) == BAD_VALUE
+    assert call(ws=None) == NULL_ARG and call(wn=16) == WORKSPACE and call(ws=FAKE + 8) == BAD_VALUE
+
+
+@pytest.mark.parametrize("rows", [
+    [(FAKE, FAKE, 64, 0), (FAKE, FAKE, 64, 0)],               # the same gradient twice
+    [(FAKE, FAKE, 64, 0), (FAKE + 252, FAKE + 252, 64, 0)],   # their last and first element
+    [(FAKE, FAKE + 4, 64, 0)],                                # an output over its own gradient
+    [(FAKE, 2 * FAKE, 64, 0), (2 * FAKE + 128, 3 * FAKE, 64, 1)],   # over another's gradient
+    [(FAKE, 3 * FAKE, 64, 0), (2 * FAKE, 3 * FAKE, 64, 0)],   # one output for two
+    [(FAKE, None, 64, 0), (FAKE, FAKE, 64, 0)]])              # read, and written elsewhere
+def test_clip_refuses_tensors_over_one_another(L, rows):
+    assert L.ck_clip_grad_norm(_tensors(*rows), len(rows), 1.0, FAKE * 8, FAKE * 16, 2**20,
+                               None) == BAD_VALUE
+    assert "over another" in L.ck_last_error().decode()
+
+
+def _beam(**kw):
+    return ctypes.byref(BeamShape(*[kw.get(k, v) for k, v in
+                                    dict(B=2, K=4, V=100, eos=3, dtype=1).items()]))
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=0), BAD_SIZE), (dict(K=0), BAD_SIZE), (dict(K=33), BAD_SIZE), (dict(V=0), BAD_SIZE),
+    (dict(V=2**31), TOO_LARGE), (dict(B=2**31), TOO_LARGE), (dict(B=2**29, V=2**20), TOO_LARGE),
+    (dict(dtype=3), BAD_VALUE), (dict(eos=100), BAD_VALUE), (dict(eos=-2), BAD_VALUE)])
+def test_beam_shape_refusals(L, kw, status):
+    assert L.ck_beam_sizes(_beam(**kw), None) == status
+    assert L.ck_beam_select(_beam(**kw), SEQ, FAKE, None, FAKE, FAKE, FAKE, None, FAKE, 2**40,
+                            None) == status
+
+
+def test_beam_call_refusals(L):
+    x = CkSeq(FAKE, 400, 100)
+
+    def call(s=_beam(), x=x, scores=FAKE, done=None, out=FAKE, parents=FAKE, tokens=FAKE, ws=FAKE,
+             n=2**40):
+        return L.ck_beam_select(s, x, scores, done, out, parents, tokens, None, ws, n, None)
+
+    assert L.ck_beam_sizes(None, None) == NULL_ARG and call(s=None) == NULL_ARG
+    assert call(x=NONE) == NULL_ARG and call(scores=None) == NULL_ARG
+    assert call(out=None) == NULL_ARG and call(parents=None) == NULL_ARG
+    assert call(tokens=None) == NULL_ARG
+    assert call(x=CkSeq(FAKE + 1, 400, 100)) == BAD_VALUE
+    assert call(x=CkSeq(FAKE, -400, 100)) == BAD_VALUE
+    assert call(scores=FAKE + 2) == BAD_VALUE and call(out=FAKE + 1) == BAD_VALUE
+    assert call(parents=FAKE + 4) == BAD_VALUE and call(tokens=FAKE + 4) == BAD_VALUE
+    assert call(s=_beam(eos=-1), done=FAKE) == BAD_VALUE
+    assert call(ws=None) == NULL_ARG and call(n=16) == WORKSPACE and call(ws=FAKE + 8) == BAD_VALUE
+
+
+def _states(*rows):
+    return (BeamState * len(rows))(*[BeamState(*r) for r in rows])
+
+
+def test_reorder_refusals(L):
+    ok = (FAKE, 2 * FAKE, 1, 64, 64, 0, 64, 0)
+    call = lambda *rows, n=None, parents=FAKE, B=2, K=4: L.ck_beam_reorder(
+        _states(*rows) if rows else None, len(rows) if n is None else n, parents, B, K, None)
+    assert call(ok, B=0) == BAD_SIZE and call(ok, K=0) == BAD_SIZE and call(ok, K=33) == BAD_SIZE
+    assert call(ok, n=-1) == BAD_SIZE and call(ok, B=2**31) == TOO_LARGE
+    assert call(n=5000) == TOO_LARGE and call(n=1) == NULL_ARG
+    assert call(ok, parents=None) == NULL_ARG and call(ok, parents=FAKE + 4) == BAD_VALUE
+    assert call((FAKE, 2 * FAKE, -1, 64, 64, 0, 64, 0)) == BAD_SIZE
+    assert call((FAKE, 2 * FAKE, 1, -64, 64, 0, 64, 0)) == BAD_SIZE
+    assert call((FAKE, 2 * FAKE, 2**30, 2**30, 64, 64, 64, 64)) == TOO_LARGE
+    assert call((None, 2 * FAKE, 1, 64, 64, 0, 64, 0)) == NULL_ARG
+    assert call((FAKE, None, 1, 64, 64, 0, 64, 0)) == NULL_ARG
+    assert call((FAKE, 2 * FAKE, 1, 64, -64, 0, 64, 0)) == BAD_VALUE
+    # rows of the output over one another; pieces over rows
+    for row, seg, segs in ((0, 0, 1), (63, 0, 1), (64, 64, 2), (128, 63, 2), (64, 500, 2),
+                           (100, 64, 2)):
+        assert call((FAKE, 2 * FAKE, segs, 64, 64, 64, row, seg)) == BAD_VALUE, (row, seg)
+    # in place with other strides; the same state twice; what another reads
+    assert call((FAKE, FAKE, 1, 64, 64, 0, 128, 0)) == BAD_VALUE
+    same = (FAKE, FAKE, 1, 64, 64, 0, 64, 0)
+    assert call(same, same) == BAD_VALUE
+    assert call(ok, (3 * FAKE, 2 * FAKE, 1, 64, 64, 0, 64, 0)) == BAD_VALUE
+    assert call(ok, (2 * FAKE, 3 * FAKE, 1, 64, 64, 0, 64, 0)) == BAD_VALUE
+
+
+def test_a_call_of_no_states_returns(L):
+    assert L.ck_beam_reorder(None, 0, FAKE, 1, 1, None) == 0
+    assert L.ck_beam_reorder(_states((None, None, 0, 64, 0, 0, 0, 0)), 1, FAKE, 1, 1, None) == 0
