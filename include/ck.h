@@ -536,7 +536,7 @@ ck_status ck_dropout_backward(const ck_dropout_shape* shape, ck_seq grad_out, ck
  *   h_t   = a_t h_{t-1} + g_t x_t
  *   out_t = h_t z_t s(z_t)            (h_t without z)
  *
- * with h_{-1} = state0.  Steps lie less than 2^30 elements apart.  A gate that is
+ * with h_{-1} = state0.  Steps lie less than 2^26 elements apart.  A gate that is
  * almost 1 is held as what it lacks, so that a state is kept over as many steps as
  * the gate says.  A state that is not finite may go on as a NaN.
  */

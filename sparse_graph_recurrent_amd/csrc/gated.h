@@ -27,9 +27,10 @@ namespace ckhip {
 
 constexpr int kGateStep = 8;      // steps of a slot, and of a saved state
 constexpr int kGateLanes = 32;    // lanes of a slot
-constexpr int kGateMaxWaves = 16; // of a workgroup
-// (a step's bytes, 4 an element and fewer, in 32 bits: see Rows)
-constexpr int64_t kGateMaxStrideT = (int64_t(1) << 30) - 1;
+constexpr int kGateFwdWaves = 8, kGateBwdWaves = 8;  // of a workgroup, at most
+// Offsets from a window's first step are 32-bit bytes; a window of a single wave (16
+// steps) reaches this far.
+constexpr int64_t kGateMaxStrideT = (int64_t(1) << 26) - 1;
 
 // How a call is spread over the chip.
 struct GatePlan {
@@ -37,7 +38,7 @@ struct GatePlan {
   int waves;    // of a workgroup
   int groups;   // of channels, in a row
   int chunks;   // of a row's steps
-  int chunk;    // steps of a chunk, a multiple of a window's unless there is one
+  int chunk;    // steps of a chunk, a multiple of a slot's unless there is one
 };
 
 template <typename E>
@@ -53,104 +54,127 @@ struct GateArgs {
   int T, B, D, groups, chunks, chunk;
 };
 
-// The logistic function of v and of -v: `small` is that of -|v|, `big` that of |v|;
-// each has its own relative error ((4 + 1.3 |v|) 2^-24 for the small one), so that a
-// gate that is almost open keeps what is missing from it.
+// A gate s(v), held as the smaller of s(v) and s(-v) with its own relative error
+// ((4 + 1.3 |v|) 2^-24), so that a gate that is almost open keeps what is missing from
+// it.  Its sign bit is set where the gate is open (v > 0): `m` is what is missing.
 struct Gate {
-  float small, big;
-};
-__device__ __forceinline__ Gate gate_hw(float v) {
-  const float e = exp2_hw(-kLog2e * fabsf(v));
-  const float r = rcp_hw(1.0f + e);
-  return Gate{e * r, r};
-}
-
-// A step's decay: -q where a >= 1/2 and a where it is below (the sign bit tells), so
-// that states neither leak by the rounding of an a next to 1 nor keep what an a next
-// to 0 should have taken.
-struct Decay {
   float m;
-  __device__ __forceinline__ float times(float h, float u) const {  // a h + u
-    const float kept = __builtin_bit_cast(
-        float, __builtin_bit_cast(int, h) & (__builtin_bit_cast(int, m) >> 31));
-    return kept + fmaf(m, h, u);
+  __device__ __forceinline__ bool open() const { return __builtin_bit_cast(int, m) < 0; }
+  __device__ __forceinline__ float value() const { return open() ? 1.0f + m : m; }
+  __device__ __forceinline__ float rest() const { return open() ? -m : 1.0f - m; }  // s(-v)
+  __device__ __forceinline__ float slope() const { return fabsf(m) * (1.0f - fabsf(m)); }
+  // 1 where the gate is open, else 0.
+  __device__ __forceinline__ float keep() const {
+    return __builtin_bit_cast(float, (__builtin_bit_cast(int, m) >> 31) & 0x3F800000);
+  }
+  // value() h + u: an open gate takes from h what it does not let through, so that
+  // states neither leak by the rounding of a decay next to 1 nor keep what one next to
+  // 0 should have taken.
+  __device__ __forceinline__ float times(float h, float u) const {
+    return fmaf(keep(), h, fmaf(m, h, u));
   }
 };
-constexpr float kKeep = -0.0f;  // Decay of a step that changes nothing
-
-// The forget gate at v: the decay, q, and a.
-struct Forget {
-  Decay decay;
-  float q, a;
-};
-__device__ __forceinline__ Forget forget_hw(float v) {
-  const Gate g = gate_hw(v);
-  const bool open = v >= 0.0f;
-  return Forget{Decay{open ? -g.small : g.small}, open ? g.small : g.big,
-                open ? g.big : g.small};
+constexpr Gate kGateKeep = {-0.0f};  // the decay of a step that changes nothing
+// The gate at -nv.
+__device__ __forceinline__ Gate gate_hw(float nv) {
+  const float e = exp2_hw(-kLog2e * fabsf(nv));
+  return Gate{__builtin_copysignf(e * rcp_hw(1.0f + e), nv)};
 }
 
-// kGateStep rows of one tensor at a slot's channels.
-template <typename E, int V>
-struct GateTile {
-  Pack<E, V> v[kGateStep];
-
-  // Rows t .. of which the first n exist for this lane (n <= 0: none).  A lane whose
-  // channels pass the row's end has them begin earlier (`c` is the first it loads).
-  __device__ __forceinline__ void load(const Seq<const E>& s, int64_t t, int64_t b, int64_t c,
-                                       int n) {
-    const Rows<const E> rows(s, t, b, c);
-    if (__all(n >= kGateStep)) {
-#pragma unroll
-      for (int k = 0; k < kGateStep; ++k) v[k] = pack_load<true, E, V>(rows.at(k), V);
-    } else {
-#pragma unroll
-      for (int k = 0; k < kGateStep; ++k) {
-        v[k] = Pack<E, V>{};
-        if (k < n) v[k] = pack_load<true, E, V>(rows.at(k), V);
-      }
-    }
+// The rows of one tensor from a window's first step on: an address that the whole
+// wave shares and 32-bit offsets.
+template <typename E>
+struct GateRows {
+  using Raw = std::remove_const_t<E>;
+  char* base;
+  uint32_t step;  // bytes
+  __device__ __forceinline__ GateRows(const Seq<E>& s, int64_t t, int64_t b, int64_t c)
+      : base(reinterpret_cast<char*>(const_cast<Raw*>(s.row(t, b) + c))),
+        step((uint32_t)s.st * (uint32_t)sizeof(E)) {}
+  __device__ __forceinline__ E* at(uint32_t offset) const {
+    return reinterpret_cast<E*>(base + offset);
   }
+  // The next step, as the wave's address.
+  __device__ __forceinline__ void next() { base += step; }
 };
+// An offset that the compiler computes where it is used: one that it carries through a
+// loop it carries as a 64-bit address a lane, for each of a tile's rows.
+__device__ __forceinline__ uint32_t gate_offset(uint32_t o) {
+  asm volatile("" : "+v"(o));
+  return o;
+}
 
-// Where a thread stands: its slot, its channels and its row.
+// Where a thread stands: its slot, its channels and its row.  Lanes whose channels pass
+// the row's end have them begin earlier: some channels are worked on in two lanes, which
+// come to the same bits and store them both.
 template <int V>
 struct GateSpot {
   int wave, waves, lane, upper;  // upper: the wave's second slot
   int group, chunk, b, len;      // len: steps of the row that hold text
-  int64_t c;                     // first channel loaded
-  int own;                       // the lane's own channels are c + own .. c + V - 1
-  bool live;                     // it has any
+  int64_t c, c0;                 // first channel loaded, and of the workgroup's
+  int cl;                        // c - c0
 
   template <typename A>
   __device__ __forceinline__ bool at(const A& s, int64_t id, int chunks) {
-    group = (int)(id % s.groups);
-    const int64_t r = id / s.groups;
-    b = (int)(r % s.B);
-    chunk = (int)(r / s.B);
+    // (groups, rows and chunks together are below 2^31: rows times channels below 2^36)
+    const uint32_t r = (uint32_t)id / (uint32_t)s.groups;
+    group = (int)((uint32_t)id - r * (uint32_t)s.groups);
+    chunk = (int)(r / (uint32_t)s.B);
+    b = (int)(r - (uint32_t)chunk * (uint32_t)s.B);
     if (chunk >= chunks) return false;
     wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     waves = (int)blockDim.x >> 6;
     lane = (int)threadIdx.x & (kGateLanes - 1);
     upper = ((int)threadIdx.x >> 5) & 1;
     const int64_t want = ((int64_t)group * kGateLanes + lane) * V;
-    live = want < s.D;
     c = min(want, (int64_t)s.D - V);
-    own = (int)min(want - c, (int64_t)V);
+    c0 = min((int64_t)group * kGateLanes * V, (int64_t)s.D - V);
+    cl = (int)(c - c0);
     len = s.lengths ? max(0, min(s.lengths[b], s.T)) : s.T;
     return true;
   }
 };
 
-// The lane's own channels of a packed result, to one row.
+template <int ALIGN>
+struct __attribute__((packed, aligned(ALIGN))) GateWord {
+  uint32_t bits;
+};
+
+// kGateStep rows of one tensor at a slot's channels.  Steps behind a row's text load
+// its last step instead: a load without branches can stay in flight over the work on
+// the tile before.
 template <typename E, int V>
-__device__ __forceinline__ void gate_store(E* p, const float (&y)[V], bool live, int own) {
-  if (!live) return;
-  if (own == 0) return pack_store<true, E, V>(p, y, V);
+struct GateTile {
+  static_assert(sizeof(E) * V <= 4, "a lane's channels are held as one register's bits");
+  uint32_t v[kGateStep];
+
+  // Channel j of step k.
+  __device__ __forceinline__ float get(int k, int j) const {
+    if constexpr (std::is_same_v<E, float>) return __builtin_bit_cast(float, v[k]);
+    else if constexpr (std::is_same_v<E, bf16_t>)
+      return __builtin_bit_cast(float, j ? v[k] & 0xFFFF0000u : v[k] << 16);
+    else return (float)__builtin_bit_cast(E, (uint16_t)(j ? v[k] >> 16 : v[k]));
+  }
+
+  // Steps from + k of the window that begins at step t, the last of them `last` (>= 0).
+  // ALL: they all come before it.
+  template <bool ALL>
+  __device__ __forceinline__ void load(const Seq<const E>& s, const GateSpot<V>& at, int t,
+                                       int from, int last) {
+    GateRows<const E> rows(s, t, at.b, at.c0);
+    uint32_t o = gate_offset((uint32_t)(ALL ? from : min(from, last)) * rows.step +
+                             (uint32_t)at.cl * (uint32_t)sizeof(E));
 #pragma unroll
-  for (int j = 0; j < V; ++j)
-    if (j >= own) p[j] = (E)y[j];
-}
+    for (int k = 0; k < kGateStep; ++k) {
+      if constexpr (sizeof(E) * V == 4)
+        v[k] = reinterpret_cast<const GateWord<alignof(E)>*>(rows.at(o))->bits;
+      else
+        v[k] = *reinterpret_cast<const uint16_t*>(rows.at(o));
+      if constexpr (ALL) rows.next();
+      else o += from + k < last ? rows.step : 0;
+    }
+  }
+};
 
 // The pair (product of a, state) of some steps.
 template <int V>
@@ -158,14 +182,21 @@ struct alignas(8 * V) GatePair {
   float p[V], h[V];
 };
 
-// Folds the pairs of a workgroup's slots.  Forward in time (REVERSE: backward):
-// `carry` is the state before the window and becomes the one behind it; returns the
-// state before the thread's slot.  The buffer takes turns, so that one barrier a
-// window is enough.
-template <bool REVERSE, int V>
-__device__ __forceinline__ void gate_fold(GatePair<V> (*lds)[kGateLanes], const GateSpot<V>& at,
-                                          const GatePair<V>& mine, float (&carry)[V],
-                                          float (&in)[V]) {
+// Where the slots of a workgroup meet.  Both take turns, so that one barrier a window
+// is enough.
+template <int V, int WAVES>
+struct GateMeet {
+  GatePair<V> pair[2][WAVES][kGateLanes];   // of each wave
+  GatePair<V> carry[2][kGateLanes];         // h: the state before a window; p: see gate_fold
+};
+
+// Folds the pairs of a workgroup's slots.  Forward in time (REVERSE: backward).
+// Returns the state before the thread's slot; the wave that comes last leaves the state
+// behind the window as the next one's carry, and with it the product of all decays so
+// far.  (The first carry is written before the first window.)
+template <bool REVERSE, int V, int WAVES>
+__device__ __forceinline__ void gate_fold(GateMeet<V, WAVES>& meet, int turn, const GateSpot<V>& at,
+                                          const GatePair<V>& mine, float (&in)[V]) {
   GatePair<V> other, both;
   const bool second = REVERSE ? !at.upper : at.upper;  // behind the wave's other slot
 #pragma unroll
@@ -176,24 +207,41 @@ __device__ __forceinline__ void gate_fold(GatePair<V> (*lds)[kGateLanes], const 
     both.h[j] = second ? fmaf(mine.p[j], other.h[j], mine.h[j])
                        : fmaf(other.p[j], mine.h[j], other.h[j]);
   }
-  if (!at.upper) lds[at.wave][at.lane] = both;
+  if (!at.upper) meet.pair[turn][at.wave][at.lane] = both;
   __syncthreads();
-  float h[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) h[j] = carry[j];
+  GatePair<V> c = meet.carry[turn][at.lane];
+  const int rank = REVERSE ? at.waves - 1 - at.wave : at.wave;
 #pragma unroll 4
-  for (int k = 0; k < at.waves; ++k) {
-    const int w = REVERSE ? at.waves - 1 - k : k;
-    const GatePair<V> one = lds[w][at.lane];
-    if (w == at.wave) {
+  for (int k = 0; k < rank; ++k) {
+    const GatePair<V> one = meet.pair[turn][REVERSE ? at.waves - 1 - k : k][at.lane];
 #pragma unroll
-      for (int j = 0; j < V; ++j) in[j] = second ? fmaf(other.p[j], h[j], other.h[j]) : h[j];
+    for (int j = 0; j < V; ++j) {
+      c.h[j] = fmaf(one.p[j], c.h[j], one.h[j]);
+      c.p[j] *= one.p[j];
     }
-#pragma unroll
-    for (int j = 0; j < V; ++j) h[j] = fmaf(one.p[j], h[j], one.h[j]);
   }
 #pragma unroll
-  for (int j = 0; j < V; ++j) carry[j] = h[j];
+  for (int j = 0; j < V; ++j) in[j] = second ? fmaf(other.p[j], c.h[j], other.h[j]) : c.h[j];
+  if (rank == at.waves - 1 && !at.upper) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      c.h[j] = fmaf(both.p[j], c.h[j], both.h[j]);
+      c.p[j] *= both.p[j];
+    }
+    meet.carry[turn ^ 1][at.lane] = c;
+  }
+}
+
+// Leaves a chunk's pair to the launch that follows.
+template <int V, typename A>
+__device__ __forceinline__ void gate_sum_store(const A& s, const GateSpot<V>& at,
+                                               const GatePair<V>& pair) {
+  float* to = s.sums + ((int64_t)at.chunk * s.B * s.D + (int64_t)at.b * s.D + at.c) * 2;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    to[2 * j] = pair.p[j];
+    to[2 * j + 1] = pair.h[j];
+  }
 }
 
 template <typename E>

@@ -3,12 +3,12 @@
 #include "gated.h"
 
 #include <algorithm>
+#include <initializer_list>
 
 namespace ckhip {
 namespace {
 
 constexpr int64_t kGateCus = 256;
-constexpr int kGateFwdWaves = kGateMaxWaves, kGateBwdWaves = 8;
 
 ck_status gate_check_shape(const ck_gated_shape* s) {
   if (!s) {
@@ -35,6 +35,16 @@ GatePlan gate_plan(const ck_gated_shape& s, int most_waves) {
   p.chunk = (int)((per + window - 1) / window * window);
   p.chunks = p.chunk ? (int)((s.T + p.chunk - 1) / p.chunk) : 1;
   return p;
+}
+
+// Fewer waves where a window's offsets would pass 32 bits (the chunks stay: the
+// workspace does not go by strides).
+void gate_reach(GatePlan* p, int dtype, std::initializer_list<const ck_seq*> tensors) {
+  int64_t step = 1;
+  for (const ck_seq* q : tensors)
+    if (q->data) step = std::max(step, q->stride_t * (int64_t)seq_elem_bytes(dtype));
+  const int64_t steps = (UINT32_MAX - 256) / step + 1;
+  p->waves = (int)std::min<int64_t>(p->waves, std::max<int64_t>(1, steps / (2 * kGateStep)));
 }
 
 // Workspace: the chunks' pairs, then (backward) the bias gradients' parts.
@@ -122,11 +132,11 @@ __global__ __launch_bounds__(kGateOneThreads) void gate_one(const GateArgs<E> s,
   for (int j = 0; j < V; ++j) {
     h[j] = y[j] = 0.0f;
     if (j >= n) continue;
-    const Forget g = forget_hw((float)f.v[j] + (s.f_bias ? s.f_bias[c + j] : 0.0f));
-    float take = g.q;
+    const Gate g = gate_hw((s.f_bias ? -s.f_bias[c + j] : 0.0f) - (float)f.v[j]);
+    float take = g.rest();
     if (s.i.p) take = sigmoid_hw((float)i.v[j] + (s.i_bias ? s.i_bias[c + j] : 0.0f));
     const float before = s.state0 ? s.state0[b * s.D + c + j] : 0.0f;
-    y[j] = h[j] = g.decay.times(before, take * (float)x.v[j]);
+    y[j] = h[j] = g.times(before, take * (float)x.v[j]);
     if (s.z.p) {
       const float v = (float)z.v[j];
       y[j] *= v * sigmoid_hw(v);
@@ -169,7 +179,8 @@ extern "C" ck_status ck_gated_forward(const ck_gated_shape* shape, const ck_gate
   if (rc == CK_OK) rc = gate_check_out(*shape, out, shape->T == 0, "out");
   if (rc == CK_OK) rc = gate_check_f32(state, "state");
   if (rc != CK_OK) return rc;
-  const GatePlan p = gate_plan(*shape, kGateFwdWaves);
+  GatePlan p = gate_plan(*shape, kGateFwdWaves);
+  gate_reach(&p, shape->dtype, {&in->x, &in->f, &in->i, &in->z, &out});
   rc = seq_check_ws(workspace, workspace_bytes, gate_ws(*shape, p, false).total);
   if (rc == CK_OK && saved) rc = check_aligned(saved, "saved");
   if (rc != CK_OK) return rc;
@@ -206,7 +217,9 @@ extern "C" ck_status ck_gated_backward(const ck_gated_shape* shape, const ck_gat
   if (rc == CK_OK) rc = gate_check_f32(grads->state0, "the gradient of state0");
   if (rc == CK_OK && saved) rc = check_aligned(saved, "saved");
   if (rc != CK_OK) return rc;
-  const GatePlan p = gate_plan(*shape, kGateBwdWaves);
+  GatePlan p = gate_plan(*shape, kGateBwdWaves);
+  gate_reach(&p, shape->dtype, {&in->x, &in->f, &in->i, &in->z, &grad_out, &grads->x, &grads->f,
+                                &grads->i, &grads->z});
   const GateWs ws = gate_ws(*shape, p, true);
   rc = seq_check_ws(workspace, workspace_bytes, ws.total);
   if (rc != CK_OK) return rc;

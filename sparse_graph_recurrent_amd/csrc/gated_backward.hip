@@ -13,8 +13,6 @@
 namespace ckhip {
 namespace {
 
-constexpr int kGateBwdWaves = 8;
-
 // silu(z) and its derivative.
 struct Silu {
   float value, slope;
@@ -24,77 +22,120 @@ __device__ __forceinline__ Silu silu_hw(float z) {
   return Silu{z * s, s * fmaf(z, 1.0f - s, 1.0f)};
 }
 
-template <typename E, int V, bool I, bool Z>
+// SUM: the pairs (product of a, adjoint) of all chunks but the first, for the launch
+// that follows.
+template <typename E, int V, bool I, bool Z, bool SUM>
 __global__ __launch_bounds__(64 * kGateBwdWaves) void gate_bwd(const GateArgs<E> s) {
-  __shared__ GatePair<V> lds[2][kGateBwdWaves][kGateLanes];
-  __shared__ float bias[2 * kGateBwdWaves][2 * V][kGateLanes];
+  __shared__ GateMeet<V, kGateBwdWaves> meet;
+  __shared__ float bias[SUM ? 1 : 2 * kGateBwdWaves][2 * V][kGateLanes];
   GateSpot<V> at;
-  if (!at.at(s, seq_block(), s.chunks)) return;
-  const int t0 = at.chunk * s.chunk, t1 = min(t0 + s.chunk, s.T);
+  if (!at.at(s, seq_block(), SUM ? s.chunks - 1 : s.chunks)) return;
+  const int t0 = (at.chunk + (SUM ? 1 : 0)) * s.chunk, t1 = min(t0 + s.chunk, s.T);
   const int window = 2 * at.waves * kGateStep;
-  float fb[V], ib[V], carry[V], sum_f[V] = {}, sum_i[V] = {};
+  const int slot = (2 * at.wave + at.upper) * kGateStep;  // its first step in a window
+  const int steps = min(at.len, t1);
   const int64_t col = (int64_t)at.b * s.D + at.c;
+  GateTile<E, V> x, f, i, z, go, nx, nf, ni, nz, ngo;
+  float nbefore[V] = {};
+  auto fetch = [&](auto all, int t) {
+    constexpr bool ALL = decltype(all)::value;
+    const int last = steps - 1 - t;
+    nf.template load<ALL>(s.f, at, t, slot, last);
+    if constexpr (!SUM) {
+      if constexpr (I) ni.template load<ALL>(s.i, at, t, slot, last);
+      nx.template load<ALL>(s.x, at, t, slot, last);
+      const float* p =
+          s.saved + ((int64_t)((t + (ALL ? slot : min(slot, last))) / kGateStep) * s.B * s.D + col);
+#pragma unroll
+      for (int j = 0; j < V; ++j) nbefore[j] = p[j];
+    }
+    if constexpr (Z) nz.template load<ALL>(s.z, at, t, slot, last);
+    ngo.template load<ALL>(s.go, at, t, slot, last);
+  };
+  int t = t0 + (t1 - t0 - 1) / window * window;  // windows from the last to the first
+  for (; t >= t0 && t >= steps; t -= window) {   // behind the text
+    if constexpr (SUM) continue;
+    GateRows<E> gx(s.gx, t, at.b, at.c0), gf(s.gf, t, at.b, at.c0), gi(s.gi, t, at.b, at.c0),
+        gz(s.gz, t, at.b, at.c0);
+    const float none[V] = {};
+    const uint32_t own = (uint32_t)at.cl * (uint32_t)sizeof(E);
+#pragma unroll 1
+    for (int k = slot; k < slot + kGateStep && t + k < t1; ++k) {
+      pack_store<true, E, V>(gx.at((uint32_t)k * gx.step + own), none, V);
+      pack_store<true, E, V>(gf.at((uint32_t)k * gf.step + own), none, V);
+      if constexpr (I) pack_store<true, E, V>(gi.at((uint32_t)k * gi.step + own), none, V);
+      if constexpr (Z) pack_store<true, E, V>(gz.at((uint32_t)k * gz.step + own), none, V);
+    }
+  }
+  if (t >= t0) fetch(std::false_type(), t);
+  float fb[V], ib[V], sum_f[V] = {}, sum_i[V] = {};  // (the biases with their sign turned)
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    fb[j] = s.f_bias ? s.f_bias[at.c + j] : 0.0f;
-    ib[j] = I && s.i_bias ? s.i_bias[at.c + j] : 0.0f;
-    carry[j] = s.gstate ? s.gstate[col + j] : 0.0f;
+    fb[j] = s.f_bias ? -s.f_bias[at.c + j] : 0.0f;
+    ib[j] = I && s.i_bias ? -s.i_bias[at.c + j] : 0.0f;
   }
-  for (int k = s.chunks - 1; k > at.chunk; --k) {
-    const float* p = s.sums + ((int64_t)(k - 1) * s.B * s.D + col) * 2;
+  if (threadIdx.x < kGateLanes) {
+    GatePair<V> c;
 #pragma unroll
-    for (int j = 0; j < V; ++j) carry[j] = fmaf(p[2 * j], carry[j], p[2 * j + 1]);
+    for (int j = 0; j < V; ++j) {
+      c.p[j] = 1.0f;
+      c.h[j] = !SUM && s.gstate ? s.gstate[col + j] : 0.0f;
+    }
+    if constexpr (!SUM)
+      for (int k = s.chunks - 1; k > at.chunk; --k) {
+        const float* p = s.sums + ((int64_t)(k - 1) * s.B * s.D + col) * 2;
+#pragma unroll
+        for (int j = 0; j < V; ++j) c.h[j] = fmaf(p[2 * j], c.h[j], p[2 * j + 1]);
+      }
+    meet.carry[0][at.lane] = c;
   }
   int turn = 0;
-  const int windows = (t1 - t0 + window - 1) / window;
-  for (int w = windows - 1; w >= 0; --w) {
-    const int t = t0 + w * window;
-    const int first = t + (2 * at.wave + at.upper) * kGateStep;
-    const Rows<E> gx(s.gx, first, at.b, at.c), gf(s.gf, first, at.b, at.c),
-        gi(s.gi, first, at.b, at.c), gz(s.gz, first, at.b, at.c);
-    if (t >= at.len) {
-      const float none[V] = {};
-      for (int k = 0; k < kGateStep && first + k < t1; ++k) {
-        gate_store<E, V>(gx.at(k), none, at.live, at.own);
-        gate_store<E, V>(gf.at(k), none, at.live, at.own);
-        if constexpr (I) gate_store<E, V>(gi.at(k), none, at.live, at.own);
-        if constexpr (Z) gate_store<E, V>(gz.at(k), none, at.live, at.own);
-      }
-      continue;
-    }
-    const int n = at.len - first;
-    GateTile<E, V> x, f, i, z, go;
-    x.load(s.x, first, at.b, at.c, n);
-    f.load(s.f, first, at.b, at.c, n);
-    if constexpr (I) i.load(s.i, first, at.b, at.c, n);
-    if constexpr (Z) z.load(s.z, first, at.b, at.c, n);
-    go.load(s.go, first, at.b, at.c, n);
-    float h[V] = {};
-    if (n > 0) {
-      const float* p = s.saved + ((int64_t)(first / kGateStep) * s.B * s.D + col);
+  // WHOLE: every slot's steps hold text.  NEXT: another window
+  // follows (full of text), and is on its way while this one is worked on.
+  auto work = [&](auto whole, auto next) {
+    constexpr bool WHOLE = decltype(whole)::value;
+    x = nx, f = nf, i = ni, z = nz, go = ngo;
+    float h[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) h[j] = p[j];
-    }
-    Decay a[kGateStep][V];
-    float before[kGateStep][V], y[kGateStep][V], dz[kGateStep][V];
+    for (int j = 0; j < V; ++j) h[j] = nbefore[j];
+    if constexpr (decltype(next)::value) fetch(std::true_type(), t - window);
+    const int n = steps - t - slot;  // the slot's steps that hold text
+    Gate a[kGateStep][V], in[kGateStep][V];
+    float before[kGateStep][V], y[kGateStep][V], c[V];
     GatePair<V> mine;
+    GateRows<E> gz(s.gz, t, at.b, at.c0);
+    const uint32_t own = (uint32_t)at.cl * (uint32_t)sizeof(E);
+    const uint32_t oz = gate_offset((uint32_t)slot * gz.step + own);
 #pragma unroll
-    for (int k = 0; k < kGateStep; ++k)
+    for (int k = 0; k < kGateStep; ++k, gz.next()) {
+      float vz[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const Forget g = forget_hw((float)f.v[k].v[j] + fb[j]);
-        float take = g.q;
-        if constexpr (I) take = sigmoid_hw((float)i.v[k].v[j] + ib[j]);
-        a[k][j] = k < n ? g.decay : Decay{kKeep};
-        before[k][j] = h[j];
-        h[j] = a[k][j].times(h[j], k < n ? take * (float)x.v[k].v[j] : 0.0f);
-        y[k][j] = k < n ? (float)go.v[k].v[j] : 0.0f;
-        if constexpr (Z) {
-          const Silu v = silu_hw((float)z.v[k].v[j]);
-          dz[k][j] = k < n ? y[k][j] * h[j] * v.slope : 0.0f;
-          y[k][j] = k < n ? y[k][j] * v.value : 0.0f;
+        Gate g = gate_hw(fb[j] - f.get(k, j));
+        if (!WHOLE && k >= n) g = kGateKeep;
+        a[k][j] = g;
+        if constexpr (!SUM) {
+          float take = g.rest();
+          if constexpr (I) {
+            in[k][j] = gate_hw(ib[j] - i.get(k, j));
+            take = in[k][j].value();
+          }
+          take *= x.get(k, j);
+          if (!WHOLE && k >= n) take = 0.0f;
+          before[k][j] = h[j];
+          h[j] = g.times(h[j], take);
         }
+        float v = go.get(k, j);
+        if constexpr (Z) {
+          const Silu gate = silu_hw(z.get(k, j));
+          if constexpr (!SUM) vz[j] = !WHOLE && k >= n ? 0.0f : v * h[j] * gate.slope;
+          v *= gate.value;
+        }
+        y[k][j] = !WHOLE && k >= n ? 0.0f : v;
       }
+      if constexpr (Z && !SUM)
+        if (WHOLE || t + slot + k < t1) pack_store<true, E, V>(gz.at(oz), vz, V);
+    }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       mine.p[j] = 1.0f;
@@ -105,52 +146,74 @@ __global__ __launch_bounds__(64 * kGateBwdWaves) void gate_bwd(const GateArgs<E>
         mine.p[j] = a[k][j].times(mine.p[j], 0.0f);
       }
     }
-    float c[V];
-    gate_fold<true, V>(lds[turn], at, mine, carry, c);
-    turn ^= 1;
+    gate_fold<true>(meet, turn, at, mine, c);
+    if constexpr (SUM) return;
+    const GateRows<E> gx(s.gx, t, at.b, at.c0), gf(s.gf, t, at.b, at.c0), gi(s.gi, t, at.b, at.c0);
+    const uint32_t ox = gate_offset((uint32_t)slot * gx.step + own),
+                   of = gate_offset((uint32_t)slot * gf.step + own),
+                   oi = I ? gate_offset((uint32_t)slot * gi.step + own) : 0;
 #pragma unroll
     for (int k = kGateStep - 1; k >= 0; --k) {
-      float vx[V], vf[V], vi[V], vz[V];
+      float vx[V], vf[V], vi[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float gh = y[k][j] + c[j], xv = (float)x.v[k].v[j];
-        const Forget g = forget_hw((float)f.v[k].v[j] + fb[j]);
-        const bool runs = k < n;
-        float take = g.q, from = before[k][j];
+        const float gh = y[k][j] + c[j], xv = x.get(k, j);
+        const bool runs = WHOLE || k < n;
+        float take, from = before[k][j];
         if constexpr (I) {
-          const float v = (float)i.v[k].v[j] + ib[j];
-          const Gate in = gate_hw(v);
-          take = v >= 0.0f ? in.big : in.small;
-          vi[j] = runs ? gh * xv * (in.big * in.small) : 0.0f;
+          take = in[k][j].value();
+          vi[j] = runs ? gh * xv * in[k][j].slope() : 0.0f;
           sum_i[j] += vi[j];
         } else {
+          take = a[k][j].rest();
           from -= xv;
         }
         vx[j] = runs ? take * gh : 0.0f;
-        vf[j] = runs ? gh * from * (g.a * g.q) : 0.0f;
+        vf[j] = runs ? gh * from * a[k][j].slope() : 0.0f;
         sum_f[j] += vf[j];
-        if constexpr (Z) vz[j] = dz[k][j];
         c[j] = a[k][j].times(gh, 0.0f);
       }
-      if (first + k < t1) {
-        gate_store<E, V>(gx.at(k), vx, at.live, at.own);
-        gate_store<E, V>(gf.at(k), vf, at.live, at.own);
-        if constexpr (I) gate_store<E, V>(gi.at(k), vi, at.live, at.own);
-        if constexpr (Z) gate_store<E, V>(gz.at(k), vz, at.live, at.own);
+      if (WHOLE || t + slot + k < t1) {
+        const auto row = [&](const GateRows<E>& r, uint32_t o) {
+          return reinterpret_cast<E*>((r.base + (uint64_t)k * r.step) + o);
+        };
+        pack_store<true, E, V>(row(gx, ox), vx, V);
+        pack_store<true, E, V>(row(gf, of), vf, V);
+        if constexpr (I) pack_store<true, E, V>(row(gi, oi), vi, V);
       }
     }
+  };
+  constexpr std::true_type yes;
+  constexpr std::false_type no;
+  // (only the first window, the row's last, can be short of text)
+  if (t > t0 && t + window > steps) {
+    work(no, yes);
+    t -= window;
+    turn ^= 1;
   }
-  if (s.gstate0 && at.chunk == 0 && threadIdx.x < kGateLanes)
-    gate_store<float, V>(s.gstate0 + col, carry, at.live, at.own);
+  for (; t > t0; t -= window, turn ^= 1) work(yes, yes);
+  if (t == t0) {
+    if (t + window <= steps) work(yes, no);
+    else work(no, no);
+    turn ^= 1;
+  }
+  if constexpr (!SUM)
+    if (s.part) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        bias[slot / kGateStep][j][at.lane] = sum_f[j];
+        bias[slot / kGateStep][V + j][at.lane] = sum_i[j];
+      }
+    }
+  __syncthreads();
+  if (threadIdx.x < kGateLanes) {
+    const GatePair<V> c = meet.carry[turn][at.lane];
+    if constexpr (SUM) gate_sum_store<V>(s, at, c);
+    else if (s.gstate0 && at.chunk == 0) pack_store<true, float, V>(s.gstate0 + col, c.h, V);
+  }
+  if constexpr (SUM) return;
   if (!s.part) return;
   // the slots' sums, one channel and gate a thread
-  const int slot = 2 * at.wave + at.upper;
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    bias[slot][j][at.lane] = sum_f[j];
-    bias[slot][V + j][at.lane] = sum_i[j];
-  }
-  __syncthreads();
   float* part = s.part + ((int64_t)at.chunk * s.B + at.b) * 2 * s.D;
   for (int o = threadIdx.x; o < 2 * V * kGateLanes; o += blockDim.x) {
     const int lane = o % kGateLanes, j = o / kGateLanes % V, gate = o / kGateLanes / V;
@@ -160,59 +223,6 @@ __global__ __launch_bounds__(64 * kGateBwdWaves) void gate_bwd(const GateArgs<E>
     const int64_t want = ((int64_t)at.group * kGateLanes + lane) * V;
     const int64_t ch = min(want, (int64_t)s.D - V) + j;
     if (want < s.D && ch >= want) part[(int64_t)gate * s.D + ch] = sum;
-  }
-}
-
-// The pairs (product of a, adjoint) of all chunks but the first.
-template <typename E, int V, bool Z>
-__global__ __launch_bounds__(64 * kGateBwdWaves) void gate_bsum(const GateArgs<E> s) {
-  __shared__ GatePair<V> lds[kGateBwdWaves][kGateLanes];
-  GateSpot<V> at;
-  if (!at.at(s, seq_block(), s.chunks - 1)) return;
-  const int run = s.chunk / (2 * at.waves);  // a multiple of a tile's steps
-  const int t0 = (at.chunk + 1) * s.chunk + (2 * at.wave + at.upper) * run;
-  float fb[V];
-  GatePair<V> all;
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    fb[j] = s.f_bias ? s.f_bias[at.c + j] : 0.0f;
-    all.p[j] = 1.0f;
-    all.h[j] = 0.0f;
-  }
-  for (int t = t0 + run - kGateStep; t >= t0; t -= kGateStep) {
-    const int n = at.len - t;
-    if (n <= 0) continue;
-    GateTile<E, V> f, z, go;
-    f.load(s.f, t, at.b, at.c, n);
-    if constexpr (Z) z.load(s.z, t, at.b, at.c, n);
-    go.load(s.go, t, at.b, at.c, n);
-#pragma unroll
-    for (int k = kGateStep - 1; k >= 0; --k)
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        Decay a = forget_hw((float)f.v[k].v[j] + fb[j]).decay;
-        float y = (float)go.v[k].v[j];
-        if constexpr (Z) y *= silu_hw((float)z.v[k].v[j]).value;
-        if (k >= n) a = Decay{kKeep}, y = 0.0f;
-        all.h[j] = a.times(all.h[j] + y, 0.0f);
-        all.p[j] = a.times(all.p[j], 0.0f);
-      }
-  }
-  float h[V] = {}, in[V], p[V];
-  gate_fold<true, V>(lds, at, all, h, in);
-#pragma unroll
-  for (int j = 0; j < V; ++j) p[j] = 1.0f;
-  for (int w = 0; w < at.waves; ++w)
-#pragma unroll
-    for (int j = 0; j < V; ++j) p[j] *= lds[w][at.lane].p[j];
-  if (threadIdx.x < kGateLanes && at.live) {
-    float* to = s.sums + ((int64_t)at.chunk * s.B * s.D + (int64_t)at.b * s.D + at.c) * 2;
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (j >= at.own) {
-        to[2 * j] = p[j];
-        to[2 * j + 1] = h[j];
-      }
   }
 }
 
@@ -242,14 +252,14 @@ ck_status gate_launch(const GateArgs<E>& a, const GatePlan& p, float* g_f, float
   const int64_t cols = (int64_t)p.groups * a.B;
   if (p.chunks > 1) {
     const dim3 grid = seq_grid(cols * (p.chunks - 1));
-    if (a.z.p) gate_bsum<E, V, true><<<grid, threads, 0, stream>>>(a);
-    else gate_bsum<E, V, false><<<grid, threads, 0, stream>>>(a);
+    if (a.z.p) gate_bwd<E, V, false, true, true><<<grid, threads, 0, stream>>>(a);
+    else gate_bwd<E, V, false, false, true><<<grid, threads, 0, stream>>>(a);
   }
   const dim3 grid = seq_grid(cols * p.chunks);
-  if (a.i.p && a.z.p) gate_bwd<E, V, true, true><<<grid, threads, 0, stream>>>(a);
-  else if (a.i.p) gate_bwd<E, V, true, false><<<grid, threads, 0, stream>>>(a);
-  else if (a.z.p) gate_bwd<E, V, false, true><<<grid, threads, 0, stream>>>(a);
-  else gate_bwd<E, V, false, false><<<grid, threads, 0, stream>>>(a);
+  if (a.i.p && a.z.p) gate_bwd<E, V, true, true, false><<<grid, threads, 0, stream>>>(a);
+  else if (a.i.p) gate_bwd<E, V, true, false, false><<<grid, threads, 0, stream>>>(a);
+  else if (a.z.p) gate_bwd<E, V, false, true, false><<<grid, threads, 0, stream>>>(a);
+  else gate_bwd<E, V, false, false, false><<<grid, threads, 0, stream>>>(a);
   if (a.part)
     gate_bias_sum<<<seq_grid((2 * (int64_t)a.D + kBiasCols - 1) / kBiasCols), kBiasCols * kBiasRows,
                     0, stream>>>(a.part, a.D, (int64_t)a.B * p.chunks, g_f, g_i);

@@ -316,22 +316,29 @@ def test_same_bits_every_time_and_on_another_stream():
             assert torch.equal(a, b)
 
 
-def test_long_strides_and_offsets_past_32_bits():
-    """Steps 2^28 elements apart, a row's last step past 2^32 bytes."""
-    T, D = 12, 40
+@pytest.mark.parametrize("T,stride", [(40, (1 << 26) - 1), (1000, (1 << 21) + 3)])
+def test_long_strides_and_offsets_past_32_bits(T, stride):
+    """The longest strides, and such as leave a window fewer waves; rows that end past
+    2^32 bytes."""
+    D = 40
     if torch.cuda.mem_get_info()[0] < 24 << 30:
         pytest.skip("needs 24 GB")
-    far = torch.empty((T - 1) * (1 << 28) + 2 * D, dtype=torch.float32, device="cuda")
-    x = far.as_strided((T, 2, D), (1 << 28, D, 1))
-    g, p = problem(16, T, 2, D, "fp32", True, False, None, "time")
-    x.copy_(g["x"])
+    far = torch.empty((T - 1) * stride + 2 * D, dtype=torch.float32, device="cuda")
+    x = far.as_strided((T, 2, D), (stride, D, 1))
+    g, p = problem(16, T, 2, D, "fp32", True, True, [T, T - 3], "time")
     near = run(g)
-    got = run(dict(g, x=x))
-    for a, b in zip((*near[:2], *near[2].values()), (*got[:2], *got[2].values())):
-        assert torch.equal(a, b)
-    sgr.gated_scan_forward(g["x"], g["f"], i=g["i"], f_bias=g["f_bias"], i_bias=g["i_bias"],
-                           state0=g["state0"], out=x)
-    assert torch.equal(x, near[0])
+    for k in ("x", "f", "i", "z", "go"):
+        x.copy_(g[k])
+        check(g, p, run(dict(g, **{k: x})))
+    kw = dict(i=g["i"], z=g["z"], f_bias=g["f_bias"], i_bias=g["i_bias"], lengths=g["lengths"])
+    _, _, saved, _ = sgr.gated_scan_forward(g["x"], g["f"], state0=g["state0"], out=x, **kw)
+    close(x, ref.gated(p)["out"], "out")
+    for k in ("g_x", "g_f", "g_i", "g_z"):
+        grads = {n: torch.empty_like(g["x"]) for n in ("g_x", "g_f", "g_i", "g_z")}
+        grads[k] = x
+        sgr.gated_scan_backward(g["x"], g["f"], saved, g["go"], grad_state=g["gstate"],
+                                grads=grads, **kw)
+        close(x, ref.gated(p)[k], k)
     check(g, p, near)
 
 

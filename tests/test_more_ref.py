@@ -127,7 +127,7 @@ def test_gated_call_refusals(L):
     assert fwd(i=_inputs(f=NONE)) == NULL_ARG
     assert fwd(i=_inputs(i=CkSeq(FAKE + 1, 128, 64))) == BAD_VALUE
     assert fwd(i=_inputs(z=CkSeq(FAKE, -128, 64))) == BAD_VALUE
-    assert fwd(i=_inputs(x=CkSeq(FAKE, 2**30, 64))) == BAD_VALUE
+    assert fwd(i=_inputs(x=CkSeq(FAKE, 2**26, 64))) == BAD_VALUE
     assert fwd(i=_inputs(f_bias=FAKE + 2)) == BAD_VALUE
     assert fwd(i=_inputs(i_bias=FAKE + 2)) == BAD_VALUE
     assert fwd(i=_inputs(state0=FAKE + 1)) == BAD_VALUE
@@ -153,6 +153,7 @@ def test_gated_call_refusals(L):
     assert back(ws=FAKE + 16) == BAD_VALUE
     # inputs may be broadcast (the next refusal is the workspace's)
     assert back(i=_inputs(x=CkSeq(FAKE, 0, 0)), go=CkSeq(FAKE, 0, 64), n=16) == WORKSPACE
+    assert back(i=_inputs(x=CkSeq(FAKE, 2**26 - 1, 2**40)), n=16) == WORKSPACE
     one = _shape(T=1)
     assert L.ck_gated_step(s, _inputs(), SEQ, FAKE, None) == BAD_SIZE
     assert L.ck_gated_step(one, None, SEQ, FAKE, None) == NULL_ARG
