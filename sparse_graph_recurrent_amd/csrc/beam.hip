@@ -51,23 +51,41 @@ __device__ __forceinline__ int lanes_below(uint64_t mask) {
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
                                    __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
 }
+// Lane i takes what a lane before it has (CTRL: a DPP control; ROWS: which rows of 16
+// lanes do), or `none` where there is no such lane.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ uint32_t lane_before(uint32_t x, uint32_t none) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)x, CTRL, ROWS, 0xF, false);
+}
+// fn over all lanes, by the vector ALU alone (an exchange through LDS takes longer than
+// all six steps here): rows of 16 lanes, then rows to rows; lane 63 has it all.
+template <typename F>
+__device__ __forceinline__ uint32_t wave_all(uint32_t x, uint32_t none, F&& fn) {
+  x = fn(x, lane_before<0x111>(x, none));
+  x = fn(x, lane_before<0x112>(x, none));
+  x = fn(x, lane_before<0x114>(x, none));
+  x = fn(x, lane_before<0x118>(x, none));
+  x = fn(x, lane_before<0x142, 0xA>(x, none));
+  x = fn(x, lane_before<0x143, 0xC>(x, none));
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+__device__ __forceinline__ uint32_t bits(float x) { return __builtin_bit_cast(uint32_t, x); }
+__device__ __forceinline__ float value(uint32_t x) { return __builtin_bit_cast(float, x); }
 __device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) x = fmaxf(x, __shfl_xor(x, m));
-  return x;
+  return value(wave_all(bits(x), bits(-__builtin_inff()), [](uint32_t a, uint32_t b) {
+    return bits(fmaxf(value(a), value(b)));
+  }));
 }
 __device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) x += __shfl_xor(x, m);
-  return x;
+  return value(wave_all(bits(x), 0u,
+                        [](uint32_t a, uint32_t b) { return bits(value(a) + value(b)); }));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  return wave_all(x, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
 __device__ __forceinline__ uint64_t wave_max(uint64_t x) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) {
-    const uint64_t o = __shfl_xor((unsigned long long)x, m);
-    x = o > x ? o : x;
-  }
-  return x;
+  const uint32_t high = wave_max((uint32_t)(x >> 32));
+  return (uint64_t)high << 32 | wave_max((uint32_t)(x >> 32) == high ? (uint32_t)x : 0u);
 }
 
 template <typename E>
@@ -92,9 +110,20 @@ __device__ __forceinline__ bool beam_skips(const BeamArgs<E>& s, int64_t row) {
   return (s.finished && s.finished[row]) || !(score > -__builtin_inff());
 }
 
+// What a wave keeps in LDS, for K beams.
+struct BeamLds {
+  int packs;       // lanes' accesses with a logit at the limit or above
+  int above;       // keys above it
+  size_t bytes;
+  __host__ __device__ explicit BeamLds(int K)
+      : packs((K - 1) * kBeamPacks + K), above((K - 1) * kBeamPacks * kBeamV),
+        bytes((size_t)(above + K) * sizeof(uint64_t) +
+              (size_t)((packs * (kBeamV + 1) + 3) & ~3) * sizeof(float)) {}
+};
+
 template <typename E>
 __global__ __launch_bounds__(64 * kBeamWaves) void beam_part(const BeamArgs<E> s, int64_t waves) {
-  extern __shared__ uint64_t beam_lds[];
+  extern __shared__ __attribute__((aligned(16))) char beam_lds[];
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   const int64_t id = seq_block() * (blockDim.x >> 6) + wave;
@@ -103,25 +132,28 @@ __global__ __launch_bounds__(64 * kBeamWaves) void beam_part(const BeamArgs<E> s
   const int part = (int)(id % s.parts);
   if (beam_skips(s, row)) return;
   const int K = s.K;
-  // Above the limit lie at most K - 1 lanes' logits; at it, K count.
-  const int room = (K - 1) * kBeamV * kBeamPacks;
-  uint64_t* above = beam_lds + (int64_t)wave * (room + K);
-  uint64_t* level = above + room;
+  const BeamLds room(K);
+  char* lds = beam_lds + wave * room.bytes;
+  float* hits = reinterpret_cast<float*>(lds);                       // [packs][kBeamV]
+  uint64_t* above = reinterpret_cast<uint64_t*>(hits + room.packs * kBeamV);
+  uint64_t* level = above + room.above;
+  int* places = reinterpret_cast<int*>(level + K);                   // [packs]
 
   const E* p = s.x.row(row / K, row % K);
   const int64_t base = (int64_t)part * kBeamSpan;
+  const int there = (int)min((int64_t)kBeamSpan, s.V - base);  // logits of this part
   float x[kBeamPacks][kBeamV];
 #pragma unroll
   for (int j = 0; j < kBeamPacks; ++j) {
-    const int64_t v = base + j * 64 * kBeamV + lane * kBeamV;
+    const int v = j * 64 * kBeamV + lane * kBeamV;
     Pack<E, kBeamV> w;
-    if (v + kBeamV <= s.V) {
-      w = pack_load<true, E, kBeamV>(p + v, kBeamV);
+    if (v + kBeamV <= there) {
+      w = pack_load<true, E, kBeamV>(p + base + v, kBeamV);
     } else {
 #pragma unroll
       for (int k = 0; k < kBeamV; ++k) {
         w.v[k] = (E)-__builtin_inff();
-        if (v + k < s.V) w.v[k] = p[v + k];
+        if (v + k < there) w.v[k] = p[base + v + k];
       }
     }
 #pragma unroll
@@ -147,10 +179,10 @@ __global__ __launch_bounds__(64 * kBeamWaves) void beam_part(const BeamArgs<E> s
     sum = wave_sum(sum);
   };
   look(-__builtin_inff());
-  if (!(sum < __builtin_inff())) {
-    // A NaN, +inf, or no logit above -inf makes the sum a NaN.  (None of the others
-    // does: each term is at most 1.)  A NaN counts as -inf, +inf as the largest
-    // finite value.
+  // A NaN, +inf, or no logit above -inf makes the sum a NaN.  (None of the others does:
+  // each term is at most 1.)  A NaN counts as -inf, +inf as the largest finite value.
+  const bool odd = !(sum < __builtin_inff());
+  if (odd) {
 #pragma unroll
     for (int j = 0; j < kBeamPacks; ++j)
 #pragma unroll
@@ -160,48 +192,63 @@ __global__ __launch_bounds__(64 * kBeamWaves) void beam_part(const BeamArgs<E> s
   }
   if (lane == 0) s.sums[row * s.parts + part] = make_float2(most, sum);
 
-  // The K-th largest of the lanes' maxima (a lane without logits: the lowest).
-  const int64_t there = s.V - base;  // logits from here on
+  // The K-th largest of the lanes' maxima (a lane without logits: the lowest), bit by
+  // bit.  16-bit logits as fp32 have the lowest bits 0, or, ordered, of negative ones 1.
+  constexpr int kFree = std::is_same_v<E, float> ? 0 : std::is_same_v<E, bf16_t> ? 16 : 13;
   const uint32_t mine = lane * kBeamV < there ? beam_order(best) : 0;
+  const int lowest = odd ? 0 : kFree;
   uint32_t limit = 0;
 #pragma unroll 1
-  for (int bit = 31; bit >= 0; --bit) {
+  for (int bit = 31; bit >= lowest; --bit) {
     const uint32_t more = limit | 1u << bit;
     if (__popcll(__ballot(mine >= more)) >= K) limit = more;
   }
   // Fewer than K lanes with logits: every logit counts.
   const bool every = limit == 0;
+  if (!(limit >> 31)) limit |= (1u << lowest) - 1;
   const float border = every ? -__builtin_inff() : beam_value(limit);
-  int n = 0, at_border = 0;
+  // The accesses with a logit above the limit, and the first K of those with one at it
+  // (in which every logit that can count lies), in the order of the vocabulary.
+  int packs = 0, ties = 0;
 #pragma unroll
   for (int j = 0; j < kBeamPacks; ++j) {
-    const int64_t first = j * 64 * kBeamV + lane * kBeamV;
-    const bool some = first < there && top[j] >= border;
-    if (!__ballot(some)) continue;
-    uint64_t hit[kBeamV];
+    const int first = j * 64 * kBeamV + lane * kBeamV;
+    const bool over = top[j] > border, at = top[j] == border && first < there;
+    const uint64_t at_mask = __ballot(at);
+    if (!(at_mask | __ballot(over))) continue;
+    const bool take = over || (at && ties + lanes_below(at_mask) < K);
+    const uint64_t mask = __ballot(take);
+    if (take) {
+      const int o = packs + lanes_below(mask);
+      places[o] = first;
 #pragma unroll
-    for (int k = 0; k < kBeamV; ++k) {
-      const bool over = first + k < there && x[j][k] > border;
-      const uint64_t mask = __ballot(over);
-      if (over) above[n + lanes_below(mask)] = beam_key(x[j][k], (uint32_t)(base + first + k));
-      n += __popcll(mask);
-      hit[k] = __ballot(first + k < there && x[j][k] == border);
+      for (int k = 0; k < kBeamV; k += 4)
+        *reinterpret_cast<float4*>(hits + o * kBeamV + k) =
+            make_float4(x[j][k], x[j][k + 1], x[j][k + 2], x[j][k + 3]);
     }
-    int before = at_border;  // of the pack's logits at the border, lanes below and own ones before
-#pragma unroll
-    for (int k = 0; k < kBeamV; ++k) before += lanes_below(hit[k]);
-#pragma unroll
-    for (int k = 0; k < kBeamV; ++k) {
-      at_border += __popcll(hit[k]);
-      if (hit[k] >> lane & 1) {
-        if (before < K) level[before] = beam_key(x[j][k], (uint32_t)(base + first + k));
-        ++before;
-      }
-    }
+    packs += __popcll(mask);
+    ties += __popcll(at_mask);
   }
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  auto settle = [] {  // a wave's own writes to LDS, before its reads by other lanes
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  };
+  settle();
+  int n = 0, at_border = 0;
+  for (int e = lane; e - lane < packs * kBeamV; e += 64) {
+    const bool is = e < packs * kBeamV;
+    const float v = is ? hits[e] : 0.0f;
+    const int place = is ? places[e / kBeamV] + e % kBeamV : there;
+    const bool over = place < there && v > border, at = place < there && v == border;
+    const uint64_t over_mask = __ballot(over), at_mask = __ballot(at);
+    const uint64_t key = beam_key(v, (uint32_t)(base + place));
+    if (over) above[n + lanes_below(over_mask)] = key;
+    if (at && at_border + lanes_below(at_mask) < K) level[at_border + lanes_below(at_mask)] = key;
+    n += __popcll(over_mask);
+    at_border += __popcll(at_mask);
+  }
+  settle();
   uint64_t* out = s.best + (row * s.parts + part) * K;
   for (int i = lane; i < n; i += 64) {
     const uint64_t key = above[i];
@@ -214,7 +261,7 @@ __global__ __launch_bounds__(64 * kBeamWaves) void beam_part(const BeamArgs<E> s
 
 // Takes the K best of `n` keys, no two alike but 0, in order: of the lane's, K times
 // the best of the wave.  Written to list[0 .. K).
-constexpr int kBeamHold = 8;  // keys a lane holds at a time
+template <int kBeamHold>  // keys a lane holds at a time
 __device__ __forceinline__ void beam_take(const uint64_t* keys, int64_t n, int K, int lane,
                                           uint64_t* list) {
   uint64_t kept = 0;  // lane i: the i-th best so far
@@ -280,7 +327,11 @@ __global__ __launch_bounds__(64 * kBeamJoinWaves) void beam_join(const BeamArgs<
       tops[k] = (double)most;
       logs[k] = sum > 0.0 ? log(sum) : 0.0;
     }
-    beam_take(s.best + row * s.parts * K, (int64_t)s.parts * K, K, lane, list[k]);
+    const int64_t keys = (int64_t)s.parts * K;
+    const uint64_t* best = s.best + row * keys;
+    if (keys <= 64) beam_take<1>(best, keys, K, lane, list[k]);
+    else if (keys <= 128) beam_take<2>(best, keys, K, lane, list[k]);
+    else beam_take<8>(best, keys, K, lane, list[k]);
   }
   __syncthreads();
   if (wave != 0) return;
@@ -323,63 +374,70 @@ struct MoveState {
   char* out;
   int64_t in_row, in_seg, out_row, out_seg;  // bytes
   int64_t bytes;                             // adjacent ones of a segment
-  int64_t packs;                             // of a segment
-  int64_t items;                             // packs of a row
   int64_t first;                             // first workgroup
   int64_t blocks;                            // workgroups a text
+  uint32_t packs, segs;                      // of a segment; of a row
 };
 struct MoveTable {
   MoveState s[kMoveTable];
   const int64_t* parents;
   int64_t first;  // one behind the last workgroup
-  int count, K, B;
+  int count, B;
 };
 
-template <int N>
-struct __attribute__((packed, aligned(1))) Bytes {
-  uint8_t v[N];
+// N bytes at any address as one access.
+template <int N> struct MoveBytes;
+template <> struct MoveBytes<16> {
+  typedef uint32_t type __attribute__((ext_vector_type(4), aligned(1)));
 };
+template <> struct MoveBytes<8> {
+  typedef uint32_t type __attribute__((ext_vector_type(2), aligned(1)));
+};
+template <> struct MoveBytes<4> { typedef uint32_t type __attribute__((aligned(1))); };
+template <> struct MoveBytes<2> { typedef uint16_t type __attribute__((aligned(1))); };
+template <> struct MoveBytes<1> { typedef uint8_t type; };
 
 // One pack of all of a text's rows: every row is read before any is written, so that
-// a state may be reordered in place.
-template <int N, int KM>
-__device__ __forceinline__ void move_pack(const MoveState& s, const int64_t* parents, int K,
-                                          const char* in, char* out) {
-  Bytes<N> v[KM];
+// a state may be reordered in place.  parent: lane k's is row k's.
+template <int N, int K>
+__device__ __forceinline__ void move_pack(const MoveState& s, int parent, const char* in,
+                                          char* out) {
+  using T = typename MoveBytes<N>::type;
+  T v[K];
 #pragma unroll
-  for (int k = 0; k < KM; ++k)
-    if (k < K) {
-      const int64_t from = min(max(parents[k], (int64_t)0), (int64_t)K - 1);
-      v[k] = *reinterpret_cast<const Bytes<N>*>(in + from * s.in_row);
-    }
+  for (int k = 0; k < K; ++k)
+    v[k] = *reinterpret_cast<const T*>(in + __builtin_amdgcn_readlane(parent, k) * s.in_row);
 #pragma unroll
-  for (int k = 0; k < KM; ++k)
-    if (k < K) *reinterpret_cast<Bytes<N>*>(out + k * s.out_row) = v[k];
+  for (int k = 0; k < K; ++k) *reinterpret_cast<T*>(out + k * s.out_row) = v[k];
 }
 
-template <int N, int KM>
+// K beams a text: known to the compiler, so that the rows of a pack stay in registers.
+template <int N, int K>
 __global__ __launch_bounds__(kMoveThreads) void move_rows(const MoveTable t) {
   const int64_t block = seq_block();
   if (block >= t.first) return;
   int i = 0;
   while (i + 1 < t.count && t.s[i + 1].first <= block) ++i;
   const MoveState& s = t.s[i];
-  const int64_t text = (block - s.first) / s.blocks;
-  const int64_t item = (block - s.first) % s.blocks * kMoveThreads + threadIdx.x;
-  if (item >= s.items) return;
-  const int64_t seg = item / s.packs, at = item % s.packs * N;
-  const int64_t* parents = t.parents + text * t.K;
-  const char* in = s.in + text * t.K * s.in_row + seg * s.in_seg + at;
-  char* out = s.out + text * t.K * s.out_row + seg * s.out_seg + at;
+  // (both fit 32 bits: workgroups of a state, and packs of a row)
+  const uint32_t of = (uint32_t)(block - s.first), blocks = (uint32_t)s.blocks;
+  const uint32_t text = of / blocks, item = of % blocks * kMoveThreads + threadIdx.x;
+  const int lane = threadIdx.x & 63;
+  int parent = 0;
+  if (lane < K)
+    parent = (int)min(max(t.parents[(int64_t)text * K + lane], (int64_t)0), (int64_t)K - 1);
+  const uint32_t seg = item / s.packs;
+  const int64_t at = (int64_t)(item - seg * s.packs) * N;
+  if (seg >= s.segs) return;
+  const char* in = s.in + (int64_t)text * K * s.in_row + (int64_t)seg * s.in_seg + at;
+  char* out = s.out + (int64_t)text * K * s.out_row + (int64_t)seg * s.out_seg + at;
   const int left = (int)min(s.bytes - at, (int64_t)N);
-  if (left == N) return move_pack<N, KM>(s, parents, t.K, in, out);
-  int o = 0;
-  if constexpr (N > 8)
-    if (left & 8) move_pack<8, KM>(s, parents, t.K, in, out), o = 8;
-  if constexpr (N > 4)
-    if (left & 4) move_pack<4, KM>(s, parents, t.K, in + o, out + o), o += 4;
-  if (left & 2) move_pack<2, KM>(s, parents, t.K, in + o, out + o), o += 2;
-  if (left & 1) move_pack<1, KM>(s, parents, t.K, in + o, out + o);
+  if (left == N) return move_pack<N, K>(s, parent, in, out);
+  int o = 0;  // a row's last bytes
+#pragma unroll 1
+  for (; o + 4 <= left; o += 4) move_pack<4, K>(s, parent, in + o, out + o);
+#pragma unroll 1
+  for (; o < left; ++o) move_pack<1, K>(s, parent, in + o, out + o);
 }
 
 ck_status beam_check_shape(const ck_beam_shape* s) {
@@ -443,18 +501,24 @@ bool move_overlaps(int64_t rows, int64_t row, int64_t segs, int64_t seg, int64_t
   return rows > 1 ? row < bytes : segs > 1 && seg < bytes;
 }
 
-template <int N, int KM>
+template <int K>
 void move_launch(MoveTable& t, hipStream_t stream) {
+  // a thread holds at most 128 bytes: packs of 16, of 8 or of 4 for more rows
+  constexpr int N = K <= 8 ? 16 : K <= 16 ? 8 : 4;
   t.first = 0;
   for (int i = 0; i < t.count; ++i) {
     MoveState& s = t.s[i];
-    s.packs = (s.bytes + N - 1) / N;
-    s.items *= s.packs;
-    s.blocks = (s.items + kMoveThreads - 1) / kMoveThreads;
+    s.packs = (uint32_t)((s.bytes + N - 1) / N);
+    s.blocks = ((int64_t)s.packs * s.segs + kMoveThreads - 1) / kMoveThreads;
     s.first = t.first;
     t.first += s.blocks * t.B;
   }
-  move_rows<N, KM><<<seq_grid(t.first), kMoveThreads, 0, stream>>>(t);
+  move_rows<N, K><<<seq_grid(t.first), kMoveThreads, 0, stream>>>(t);
+}
+template <int K>
+void move_by_beams(int64_t k, MoveTable& t, hipStream_t stream) {
+  if (k == K) return move_launch<K>(t, stream);
+  if constexpr (K > 1) move_by_beams<K - 1>(k, t, stream);
 }
 
 }  // namespace
@@ -509,8 +573,7 @@ extern "C" ck_status ck_beam_select(const ck_beam_shape* shape, ck_seq logits, c
     a.parts = ws.parts;
     const int64_t waves = shape->B * shape->K * ws.parts;
     const int per = shape->K > 16 ? kBeamWaves / 2 : kBeamWaves;  // (32 KB of LDS at most)
-    const size_t lds =
-        (size_t)per * sizeof(uint64_t) * ((shape->K - 1) * kBeamV * kBeamPacks + shape->K);
+    const size_t lds = per * BeamLds((int)shape->K).bytes;
     beam_part<E><<<seq_grid((waves + per - 1) / per), 64 * per, lds, stream>>>(a, waves);
     // (a launch holds fewer than 2^32 threads along its first dimension)
     const int64_t join = shape->B < kSeqGridX / 2 ? kBeamJoinWaves : kBeamWaves;
@@ -541,7 +604,7 @@ extern "C" ck_status ck_beam_reorder(const ck_beam_state* states, int64_t count,
     set_error("parents are not aligned to their element type");
     return CK_ERR_BAD_VALUE;
   }
-  const int64_t most = int64_t(1) << 44;
+  const int64_t most = int64_t(1) << 40;  // bytes of a beam of all texts; of a row 2^32
   for (int64_t i = 0; i < count; ++i) {
     const ck_beam_state& s = states[i];
     if (s.segments < 0 || s.bytes < 0) {
@@ -549,7 +612,7 @@ extern "C" ck_status ck_beam_reorder(const ck_beam_state* states, int64_t count,
       return CK_ERR_BAD_SIZE;
     }
     if (s.segments == 0 || s.bytes == 0) continue;
-    if (s.segments > most / s.bytes || s.segments * s.bytes > most / B) {
+    if (s.segments > (int64_t(1) << 32) / s.bytes || s.segments * s.bytes > most / B) {
       set_error("state %lld is too large", (long long)i);
       return CK_ERR_TOO_LARGE;
     }
@@ -576,7 +639,6 @@ extern "C" ck_status ck_beam_reorder(const ck_beam_state* states, int64_t count,
   }
   MoveTable t = {};
   t.parents = parents;
-  t.K = (int)K;
   t.B = (int)B;
   for (int64_t i = 0; i < count;) {
     t.count = 0;
@@ -591,13 +653,10 @@ extern "C" ck_status ck_beam_reorder(const ck_beam_state* states, int64_t count,
       m.out_row = s.out_row;
       m.out_seg = s.out_segment;
       m.bytes = s.bytes;
-      m.items = s.segments;
+      m.segs = (uint32_t)s.segments;
     }
     if (t.count == 0) break;
-    // as many bytes a thread holds for every width: 8 rows of 16, 16 of 8, 32 of 4
-    if (K <= 8) move_launch<16, 8>(t, stream);
-    else if (K <= 16) move_launch<8, 16>(t, stream);
-    else move_launch<4, 32>(t, stream);
+    move_by_beams<kBeamMaxK>(K, t, stream);
     CK_HIP_TRY(hipGetLastError());
   }
   return CK_OK;
