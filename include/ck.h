@@ -631,7 +631,8 @@ ck_status ck_clip_grad_norm(const ck_clip_tensor* tensors, int64_t count, double
  *   score(k, v) = scores[k] + x[k][v] - log sum_w exp x[k][w]
  *
  * over all beams k and tokens v of a text, best first; of equal scores the lower
- * k V + v is first.  A finished beam has one continuation, the end token, at its own
+ * k V + v is first (of one beam's, the one of the larger logit: where the scores'
+ * rounding makes unlike logits alike, their order stays).  A finished beam has one continuation, the end token, at its own
  * score.  A logit of -inf, and a NaN, is never taken before any other (its score is
  * -inf, as are all of a beam whose own score is -inf or NaN, and of a finished beam
  * but the end token's); +inf counts as the largest finite fp32 value.  Logits of a

@@ -128,8 +128,8 @@ __global__ __launch_bounds__(64 * kBeamWaves) void beam_part(const BeamArgs<E> s
   const int lane = threadIdx.x & 63;
   const int64_t id = seq_block() * (blockDim.x >> 6) + wave;
   if (id >= waves) return;
-  const int64_t row = id / s.parts;
-  const int part = (int)(id % s.parts);
+  const uint32_t row = (uint32_t)id / (uint32_t)s.parts;  // (waves are below 2^31)
+  const int part = (int)((uint32_t)id - row * (uint32_t)s.parts);
   if (beam_skips(s, row)) return;
   const int K = s.K;
   const BeamLds room(K);
@@ -139,7 +139,8 @@ __global__ __launch_bounds__(64 * kBeamWaves) void beam_part(const BeamArgs<E> s
   uint64_t* level = above + room.above;
   int* places = reinterpret_cast<int*>(level + K);                   // [packs]
 
-  const E* p = s.x.row(row / K, row % K);
+  const uint32_t text = row / (uint32_t)K;
+  const E* p = s.x.row(text, row - text * (uint32_t)K);
   const int64_t base = (int64_t)part * kBeamSpan;
   const int there = (int)min((int64_t)kBeamSpan, s.V - base);  // logits of this part
   float x[kBeamPacks][kBeamV];
@@ -160,7 +161,7 @@ __global__ __launch_bounds__(64 * kBeamWaves) void beam_part(const BeamArgs<E> s
     for (int k = 0; k < kBeamV; ++k) x[j][k] = (float)w.v[k];
   }
   float top[kBeamPacks], best, most, sum;
-  auto look = [&](float zero) {  // maxima and the sum
+  auto look = [&](auto careful) {  // maxima and the sum
     best = -__builtin_inff();
 #pragma unroll
     for (int j = 0; j < kBeamPacks; ++j) {
@@ -170,17 +171,22 @@ __global__ __launch_bounds__(64 * kBeamWaves) void beam_part(const BeamArgs<E> s
       best = fmaxf(best, top[j]);
     }
     most = wave_max(best);
-    const float m = most == -__builtin_inff() ? zero : most;
+    constexpr bool CAREFUL = decltype(careful)::value;
+    const float m = CAREFUL && most == -__builtin_inff() ? 0.0f : most, shift = m * kLog2e;
     sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < kBeamPacks; ++j)
 #pragma unroll
-      for (int k = 0; k < kBeamV; ++k) sum += exp2_hw((x[j][k] - m) * kLog2e);
+      for (int k = 0; k < kBeamV; ++k)
+        sum += exp2_hw(CAREFUL ? (x[j][k] - m) * kLog2e : fmaf(x[j][k], kLog2e, -shift));
     sum = wave_sum(sum);
+    // (what `shift` was rounded by is the same in every term)
+    if constexpr (!CAREFUL) sum *= exp2_hw(-fmaf(m, kLog2e, -shift));
   };
-  look(-__builtin_inff());
-  // A NaN, +inf, or no logit above -inf makes the sum a NaN.  (None of the others does:
-  // each term is at most 1.)  A NaN counts as -inf, +inf as the largest finite value.
+  look(std::false_type());
+  // A NaN, +inf, no logit above -inf, or a maximum that times log2(e) is beyond range
+  // makes the sum a NaN or infinite.  (None of the others does: each term is about 1 at
+  // most.)  A NaN counts as -inf, +inf as the largest finite value.
   const bool odd = !(sum < __builtin_inff());
   if (odd) {
 #pragma unroll
@@ -188,9 +194,9 @@ __global__ __launch_bounds__(64 * kBeamWaves) void beam_part(const BeamArgs<E> s
 #pragma unroll
       for (int k = 0; k < kBeamV; ++k)
         x[j][k] = x[j][k] != x[j][k] ? -__builtin_inff() : fminf(x[j][k], FLT_MAX);
-    look(0.0f);
+    look(std::true_type());
   }
-  if (lane == 0) s.sums[row * s.parts + part] = make_float2(most, sum);
+  if (lane == 0) s.sums[(int64_t)row * s.parts + part] = make_float2(most, sum);
 
   // The K-th largest of the lanes' maxima (a lane without logits: the lowest), bit by
   // bit.  16-bit logits as fp32 have the lowest bits 0, or, ordered, of negative ones 1.
@@ -198,11 +204,14 @@ __global__ __launch_bounds__(64 * kBeamWaves) void beam_part(const BeamArgs<E> s
   const uint32_t mine = lane * kBeamV < there ? beam_order(best) : 0;
   const int lowest = odd ? 0 : kFree;
   uint32_t limit = 0;
-#pragma unroll 1
-  for (int bit = 31; bit >= lowest; --bit) {
+  auto decide = [&](int bit) {
     const uint32_t more = limit | 1u << bit;
     if (__popcll(__ballot(mine >= more)) >= K) limit = more;
-  }
+  };
+#pragma unroll
+  for (int bit = 31; bit >= kFree; --bit) decide(bit);
+#pragma unroll 1
+  for (int bit = kFree - 1; bit >= lowest; --bit) decide(bit);
   // Fewer than K lanes with logits: every logit counts.
   const bool every = limit == 0;
   if (!(limit >> 31)) limit |= (1u << lowest) - 1;
@@ -249,7 +258,7 @@ __global__ __launch_bounds__(64 * kBeamWaves) void beam_part(const BeamArgs<E> s
     at_border += __popcll(at_mask);
   }
   settle();
-  uint64_t* out = s.best + (row * s.parts + part) * K;
+  uint64_t* out = s.best + ((int64_t)row * s.parts + part) * K;
   for (int i = lane; i < n; i += 64) {
     const uint64_t key = above[i];
     int rank = 0;
@@ -452,6 +461,11 @@ ck_status beam_check_shape(const ck_beam_shape* s) {
   }
   if (s->V > INT_MAX - 2 * kBeamSpan || s->B > (int64_t(1) << 30) ||
       s->B * s->K > (int64_t(1) << 40) / s->V) {
+    set_error("B=%lld, K=%lld or V=%lld is too large", (long long)s->B, (long long)s->K,
+              (long long)s->V);
+    return CK_ERR_TOO_LARGE;
+  }
+  if (s->B * s->K * ((s->V + kBeamSpan - 1) / kBeamSpan) >= INT_MAX) {
     set_error("B=%lld, K=%lld or V=%lld is too large", (long long)s->B, (long long)s->K,
               (long long)s->V);
     return CK_ERR_TOO_LARGE;

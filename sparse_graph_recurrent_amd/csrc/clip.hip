@@ -22,53 +22,91 @@ namespace {
 
 constexpr int kClipThreads = 256;
 constexpr int kClipTable = 96;      // tensors a launch (the table is its argument: at most 4 KB)
-constexpr int kClipV = 8;           // elements a thread and access
-constexpr int kClipDeep = 4;        // accesses in flight
-constexpr int kClipUnit = kClipThreads * kClipV;  // elements of a chunk, times 1 .. kClipDeep
-constexpr int kClipBlocks = 1024;   // of a launch that sums: as many partial sums
+constexpr int kClipAccess = 16;     // bytes a thread and access
+constexpr int kClipDeep = 8;        // accesses of a thread in a chunk, at most
+constexpr int kClipUnit = kClipThreads * kClipAccess;  // bytes of a chunk of one access a thread
+constexpr int kClipBlocks = 2048;   // of a launch: all run at once (8 waves a SIMD); as many
+                                    // partial sums
 
 struct ClipTable {
   const void* in[kClipTable];
   void* out[kClipTable];
-  int64_t n[kClipTable];
+  int64_t n[kClipTable];          // bytes
   int64_t first[kClipTable + 1];  // first chunk of each tensor
   int8_t dtype[kClipTable];
   int count;
   int units;  // of a chunk
 };
 
-// The tensor that a chunk lies in.
-__device__ __forceinline__ int clip_find(const ClipTable& t, int64_t chunk) {
-  int lo = 0, hi = t.count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (t.first[mid] <= chunk) lo = mid; else hi = mid;
-  }
-  return lo;
-}
+// A thread's share of a chunk: as many accesses as the chunk has units.
+typedef uint32_t ClipWord __attribute__((ext_vector_type(4), aligned(2)));
+struct ClipChunk {
+  ClipWord v[kClipDeep];
 
-// fn(pack, first element, elements there are) for the thread's share of a chunk,
-// all loads before the first call.
-template <typename E, typename F>
-__device__ __forceinline__ void clip_chunk(const void* data, int64_t n, int64_t chunk, int units,
-                                           F&& fn) {
-  const E* p = static_cast<const E*>(data);
-  const int64_t base = chunk * units * kClipUnit;
-  Pack<E, kClipV> v[kClipDeep];
+  // Chunk `chunk` of tensor i.  What lies behind the tensor's end counts as 0.
+  __device__ __forceinline__ void load(const ClipTable& t, int i, int64_t chunk) {
+    const char* p = static_cast<const char*>(t.in[i]);
+    const int64_t n = t.n[i], base = chunk * t.units * kClipUnit;
+    const int thread = threadIdx.x * kClipAccess;
+    if (base + (int64_t)t.units * kClipUnit <= n) {
 #pragma unroll
-  for (int u = 0; u < kClipDeep; ++u) {
-    if (u >= units) continue;
-    const int64_t at = base + u * kClipUnit + (int64_t)threadIdx.x * kClipV;
-    if (at + kClipV <= n) v[u] = pack_load<true, E, kClipV>(p + at, kClipV);
-    else if (at < n) v[u] = pack_load<false, E, kClipV>(p + at, (int)(n - at));
-  }
+      for (int u = 0; u < kClipDeep; ++u)
+        if (u < t.units)
+          v[u] = *reinterpret_cast<const ClipWord*>(p + base + u * kClipUnit + thread);
+    } else {
 #pragma unroll
-  for (int u = 0; u < kClipDeep; ++u) {
-    if (u >= units) continue;
-    const int64_t at = base + u * kClipUnit + (int64_t)threadIdx.x * kClipV;
-    if (at < n) fn(v[u], at, (int)min(n - at, (int64_t)kClipV));
+      for (int u = 0; u < kClipDeep; ++u) {
+        v[u] = ClipWord{};
+        if (u >= t.units) continue;
+        const int64_t at = base + u * kClipUnit + thread;
+        if (at + kClipAccess <= n) {
+          v[u] = *reinterpret_cast<const ClipWord*>(p + at);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kClipAccess / 2; ++k)  // (elements are 2 or 4 bytes)
+            if (at + 2 * k < n)
+              v[u][k / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + at + 2 * k)
+                             << 16 * (k & 1);
+        }
+      }
+    }
   }
+};
+
+// Elements of an access as fp32, and back.
+template <typename E>
+__device__ __forceinline__ float clip_get(const ClipWord& w, int k) {
+  if constexpr (sizeof(E) == 4) return __builtin_bit_cast(float, (uint32_t)w[k]);
+  else return (float)__builtin_bit_cast(E, (uint16_t)(w[k / 2] >> 16 * (k & 1)));
 }
+template <typename E>
+constexpr int kClipElems = kClipAccess / (int)sizeof(E);
+
+// Chunks b, b + G, .. of a table, in turn (BACK: from the last).
+template <bool BACK>
+struct ClipWalk {
+  const ClipTable& t;
+  int64_t chunks, k;
+  int i;
+  __device__ __forceinline__ explicit ClipWalk(const ClipTable& table)
+      : t(table), chunks(table.first[table.count]), k(blockIdx.x), i(BACK ? table.count - 1 : 0) {
+    seek();
+  }
+  __device__ __forceinline__ bool more() const { return k < chunks; }
+  __device__ __forceinline__ void next() {
+    k += gridDim.x;
+    seek();
+  }
+  // The chunk within tensor i.
+  __device__ __forceinline__ int64_t chunk() const {
+    return (BACK ? chunks - 1 - k : k) - t.first[i];
+  }
+  __device__ __forceinline__ void seek() {
+    if (!more()) return;
+    if constexpr (BACK) while (chunks - 1 - k < t.first[i]) --i;
+    else while (k >= t.first[i + 1]) ++i;
+  }
+};
 
 __device__ __forceinline__ double clip_block_sum(double x) {
   __shared__ double lds[kClipThreads / 64];
@@ -83,44 +121,50 @@ __device__ __forceinline__ double clip_block_sum(double x) {
 }
 
 template <typename E>
-__device__ __forceinline__ void clip_square(const ClipTable& t, int i, int64_t chunk, double& sum) {
-  clip_chunk<E>(t.in[i], t.n[i], chunk, t.units, [&](const Pack<E, kClipV>& v, int64_t, int) {
+__device__ __forceinline__ void clip_square(const ClipChunk& c, int units, double& sum) {
 #pragma unroll
-    for (int j = 0; j < kClipV; ++j) {  // (elements there are not are 0)
-      const double g = (double)(float)v.v[j];
-      sum = fma(g, g, sum);
-    }
-  });
+  for (int u = 0; u < kClipDeep; ++u)
+    if (u < units)
+#pragma unroll
+      for (int k = 0; k < kClipElems<E>; ++k) {
+        const double g = (double)clip_get<E>(c.v[u], k);
+        sum = fma(g, g, sum);
+      }
 }
 
 __global__ __launch_bounds__(kClipThreads) void clip_norm(const ClipTable t, double* part) {
   double sum = 0.0;
-  const int64_t chunks = t.first[t.count];
-  for (int64_t k = blockIdx.x; k < chunks; k += gridDim.x) {
-    const int i = clip_find(t, k);
-    const int64_t chunk = k - t.first[i];
-    if (t.dtype[i] == CK_F32) clip_square<float>(t, i, chunk, sum);
-    else if (t.dtype[i] == CK_BF16) clip_square<bf16_t>(t, i, chunk, sum);
-    else clip_square<f16_t>(t, i, chunk, sum);
+  for (ClipWalk<false> w(t); w.more(); w.next()) {
+    ClipChunk c;
+    c.load(t, w.i, w.chunk());
+    if (t.dtype[w.i] == CK_F32) clip_square<float>(c, t.units, sum);
+    else if (t.dtype[w.i] == CK_BF16) clip_square<bf16_t>(c, t.units, sum);
+    else clip_square<f16_t>(c, t.units, sum);
   }
   sum = clip_block_sum(sum);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
 template <typename E>
-__device__ __forceinline__ void clip_write(const ClipTable& t, int i, int64_t chunk, double c) {
-  E* out = static_cast<E*>(t.out[i]);
-  clip_chunk<E>(t.in[i], t.n[i], chunk, t.units,
-                [&](const Pack<E, kClipV>& v, int64_t at, int n) {
-    float y[kClipV];
+__device__ __forceinline__ void clip_write(const ClipTable& t, int i, int64_t chunk,
+                                           const ClipChunk& c, double scale) {
+  char* p = static_cast<char*>(t.out[i]);
+  const int64_t n = t.n[i], base = chunk * t.units * kClipUnit;
 #pragma unroll
-    for (int j = 0; j < kClipV; ++j) {
-      if constexpr (sizeof(E) == 4) y[j] = (float)((double)(float)v.v[j] * c);
-      else y[j] = (float)v.v[j] * (float)c;
+  for (int u = 0; u < kClipDeep; ++u) {
+    if (u >= t.units) continue;
+    const int64_t at = base + u * kClipUnit + (int64_t)threadIdx.x * kClipAccess;
+    float y[kClipElems<E>];
+#pragma unroll
+    for (int k = 0; k < kClipElems<E>; ++k) {
+      const float g = clip_get<E>(c.v[u], k);
+      if constexpr (sizeof(E) == 4) y[k] = (float)((double)g * scale);
+      else y[k] = g * (float)scale;
     }
-    if (n == kClipV) pack_store<true, E, kClipV>(out + at, y, n);
-    else pack_store<false, E, kClipV>(out + at, y, n);
-  });
+    E* to = reinterpret_cast<E*>(p + at);
+    if (at + kClipAccess <= n) pack_store<true, E, kClipElems<E>>(to, y, 0);
+    else if (at < n) pack_store<false, E, kClipElems<E>>(to, y, (int)((n - at) / (int)sizeof(E)));
+  }
 }
 
 // Every workgroup adds the partial sums, in one order, for itself.  `same`: every
@@ -138,17 +182,17 @@ __global__ __launch_bounds__(kClipThreads) void clip_scale(const ClipTable t, co
   const bool scales = n > max_norm && (float)n < __builtin_inff();
   if (!scales && same) return;
   const double c = scales ? max_norm / n : 1.0;
-  const int64_t chunks = t.first[t.count];
-  for (int64_t k = blockIdx.x; k < chunks; k += gridDim.x) {
-    const int i = clip_find(t, chunks - 1 - k);
-    const int64_t chunk = chunks - 1 - k - t.first[i];
-    if (!t.out[i]) continue;
-    if (t.dtype[i] == CK_F32) clip_write<float>(t, i, chunk, c);
-    else if (t.dtype[i] == CK_BF16) clip_write<bf16_t>(t, i, chunk, c);
-    else clip_write<f16_t>(t, i, chunk, c);
+  for (ClipWalk<true> w(t); w.more(); w.next()) {
+    if (!t.out[w.i]) continue;
+    ClipChunk x;
+    x.load(t, w.i, w.chunk());
+    if (t.dtype[w.i] == CK_F32) clip_write<float>(t, w.i, w.chunk(), x, c);
+    else if (t.dtype[w.i] == CK_BF16) clip_write<bf16_t>(t, w.i, w.chunk(), x, c);
+    else clip_write<f16_t>(t, w.i, w.chunk(), x, c);
   }
 }
 
+// most: the bytes of all gradients.
 ck_status clip_check(const ck_clip_tensor* tensors, int64_t count, int64_t* most) {
   *most = 0;
   if (count < 0) {
@@ -186,7 +230,7 @@ ck_status clip_check(const ck_clip_tensor* tensors, int64_t count, int64_t* most
       set_error("tensor %lld is not aligned to its element type", (long long)i);
       return CK_ERR_BAD_VALUE;
     }
-    *most += t.n;
+    *most += t.n * (int64_t)e;
   }
   return CK_OK;
 }
@@ -237,10 +281,10 @@ int64_t clip_fill(const ck_clip_tensor* tensors, int64_t count, int64_t i, int u
     const int k = t->count++;
     t->in[k] = x.grad;
     t->out[k] = x.out;
-    t->n[k] = x.n;
+    t->n[k] = x.n * (int64_t)seq_elem_bytes(x.dtype);
     t->dtype[k] = (int8_t)x.dtype;
     const int64_t unit = (int64_t)units * kClipUnit;
-    t->first[k + 1] = t->first[k] + (x.n + unit - 1) / unit;
+    t->first[k + 1] = t->first[k] + (t->n[k] + unit - 1) / unit;
     if (x.out && x.out != x.grad) *same = false;
   }
   return i;
@@ -314,7 +358,7 @@ extern "C" ck_status ck_clip_grad_norm(const ck_clip_tensor* tensors, int64_t co
     for (int k = 0; k < t.count; ++k) writes = writes || t.out[k];
     if (!writes && !to) continue;
     const int64_t chunks = writes ? t.first[t.count] : 1;
-    const int blocks = (int)std::min<int64_t>(2 * kClipBlocks, std::max<int64_t>(1, chunks));
+    const int blocks = (int)std::min<int64_t>(kClipBlocks, std::max<int64_t>(1, chunks));
     clip_scale<<<blocks, kClipThreads, 0, stream>>>(t, part, parts, writes ? max_norm : INFINITY,
                                                     same ? 1 : 0, to);
     to = nullptr;

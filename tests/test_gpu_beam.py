@@ -24,7 +24,8 @@ def _need_gpu():
 
 
 def select(x, scores, finished=None, eos=None):
-    """The definition: (scores, parents, tokens, finished) in fp64."""
+    """The definition: (scores, parents, tokens, finished) in fp64.  Of equal scores the
+    lower beam is first, and in one beam the larger logit, then the lower token."""
     B, K, V = x.shape
     x = np.where(np.isnan(x), -np.inf, np.minimum(x, np.finfo(np.float32).max))
     top = x.max(-1, keepdims=True)
@@ -37,8 +38,12 @@ def select(x, scores, finished=None, eos=None):
         end[:, :, eos] = scores
         s = np.where(finished[..., None], end, s)
     s = np.where(~(scores > -np.inf)[..., None], -np.inf, s)
-    s = s.reshape(B, K * V)
-    order = np.argsort(-s, axis=1, kind="stable")[:, :K]
+    x = np.where(s == -np.inf, -np.inf, x)
+    if finished is not None:
+        x = np.where(finished[..., None] & (s > -np.inf), 0.0, x)
+    s, x = s.reshape(B, K * V), x.reshape(B, K * V)
+    beam = np.repeat(np.arange(K), V)
+    order = np.stack([np.lexsort((-x[b], beam, -s[b])) for b in range(B)])[:, :K]
     got = np.take_along_axis(s, order, 1)
     parents, tokens = order // V, order % V
     done = None if eos is None else tokens == eos
@@ -171,6 +176,18 @@ def test_masked_rows_infinities_and_nan(dtype):
     done[0, 1] = done[1, 0] = done[5, 2] = done[5, 3] = True
     check(sgr.beam_select(x, scores, torch.from_numpy(done).cuda(), 4999),
           select(xv, sv, done, 4999))
+
+
+@pytest.mark.parametrize("scale", [1e38, 3.3e38, 1e-39])
+def test_logits_near_the_ends_of_fp32(scale):
+    """Differences beyond fp32's range; and all alike to it but in their order."""
+    r = np.random.default_rng(11)
+    xv = (scale * r.uniform(-1, 1, (3, 4, 700))).astype(np.float32)
+    xv[1] = -np.abs(xv[1]) - np.float32(scale * 0.01)
+    xv[2, 1, 5], xv[2, 2, 9] = np.inf, -np.inf
+    sv = -20 * r.random((3, 4)).astype(np.float32)
+    check(sgr.beam_select(torch.from_numpy(xv).cuda(), torch.from_numpy(sv).cuda()),
+          select(xv.astype(np.float64), sv))
 
 
 def test_all_beams_finished():
