@@ -12,9 +12,10 @@
 // slot runs through its steps again, in registers, from there.  So every element is
 // read once, whatever the number of waves over the time axis.
 //
-// Where rows and channels have too few groups for the chip, the steps are cut into
-// chunks of workgroups of their own, and a launch before sums up every chunk but the
-// one that nothing follows.
+// A workgroup goes through all windows of its columns (a group of a row's channels).
+// Where there are too few columns for the chip, every window has a workgroup of its own
+// instead (gate_chain): it leaves its pair where the others see it, and takes the state
+// before it from the pairs of the windows before, so that elements are still read once.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -27,7 +28,7 @@ namespace ckhip {
 
 constexpr int kGateStep = 8;      // steps of a slot, and of a saved state
 constexpr int kGateLanes = 32;    // lanes of a slot
-constexpr int kGateFwdWaves = 8, kGateBwdWaves = 8;  // of a workgroup, at most
+constexpr int kGateWaves = 8;     // of a workgroup, at most
 // Offsets from a window's first step are 32-bit bytes; a window of a single wave (16
 // steps) reaches this far.
 constexpr int64_t kGateMaxStrideT = (int64_t(1) << 26) - 1;
@@ -37,8 +38,7 @@ struct GatePlan {
   int v;        // channels a lane
   int waves;    // of a workgroup
   int groups;   // of channels, in a row
-  int chunks;   // of a row's steps
-  int chunk;    // steps of a chunk, a multiple of a slot's unless there is one
+  int windows;  // that are handed out as workgroups of their own (1: none is)
 };
 
 template <typename E>
@@ -48,10 +48,11 @@ struct GateArgs {
   const float *f_bias, *i_bias, *state0, *gstate;
   float *state, *gstate0;
   float* saved;       // [ceil(T / kGateStep)][B][D]: the state before each tile
-  float* sums;        // [chunks - 1][B][D][2]: product of a and state (or adjoint) of a chunk
-  float* part;        // [B][chunks][2][D]: sums of gf and gi
+  float* part;        // [windows][B][2][D]: sums of gf and gi
+  uint32_t* ticket;   // see GateChain
+  uint64_t *pairs, *states;
   const int32_t* lengths;
-  int T, B, D, groups, chunks, chunk;
+  int T, B, D, groups, windows;
 };
 
 // A gate s(v), held as the smaller of s(v) and s(-v) with its own relative error
@@ -110,18 +111,17 @@ __device__ __forceinline__ uint32_t gate_offset(uint32_t o) {
 template <int V>
 struct GateSpot {
   int wave, waves, lane, upper;  // upper: the wave's second slot
-  int group, chunk, b, len;      // len: steps of the row that hold text
+  int group, b, len;             // len: steps of the row that hold text
   int64_t c, c0;                 // first channel loaded, and of the workgroup's
   int cl;                        // c - c0
 
+  // Column `id`, if there is one.  (Groups times rows are below 2^31: rows times channels
+  // below 2^36.)
   template <typename A>
-  __device__ __forceinline__ bool at(const A& s, int64_t id, int chunks) {
-    // (groups, rows and chunks together are below 2^31: rows times channels below 2^36)
-    const uint32_t r = (uint32_t)id / (uint32_t)s.groups;
-    group = (int)((uint32_t)id - r * (uint32_t)s.groups);
-    chunk = (int)(r / (uint32_t)s.B);
-    b = (int)(r - (uint32_t)chunk * (uint32_t)s.B);
-    if (chunk >= chunks) return false;
+  __device__ __forceinline__ bool at(const A& s, uint32_t id) {
+    b = (int)(id / (uint32_t)s.groups);
+    group = (int)(id - (uint32_t)b * (uint32_t)s.groups);
+    if (b >= s.B) return false;
     wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     waves = (int)blockDim.x >> 6;
     lane = (int)threadIdx.x & (kGateLanes - 1);
@@ -186,18 +186,16 @@ struct alignas(8 * V) GatePair {
 // is enough.
 template <int V, int WAVES>
 struct GateMeet {
-  GatePair<V> pair[2][WAVES][kGateLanes];   // of each wave
-  GatePair<V> carry[2][kGateLanes];         // h: the state before a window; p: see gate_fold
+  GatePair<V> pair[2][WAVES][kGateLanes];  // of each wave
+  float carry[2][kGateLanes][V];           // the state before a window
 };
 
-// Folds the pairs of a workgroup's slots.  Forward in time (REVERSE: backward).
-// Returns the state before the thread's slot; the wave that comes last leaves the state
-// behind the window as the next one's carry, and with it the product of all decays so
-// far.  (The first carry is written before the first window.)
-template <bool REVERSE, int V, int WAVES>
-__device__ __forceinline__ void gate_fold(GateMeet<V, WAVES>& meet, int turn, const GateSpot<V>& at,
-                                          const GatePair<V>& mine, float (&in)[V]) {
-  GatePair<V> other, both;
+// The pair of a wave's two slots, of the pair of the thread's; `other`: the wave's other
+// slot's.
+template <bool REVERSE, int V>
+__device__ __forceinline__ GatePair<V> gate_both(const GateSpot<V>& at, const GatePair<V>& mine,
+                                                 GatePair<V>& other) {
+  GatePair<V> both;
   const bool second = REVERSE ? !at.upper : at.upper;  // behind the wave's other slot
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -207,41 +205,181 @@ __device__ __forceinline__ void gate_fold(GateMeet<V, WAVES>& meet, int turn, co
     both.h[j] = second ? fmaf(mine.p[j], other.h[j], mine.h[j])
                        : fmaf(other.p[j], mine.h[j], other.h[j]);
   }
-  if (!at.upper) meet.pair[turn][at.wave][at.lane] = both;
-  __syncthreads();
-  GatePair<V> c = meet.carry[turn][at.lane];
+  return both;
+}
+
+// h: the state before a window; becomes that before the thread's slot.  Returns the
+// state behind the wave's steps.
+template <bool REVERSE, int V>
+__device__ __forceinline__ GatePair<V> gate_through(const GatePair<V> (*pair)[kGateLanes],
+                                                    const GateSpot<V>& at,
+                                                    const GatePair<V>& both,
+                                                    const GatePair<V>& other, float (&h)[V]) {
   const int rank = REVERSE ? at.waves - 1 - at.wave : at.wave;
 #pragma unroll 4
   for (int k = 0; k < rank; ++k) {
-    const GatePair<V> one = meet.pair[turn][REVERSE ? at.waves - 1 - k : k][at.lane];
+    const GatePair<V> one = pair[REVERSE ? at.waves - 1 - k : k][at.lane];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      c.h[j] = fmaf(one.p[j], c.h[j], one.h[j]);
-      c.p[j] *= one.p[j];
-    }
+    for (int j = 0; j < V; ++j) h[j] = fmaf(one.p[j], h[j], one.h[j]);
   }
+  GatePair<V> behind;
+  const bool second = REVERSE ? !at.upper : at.upper;
 #pragma unroll
-  for (int j = 0; j < V; ++j) in[j] = second ? fmaf(other.p[j], c.h[j], other.h[j]) : c.h[j];
-  if (rank == at.waves - 1 && !at.upper) {
+  for (int j = 0; j < V; ++j) {
+    behind.h[j] = fmaf(both.p[j], h[j], both.h[j]);
+    if (second) h[j] = fmaf(other.p[j], h[j], other.h[j]);
+  }
+  return behind;
+}
+
+// Folds the pairs of a workgroup's slots.  Forward in time (REVERSE: backward).
+// Returns the state before the thread's slot; the wave that comes last leaves the state
+// behind the window as the next one's carry.  (The first carry is written before the
+// first window.)
+template <bool REVERSE, int V, int WAVES>
+__device__ __forceinline__ void gate_fold(GateMeet<V, WAVES>& meet, int turn, const GateSpot<V>& at,
+                                          const GatePair<V>& mine, float (&in)[V]) {
+  GatePair<V> other;
+  const GatePair<V> both = gate_both<REVERSE>(at, mine, other);
+  if (!at.upper) meet.pair[turn][at.wave][at.lane] = both;
+  __syncthreads();
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      c.h[j] = fmaf(both.p[j], c.h[j], both.h[j]);
-      c.p[j] *= both.p[j];
-    }
-    meet.carry[turn ^ 1][at.lane] = c;
+  for (int j = 0; j < V; ++j) in[j] = meet.carry[turn][at.lane][j];
+  const GatePair<V> behind = gate_through<REVERSE>(meet.pair[turn], at, both, other, in);
+  if ((REVERSE ? at.wave == 0 : at.wave == at.waves - 1) && !at.upper) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) meet.carry[turn ^ 1][at.lane][j] = behind.h[j];
   }
 }
 
-// Leaves a chunk's pair to the launch that follows.
-template <int V, typename A>
-__device__ __forceinline__ void gate_sum_store(const A& s, const GateSpot<V>& at,
-                                               const GatePair<V>& pair) {
-  float* to = s.sums + ((int64_t)at.chunk * s.B * s.D + (int64_t)at.b * s.D + at.c) * 2;
+// Windows that are workgroups of their own.  Those of a column take their numbers by the
+// column's ticket, in the order in which states pass (by time; in the backward against
+// it): a workgroup waits only for such of its column with a lower number, which run
+// already, so that every wait ends whatever else the chip runs and in whatever order
+// workgroups start.  (One ticket for all columns: its additions, one after the other
+// where the chip's parts meet, took longer than the work.)  Window number n
+//   - leaves the pair of its steps, which needs no other window;
+//   - takes the state before windows kGateRun (n / kGateRun) ..., and the pairs of those
+//     between that one and itself;
+//   - leaves the state behind it where the next run of windows begins.
+// What is left is one 64-bit word a channel, complete in itself, written and read past
+// the caches that are not common to the chip, so that no order of other accesses
+// matters: a pair's product, never negative, and state; a state with a zero.  Before
+// the launch all words hold kGateAbsent.  Runs have a fixed length: results do not go by
+// who came first.  A wait of kGatePolls polls (seconds) gives up and goes on with NaN.
+constexpr int kGateRun = 8;  // a wave each waits for one of the others, and for the state
+constexpr uint64_t kGateAbsent = ~0ull;
+constexpr int kGatePolls = 1 << 22;
+constexpr int kGateTicket = 32;  // words between two columns' tickets: a cache line each
+
+__device__ __forceinline__ void gate_leave(uint64_t* to, float p, float h) {
+  const uint64_t w = (uint64_t)(__builtin_bit_cast(uint32_t, p) & 0x7FFFFFFFu) << 32 |
+                     __builtin_bit_cast(uint32_t, h);
+  __hip_atomic_store(to, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// The words of a lane's channels; each lane of the wave waits for all of them.
+template <int V>
+__device__ __forceinline__ GatePair<V> gate_await(uint64_t* from) {
+  uint64_t w[V];
+  bool there = false;
+  for (int poll = 0; poll < kGatePolls && !there; ++poll) {
+    if (poll) __builtin_amdgcn_s_sleep(1);
+    bool mine = true;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      w[j] = __hip_atomic_load(from + j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      mine = mine && w[j] != kGateAbsent;
+    }
+    there = __all(mine);
+  }
+  GatePair<V> r;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    to[2 * j] = pair.p[j];
-    to[2 * j + 1] = pair.h[j];
+    r.p[j] = __builtin_bit_cast(float, (uint32_t)(w[j] >> 32));
+    r.h[j] = there ? __builtin_bit_cast(float, (uint32_t)w[j]) : __builtin_nanf("");
   }
+  return r;
+}
+
+template <int V>
+struct GateChain {
+  GatePair<V> pair[kGateWaves][kGateLanes];    // of the workgroup's waves
+  GatePair<V> before[kGateRun][kGateLanes];    // of windows, and the run's state (the last)
+  uint32_t ticket;
+};
+
+// The workgroup's column (false: it has none), and the number it takes there.
+template <int V, typename A>
+__device__ __forceinline__ bool gate_number(GateChain<V>& chain, const A& s, GateSpot<V>& at,
+                                            int* number) {
+  const int64_t id = seq_block();
+  const uint32_t cols = (uint32_t)s.groups * (uint32_t)s.B;
+  if (id >= (int64_t)cols * s.windows) return false;
+  // (a column's windows on all XCDs: 93 us a prompt of 16384 x 1 x 2048 bf16, 105 on one)
+  const uint32_t col = ((uint32_t)id + (uint32_t)id / cols) % cols;
+  if (threadIdx.x == 0)
+    chain.ticket = __hip_atomic_fetch_add(s.ticket + (int64_t)col * kGateTicket, 1u,
+                                          __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  at.at(s, col);
+  __syncthreads();
+  *number = (int)__builtin_amdgcn_readfirstlane(chain.ticket);
+  return true;
+}
+
+// As gate_fold, for window `n` of a chain whose first state is `first`.  `last`: nothing
+// comes behind it.  Returns the state behind the window where the thread's wave ends it.
+template <bool REVERSE, int V, typename A>
+__device__ __forceinline__ GatePair<V> gate_chain(GateChain<V>& chain, const A& s,
+                                                  const GateSpot<V>& at, int n, bool last,
+                                                  const float* first, const GatePair<V>& mine,
+                                                  float (&in)[V]) {
+  const int64_t cols = (int64_t)s.B * s.D, col = (int64_t)at.b * s.D + at.c;
+  GatePair<V> other;
+  const GatePair<V> both = gate_both<REVERSE>(at, mine, other);
+  if (!at.upper) chain.pair[at.wave][at.lane] = both;
+  __syncthreads();
+  const int run = n / kGateRun, place = n % kGateRun;
+  if (at.wave == 0 && !last && place != kGateRun - 1) {
+    GatePair<V> all = chain.pair[REVERSE ? at.waves - 1 : 0][at.lane];
+    for (int k = 1; k < at.waves; ++k) {
+      const GatePair<V> one = chain.pair[REVERSE ? at.waves - 1 - k : k][at.lane];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        all.p[j] *= one.p[j];
+        all.h[j] = fmaf(one.p[j], all.h[j], one.h[j]);
+      }
+    }
+    if (!at.upper)
+#pragma unroll
+      for (int j = 0; j < V; ++j) gate_leave(s.pairs + n * cols + col + j, all.p[j], all.h[j]);
+  }
+  if (at.wave < place || at.wave == kGateRun - 1) {
+    GatePair<V> got;
+    if (at.wave < place) {
+      got = gate_await<V>(s.pairs + (int64_t)(run * kGateRun + at.wave) * cols + col);
+    } else if (run > 0) {
+      got = gate_await<V>(s.states + (int64_t)(run - 1) * cols + col);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) got.h[j] = first ? first[col + j] : 0.0f;
+    }
+    if (!at.upper) chain.before[at.wave][at.lane] = got;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < V; ++j) in[j] = chain.before[kGateRun - 1][at.lane].h[j];
+  for (int k = 0; k < place; ++k) {
+    const GatePair<V> one = chain.before[k][at.lane];
+#pragma unroll
+    for (int j = 0; j < V; ++j) in[j] = fmaf(one.p[j], in[j], one.h[j]);
+  }
+  const GatePair<V> behind = gate_through<REVERSE>(chain.pair, at, both, other, in);
+  if ((REVERSE ? at.wave == 0 : at.wave == at.waves - 1) && !at.upper && !last &&
+      place == kGateRun - 1) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) gate_leave(s.states + run * cols + col + j, 0.0f, behind.h[j]);
+  }
+  return behind;
 }
 
 template <typename E>

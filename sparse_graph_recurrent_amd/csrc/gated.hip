@@ -8,7 +8,8 @@
 namespace ckhip {
 namespace {
 
-constexpr int64_t kGateCus = 256;
+// Below as many columns every window is a workgroup of its own.
+constexpr int64_t kGateColumns = 256;
 
 ck_status gate_check_shape(const ck_gated_shape* s) {
   if (!s) {
@@ -18,44 +19,45 @@ ck_status gate_check_shape(const ck_gated_shape* s) {
   return seq_check_shape(s->T, s->B, s->D, s->dtype);
 }
 
-GatePlan gate_plan(const ck_gated_shape& s, int most_waves) {
+// How a call with these step strides (bytes; 0: any) is spread over the chip.
+GatePlan gate_plan(const ck_gated_shape& s, int64_t step) {
   GatePlan p;
   p.v = s.dtype == CK_F32 || s.D < 2 ? 1 : 2;
   const int64_t groups = (s.D + kGateLanes * p.v - 1) / (kGateLanes * p.v);
   p.groups = (int)groups;
   const int64_t cols = groups * s.B;
-  // (a launch holds fewer than 2^32 threads along its first dimension)
-  if (cols >= kSeqGridX / 4) most_waves = std::min(most_waves, 8);
   const int64_t pairs = (s.T + 2 * kGateStep - 1) / (2 * kGateStep);
-  p.waves = (int)std::min<int64_t>(most_waves, std::max<int64_t>(1, pairs));
-  const int64_t window = 2 * kGateStep * p.waves;
-  int64_t want = std::max<int64_t>(1, kGateCus / cols);
-  want = std::max<int64_t>(1, std::min(want, s.T / window));
-  const int64_t per = (s.T + want - 1) / want;
-  p.chunk = (int)((per + window - 1) / window * window);
-  p.chunks = p.chunk ? (int)((s.T + p.chunk - 1) / p.chunk) : 1;
+  // a window's offsets are 32 bits
+  const int64_t reach = step ? ((UINT32_MAX - 256) / step + 1) / (2 * kGateStep) : kGateWaves;
+  p.waves = (int)std::max<int64_t>(1, std::min({(int64_t)kGateWaves, pairs, reach}));
+  p.windows = 1;
+  const int64_t windows = (pairs + kGateWaves - 1) / kGateWaves;
+  if (cols < kGateColumns && windows > 1 && p.waves == kGateWaves && windows * cols < INT_MAX)
+    p.windows = (int)windows;
   return p;
 }
 
-// Fewer waves where a window's offsets would pass 32 bits (the chunks stay: the
-// workspace does not go by strides).
-void gate_reach(GatePlan* p, int dtype, std::initializer_list<const ck_seq*> tensors) {
+int64_t gate_step(int dtype, std::initializer_list<const ck_seq*> tensors) {
   int64_t step = 1;
   for (const ck_seq* q : tensors)
     if (q->data) step = std::max(step, q->stride_t * (int64_t)seq_elem_bytes(dtype));
-  const int64_t steps = (UINT32_MAX - 256) / step + 1;
-  p->waves = (int)std::min<int64_t>(p->waves, std::max<int64_t>(1, steps / (2 * kGateStep)));
+  return step;
 }
 
-// Workspace: the chunks' pairs, then (backward) the bias gradients' parts.
+// Workspace: a chain's tickets and words, then (backward) the bias gradients' parts.  (It
+// does not go by strides: long ones leave the chain's share unused.)
 struct GateWs {
-  size_t part, total;
+  size_t pairs, states, part, total;
 };
-GateWs gate_ws(const ck_gated_shape& s, const GatePlan& p, bool backward) {
-  const size_t col = (size_t)s.B * s.D * sizeof(float);
+GateWs gate_ws(const ck_gated_shape& s, bool backward) {
+  const int64_t windows = gate_plan(s, 0).windows;
+  const int64_t col = s.B * s.D, runs = windows / kGateRun;
   GateWs w;
-  w.part = ((size_t)(p.chunks - 1) * 2 * col + 255) & ~size_t(255);
-  w.total = w.part + (backward ? (size_t)p.chunks * 2 * col : 0);
+  w.pairs = windows > 1 ? kGateColumns * kGateTicket * sizeof(uint32_t) : 0;
+  w.states = w.pairs + (windows > 1 ? (size_t)windows * col * sizeof(uint64_t) : 0);
+  w.part = (w.states + (windows > 1 ? (size_t)runs * col * sizeof(uint64_t) : 0) + 255) &
+           ~size_t(255);
+  w.total = w.part + (backward ? (size_t)windows * 2 * col * sizeof(float) : 0);
   return w;
 }
 
@@ -90,7 +92,7 @@ ck_status gate_check_inputs(const ck_gated_shape* shape, const ck_gated_inputs* 
 
 template <typename E>
 GateArgs<E> gate_args(const ck_gated_shape& s, const GatePlan& p, const ck_gated_inputs& in,
-                      void* workspace) {
+                      void* workspace, const GateWs& ws) {
   GateArgs<E> a = {};
   a.x = seq_of<const E>(in.x);
   a.f = seq_of<const E>(in.f);
@@ -100,14 +102,39 @@ GateArgs<E> gate_args(const ck_gated_shape& s, const GatePlan& p, const ck_gated
   a.i_bias = in.i_bias;
   a.state0 = in.state0;
   a.lengths = in.lengths;
-  a.sums = static_cast<float*>(workspace);
+  if (p.windows > 1) {
+    char* at = static_cast<char*>(workspace);
+    a.ticket = reinterpret_cast<uint32_t*>(at);
+    a.pairs = reinterpret_cast<uint64_t*>(at + ws.pairs);
+    a.states = reinterpret_cast<uint64_t*>(at + ws.states);
+  }
   a.T = (int)s.T;
   a.B = (int)s.B;
   a.D = (int)s.D;
   a.groups = p.groups;
-  a.chunks = p.chunks;
-  a.chunk = p.chunk;
+  a.windows = p.windows;
   return a;
+}
+
+// The tickets and words of a chain, before its launch: all of `bytes` from `base` on,
+// zeros up to `tickets`.  (A kernel: a graph's own memory sets have come out wrong when
+// replayed.)
+constexpr int kGateClearThreads = 256;
+__global__ __launch_bounds__(kGateClearThreads) void gate_clear(char* base, int64_t tickets,
+                                                                int64_t bytes) {
+  const int64_t at = ((int64_t)blockIdx.x * kGateClearThreads + threadIdx.x) * 16;
+  const uint32_t w = at < tickets ? 0u : ~0u;
+  if (at + 16 <= bytes) *reinterpret_cast<uint4*>(base + at) = make_uint4(w, w, w, w);
+  else if (at < bytes) *reinterpret_cast<uint2*>(base + at) = make_uint2(w, w);
+}
+template <typename E>
+void gate_prepare(const GateArgs<E>& a, const GateWs& ws, hipStream_t stream) {
+  static_assert(kGateAbsent == ~0ull);
+  if (!a.ticket) return;
+  const int64_t bytes = ws.states + a.windows / kGateRun * (int64_t)a.B * a.D * sizeof(uint64_t);
+  const int64_t each = kGateClearThreads * 16;
+  gate_clear<<<(unsigned)((bytes + each - 1) / each), kGateClearThreads, 0, stream>>>(
+      reinterpret_cast<char*>(a.ticket), ws.pairs, bytes);
 }
 
 // One token a row: a thread owns V channels.  Bound by the launch.
@@ -166,8 +193,8 @@ extern "C" ck_status ck_gated_sizes(const ck_gated_shape* shape, size_t* saved_b
   const ck_gated_shape& s = *shape;
   if (saved_bytes)
     *saved_bytes = (size_t)((s.T + kGateStep - 1) / kGateStep) * s.B * s.D * sizeof(float);
-  if (forward_bytes) *forward_bytes = gate_ws(s, gate_plan(s, kGateFwdWaves), false).total;
-  if (backward_bytes) *backward_bytes = gate_ws(s, gate_plan(s, kGateBwdWaves), true).total;
+  if (forward_bytes) *forward_bytes = gate_ws(s, false).total;
+  if (backward_bytes) *backward_bytes = gate_ws(s, true).total;
   return CK_OK;
 }
 
@@ -179,17 +206,19 @@ extern "C" ck_status ck_gated_forward(const ck_gated_shape* shape, const ck_gate
   if (rc == CK_OK) rc = gate_check_out(*shape, out, shape->T == 0, "out");
   if (rc == CK_OK) rc = gate_check_f32(state, "state");
   if (rc != CK_OK) return rc;
-  GatePlan p = gate_plan(*shape, kGateFwdWaves);
-  gate_reach(&p, shape->dtype, {&in->x, &in->f, &in->i, &in->z, &out});
-  rc = seq_check_ws(workspace, workspace_bytes, gate_ws(*shape, p, false).total);
+  const GatePlan p =
+      gate_plan(*shape, gate_step(shape->dtype, {&in->x, &in->f, &in->i, &in->z, &out}));
+  const GateWs ws = gate_ws(*shape, false);
+  rc = seq_check_ws(workspace, workspace_bytes, ws.total);
   if (rc == CK_OK && saved) rc = check_aligned(saved, "saved");
   if (rc != CK_OK) return rc;
   return seq_dispatch(shape->dtype, [&](auto* e) -> ck_status {
     using E = std::remove_pointer_t<decltype(e)>;
-    GateArgs<E> a = gate_args<E>(*shape, p, *in, workspace);
+    GateArgs<E> a = gate_args<E>(*shape, p, *in, workspace, ws);
     a.out = seq_of<E>(out);
     a.state = state;
     a.saved = static_cast<float*>(saved);
+    gate_prepare(a, ws, stream);
     return gate_run_forward(a, p, stream);
   });
 }
@@ -217,15 +246,15 @@ extern "C" ck_status ck_gated_backward(const ck_gated_shape* shape, const ck_gat
   if (rc == CK_OK) rc = gate_check_f32(grads->state0, "the gradient of state0");
   if (rc == CK_OK && saved) rc = check_aligned(saved, "saved");
   if (rc != CK_OK) return rc;
-  GatePlan p = gate_plan(*shape, kGateBwdWaves);
-  gate_reach(&p, shape->dtype, {&in->x, &in->f, &in->i, &in->z, &grad_out, &grads->x, &grads->f,
-                                &grads->i, &grads->z});
-  const GateWs ws = gate_ws(*shape, p, true);
+  const GatePlan p = gate_plan(
+      *shape, gate_step(shape->dtype, {&in->x, &in->f, &in->i, &in->z, &grad_out, &grads->x,
+                                       &grads->f, &grads->i, &grads->z}));
+  const GateWs ws = gate_ws(*shape, true);
   rc = seq_check_ws(workspace, workspace_bytes, ws.total);
   if (rc != CK_OK) return rc;
   return seq_dispatch(shape->dtype, [&](auto* e) -> ck_status {
     using E = std::remove_pointer_t<decltype(e)>;
-    GateArgs<E> a = gate_args<E>(*shape, p, *in, workspace);
+    GateArgs<E> a = gate_args<E>(*shape, p, *in, workspace, ws);
     a.saved = static_cast<float*>(const_cast<void*>(saved));
     a.go = seq_of<const E>(grad_out);
     a.gstate = grad_state;
@@ -236,6 +265,7 @@ extern "C" ck_status ck_gated_backward(const ck_gated_shape* shape, const ck_gat
     a.gstate0 = grads->state0;
     if (grads->f_bias || grads->i_bias)
       a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.part);
+    gate_prepare(a, ws, stream);
     return gate_run_backward(a, p, grads->f_bias, grads->i_bias, stream);
   });
 }
@@ -261,7 +291,7 @@ extern "C" ck_status ck_gated_step(const ck_gated_shape* shape, const ck_gated_i
   return seq_dispatch(shape->dtype, [&](auto* e) -> ck_status {
     using E = std::remove_pointer_t<decltype(e)>;
     constexpr int V = sizeof(E) == 2 ? 2 : 1;
-    GateArgs<E> a = gate_args<E>(*shape, GatePlan{}, *in, nullptr);
+    GateArgs<E> a = gate_args<E>(*shape, GatePlan{}, *in, nullptr, GateWs{});
     a.out = seq_of<E>(out);
     a.state = state;
     const int64_t threads = shape->B * ((shape->D + V - 1) / V);

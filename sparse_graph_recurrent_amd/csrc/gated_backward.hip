@@ -22,120 +22,87 @@ __device__ __forceinline__ Silu silu_hw(float z) {
   return Silu{z * s, s * fmaf(z, 1.0f - s, 1.0f)};
 }
 
-// SUM: the pairs (product of a, adjoint) of all chunks but the first, for the launch
-// that follows.
-template <typename E, int V, bool I, bool Z, bool SUM>
-__global__ __launch_bounds__(64 * kGateBwdWaves) void gate_bwd(const GateArgs<E> s) {
-  __shared__ GateMeet<V, kGateBwdWaves> meet;
-  __shared__ float bias[SUM ? 1 : 2 * kGateBwdWaves][2 * V][kGateLanes];
-  GateSpot<V> at;
-  if (!at.at(s, seq_block(), SUM ? s.chunks - 1 : s.chunks)) return;
-  const int t0 = (at.chunk + (SUM ? 1 : 0)) * s.chunk, t1 = min(t0 + s.chunk, s.T);
-  const int window = 2 * at.waves * kGateStep;
-  const int slot = (2 * at.wave + at.upper) * kGateStep;  // its first step in a window
-  const int steps = min(at.len, t1);
-  const int64_t col = (int64_t)at.b * s.D + at.c;
-  GateTile<E, V> x, f, i, z, go, nx, nf, ni, nz, ngo;
-  float nbefore[V] = {};
-  auto fetch = [&](auto all, int t) {
-    constexpr bool ALL = decltype(all)::value;
-    const int last = steps - 1 - t;
-    nf.template load<ALL>(s.f, at, t, slot, last);
-    if constexpr (!SUM) {
-      if constexpr (I) ni.template load<ALL>(s.i, at, t, slot, last);
-      nx.template load<ALL>(s.x, at, t, slot, last);
-      const float* p =
-          s.saved + ((int64_t)((t + (ALL ? slot : min(slot, last))) / kGateStep) * s.B * s.D + col);
+// What a slot reads of a window.
+template <typename E, int V, bool I, bool Z>
+struct GateInputs {
+  GateTile<E, V> x, f, i, z, go;
+  float before[V];
+  template <bool ALL>
+  __device__ __forceinline__ void load(const GateArgs<E>& s, const GateSpot<V>& at, int t, int slot,
+                                       int last) {
+    f.template load<ALL>(s.f, at, t, slot, last);
+    if constexpr (I) i.template load<ALL>(s.i, at, t, slot, last);
+    x.template load<ALL>(s.x, at, t, slot, last);
+    const float* p = s.saved + ((int64_t)((t + (ALL ? slot : min(slot, last))) / kGateStep) * s.B *
+                                    s.D + (int64_t)at.b * s.D + at.c);
 #pragma unroll
-      for (int j = 0; j < V; ++j) nbefore[j] = p[j];
-    }
-    if constexpr (Z) nz.template load<ALL>(s.z, at, t, slot, last);
-    ngo.template load<ALL>(s.go, at, t, slot, last);
-  };
-  int t = t0 + (t1 - t0 - 1) / window * window;  // windows from the last to the first
-  for (; t >= t0 && t >= steps; t -= window) {   // behind the text
-    if constexpr (SUM) continue;
-    GateRows<E> gx(s.gx, t, at.b, at.c0), gf(s.gf, t, at.b, at.c0), gi(s.gi, t, at.b, at.c0),
-        gz(s.gz, t, at.b, at.c0);
-    const float none[V] = {};
-    const uint32_t own = (uint32_t)at.cl * (uint32_t)sizeof(E);
-#pragma unroll 1
-    for (int k = slot; k < slot + kGateStep && t + k < t1; ++k) {
-      pack_store<true, E, V>(gx.at((uint32_t)k * gx.step + own), none, V);
-      pack_store<true, E, V>(gf.at((uint32_t)k * gf.step + own), none, V);
-      if constexpr (I) pack_store<true, E, V>(gi.at((uint32_t)k * gi.step + own), none, V);
-      if constexpr (Z) pack_store<true, E, V>(gz.at((uint32_t)k * gz.step + own), none, V);
-    }
+    for (int j = 0; j < V; ++j) before[j] = p[j];
+    if constexpr (Z) z.template load<ALL>(s.z, at, t, slot, last);
+    go.template load<ALL>(s.go, at, t, slot, last);
   }
-  if (t >= t0) fetch(std::false_type(), t);
-  float fb[V], ib[V], sum_f[V] = {}, sum_i[V] = {};  // (the biases with their sign turned)
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    fb[j] = s.f_bias ? -s.f_bias[at.c + j] : 0.0f;
-    ib[j] = I && s.i_bias ? -s.i_bias[at.c + j] : 0.0f;
-  }
-  if (threadIdx.x < kGateLanes) {
-    GatePair<V> c;
+};
+
+// The biases of a lane's channels, their sign turned, and what their gradients add up to.
+template <int V>
+struct GateBias {
+  float f[V], i[V], sum_f[V] = {}, sum_i[V] = {};
+  template <typename A>
+  __device__ __forceinline__ GateBias(const A& s, const GateSpot<V>& at, bool own) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      c.p[j] = 1.0f;
-      c.h[j] = !SUM && s.gstate ? s.gstate[col + j] : 0.0f;
+      f[j] = s.f_bias ? -s.f_bias[at.c + j] : 0.0f;
+      i[j] = own && s.i_bias ? -s.i_bias[at.c + j] : 0.0f;
     }
-    if constexpr (!SUM)
-      for (int k = s.chunks - 1; k > at.chunk; --k) {
-        const float* p = s.sums + ((int64_t)(k - 1) * s.B * s.D + col) * 2;
-#pragma unroll
-        for (int j = 0; j < V; ++j) c.h[j] = fmaf(p[2 * j], c.h[j], p[2 * j + 1]);
-      }
-    meet.carry[0][at.lane] = c;
   }
-  int turn = 0;
-  // WHOLE: every slot's steps hold text.  NEXT: another window
-  // follows (full of text), and is on its way while this one is worked on.
-  auto work = [&](auto whole, auto next) {
-    constexpr bool WHOLE = decltype(whole)::value;
-    x = nx, f = nf, i = ni, z = nz, go = ngo;
+};
+
+// A slot's way back through its steps: from an adjoint of zero, and then from the one
+// behind it.  WHOLE: all steps hold text, else the first n.
+template <typename E, int V, bool I, bool Z>
+struct GateBackward {
+  Gate a[kGateStep][V], own[kGateStep][V];
+  float before[kGateStep][V], y[kGateStep][V];
+
+  template <bool WHOLE>
+  __device__ __forceinline__ GatePair<V> enter(const GateArgs<E>& s, const GateSpot<V>& at, int t,
+                                               int slot, int t1, int n,
+                                               const GateInputs<E, V, I, Z>& in,
+                                               const GateBias<V>& bias) {
     float h[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) h[j] = nbefore[j];
-    if constexpr (decltype(next)::value) fetch(std::true_type(), t - window);
-    const int n = steps - t - slot;  // the slot's steps that hold text
-    Gate a[kGateStep][V], in[kGateStep][V];
-    float before[kGateStep][V], y[kGateStep][V], c[V];
-    GatePair<V> mine;
+    for (int j = 0; j < V; ++j) h[j] = in.before[j];
     GateRows<E> gz(s.gz, t, at.b, at.c0);
-    const uint32_t own = (uint32_t)at.cl * (uint32_t)sizeof(E);
-    const uint32_t oz = gate_offset((uint32_t)slot * gz.step + own);
+    const uint32_t oz =
+        gate_offset((uint32_t)slot * gz.step + (uint32_t)at.cl * (uint32_t)sizeof(E));
 #pragma unroll
     for (int k = 0; k < kGateStep; ++k, gz.next()) {
       float vz[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        Gate g = gate_hw(fb[j] - f.get(k, j));
+        Gate g = gate_hw(bias.f[j] - in.f.get(k, j));
         if (!WHOLE && k >= n) g = kGateKeep;
         a[k][j] = g;
-        if constexpr (!SUM) {
-          float take = g.rest();
-          if constexpr (I) {
-            in[k][j] = gate_hw(ib[j] - i.get(k, j));
-            take = in[k][j].value();
-          }
-          take *= x.get(k, j);
-          if (!WHOLE && k >= n) take = 0.0f;
-          before[k][j] = h[j];
-          h[j] = g.times(h[j], take);
+        float take = g.rest();
+        if constexpr (I) {
+          own[k][j] = gate_hw(bias.i[j] - in.i.get(k, j));
+          take = own[k][j].value();
         }
-        float v = go.get(k, j);
+        take *= in.x.get(k, j);
+        if (!WHOLE && k >= n) take = 0.0f;
+        before[k][j] = h[j];
+        h[j] = g.times(h[j], take);
+        float v = in.go.get(k, j);
         if constexpr (Z) {
-          const Silu gate = silu_hw(z.get(k, j));
-          if constexpr (!SUM) vz[j] = !WHOLE && k >= n ? 0.0f : v * h[j] * gate.slope;
+          const Silu gate = silu_hw(in.z.get(k, j));
+          vz[j] = !WHOLE && k >= n ? 0.0f : v * h[j] * gate.slope;
           v *= gate.value;
         }
         y[k][j] = !WHOLE && k >= n ? 0.0f : v;
       }
-      if constexpr (Z && !SUM)
+      if constexpr (Z)
         if (WHOLE || t + slot + k < t1) pack_store<true, E, V>(gz.at(oz), vz, V);
     }
+    GatePair<V> mine;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       mine.p[j] = 1.0f;
@@ -146,12 +113,19 @@ __global__ __launch_bounds__(64 * kGateBwdWaves) void gate_bwd(const GateArgs<E>
         mine.p[j] = a[k][j].times(mine.p[j], 0.0f);
       }
     }
-    gate_fold<true>(meet, turn, at, mine, c);
-    if constexpr (SUM) return;
+    return mine;
+  }
+
+  // c: a H of the step behind the slot.
+  template <bool WHOLE>
+  __device__ __forceinline__ void leave(const GateArgs<E>& s, const GateSpot<V>& at, int t, int slot,
+                                        int t1, int n, const GateTile<E, V>& x, GateBias<V>& bias,
+                                        float (&c)[V]) {
     const GateRows<E> gx(s.gx, t, at.b, at.c0), gf(s.gf, t, at.b, at.c0), gi(s.gi, t, at.b, at.c0);
-    const uint32_t ox = gate_offset((uint32_t)slot * gx.step + own),
-                   of = gate_offset((uint32_t)slot * gf.step + own),
-                   oi = I ? gate_offset((uint32_t)slot * gi.step + own) : 0;
+    const uint32_t lane = (uint32_t)at.cl * (uint32_t)sizeof(E);
+    const uint32_t ox = gate_offset((uint32_t)slot * gx.step + lane),
+                   of = gate_offset((uint32_t)slot * gf.step + lane),
+                   oi = I ? gate_offset((uint32_t)slot * gi.step + lane) : 0;
 #pragma unroll
     for (int k = kGateStep - 1; k >= 0; --k) {
       float vx[V], vf[V], vi[V];
@@ -161,16 +135,16 @@ __global__ __launch_bounds__(64 * kGateBwdWaves) void gate_bwd(const GateArgs<E>
         const bool runs = WHOLE || k < n;
         float take, from = before[k][j];
         if constexpr (I) {
-          take = in[k][j].value();
-          vi[j] = runs ? gh * xv * in[k][j].slope() : 0.0f;
-          sum_i[j] += vi[j];
+          take = own[k][j].value();
+          vi[j] = runs ? gh * xv * own[k][j].slope() : 0.0f;
+          bias.sum_i[j] += vi[j];
         } else {
           take = a[k][j].rest();
           from -= xv;
         }
         vx[j] = runs ? take * gh : 0.0f;
         vf[j] = runs ? gh * from * a[k][j].slope() : 0.0f;
-        sum_f[j] += vf[j];
+        bias.sum_f[j] += vf[j];
         c[j] = a[k][j].times(gh, 0.0f);
       }
       if (WHOLE || t + slot + k < t1) {
@@ -182,48 +156,139 @@ __global__ __launch_bounds__(64 * kGateBwdWaves) void gate_bwd(const GateArgs<E>
         if constexpr (I) pack_store<true, E, V>(row(gi, oi), vi, V);
       }
     }
-  };
-  constexpr std::true_type yes;
-  constexpr std::false_type no;
-  // (only the first window, the row's last, can be short of text)
-  if (t > t0 && t + window > steps) {
-    work(no, yes);
-    t -= window;
-    turn ^= 1;
   }
-  for (; t > t0; t -= window, turn ^= 1) work(yes, yes);
-  if (t == t0) {
-    if (t + window <= steps) work(yes, no);
-    else work(no, no);
-    turn ^= 1;
+};
+
+// Zeros in a window behind the text.
+template <typename E, int V, bool I, bool Z>
+__device__ __forceinline__ void gate_blank(const GateArgs<E>& s, const GateSpot<V>& at, int t,
+                                           int slot, int t1) {
+  const GateRows<E> gx(s.gx, t, at.b, at.c0), gf(s.gf, t, at.b, at.c0), gi(s.gi, t, at.b, at.c0),
+      gz(s.gz, t, at.b, at.c0);
+  const float none[V] = {};
+  const uint32_t lane = (uint32_t)at.cl * (uint32_t)sizeof(E);
+#pragma unroll 1
+  for (uint32_t k = slot; k < (uint32_t)slot + kGateStep && t + (int)k < t1; ++k) {
+    pack_store<true, E, V>(gx.at(k * gx.step + lane), none, V);
+    pack_store<true, E, V>(gf.at(k * gf.step + lane), none, V);
+    if constexpr (I) pack_store<true, E, V>(gi.at(k * gi.step + lane), none, V);
+    if constexpr (Z) pack_store<true, E, V>(gz.at(k * gz.step + lane), none, V);
   }
-  if constexpr (!SUM)
-    if (s.part) {
+}
+
+// A workgroup's part of the bias gradients: its slots' sums in their order, one channel
+// and gate a thread.  (All threads call it.)
+template <int V, typename A>
+__device__ __forceinline__ void gate_part(const A& s, const GateSpot<V>& at,
+                                          float (*lds)[2 * V][kGateLanes], const GateBias<V>& bias,
+                                          int64_t row) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        bias[slot / kGateStep][j][at.lane] = sum_f[j];
-        bias[slot / kGateStep][V + j][at.lane] = sum_i[j];
-      }
-    }
-  __syncthreads();
-  if (threadIdx.x < kGateLanes) {
-    const GatePair<V> c = meet.carry[turn][at.lane];
-    if constexpr (SUM) gate_sum_store<V>(s, at, c);
-    else if (s.gstate0 && at.chunk == 0) pack_store<true, float, V>(s.gstate0 + col, c.h, V);
+  for (int j = 0; j < V; ++j) {
+    lds[2 * at.wave + at.upper][j][at.lane] = bias.sum_f[j];
+    lds[2 * at.wave + at.upper][V + j][at.lane] = bias.sum_i[j];
   }
-  if constexpr (SUM) return;
-  if (!s.part) return;
-  // the slots' sums, one channel and gate a thread
-  float* part = s.part + ((int64_t)at.chunk * s.B + at.b) * 2 * s.D;
+  __syncthreads();
+  float* part = s.part + row * 2 * s.D;
   for (int o = threadIdx.x; o < 2 * V * kGateLanes; o += blockDim.x) {
     const int lane = o % kGateLanes, j = o / kGateLanes % V, gate = o / kGateLanes / V;
     float sum = 0.0f;
-    for (int k = 0; k < 2 * at.waves; ++k) sum += bias[k][gate * V + j][lane];
+    for (int k = 0; k < 2 * at.waves; ++k) sum += lds[k][gate * V + j][lane];
     // (a lane's channels begin earlier where they pass the row's end)
     const int64_t want = ((int64_t)at.group * kGateLanes + lane) * V;
     const int64_t ch = min(want, (int64_t)s.D - V) + j;
     if (want < s.D && ch >= want) part[(int64_t)gate * s.D + ch] = sum;
   }
+}
+
+// All windows of a column, from the last to the first.
+template <typename E, int V, bool I, bool Z>
+__global__ __launch_bounds__(64 * kGateWaves) void gate_bwd(const GateArgs<E> s) {
+  __shared__ GateMeet<V, kGateWaves> meet;
+  __shared__ float sums[2 * kGateWaves][2 * V][kGateLanes];
+  GateSpot<V> at;
+  const int64_t id = seq_block();
+  if (id > INT_MAX || !at.at(s, (uint32_t)id)) return;
+  const int window = 2 * at.waves * kGateStep, steps = at.len;
+  const int slot = (2 * at.wave + at.upper) * kGateStep;  // its first step in a window
+  const int64_t col = (int64_t)at.b * s.D + at.c;
+  int t = s.T > 0 ? (s.T - 1) / window * window : -window;
+  for (; t >= 0 && t >= steps; t -= window) gate_blank<E, V, I, Z>(s, at, t, slot, s.T);
+  GateInputs<E, V, I, Z> in, next;
+  if (t >= 0) next.template load<false>(s, at, t, slot, steps - 1 - t);
+  GateBias<V> bias(s, at, I);
+  if (threadIdx.x < kGateLanes)
+#pragma unroll
+    for (int j = 0; j < V; ++j) meet.carry[0][at.lane][j] = s.gstate ? s.gstate[col + j] : 0.0f;
+  int turn = 0;
+  // WHOLE: every slot's steps hold text.  NEXT: another window follows (full of text), and
+  // is on its way while this one is worked on.
+  auto work = [&](auto whole, auto follows) {
+    constexpr bool WHOLE = decltype(whole)::value;
+    in = next;
+    if constexpr (decltype(follows)::value)
+      next.template load<true>(s, at, t - window, slot, 0);
+    const int n = steps - t - slot;  // the slot's steps that hold text
+    GateBackward<E, V, I, Z> way;
+    float c[V];
+    const GatePair<V> mine = way.template enter<WHOLE>(s, at, t, slot, s.T, n, in, bias);
+    gate_fold<true>(meet, turn, at, mine, c);
+    way.template leave<WHOLE>(s, at, t, slot, s.T, n, in.x, bias, c);
+    t -= window;
+    turn ^= 1;
+  };
+  constexpr std::true_type yes;
+  constexpr std::false_type no;
+  // (only the first window, the row's last, can be short of text)
+  if (t > 0 && t + window > steps) work(no, yes);
+  while (t > 0) work(yes, yes);
+  if (t == 0) {
+    if (window <= steps) work(yes, no);
+    else work(no, no);
+  }
+  __syncthreads();
+  if (threadIdx.x < kGateLanes && s.gstate0)
+    pack_store<true, float, V>(s.gstate0 + col, meet.carry[turn][at.lane], V);
+  if (s.part) gate_part<V>(s, at, sums, bias, at.b);
+}
+
+// A window of a column a workgroup.
+template <typename E, int V, bool I, bool Z>
+__global__ __launch_bounds__(64 * kGateWaves) void gate_bwd_chain(const GateArgs<E> s) {
+  __shared__ GateChain<V> chain;
+  __shared__ float sums[2 * kGateWaves][2 * V][kGateLanes];
+  GateSpot<V> at;
+  int behind;  // windows behind this one
+  if (!gate_number(chain, s, at, &behind)) return;
+  const int index = s.windows - 1 - behind;
+  const int window = 2 * at.waves * kGateStep, t = index * window, t1 = min(t + window, s.T);
+  const int slot = (2 * at.wave + at.upper) * kGateStep;
+  const int64_t col = (int64_t)at.b * s.D + at.c;
+  GateBias<V> bias(s, at, I);
+  if (t >= at.len) {  // behind the text; a row without any hands its adjoint on
+    gate_blank<E, V, I, Z>(s, at, t, slot, t1);
+    if (t == 0 && s.gstate0 && threadIdx.x < kGateLanes)
+#pragma unroll
+      for (int j = 0; j < V; ++j) s.gstate0[col + j] = s.gstate ? s.gstate[col + j] : 0.0f;
+  } else {
+    auto work = [&](auto whole) {  // whether every slot's steps hold text
+      constexpr bool WHOLE = decltype(whole)::value;
+      const int n = at.len - t - slot;
+      GateInputs<E, V, I, Z> in;
+      in.template load<WHOLE>(s, at, t, slot, at.len - 1 - t);
+      GateBackward<E, V, I, Z> way;
+      float c[V];
+      const GatePair<V> mine = way.template enter<WHOLE>(s, at, t, slot, t1, n, in, bias);
+      const int number = (at.len - 1) / window - index;
+      const GatePair<V> before =
+          gate_chain<true>(chain, s, at, number, index == 0, s.gstate, mine, c);
+      if (index == 0 && s.gstate0 && at.wave == 0 && !at.upper)
+        pack_store<true, float, V>(s.gstate0 + col, before.h, V);
+      way.template leave<WHOLE>(s, at, t, slot, t1, n, in.x, bias, c);
+    };
+    if (t + window <= at.len) work(std::true_type());
+    else work(std::false_type());
+  }
+  if (s.part) gate_part<V>(s, at, sums, bias, (int64_t)index * s.B + at.b);
 }
 
 // g_f_bias and g_i_bias: the workgroups' sums, in their order.  A wave an output's 64
@@ -245,24 +310,23 @@ __global__ __launch_bounds__(kBiasCols * kBiasRows) void gate_bias_sum(
   if (to) to[o < D ? o : o - D] = sum;
 }
 
+template <typename E, int V, bool I, bool Z>
+void gate_start(const GateArgs<E>& a, const GatePlan& p, hipStream_t stream) {
+  const dim3 grid = seq_grid((int64_t)p.groups * a.B * p.windows);
+  if (p.windows > 1) gate_bwd_chain<E, V, I, Z><<<grid, 64 * p.waves, 0, stream>>>(a);
+  else gate_bwd<E, V, I, Z><<<grid, 64 * p.waves, 0, stream>>>(a);
+}
+
 template <typename E, int V>
 ck_status gate_launch(const GateArgs<E>& a, const GatePlan& p, float* g_f, float* g_i,
                       hipStream_t stream) {
-  const int threads = 64 * p.waves;
-  const int64_t cols = (int64_t)p.groups * a.B;
-  if (p.chunks > 1) {
-    const dim3 grid = seq_grid(cols * (p.chunks - 1));
-    if (a.z.p) gate_bwd<E, V, false, true, true><<<grid, threads, 0, stream>>>(a);
-    else gate_bwd<E, V, false, false, true><<<grid, threads, 0, stream>>>(a);
-  }
-  const dim3 grid = seq_grid(cols * p.chunks);
-  if (a.i.p && a.z.p) gate_bwd<E, V, true, true, false><<<grid, threads, 0, stream>>>(a);
-  else if (a.i.p) gate_bwd<E, V, true, false, false><<<grid, threads, 0, stream>>>(a);
-  else if (a.z.p) gate_bwd<E, V, false, true, false><<<grid, threads, 0, stream>>>(a);
-  else gate_bwd<E, V, false, false, false><<<grid, threads, 0, stream>>>(a);
+  if (a.i.p && a.z.p) gate_start<E, V, true, true>(a, p, stream);
+  else if (a.i.p) gate_start<E, V, true, false>(a, p, stream);
+  else if (a.z.p) gate_start<E, V, false, true>(a, p, stream);
+  else gate_start<E, V, false, false>(a, p, stream);
   if (a.part)
     gate_bias_sum<<<seq_grid((2 * (int64_t)a.D + kBiasCols - 1) / kBiasCols), kBiasCols * kBiasRows,
-                    0, stream>>>(a.part, a.D, (int64_t)a.B * p.chunks, g_f, g_i);
+                    0, stream>>>(a.part, a.D, (int64_t)a.B * p.windows, g_f, g_i);
   CK_HIP_TRY(hipGetLastError());
   return CK_OK;
 }
