@@ -8,8 +8,15 @@
 namespace ckhip {
 namespace {
 
-// Below as many columns every window is a workgroup of its own.
-constexpr int64_t kGateColumns = 256;
+// A workgroup of the loop over windows fills a CU, so that columns are worked on in
+// rounds of one a CU.  Where they fill them, the loop is the faster one (2048 steps of 256
+// columns, bf16: forward 83 us against 88 as a chain, backward 140 against 176), where
+// they do not, the chain (288 columns: 134 against 98 and 232 against 199; 32 columns: 82
+// against 19 and 140 against 30).  The forward's chain, two workgroups a CU, wins from the
+// second round on (1024 columns of 256 steps: 55 against 45), the backward's, one a CU,
+// where a round in four is lost.
+constexpr int64_t kGateCus = 256;
+constexpr int64_t kGateColumns = 4096;  // of a chain, at most: each has a ticket
 
 ck_status gate_check_shape(const ck_gated_shape* s) {
   if (!s) {
@@ -20,7 +27,7 @@ ck_status gate_check_shape(const ck_gated_shape* s) {
 }
 
 // How a call with these step strides (bytes; 0: any) is spread over the chip.
-GatePlan gate_plan(const ck_gated_shape& s, int64_t step) {
+GatePlan gate_plan(const ck_gated_shape& s, int64_t step, bool backward) {
   GatePlan p;
   p.v = s.dtype == CK_F32 || s.D < 2 ? 1 : 2;
   const int64_t groups = (s.D + kGateLanes * p.v - 1) / (kGateLanes * p.v);
@@ -32,7 +39,11 @@ GatePlan gate_plan(const ck_gated_shape& s, int64_t step) {
   p.waves = (int)std::max<int64_t>(1, std::min({(int64_t)kGateWaves, pairs, reach}));
   p.windows = 1;
   const int64_t windows = (pairs + kGateWaves - 1) / kGateWaves;
-  if (cols < kGateColumns && windows > 1 && p.waves == kGateWaves && windows * cols < INT_MAX)
+  const int64_t rounds = (cols + kGateCus - 1) / kGateCus;
+  const bool full = backward ? 4 * cols >= 3 * kGateCus * rounds
+                             : rounds == 1 && 20 * cols >= 19 * kGateCus;
+  if (!full && cols <= kGateColumns && windows > 1 && p.waves == kGateWaves &&
+      windows * cols < INT_MAX)
     p.windows = (int)windows;
   return p;
 }
@@ -50,10 +61,12 @@ struct GateWs {
   size_t pairs, states, part, total;
 };
 GateWs gate_ws(const ck_gated_shape& s, bool backward) {
-  const int64_t windows = gate_plan(s, 0).windows;
+  const GatePlan p = gate_plan(s, 0, backward);
+  const int64_t windows = p.windows;
   const int64_t col = s.B * s.D, runs = windows / kGateRun;
   GateWs w;
-  w.pairs = windows > 1 ? kGateColumns * kGateTicket * sizeof(uint32_t) : 0;
+  w.pairs = windows > 1 ? (size_t)p.groups * s.B * kGateTicket * sizeof(uint32_t) : 0;
+  w.pairs = (w.pairs + 255) & ~size_t(255);
   w.states = w.pairs + (windows > 1 ? (size_t)windows * col * sizeof(uint64_t) : 0);
   w.part = (w.states + (windows > 1 ? (size_t)runs * col * sizeof(uint64_t) : 0) + 255) &
            ~size_t(255);
@@ -207,7 +220,7 @@ extern "C" ck_status ck_gated_forward(const ck_gated_shape* shape, const ck_gate
   if (rc == CK_OK) rc = gate_check_f32(state, "state");
   if (rc != CK_OK) return rc;
   const GatePlan p =
-      gate_plan(*shape, gate_step(shape->dtype, {&in->x, &in->f, &in->i, &in->z, &out}));
+      gate_plan(*shape, gate_step(shape->dtype, {&in->x, &in->f, &in->i, &in->z, &out}), false);
   const GateWs ws = gate_ws(*shape, false);
   rc = seq_check_ws(workspace, workspace_bytes, ws.total);
   if (rc == CK_OK && saved) rc = check_aligned(saved, "saved");
@@ -248,7 +261,7 @@ extern "C" ck_status ck_gated_backward(const ck_gated_shape* shape, const ck_gat
   if (rc != CK_OK) return rc;
   const GatePlan p = gate_plan(
       *shape, gate_step(shape->dtype, {&in->x, &in->f, &in->i, &in->z, &grad_out, &grads->x,
-                                       &grads->f, &grads->i, &grads->z}));
+                                       &grads->f, &grads->i, &grads->z}), true);
   const GateWs ws = gate_ws(*shape, true);
   rc = seq_check_ws(workspace, workspace_bytes, ws.total);
   if (rc != CK_OK) return rc;

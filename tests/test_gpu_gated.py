@@ -114,7 +114,11 @@ CASES = [  # T, B, D, dtype, own input gate, output gate, lengths, layout
     (257, 3, 70, "fp16", True, False, [257, 256, 255], "time"),
     (300, 4, 3, "bf16", False, False, [-1, 301, 300, 8], "slice"),
 ]
-CUT = [  # few rows: the steps are cut into chunks
+CUT = [  # few rows: every window of 128 steps is a workgroup, runs of eight windows
+    (129, 1, 64, "fp32", True, True, [129], "time"),
+    (1024, 5, 33, "fp16", False, False, [1024, 1023, 897, 896, 128], "time"),
+    (1025, 4, 64, "bf16", True, False, [1025, 1024, 0, 129], "slice"),
+    (2200, 5, 31, "fp32", True, True, [2200, 2049, 2048, 2047, 1], "batch"),
     (513, 1, 64, "bf16", True, True, None, "time"),
     (1000, 1, 63, "fp32", True, True, None, "slice"),
     (1025, 2, 65, "fp16", False, True, [1025, 511], "batch"),
@@ -133,8 +137,19 @@ def test_scan(case):
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_many_columns(dtype):
-    """Rows and channels fill the chip: workgroups of fewer waves, several windows each."""
+    """More columns than CUs."""
     check(*problem(2, 150, 40, 1030, dtype, True, True, None, "batch"))
+
+
+LENS = [900, 0, 1, 127, 128, 129, 255, 256, 257, 383, 384, 385, 511, 512, 513, 640] * 2
+
+
+@pytest.mark.parametrize("own,z", [(True, True), (False, False)])
+@pytest.mark.parametrize("lengths", [None, LENS])
+def test_a_column_a_cu(own, z, lengths):
+    """As many columns as CUs: workgroups that go through all windows of one."""
+    check(*problem(20, 900, 32, 256, "fp32", own, z, lengths, "time"))
+    check(*problem(21, 300, 8, 2048, "bf16", own, z, lengths and lengths[:8], "slice"))
 
 
 @pytest.mark.parametrize("own", [True, False])
@@ -314,6 +329,33 @@ def test_same_bits_every_time_and_on_another_stream():
         torch.cuda.current_stream().wait_stream(side)
         for a, b in zip((*first[:2], *first[2].values()), (*got[:2], *got[2].values())):
             assert torch.equal(a, b)
+
+
+def test_calls_side_by_side():
+    """Windows wait for one another within their call alone: several calls at once, with
+    other work, come to the bits of one after the other; the workspace may hold anything."""
+    probs = [problem(22 + k, 1500 + 100 * k, 2, 500, "bf16", True, True, None, "time")[0]
+             for k in range(3)]
+    want = [run(g) for g in probs]
+    streams = [torch.cuda.Stream() for _ in probs]
+    ws = [torch.randint(0, 256, (8 << 20,), dtype=torch.uint8, device="cuda") for _ in probs]
+    busy = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    got = [[] for _ in probs]
+    for _ in range(5):
+        for k, (g, st) in enumerate(zip(probs, streams)):
+            kw = dict(i=g["i"], z=g["z"], f_bias=g["f_bias"], i_bias=g["i_bias"],
+                      workspace=ws[k], stream=st)
+            out, state, saved, _ = sgr.gated_scan_forward(g["x"], g["f"], state0=g["state0"], **kw)
+            grads = sgr.gated_scan_backward(g["x"], g["f"], saved, g["go"],
+                                            grad_state=g["gstate"], **kw)
+            got[k].append((out, state, *grads.values()))
+        busy = busy @ busy * 1e-3
+    torch.cuda.synchronize()
+    for w, rounds in zip(want, got):
+        w = (w[0], w[1], *w[2].values())
+        for res in rounds:
+            assert all(map(torch.equal, w, res))
 
 
 @pytest.mark.parametrize("T,stride", [(40, (1 << 26) - 1), (1000, (1 << 21) + 3)])
