@@ -269,30 +269,40 @@ __global__ __launch_bounds__(64 * kBeamWaves) void beam_part(const BeamArgs<E> s
 }
 
 // Takes the K best of `n` keys, no two alike but 0, in order: of the lane's, K times
-// the best of the wave.  Written to list[0 .. K).
-template <int kBeamHold>  // keys a lane holds at a time
-__device__ __forceinline__ void beam_take(const uint64_t* keys, int64_t n, int K, int lane,
-                                          uint64_t* list) {
-  uint64_t kept = 0;  // lane i: the i-th best so far
-  for (int64_t base = 0; base < n; base += 64 * kBeamHold) {
-    uint64_t hold[kBeamHold], next = 0;
+// the best of the wave.  Written to list[0 .. K).  `hold`: the first HOLD keys of the
+// lane, loaded.
+template <int HOLD>
+struct BeamHold {
+  uint64_t key[HOLD];
+  __device__ __forceinline__ void load(const uint64_t* keys, int64_t n, int64_t base, int lane) {
 #pragma unroll
-    for (int e = 0; e < kBeamHold; ++e) {
+    for (int e = 0; e < HOLD; ++e) {
       const int64_t i = base + e * 64 + lane;
-      hold[e] = i < n ? keys[i] : 0;
+      key[e] = i < n ? keys[i] : 0;
     }
+  }
+};
+template <int HOLD>
+__device__ __forceinline__ void beam_take(BeamHold<HOLD> hold, const uint64_t* keys, int64_t n,
+                                          int K, int lane, uint64_t* list) {
+  uint64_t kept = 0;  // lane i: the i-th best so far
+  for (int64_t base = 0;;) {
+    uint64_t next = 0;
     for (int k = 0; k < K; ++k) {
       uint64_t best = kept;
 #pragma unroll
-      for (int e = 0; e < kBeamHold; ++e) best = hold[e] > best ? hold[e] : best;
+      for (int e = 0; e < HOLD; ++e) best = hold.key[e] > best ? hold.key[e] : best;
       best = wave_max(best);
+      if (best == 0) break;
       if (lane == k) next = best;
-      if (best == 0) continue;
       if (kept == best) kept = 0;
 #pragma unroll
-      for (int e = 0; e < kBeamHold; ++e) hold[e] = hold[e] == best ? 0 : hold[e];
+      for (int e = 0; e < HOLD; ++e) hold.key[e] = hold.key[e] == best ? 0 : hold.key[e];
     }
     kept = next;
+    base += 64 * HOLD;
+    if (base >= n) break;
+    hold.load(keys, n, base, lane);
   }
   if (lane < K) list[lane] = kept;
 }
@@ -307,8 +317,15 @@ __global__ __launch_bounds__(64 * kBeamJoinWaves) void beam_join(const BeamArgs<
   if (text >= s.B) return;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int waves = (int)blockDim.x >> 6, lane = threadIdx.x & 63, K = s.K;
+  const int64_t keys = (int64_t)s.parts * K;
   for (int k = wave; k < K; k += waves) {
     const int64_t row = text * K + k;
+    // (what a row that is skipped left there is not used: all loads set out together)
+    const uint64_t* from = s.best + row * keys;
+    BeamHold<2> hold;
+    hold.load(from, keys, 0, lane);
+    const float2* sums = s.sums + row * s.parts;
+    const float2 one = lane < s.parts ? sums[lane] : make_float2(-__builtin_inff(), 0.0f);
     if (beam_skips(s, row)) {
       // (the end token first, if there is one to go on with, then the others: no score)
       if (lane < K) {
@@ -321,26 +338,29 @@ __global__ __launch_bounds__(64 * kBeamJoinWaves) void beam_join(const BeamArgs<
       if (lane == 0) tops[k] = logs[k] = 0.0;
       continue;
     }
-    const float2* sums = s.sums + row * s.parts;
-    float most = -__builtin_inff();
-    for (int p = lane; p < s.parts; p += 64) most = fmaxf(most, sums[p].x);
+    float most = one.x;
+    for (int p = lane + 64; p < s.parts; p += 64) most = fmaxf(most, sums[p].x);
     most = wave_max(most);
     double sum = 0.0;
-    if (most > -__builtin_inff())
-      for (int p = lane; p < s.parts; p += 64)
+    if (most > -__builtin_inff()) {
+      if (one.x > -__builtin_inff()) sum = (double)one.y * exp((double)one.x - (double)most);
+      for (int p = lane + 64; p < s.parts; p += 64)
         if (sums[p].x > -__builtin_inff())
           sum += (double)sums[p].y * exp((double)sums[p].x - (double)most);
+    }
 #pragma unroll
     for (int m = 32; m; m >>= 1) sum += __shfl_xor(sum, m);
     if (lane == 0) {
       tops[k] = (double)most;
       logs[k] = sum > 0.0 ? log(sum) : 0.0;
     }
-    const int64_t keys = (int64_t)s.parts * K;
-    const uint64_t* best = s.best + row * keys;
-    if (keys <= 64) beam_take<1>(best, keys, K, lane, list[k]);
-    else if (keys <= 128) beam_take<2>(best, keys, K, lane, list[k]);
-    else beam_take<8>(best, keys, K, lane, list[k]);
+    if (keys <= 128) {
+      beam_take(hold, from, keys, K, lane, list[k]);
+    } else {
+      BeamHold<8> more;
+      more.load(from, keys, 0, lane);
+      beam_take(more, from, keys, K, lane, list[k]);
+    }
   }
   __syncthreads();
   if (wave != 0) return;

@@ -25,7 +25,7 @@ constexpr int kClipTable = 96;      // tensors a launch (the table is its argume
 constexpr int kClipAccess = 16;     // bytes a thread and access
 constexpr int kClipDeep = 8;        // accesses of a thread in a chunk, at most
 constexpr int kClipUnit = kClipThreads * kClipAccess;  // bytes of a chunk of one access a thread
-constexpr int kClipBlocks = 2048;   // of a launch: all run at once (8 waves a SIMD); as many
+constexpr int kClipBlocks = 1024;   // of a launch: all run at once (4 waves a SIMD); as many
                                     // partial sums
 
 struct ClipTable {
