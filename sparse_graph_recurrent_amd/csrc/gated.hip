@@ -48,11 +48,22 @@ GatePlan gate_plan(const ck_gated_shape& s, int64_t step, bool backward) {
   return p;
 }
 
-int64_t gate_step(int dtype, std::initializer_list<const ck_seq*> tensors) {
+using GateTensors = std::initializer_list<const ck_seq*>;
+int64_t gate_step(int dtype, GateTensors tensors) {
   int64_t step = 1;
   for (const ck_seq* q : tensors)
     if (q->data) step = std::max(step, q->stride_t * (int64_t)seq_elem_bytes(dtype));
   return step;
+}
+
+// Whether columns of the tensors begin off cache lines.
+int gate_split(const ck_gated_shape& s, GateTensors tensors) {
+  const uint64_t e = seq_elem_bytes(s.dtype);
+  uint64_t bits = s.D * e;
+  for (const ck_seq* q : tensors)
+    if (q->data)
+      bits |= reinterpret_cast<uintptr_t>(q->data) | (q->stride_t * e) | (q->stride_b * e);
+  return bits % 128 != 0;
 }
 
 // Workspace: a chain's tickets and words, then (backward) the bias gradients' parts.  (It
@@ -219,8 +230,8 @@ extern "C" ck_status ck_gated_forward(const ck_gated_shape* shape, const ck_gate
   if (rc == CK_OK) rc = gate_check_out(*shape, out, shape->T == 0, "out");
   if (rc == CK_OK) rc = gate_check_f32(state, "state");
   if (rc != CK_OK) return rc;
-  const GatePlan p =
-      gate_plan(*shape, gate_step(shape->dtype, {&in->x, &in->f, &in->i, &in->z, &out}), false);
+  const GateTensors tensors = {&in->x, &in->f, &in->i, &in->z, &out};
+  const GatePlan p = gate_plan(*shape, gate_step(shape->dtype, tensors), false);
   const GateWs ws = gate_ws(*shape, false);
   rc = seq_check_ws(workspace, workspace_bytes, ws.total);
   if (rc == CK_OK && saved) rc = check_aligned(saved, "saved");
@@ -231,6 +242,7 @@ extern "C" ck_status ck_gated_forward(const ck_gated_shape* shape, const ck_gate
     a.out = seq_of<E>(out);
     a.state = state;
     a.saved = static_cast<float*>(saved);
+    a.split = gate_split(*shape, tensors);
     gate_prepare(a, ws, stream);
     return gate_run_forward(a, p, stream);
   });
@@ -259,9 +271,9 @@ extern "C" ck_status ck_gated_backward(const ck_gated_shape* shape, const ck_gat
   if (rc == CK_OK) rc = gate_check_f32(grads->state0, "the gradient of state0");
   if (rc == CK_OK && saved) rc = check_aligned(saved, "saved");
   if (rc != CK_OK) return rc;
-  const GatePlan p = gate_plan(
-      *shape, gate_step(shape->dtype, {&in->x, &in->f, &in->i, &in->z, &grad_out, &grads->x,
-                                       &grads->f, &grads->i, &grads->z}), true);
+  const GateTensors tensors = {&in->x, &in->f, &in->i, &in->z, &grad_out,
+                               &grads->x, &grads->f, &grads->i, &grads->z};
+  const GatePlan p = gate_plan(*shape, gate_step(shape->dtype, tensors), true);
   const GateWs ws = gate_ws(*shape, true);
   rc = seq_check_ws(workspace, workspace_bytes, ws.total);
   if (rc != CK_OK) return rc;
@@ -278,6 +290,7 @@ extern "C" ck_status ck_gated_backward(const ck_gated_shape* shape, const ck_gat
     a.gstate0 = grads->state0;
     if (grads->f_bias || grads->i_bias)
       a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.part);
+    a.split = gate_split(*shape, tensors);
     gate_prepare(a, ws, stream);
     return gate_run_backward(a, p, grads->f_bias, grads->i_bias, stream);
   });

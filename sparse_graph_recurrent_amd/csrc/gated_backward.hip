@@ -206,8 +206,9 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd(const GateArgs<E> s)
   __shared__ GateMeet<V, kGateWaves> meet;
   __shared__ float sums[2 * kGateWaves][2 * V][kGateLanes];
   GateSpot<V> at;
-  const int64_t id = seq_block();
-  if (id > INT_MAX || !at.at(s, (uint32_t)id)) return;
+  const int64_t id = seq_block(), cols = (int64_t)s.groups * s.B;
+  if (id >= cols) return;
+  at.at(s, gate_column((uint32_t)id, (uint32_t)cols, s.split));
   const int window = 2 * at.waves * kGateStep, steps = at.len;
   const int slot = (2 * at.wave + at.upper) * kGateStep;  // its first step in a window
   const int64_t col = (int64_t)at.b * s.D + at.c;

@@ -114,8 +114,9 @@ template <typename E, int V, bool I, bool Z>
 __global__ __launch_bounds__(64 * kGateWaves) void gate_fwd(const GateArgs<E> s) {
   __shared__ GateMeet<V, kGateWaves> meet;
   GateSpot<V> at;
-  const int64_t id = seq_block();
-  if (id > INT_MAX || !at.at(s, (uint32_t)id)) return;
+  const int64_t id = seq_block(), cols = (int64_t)s.groups * s.B;
+  if (id >= cols) return;
+  at.at(s, gate_column((uint32_t)id, (uint32_t)cols, s.split));
   const int window = 2 * at.waves * kGateStep, steps = at.len;
   const int slot = (2 * at.wave + at.upper) * kGateStep;  // its first step in a window
   // A window's inputs are asked for two windows ahead, so that requests are under way
