@@ -535,6 +535,18 @@ bool move_overlaps(int64_t rows, int64_t row, int64_t segs, int64_t seg, int64_t
   return rows > 1 ? row < bytes : segs > 1 && seg < bytes;
 }
 
+// Whether a state's output lies over its input elsewhere than in place, as far as two
+// ranges without gaps show it.
+bool move_crosses(const ck_beam_state& s, int64_t rows) {
+  const int64_t row = s.segments * s.bytes, all = rows * row;
+  const auto dense = [&](int64_t of_row, int64_t of_segment) {
+    return (s.segments == 1 || of_segment == s.bytes) && (rows == 1 || of_row == row);
+  };
+  const uintptr_t in = reinterpret_cast<uintptr_t>(s.in), out = reinterpret_cast<uintptr_t>(s.out);
+  return in != out && dense(s.in_row, s.in_segment) && dense(s.out_row, s.out_segment) &&
+         in < out + all && out < in + all;
+}
+
 template <int K>
 void move_launch(MoveTable& t, hipStream_t stream) {
   // a thread holds at most 128 bytes: packs of 16, of 8 or of 4 for more rows
@@ -638,7 +650,7 @@ extern "C" ck_status ck_beam_reorder(const ck_beam_state* states, int64_t count,
     set_error("parents are not aligned to their element type");
     return CK_ERR_BAD_VALUE;
   }
-  const int64_t most = int64_t(1) << 40;  // bytes of a beam of all texts; of a row 2^32
+  const int64_t most = int64_t(1) << 39;  // bytes of a beam of all texts; of a row below 2^32
   for (int64_t i = 0; i < count; ++i) {
     const ck_beam_state& s = states[i];
     if (s.segments < 0 || s.bytes < 0) {
@@ -646,7 +658,7 @@ extern "C" ck_status ck_beam_reorder(const ck_beam_state* states, int64_t count,
       return CK_ERR_BAD_SIZE;
     }
     if (s.segments == 0 || s.bytes == 0) continue;
-    if (s.segments > (int64_t(1) << 32) / s.bytes || s.segments * s.bytes > most / B) {
+    if (s.segments > (int64_t)UINT32_MAX / s.bytes || s.segments * s.bytes > most / B) {
       set_error("state %lld is too large", (long long)i);
       return CK_ERR_TOO_LARGE;
     }
@@ -662,6 +674,10 @@ extern "C" ck_status ck_beam_reorder(const ck_beam_state* states, int64_t count,
     if (s.in == s.out && ((B * K > 1 && s.in_row != s.out_row) ||
                           (s.segments > 1 && s.in_segment != s.out_segment))) {
       set_error("state %lld: its output is the state itself with other strides", (long long)i);
+      return CK_ERR_BAD_VALUE;
+    }
+    if (move_crosses(s, B * K)) {
+      set_error("state %lld: its output lies over it", (long long)i);
       return CK_ERR_BAD_VALUE;
     }
     for (int64_t o = 0; o < i; ++o)

@@ -157,9 +157,8 @@ __device__ __forceinline__ void clip_write(const ClipTable& t, int i, int64_t ch
     float y[kClipElems<E>];
 #pragma unroll
     for (int k = 0; k < kClipElems<E>; ++k) {
-      const float g = clip_get<E>(c.v[u], k);
-      if constexpr (sizeof(E) == 4) y[k] = (float)((double)g * scale);
-      else y[k] = g * (float)scale;
+      // (in 64 bits: a factor may lie below the range of fp32 though no gradient does)
+      y[k] = (float)((double)clip_get<E>(c.v[u], k) * scale);
     }
     E* to = reinterpret_cast<E*>(p + at);
     if (at + kClipAccess <= n) pack_store<true, E, kClipElems<E>>(to, y, 0);
@@ -231,19 +230,25 @@ ck_status clip_check(const ck_clip_tensor* tensors, int64_t count, int64_t* most
       return CK_ERR_BAD_VALUE;
     }
     *most += t.n * (int64_t)e;
+    if (*most > (int64_t(1) << 60)) {
+      set_error("the tensors are too large");
+      return CK_ERR_TOO_LARGE;
+    }
   }
   return CK_OK;
 }
 
 // Whether what is written lies over something else that is written, or that is read
 // as another tensor.
-bool clip_overlaps(const ck_clip_tensor* tensors, int64_t count) {
+bool clip_overlaps(const ck_clip_tensor* tensors, int64_t count, const float* norm) {
   struct Range {
     uintptr_t from, to;
     bool written;
   };
   std::vector<Range> ranges;
-  ranges.reserve(2 * count);
+  ranges.reserve(2 * count + 1);
+  const uintptr_t n = reinterpret_cast<uintptr_t>(norm);
+  ranges.push_back({n, n + sizeof(float), true});
   for (int64_t i = 0; i < count; ++i) {
     const ck_clip_tensor& t = tensors[i];
     const size_t bytes = (size_t)t.n * seq_elem_bytes(t.dtype);
@@ -327,7 +332,7 @@ extern "C" ck_status ck_clip_grad_norm(const ck_clip_tensor* tensors, int64_t co
   rc = seq_check_ws(workspace, workspace_bytes, clip_workspace(count));
   if (rc != CK_OK) return rc;
   try {
-    if (clip_overlaps(tensors, count)) {
+    if (clip_overlaps(tensors, count, norm)) {
       set_error("a tensor that is written lies over another one");
       return CK_ERR_BAD_VALUE;
     }

@@ -91,6 +91,13 @@ ck_status gate_check_f32(const void* p, const char* what) {
   return CK_ERR_BAD_VALUE;
 }
 
+// (windows that wait for one another read the one while others have written the other)
+ck_status gate_check_apart(const void* read, const void* written, const char* what) {
+  if (!read || read != written) return CK_OK;
+  set_error("%s must not lie over what it is made from", what);
+  return CK_ERR_BAD_VALUE;
+}
+
 ck_status gate_check_out(const ck_gated_shape& s, const ck_seq& q, bool optional,
                          const char* what) {
   return seq_check_out(q, s.T, s.B, s.D, s.dtype, optional, what, kGateMaxStrideT);
@@ -229,6 +236,7 @@ extern "C" ck_status ck_gated_forward(const ck_gated_shape* shape, const ck_gate
   ck_status rc = gate_check_inputs(shape, in);
   if (rc == CK_OK) rc = gate_check_out(*shape, out, shape->T == 0, "out");
   if (rc == CK_OK) rc = gate_check_f32(state, "state");
+  if (rc == CK_OK) rc = gate_check_apart(in->state0, state, "state");
   if (rc != CK_OK) return rc;
   const GateTensors tensors = {&in->x, &in->f, &in->i, &in->z, &out};
   const GatePlan p = gate_plan(*shape, gate_step(shape->dtype, tensors), false);
@@ -269,6 +277,7 @@ extern "C" ck_status ck_gated_backward(const ck_gated_shape* shape, const ck_gat
   if (rc == CK_OK) rc = gate_check_f32(grads->f_bias, "the gradient of f_bias");
   if (rc == CK_OK) rc = gate_check_f32(grads->i_bias, "the gradient of i_bias");
   if (rc == CK_OK) rc = gate_check_f32(grads->state0, "the gradient of state0");
+  if (rc == CK_OK) rc = gate_check_apart(grad_state, grads->state0, "the gradient of state0");
   if (rc == CK_OK && saved) rc = check_aligned(saved, "saved");
   if (rc != CK_OK) return rc;
   const GateTensors tensors = {&in->x, &in->f, &in->i, &in->z, &grad_out,

@@ -773,6 +773,6 @@ def dropout(x, p: float, seed: int, offset: int = 0, residual=None, held: bool =
 
 __all__ = ["selective_scan", "selective_scan_sizes", "selective_scan_forward",
            "selective_scan_backward", "selective_scan_step", "gated_scan", "gated_scan_sizes",
-           "gated_scan_forward", "gated_scan_backward", "gated_scan_step", "short_conv", "short_conv_forward",
-           "short_conv_backward", "short_conv_step", "dropout", "dropout_forward",
+           "gated_scan_forward", "gated_scan_backward", "gated_scan_step", "short_conv",
+           "short_conv_forward", "short_conv_backward", "short_conv_step", "dropout", "dropout_forward",
            "dropout_backward"]

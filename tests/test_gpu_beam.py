@@ -288,6 +288,16 @@ def test_reorder(B, K, in_place):
         assert all(map(torch.equal, states, before))
 
 
+def test_reorder_every_number_of_beams():
+    for K in range(1, 33):
+        log(f"beam_reorder K={K}")
+        t = torch.arange(2 * K * 37, dtype=torch.int16, device="cuda").view(2 * K, 37)
+        parents = torch.stack([torch.arange(K - 1, -1, -1, device="cuda"),
+                               torch.arange(K, device="cuda") * 7 % K])
+        want = t[(parents + K * torch.arange(2, device="cuda")[:, None]).view(-1)].clone()
+        assert torch.equal(sgr.beam_reorder([t], parents)[0], want), K
+
+
 def test_reorder_many_states_bad_parents_and_other_streams():
     states = [torch.randn(6, k + 1, device="cuda") for k in range(70)]   # several tables
     parents = torch.tensor([[0, -5, 99], [2, 1, 1 << 40]], device="cuda")   # the nearer bound

@@ -2,8 +2,8 @@
 
 Tolerances: squares and their sum are in fp64 (n additions: n 2^-53, less than a
 2^-25 for every size here), the norm is rounded once to fp32, the factor c is fp64;
-fp32 outputs are rounded once, 16-bit ones after a product in fp32 with c rounded to
-it (2 2^-24 more)."""
+outputs are rounded once, 16-bit ones from a product that was rounded to fp32 (2^-24
+more)."""
 import numpy as np
 import pytest
 import torch
@@ -89,6 +89,14 @@ def test_values_whose_squares_leave_fp32():
         before = [t.clone() for t in grads]
         norm, outs = sgr.clip_grad_norm(grads, 0.25 * norm_of(before))
         check(grads, 0.25 * norm_of(before), norm, outs, before)
+
+
+def test_a_factor_below_the_range_of_fp32():
+    """c = 1e-7 / 8e37 or so has no bits left in fp32; what it gives has."""
+    grads = make(6, [64, 40], ["bf16", "fp32"], 1e37)
+    before = [t.clone() for t in grads]
+    norm, outs = sgr.clip_grad_norm(grads, 1e-7)
+    check(grads, 1e-7, norm, outs, before)
 
 
 def test_limits():

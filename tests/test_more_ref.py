@@ -185,6 +185,14 @@ def test_clip_refusals(L):
     assert call(ws=None) == NULL_ARG and call(wn=16) == WORKSPACE and call(ws=FAKE + 8) == BAD_VALUE
 
 
+def test_clip_refuses_a_norm_in_a_gradient_and_sums_past_64_bits(L):
+    for g, norm in (((FAKE, FAKE, 64, 0), FAKE + 252), ((FAKE, 2 * FAKE, 64, 0), FAKE),
+                    ((FAKE, None, 64, 0), FAKE), ((FAKE, 2 * FAKE, 64, 1), 2 * FAKE)):
+        assert L.ck_clip_grad_norm(_tensors(g), 1, 1.0, norm, FAKE * 16, 2**20, None) == BAD_VALUE
+    big = _tensors(*[(FAKE, None, 2**44, 0)] * 2**15)
+    assert L.ck_clip_grad_norm(big, 2**15, 1.0, FAKE * 8, FAKE * 16, 2**30, None) == TOO_LARGE
+
+
 @pytest.mark.parametrize("rows", [
     [(FAKE, FAKE, 64, 0), (FAKE, FAKE, 64, 0)],               # the same gradient twice
     [(FAKE, FAKE, 64, 0), (FAKE + 252, FAKE + 252, 64, 0)],   # their last and first element
@@ -260,6 +268,27 @@ def test_reorder_refusals(L):
     assert call(same, same) == BAD_VALUE
     assert call(ok, (3 * FAKE, 2 * FAKE, 1, 64, 64, 0, 64, 0)) == BAD_VALUE
     assert call(ok, (2 * FAKE, 3 * FAKE, 1, 64, 64, 0, 64, 0)) == BAD_VALUE
+
+
+def test_reorder_refuses_an_output_over_its_input(L):
+    call = lambda *row, B=2, K=4: L.ck_beam_reorder(_states(row), 1, FAKE, B, K, None)
+    # a row further, a byte before the end, pieces without gaps, and the other way round
+    for a, b in ((FAKE, FAKE + 64), (FAKE, FAKE + 511), (FAKE + 64, FAKE)):
+        assert call(a, b, 1, 64, 64, 0, 64, 0) == BAD_VALUE
+        assert call(a, b, 4, 16, 64, 16, 64, 16) == BAD_VALUE
+    assert call(FAKE, FAKE + 1, 1, 64, 0, 0, 0, 0, B=1, K=1) == BAD_VALUE
+    # a row of 2^32 bytes in pieces of one, which a 32-bit count of pieces would lose
+    assert call(FAKE, 2**50, 2**32, 1, 2**32, 1, 2**32, 1, B=1) == TOO_LARGE
+    assert call(FAKE, 2**50, 2**31, 2, 2**32, 2, 2**32, 2, B=1) == TOO_LARGE
+
+
+def test_gated_refuses_a_state_over_its_start(L):
+    ws = 2**40
+    assert L.ck_gated_forward(_shape(), _inputs(state0=FAKE), SEQ, FAKE, FAKE, FAKE, ws,
+                              None) == BAD_VALUE
+    assert L.ck_gated_backward(_shape(), _inputs(), FAKE, SEQ, FAKE, _grads(state0=FAKE), FAKE, ws,
+                               None) == BAD_VALUE
+    assert "must not lie over" in L.ck_last_error().decode()
 
 
 def test_a_call_of_no_states_returns(L):
