@@ -8,7 +8,7 @@
 // takes kBeamSpan adjacent logits of a row (so few rows still fill the chip) and
 // leaves their maximum, their sum of exponentials and their K best in order; a
 // workgroup a text joins these row by row and then takes K times the best head of
-// the K rows' lists.
+// the K rows' lists.  Rows of one part each are looked at and joined by one workgroup.
 //
 // The K best of a wave: the K-th largest of its lanes' maxima is a limit that at
 // least K logits reach and few more (fewer than K lanes lie above it).  Those above it
@@ -31,6 +31,7 @@ constexpr int kBeamPacks = 8;    // accesses of a wave
 constexpr int kBeamSpan = 64 * kBeamV * kBeamPacks;
 constexpr int kBeamWaves = 4;    // of a workgroup that reads logits
 constexpr int kBeamJoinWaves = 16;
+constexpr size_t kBeamWholeLds = 48 << 10;  // of a workgroup that does all of a text, at most
 
 // A logit and its place as one number that orders by value, then by the lower place;
 // 0: none.
@@ -107,7 +108,8 @@ struct BeamArgs {
 template <typename E>
 __device__ __forceinline__ bool beam_skips(const BeamArgs<E>& s, int64_t row) {
   const float score = s.scores[row];
-  return (s.finished && s.finished[row]) || !(score > -__builtin_inff());
+  const uint8_t done = s.finished ? s.finished[row] : 0;
+  return (done != 0) | !(score > -__builtin_inff());  // (both loads set out together)
 }
 
 // What a wave keeps in LDS, for K beams.
@@ -121,19 +123,82 @@ struct BeamLds {
               (size_t)((packs * (kBeamV + 1) + 3) & ~3) * sizeof(float)) {}
 };
 
+// A lane's logits, as they came: 16-bit ones in half the registers, so that all waves of
+// a call find room at once.
+typedef uint32_t BeamWords __attribute__((ext_vector_type(4), aligned(2)));
 template <typename E>
-__global__ __launch_bounds__(64 * kBeamWaves) void beam_part(const BeamArgs<E> s, int64_t waves) {
-  extern __shared__ __attribute__((aligned(16))) char beam_lds[];
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  const int64_t id = seq_block() * (blockDim.x >> 6) + wave;
-  if (id >= waves) return;
-  const uint32_t row = (uint32_t)id / (uint32_t)s.parts;  // (waves are below 2^31)
-  const int part = (int)((uint32_t)id - row * (uint32_t)s.parts);
+struct BeamLogits {
+  static constexpr int kParts = kBeamV * (int)sizeof(E) / 16;
+  BeamWords w[kBeamPacks][kParts];
+
+  // A wave's logits from p on, the first `there` of them, at this lane's places; -inf
+  // behind them.  (One branch for all: loads stay in flight together.)
+  __device__ __forceinline__ void load(const E* p, int there) {
+    if (there == kBeamSpan) {
+#pragma unroll
+      for (int j = 0; j < kBeamPacks; ++j)
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+          w[j][i] = reinterpret_cast<const BeamWords*>(p + j * 64 * kBeamV)[i];
+    } else {
+      const uint32_t none = sizeof(E) == 4 ? 0xFF800000u
+                            : std::is_same_v<E, bf16_t> ? 0xFF80FF80u : 0xFC00FC00u;
+      const int left = there - ((int)threadIdx.x & 63) * kBeamV;
+#pragma unroll
+      for (int j = 0; j < kBeamPacks; ++j) {
+        BeamWords t[kParts];
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) t[i] = BeamWords{none, none, none, none};
+        const E* at = p + j * 64 * kBeamV;
+        const int n = left - j * 64 * kBeamV;
+        if (n >= kBeamV) {
+#pragma unroll
+          for (int i = 0; i < kParts; ++i) t[i] = reinterpret_cast<const BeamWords*>(at)[i];
+        } else {
+#pragma unroll
+          for (int k = 0; k < kBeamV; ++k)
+            if (k < n) put(t, k, at[k]);
+        }
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) w[j][i] = t[i];
+      }
+    }
+    anew();
+  }
+  static __device__ __forceinline__ void put(BeamWords (&t)[kParts], int k, E x) {
+    if constexpr (sizeof(E) == 4) {
+      t[k / 4][k % 4] = bits((float)x);
+    } else {
+      const uint32_t was = t[0][k / 2], u = __builtin_bit_cast(uint16_t, x);
+      t[0][k / 2] = k & 1 ? (was & 0xFFFFu) | u << 16 : (was & 0xFFFF0000u) | u;
+    }
+  }
+  __device__ __forceinline__ float get(int j, int k) const {
+    if constexpr (sizeof(E) == 4) return value(w[j][k / 4][k % 4]);
+    else if constexpr (std::is_same_v<E, bf16_t>)
+      return value(k & 1 ? w[j][0][k / 2] & 0xFFFF0000u : w[j][0][k / 2] << 16);
+    else return (float)__builtin_bit_cast(E, (uint16_t)(w[j][0][k / 2] >> 16 * (k & 1)));
+  }
+  // A NaN counts as -inf, +inf as the largest finite value.
+  __device__ __forceinline__ float sane(int j, int k) const {
+    const float x = get(j, k);
+    return x != x ? -__builtin_inff() : fminf(x, FLT_MAX);
+  }
+  // Has the compiler convert again what follows, rather than keep it.
+  __device__ __forceinline__ void anew() {
+#pragma unroll
+    for (int j = 0; j < kBeamPacks; ++j)
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) asm("" : "+v"(w[j][i]));
+  }
+};
+
+// A wave's part of a row.
+template <typename E>
+__device__ __forceinline__ void beam_look(const BeamArgs<E>& s, uint32_t row, int part, char* lds) {
   if (beam_skips(s, row)) return;
-  const int K = s.K;
+  const int K = s.K, lane = threadIdx.x & 63;
   const BeamLds room(K);
-  char* lds = beam_lds + wave * room.bytes;
   float* hits = reinterpret_cast<float*>(lds);                       // [packs][kBeamV]
   uint64_t* above = reinterpret_cast<uint64_t*>(hits + room.packs * kBeamV);
   uint64_t* level = above + room.above;
@@ -143,42 +208,29 @@ __global__ __launch_bounds__(64 * kBeamWaves) void beam_part(const BeamArgs<E> s
   const E* p = s.x.row(text, row - text * (uint32_t)K);
   const int64_t base = (int64_t)part * kBeamSpan;
   const int there = (int)min((int64_t)kBeamSpan, s.V - base);  // logits of this part
-  float x[kBeamPacks][kBeamV];
-#pragma unroll
-  for (int j = 0; j < kBeamPacks; ++j) {
-    const int v = j * 64 * kBeamV + lane * kBeamV;
-    Pack<E, kBeamV> w;
-    if (v + kBeamV <= there) {
-      w = pack_load<true, E, kBeamV>(p + base + v, kBeamV);
-    } else {
-#pragma unroll
-      for (int k = 0; k < kBeamV; ++k) {
-        w.v[k] = (E)-__builtin_inff();
-        if (v + k < there) w.v[k] = p[base + v + k];
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kBeamV; ++k) x[j][k] = (float)w.v[k];
-  }
+  BeamLogits<E> x;
+  x.load(p + base + lane * kBeamV, there);
   float top[kBeamPacks], best, most, sum;
   auto look = [&](auto careful) {  // maxima and the sum
+    constexpr bool CAREFUL = decltype(careful)::value;
+    const auto get = [&](int j, int k) { return CAREFUL ? x.sane(j, k) : x.get(j, k); };
     best = -__builtin_inff();
 #pragma unroll
     for (int j = 0; j < kBeamPacks; ++j) {
-      top[j] = x[j][0];
+      top[j] = get(j, 0);
 #pragma unroll
-      for (int k = 1; k < kBeamV; ++k) top[j] = fmaxf(top[j], x[j][k]);
+      for (int k = 1; k < kBeamV; ++k) top[j] = fmaxf(top[j], get(j, k));
       best = fmaxf(best, top[j]);
     }
     most = wave_max(best);
-    constexpr bool CAREFUL = decltype(careful)::value;
+    x.anew();
     const float m = CAREFUL && most == -__builtin_inff() ? 0.0f : most, shift = m * kLog2e;
     sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < kBeamPacks; ++j)
 #pragma unroll
       for (int k = 0; k < kBeamV; ++k)
-        sum += exp2_hw(CAREFUL ? (x[j][k] - m) * kLog2e : fmaf(x[j][k], kLog2e, -shift));
+        sum += exp2_hw(CAREFUL ? (get(j, k) - m) * kLog2e : fmaf(get(j, k), kLog2e, -shift));
     sum = wave_sum(sum);
     // (what `shift` was rounded by is the same in every term)
     if constexpr (!CAREFUL) sum *= exp2_hw(-fmaf(m, kLog2e, -shift));
@@ -186,15 +238,12 @@ __global__ __launch_bounds__(64 * kBeamWaves) void beam_part(const BeamArgs<E> s
   look(std::false_type());
   // A NaN, +inf, no logit above -inf, or a maximum that times log2(e) is beyond range
   // makes the sum a NaN or infinite.  (None of the others does: each term is about 1 at
-  // most.)  A NaN counts as -inf, +inf as the largest finite value.
+  // most.)
   const bool odd = !(sum < __builtin_inff());
+  x.anew();
   if (odd) {
-#pragma unroll
-    for (int j = 0; j < kBeamPacks; ++j)
-#pragma unroll
-      for (int k = 0; k < kBeamV; ++k)
-        x[j][k] = x[j][k] != x[j][k] ? -__builtin_inff() : fminf(x[j][k], FLT_MAX);
     look(std::true_type());
+    x.anew();
   }
   if (lane == 0) s.sums[(int64_t)row * s.parts + part] = make_float2(most, sum);
 
@@ -233,7 +282,7 @@ __global__ __launch_bounds__(64 * kBeamWaves) void beam_part(const BeamArgs<E> s
 #pragma unroll
       for (int k = 0; k < kBeamV; k += 4)
         *reinterpret_cast<float4*>(hits + o * kBeamV + k) =
-            make_float4(x[j][k], x[j][k + 1], x[j][k + 2], x[j][k + 3]);
+            make_float4(x.sane(j, k), x.sane(j, k + 1), x.sane(j, k + 2), x.sane(j, k + 3));
     }
     packs += __popcll(mask);
     ties += __popcll(at_mask);
@@ -266,6 +315,18 @@ __global__ __launch_bounds__(64 * kBeamWaves) void beam_part(const BeamArgs<E> s
     if (rank < K) out[rank] = key;
   }
   for (int i = lane; i < K - n; i += 64) out[n + i] = i < at_border ? level[i] : 0;
+}
+
+extern __shared__ __attribute__((aligned(16))) char beam_lds[];
+
+template <typename E>
+__global__ __launch_bounds__(64 * kBeamWaves) void beam_part(const BeamArgs<E> s, int64_t waves) {
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int64_t id = seq_block() * (blockDim.x >> 6) + wave;
+  if (id >= waves) return;
+  const uint32_t row = (uint32_t)id / (uint32_t)s.parts;  // (waves are below 2^31)
+  beam_look(s, row, (int)((uint32_t)id - row * (uint32_t)s.parts),
+            beam_lds + wave * BeamLds(s.K).bytes);
 }
 
 // Takes the K best of `n` keys, no two alike but 0, in order: of the lane's, K times
@@ -307,14 +368,13 @@ __device__ __forceinline__ void beam_take(BeamHold<HOLD> hold, const uint64_t* k
   if (lane < K) list[lane] = kept;
 }
 
+// Joins a text's rows.  (All waves of the workgroup call it.)
 template <typename E>
-__global__ __launch_bounds__(64 * kBeamJoinWaves) void beam_join(const BeamArgs<E> s) {
+__device__ __forceinline__ void beam_merge(const BeamArgs<E>& s, int64_t text) {
   __shared__ uint64_t list[kBeamMaxK][kBeamMaxK];
   // a row's maximum, and the logarithm of its sum relative to that (their sum would
   // lose the one in the other where logits are large)
   __shared__ double tops[kBeamMaxK], logs[kBeamMaxK];
-  const int64_t text = seq_block();
-  if (text >= s.B) return;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int waves = (int)blockDim.x >> 6, lane = threadIdx.x & 63, K = s.K;
   const int64_t keys = (int64_t)s.parts * K;
@@ -354,7 +414,9 @@ __global__ __launch_bounds__(64 * kBeamJoinWaves) void beam_join(const BeamArgs<
       tops[k] = (double)most;
       logs[k] = sum > 0.0 ? log(sum) : 0.0;
     }
-    if (keys <= 128) {
+    if (s.parts == 1) {  // (in order already)
+      if (lane < K) list[k][lane] = hold.key[0];
+    } else if (keys <= 128) {
       beam_take(hold, from, keys, K, lane, list[k]);
     } else {
       BeamHold<8> more;
@@ -364,33 +426,80 @@ __global__ __launch_bounds__(64 * kBeamJoinWaves) void beam_join(const BeamArgs<
   }
   __syncthreads();
   if (wave != 0) return;
-  // Lane k goes through row k's list; scores are compared in 64 bits.
-  int taken = 0;
-  const double from = lane < K ? (double)s.scores[text * K + lane] : 0.0;
-  const bool done = lane < K && s.finished && s.finished[text * K + lane];
-  auto head = [&]() -> uint64_t {  // ordered score; 0: the list is at its end
-    const uint64_t key = lane < K && taken < K ? list[lane][taken] : 0;
+  // Scores are compared in 64 bits, ordered as numbers; 0: the list is at its end.
+  // (Scores are read before any is written: the outputs may be they.)
+  const auto score_of = [&](int k, double from, uint64_t key) -> uint64_t {
     if (key == 0) return 0;
     const float x = beam_value((uint32_t)(key >> 32));
-    double score = from + (((double)x - tops[lane]) - logs[lane]);
+    double score = from + (((double)x - tops[k]) - logs[k]);
     if (!(x > -__builtin_inff()) || !(score > -__builtin_inf())) score = -__builtin_inf();
     const uint64_t u = __builtin_bit_cast(uint64_t, score + 0.0);
     return u ^ ((uint64_t)((int64_t)u >> 63) | 0x8000000000000000ull);
   };
-  uint64_t mine = head();
+  const auto write = [&](int r, int k, uint64_t key, uint64_t order, bool done) {
+    const uint64_t u = order ^ ((uint64_t)((int64_t)~order >> 63) | 0x8000000000000000ull);
+    const int64_t o = text * K + r, v = beam_place(key);
+    s.out_scores[o] = (float)__builtin_bit_cast(double, u);
+    s.parents[o] = k;
+    s.tokens[o] = v;
+    if (s.out_finished) s.out_finished[o] = done || v == s.eos;
+  };
+  const auto ends = [&](int k) { return s.finished && s.finished[text * K + k]; };
+  // A continuation a lane, its place by how many come before it: 0.4 us faster than one
+  // after the other with 4 beams, 0.6 slower with 8.
+  if (K <= 4) {
+    const int k = min(lane / K, K - 1);
+    const uint64_t key = lane < K * K ? list[k][lane % K] : 0;
+    const uint64_t mine = score_of(k, (double)s.scores[text * K + k], key);
+    const bool done = ends(k);
+    int rank = 0;
+    for (int o = 0; o < K * K; ++o) {
+      const uint64_t other =
+          (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(mine >> 32), o) << 32 |
+          (uint32_t)__builtin_amdgcn_readlane((int)mine, o);
+      rank += other > mine || (other == mine && o < lane);
+    }
+    if (mine && rank < K) write(rank, k, key, mine, done);
+    return;
+  }
+  // Lane k goes through row k's list.
+  int taken = 0;
+  const bool done = lane < K && ends(lane);
+  const double from = lane < K ? (double)s.scores[text * K + lane] : 0.0;
+  const auto head = [&] { return lane < K && taken < K ? list[lane][taken] : 0; };
+  uint64_t key = head(), mine = score_of(lane, from, key);
+  const auto next = [&] {
+    ++taken;
+    key = head();
+    mine = score_of(lane, from, key);
+  };
   for (int r = 0; r < K; ++r) {
     const uint64_t best = wave_max(mine);
     if (lane == __ffsll((unsigned long long)__ballot(mine == best)) - 1) {
-      const uint64_t u = best ^ ((uint64_t)((int64_t)~best >> 63) | 0x8000000000000000ull);
-      const int64_t o = text * K + r, v = beam_place(list[lane][taken]);
-      s.out_scores[o] = (float)__builtin_bit_cast(double, u);
-      s.parents[o] = lane;
-      s.tokens[o] = v;
-      if (s.out_finished) s.out_finished[o] = done || v == s.eos;
-      ++taken;
-      mine = head();
+      write(r, lane, key, best, done);
+      next();
     }
   }
+}
+
+template <typename E>
+__global__ __launch_bounds__(64 * kBeamJoinWaves) void beam_join(const BeamArgs<E> s) {
+  const int64_t text = seq_block();
+  if (text < s.B) beam_merge(s, text);
+}
+
+// Both for a text, where its rows are a wave each: with 4 beams of 28 logits 8.9 us
+// against 10.5 in two launches, of 4096 (bf16) 8.0 against 9.7, 1024 texts of those 13.6
+// against 16.5.  (Rows of several waves: 1024 x 4 x 16384 49 us against 35.)
+template <typename E>
+__global__ __launch_bounds__(64 * kBeamJoinWaves) void beam_whole(const BeamArgs<E> s) {
+  const int64_t text = seq_block();
+  if (text >= s.B) return;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  beam_look(s, (uint32_t)text * s.K + (uint32_t)(wave / s.parts), wave % s.parts,
+            beam_lds + wave * BeamLds(s.K).bytes);
+  __syncthreads();
+  beam_merge(s, text);
 }
 
 // ------------------------------------------------------------------ reordering
@@ -617,10 +726,16 @@ extern "C" ck_status ck_beam_select(const ck_beam_shape* shape, ck_seq logits, c
     a.K = (int)shape->K;
     a.V = (int)shape->V;
     a.parts = ws.parts;
-    const int64_t waves = shape->B * shape->K * ws.parts;
+    const int64_t each = shape->K * ws.parts, waves = shape->B * each;
+    const size_t one = BeamLds((int)shape->K).bytes;
+    if (ws.parts == 1 && each <= kBeamJoinWaves && each * one <= kBeamWholeLds &&
+        shape->B < kSeqGridX / 4) {
+      beam_whole<E><<<seq_grid(shape->B), 64 * (int)each, each * one, stream>>>(a);
+      CK_HIP_TRY(hipGetLastError());
+      return CK_OK;
+    }
     const int per = shape->K > 16 ? kBeamWaves / 2 : kBeamWaves;  // (32 KB of LDS at most)
-    const size_t lds = per * BeamLds((int)shape->K).bytes;
-    beam_part<E><<<seq_grid((waves + per - 1) / per), 64 * per, lds, stream>>>(a, waves);
+    beam_part<E><<<seq_grid((waves + per - 1) / per), 64 * per, per * one, stream>>>(a, waves);
     // (a launch holds fewer than 2^32 threads along its first dimension)
     const int64_t join = shape->B < kSeqGridX / 2 ? kBeamJoinWaves : kBeamWaves;
     beam_join<E><<<seq_grid(shape->B), 64 * (int)std::min(shape->K, join), 0, stream>>>(a);

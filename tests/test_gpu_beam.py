@@ -240,6 +240,18 @@ def test_scores_in_place_streams_and_graphs():
         assert torch.equal(s, s2) and torch.equal(d, d2) and all(map(torch.equal, st, st2)), k
 
 
+@pytest.mark.parametrize("K,V", [(1, 28), (4, 28), (8, 4000), (16, 50), (3, 9000), (32, 4096)])
+def test_scores_and_ends_in_place(K, V):
+    """Rows of one part and of more, few beams and many."""
+    log(f"beam_select in place K={K} V={V}")
+    x, _, scores, _ = make(11, 3, K, V, "bf16")
+    done = torch.zeros(3, K, dtype=torch.bool, device="cuda")
+    done[1, K // 2] = True
+    want = sgr.beam_select(x, scores, done, 2)
+    out = (scores, torch.empty_like(want[1]), torch.empty_like(want[2]), done)
+    assert all(map(torch.equal, want, sgr.beam_select(x, scores, done, 2, out=out)))
+
+
 def test_offsets_past_32_bits():
     """Texts 2^31 elements apart."""
     if torch.cuda.mem_get_info()[0] < 16 << 30:
