@@ -539,6 +539,13 @@ ck_status ck_dropout_backward(const ck_dropout_shape* shape, ck_seq grad_out, ck
  * with h_{-1} = state0.  Steps lie less than 2^26 elements apart.  A gate that is
  * almost 1 is held as what it lacks, so that a state is kept over as many steps as
  * the gate says.  A state that is not finite may go on as a NaN.
+ *
+ * A call of few rows and channels has workgroups that wait for others of the same call
+ * (through its workspace, which the call prepares itself and no other call may use at
+ * the same time).  They only wait for such as run already, so a call ends whatever else
+ * the device does; a wait that went on for seconds would give up and leave NaN behind.
+ * `state` must not be state0, nor the gradient of state0 grad_state (CK_ERR_BAD_VALUE;
+ * ck_gated_step may write in place).
  */
 typedef struct {
   int64_t T, B, D; /* steps, batch rows, channels */
@@ -632,8 +639,8 @@ ck_status ck_clip_grad_norm(const ck_clip_tensor* tensors, int64_t count, double
  *
  * over all beams k and tokens v of a text, best first; of equal scores the lower
  * k V + v is first (of one beam's, the one of the larger logit: where the scores'
- * rounding makes unlike logits alike, their order stays).  A finished beam has one continuation, the end token, at its own
- * score.  A logit of -inf, and a NaN, is never taken before any other (its score is
+ * rounding makes unlike logits alike, their order stays).  A finished beam has one
+ * continuation, the end token, at its own score.  A logit of -inf, and a NaN, is never taken before any other (its score is
  * -inf, as are all of a beam whose own score is -inf or NaN, and of a finished beam
  * but the end token's); +inf counts as the largest finite fp32 value.  Logits of a
  * beam without any above -inf, or whose score is -inf, or that is finished, are not

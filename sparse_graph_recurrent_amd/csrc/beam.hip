@@ -8,7 +8,11 @@
 // takes kBeamSpan adjacent logits of a row (so few rows still fill the chip) and
 // leaves their maximum, their sum of exponentials and their K best in order; a
 // workgroup a text joins these row by row and then takes K times the best head of
-// the K rows' lists.  Rows of one part each are looked at and joined by one workgroup.
+// the K rows' lists.  64 texts x 8 beams x 50021 logits, bf16, some beams
+// finished: 17 us (43 MB of logits, 2.5 TB/s: a wave's loads, 8 us at a copy's rate, then its
+// sums and its search, and nothing follows that would cover them) and 7.6 for the join
+// (latency: 8 rows' 104 keys, then 8 rounds).  Parts of 2048 logits: the same.
+// Rows of one part each are looked at and joined by one workgroup.
 //
 // The K best of a wave: the K-th largest of its lanes' maxima is a limit that at
 // least K logits reach and few more (fewer than K lanes lie above it).  Those above it
@@ -535,6 +539,8 @@ template <> struct MoveBytes<4> { typedef uint32_t type __attribute__((aligned(1
 template <> struct MoveBytes<2> { typedef uint16_t type __attribute__((aligned(1))); };
 template <> struct MoveBytes<1> { typedef uint8_t type; };
 
+// HBM bounds it: 64 x 8 beams of 172 KB each, four states: 31 us (5.7 TB/s; parents that
+// are taken twice come from a cache), 22 where the last-level cache has them.
 // One pack of all of a text's rows: every row is read before any is written, so that
 // a state may be reordered in place.  parent: lane k's is row k's.
 template <int N, int K>

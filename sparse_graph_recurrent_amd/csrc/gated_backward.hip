@@ -200,7 +200,8 @@ __device__ __forceinline__ void gate_part(const A& s, const GateSpot<V>& at,
   }
 }
 
-// All windows of a column, from the last to the first.
+// All windows of a column, from the last to the first.  256 columns of 2048 steps, bf16,
+// with an output gate: 123 us (5.1 TB/s).
 template <typename E, int V, bool I, bool Z>
 __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd(const GateArgs<E> s) {
   __shared__ GateMeet<V, kGateWaves> meet;
@@ -252,7 +253,8 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd(const GateArgs<E> s)
   if (s.part) gate_part<V>(s, at, sums, bias, at.b);
 }
 
-// A window of a column a workgroup.
+// A window of a column a workgroup: one a CU (136 registers; held to 128 for a second one
+// it spills, 94 -> 139 us).  80 columns of 777 steps, fp16: 21 us.
 template <typename E, int V, bool I, bool Z>
 __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd_chain(const GateArgs<E> s) {
   __shared__ GateChain<V> chain;
@@ -293,7 +295,8 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd_chain(const GateArgs
 }
 
 // g_f_bias and g_i_bias: the workgroups' sums, in their order.  A wave an output's 64
-// channels would have long walks: kBiasRows threads share them.
+// channels would have long walks: kBiasRows threads share them (4.7 us for 8 rows of
+// 2 x 2048 channels: latency).
 constexpr int kBiasCols = 32, kBiasRows = 8;
 __global__ __launch_bounds__(kBiasCols * kBiasRows) void gate_bias_sum(
     const float* part, int D, int64_t rows, float* g_f, float* g_i) {

