@@ -414,6 +414,32 @@ def test_captured_graph_replays():
             assert torch.equal(a, b), k
 
 
+def test_autograd_in_a_captured_graph():
+    """Gradients asked for within a capture, of windows that wait for one another."""
+    g, _ = problem(20, 700, 2, 70, "bf16", True, True, None, "time")
+    leaves = [g[k].requires_grad_() for k in ("x", "f", "i", "z", "f_bias", "i_bias", "state0")]
+
+    def work():
+        out, state = sgr.gated_scan(*leaves)
+        return torch.autograd.grad([out, state], leaves, [g["go"], g["gstate"]])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = work()
+    for k in range(3):
+        with torch.no_grad():
+            g["x"].mul_(0.5).add_(0.1 * k)
+        graph.replay()
+        want = work()
+        torch.cuda.synchronize()
+        assert all(map(torch.equal, held, want)), k
+
+
 def test_binding_refusals():
     g, _ = problem(19, 5, 2, 8, "fp32", True, True, None, "time")
     x, f = g["x"], g["f"]
