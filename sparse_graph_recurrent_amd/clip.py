@@ -49,8 +49,6 @@ def _sizes(count: int) -> int:
 
 def _dense(t: torch.Tensor) -> bool:
     """True when t's elements fill its memory without gaps, in any order of dimensions."""
-    if t.is_contiguous():
-        return True
     want = 1
     for stride, size in sorted(zip(t.stride(), t.shape)):
         if size == 1:
@@ -81,24 +79,25 @@ def _run(grads, outs, max_norm: float, norm, workspace, device):
     else:
         dev = torch.device("cuda" if device is None else device).index
         dev = torch.cuda.current_device() if dev is None else dev
-    args = []
+    args, last, code = [], None, None
+    same = outs is grads
     for k, t in enumerate(grads):
-        if not (isinstance(t, torch.Tensor) and t.dtype in _DTYPES and t.get_device() == dev
-                and _dense(t)):
+        dtype = t.dtype if isinstance(t, torch.Tensor) else None
+        if dtype is not last:
+            last, code = dtype, _DTYPES.get(dtype)
+        if code is None or t.get_device() != dev or not (t.is_contiguous() or _dense(t)):
             _refuse(t, f"gradient {k}", dev)
         at = t.data_ptr()
-        to = 0
-        if outs is grads:
-            to = at
-        elif outs is not None:
+        to = at if same else 0
+        if not same and outs is not None:
             o = outs[k]
-            if not (isinstance(o, torch.Tensor) and o.dtype is t.dtype and o.shape == t.shape
+            if not (isinstance(o, torch.Tensor) and o.dtype is dtype and o.shape == t.shape
                     and o.get_device() == dev and (o.stride() == t.stride() or o.is_contiguous()
                                                    and t.is_contiguous())):
                 raise ValueError(f"output {k} must be on cuda:{dev}, with its gradient's type, "
                                  "shape and strides")
             to = o.data_ptr()
-        args += (at, to, t.numel(), _DTYPES[t.dtype])
+        args += (at, to, t.numel(), code)
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=f"cuda:{dev}")
     elif not (isinstance(norm, torch.Tensor) and norm.dtype is torch.float32
