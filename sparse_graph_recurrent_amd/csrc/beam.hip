@@ -22,6 +22,7 @@
 #include <algorithm>
 #include <cfloat>
 
+#include "beam_lds.h"
 #include "ck.h"
 #include "ck_internal.h"
 #include "sequence.h"
@@ -29,9 +30,6 @@
 namespace ckhip {
 namespace {
 
-constexpr int kBeamMaxK = 32;
-constexpr int kBeamV = 8;        // logits a lane and access
-constexpr int kBeamPacks = 8;    // accesses of a wave
 constexpr int kBeamSpan = 64 * kBeamV * kBeamPacks;
 constexpr int kBeamWaves = 4;    // of a workgroup that reads logits
 constexpr int kBeamJoinWaves = 16;
@@ -116,17 +114,6 @@ __device__ __forceinline__ bool beam_skips(const BeamArgs<E>& s, int64_t row) {
   return (done != 0) | !(score > -__builtin_inff());  // (both loads set out together)
 }
 
-// What a wave keeps in LDS, for K beams.
-struct BeamLds {
-  int packs;       // lanes' accesses with a logit at the limit or above
-  int above;       // keys above it
-  size_t bytes;
-  __host__ __device__ explicit BeamLds(int K)
-      : packs((K - 1) * kBeamPacks + K), above((K - 1) * kBeamPacks * kBeamV),
-        bytes((size_t)(above + K) * sizeof(uint64_t) +
-              (size_t)((packs * (kBeamV + 1) + 3) & ~3) * sizeof(float)) {}
-};
-
 // A lane's logits, as they came: 16-bit ones in half the registers, so that all waves of
 // a call find room at once.
 typedef uint32_t BeamWords __attribute__((ext_vector_type(4), aligned(2)));
@@ -204,9 +191,9 @@ __device__ __forceinline__ void beam_look(const BeamArgs<E>& s, uint32_t row, in
   const int K = s.K, lane = threadIdx.x & 63;
   const BeamLds room(K);
   float* hits = reinterpret_cast<float*>(lds);                       // [packs][kBeamV]
-  uint64_t* above = reinterpret_cast<uint64_t*>(hits + room.packs * kBeamV);
-  uint64_t* level = above + room.above;
-  int* places = reinterpret_cast<int*>(level + K);                   // [packs]
+  uint64_t* above = reinterpret_cast<uint64_t*>(lds + room.above_at);
+  uint64_t* level = reinterpret_cast<uint64_t*>(lds + room.level_at);  // [K]
+  int* places = reinterpret_cast<int*>(lds + room.places_at);        // [packs]
 
   const uint32_t text = row / (uint32_t)K;
   const E* p = s.x.row(text, row - text * (uint32_t)K);
@@ -740,7 +727,8 @@ extern "C" ck_status ck_beam_select(const ck_beam_shape* shape, ck_seq logits, c
       CK_HIP_TRY(hipGetLastError());
       return CK_OK;
     }
-    const int per = shape->K > 16 ? kBeamWaves / 2 : kBeamWaves;  // (32 KB of LDS at most)
+    // (at most 52.4 KB of LDS: 32 beams; 50.8 with 16)
+    const int per = shape->K > 16 ? kBeamWaves / 2 : kBeamWaves;
     beam_part<E><<<seq_grid((waves + per - 1) / per), 64 * per, per * one, stream>>>(a, waves);
     // (a launch holds fewer than 2^32 threads along its first dimension)
     const int64_t join = shape->B < kSeqGridX / 2 ? kBeamJoinWaves : kBeamWaves;
