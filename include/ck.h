@@ -544,8 +544,9 @@ ck_status ck_dropout_backward(const ck_dropout_shape* shape, ck_seq grad_out, ck
  * (through its workspace, which the call prepares itself and no other call may use at
  * the same time).  They only wait for such as run already, so a call ends whatever else
  * the device does; a wait that went on for seconds would give up and leave NaN behind.
- * `state` must not be state0, nor the gradient of state0 grad_state (CK_ERR_BAD_VALUE;
- * ck_gated_step may write in place).
+ * Outputs over an input or over one another (`state` over state0, `out` over x, two
+ * gradients that are one tensor) are refused (CK_ERR_BAD_VALUE) where addresses, sizes
+ * and strides show it; ck_gated_step may write in place.
  */
 typedef struct {
   int64_t T, B, D; /* steps, batch rows, channels */
@@ -594,7 +595,8 @@ ck_status ck_gated_backward(const ck_gated_shape* shape, const ck_gated_inputs* 
                             hipStream_t stream);
 
 /* One token per row (shape->T must be 1, lengths NULL): out[0] and the new state from
- * state0.  `state` may be state0 itself (updated in place). */
+ * state0.  `state` may be state0 itself (updated in place), and `out` x or one of the
+ * gates itself. */
 ck_status ck_gated_step(const ck_gated_shape* shape, const ck_gated_inputs* in, ck_seq out,
                         float* state, hipStream_t stream);
 

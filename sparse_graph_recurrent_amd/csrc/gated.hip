@@ -5,6 +5,8 @@
 #include <algorithm>
 #include <initializer_list>
 
+#include "overlap.h"
+
 namespace ckhip {
 namespace {
 
@@ -85,18 +87,89 @@ GateWs gate_ws(const ck_gated_shape& s, bool backward) {
   return w;
 }
 
+// The states that a forward leaves, in bytes.
+size_t gate_saved(const ck_gated_shape& s) {
+  return (size_t)((s.T + kGateStep - 1) / kGateStep) * s.B * s.D * sizeof(float);
+}
+
 ck_status gate_check_f32(const void* p, const char* what) {
   if (reinterpret_cast<uintptr_t>(p) % sizeof(float) == 0) return CK_OK;
   set_error("%s is not aligned to its element type", what);
   return CK_ERR_BAD_VALUE;
 }
 
-// (windows that wait for one another read the one while others have written the other)
-ck_status gate_check_apart(const void* read, const void* written, const char* what) {
-  if (!read || read != written) return CK_OK;
-  set_error("%s must not lie over what it is made from", what);
-  return CK_ERR_BAD_VALUE;
-}
+// The tensors of a call, for which of them may not share memory.
+class GateSpans {
+ public:
+  explicit GateSpans(const ck_gated_shape& s) : s_(s), e_((int64_t)seq_elem_bytes(s.dtype)) {}
+  void seq(const char* name, const ck_seq& q, bool written = false) {
+    // (strides up to 2^60 elements: nothing lies further apart, their bytes stay in 64 bits)
+    add(name, q.data, s_.T, s_.T > 1 ? std::min(q.stride_t, kFar) * e_ : 0, s_.B,
+        s_.B > 1 ? std::min(q.stride_b, kFar) * e_ : 0, s_.D * e_, written);
+  }
+  void state(const char* name, const float* p, bool written = false) {
+    bytes(name, p, (size_t)(s_.B * s_.D) * sizeof(float), written);
+  }
+  void bias(const char* name, const float* p, bool written = false) {
+    bytes(name, p, (size_t)s_.D * sizeof(float), written);
+  }
+  void bytes(const char* name, const void* p, size_t n, bool written) {
+    add(name, p, 1, 0, 1, 0, (int64_t)n, written);
+  }
+  // What a call reads of its inputs (a backward does not read state0).
+  void inputs(const ck_gated_inputs& in, bool backward = false) {
+    seq("x", in.x), seq("f", in.f), seq("i", in.i), seq("z", in.z);
+    bias("f_bias", in.f_bias);
+    if (in.i.data) bias("i_bias", in.i_bias);
+    if (!backward) state("state0", in.state0);
+    bytes("lengths", in.lengths, (size_t)s_.B * sizeof(int32_t), false);
+  }
+  // in_place: what is written may be an input itself (the same elements).
+  ck_status check(bool in_place = false) const {
+    for (int k = 0; k < n_; ++k) {
+      const Span& w = v_[k];
+      if (!w.written) continue;
+      for (int o = 0; o < n_; ++o) {
+        const Span& r = v_[o];
+        if (w.end <= r.at || r.end <= w.at || o == k || (r.written && o < k)) continue;
+        if (!pieces_meet(pieces(w), pieces(r)) || (in_place && !r.written && same(w, r))) continue;
+        set_error("%s must not lie over %s", w.name, r.name);
+        return CK_ERR_BAD_VALUE;
+      }
+    }
+    return CK_OK;
+  }
+
+ private:
+  struct Span {  // (as Pieces)
+    uintptr_t at, end;
+    int64_t n0, s0, n1, s1, bytes;
+    const char* name;
+    bool written;
+  };
+  static constexpr int64_t kFar = int64_t(1) << 60;
+  static Pieces pieces(const Span& p) {
+    Pieces q;
+    q.at = p.at, q.n0 = p.n0, q.s0 = p.s0, q.n1 = p.n1, q.s1 = p.s1, q.bytes = p.bytes;
+    return q;
+  }
+  static bool same(const Span& a, const Span& b) {
+    return a.at == b.at && a.n0 == b.n0 && a.s0 == b.s0 && a.n1 == b.n1 && a.s1 == b.s1 &&
+           a.bytes == b.bytes;
+  }
+  void add(const char* name, const void* p, int64_t n0, int64_t s0, int64_t n1, int64_t s1,
+           int64_t bytes, bool written) {
+    if (!p || n0 <= 0 || bytes <= 0) return;
+    Span& q = v_[n_++];
+    q = Span{reinterpret_cast<uintptr_t>(p), 0, n0, s0, n1, s1, bytes, name, written};
+    const __int128 end = pieces(q).end();
+    q.end = end > (__int128)UINTPTR_MAX ? UINTPTR_MAX : (uintptr_t)end;
+  }
+  const ck_gated_shape& s_;
+  int64_t e_;
+  int n_ = 0;
+  Span v_[20];
+};
 
 ck_status gate_check_out(const ck_gated_shape& s, const ck_seq& q, bool optional,
                          const char* what) {
@@ -222,8 +295,7 @@ extern "C" ck_status ck_gated_sizes(const ck_gated_shape* shape, size_t* saved_b
   const ck_status rc = gate_check_shape(shape);
   if (rc != CK_OK) return rc;
   const ck_gated_shape& s = *shape;
-  if (saved_bytes)
-    *saved_bytes = (size_t)((s.T + kGateStep - 1) / kGateStep) * s.B * s.D * sizeof(float);
+  if (saved_bytes) *saved_bytes = gate_saved(s);
   if (forward_bytes) *forward_bytes = gate_ws(s, false).total;
   if (backward_bytes) *backward_bytes = gate_ws(s, true).total;
   return CK_OK;
@@ -236,13 +308,22 @@ extern "C" ck_status ck_gated_forward(const ck_gated_shape* shape, const ck_gate
   ck_status rc = gate_check_inputs(shape, in);
   if (rc == CK_OK) rc = gate_check_out(*shape, out, shape->T == 0, "out");
   if (rc == CK_OK) rc = gate_check_f32(state, "state");
-  if (rc == CK_OK) rc = gate_check_apart(in->state0, state, "state");
   if (rc != CK_OK) return rc;
   const GateTensors tensors = {&in->x, &in->f, &in->i, &in->z, &out};
   const GatePlan p = gate_plan(*shape, gate_step(shape->dtype, tensors), false);
   const GateWs ws = gate_ws(*shape, false);
   rc = seq_check_ws(workspace, workspace_bytes, ws.total);
   if (rc == CK_OK && saved) rc = check_aligned(saved, "saved");
+  if (rc != CK_OK) return rc;
+  // (windows that wait for one another read the inputs while others have written; groups
+  // of channels that do not fill one share a channel)
+  GateSpans spans(*shape);
+  spans.seq("out", out, true);
+  spans.state("state", state, true);
+  spans.bytes("saved", saved, gate_saved(*shape), true);
+  spans.bytes("the workspace", workspace, ws.total, true);
+  spans.inputs(*in);
+  rc = spans.check();
   if (rc != CK_OK) return rc;
   return seq_dispatch(shape->dtype, [&](auto* e) -> ck_status {
     using E = std::remove_pointer_t<decltype(e)>;
@@ -277,7 +358,6 @@ extern "C" ck_status ck_gated_backward(const ck_gated_shape* shape, const ck_gat
   if (rc == CK_OK) rc = gate_check_f32(grads->f_bias, "the gradient of f_bias");
   if (rc == CK_OK) rc = gate_check_f32(grads->i_bias, "the gradient of i_bias");
   if (rc == CK_OK) rc = gate_check_f32(grads->state0, "the gradient of state0");
-  if (rc == CK_OK) rc = gate_check_apart(grad_state, grads->state0, "the gradient of state0");
   if (rc == CK_OK && saved) rc = check_aligned(saved, "saved");
   if (rc != CK_OK) return rc;
   const GateTensors tensors = {&in->x, &in->f, &in->i, &in->z, &grad_out,
@@ -285,6 +365,21 @@ extern "C" ck_status ck_gated_backward(const ck_gated_shape* shape, const ck_gat
   const GatePlan p = gate_plan(*shape, gate_step(shape->dtype, tensors), true);
   const GateWs ws = gate_ws(*shape, true);
   rc = seq_check_ws(workspace, workspace_bytes, ws.total);
+  if (rc != CK_OK) return rc;
+  GateSpans spans(*shape);
+  spans.seq("the gradient of x", grads->x, true);
+  spans.seq("the gradient of f", grads->f, true);
+  if (in->i.data) spans.seq("the gradient of i", grads->i, true);
+  if (in->z.data) spans.seq("the gradient of z", grads->z, true);
+  spans.bias("the gradient of f_bias", grads->f_bias, true);
+  spans.bias("the gradient of i_bias", grads->i_bias, true);
+  spans.state("the gradient of state0", grads->state0, true);
+  spans.bytes("the workspace", workspace, ws.total, true);
+  spans.bytes("saved", saved, gate_saved(*shape), false);
+  spans.seq("grad_out", grad_out);
+  spans.state("grad_state", grad_state);
+  spans.inputs(*in, true);
+  rc = spans.check();
   if (rc != CK_OK) return rc;
   return seq_dispatch(shape->dtype, [&](auto* e) -> ck_status {
     using E = std::remove_pointer_t<decltype(e)>;
@@ -322,6 +417,12 @@ extern "C" ck_status ck_gated_step(const ck_gated_shape* shape, const ck_gated_i
     return state ? CK_ERR_BAD_VALUE : CK_ERR_NULL_ARG;
   }
   rc = gate_check_f32(state, "state");
+  if (rc != CK_OK) return rc;
+  GateSpans spans(*shape);  // (a thread reads its channels' inputs before it writes them)
+  spans.seq("out", out, true);
+  spans.state("state", state, true);
+  spans.inputs(*in);
+  rc = spans.check(true);
   if (rc != CK_OK) return rc;
   return seq_dispatch(shape->dtype, [&](auto* e) -> ck_status {
     using E = std::remove_pointer_t<decltype(e)>;

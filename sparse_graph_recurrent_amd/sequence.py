@@ -479,7 +479,8 @@ def gated_scan_forward(x, f, i=None, z=None, f_bias=None, i_bias=None, state0=No
     x, the gates f (forget), i (input; None: what the forget gate lets go) and
     z (output; None: open): [T, B, D]; f_bias, i_bias: [D]; state0 and the
     returned state: fp32 [B, D].  ``saved`` is what ``gated_scan_backward``
-    needs (None with save=False)."""
+    needs (None with save=False).  ``out`` and ``state`` must not lie over an
+    input or over one another."""
     if stream is not None:
         return _on_stream(stream, gated_scan_forward, x, f, i, z, f_bias, i_bias, state0, lengths,
                           save, out, state, saved, workspace)
@@ -499,7 +500,8 @@ def gated_scan_backward(x, f, saved, grad_out, i=None, z=None, f_bias=None, i_bi
                         stream=None) -> dict:
     """Run ``ck_gated_backward``; returns the gradients (overwritten) by the
     names g_x, g_f, g_f_bias, g_state0 and, with that gate, g_i and g_i_bias,
-    g_z."""
+    g_z.  ``grads``: a dict of such to write, which must not lie over what is
+    read or over one another."""
     if stream is not None:
         return _on_stream(stream, gated_scan_backward, x, f, saved, grad_out, i, z, f_bias, i_bias,
                           lengths, grad_state, grads, workspace)
@@ -542,8 +544,8 @@ def gated_scan_backward(x, f, saved, grad_out, i=None, z=None, f_bias=None, i_bi
 def gated_scan_step(state, x, f, i=None, z=None, f_bias=None, i_bias=None, out=None,
                     new_state=None, stream=None):
     """Run ``ck_gated_step``: one token per row.  x, f, i, z: [B, D]; state:
-    fp32 [B, D], updated in place unless ``new_state`` is given.  Returns (out
-    [B, D], the new state)."""
+    fp32 [B, D], updated in place unless ``new_state`` is given; ``out`` may be
+    x or a gate itself.  Returns (out [B, D], the new state)."""
     if stream is not None:
         return _on_stream(stream, gated_scan_step, state, x, f, i, z, f_bias, i_bias, out,
                           new_state)
