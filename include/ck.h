@@ -681,9 +681,9 @@ ck_status ck_beam_select(const ck_beam_shape* shape, ck_seq logits, const float*
  *
  * A state's row is `segments` pieces of `bytes` adjacent bytes.  `out` is the state
  * itself (the same strides: reordered in place) or does not overlap it; rows of `out`
- * must not lie over one another, nor one state over what is written of another
- * (CK_ERR_BAD_VALUE where the addresses show it).  A parent outside [0, K) counts as
- * the nearer bound.
+ * must not lie over one another, nor a state or the parents over what is written of
+ * another state (CK_ERR_BAD_VALUE where addresses, sizes and strides show it).  A parent
+ * outside [0, K) counts as the nearer bound.
  */
 typedef struct {
   const void* in;

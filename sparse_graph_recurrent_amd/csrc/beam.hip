@@ -21,10 +21,13 @@
 
 #include <algorithm>
 #include <cfloat>
+#include <new>
+#include <vector>
 
 #include "beam_lds.h"
 #include "ck.h"
 #include "ck_internal.h"
+#include "overlap.h"
 #include "sequence.h"
 
 namespace ckhip {
@@ -637,16 +640,43 @@ bool move_overlaps(int64_t rows, int64_t row, int64_t segs, int64_t seg, int64_t
   return rows > 1 ? row < bytes : segs > 1 && seg < bytes;
 }
 
-// Whether a state's output lies over its input elsewhere than in place, as far as two
-// ranges without gaps show it.
-bool move_crosses(const ck_beam_state& s, int64_t rows) {
-  const int64_t row = s.segments * s.bytes, all = rows * row;
-  const auto dense = [&](int64_t of_row, int64_t of_segment) {
-    return (s.segments == 1 || of_segment == s.bytes) && (rows == 1 || of_row == row);
+// What is written must not lie over anything else of a call, but a state's output over
+// the state itself.
+ck_status move_check_apart(const ck_beam_state* states, int64_t count, const int64_t* parents,
+                           int64_t rows) {
+  struct Span {
+    Pieces p;
+    __int128 end;
   };
-  const uintptr_t in = reinterpret_cast<uintptr_t>(s.in), out = reinterpret_cast<uintptr_t>(s.out);
-  return in != out && dense(s.in_row, s.in_segment) && dense(s.out_row, s.out_segment) &&
-         in < out + all && out < in + all;
+  const auto span = [](const Pieces& p) { return Span{p, p.end()}; };
+  const auto meet = [](const Span& a, const Span& b) {
+    return a.p.at < b.end && b.p.at < a.end && pieces_meet(a.p, b.p);
+  };
+  std::vector<Span> in(count), out(count);
+  const Span par = span(range_of(parents, (size_t)rows * sizeof(int64_t)));
+  for (int64_t i = 0; i < count; ++i) {
+    const ck_beam_state& s = states[i];
+    if (s.segments == 0 || s.bytes == 0) continue;  // (empty: meets nothing)
+    Pieces p = range_of(s.in, (size_t)s.bytes);
+    p.n0 = rows, p.s0 = s.in_row, p.n1 = s.segments, p.s1 = s.in_segment;
+    in[i] = span(p);
+    p.at = reinterpret_cast<uintptr_t>(s.out), p.s0 = s.out_row, p.s1 = s.out_segment;
+    out[i] = span(p);
+    if (s.in != s.out && meet(in[i], out[i])) {
+      set_error("state %lld: its output lies over it", (long long)i);
+      return CK_ERR_BAD_VALUE;
+    }
+    if (meet(out[i], par)) {
+      set_error("state %lld: its output lies over the parents", (long long)i);
+      return CK_ERR_BAD_VALUE;
+    }
+    for (int64_t o = 0; o < i; ++o)
+      if (meet(out[o], out[i]) || meet(in[o], out[i]) || meet(out[o], in[i])) {
+        set_error("states %lld and %lld share memory that is written", (long long)o, (long long)i);
+        return CK_ERR_BAD_VALUE;
+      }
+  }
+  return CK_OK;
 }
 
 template <int K>
@@ -785,16 +815,13 @@ extern "C" ck_status ck_beam_reorder(const ck_beam_state* states, int64_t count,
       set_error("state %lld: its output is the state itself with other strides", (long long)i);
       return CK_ERR_BAD_VALUE;
     }
-    if (move_crosses(s, B * K)) {
-      set_error("state %lld: its output lies over it", (long long)i);
-      return CK_ERR_BAD_VALUE;
-    }
-    for (int64_t o = 0; o < i; ++o)
-      if (states[o].segments && states[o].bytes &&
-          (states[o].out == s.out || states[o].in == s.out || states[o].out == s.in)) {
-        set_error("states %lld and %lld share memory that is written", (long long)o, (long long)i);
-        return CK_ERR_BAD_VALUE;
-      }
+  }
+  try {
+    const ck_status rc = move_check_apart(states, count, parents, B * K);
+    if (rc != CK_OK) return rc;
+  } catch (const std::bad_alloc&) {
+    set_error("out of host memory");
+    return CK_ERR_NOMEM;
   }
   MoveTable t = {};
   t.parents = parents;
