@@ -668,6 +668,7 @@ ck_status ck_beam_sizes(const ck_beam_shape* shape, size_t* workspace_bytes);
  *   tokens        int64[B][K]   written
  *   out_finished  uint8[B][K]   written (may be finished): the parent was, or the token is
  *                               eos; NULL: not wanted
+ * Outputs over one another or otherwise over what is read are refused (CK_ERR_BAD_VALUE).
  */
 ck_status ck_beam_select(const ck_beam_shape* shape, ck_seq logits, const float* scores,
                          const uint8_t* finished, float* out_scores, int64_t* parents,

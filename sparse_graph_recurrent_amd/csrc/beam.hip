@@ -631,6 +631,51 @@ ck_status beam_check_out(const void* p, size_t align, const char* what) {
   return CK_OK;
 }
 
+// What is written must not lie over anything else of a call, but new scores and ends over
+// the old ones.
+ck_status beam_check_apart(const ck_beam_shape& s, const ck_seq& logits, const float* scores,
+                           const uint8_t* finished, const float* out_scores,
+                           const int64_t* parents, const int64_t* tokens,
+                           const uint8_t* out_finished, const void* workspace, size_t ws_bytes) {
+  struct Span {
+    const char* name;
+    uintptr_t at;
+    size_t bytes;
+  };
+  const size_t n = (size_t)(s.B * s.K);
+  const auto span = [](const char* name, const void* p, size_t bytes) {
+    return Span{name, reinterpret_cast<uintptr_t>(p), p ? bytes : 0};
+  };
+  const Span v[] = {span("out_scores", out_scores, 4 * n), span("parents", parents, 8 * n),
+                    span("tokens", tokens, 8 * n), span("out_finished", out_finished, n),
+                    span("the workspace", workspace, ws_bytes), span("scores", scores, 4 * n),
+                    span("finished", finished, n)};
+  constexpr int kWritten = 5, kAll = 7;
+  const int64_t e = (int64_t)seq_elem_bytes(s.dtype);
+  Pieces x = range_of(logits.data, (size_t)(s.V * e));
+  const int64_t far = int64_t(1) << 60;  // (nothing lies further apart)
+  x.n0 = s.B, x.s0 = s.B > 1 ? std::min(logits.stride_t, far) * e : 0;
+  x.n1 = s.K, x.s1 = s.K > 1 ? std::min(logits.stride_b, far) * e : 0;
+  const __int128 end = x.end();
+  for (int k = 0; k < kWritten; ++k) {
+    const Span& w = v[k];
+    if (!w.bytes) continue;
+    const char* over = nullptr;
+    for (int o = k + 1; o < kAll; ++o)
+      if (w.at < v[o].at + v[o].bytes && v[o].at < w.at + w.bytes &&
+          !(w.at == v[o].at && ((k == 0 && o == 5) || (k == 3 && o == 6))))
+        over = v[o].name;
+    if (w.at < end && x.at < w.at + w.bytes &&
+        pieces_meet(x, range_of(reinterpret_cast<const void*>(w.at), w.bytes)))
+      over = "logits";
+    if (over) {
+      set_error("%s must not lie over %s", w.name, over);
+      return CK_ERR_BAD_VALUE;
+    }
+  }
+  return CK_OK;
+}
+
 // Rows or segments of a state lie over one another.
 bool move_overlaps(int64_t rows, int64_t row, int64_t segs, int64_t seg, int64_t bytes) {
   if (rows > 1 && segs > 1) {
@@ -731,6 +776,9 @@ extern "C" ck_status ck_beam_select(const ck_beam_shape* shape, ck_seq logits, c
   }
   const BeamWs ws = beam_ws(*shape);
   rc = seq_check_ws(workspace, workspace_bytes, ws.total);
+  if (rc == CK_OK)
+    rc = beam_check_apart(*shape, logits, scores, finished, out_scores, parents, tokens,
+                          out_finished, workspace, ws.total);
   if (rc != CK_OK) return rc;
   return seq_dispatch(shape->dtype, [&](auto* e) -> ck_status {
     using E = std::remove_pointer_t<decltype(e)>;

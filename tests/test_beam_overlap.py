@@ -1,11 +1,13 @@
 """Beam search's calls whose outputs lie over what they read, or over one another, are
 refused before any device work, where addresses, sizes and strides show it."""
+import ctypes
 import os
 
 import pytest
 
 import sparse_graph_recurrent_amd as sgr
-from sparse_graph_recurrent_amd.beam import BeamState
+from sparse_graph_recurrent_amd.beam import BeamShape, BeamState
+from sparse_graph_recurrent_amd.sequence import CkSeq
 
 BAD_VALUE = 12
 B, K = 2, 4
@@ -61,3 +63,47 @@ def test_reorder_output_over_the_parents(L):
     for par in (A, A + 64, A + 64 * ROWS - 8, A - 8 * (ROWS - 1)):
         assert "parents" in reorder(L, dense(2 * A, A), parents=par)
         assert "parents" in reorder(L, dense(A), parents=par)
+
+
+V = 100
+PLACES = {n: (k + 2) * A for k, n in enumerate(
+    ("logits", "scores", "finished", "out_scores", "parents", "tokens", "out_finished",
+     "workspace"))}
+
+
+def select(L, name, **kw):
+    a = {**PLACES, **kw}
+    x = a["logits"]
+    x = x if isinstance(x, CkSeq) else CkSeq(x, K * V, V)
+    shape = ctypes.byref(BeamShape(B, K, V, 3, 1))
+    assert L.ck_beam_select(shape, x, a["scores"], a["finished"], a["out_scores"], a["parents"],
+                            a["tokens"], a["out_finished"], a["workspace"], 2**40, None) == BAD_VALUE
+    text = L.ck_last_error().decode()
+    assert "must not lie over" in text and name in text, text
+
+
+def test_select_outputs_over_what_is_read(L):
+    p = PLACES
+    for out in ("out_scores", "parents", "tokens", "out_finished", "workspace"):
+        select(L, "logits", **{out: p["logits"]})
+        select(L, "logits", **{out: p["logits"] + 2 * V * ROWS // 256 * 256 - 256})
+    for at in (p["scores"] + 4, p["scores"] - 4, p["scores"] + 4 * (ROWS - 1)):
+        select(L, "scores", out_scores=at)
+    select(L, "scores", parents=p["scores"])
+    select(L, "scores", out_finished=p["scores"] + 4 * ROWS - 1)
+    select(L, "finished", out_finished=p["finished"] + 1)
+    select(L, "finished", tokens=p["finished"])
+    # a padded projection's rows: the last of them, and the next beam's first logit
+    select(L, "logits", logits=CkSeq(p["logits"], K * 128, 128),
+           out_scores=p["logits"] + 2 * (7 * 128 + V) - 4)
+    select(L, "logits", logits=CkSeq(p["logits"], K * 128, 128), out_scores=p["logits"] + 2 * 128 - 4)
+    select(L, "logits", logits=CkSeq(p["logits"], 0, 0), out_scores=p["logits"] + 2 * V - 4)
+
+
+def test_select_outputs_over_one_another(L):
+    p = PLACES
+    select(L, "tokens", parents=p["tokens"])
+    select(L, "tokens", parents=p["tokens"] + 8 * (ROWS - 1))
+    select(L, "parents", out_scores=p["parents"] + 8)
+    select(L, "out_finished", out_finished=p["out_scores"] + 31)
+    select(L, "workspace", tokens=p["workspace"])

@@ -1,4 +1,5 @@
-"""Reordering of states that are slices of one tensor: the values of separate ones."""
+"""Selection and reordering where inputs and outputs are slices of one tensor: the values
+of separate ones."""
 import pytest
 import torch
 
@@ -41,3 +42,18 @@ def test_reorder_over_other_states_is_refused():
         sgr.beam_reorder([parents.view(4, 1)], parents)
     torch.cuda.synchronize()
     assert torch.equal(buf, before)
+
+
+def test_select_writes_into_the_padding_of_its_logits():
+    """Rows of a padded projection, whose last elements hold the outputs."""
+    x = torch.randn(1, 4, 32, device="cuda")
+    scores = -torch.rand(1, 4, device="cuda")
+    logits = x[:, :, :20]
+    want = sgr.beam_select(logits.clone(), scores)
+    out = (x[:, 0, 20:24], x[0, 1, 20:28].view(torch.int64).view(1, 4),
+           x[0, 2, 20:28].view(torch.int64).view(1, 4), None)
+    got = sgr.beam_select(logits, scores, out=out)
+    assert all(map(torch.equal, want[:3], got[:3]))
+    for bad in ((x[:, 0, 16:20], *out[1:]), (out[0], out[1], out[1], None)):
+        with pytest.raises(sgr.CkError, match="must not lie over"):
+            sgr.beam_select(logits, scores, out=bad)
