@@ -538,7 +538,8 @@ ck_status ck_dropout_backward(const ck_dropout_shape* shape, ck_seq grad_out, ck
  *
  * with h_{-1} = state0.  Steps lie less than 2^26 elements apart.  A gate that is
  * almost 1 is held as what it lacks, so that a state is kept over as many steps as
- * the gate says.  A state that is not finite may go on as a NaN.
+ * the gate says.  A state that is not finite may be a NaN from the next step of its text
+ * on, a gradient in all steps before its own.
  *
  * A call of few rows and channels has workgroups that wait for others of the same call
  * (through its workspace, which the call prepares itself and no other call may use at

@@ -57,9 +57,10 @@ struct GateForward {
         if constexpr (I) take = sigmoid_hw(in.i.get(k, j) + bias.i[j]);
         else take = g.rest();
         take *= in.x.get(k, j);
-        if (!WHOLE && k >= n) g = kGateKeep, take = 0.0f;
         a[k][j] = g;
         u[k][j] = take;
+        // (no step at all: one that keeps all of an infinite state makes a NaN of it)
+        if (!WHOLE && k >= n) continue;
         mine.h[j] = g.times(mine.h[j], take);
         mine.p[j] = g.times(mine.p[j], 0.0f);
       }
@@ -82,7 +83,7 @@ struct GateForward {
       float y[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        h[j] = a[k][j].times(h[j], u[k][j]);
+        if (WHOLE || k < n) h[j] = a[k][j].times(h[j], u[k][j]);
         y[j] = h[j];
         if constexpr (Z) {
           const float v = z.get(k, j);
