@@ -42,10 +42,16 @@ struct GateInputs {
   }
 };
 
-// The biases of a lane's channels, their sign turned, and what their gradients add up to.
+// What the bias gradients of a thread's channels add up to: within a window in fp32,
+// from window to window in 64 bits (a long row's sum would swallow its steps' parts one
+// by one), which wait in LDS meanwhile.
+template <int V>
+using GateSums = double[2 * kGateWaves][2 * V][kGateLanes];
+
+// The biases of a lane's channels, their sign turned.
 template <int V>
 struct GateBias {
-  float f[V], i[V], sum_f[V] = {}, sum_i[V] = {};
+  float f[V], i[V];
   template <typename A>
   __device__ __forceinline__ GateBias(const A& s, const GateSpot<V>& at, bool own) {
 #pragma unroll
@@ -116,11 +122,12 @@ struct GateBackward {
     return mine;
   }
 
-  // c: a H of the step behind the slot.
-  template <bool WHOLE>
+  // c: a H of the step behind the slot.  ONE: the workgroup's only window.
+  template <bool WHOLE, bool ONE>
   __device__ __forceinline__ void leave(const GateArgs<E>& s, const GateSpot<V>& at, int t, int slot,
-                                        int t1, int n, const GateTile<E, V>& x, GateBias<V>& bias,
+                                        int t1, int n, const GateTile<E, V>& x, GateSums<V>& sums,
                                         float (&c)[V]) {
+    float sum_f[V] = {}, sum_i[V] = {};
     const GateRows<E> gx(s.gx, t, at.b, at.c0), gf(s.gf, t, at.b, at.c0), gi(s.gi, t, at.b, at.c0);
     const uint32_t lane = (uint32_t)at.cl * (uint32_t)sizeof(E);
     const uint32_t ox = gate_offset((uint32_t)slot * gx.step + lane),
@@ -137,14 +144,14 @@ struct GateBackward {
         if constexpr (I) {
           take = own[k][j].value();
           vi[j] = runs ? gh * xv * own[k][j].slope() : 0.0f;
-          bias.sum_i[j] += vi[j];
+          sum_i[j] += vi[j];
         } else {
           take = a[k][j].rest();
           from -= xv;
         }
         vx[j] = runs ? take * gh : 0.0f;
         vf[j] = runs ? gh * from * a[k][j].slope() : 0.0f;
-        bias.sum_f[j] += vf[j];
+        sum_f[j] += vf[j];
         c[j] = a[k][j].times(gh, 0.0f);
       }
       if (WHOLE || t + slot + k < t1) {
@@ -155,6 +162,14 @@ struct GateBackward {
         pack_store<true, E, V>(row(gf, of), vf, V);
         if constexpr (I) pack_store<true, E, V>(row(gi, oi), vi, V);
       }
+    }
+    if (!s.part) return;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      double &f = sums[2 * at.wave + at.upper][j][at.lane],
+             &i = sums[2 * at.wave + at.upper][V + j][at.lane];
+      f = (ONE ? 0.0 : f) + (double)sum_f[j];
+      if (I || ONE) i = (ONE ? 0.0 : i) + (double)sum_i[j];
     }
   }
 };
@@ -176,27 +191,29 @@ __device__ __forceinline__ void gate_blank(const GateArgs<E>& s, const GateSpot<
   }
 }
 
+// (a thread clears and adds to its own sums alone, until gate_part)
+template <int V>
+__device__ __forceinline__ void gate_clear_sums(GateSums<V>& sums, const GateSpot<V>& at) {
+#pragma unroll
+  for (int j = 0; j < 2 * V; ++j) sums[2 * at.wave + at.upper][j][at.lane] = 0.0;
+}
+
 // A workgroup's part of the bias gradients: its slots' sums in their order, one channel
-// and gate a thread.  (All threads call it.)
+// and gate a thread.  (All threads call it.)  It is rounded to fp32, as what comes of the
+// parts is: both by half a step of theirs, however many steps and rows there are.
 template <int V, typename A>
 __device__ __forceinline__ void gate_part(const A& s, const GateSpot<V>& at,
-                                          float (*lds)[2 * V][kGateLanes], const GateBias<V>& bias,
-                                          int64_t row) {
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    lds[2 * at.wave + at.upper][j][at.lane] = bias.sum_f[j];
-    lds[2 * at.wave + at.upper][V + j][at.lane] = bias.sum_i[j];
-  }
+                                          const GateSums<V>& sums, int64_t row) {
   __syncthreads();
   float* part = s.part + row * 2 * s.D;
   for (int o = threadIdx.x; o < 2 * V * kGateLanes; o += blockDim.x) {
     const int lane = o % kGateLanes, j = o / kGateLanes % V, gate = o / kGateLanes / V;
-    float sum = 0.0f;
-    for (int k = 0; k < 2 * at.waves; ++k) sum += lds[k][gate * V + j][lane];
+    double sum = 0.0;
+    for (int k = 0; k < 2 * at.waves; ++k) sum += sums[k][gate * V + j][lane];
     // (a lane's channels begin earlier where they pass the row's end)
     const int64_t want = ((int64_t)at.group * kGateLanes + lane) * V;
     const int64_t ch = min(want, (int64_t)s.D - V) + j;
-    if (want < s.D && ch >= want) part[(int64_t)gate * s.D + ch] = sum;
+    if (want < s.D && ch >= want) part[(int64_t)gate * s.D + ch] = (float)sum;
   }
 }
 
@@ -205,7 +222,7 @@ __device__ __forceinline__ void gate_part(const A& s, const GateSpot<V>& at,
 template <typename E, int V, bool I, bool Z>
 __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd(const GateArgs<E> s) {
   __shared__ GateMeet<V, kGateWaves> meet;
-  __shared__ float sums[2 * kGateWaves][2 * V][kGateLanes];
+  __shared__ GateSums<V> sums;
   GateSpot<V> at;
   const int64_t id = seq_block(), cols = (int64_t)s.groups * s.B;
   if (id >= cols) return;
@@ -217,7 +234,8 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd(const GateArgs<E> s)
   for (; t >= 0 && t >= steps; t -= window) gate_blank<E, V, I, Z>(s, at, t, slot, s.T);
   GateInputs<E, V, I, Z> in, next;
   if (t >= 0) next.template load<false>(s, at, t, slot, steps - 1 - t);
-  GateBias<V> bias(s, at, I);
+  const GateBias<V> bias(s, at, I);
+  if (s.part) gate_clear_sums<V>(sums, at);
   if (threadIdx.x < kGateLanes)
 #pragma unroll
     for (int j = 0; j < V; ++j) meet.carry[0][at.lane][j] = s.gstate ? s.gstate[col + j] : 0.0f;
@@ -234,7 +252,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd(const GateArgs<E> s)
     float c[V];
     const GatePair<V> mine = way.template enter<WHOLE>(s, at, t, slot, s.T, n, in, bias);
     gate_fold<true>(meet, turn, at, mine, c);
-    way.template leave<WHOLE>(s, at, t, slot, s.T, n, in.x, bias, c);
+    way.template leave<WHOLE, false>(s, at, t, slot, s.T, n, in.x, sums, c);
     t -= window;
     turn ^= 1;
   };
@@ -250,15 +268,18 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd(const GateArgs<E> s)
   __syncthreads();
   if (threadIdx.x < kGateLanes && s.gstate0)
     pack_store<true, float, V>(s.gstate0 + col, meet.carry[turn][at.lane], V);
-  if (s.part) gate_part<V>(s, at, sums, bias, at.b);
+  if (s.part) gate_part<V>(s, at, sums, at.b);
 }
 
-// A window of a column a workgroup: one a CU (136 registers; held to 128 for a second one
-// it spills, 94 -> 139 us).  80 columns of 777 steps, fp16: 21 us.
+// A window of a column a workgroup.  Two run on a CU where a thread has 128 registers:
+// with fp32 (81 to 110), and with 16-bit types without gates of their own, which are held
+// there (127; 2048 steps of 64 columns: 30.5 us, and 34.6 with the 129 they would take).
+// With such gates (148 to 190) one does: held to 128 it spills, 94 -> 139 us.  80 columns
+// of 777 steps, fp16: 21 us.
 template <typename E, int V, bool I, bool Z>
-__global__ __launch_bounds__(64 * kGateWaves) void gate_bwd_chain(const GateArgs<E> s) {
+__global__ __launch_bounds__(64 * kGateWaves, V == 2 && !I && !Z ? 4 : 2) void gate_bwd_chain(const GateArgs<E> s) {
   __shared__ GateChain<V> chain;
-  __shared__ float sums[2 * kGateWaves][2 * V][kGateLanes];
+  __shared__ GateSums<V> sums;
   GateSpot<V> at;
   int behind;  // windows behind this one
   if (!gate_number(chain, s, at, &behind)) return;
@@ -266,9 +287,10 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd_chain(const GateArgs
   const int window = 2 * at.waves * kGateStep, t = index * window, t1 = min(t + window, s.T);
   const int slot = (2 * at.wave + at.upper) * kGateStep;
   const int64_t col = (int64_t)at.b * s.D + at.c;
-  GateBias<V> bias(s, at, I);
+  const GateBias<V> bias(s, at, I);
   if (t >= at.len) {  // behind the text; a row without any hands its adjoint on
     gate_blank<E, V, I, Z>(s, at, t, slot, t1);
+    if (s.part) gate_clear_sums<V>(sums, at);
     if (t == 0 && s.gstate0 && threadIdx.x < kGateLanes)
 #pragma unroll
       for (int j = 0; j < V; ++j) s.gstate0[col + j] = s.gstate ? s.gstate[col + j] : 0.0f;
@@ -286,12 +308,12 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd_chain(const GateArgs
           gate_chain<true>(chain, s, at, number, index == 0, s.gstate, mine, c);
       if (index == 0 && s.gstate0 && at.wave == 0 && !at.upper)
         pack_store<true, float, V>(s.gstate0 + col, before.h, V);
-      way.template leave<WHOLE>(s, at, t, slot, t1, n, in.x, bias, c);
+      way.template leave<WHOLE, true>(s, at, t, slot, t1, n, in.x, sums, c);
     };
     if (t + window <= at.len) work(std::true_type());
     else work(std::false_type());
   }
-  if (s.part) gate_part<V>(s, at, sums, bias, (int64_t)index * s.B + at.b);
+  if (s.part) gate_part<V>(s, at, sums, (int64_t)index * s.B + at.b);
 }
 
 // g_f_bias and g_i_bias: the workgroups' sums, in their order.  A wave an output's 64
@@ -300,18 +322,19 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_bwd_chain(const GateArgs
 constexpr int kBiasCols = 32, kBiasRows = 8;
 __global__ __launch_bounds__(kBiasCols * kBiasRows) void gate_bias_sum(
     const float* part, int D, int64_t rows, float* g_f, float* g_i) {
-  __shared__ float lds[kBiasRows][kBiasCols];
+  __shared__ double lds[kBiasRows][kBiasCols];
   const int x = threadIdx.x % kBiasCols, y = threadIdx.x / kBiasCols;
   const int64_t o = seq_block() * kBiasCols + x;
-  float sum = 0.0f;
+  double sum = 0.0;
   if (o < 2 * (int64_t)D)
-    for (int64_t r = y; r < rows; r += kBiasRows) sum += part[r * 2 * D + o];
+#pragma unroll 4
+    for (int64_t r = y; r < rows; r += kBiasRows) sum += (double)part[r * 2 * D + o];
   lds[y][x] = sum;
   __syncthreads();
   if (y != 0 || o >= 2 * (int64_t)D) return;
   for (int k = 1; k < kBiasRows; ++k) sum += lds[k][x];
   float* to = o < D ? g_f : g_i;
-  if (to) to[o < D ? o : o - D] = sum;
+  if (to) to[o < D ? o : o - D] = (float)sum;
 }
 
 template <typename E, int V, bool I, bool Z>
