@@ -169,6 +169,22 @@ __device__ __forceinline__ void clip_write(const ClipTable& t, int i, int64_t ch
   }
 }
 
+// A thread's share of the partial sums.
+__device__ __forceinline__ double clip_parts(const double* part, int64_t parts) {
+  double sum = 0.0;
+#pragma unroll 4
+  for (int64_t k = threadIdx.x; k < parts; k += kClipThreads) sum += part[k];
+  return sum;
+}
+
+// The sum of the partial sums of several launches, left as the first of them.  (Each of as
+// many scaling launches would have all its workgroups add all of them up: work by the
+// square of the number of tensors.)
+__global__ __launch_bounds__(kClipThreads) void clip_fold(double* part, int64_t parts) {
+  const double sum = clip_block_sum(clip_parts(part, parts));  // (read before it is written)
+  if (threadIdx.x == 0) part[0] = sum;
+}
+
 // Every workgroup adds the partial sums, in one order, for itself.  `same`: every
 // output of the table is its gradient, so that nothing is to do where nothing is
 // scaled.  Chunks are taken last first: the last are what the sums' launch left in
@@ -176,9 +192,7 @@ __device__ __forceinline__ void clip_write(const ClipTable& t, int i, int64_t ch
 __global__ __launch_bounds__(kClipThreads) void clip_scale(const ClipTable t, const double* part,
                                                            int parts, double max_norm, int same,
                                                            float* norm) {
-  double sum = 0.0;
-  for (int k = threadIdx.x; k < parts; k += kClipThreads) sum += part[k];
-  const double n = sqrt(clip_block_sum(sum));
+  const double n = sqrt(clip_block_sum(clip_parts(part, parts)));
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
   // a norm that is not finite scales nothing: there is no direction to keep
   const bool scales = n > max_norm && (float)n < __builtin_inff();
@@ -349,7 +363,7 @@ extern "C" ck_status ck_clip_grad_norm(const ck_clip_tensor* tensors, int64_t co
   double* part = static_cast<double*>(workspace);
   ClipTable t;
   bool same;
-  int parts = 0;
+  int parts = 0, launches = 0;
   int64_t i = 0;
   do {
     i = clip_fill(tensors, count, i, units, &t, &same);
@@ -357,7 +371,12 @@ extern "C" ck_status ck_clip_grad_norm(const ck_clip_tensor* tensors, int64_t co
         (int)std::min<int64_t>(kClipBlocks, std::max<int64_t>(1, t.first[t.count]));
     clip_norm<<<blocks, kClipThreads, 0, stream>>>(t, part + parts);
     parts += blocks;
+    ++launches;
   } while (i < count);
+  if (launches > 1) {
+    clip_fold<<<1, kClipThreads, 0, stream>>>(part, parts);
+    parts = 1;
+  }
   i = 0;
   float* to = norm;
   do {
