@@ -152,7 +152,8 @@ def train(model: TextMixer, text: torch.Tensor, steps: int, T: int = 64, B: int 
         opt.zero_grad()
         loss.backward()
         if max_norm is not None:
-            sgr.clip_grad_norm([p.grad for p in model.parameters()], max_norm)
+            sgr.clip_grad_norm([p.grad for p in model.parameters() if p.grad is not None],
+                               max_norm)
         opt.step()
         losses.append(loss.item())
     return losses

@@ -1,7 +1,8 @@
 """The norm of a model's gradients and their scaling to a limit, as a training
 step runs them between its backward and its optimizer:
 
-    norm, _ = clip_grad_norm([p.grad for p in model.parameters()], 1.0)
+    grads = [p.grad for p in model.parameters() if p.grad is not None]
+    norm, _ = clip_grad_norm(grads, 1.0)
 
 Backpropagation through a window of the recurrence multiplies by its steps'
 derivatives once a microstep; a limit on the whole gradient's norm keeps one
@@ -134,7 +135,9 @@ def clip_grad_norm(grads, max_norm: float, out=None, norm=None, workspace=None, 
     fp16, mixed as they come; each without gaps) so that their norm together is
     at most ``max_norm``.  In place, or into ``out``, a tensor for each.
     Returns (the norm before, fp32 [1] on the device; the scaled tensors).  A
-    norm that is not finite scales nothing."""
+    norm that is not finite scales nothing.  (``torch.nn.utils.clip_grad_norm_``
+    takes parameters, leaves out those without a gradient, adds 1e-6 to the norm
+    that it divides by, and scales by a norm that is not finite as well.)"""
     grads = list(grads)
     outs = grads if out is None else list(out)
     if len(outs) != len(grads):
