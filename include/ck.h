@@ -643,9 +643,10 @@ ck_status ck_clip_grad_norm(const ck_clip_tensor* tensors, int64_t count, double
  * over all beams k and tokens v of a text, best first; of equal scores the lower
  * k V + v is first (of one beam's, the one of the larger logit: where the scores'
  * rounding makes unlike logits alike, their order stays).  A finished beam has one
- * continuation, the end token, at its own score.  A logit of -inf, and a NaN, is never taken before any other (its score is
- * -inf, as are all of a beam whose own score is -inf or NaN, and of a finished beam
- * but the end token's); +inf counts as the largest finite fp32 value.  Logits of a
+ * continuation, the end token, at its own score.  A logit of -inf, and a NaN, is never
+ * taken before any other (its score is -inf, as are all of a beam whose own score is -inf
+ * or NaN, and of a finished beam but the end token's); +inf counts as the largest finite
+ * fp32 value.  Logits of a
  * beam without any above -inf, or whose score is -inf, or that is finished, are not
  * looked at for a sum.  Scores are compared in 64 bits (sums of exponentials are held
  * in 32) and rounded once.  Two calls on the same inputs give the same bits.

@@ -11,12 +11,24 @@ namespace ckhip {
 namespace {
 
 // A workgroup of the loop over windows fills a CU, so that columns are worked on in
-// rounds of one a CU.  Where they fill them, the loop is the faster one (2048 steps of 256
-// columns, bf16: forward 83 us against 88 as a chain, backward 140 against 176), where
-// they do not, the chain (288 columns: 134 against 98 and 232 against 199; 32 columns: 82
-// against 19 and 140 against 30).  The forward's chain, two workgroups a CU, wins from the
-// second round on (1024 columns of 256 steps: 55 against 45), the backward's, one a CU,
-// where a round in four is lost.
+// rounds of one a CU; a chain has a workgroup a window, whatever the columns.  Loop / chain,
+// us, with both gates (2048 steps of so many columns, and 256 of them):
+//
+//                          32          128          256          288          512
+//   bf16 forward        48 / 17      51 / 42      80 / 83     132 / 95     159 / 156
+//        backward       83 / 30     111 / 96     141 / 180    232 / 202    279 / 342
+//   fp32 forward        31 / 14      37 / 32      72 / 66     117 / 76     147 / 128
+//        backward       55 / 22      89 / 64     134 / 129    201 / 148    257 / 247
+//   256 steps, bf16   10 / 9.4      11 / 10      13 / 14      23 / 19      27 / 23
+//        backward       17 / 14      20 / 17      23 / 30      35 / 36      40 / 51
+//
+// So the forward loops where its columns are one full round, the backward where no round in
+// four is lost.  The rule is that of 16-bit types with gates of their own, of whose chain
+// one workgroup runs on a CU backward and two forward.  fp32 has two or more in both
+// directions, and would gain up to 9 % from the chain at 256 columns (512 backward: 4 %).
+// Where it is taken at a loss: without gates of their own a chain of two to eight windows
+// pays more for its words than it gains (fp32, 256 steps of 32 columns 7.1 / 10.0 us, and
+// 6.3 / 8.7 looped; 1024 of 128 backward 26, and 22).
 constexpr int64_t kGateCus = 256;
 constexpr int64_t kGateColumns = 4096;  // of a chain, at most: each has a ticket
 

@@ -89,6 +89,9 @@ def test_time_grows_as_the_number_of_tensors():
             torch.cuda.synchronize()
             best = min(best, a.elapsed_time(b))
         took.append(best)
+        replayed = torch.cat(outs)
+        run()
+        assert torch.equal(replayed, torch.cat(outs))
     log(f"clip: {took[0]:.3f} and {took[1]:.3f} ms")
     # (the fold of the sums is one workgroup's: it may take a part of its own)
     assert took[1] <= 2 * 16 * took[0], took
