@@ -166,9 +166,16 @@ def _dev(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> torch.Te
     return t
 
 
+# Handles of graphs that were let go of while a HIP graph was being captured: memory that
+# is freed then ends the capture, and the garbage collector may let a graph go at any time.
+_waiting = []
+
+
 class SparseGraph:
     """Device graph: CSR by destination, transposed CSR, edge permutations,
-    input-slot map and row schedules, built by ``ck_graph_create``."""
+    input-slot map and row schedules, built by ``ck_graph_create``.  Its device
+    memory is freed with it; where the current stream is being captured, with the
+    next graph that is made or goes outside of a capture."""
 
     def __init__(self, src: torch.Tensor, dst: torch.Tensor, num_nodes: int,
                  input_nodes: torch.Tensor, stream=None):
@@ -178,6 +185,7 @@ class SparseGraph:
         _dev(input_nodes, "input_nodes", torch.int64, (input_nodes.numel(),))
         h = ctypes.c_void_p()
         self._lib = lib()
+        self._free_waiting()
         self.device = src.device
         _check(self._lib.ck_graph_create(_ptr(src), _ptr(dst), E, int(num_nodes),
                                          _ptr(input_nodes), input_nodes.numel(), _stream(stream),
@@ -213,10 +221,16 @@ class SparseGraph:
             _stream()))
         return res
 
+    def _free_waiting(self):
+        """Destroys the graphs that wait for it, if nothing is being captured."""
+        while _waiting and not torch.cuda.is_current_stream_capturing():
+            _check(self._lib.ck_graph_destroy(_waiting.pop()))
+
     def destroy(self):
         if getattr(self, "_h", None) is not None:
-            _check(self._lib.ck_graph_destroy(self._h))
+            _waiting.append(self._h)
             self._h = None
+            self._free_waiting()
 
     def __del__(self):
         try:
