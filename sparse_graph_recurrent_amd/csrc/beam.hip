@@ -686,41 +686,50 @@ bool move_overlaps(int64_t rows, int64_t row, int64_t segs, int64_t seg, int64_t
 }
 
 // What is written must not lie over anything else of a call, but a state's output over
-// the state itself.
+// the state itself.  Tensors are looked at in the order of their addresses, so that only
+// those are compared whose ranges cross: of many states, slices of one tensor, which lie
+// side by side in its rows.
 ck_status move_check_apart(const ck_beam_state* states, int64_t count, const int64_t* parents,
                            int64_t rows) {
   struct Span {
-    Pieces p;
-    __int128 end;
+    Slice at;
+    int64_t state;  // -1: the parents
+    int written;    // 0 or 1
+    int pieces;     // which
   };
-  const auto span = [](const Pieces& p) { return Span{p, p.end()}; };
-  const auto meet = [](const Span& a, const Span& b) {
-    return a.p.at < b.end && b.p.at < a.end && pieces_meet(a.p, b.p);
+  std::vector<Span> v;
+  std::vector<Pieces> pieces;
+  v.reserve(2 * count + 1), pieces.reserve(2 * count + 1);
+  const auto add = [&](const Pieces& p, int64_t state, int written) {
+    v.push_back(Span{slice_of(p), state, written, (int)pieces.size()});
+    pieces.push_back(p);
   };
-  std::vector<Span> in(count), out(count);
-  const Span par = span(range_of(parents, (size_t)rows * sizeof(int64_t)));
+  add(range_of(parents, (size_t)rows * sizeof(int64_t)), -1, 0);
   for (int64_t i = 0; i < count; ++i) {
     const ck_beam_state& s = states[i];
-    if (s.segments == 0 || s.bytes == 0) continue;  // (empty: meets nothing)
-    Pieces p = range_of(s.in, (size_t)s.bytes);
-    p.n0 = rows, p.s0 = s.in_row, p.n1 = s.segments, p.s1 = s.in_segment;
-    in[i] = span(p);
-    p.at = reinterpret_cast<uintptr_t>(s.out), p.s0 = s.out_row, p.s1 = s.out_segment;
-    out[i] = span(p);
-    if (s.in != s.out && meet(in[i], out[i])) {
-      set_error("state %lld: its output lies over it", (long long)i);
-      return CK_ERR_BAD_VALUE;
-    }
-    if (meet(out[i], par)) {
-      set_error("state %lld: its output lies over the parents", (long long)i);
-      return CK_ERR_BAD_VALUE;
-    }
-    for (int64_t o = 0; o < i; ++o)
-      if (meet(out[o], out[i]) || meet(in[o], out[i]) || meet(out[o], in[i])) {
-        set_error("states %lld and %lld share memory that is written", (long long)o, (long long)i);
-        return CK_ERR_BAD_VALUE;
-      }
+    if (s.segments == 0 || s.bytes == 0) continue;
+    Pieces p = range_of(s.out, (size_t)s.bytes);
+    p.n0 = rows, p.s0 = s.out_row, p.n1 = s.segments, p.s1 = s.out_segment;
+    add(p, i, 1);
+    if (s.in == s.out) continue;
+    p.at = reinterpret_cast<uintptr_t>(s.in), p.s0 = s.in_row, p.s1 = s.in_segment;
+    add(p, i, 0);
   }
+  std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.at.at < b.at.at; });
+  for (size_t i = 0; i < v.size(); ++i)
+    for (size_t o = i + 1; o < v.size() && v[o].at.at < v[i].at.end; ++o) {
+      const Span &a = v[i], &b = v[o];
+      if (side_by_side(a.at, b.at) || !(a.written | b.written) ||
+          !pieces_meet(pieces[a.pieces], pieces[b.pieces]))
+        continue;
+      const int64_t first = std::min(a.state, b.state), last = std::max(a.state, b.state);
+      if (first < 0) set_error("state %lld: its output lies over the parents", (long long)last);
+      else if (first == last) set_error("state %lld: its output lies over it", (long long)last);
+      else
+        set_error("states %lld and %lld share memory that is written", (long long)first,
+                  (long long)last);
+      return CK_ERR_BAD_VALUE;
+    }
   return CK_OK;
 }
 

@@ -76,6 +76,27 @@ inline bool solid_meets(const Pieces& a, const Pieces& solid) {
 
 }  // namespace overlap
 
+// A tensor as a slice of a wider one's rows, for many comparisons: all its pieces begin at
+// `at` and a multiple of `step` (0: no such step).
+struct Slice {
+  uintptr_t at, end;
+  int64_t step, bytes;
+};
+inline Slice slice_of(const Pieces& whole) {
+  const Pieces p = overlap::plain(whole);
+  const __int128 end = p.end();
+  return Slice{p.at, end > (__int128)UINTPTR_MAX ? UINTPTR_MAX : (uintptr_t)end,
+               !p.s1 ? p.s0 : p.s0 % p.s1 ? 0 : p.s1, p.bytes};
+}
+// Whether two of them, b not before a, lie beside one another in the same rows.  (Quick;
+// no other answer than yes says anything.)
+inline bool side_by_side(const Slice& a, const Slice& b) {
+  if (a.step != b.step || !a.step) return false;
+  uintptr_t by = b.at - a.at;
+  if (by >= (uintptr_t)a.step) by %= (uintptr_t)a.step;
+  return by >= (uintptr_t)a.bytes && by + (uintptr_t)b.bytes <= (uintptr_t)a.step;
+}
+
 // Whether a byte lies in both.  Exact where one has no gaps, where both have the same
 // strides (slices of one tensor) or where one has few pieces; of others with gaps only
 // such are found as begin at the same address.

@@ -1,5 +1,6 @@
 // CPU driver for csrc/overlap.h: reads two tensors a line (address, n0, s0, n1, s1, bytes
-// of each) and prints whether they are found to share memory.
+// of each) and prints whether they are found to share memory (bit 0), and to lie side by
+// side (bit 1).
 #include <cstdio>
 
 #include "overlap.h"
@@ -16,6 +17,8 @@ int main() {
       p[k].n1 = v[6 * k + 3], p[k].s1 = v[6 * k + 4];
       p[k].bytes = v[6 * k + 5];
     }
-    std::printf("%d\n", ckhip::pieces_meet(p[0], p[1]) ? 1 : 0);
+    const auto a = ckhip::slice_of(p[0]), b = ckhip::slice_of(p[1]);
+    const bool beside = a.at <= b.at ? ckhip::side_by_side(a, b) : ckhip::side_by_side(b, a);
+    std::printf("%d\n", (ckhip::pieces_meet(p[0], p[1]) ? 1 : 0) | (beside ? 2 : 0));
   }
 }

@@ -24,8 +24,10 @@ def meet(tmp_path_factory):
         text = "".join(" ".join(map(str, a + b)) + "\n" for a, b in pairs)
         out = subprocess.run([exe], input=text, capture_output=True, text=True, check=True)
         assert not out.stderr
-        return [ln == "1" for ln in out.stdout.split()]
-    return run
+        both = [int(ln) for ln in out.stdout.split()]
+        assert 3 not in both, "side by side, and over one another"
+        return [k & 1 == 1 for k in both], [k & 2 == 2 for k in both]
+    return lambda pairs, beside=False: run(pairs)[1 if beside else 0]
 
 
 def held(p):
@@ -65,6 +67,19 @@ def test_slices_of_a_projection(meet):
     turn = lambda p: (p[0], p[3], 4 * wide * 1000, p[1], 4 * wide, p[5])
     assert meet(apart + over) == [False] * 4 + [True] * 5
     assert meet([(turn(cut(0)), turn(cut(16))), (turn(cut(0)), turn(cut(15)))]) == [False, True]
+
+
+def test_side_by_side(meet):
+    """Slices of a tensor's rows, of its pieces, and such as wrap around a row's end."""
+    a = (4096, 8, 256, 1, 0, 64)
+    to = lambda at, size=64, n=8, s=256: (4096 + at, n, s, 1, 0, size)
+    pairs = [(a, to(64)), (a, to(192)), (a, to(256 + 64)), (a, to(63)), (a, to(193)),
+             (a, to(64, s=128)), (a, to(64, 192)), (a, to(64, 193)), (to(128), a)]
+    assert meet(pairs, True) == [True, True, True, False, False, False, True, False, True]
+    b = (4096, 3, 1024, 4, 256, 64)
+    assert meet([(b, (4096 + 64, 3, 1024, 4, 256, 64)), (b, (4096 + 32, 3, 1024, 4, 256, 64)),
+                 ((4096, 3, 1000, 4, 256, 64), (4096 + 64, 3, 1000, 4, 256, 64))], True) == \
+        [True, False, False]
 
 
 def test_nothing_meets_nothing_and_far_strides(meet):
