@@ -100,7 +100,8 @@ ck_status ck_graph_create(const int64_t* src, const int64_t* dst, int64_t num_ed
                           int64_t num_nodes, const int64_t* input_nodes, int64_t num_inputs,
                           hipStream_t stream, ck_graph_t* out);
 
-/* Release a handle and its device arrays (synchronises the device).  NULL is accepted. */
+/* Release a handle and its device arrays (synchronises the device, so not while a stream
+ * is being captured: that ends the capture).  NULL is accepted. */
 ck_status ck_graph_destroy(ck_graph_t g);
 
 /* Sizes the graph was created with (any output pointer may be NULL). */
